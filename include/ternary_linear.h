@@ -1,6 +1,7 @@
 /*
  * ternary_linear.h -- C ABI of libternary_gb300.so, a ternary-weight linear
- * layer for NVIDIA GB300 (sm_103a).
+ * layer for NVIDIA GB300 (sm_103a), with the rotary positions, quantised cache and
+ * attention that a decode step needs between its QKV and its o layer.
  *
  * Format (all calls): a weight matrix W[N,K] with entries in {-1,0,+1} is
  * stored packed as uint8 [N, ceil(K/4)], row-major, K contiguous (written
@@ -46,8 +47,9 @@ typedef enum {
                                group size, or a size beyond the supported range  */
     TL_ERR_DTYPE = 3,       /* unknown dtype code or unsupported group size      */
     TL_ERR_ALIGN = 4,       /* pointer not 16-byte aligned                      */
-    TL_ERR_VALUE = 5,       /* reserved for callers mapping a non-zero invalid /
-                               reserved count to an error                        */
+    TL_ERR_VALUE = 5,       /* an index read on the device was out of range (see
+                               ternary_device_status); also for callers mapping a
+                               non-zero invalid / reserved count to an error     */
     TL_ERR_CUDA = 6,        /* a CUDA runtime call or a kernel launch failed     */
     TL_ERR_TIMEOUT = 7,     /* a bounded device-side wait gave up (see
                                ternary_device_status)                            */
@@ -216,6 +218,167 @@ tl_status ternary_linear_silu_mul_masked(const void *x, int32_t x_dtype, const u
                                          int64_t M, int64_t N, int64_t K, uint32_t flags,
                                          void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the fused QKV call and the o call of a layer: rotary positions, a
+ * paged 8- or 4-bit cache of keys and values, and attention over that cache.
+ *
+ * These calls follow the conventions above with three differences, stated once:
+ * strided tensors take their strides in elements (the last axis is dense) and any
+ * element-aligned pointer (16-byte aligned pointers and strides run faster);
+ * index arrays (positions, slots, page tables, lengths) are read on the device, and
+ * an index out of range never leads to an access out of bounds: the work it
+ * names is skipped as each call says, and the device status word is set to
+ * TL_ERR_VALUE; and the status word is created by the first of these calls on a
+ * device too (make it before any stream capture).
+ * ------------------------------------------------------------------------- */
+
+/* Rotation flags of ternary_rope and ternary_kv_append. */
+typedef enum {
+    TL_ROPE_INTERLEAVED = 1, /* pairs (x[2i], x[2i+1]); without it (x[i], x[i + R/2])     */
+    TL_ROPE_INVERSE = 2      /* rotate by the negative angle: the transpose, which is the
+                                gradient of the rotation (ternary_rope only)             */
+} tl_rope_flags;
+
+/*
+ * ternary_rope_table -- the cosines and sines of every position, once per model:
+ *   table fp32 [positions, R]: row p = (m cos(p f_0) .. m cos(p f_{R/2-1}),
+ *                                       m sin(p f_0) .. m sin(p f_{R/2-1}))
+ *   f_i = base^(-2i/R), stretched for contexts beyond the trained length:
+ *   turns_i = original_len f_i / (2 pi)  (full turns within the trained length)
+ *   g_i = clamp((turns_i - ramp_lo) / (ramp_hi - ramp_lo), 0, 1)
+ *   f_i <- f_i (g_i + (1 - g_i) / factor)
+ * so that frequencies of more than ramp_hi turns stay and those of fewer than
+ * ramp_lo are divided by factor.  factor = 1: no stretching; original_len = 0
+ * (or ramp_hi <= ramp_lo): every frequency is divided by factor.  m = magnitude.
+ * Angles are computed in fp64 and each entry is rounded once to fp32.
+ * R = rotary_dim, even, 2..1024; base > 0, factor > 0; positions < 2^31.
+ */
+tl_status ternary_rope_table(float *table, int64_t positions, int32_t rotary_dim, double base,
+                             double factor, double original_len, double ramp_lo, double ramp_hi,
+                             double magnitude, void *stream);
+
+/*
+ * ternary_rope -- out[t, h, :] = x[t, h, :] rotated by position positions[t]:
+ *   each pair (a, b) becomes (a c - b s, b c + a s) with c, s from row
+ *   positions[t] of table [table_rows, R]; elements at and beyond R = rotary_dim
+ *   are copied.  Computed in fp32, rounded once.  dtype: TL_F16, TL_BF16, TL_F32.
+ *   x and out: [tokens, heads, head_dim] with token and head strides; out == x with
+ *   the same strides rotates in place, any other overlap is not allowed.
+ *   A token whose position is outside [0, table_rows) is not written and sets the
+ *   device status word to TL_ERR_VALUE.
+ *   R even, R <= head_dim <= 1024; table 16-byte aligned; tokens, heads >= 0 (0: no-op).
+ * HBM-bound: x read once, out written once.
+ */
+tl_status ternary_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                       int64_t out_token_stride, int64_t out_head_stride, int32_t dtype,
+                       int64_t tokens, int32_t heads, int32_t head_dim, const int64_t *positions,
+                       const float *table, int64_t table_rows, int32_t rotary_dim, uint32_t flags,
+                       void *stream);
+
+typedef enum {
+    TL_KV_INT8 = 0, /* two's complement -127..127                                       */
+    TL_KV_FP8 = 1,  /* e4m3 (largest 448)                                               */
+    TL_KV_INT4 = 2  /* two per byte, field value + 8 (1..15), the even element in the low
+                       bits                                                             */
+} tl_kv_format;
+
+/*
+ * A paged cache of keys and values (host struct, device pointers).  The cache is a
+ * pool of pages of page_size tokens; slot s is place s % page_size of page
+ * s / page_size.  Each (token, kv head) row has one fp32 scale: value = code * scale.
+ *   codes  [pages, kv_heads, page_size, head_dim]  (INT4: head_dim / 2 bytes per row)
+ *   scales [pages, kv_heads, page_size] fp32
+ * A head's rows of a page are contiguous, which is how the attention reads them.
+ * head_dim 64 or 128; page_size a multiple of 16; codes and scales 16-byte aligned.
+ */
+typedef struct {
+    void *k_codes;
+    void *v_codes;
+    float *k_scale;
+    float *v_scale;
+    int64_t pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format; /* tl_kv_format */
+} tl_kv_cache;
+
+/*
+ * ternary_kv_append -- write tokens' keys and values into the cache, with the
+ * rotation of the queries and keys in the same pass over the fused QKV output.
+ *   k, v: [tokens, kv_heads, head_dim] (token and head strides), TL_F16 or TL_BF16.
+ *   table != NULL: k (and q) are rotated by positions as ternary_rope does, R =
+ *     rotary_dim a multiple of 16, flags 0 or TL_ROPE_INTERLEAVED; table == NULL:
+ *     k is stored as it is (and q must be NULL).
+ *   q != NULL: [tokens, q_heads, head_dim], rotated into q_out (q_out == q with the
+ *     same strides rotates in place).
+ *   slots[t]: where token t goes; negative: its k and v are not stored (padding).  A
+ *     slot at or beyond pages * page_size stores nothing and sets the device status
+ *     word to TL_ERR_VALUE, as does a position outside the table (neither q nor
+ *     the cache is then written for that token).  Tokens with the same slot:
+ *     either may be the one kept.
+ *   Quantisation of a row y (fp32, after the rotation, not rounded in between):
+ *     scale = max|y| (1 / Q) with Q = 127, 448, 7; code = y / scale rounded to nearest
+ *     even on the format's grid, 0 where scale is 0 (1 / Q rounded to fp32 first).  A
+ *     row with a NaN or an infinity gets scale NaN and codes 0.
+ * HBM-bound: q, k, v read once; q_out, codes and scales written once.
+ */
+tl_status ternary_kv_append(const tl_kv_cache *cache, const void *k, int64_t k_token_stride,
+                            int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                            int64_t v_head_stride, int32_t dtype, int64_t tokens,
+                            const int64_t *slots, const void *q, int64_t q_token_stride,
+                            int64_t q_head_stride, void *q_out, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, int32_t q_heads, const int64_t *positions,
+                            const float *table, int64_t table_rows, int32_t rotary_dim,
+                            uint32_t flags, void *stream);
+
+/*
+ * ternary_kv_read -- k, v [tokens, kv_heads, head_dim] (dense, out_dtype) = the values
+ * at slots[t], code * scale in fp32 rounded once.  A negative slot gives zeros; a
+ * slot beyond the cache gives zeros and sets the device status word to TL_ERR_VALUE.
+ * k or v may be NULL (not wanted).  HBM-bound.
+ */
+tl_status ternary_kv_read(const tl_kv_cache *cache, const int64_t *slots, int64_t tokens, void *k,
+                          void *v, int32_t out_dtype, void *stream);
+
+/*
+ * ternary_tree_attention -- attention of `draft` new tokens per sequence over the
+ * sequence's cached keys and values.
+ *   q [batch, draft, q_heads, head_dim] (strides of the first three axes), TL_F16 or
+ *     TL_BF16; out the same shape and dtype, dense; query head h reads kv head
+ *     h / (q_heads / kv_heads).
+ *   page_table int32 [batch, max_pages] (row stride in elements): page of key j of a
+ *     sequence is page_table[b, j / page_size].
+ *   context_len int32 [batch]: keys 0 .. context_len[b] - 1 are committed and seen by
+ *     every new token; keys context_len[b] + i, i < draft, are the new tokens' own
+ *     (already written to the cache).
+ *   tree: uint8 [batch, draft, draft] (batch and row stride; a batch stride of 0 shares
+ *     one tree): new token t sees new token i where tree[b, t, i] != 0.  NULL: i <= t
+ *     (a chain; draft == 1 is plain decoding).
+ *   out = softmax_j(scale q.k_j) v_j over the seen keys, lse (fp32 [batch, draft,
+ *     q_heads], may be NULL) = ln sum_j exp(scale q.k_j); a token that sees no key
+ *     gets zeros and -inf.  Keys that a token does not see have no effect on it,
+ *     whatever their codes and scales hold.
+ *   scale > 0 and finite.  q_heads a multiple of kv_heads.
+ *   A length outside [0, max_pages * page_size - draft] is clamped, an unknown page is
+ *     read as page 0; both set the device status word to TL_ERR_VALUE.
+ *   workspace: device, 16-byte aligned, at least
+ *     ternary_tree_attention_workspace(...) bytes; free for other use once the call's
+ *     work has run.
+ * Scores, softmax sums and the joined outputs are fp32.  Every run of the same call
+ * gives the same bits.
+ */
+int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
+                                         int32_t kv_heads, int32_t head_dim); /* -1: invalid */
+tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
+                                 int64_t q_head_stride, int32_t dtype, int64_t batch,
+                                 int64_t draft, int32_t q_heads, const tl_kv_cache *cache,
+                                 const int32_t *page_table, int64_t page_table_stride,
+                                 int64_t max_pages, const int32_t *context_len,
+                                 const uint8_t *tree, int64_t tree_batch_stride,
+                                 int64_t tree_row_stride, float scale, void *out, float *lse,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Kernels by M (TL_PATH_AUTO, K % 64 == 0): M <= 16 -> the decode kernel
  * (register-fed warp MMAs, TMA-staged weights) or, for 9 <= M and for plain
  * layers of 2049..4608 rows at M <= 8, the tcgen05 skinny kernel (groups 0 /
@@ -234,7 +397,8 @@ int32_t ternary_skinny_max_m(void);
 /*
  * ternary_device_status -- read (and optionally clear) the current device's
  * status word.  Kernels whose waits are bounded write a non-zero code there
- * when a wait gives up; *code receives TL_OK or TL_ERR_TIMEOUT.  Synchronous:
+ * when a wait gives up, and the cache and attention calls when an index is out of
+ * range; *code receives TL_OK, TL_ERR_TIMEOUT or TL_ERR_VALUE.  Synchronous:
  * call after the work in question has completed (e.g. after a stream sync).
  */
 tl_status ternary_device_status(int32_t *code, int32_t clear);
@@ -242,7 +406,8 @@ tl_status ternary_device_status(int32_t *code, int32_t clear);
 /*
  * ternary_device_status_async -- enqueue on `stream` a copy of the current
  * device's status word into *dst (device memory or pinned host memory, 4-byte
- * aligned; the raw word: 0 = OK, 7 = a bounded wait gave up), then, if clear is
+ * aligned; the raw word: 0 = OK, 7 = a bounded wait gave up, 5 = an index of a
+ * cache or attention call was out of range), then, if clear is
  * non-zero, reset the word.  The copy is ordered after the work already on
  * `stream`, so a non-zero value read after synchronising `stream` was set by
  * that work or by work on another stream that ran before it.  Asynchronous.

@@ -22,6 +22,7 @@ __all__ = [
     "row_bytes",
     "linear_fused",
     "linear_silu_mul",
+    "KVCache", "KV_FORMATS", "rope_table", "rope", "kv_append", "kv_read", "tree_attention",
     "device_status", "device_status_async", "status_string", "skinny_max_m", "PATHS",
 ]
 
@@ -348,3 +349,7 @@ def linear_silu_mul(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
                                         _stream(x.device))
     _check(rc, "ternary_linear_silu_mul")
     return out.reshape(*lead, N)
+
+
+from .attention import (KVCache, KV_FORMATS, kv_append, kv_read, rope, rope_table,  # noqa: E402
+                        tree_attention)

@@ -437,6 +437,18 @@ tl_status check_packing(const void *t, const void *packed, int64_t N, int64_t K,
 
 }  // namespace
 
+// Start of a call of api_attn.cu, after its argument checks: the injected failure of the
+// tests, then the current device's facts and its status word.
+int tl::begin_call(CallDevice *out) {
+    if (take_injected_failure()) return TL_ERR_CUDA;
+    DevInfo *d = nullptr;
+    const tl_status s = current_device(&d, true);
+    if (s != TL_OK) return s;
+    out->sm_count = d->sm_count;
+    out->status = d->status;
+    return TL_OK;
+}
+
 extern "C" {
 
 tl_status ternary_pack(const int8_t *t, uint8_t *packed, int64_t N, int64_t K,
@@ -561,7 +573,7 @@ tl_status ternary_device_status(int32_t *code, int32_t clear) {
     int v = 0;
     s = from_cuda(cudaMemcpy(&v, d->status, sizeof(int), cudaMemcpyDeviceToHost));
     if (s != TL_OK) return s;
-    if (v != 0) *code = TL_ERR_TIMEOUT;
+    if (v != 0) *code = v == TL_ERR_VALUE ? TL_ERR_VALUE : TL_ERR_TIMEOUT;
     if (clear && v != 0) s = from_cuda(cudaMemset(d->status, 0, sizeof(int)));
     return s;
 }
@@ -573,7 +585,7 @@ const char *ternary_status_string(int32_t status) {
     case TL_ERR_SHAPE: return "TL_ERR_SHAPE: invalid or unsupported sizes";
     case TL_ERR_DTYPE: return "TL_ERR_DTYPE: unknown dtype, group size (0, 32, 64, 128, 256) or path code";
     case TL_ERR_ALIGN: return "TL_ERR_ALIGN: pointer not 16-byte aligned";
-    case TL_ERR_VALUE: return "TL_ERR_VALUE: invalid or reserved values present";
+    case TL_ERR_VALUE: return "TL_ERR_VALUE: an index out of range, or invalid or reserved values present";
     case TL_ERR_CUDA: return "TL_ERR_CUDA: a CUDA call or kernel launch failed";
     case TL_ERR_TIMEOUT: return "TL_ERR_TIMEOUT: a bounded device-side wait gave up";
     case TL_ERR_UNSUPPORTED: return "TL_ERR_UNSUPPORTED: no sm_103 device, or the forced path "

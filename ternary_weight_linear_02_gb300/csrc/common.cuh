@@ -202,6 +202,12 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
 
 // Device status word codes (written with atomicExch; 0 = OK)
 constexpr int kStatusTimeout = 7;
+// an index read on the device (slot, position, page, length) was out of range;
+// does not replace a code already set
+constexpr int kStatusValue = 5;
+__device__ __forceinline__ void flag_value(int *status) {
+    if (status) atomicCAS(status, 0, kStatusValue);
+}
 
 __device__ __forceinline__ uint2 ldg_nc_v2(const void *p) {
     uint2 r;

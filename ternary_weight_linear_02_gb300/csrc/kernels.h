@@ -8,6 +8,13 @@
 
 namespace tl {
 
+// ------------------------------------------------------------ shared by the ABI files
+struct CallDevice {
+    int sm_count;
+    int *status;  // device status word
+};
+int begin_call(CallDevice *out);  // a tl_status (api.cu)
+
 // ------------------------------------------------------------ pack / unpack
 cudaError_t launch_unpack(const uint8_t *packed, int8_t *t, int64_t nbytes,
                           unsigned long long *reserved, int sm_count, cudaStream_t st);
@@ -187,5 +194,83 @@ struct GenArgs {
 };
 cudaError_t launch_generic(const GenArgs &a, bool bf, bool group, bool silu, cudaStream_t st,
                            bool pdl);
+
+// ------------------------------------------------------------ rotary positions
+struct RopeTableArgs {
+    float *table;  // [positions, R]
+    int64_t positions;
+    int R;
+    double base, factor, original_len, ramp_lo, ramp_hi, magnitude;
+};
+cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t st);
+
+struct RopeArgs {
+    const void *x;
+    void *out;
+    int64_t xt, xh, ot, oh;  // token and head strides (elements)
+    const int64_t *positions;
+    const float *table;      // [table_rows, R]: cosines, then sines
+    int64_t table_rows;
+    int64_t tokens;
+    int heads, D, R;
+    int inverse;
+    int *status;
+};
+cudaError_t launch_rope(const RopeArgs &a, int dtype, bool interleaved, bool vec, int sm_count,
+                        cudaStream_t st);
+
+// ------------------------------------------------------------ quantised cache
+struct KvCache {
+    uint8_t *kc, *vc;    // codes [pages, Hk, P, row bytes]
+    float *ks, *vs;      // scales [pages, Hk, P]
+    int64_t pages;
+    int P, Hk, D, fmt;   // page size, kv heads, head size, tl_kv_format
+};
+
+struct KvAppendArgs {
+    KvCache c;
+    const void *k, *v, *q;
+    void *qo;
+    int64_t kt, kh, vt, vh, qt, qh, qot, qoh;  // token and head strides (elements)
+    const int64_t *slots, *positions;
+    const float *table;
+    int64_t table_rows, tokens;
+    int Hq, R;
+    int *status;
+};
+// vec: every row of q, k, v, q_out starts on a 16-byte boundary
+cudaError_t launch_kv_append(const KvAppendArgs &a, bool bf, bool interleaved, bool vec,
+                             cudaStream_t st);
+
+struct KvReadArgs {
+    KvCache c;
+    const int64_t *slots;
+    int64_t tokens;
+    void *k, *v;
+    int *status;
+};
+cudaError_t launch_kv_read(const KvReadArgs &a, int out_dtype, cudaStream_t st);
+
+// ------------------------------------------------------------ tree attention
+struct AttnArgs {
+    KvCache c;
+    const void *q;
+    int64_t qb, qt, qh;  // strides (elements)
+    const int *pages;    // page table
+    int64_t pages_stride;
+    int64_t max_keys;    // keys a page-table row holds
+    const int *ctx;
+    const uint8_t *tree;
+    int64_t tree_b, tree_r;
+    float scale;
+    void *out;
+    float *lse;
+    float *ws;
+    int B, T, Hq, G;     // batch, new tokens, query heads, query heads per kv head
+    int q_vec;           // every q row starts on a 16-byte boundary
+    int *status;
+};
+cudaError_t launch_tree_attention(const AttnArgs &a, bool bf, int sm_count, cudaStream_t st);
+int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D);
 
 }  // namespace tl
