@@ -200,7 +200,8 @@ static bool attention_sizes(int64_t batch, int64_t draft, int32_t q_heads, int32
     if (kv_heads < 1 || kv_heads > (1 << 16) || q_heads < 1 || q_heads > (1 << 16) || q_heads % kv_heads != 0)
         return false;
     if (head_dim != 64 && head_dim != 128) return false;
-    return batch * draft * q_heads < kMaxTokens;
+    // rows, rounded up to whole row blocks, are counted in 31 bits
+    return batch * kv_heads * (draft * (q_heads / kv_heads) + 128) < kMaxTokens;
 }
 
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,

@@ -270,6 +270,11 @@ struct AttnArgs {
     int q_vec;           // every q row starts on a 16-byte boundary
     int *status;
 };
+// SMs that a workspace is laid out for (the GPU has 152; more are left unused)
+constexpr int kMaxSms = 160;
+cudaError_t launch_stream_int8(const AttnArgs &a, bool bf, int nc, cudaStream_t st);
+cudaError_t launch_stream_fp8(const AttnArgs &a, bool bf, int nc, cudaStream_t st);
+cudaError_t launch_stream_int4(const AttnArgs &a, bool bf, int nc, cudaStream_t st);
 cudaError_t launch_tree_attention(const AttnArgs &a, bool bf, int sm_count, cudaStream_t st);
 int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D);
 
