@@ -169,22 +169,17 @@ __device__ __forceinline__ int attn_page(const AttnArgs &a, int b, int key) {
     return p;
 }
 
-// Joins the partial results of each unit that more than one block worked on: one block
-// per (unit, row), its four warps sharing the partial results, sums in block order.
-// Launched as a dependent of the main kernel, so it computes its place meanwhile.
-template <bool BF, int KT, int ROWS, int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, int nc) {
-    __shared__ int64_t sh[8];
-    __shared__ float sm[4], sl[4], so[4][D];
-    constexpr int E = D / 32;
+// Where a unit's partial results lie: blocks c0 .. c1 (c0 == c1: none, its one block wrote
+// the output), the first of them in slot `first`.  Executed by a whole block of 128
+// threads; sh: 8 64-bit words.
+struct AttnParts {
+    int c0, c1, first;
+    int64_t N;
+};
+template <int KT>
+__device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int unit, int units, int nc, int64_t *sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int R = a.T * a.G, units = a.c.Hk * rtiles;
-    const int row = blockIdx.x % ROWS;
-    const int64_t u = blockIdx.x / ROWS;
-    const int b = (int)(u / units), unit = (int)(u % units), hk = unit / rtiles, rt = unit % rtiles;
-    const int grow = rt * ROWS + row;  // row of the (sequence, kv head)
-    // tiles before sequence b, and all of them
-    int64_t pre = 0, all = 0;
+    int64_t pre = 0, all = 0;  // tiles before sequence b, and of the call
     for (int i = threadIdx.x; i < a.B; i += 128) {
         const int64_t n = attn_tiles<KT>(a, i, units);
         all += n;
@@ -197,29 +192,31 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
     }
     if (lane == 0) sh[warp] = pre, sh[4 + warp] = all;
     __syncthreads();
+    AttnParts r;
     pre = sh[0] + sh[1] + sh[2] + sh[3];
-    const int64_t N = sh[4] + sh[5] + sh[6] + sh[7];
-    const int64_t tiles = attn_tiles<KT>(a, b, 1);
-    const int64_t s = pre + unit * tiles;
-    const int c0 = attn_block_of(s, N, nc), c1 = attn_block_of(s + tiles - 1, N, nc);
-    pdl_wait();
-    if (c0 == c1 || grow >= R) return;
-    using Slot = AttnSlot<ROWS, D>;
-    const int first = attn_first_tile(c0, N, nc) == s ? 0 : 1;  // slot of the unit in its first block
+    r.N = sh[4] + sh[5] + sh[6] + sh[7];
+    const int64_t tiles = attn_tiles<KT>(a, b, 1), s = pre + unit * tiles;
+    r.c0 = attn_block_of(s, r.N, nc);
+    r.c1 = attn_block_of(s + tiles - 1, r.N, nc);
+    r.first = attn_first_tile(r.c0, r.N, nc) == s ? 0 : 1;
+    return r;
+}
+
+// A row's running maximum, sum and this lane's E = D / 32 outputs, and one more partial result.
+template <int E>
+struct AttnSum {
     float m = kAttnLow, l = 0.f, o[E];
+    __device__ __forceinline__ AttnSum() {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    // blocks with no tile (N < nc) lie between: they hold nothing of the unit
-    for (int c = c0 + warp; c <= c1; c += 4) {
-        if (attn_first_tile(c, N, nc) == attn_first_tile(c + 1, N, nc)) continue;
-        const float *p = Slot::at(a.ws, c, c == c0 ? first : 0);
-        const float pm = p[ROWS * D + row], pl = p[ROWS * (D + 1) + row];
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+    }
+    __device__ __forceinline__ void add(float pm, float pl, const float *row, int lane) {
         float v[E];
         if constexpr (E == 4) {
-            const float4 x = reinterpret_cast<const float4 *>(p + row * D)[lane];
+            const float4 x = reinterpret_cast<const float4 *>(row)[lane];
             v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         } else {
-            const float2 x = reinterpret_cast<const float2 *>(p + row * D)[lane];
+            const float2 x = reinterpret_cast<const float2 *>(row)[lane];
             v[0] = x.x, v[1] = x.y;
         }
         const float mn = fmaxf(m, pm), f = ex2(m - mn), g = ex2(pm - mn);
@@ -228,22 +225,85 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[e] * g;
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
+};
+
+// Joins the partial results of each unit that more than one block worked on, in block
+// order; the grid covers every unit, and blocks of units with nothing to join leave.
+// Launched as a dependent of the main kernel: the place is computed meanwhile.
+// WIDE (few rows, many parts: single tokens over long contexts): one block per row,
+// its four warps sharing the parts.  Otherwise 16 rows per block, each warp taking
+// whole rows.
+template <bool BF, int KT, int ROWS, int D, bool WIDE>
+__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
+    __shared__ int64_t sh[8];
+    __shared__ float sm[4], sl[4], so[4][D];
+    constexpr int E = D / 32;
+    using Slot = AttnSlot<ROWS, D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int R = a.T * a.G, units = a.c.Hk * rtiles;
+    const int64_t u = blockIdx.x / per_unit;
+    const int slice = blockIdx.x % per_unit;
+    const int b = (int)(u / units), unit = (int)(u % units), hk = unit / rtiles, rt = unit % rtiles;
+    const AttnParts p = attn_parts<KT>(a, b, unit, units, nc, sh);
+    pdl_wait();
+    if (p.c0 == p.c1) return;
+    // the output row of row `grow` of the unit's (sequence, kv head)
+    auto out_row = [&](int grow) { return ((int64_t)b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G; };
+    // blocks without a tile (fewer tiles than blocks) lie between and hold nothing
+    auto part = [&](int c) -> const float * {
+        if (attn_first_tile(c, p.N, nc) == attn_first_tile(c + 1, p.N, nc)) return nullptr;
+        return Slot::at(a.ws, c, c == p.c0 ? p.first : 0);
+    };
+    if constexpr (WIDE) {
+        const int row = slice;
+        AttnSum<E> s;
+        for (int c = p.c0 + warp; c <= p.c1; c += 4)
+            if (const float *x = part(c)) s.add(x[ROWS * D + row], x[ROWS * (D + 1) + row], x + row * D, lane);
+        if (lane == 0) sm[warp] = s.m, sl[warp] = s.l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    __syncthreads();
-    const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float L = 0.f, x = 0.f;
-    const int d = threadIdx.x;
+        for (int e = 0; e < E; ++e) so[warp][lane * E + e] = s.o[e];
+        __syncthreads();
+        const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+        float L = 0.f, x = 0.f;
+        const int d = threadIdx.x;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float g = ex2(sm[w] - M);
-        L += sl[w] * g;
-        if (d < D) x += so[w][d] * g;
+        for (int w = 0; w < 4; ++w) {
+            const float g = ex2(sm[w] - M);
+            L += sl[w] * g;
+            if (d < D) x += so[w][d] * g;
+        }
+        const int64_t o = out_row(row);
+        if (d < D) OutStore<BF ? 1 : 0>::st(a.out, o * D + d, L == 0.f ? 0.f : x / L);
+        if (a.lse && d == 0) a.lse[o] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    } else {
+        for (int row = slice * 16 + warp; row < slice * 16 + 16; row += 4) {
+            const int grow = rt * ROWS + row;
+            if (grow >= R) return;
+            AttnSum<E> s;
+            for (int c = p.c0; c <= p.c1; ++c)
+                if (const float *x = part(c)) s.add(x[ROWS * D + row], x[ROWS * (D + 1) + row], x + row * D, lane);
+            const int64_t o = out_row(grow);
+            const float r = s.l == 0.f ? 0.f : 1.f / s.l;
+#pragma unroll
+            for (int e = 0; e < E; ++e) OutStore<BF ? 1 : 0>::st(a.out, o * D + lane * E + e, s.o[e] * r);
+            if (a.lse && lane == 0) a.lse[o] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
+        }
     }
-    const int64_t out_row = ((int64_t)b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G;
-    if (d < D) OutStore<BF ? 1 : 0>::st(a.out, out_row * D + d, L == 0.f ? 0.f : x / L);
-    if (a.lse && d == 0) a.lse[out_row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+template <bool BF, int KT, int ROWS, int D, bool WIDE>
+cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
+    const int R = a.T * a.G, per_unit = WIDE ? R : ((R < ROWS ? R : ROWS) + 15) / 16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.c.Hk * rtiles * per_unit), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF, KT, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
 }
 
 }  // namespace tl

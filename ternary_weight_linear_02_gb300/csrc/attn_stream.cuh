@@ -1,20 +1,22 @@
 // attn_stream.cuh -- attention for few rows per kv head (single tokens, small trees):
 // the cache streams through registers once, fed to warp MMAs.
 //
-//   S = Q K^T, P = exp2(S sk f - m) sv, O += P V    (f = scale log2 e)
+//   S^T = K Q^T, P = exp2(S sk f - m) sv, O^T += V^T P^T    (f = scale log2 e)
 //
 // For at most 16 rows the bytes of the cache bound the call (16 rows x 4 flops per
 // 8-bit element: about 32 flops a byte), so everything is laid out for the stream:
+//  * keys are the 16-wide side of mma.m16n8k16 and rows the 8-wide one: blocks of up to 8
+//    rows (NB = 1) need half the MMAs, exponentials and registers of the other way round.
 //  * a tile is 64 keys, 16 for each of the block's 4 warps; warps share nothing until a
 //    unit ends.  Pages hold multiples of 16 keys, so a warp's 16 keys lie in one page.
 //  * each thread copies exactly the bytes that its own MMA fragments need, with
 //    cp.async into a ring of its warp, several tiles ahead: no block barriers in the
-//    loop, and no fragment is exchanged.  mma.m16n8k16 leaves the order of the
-//    contracted axis free, so thread t of a quad takes 16 neighbouring elements of a
-//    key (and of the next 64) for S, and for V its four keys' elements
-//    [g D/8, (g + 1) D/8) of column group g: every global read is 64 or 128 bytes of
-//    one row over a quad or eight lanes.
-//  * S comes out in the layout in which P enters the second product.
+//    loop, and no fragment is exchanged.  The order of the contracted axis and of the
+//    output's elements is free, so thread t of a quad takes 16 neighbouring elements of
+//    keys g and g + 8 (and of the next 64) for S, and of its four keys' values the
+//    elements [g D/8, (g + 1) D/8): every global read is 64 or 128 bytes of one row
+//    over a quad or eight lanes.
+//  * P changes from (keys x rows) to (rows x keys) fragments by one movmatrix per 8 keys.
 //  * codes become f16 (exact); the products are exact, sums fp32.  Queries in bf16
 //    enter as f16 scaled by the power of two of their row's largest element: exact
 //    within 2^-14 of it, below that rounded at 2^-25 of it, far under the fp32 sums.
@@ -33,7 +35,7 @@ namespace tl {
 
 namespace {
 
-constexpr int kStreamKeys = 64, kStreamRows = 16, kStreamThreads = 128;
+constexpr int kStreamKeys = 64, kStreamThreads = 128;
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool valid) {
@@ -48,6 +50,12 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -76,8 +84,9 @@ __device__ __forceinline__ uint32_t int4_hi(uint32_t x) {  // 1024 + 16 u
     return h2_bits(__hfma2(h2_of((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int NB>
 struct StreamCfg {
+    static constexpr int ROWS = 8 * NB;
     static constexpr int RB = D * KvCode<FMT>::bits / 8;  // bytes per row of codes
     static constexpr int KB = RB / 4;                     // bytes of a key per thread (scores)
     static constexpr int KC = KB > 16 ? 16 : KB;          // bytes per copy
@@ -87,108 +96,128 @@ struct StreamCfg {
     // one stage of one warp: keys' copies, values' copies, 16 + 16 scales
     static constexpr int KOFF = 0, VOFF = 2 * NKC * KC * 32, SOFF = VOFF + 4 * VB * 32;
     static constexpr int STAGE = SOFF + 128;
+    static constexpr int BLOCKS = NB == 1 ? 4 : 3;        // per SM (registers)
     static constexpr int NS = STAGE > 3000 ? 3 : STAGE > 2000 ? 5 : 8;  // stages per warp
-    static constexpr int PITCH = D == 128 ? 144 : 80;     // floats per row of the join buffer
-    // [stages of 4 warps][join rows][queries f16][row factors][per-warp max, sum, svref]
+    static constexpr int PITCH = D + 8;                   // floats per row of the join buffer
+    // [stages of 4 warps][join rows; at a unit's start, its queries in f16]
+    // [row factors][per-warp maxima and sums][place]
     static constexpr int JOFF = 4 * NS * STAGE;
-    static constexpr int QOFF = JOFF + kStreamRows * PITCH * 4;
-    static constexpr int FOFF = QOFF + kStreamRows * (D + 8) * 2;
-    static constexpr int WOFF = FOFF + kStreamRows * 4;
-    static constexpr int POFF = WOFF + 3 * 4 * kStreamRows * 4;
+    static constexpr int FOFF = JOFF + ROWS * PITCH * 4;
+    static constexpr int WOFF = FOFF + ROWS * 4;
+    static constexpr int POFF = WOFF + 2 * 4 * ROWS * 4;
     static constexpr int SMEM = POFF + 64;
-    static_assert(3 * (SMEM + 1024) <= 228 * 1024, "three blocks per SM");
+    static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
 };
 
-template <int FMT, bool BF, int D>
-__global__ void __launch_bounds__(kStreamThreads, 3) attn_stream_kernel(AttnArgs a, int rtiles) {
-    using C = StreamCfg<FMT, D>;
+template <int FMT, bool BF, int D, int NB>
+__global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS) attn_stream_kernel(AttnArgs a) {
+    using C = StreamCfg<FMT, D, NB>;
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    constexpr int KT = kStreamKeys, ROWS = kStreamRows, NT = D / 8;
+    constexpr int KT = kStreamKeys, ROWS = C::ROWS, NT = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int nc = gridDim.x, units = a.c.Hk * rtiles, R = a.T * a.G;
+    const int nc = gridDim.x, R = a.T * a.G;
     pdl_launch_dependents();
 
-    AttnPlace place = attn_place<KT, kStreamThreads>(a, units, reinterpret_cast<int64_t *>(smem + C::POFF),
-                                                     [&](int64_t N) { return attn_first_tile(blockIdx.x, N, nc); });
+    const AttnPlace place = attn_place<KT, kStreamThreads>(a, a.c.Hk, reinterpret_cast<int64_t *>(smem + C::POFF),
+                                                           [&](int64_t N) { return attn_first_tile(blockIdx.x, N, nc); });
     const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
     if (x0 == x1) return;
     const int steps = (int)(x1 - x0);
 
     uint8_t *ring = smem + warp * C::NS * C::STAGE;
-    const uint32_t ring_u32 = smem_u32(ring);
-    AttnWalk in, out;  // the tile being copied, the tile being computed
+    AttnWalk in, out;  // the tile being copied, the tile being computed (unit = kv head)
     in.template start<KT>(a, place, x0);
     out = in;
 
     // Copies run NS - 1 tiles ahead; the page of the tile after that is already on its way.
-    auto first_key = [&](const AttnWalk &w) { return w.tile * KT + warp * 16; };
-    auto page_of = [&](const AttnWalk &w) {
-        const int key = first_key(w);
-        return key < w.ctx + a.T ? attn_page(a, w.b, key) : -1;
+    // pi, off: page index and place in it of this warp's first key of the tile `in`.
+    int pi, off, page;
+    auto locate = [&]() {
+        const unsigned key = (unsigned)(in.tile * KT + warp * 16);
+        pi = (int)(key / (unsigned)a.c.P);
+        off = (int)(key - (unsigned)pi * (unsigned)a.c.P);
     };
-    int page = page_of(in);
-    auto issue = [&](int step) {
-        const int key = first_key(in), L = in.ctx + a.T;
-        const uint32_t st = ring_u32 + (uint32_t)(step % C::NS) * C::STAGE;
-        if (page >= 0) {
-            const int hk = in.unit / rtiles;
-            const int64_t row = ((int64_t)page * a.c.Hk + hk) * a.c.P + (unsigned)key % (unsigned)a.c.P;
-            const uint8_t *kp = a.c.kc + row * C::RB, *vp = a.c.vc + row * C::RB;
+    auto fetch_page = [&]() {
+        page = in.tile * KT + warp * 16 < in.ctx + a.T ? __ldg(a.pages + in.b * a.pages_stride + pi) : -1;
+    };
+    locate();
+    fetch_page();
+    const uint32_t dst0 = smem_u32(ring) + lane * C::KC;
+    const int ksrc = g * C::RB + t * C::KC, vsrc = 2 * t * C::RB + g * C::VB;
+    int put = 0;  // stage being filled
+    auto issue = [&](bool more) {
+        const int left = in.ctx + a.T - (in.tile * KT + warp * 16);  // keys from the warp's first one on
+        if (left > 0) {
+            if ((unsigned)page >= (unsigned)a.c.pages) {
+                flag_value(a.status);
+                page = 0;
+            }
+            const int64_t row = ((int64_t)page * a.c.Hk + in.unit) * a.c.P + off;
+            const uint8_t *kp = a.c.kc + row * C::RB + ksrc, *vp = a.c.vc + row * C::RB + vsrc;
+            const uint32_t st = dst0 + (uint32_t)put * C::STAGE;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int j = 0; j < C::NKC; ++j)
-                    cp_async<C::KC>(st + C::KOFF + ((n * C::NKC + j) * 32 + lane) * C::KC,
-                                    kp + (n * 8 + g) * C::RB + j * 4 * C::KC + t * C::KC, key + n * 8 + g < L);
+                    cp_async<C::KC>(st + C::KOFF + (n * C::NKC + j) * 32 * C::KC, kp + n * 8 * C::RB + j * 4 * C::KC,
+                                    n * 8 + g < left);
+            const uint32_t sv = st + C::VOFF - lane * (C::KC - C::VB);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = 2 * t + (j & 1) + (j >> 1) * 8;
-                cp_async<C::VB>(st + C::VOFF + (j * 32 + lane) * C::VB, vp + r * C::RB + g * C::VB, key + r < L);
+                const int r = (j & 1) + (j >> 1) * 8;
+                cp_async<C::VB>(sv + j * 32 * C::VB, vp + r * C::RB, 2 * t + r < left);
             }
             if (lane < 8)
-                cp_async<16>(st + C::SOFF + lane * 16, (lane < 4 ? a.c.ks : a.c.vs) + row + (lane & 3) * 4, true);
+                cp_async<16>(st + C::SOFF + lane * (16 - C::KC), (lane < 4 ? a.c.ks : a.c.vs) + row + (lane & 3) * 4, true);
         }
         cp_commit();
-        if (step + 1 < steps) {
-            in.template next<KT>(a, units);
-            page = page_of(in);
+        put = put + 1 == C::NS ? 0 : put + 1;
+        if (more) {
+            const int b = in.b, unit = in.unit;
+            in.template next<KT>(a, a.c.Hk);
+            if (in.b == b && in.unit == unit) {
+                off += KT;
+                while (off >= a.c.P) off -= a.c.P, ++pi;
+            } else {
+                locate();
+            }
+            fetch_page();
         }
     };
-    int issued = 0;
 #pragma unroll 1
-    for (; issued < C::NS - 1; ++issued) {
-        if (issued < steps) issue(issued);
+    for (int i = 0; i < C::NS - 1; ++i) {
+        if (i < steps) issue(i + 1 < steps);
         else cp_commit();
     }
 
-    uint32_t qf[C::KSTEPS][4];
-    float f0 = 0.f, f1 = 0.f;              // score factors of rows g and g + 8
-    float m0 = kAttnLow, m1 = kAttnLow, l0 = 0.f, l1 = 0.f, svref = 1e-30f;
-    float acc[NT][4];
-    int tok0 = 0, tok1 = 0;                // new token of rows g and g + 8
+    uint32_t qf[NB][C::KSTEPS][2];
+    float f[NB][2];                        // score factors of rows 8 n + 2t and + 1
+    float m[NB][2], l[NB][2], svref = 1e-30f;
+    float acc[NB][NT][4];
     bool fresh = true;                     // the next tile begins a unit (for this block)
-    int which = 0;                         // slot of a partial result
+    int which = 0, get = 0;                // slot of a partial result; stage being read
 
 #pragma unroll 1
     for (int step = 0; step < steps; ++step) {
-        const int hk = out.unit / rtiles, rt = out.unit % rtiles;
         if (fresh) {
             // ---------------- queries of the unit: rows as f16 in shared memory, then fragments
             fresh = false;
-            const int row = threadIdx.x >> 3, part = threadIdx.x & 7, grow = rt * ROWS + row;
-            constexpr int EPT = D / 8;
+            constexpr int TPR = kStreamThreads / ROWS, EPT = D / TPR;  // threads per row, elements per thread
+            const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
             float v[EPT];
-            if (grow < R) {
-                const T *q = static_cast<const T *>(a.q) + out.b * a.qb + (int64_t)(grow / a.G) * a.qt +
-                             (int64_t)(hk * a.G + grow % a.G) * a.qh + part * EPT;
-                if (a.q_vec) {
+            if (row < R) {
+                const T *q = static_cast<const T *>(a.q) + out.b * a.qb + (int64_t)(row / a.G) * a.qt +
+                             (int64_t)(out.unit * a.G + row % a.G) * a.qh + part * EPT;
+                if (EPT % 8 == 0 && a.q_vec) {
+                    if constexpr (EPT % 8 == 0) {
 #pragma unroll
-                    for (int i = 0; i < EPT; i += 8) {
-                        float u[8];
-                        ld8(q + i, u);
+                        for (int i = 0; i < EPT; i += 8) {
+                            float u[8];
+                            ld8(q + i, u);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[i + k] = u[k];
+                            for (int k = 0; k < 8; ++k) v[i + k] = u[k];
+                        }
                     }
                 } else {
 #pragma unroll
@@ -204,327 +233,296 @@ __global__ void __launch_bounds__(kStreamThreads, 3) attn_stream_kernel(AttnArgs
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) mx = fmaxf(mx, fabsf(v[i]));
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                for (int o = TPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const int e = (int)(__float_as_uint(mx) >> 23);  // biased exponent of the largest
                 if (e > 0 && e < 254) {
                     down = __uint_as_float((uint32_t)(254 - e) << 23);
                     up = __uint_as_float((uint32_t)e << 23);
                 }
             }
-            __half *qs = reinterpret_cast<__half *>(smem + C::QOFF) + row * (D + 8) + part * EPT;
+            __half *qs = reinterpret_cast<__half *>(smem + C::JOFF) + row * (D + 8) + part * EPT;
 #pragma unroll
             for (int i = 0; i < EPT; i += 2)
                 *reinterpret_cast<__half2 *>(qs + i) = __floats2half2_rn(v[i] * down, v[i + 1] * down);
             float *fac = reinterpret_cast<float *>(smem + C::FOFF);
             if (part == 0) fac[row] = a.scale * kLog2e * up;
             __syncthreads();
-            const __half *qr = reinterpret_cast<const __half *>(smem + C::QOFF);
-            auto pair = [&](int r, int d0, int d1) {
-                const uint32_t lo = __half_as_ushort(qr[r * (D + 8) + d0]), hi = __half_as_ushort(qr[r * (D + 8) + d1]);
-                return lo | (hi << 16);
-            };
+            const uint16_t *qr = reinterpret_cast<const uint16_t *>(smem + C::JOFF);
 #pragma unroll
-            for (int s = 0; s < C::KSTEPS; ++s) {
-                int d0, d1, d2, d3;  // the elements of this thread in step s, in the order its code words give
-                if constexpr (FMT == kKvInt4) {
-                    const int e = t * (D / 4) + (s >> 1) * 8 + (s & 1) * 2;
-                    d0 = e, d1 = e + 4, d2 = e + 1, d3 = e + 5;
-                } else {
-                    const int e = (s >> 2) * 64 + t * 16 + (s & 3) * 4;
-                    d0 = e, d1 = e + 1, d2 = e + 2, d3 = e + 3;
+            for (int n = 0; n < NB; ++n) {
+                const uint16_t *r = qr + (8 * n + g) * (D + 8);
+#pragma unroll
+                for (int s = 0; s < C::KSTEPS; ++s) {
+                    // the elements of this thread in step s, in the order its code words give
+                    if constexpr (FMT == kKvInt4) {
+                        const uint16_t *p = r + t * (D / 4) + (s >> 1) * 8 + (s & 1) * 2;
+                        qf[n][s][0] = p[0] | ((uint32_t)p[4] << 16);
+                        qf[n][s][1] = p[1] | ((uint32_t)p[5] << 16);
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(r + (s >> 2) * 64 + t * 16 + (s & 3) * 4);
+                        qf[n][s][0] = u.x;
+                        qf[n][s][1] = u.y;
+                    }
                 }
-                qf[s][0] = pair(g, d0, d1);
-                qf[s][1] = pair(g + 8, d0, d1);
-                qf[s][2] = pair(g, d2, d3);
-                qf[s][3] = pair(g + 8, d2, d3);
-            }
-            f0 = fac[g];
-            f1 = fac[g + 8];
-            tok0 = min(R - 1, rt * ROWS + g) / a.G;
-            tok1 = min(R - 1, rt * ROWS + g + 8) / a.G;
-            m0 = m1 = kAttnLow;
-            l0 = l1 = 0.f;
-            svref = 1e-30f;
+                f[n][0] = fac[8 * n + 2 * t];
+                f[n][1] = fac[8 * n + 2 * t + 1];
+                m[n][0] = m[n][1] = kAttnLow;
+                l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-            __syncthreads();  // the queries' buffer may be written again
+                for (int i = 0; i < NT; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+            }
+            svref = 1e-30f;
+            __syncthreads();  // the queries' buffer is the join buffer too
         }
 
         // ---------------- one group of 16 keys
-        if (issued < steps) issue(issued);
+        if (step + C::NS - 1 < steps) issue(step + C::NS < steps);
         else cp_commit();
-        ++issued;
         cp_wait<C::NS - 1>();
         __syncwarp();  // the scales were copied by other lanes
-        const int key = first_key(out), L = out.ctx + a.T;
-        if (key < L) {
-            const uint8_t *st = ring + (step % C::NS) * C::STAGE;
-            float s[2][4];
+        const int key = out.tile * KT + warp * 16;
+        if (key < out.ctx + a.T) {
+            const uint8_t *st = ring + get * C::STAGE;
+            float s[NB][4], s2[NB][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-                uint32_t w[C::KB / 4];
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] = s2[n][j] = 0.f;
+            uint32_t w[2][C::KB / 4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int j = 0; j < C::NKC; ++j) {
                     const uint8_t *p = st + C::KOFF + ((n * C::NKC + j) * 32 + lane) * C::KC;
                     if constexpr (C::KC == 16) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(p);
-                        w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+                        w[n][4 * j] = u.x, w[n][4 * j + 1] = u.y, w[n][4 * j + 2] = u.z, w[n][4 * j + 3] = u.w;
                     } else {
                         const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                        w[0] = u.x, w[1] = u.y;
+                        w[n][0] = u.x, w[n][1] = u.y;
                     }
                 }
-                if constexpr (FMT == kKvInt4) {
+            // two chains of sums (even and odd steps): half the latency of one
 #pragma unroll
-                    for (int i = 0; i < C::KSTEPS / 2; ++i) {
-                        mma16816(s[n], qf[2 * i], int4_lo(w[i]), int4_hi(w[i]));
-                        mma16816(s[n], qf[2 * i + 1], int4_lo(w[i] >> 8), int4_hi(w[i] >> 8));
-                    }
-                } else {
+            for (int i = 0; i < C::KSTEPS; ++i) {
+                uint32_t x[4];
 #pragma unroll
-                    for (int i = 0; i < C::KSTEPS; ++i) {
-                        uint32_t b0, b1;
-                        if constexpr (FMT == kKvInt8) {
-                            const uint32_t u = w[i] ^ 0x80808080u;
-                            b0 = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4140));
-                            b1 = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4342));
-                        } else {
-                            b0 = e4m3x2_raw(w[i]);
-                            b1 = e4m3x2_raw(w[i] >> 16);
-                        }
-                        mma16816(s[n], qf[i], b0, b1);
+                for (int n = 0; n < 2; ++n) {
+                    if constexpr (FMT == kKvInt4) {
+                        const uint32_t u = i & 1 ? w[n][i >> 1] >> 8 : w[n][i >> 1];
+                        x[n] = int4_lo(u);
+                        x[2 + n] = int4_hi(u);
+                    } else if constexpr (FMT == kKvInt8) {
+                        const uint32_t u = w[n][i] ^ 0x80808080u;
+                        x[n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4140));
+                        x[2 + n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4342));
+                    } else {
+                        x[n] = e4m3x2_raw(w[n][i]);
+                        x[2 + n] = e4m3x2_raw(w[n][i] >> 16);
                     }
                 }
-            }
-            // keys of this thread: key + 2t, + 1, + 8 + 2t, + 1
-            const float2 ka = *reinterpret_cast<const float2 *>(st + C::SOFF + t * 8);
-            const float2 kb = *reinterpret_cast<const float2 *>(st + C::SOFF + 32 + t * 8);
-            const float2 va = *reinterpret_cast<const float2 *>(st + C::SOFF + 64 + t * 8);
-            const float2 vb = *reinterpret_cast<const float2 *>(st + C::SOFF + 96 + t * 8);
-            const float sk[4] = {ka.x, ka.y, kb.x, kb.y};
-            float sv[4] = {va.x, va.y, vb.x, vb.y};
-            // z: scores in powers of two, rows g and g + 8
-            float z0[4], z1[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                z0[j] = s[j >> 1][j & 1] * sk[j] * f0;
-                z1[j] = s[j >> 1][2 + (j & 1)] * sk[j] * f1;
+                for (int n = 0; n < NB; ++n) mma16816(i & 1 ? s2[n] : s[n], x, qf[n][i][0], qf[n][i][1]);
             }
-            uint32_t see0 = 0xFu, see1 = 0xFu;
-            const bool edge = key + 16 > out.ctx;  // new tokens' keys, or the end
-            if (edge) {
-                see0 = see1 = 0u;
+            const float *sc = reinterpret_cast<const float *>(st + C::SOFF);
+            const float sk[2] = {sc[g], sc[g + 8]};
+            float sv[2] = {sc[16 + g], sc[24 + g]};
+            // z: scores in powers of two; [0], [1]: key g of rows 2t, 2t + 1; [2], [3]: key g + 8
+            float z[NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[n][j] = (s[n][j] + s2[n][j]) * sk[j >> 1] * f[n][j & 1];
+            uint32_t unseen = 0;
+            if (key + 16 > out.ctx) {  // new tokens' keys, or the end
                 const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
+                bool any[2] = {false, false};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = key + 2 * t + (j & 1) + (j >> 1) * 8 - out.ctx;  // index of the new token
-                    bool u0 = i < 0, u1 = i < 0;
-                    if (i >= 0 && i < a.T) {
-                        u0 = tree ? tree[tok0 * a.tree_r + i] != 0 : i <= tok0;
-                        u1 = tree ? tree[tok1 * a.tree_r + i] != 0 : i <= tok1;
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = key + g + (j >> 1) * 8 - out.ctx;  // index of the new token
+                        const int tok = min(R - 1, 8 * n + 2 * t + (j & 1)) / a.G;
+                        bool u = i < 0;
+                        if (i >= 0 && i < a.T) u = tree ? tree[tok * a.tree_r + i] != 0 : i <= tok;
+                        if (u) any[j >> 1] = true;
+                        else z[n][j] = -INFINITY, unseen |= 1u << (4 * n + j);
                     }
-                    if (u0) see0 |= 1u << j;
-                    else z0[j] = -INFINITY;
-                    if (u1) see1 |= 1u << j;
-                    else z1[j] = -INFINITY;
-                    if (!u0 && !u1) sv[j] = 0.f;  // unseen scales may hold anything
-                }
+                if (!any[0]) sv[0] = 0.f;  // unseen scales may hold anything
+                if (!any[1]) sv[1] = 0.f;
             }
-            const float x0v = fmaxf(fmaxf(z0[0], z0[1]), fmaxf(z0[2], z0[3]));
-            const float x1v = fmaxf(fmaxf(z1[0], z1[1]), fmaxf(z1[2], z1[3]));
-            const float svm = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-            if (__any_sync(0xffffffffu, x0v > m0 + kAttnSlack || x1v > m1 + kAttnSlack || svm > svref)) {
-                float r0 = x0v, r1 = x1v, rv = svm;
+            bool move = fmaxf(sv[0], sv[1]) > svref;
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, o));
-                    r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, o));
-                }
+            for (int n = 0; n < NB; ++n)
+                move = move || fmaxf(z[n][0], z[n][2]) > m[n][0] + kAttnSlack || fmaxf(z[n][1], z[n][3]) > m[n][1] + kAttnSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                float rv = fmaxf(sv[0], sv[1]), cv = 1.f;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) rv = fmaxf(rv, __shfl_xor_sync(0xffffffffu, rv, o));
-                r0 = fmaxf(r0, m0);
-                r1 = fmaxf(r1, m1);
-                const float c0 = ex2(m0 - r0), c1 = ex2(m1 - r1);
-                float cv = 1.f;
                 if (rv > svref) {  // twice the largest: the next slightly larger one changes nothing
                     cv = svref / (2.f * rv);
                     svref = 2.f * rv;
                 }
-                m0 = r0;
-                m1 = r1;
-                l0 *= c0;
-                l1 *= c1;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    acc[i][0] *= c0 * cv;
-                    acc[i][1] *= c0 * cv;
-                    acc[i][2] *= c1 * cv;
-                    acc[i][3] *= c1 * cv;
-                }
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float x = fmaxf(z[n][r], z[n][2 + r]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                        x = fmaxf(x, m[n][r]);
+                        const float c = ex2(m[n][r] - x);
+                        m[n][r] = x;
+                        l[n][r] *= c;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            acc[n][i][r] *= c * cv;
+                            acc[n][i][2 + r] *= c * cv;
+                        }
+                    }
             }
             const float inv = __frcp_rn(svref);
-            float p0[4], p1[4];
+            const float wv[2] = {sv[0] * inv, sv[1] * inv};
+            uint32_t pb[NB][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float e0 = ex2(z0[j] - m0 + kAttnUp), e1 = ex2(z1[j] - m1 + kAttnUp);
-                l0 += e0;
-                l1 += e1;
-                const float w = sv[j] * inv;
-                p0[j] = e0 * w;
-                p1[j] = e1 * w;
-            }
-            if (edge) {
+            for (int n = 0; n < NB; ++n) {
+                float p[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!(see0 >> j & 1u)) p0[j] = 0.f;
-                    if (!(see1 >> j & 1u)) p1[j] = 0.f;
+                    const float e = ex2(z[n][j] - m[n][j & 1] + kAttnUp);
+                    l[n][j & 1] += e;
+                    p[j] = e * wv[j >> 1];
                 }
+                if (unseen) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (unseen >> (4 * n + j) & 1u) p[j] = 0.f;
+                }
+                pb[n][0] = transpose8x8(pack2(__half(), p[0], p[1]));
+                pb[n][1] = transpose8x8(pack2(__half(), p[2], p[3]));
             }
-            uint32_t pa[4];
-            pa[0] = pack2(__half(), p0[0], p0[1]);
-            pa[1] = pack2(__half(), p1[0], p1[1]);
-            pa[2] = pack2(__half(), p0[2], p0[3]);
-            pa[3] = pack2(__half(), p1[2], p1[3]);
-            // values: column d = (D / 8) n + i of MMA i belongs to lane group n
-            uint32_t w[4][C::VB / 4];
+            // values: elements 2i and 2i + 1 of lane group g's run are its rows of MMA i
+            uint32_t v[4][C::VB / 4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint8_t *p = st + C::VOFF + (j * 32 + lane) * C::VB;
                 if constexpr (C::VB == 16) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(p);
-                    w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
+                    v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
                 } else if constexpr (C::VB == 8) {
                     const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                    w[j][0] = u.x, w[j][1] = u.y;
+                    v[j][0] = u.x, v[j][1] = u.y;
                 } else {
-                    w[j][0] = *reinterpret_cast<const uint32_t *>(p);
+                    v[j][0] = *reinterpret_cast<const uint32_t *>(p);
                 }
             }
 #pragma unroll
             for (int i = 0; i < C::VB / 4; ++i) {
-                if constexpr (FMT == kKvInt4) {
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {  // elements 0-3, then 4-7, of the two keys of a pair
+                for (int hh = 0; hh < 2; ++hh) {
+                    if constexpr (FMT == kKvInt4) {  // elements 0-3, then 4-7, of the two keys of a pair
                         const uint32_t sel = hh ? 0x7632 : 0x5410;
-                        const uint32_t x = __byte_perm(w[0][i], w[1][i], sel), y = __byte_perm(w[2][i], w[3][i], sel);
-                        mma16816(acc[8 * i + 4 * hh], pa, int4_lo(x), int4_lo(y));
-                        mma16816(acc[8 * i + 4 * hh + 1], pa, int4_hi(x), int4_hi(y));
-                        mma16816(acc[8 * i + 4 * hh + 2], pa, int4_lo(x >> 8), int4_lo(y >> 8));
-                        mma16816(acc[8 * i + 4 * hh + 3], pa, int4_hi(x >> 8), int4_hi(y >> 8));
-                    }
-                } else {
+                        const uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
+                        const uint32_t a0[4] = {int4_lo(x), int4_hi(x), int4_lo(y), int4_hi(y)};
+                        const uint32_t a1[4] = {int4_lo(x >> 8), int4_hi(x >> 8), int4_lo(y >> 8), int4_hi(y >> 8)};
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {  // bytes 0, 1, then 2, 3, interleaved over the pair's keys
+                        for (int n = 0; n < NB; ++n) {
+                            mma16816(acc[n][4 * i + 2 * hh], a0, pb[n][0], pb[n][1]);
+                            mma16816(acc[n][4 * i + 2 * hh + 1], a1, pb[n][0], pb[n][1]);
+                        }
+                    } else {  // bytes 0, 1, then 2, 3, interleaved over the pair's keys
                         const uint32_t sel = hh ? 0x7362 : 0x5140;
-                        uint32_t x = __byte_perm(w[0][i], w[1][i], sel), y = __byte_perm(w[2][i], w[3][i], sel);
-                        uint32_t xa, xb, ya, yb;
+                        uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
+                        uint32_t a0[4];
                         if constexpr (FMT == kKvInt8) {
                             x ^= 0x80808080u;
                             y ^= 0x80808080u;
-                            xa = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4140));
-                            xb = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4342));
-                            ya = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4140));
-                            yb = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4342));
+                            a0[0] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4140));
+                            a0[1] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4342));
+                            a0[2] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4140));
+                            a0[3] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4342));
                         } else {
-                            xa = e4m3x2_f16x2(x);
-                            xb = e4m3x2_f16x2(x >> 16);
-                            ya = e4m3x2_f16x2(y);
-                            yb = e4m3x2_f16x2(y >> 16);
+                            a0[0] = e4m3x2_f16x2(x);
+                            a0[1] = e4m3x2_f16x2(x >> 16);
+                            a0[2] = e4m3x2_f16x2(y);
+                            a0[3] = e4m3x2_f16x2(y >> 16);
                         }
-                        mma16816(acc[4 * i + 2 * hh], pa, xa, ya);
-                        mma16816(acc[4 * i + 2 * hh + 1], pa, xb, yb);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) mma16816(acc[n][2 * i + hh], a0, pb[n][0], pb[n][1]);
                     }
                 }
             }
         }
         __syncwarp();  // every lane is done with the stage (its scales are shared)
+        get = get + 1 == C::NS ? 0 : get + 1;
 
         // ---------------- the end of a unit, or of the run: join the warps, write
         const bool last = out.tile + 1 == out.tiles;
         if (last || step + 1 == steps) {
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-            }
             float *wm = reinterpret_cast<float *>(smem + C::WOFF), *wl = wm + 4 * ROWS;
-            if (t == 0) {
-                wm[warp * ROWS + g] = m0;
-                wm[warp * ROWS + g + 8] = m1;
-                wl[warp * ROWS + g] = l0;
-                wl[warp * ROWS + g + 8] = l1;
-            }
-            __syncthreads();
-            float M0 = wm[g], M1 = wm[g + 8];
 #pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                M0 = fmaxf(M0, wm[i * ROWS + g]);
-                M1 = fmaxf(M1, wm[i * ROWS + g + 8]);
-            }
-            const float c0 = ex2(m0 - M0) * svref, c1 = ex2(m1 - M1) * svref;
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], o);
+                    if (g == 0) {
+                        wm[warp * ROWS + 8 * n + 2 * t + r] = m[n][r];
+                        wl[warp * ROWS + 8 * n + 2 * t + r] = l[n][r];
+                    }
+                }
+            __syncthreads();
             float *jb = reinterpret_cast<float *>(smem + C::JOFF);
-            constexpr int RUN = D / 4;  // this thread's neighbouring elements of a row
+            float c[NB][2];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float *p = wm + 8 * n + 2 * t + r;
+                    const float M = fmaxf(fmaxf(p[0], p[ROWS]), fmaxf(p[2 * ROWS], p[3 * ROWS]));
+                    c[n][r] = ex2(m[n][r] - M) * svref;
+                }
 #pragma unroll 1
             for (int turn = 0; turn < 4; ++turn) {
                 if (turn == warp) {
-                    float *r0 = jb + g * C::PITCH + t * (RUN + 4), *r1 = r0 + 8 * C::PITCH;
 #pragma unroll
-                    for (int e = 0; e < RUN; e += 4) {
-                        float4 u, v;
-                        float *pu = &u.x, *pv = &v.x;
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int i = (e + k) % NT, h = (e + k) / NT;
-                            pu[k] = acc[i][h] * c0;
-                            pv[k] = acc[i][2 + h] * c1;
+                        for (int r = 0; r < 2; ++r) {
+                            float2 *d = reinterpret_cast<float2 *>(jb + (8 * n + 2 * t + r) * C::PITCH + g * (D / 8));
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {  // elements 2i, 2i + 1 of the run
+                                float2 u = make_float2(acc[n][i][r] * c[n][r], acc[n][i][2 + r] * c[n][r]);
+                                if (turn > 0) u.x += d[i].x, u.y += d[i].y;
+                                d[i] = u;
+                            }
                         }
-                        float4 *d0 = reinterpret_cast<float4 *>(r0 + e), *d1 = reinterpret_cast<float4 *>(r1 + e);
-                        if (turn > 0) {
-                            const float4 x = *d0, y = *d1;
-                            u.x += x.x, u.y += x.y, u.z += x.z, u.w += x.w;
-                            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-                        }
-                        *d0 = u;
-                        *d1 = v;
-                    }
                 }
                 __syncthreads();
             }
             const bool whole = last && step >= out.tile;  // the block saw the unit from its first tile on
-            const int row = threadIdx.x >> 3, part = threadIdx.x & 7, grow = rt * ROWS + row;
-            if (grow < R) {
+            constexpr int TPR = kStreamThreads / ROWS, EPT = D / TPR;
+            const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
+            if (row < R) {
                 float M = wm[row], Ls = 0.f;
 #pragma unroll
                 for (int i = 1; i < 4; ++i) M = fmaxf(M, wm[i * ROWS + row]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) Ls += wl[i * ROWS + row] * ex2(wm[i * ROWS + row] - M);
-                constexpr int EPT = D / 8;
-                const float *src = jb + row * C::PITCH + (part * EPT) / RUN * (RUN + 4) + (part * EPT) % RUN;
-                float v[EPT];
-#pragma unroll
-                for (int e = 0; e < EPT; e += 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(src + e);
-                    v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
-                }
+                const float *src = jb + row * C::PITCH + part * EPT;
                 if (whole) {
                     const float rl = Ls == 0.f ? 0.f : 1.f / Ls;
-                    const int64_t out_row = ((int64_t)out.b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G;
-                    T *o = static_cast<T *>(a.out) + out_row * D + part * EPT;
+                    const int64_t out_row = ((int64_t)out.b * a.T + row / a.G) * a.Hq + out.unit * a.G + row % a.G;
+                    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + out_row * D + part * EPT);
 #pragma unroll
-                    for (int e = 0; e < EPT; e += 8) {
-                        float u[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = v[e + k] * rl;
-                        st8(o + e, u);
-                    }
+                    for (int e = 0; e < EPT; e += 2) o[e / 2] = pack2(T(), src[e] * rl, src[e + 1] * rl);
                     if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnUp + log2f(Ls)) * kLn2;
                 } else {
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
                     float *o = slot + row * D + part * EPT;
 #pragma unroll
                     for (int e = 0; e < EPT; e += 4)
-                        *reinterpret_cast<float4 *>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        *reinterpret_cast<float4 *>(o + e) = *reinterpret_cast<const float4 *>(src + e);
                     if (part == 0) {
                         slot[ROWS * D + row] = M - kAttnUp;
                         slot[ROWS * (D + 1) + row] = Ls;
@@ -535,38 +533,33 @@ __global__ void __launch_bounds__(kStreamThreads, 3) attn_stream_kernel(AttnArgs
             fresh = true;
             __syncthreads();  // the join buffers may be written again
         }
-        if (step + 1 < steps) out.template next<KT>(a, units);
+        if (step + 1 < steps) out.template next<KT>(a, a.c.Hk);
     }
     cp_wait<0>();
 }
 
-template <int FMT, bool BF, int D>
-cudaError_t launch_stream_d(const AttnArgs &a, int nc, int rtiles, cudaStream_t st) {
-    using C = StreamCfg<FMT, D>;
+template <int FMT, bool BF, int D, int NB>
+cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
+    using C = StreamCfg<FMT, D, NB>;
     static const cudaError_t attr = cudaFuncSetAttribute(
-        attn_stream_kernel<FMT, BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        attn_stream_kernel<FMT, BF, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (attr != cudaSuccess) return attr;
-    attn_stream_kernel<FMT, BF, D><<<nc, kStreamThreads, C::SMEM, st>>>(a, rtiles);
+    const int nc = sms * C::BLOCKS;
+    attn_stream_kernel<FMT, BF, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.c.Hk * rtiles * kStreamRows), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF, kStreamKeys, kStreamRows, D>, a, rtiles, nc);
+    return launch_join<BF, kStreamKeys, C::ROWS, D, true>(a, 1, nc, st);
+}
+
+template <int FMT, bool BF, int D>
+cudaError_t launch_stream_n(const AttnArgs &a, int sms, cudaStream_t st) {
+    return a.T * a.G <= 8 ? launch_stream_d<FMT, BF, D, 1>(a, sms, st) : launch_stream_d<FMT, BF, D, 2>(a, sms, st);
 }
 
 template <int FMT>
-cudaError_t launch_stream(const AttnArgs &a, bool bf, int nc, cudaStream_t st) {
-    const int rtiles = (a.T * a.G + kStreamRows - 1) / kStreamRows;
-    if (a.c.D == 128)
-        return bf ? launch_stream_d<FMT, true, 128>(a, nc, rtiles, st) : launch_stream_d<FMT, false, 128>(a, nc, rtiles, st);
-    return bf ? launch_stream_d<FMT, true, 64>(a, nc, rtiles, st) : launch_stream_d<FMT, false, 64>(a, nc, rtiles, st);
+cudaError_t launch_stream(const AttnArgs &a, bool bf, int sms, cudaStream_t st) {
+    if (a.c.D == 128) return bf ? launch_stream_n<FMT, true, 128>(a, sms, st) : launch_stream_n<FMT, false, 128>(a, sms, st);
+    return bf ? launch_stream_n<FMT, true, 64>(a, sms, st) : launch_stream_n<FMT, false, 64>(a, sms, st);
 }
 
 }  // namespace

@@ -1,10 +1,11 @@
 // kern_attn_int4.cu -- the attention kernels for caches in int4.
 #include "attn_stream.cuh"
+#include "attn_tile.cuh"
 
 namespace tl {
 
-cudaError_t launch_stream_int4(const AttnArgs &a, bool bf, int nc, cudaStream_t st) {
-    return launch_stream<kKvInt4>(a, bf, nc, st);
+cudaError_t launch_attn_int4(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st) {
+    return tile ? launch_tile<kKvInt4>(a, bf, sms, st) : launch_stream<kKvInt4>(a, bf, sms, st);
 }
 
 }  // namespace tl

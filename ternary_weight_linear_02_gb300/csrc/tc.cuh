@@ -44,6 +44,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16, cta_group::1.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05.mma issued so far by this thread has
 // completed.
 __device__ __forceinline__ void commit(uint64_t *bar) {
@@ -62,6 +73,22 @@ __host__ __device__ constexpr uint32_t idesc_f16(int n, bool ab_bf16) {
            | ((ab_bf16 ? 1u : 0u) << 10)      // B format
            | ((uint32_t)(n >> 3) << 17)       // N >> 3
            | ((uint32_t)(128 >> 4) << 24);    // M >> 4
+}
+
+// idesc_f16 flag: B is MN-major (rows of N run along memory, K across them)
+constexpr uint32_t kIdescBTransposed = 1u << 16;
+
+// Shared-memory matrix descriptor, MN-major, 128-byte swizzle: rows of 64 16-bit MN
+// elements (128 B), one per k, in 8-row atoms of 1024 B stacked along k (stride byte
+// offset 1024); the next 64 MN elements lie mn_stride bytes further (leading byte
+// offset).  Advancing K by 16 adds 2048 B.
+__device__ __forceinline__ uint64_t desc_sw128_mn(const void *smem_ptr, uint32_t mn_stride) {
+    const uint32_t a = smem_u32(smem_ptr);
+    return (uint64_t)((a >> 4) & 0x3FFFu)
+           | ((uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16)
+           | ((uint64_t)(1024 >> 4) << 32)
+           | ((uint64_t)1 << 46)
+           | ((uint64_t)2 << 61);
 }
 
 // Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128 B
@@ -89,6 +116,14 @@ __device__ __forceinline__ void st_32x32b_x32(uint32_t taddr, const uint32_t (&r
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void wait_st() {
