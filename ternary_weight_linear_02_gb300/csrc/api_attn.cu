@@ -30,6 +30,8 @@ tl_status check_cache(const tl_kv_cache *c, tl::KvCache *out) {
     if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > (1 << 20)) return TL_ERR_SHAPE;
     if (c->kv_heads < 1 || c->kv_heads > (1 << 16)) return TL_ERR_SHAPE;
     if (c->pages < 1 || c->pages >= ((int64_t)1 << 31)) return TL_ERR_SHAPE;
+    // groups of 16 places are counted in 32 bits (2^36 places: beyond any memory)
+    if (c->pages > ((int64_t)1 << 32) / ((int64_t)c->kv_heads * (c->page_size / 16))) return TL_ERR_SHAPE;
     if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return TL_ERR_NULL;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 16) ||
         !aligned(c->v_scale, 16))

@@ -133,40 +133,63 @@ struct AttnSlot {
     }
 };
 
-// A walk over a block's run of tiles.
+// A walk over a block's run of tiles: sequence b, kv head hk, row block rt, tile of the unit.
 struct AttnWalk {
-    int b, unit, tile, tiles, ctx;  // unit: index within the sequence
+    int b, hk, rt, tile, tiles, ctx;
     template <int KT>
-    __device__ __forceinline__ void start(const AttnArgs &a, const AttnPlace &p, int64_t x) {
+    __device__ __forceinline__ void start(const AttnArgs &a, const AttnPlace &p, int64_t x, int rtiles) {
         b = p.b;
         ctx = attn_context(a, b);
         tiles = (ctx + a.T + KT - 1) / KT;
         const int64_t r = x - p.before;
-        unit = (int)(r / tiles);
+        const int unit = (int)(r / tiles);
         tile = (int)(r - (int64_t)unit * tiles);
+        hk = unit / rtiles;
+        rt = unit - hk * rtiles;
     }
-    // to the next tile (not past the last of the call)
+    // to the next tile (not past the last of the call); whether a unit begins there
     template <int KT>
-    __device__ __forceinline__ void next(const AttnArgs &a, int units) {
-        if (++tile < tiles) return;
+    __device__ __forceinline__ bool next(const AttnArgs &a, int rtiles) {
+        if (++tile < tiles) return false;
         tile = 0;
-        if (++unit < units) return;
-        unit = 0;
+        if (++rt < rtiles) return true;
+        rt = 0;
+        if (++hk < a.c.Hk) return true;
+        hk = 0;
         if (++b < a.B) {
             ctx = attn_context(a, b);
             tiles = (ctx + a.T + KT - 1) / KT;
         }
+        return true;
     }
 };
 
-// Page of a key, checked.
-__device__ __forceinline__ int attn_page(const AttnArgs &a, int b, int key) {
-    int p = __ldg(a.pages + b * a.pages_stride + (unsigned)key / (unsigned)a.c.P);
-    if ((unsigned)p >= (unsigned)a.c.pages) {
-        flag_value(a.status);
-        p = 0;
+// Pages of the keys key0 + KT tile of a unit's tiles, without a division per tile: page index pi
+// in the sequence's row of the page table, place off in the page.
+struct AttnPages {
+    int pi, off, last;  // last: page index of the unit's last key
+    __device__ __forceinline__ void start(const AttnArgs &a, const AttnWalk &w, int key) {
+        pi = (int)((unsigned)key / (unsigned)a.c.P);
+        off = key - pi * a.c.P;
+        last = (int)((unsigned)(w.ctx + a.T - 1) / (unsigned)a.c.P);
     }
-    return p;
+    __device__ __forceinline__ void next(const AttnArgs &a, int keys) {
+        off += keys;
+        while (off >= a.c.P) off -= a.c.P, ++pi;
+    }
+    // the page (unchecked) that holds the key, or for a place beyond the last key that key's
+    __device__ __forceinline__ int fetch(const AttnArgs &a, int b) const {
+        return __ldg(a.pages + b * a.pages_stride + min(pi, last));
+    }
+};
+
+// A group is 16 places of one (page, kv head); its index fits 32 bits (checked by the call).
+__device__ __forceinline__ uint32_t attn_group(const AttnArgs &a, int page, int hk, int off) {
+    if ((unsigned)page >= (unsigned)a.c.pages) {
+        flag_value(a.status);
+        page = 0;
+    }
+    return ((uint32_t)page * (uint32_t)a.c.Hk + (uint32_t)hk) * (uint32_t)(a.c.P >> 4) + (uint32_t)(off >> 4);
 }
 
 // Where a unit's partial results lie: blocks c0 .. c1 (c0 == c1: none, its one block wrote

@@ -126,34 +126,21 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     const int steps = (int)(x1 - x0);
 
     uint8_t *ring = smem + warp * C::NS * C::STAGE;
-    AttnWalk in, out;  // the tile being copied, the tile being computed (unit = kv head)
-    in.template start<KT>(a, place, x0);
+    AttnWalk in, out;  // the tile being copied, the tile being computed
+    in.template start<KT>(a, place, x0, 1);
     out = in;
 
     // Copies run NS - 1 tiles ahead; the page of the tile after that is already on its way.
-    // pi, off: page index and place in it of this warp's first key of the tile `in`.
-    int pi, off, page;
-    auto locate = [&]() {
-        const unsigned key = (unsigned)(in.tile * KT + warp * 16);
-        pi = (int)(key / (unsigned)a.c.P);
-        off = (int)(key - (unsigned)pi * (unsigned)a.c.P);
-    };
-    auto fetch_page = [&]() {
-        page = in.tile * KT + warp * 16 < in.ctx + a.T ? __ldg(a.pages + in.b * a.pages_stride + pi) : -1;
-    };
-    locate();
-    fetch_page();
+    AttnPages where;
+    where.start(a, in, in.tile * KT + warp * 16);
+    int page = where.fetch(a, in.b);
     const uint32_t dst0 = smem_u32(ring) + lane * C::KC;
     const int ksrc = g * C::RB + t * C::KC, vsrc = 2 * t * C::RB + g * C::VB;
     int put = 0;  // stage being filled
     auto issue = [&](bool more) {
         const int left = in.ctx + a.T - (in.tile * KT + warp * 16);  // keys from the warp's first one on
         if (left > 0) {
-            if ((unsigned)page >= (unsigned)a.c.pages) {
-                flag_value(a.status);
-                page = 0;
-            }
-            const int64_t row = ((int64_t)page * a.c.Hk + in.unit) * a.c.P + off;
+            const int64_t row = (int64_t)attn_group(a, page, in.hk, where.off) << 4;
             const uint8_t *kp = a.c.kc + row * C::RB + ksrc, *vp = a.c.vc + row * C::RB + vsrc;
             const uint32_t st = dst0 + (uint32_t)put * C::STAGE;
 #pragma unroll
@@ -174,15 +161,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         cp_commit();
         put = put + 1 == C::NS ? 0 : put + 1;
         if (more) {
-            const int b = in.b, unit = in.unit;
-            in.template next<KT>(a, a.c.Hk);
-            if (in.b == b && in.unit == unit) {
-                off += KT;
-                while (off >= a.c.P) off -= a.c.P, ++pi;
-            } else {
-                locate();
-            }
-            fetch_page();
+            if (in.template next<KT>(a, 1)) where.start(a, in, in.tile * KT + warp * 16);
+            else where.next(a, KT);
+            page = where.fetch(a, in.b);
         }
     };
 #pragma unroll 1
@@ -208,7 +189,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             float v[EPT];
             if (row < R) {
                 const T *q = static_cast<const T *>(a.q) + out.b * a.qb + (int64_t)(row / a.G) * a.qt +
-                             (int64_t)(out.unit * a.G + row % a.G) * a.qh + part * EPT;
+                             (int64_t)(out.hk * a.G + row % a.G) * a.qh + part * EPT;
                 if (EPT % 8 == 0 && a.q_vec) {
                     if constexpr (EPT % 8 == 0) {
 #pragma unroll
@@ -512,7 +493,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 const float *src = jb + row * C::PITCH + part * EPT;
                 if (whole) {
                     const float rl = Ls == 0.f ? 0.f : 1.f / Ls;
-                    const int64_t out_row = ((int64_t)out.b * a.T + row / a.G) * a.Hq + out.unit * a.G + row % a.G;
+                    const int64_t out_row = ((int64_t)out.b * a.T + row / a.G) * a.Hq + out.hk * a.G + row % a.G;
                     uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + out_row * D + part * EPT);
 #pragma unroll
                     for (int e = 0; e < EPT; e += 2) o[e / 2] = pack2(T(), src[e] * rl, src[e + 1] * rl);
@@ -533,7 +514,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             fresh = true;
             __syncthreads();  // the join buffers may be written again
         }
-        if (step + 1 < steps) out.template next<KT>(a, a.c.Hk);
+        if (step + 1 < steps) out.template next<KT>(a, 1);
     }
     cp_wait<0>();
 }
