@@ -38,30 +38,38 @@ def _stream(dev: torch.device) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _cuda(t: torch.Tensor, what: str) -> torch.Tensor:
+def _index(t: torch.Tensor, what: str, dtype: torch.dtype, n: int) -> torch.Tensor:
+    if t.dtype is not dtype or t.shape != (n,):
+        raise ValueError(f"{what} must be a 1-D {dtype} tensor of {n} elements")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a CUDA device (no CPU path)")
-    return t
-
-
-def _index(t: torch.Tensor, what: str, dtype: torch.dtype, n: int) -> torch.Tensor:
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what} must be a 1-D {dtype} tensor of {n} elements")
-    _cuda(t, what)
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _rows(t: torch.Tensor, what: str, dims: int) -> torch.Tensor:
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions")
-    _cuda(t, what)
-    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+def _rows(t: torch.Tensor, what: str) -> tuple[torch.Tensor, tuple]:
+    """The tensor with a dense last axis, and its strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a CUDA device (no CPU path)")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        t = t.contiguous()
+        st = t.stride()
+    return t, st
 
 
-def _table(table: torch.Tensor) -> torch.Tensor:
-    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+def _out(out: torch.Tensor, like: torch.Tensor, what: str) -> tuple:
+    st = out.stride()
+    if out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device or st[-1] != 1:
+        raise ValueError(f"{what} must have the input's shape, dtype and device, its last axis dense")
+    return st
+
+
+def _table(table: torch.Tensor) -> tuple[int, int]:
+    if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous fp32 tensor [positions, rotary_dim] (rope_table)")
-    return _cuda(table, "table")
+    if not table.is_cuda:
+        raise ValueError("table must be on a CUDA device (no CPU path)")
+    return table.shape
 
 
 class _Cache(ctypes.Structure):
@@ -100,7 +108,9 @@ class KVCache:
         if v_codes.shape != k_codes.shape:
             raise ValueError("key and value codes must have one shape")
         for t in (k_codes, v_codes, k_scale, v_scale):
-            if _cuda(t, "the cache").device != k_codes.device:
+            if not t.is_cuda:
+                raise ValueError("the cache must be on a CUDA device (no CPU path)")
+            if t.device != k_codes.device:
                 raise ValueError("the cache's tensors must be on one device")
         self.format = format
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
@@ -185,21 +195,23 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, *, inter
     (int64 [tokens]): pairs (x[i], x[i + R/2]), or (x[2i], x[2i+1]) interleaved.
     inverse: the negative angle, which takes the output's gradient to the input's.
     out: where to write; x itself rotates in place."""
-    if x.dtype not in _DT:
-        raise ValueError("x must be fp16, bf16 or fp32")
-    x = _rows(x, "x", 3)
-    n, heads, dim = x.shape
+    dt = _DT.get(x.dtype)
+    if dt is None or x.dim() != 3:
+        raise ValueError("x must be [tokens, heads, head_dim] in fp16, bf16 or fp32")
+    x, xs = _rows(x, "x")
+    shape = x.shape
+    n, heads, dim = shape
     positions = _index(positions, "positions", torch.int64, n)
-    table = _table(table)
+    t_rows, rot = _table(table)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or out.stride(-1) != 1:
-        raise ValueError("out must have x's shape, dtype and device, its last axis dense")
-    rc = _lib().ternary_rope(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-                             out.stride(1), _DT[x.dtype], n, heads, dim, positions.data_ptr(),
-                             table.data_ptr(), table.shape[0], table.shape[1],
-                             (_INTERLEAVED if interleaved else 0) | (_INVERSE if inverse else 0),
-                             _stream(x.device))
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ot, oh = heads * dim, dim
+    else:
+        ot, oh, _ = _out(out, x, "out")
+    rc = (_ready or _lib()).ternary_rope(
+        x.data_ptr(), xs[0], xs[1], out.data_ptr(), ot, oh, dt, n, heads, dim, positions.data_ptr(),
+        table.data_ptr(), t_rows, rot, (_INTERLEAVED if interleaved else 0) | (_INVERSE if inverse else 0),
+        _stream(x.device))
     if rc:
         _check(rc, "ternary_rope")
     return out
@@ -215,42 +227,49 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     given, are rotated by positions (int64 [tokens]) in the same pass; the rotated q is
     returned (written to q_out; q itself rotates in place).  k is not rounded
     between its rotation and its quantisation."""
-    if k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype:
+    dtype = k.dtype
+    dt = _DT.get(dtype)
+    if dt is None or dt == TL_F32 or v.dtype is not dtype:
         raise ValueError("k and v must be fp16 or bf16, both the same")
-    k, v = _rows(k, "k", 3), _rows(v, "v", 3)
-    n = k.shape[0]
-    want = (n, cache.kv_heads, cache.head_dim)
-    if k.shape != want or v.shape != want:
-        raise ValueError(f"k and v must be {want}: got {tuple(k.shape)} and {tuple(v.shape)}")
+    shape = k.shape
+    n = shape[0] if shape else 0
+    if shape != (n, cache.kv_heads, cache.head_dim) or v.shape != shape:
+        raise ValueError(f"k and v must be [tokens, {cache.kv_heads}, {cache.head_dim}]: "
+                         f"got {tuple(shape)} and {tuple(v.shape)}")
+    k, ks = _rows(k, "k")
+    v, vs = _rows(v, "v")
     slots = _index(slots, "slots", torch.int64, n)
+    dev = k.device
     if table is not None:
-        table = _table(table)
+        t_rows, rot = _table(table)
         if positions is None:
             raise ValueError("a table needs positions")
-        positions = _index(positions, "positions", torch.int64, n)
-        tp, pp, t_rows, rot = table.data_ptr(), positions.data_ptr(), table.shape[0], table.shape[1]
+        tp, pp = table.data_ptr(), _index(positions, "positions", torch.int64, n).data_ptr()
     else:
         if q is not None or interleaved:
             raise ValueError("q and interleaved need a table")
         tp = pp = None
         t_rows = rot = 0
     if q is not None:
-        q = _rows(q, "q", 3)
-        if q.dtype != k.dtype or q.shape[0] != n or q.shape[2] != cache.head_dim:
+        qshape = q.shape
+        if q.dtype is not dtype or len(qshape) != 3 or qshape[0] != n or qshape[2] != cache.head_dim:
             raise ValueError("q must be [tokens, q_heads, head_dim] in k's dtype")
+        q, qs = _rows(q, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != q.device or q_out.stride(-1) != 1:
-            raise ValueError("q_out must have q's shape, dtype and device, its last axis dense")
-        qa = (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1),
-              q.shape[1])
+            q_out = torch.empty(qshape, dtype=dtype, device=dev)
+            ot, oh = qshape[1] * qshape[2], qshape[2]
+        else:
+            ot, oh, _ = _out(q_out, q, "q_out")
+        rc = (_ready or _lib()).ternary_kv_append(
+            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, n, slots.data_ptr(),
+            q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), ot, oh, qshape[1], pp, tp, t_rows, rot,
+            _INTERLEAVED if interleaved else 0, _stream(dev))
     else:
         if q_out is not None:
             raise ValueError("q_out needs q")
-        qa = (None, 0, 0, None, 0, 0, 0)
-    rc = _lib().ternary_kv_append(cache._ref, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                                  v.stride(0), v.stride(1), _DT[k.dtype], n, slots.data_ptr(), *qa, pp, tp,
-                                  t_rows, rot, _INTERLEAVED if interleaved else 0, _stream(k.device))
+        rc = (_ready or _lib()).ternary_kv_append(
+            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, n, slots.data_ptr(),
+            None, 0, 0, None, 0, 0, 0, pp, tp, t_rows, rot, _INTERLEAVED if interleaved else 0, _stream(dev))
     if rc:
         _check(rc, "ternary_kv_append")
     return q_out
@@ -260,15 +279,16 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bflo
             ) -> tuple[torch.Tensor, torch.Tensor]:
     """(k, v) [tokens, kv_heads, head_dim] in dtype (fp16, bf16 or fp32): the values at
     slots (int64 [tokens]); zeros where a slot is negative."""
-    if dtype not in _DT:
+    dt = _DT.get(dtype)
+    if dt is None:
         raise ValueError("dtype must be fp16, bf16 or fp32")
     n = slots.shape[0] if slots.dim() == 1 else -1
     slots = _index(slots, "slots", torch.int64, n)
-    shape = (n, cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=slots.device)
-    v = torch.empty(shape, dtype=dtype, device=slots.device)
-    rc = _lib().ternary_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
-                                _stream(slots.device))
+    dev = slots.device
+    both = torch.empty((2, n, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+    k, v = both[0], both[1]
+    rc = (_ready or _lib()).ternary_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
+                                            _stream(dev))
     if rc:
         _check(rc, "ternary_kv_read")
     return k, v
@@ -290,45 +310,52 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
     head_dim ** -0.5.  Returns [batch, draft, q_heads, head_dim] in q's dtype (zeros for a
     token that sees nothing) and, with return_lse, ln of the sum of exp of its scores,
     fp32 [batch, draft, q_heads]."""
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("q must be fp16 or bf16")
-    q = _rows(q, "q", 4)
-    b, t, heads, dim = q.shape
+    dtype = q.dtype
+    dt = _DT.get(dtype)
+    if dt is None or dt == TL_F32 or q.dim() != 4:
+        raise ValueError("q must be [batch, draft, q_heads, head_dim] in fp16 or bf16")
+    q, qs = _rows(q, "q")
+    shape = q.shape
+    b, t, heads, dim = shape
     if dim != cache.head_dim or heads % cache.kv_heads:
         raise ValueError("q must be [batch, draft, a multiple of kv_heads, head_dim]")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != b:
-        raise ValueError("page_table must be int32 [batch, max_pages]")
-    if page_table.stride(1) != 1:
+    pshape = page_table.shape
+    if page_table.dtype is not torch.int32 or len(pshape) != 2 or pshape[0] != b or not page_table.is_cuda:
+        raise ValueError("page_table must be int32 [batch, max_pages] on a CUDA device")
+    pstride = page_table.stride()
+    if pstride[1] != 1:
         page_table = page_table.contiguous()
-    _cuda(page_table, "page_table")
+        pstride = page_table.stride()
     context_len = _index(context_len, "context_len", torch.int32, b)
     tp, tb, tr = None, 0, 0
     if tree is not None:
-        if tree.dtype not in (torch.bool, torch.uint8) or tree.shape[-2:] != (t, t) or tree.dim() not in (2, 3) \
-                or (tree.dim() == 3 and tree.shape[0] not in (1, b)):
+        tshape = tree.shape
+        if (tree.dtype is not torch.bool and tree.dtype is not torch.uint8) or not (
+                tshape == (b, t, t) or tshape == (t, t) or tshape == (1, t, t)):
             raise ValueError("tree must be bool or uint8 [draft, draft] or [batch, draft, draft]")
-        _cuda(tree, "tree")
+        if not tree.is_cuda:
+            raise ValueError("tree must be on a CUDA device (no CPU path)")
         if tree.stride(-1) != 1:
             tree = tree.contiguous()
-        tp, tr = tree.data_ptr(), tree.stride(-2)
-        tb = tree.stride(0) if tree.dim() == 3 and tree.shape[0] > 1 else 0
+        ts = tree.stride()
+        tp, tr = tree.data_ptr(), ts[-2]
+        tb = ts[0] if len(tshape) == 3 and tshape[0] > 1 else 0
+    dev = q.device
     if out is None:
-        out = torch.empty((b, t, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif out.shape != shape or out.dtype is not dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be contiguous with q's shape, dtype and device")
-    lse = torch.empty((b, t, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    lib = _lib()
+    lse = torch.empty((b, t, heads), dtype=torch.float32, device=dev) if return_lse else None
+    lib = _ready or _lib()
     key = (b, t, heads, cache.kv_heads, dim)
     need = _ws_bytes.get(key)
     if need is None:
         need = _ws_bytes[key] = int(lib.ternary_tree_attention_workspace(*key))
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-    rc = lib.ternary_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _DT[q.dtype], b, t,
-                                    heads, cache._ref, page_table.data_ptr(), page_table.stride(0),
-                                    page_table.shape[1], context_len.data_ptr(), tp, tb, tr,
-                                    dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
-                                    None if lse is None else lse.data_ptr(),
-                                    None if ws is None else ws.data_ptr(), max(need, 0), _stream(q.device))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    rc = lib.ternary_tree_attention(
+        q.data_ptr(), qs[0], qs[1], qs[2], dt, b, t, heads, cache._ref, page_table.data_ptr(), pstride[0], pshape[1],
+        context_len.data_ptr(), tp, tb, tr, dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), max(need, 0), _stream(dev))
     if rc:
         _check(rc, "ternary_tree_attention")
     return (out, lse) if return_lse else out

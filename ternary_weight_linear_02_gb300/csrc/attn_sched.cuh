@@ -4,7 +4,7 @@
 // A unit is one block of rows of one (sequence, kv head); it has ceil(L / KT) tiles of
 // KT keys, L = context + new tokens.  The tiles of all units, unit after unit, are
 // dealt to the blocks in equal consecutive runs: block c of nc takes tiles
-// [c N / nc, (c + 1) N / nc).  Lengths live on the device, so every block computes N
+// [c N / nc, (c + 1) N / nc), nc being the blocks launched or N if that is less.  Lengths live on the device, so every block computes N
 // and its first unit itself.  Ragged batches and single long sequences both fill the
 // GPU, and the division -- and with it the order of every sum -- depends on the
 // sizes alone.
@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rope.cuh"
 
 namespace tl {
 
@@ -49,7 +50,7 @@ __device__ __forceinline__ int attn_context(const AttnArgs &a, int b) {
 struct AttnPlace {
     int64_t N;       // tiles of the whole call
     int64_t before;  // tiles of the sequences before b
-    int b;
+    int b, ctx;      // ctx: b's context
 };
 
 // Number of tiles of sequence b over all its units.
@@ -58,10 +59,54 @@ __device__ __forceinline__ int64_t attn_tiles(const AttnArgs &a, int b, int unit
     return (int64_t)((attn_context(a, b) + a.T + KT - 1) / KT) * units;
 }
 
+// Up to kPlaceFast sequences: every warp on its own, one load per 32 sequences and no barrier.
+constexpr int kPlaceFast = 128;
+template <int KT, typename Pick>
+__device__ __forceinline__ AttnPlace attn_place_warp(const AttnArgs &a, int units, Pick pick) {
+    constexpr int CH = kPlaceFast / 32;
+    const int lane = threadIdx.x & 31;
+    int ctx[CH], incl[CH];  // tiles of one unit per sequence fit 32 bits, and so do 32 of them
+    int64_t N = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int b = c * 32 + lane;
+        ctx[c] = b < a.B ? attn_context(a, b) : 0;
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        int v = c * 32 + lane < a.B ? (ctx[c] + a.T + KT - 1) / KT : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        incl[c] = v;
+        N += __shfl_sync(0xffffffffu, v, 31);
+    }
+    AttnPlace r{N * units, 0, 0, 0};
+    int64_t x = pick(r.N), base = 0;
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const uint32_t beyond = __ballot_sync(0xffffffffu, (base + incl[c]) * units > x);
+        if (!found && beyond) {
+            const int l = __ffs(beyond) - 1;
+            found = true;
+            r.b = c * 32 + l;
+            r.ctx = __shfl_sync(0xffffffffu, ctx[c], l);
+            const int upto = __shfl_sync(0xffffffffu, incl[c], l > 0 ? l - 1 : 0);
+            r.before = (base + (l > 0 ? upto : 0)) * units;
+        }
+        base += __shfl_sync(0xffffffffu, incl[c], 31);
+    }
+    return r;
+}
+
 // Executed by the whole block (NTHR threads); sh: NTHR / 32 + 2 64-bit words of shared
 // memory.  pick(N) gives the tile that is looked for.
 template <int KT, int NTHR, typename Pick>
 __device__ __forceinline__ AttnPlace attn_place(const AttnArgs &a, int units, int64_t *sh, Pick pick) {
+    if (a.B <= kPlaceFast) return attn_place_warp<KT>(a, units, pick);
     constexpr int NW = NTHR / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // inclusive sums over one chunk of NTHR sequences; `total` of the chunk in sh[NW]
@@ -80,7 +125,7 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs &a, int units, in
         if (tid == NTHR - 1) sh[NW] = pre + v;
         return pre + v - own;  // exclusive
     };
-    AttnPlace r{0, 0, 0};
+    AttnPlace r{0, 0, 0, 0};
     int64_t first = 0;  // this thread's exclusive sum in the first chunk
     for (int b0 = 0; b0 < a.B; b0 += NTHR) {
         const int64_t e = scan(b0);
@@ -115,14 +160,19 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs &a, int units, in
         __syncthreads();
     }
     __syncthreads();
+    r.ctx = attn_context(a, r.b);
     return r;
 }
 
 // The block that holds tile x.
 __device__ __forceinline__ int attn_block_of(int64_t x, int64_t N, int nc) {
-    return (int)(((x + 1) * nc - 1) / N);
+    const int64_t n = (x + 1) * nc - 1;
+    return (n >> 32) || (N >> 32) ? (int)(n / N) : (int)((uint32_t)n / (uint32_t)N);
 }
-__device__ __forceinline__ int64_t attn_first_tile(int c, int64_t N, int nc) { return c * N / nc; }
+__device__ __forceinline__ int64_t attn_first_tile(int c, int64_t N, int nc) {
+    const int64_t n = c * N;
+    return n >> 32 ? n / nc : (uint32_t)n / (uint32_t)nc;
+}
 
 // A slot of partial results: ROWS rows of D, then their maxima, then their sums.
 template <int ROWS, int D>
@@ -139,12 +189,13 @@ struct AttnWalk {
     template <int KT>
     __device__ __forceinline__ void start(const AttnArgs &a, const AttnPlace &p, int64_t x, int rtiles) {
         b = p.b;
-        ctx = attn_context(a, b);
+        ctx = p.ctx;
         tiles = (ctx + a.T + KT - 1) / KT;
         const int64_t r = x - p.before;
-        const int unit = (int)(r / tiles);
+        // a sequence's tiles fit 32 bits in any cache that fits memory; wider division otherwise
+        const int unit = r < (1ll << 31) ? (int)((unsigned)r / (unsigned)tiles) : (int)(r / tiles);
         tile = (int)(r - (int64_t)unit * tiles);
-        hk = unit / rtiles;
+        hk = rtiles == 1 ? unit : unit / rtiles;
         rt = unit - hk * rtiles;
     }
     // to the next tile (not past the last of the call); whether a unit begins there
@@ -192,12 +243,23 @@ __device__ __forceinline__ uint32_t attn_group(const AttnArgs &a, int page, int 
     return ((uint32_t)page * (uint32_t)a.c.Hk + (uint32_t)hk) * (uint32_t)(a.c.P >> 4) + (uint32_t)(off >> 4);
 }
 
+// 16-bit values of the call's dtype
+__device__ __forceinline__ uint32_t attn_pack(const AttnArgs &a, float lo, float hi) {
+    return a.bf ? pack2(__nv_bfloat16(), lo, hi) : pack2(__half(), lo, hi);
+}
+__device__ __forceinline__ float2 attn_unpack(const AttnArgs &a, uint32_t w) {
+    return a.bf ? unpack2(__nv_bfloat16(), w) : unpack2(__half(), w);
+}
+__device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v) {
+    if (a.bf) OutStore<1>::st(a.out, i, v);
+    else OutStore<0>::st(a.out, i, v);
+}
+
 // Where a unit's partial results lie: blocks c0 .. c1 (c0 == c1: none, its one block wrote
 // the output), the first of them in slot `first`.  Executed by a whole block of 128
 // threads; sh: 8 64-bit words.
 struct AttnParts {
     int c0, c1, first;
-    int64_t N;
 };
 template <int KT>
 __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int unit, int units, int nc, int64_t *sh) {
@@ -217,11 +279,12 @@ __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int un
     __syncthreads();
     AttnParts r;
     pre = sh[0] + sh[1] + sh[2] + sh[3];
-    r.N = sh[4] + sh[5] + sh[6] + sh[7];
+    const int64_t N = sh[4] + sh[5] + sh[6] + sh[7];
+    if (N < nc) nc = (int)N;
     const int64_t tiles = attn_tiles<KT>(a, b, 1), s = pre + unit * tiles;
-    r.c0 = attn_block_of(s, r.N, nc);
-    r.c1 = attn_block_of(s + tiles - 1, r.N, nc);
-    r.first = attn_first_tile(r.c0, r.N, nc) == s ? 0 : 1;
+    r.c0 = attn_block_of(s, N, nc);
+    r.c1 = attn_block_of(s + tiles - 1, N, nc);
+    r.first = attn_first_tile(r.c0, N, nc) == s ? 0 : 1;
     return r;
 }
 
@@ -233,20 +296,36 @@ struct AttnSum {
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
     }
-    __device__ __forceinline__ void add(float pm, float pl, const float *row, int lane) {
-        float v[E];
-        if constexpr (E == 4) {
-            const float4 x = reinterpret_cast<const float4 *>(row)[lane];
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            const float2 x = reinterpret_cast<const float2 *>(row)[lane];
-            v[0] = x.x, v[1] = x.y;
-        }
-        const float mn = fmaxf(m, pm), f = ex2(m - mn), g = ex2(pm - mn);
-        m = mn;
-        l = l * f + pl * g;
+    // four parts at once, their loads in flight together; absent ones are null
+    template <int ROWS, int D>
+    __device__ __forceinline__ void add4(const float *const (&x)[4], int row, int lane) {
+        float pm[4], pl[4], v[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[e] * g;
+        for (int k = 0; k < 4; ++k) {
+            pm[k] = kAttnLow;
+            pl[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+            if (x[k]) {
+                pm[k] = x[k][ROWS * D + row];
+                pl[k] = x[k][ROWS * (D + 1) + row];
+                if constexpr (E == 4) {
+                    const float4 u = reinterpret_cast<const float4 *>(x[k] + row * D)[lane];
+                    v[k][0] = u.x, v[k][1] = u.y, v[k][2] = u.z, v[k][3] = u.w;
+                } else {
+                    const float2 u = reinterpret_cast<const float2 *>(x[k] + row * D)[lane];
+                    v[k][0] = u.x, v[k][1] = u.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float mn = fmaxf(m, pm[k]), f = ex2(m - mn), g = ex2(pm[k] - mn);
+            m = mn;
+            l = l * f + pl[k] * g;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[k][e] * g;
+        }
     }
 };
 
@@ -256,7 +335,7 @@ struct AttnSum {
 // WIDE (few rows, many parts: single tokens over long contexts): one block per row,
 // its four warps sharing the parts.  Otherwise 16 rows per block, each warp taking
 // whole rows.
-template <bool BF, int KT, int ROWS, int D, bool WIDE>
+template <int KT, int ROWS, int D, bool WIDE>
 __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
     __shared__ int64_t sh[8];
     __shared__ float sm[4], sl[4], so[4][D];
@@ -272,16 +351,14 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
     if (p.c0 == p.c1) return;
     // the output row of row `grow` of the unit's (sequence, kv head)
     auto out_row = [&](int grow) { return ((int64_t)b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G; };
-    // blocks without a tile (fewer tiles than blocks) lie between and hold nothing
-    auto part = [&](int c) -> const float * {
-        if (attn_first_tile(c, p.N, nc) == attn_first_tile(c + 1, p.N, nc)) return nullptr;
-        return Slot::at(a.ws, c, c == p.c0 ? p.first : 0);
-    };
+    auto part = [&](int c) -> const float * { return c > p.c1 ? nullptr : Slot::at(a.ws, c, c == p.c0 ? p.first : 0); };
     if constexpr (WIDE) {
         const int row = slice;
         AttnSum<E> s;
-        for (int c = p.c0 + warp; c <= p.c1; c += 4)
-            if (const float *x = part(c)) s.add(x[ROWS * D + row], x[ROWS * (D + 1) + row], x + row * D, lane);
+        for (int c = p.c0 + warp; c <= p.c1; c += 16) {
+            const float *const x[4] = {part(c), part(c + 4), part(c + 8), part(c + 12)};
+            s.template add4<ROWS, D>(x, row, lane);
+        }
         if (lane == 0) sm[warp] = s.m, sl[warp] = s.l;
 #pragma unroll
         for (int e = 0; e < E; ++e) so[warp][lane * E + e] = s.o[e];
@@ -296,25 +373,27 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
             if (d < D) x += so[w][d] * g;
         }
         const int64_t o = out_row(row);
-        if (d < D) OutStore<BF ? 1 : 0>::st(a.out, o * D + d, L == 0.f ? 0.f : x / L);
+        if (d < D) attn_store(a, o * D + d, L == 0.f ? 0.f : x / L);
         if (a.lse && d == 0) a.lse[o] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     } else {
         for (int row = slice * 16 + warp; row < slice * 16 + 16; row += 4) {
             const int grow = rt * ROWS + row;
             if (grow >= R) return;
             AttnSum<E> s;
-            for (int c = p.c0; c <= p.c1; ++c)
-                if (const float *x = part(c)) s.add(x[ROWS * D + row], x[ROWS * (D + 1) + row], x + row * D, lane);
+            for (int c = p.c0; c <= p.c1; c += 4) {
+                const float *const x[4] = {part(c), part(c + 1), part(c + 2), part(c + 3)};
+                s.template add4<ROWS, D>(x, row, lane);
+            }
             const int64_t o = out_row(grow);
             const float r = s.l == 0.f ? 0.f : 1.f / s.l;
 #pragma unroll
-            for (int e = 0; e < E; ++e) OutStore<BF ? 1 : 0>::st(a.out, o * D + lane * E + e, s.o[e] * r);
+            for (int e = 0; e < E; ++e) attn_store(a, o * D + lane * E + e, s.o[e] * r);
             if (a.lse && lane == 0) a.lse[o] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
         }
     }
 }
 
-template <bool BF, int KT, int ROWS, int D, bool WIDE>
+template <int KT, int ROWS, int D, bool WIDE>
 cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
     const int R = a.T * a.G, per_unit = WIDE ? R : ((R < ROWS ? R : ROWS) + 15) / 16;
     cudaLaunchConfig_t cfg = {};
@@ -326,7 +405,7 @@ cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF, KT, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<KT, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
 }
 
 }  // namespace tl

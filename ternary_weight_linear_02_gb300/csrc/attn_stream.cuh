@@ -96,39 +96,72 @@ struct StreamCfg {
     // one stage of one warp: keys' copies, values' copies, 16 + 16 scales
     static constexpr int KOFF = 0, VOFF = 2 * NKC * KC * 32, SOFF = VOFF + 4 * VB * 32;
     static constexpr int STAGE = SOFF + 128;
-    static constexpr int BLOCKS = NB == 1 ? 4 : 3;        // per SM (registers)
-    static constexpr int NS = STAGE > 3000 ? 3 : STAGE > 2000 ? 5 : 8;  // stages per warp
-    static constexpr int PITCH = D + 8;                   // floats per row of the join buffer
+    static constexpr int BLOCKS = NB == 1 ? 4 : NB == 2 ? 3 : 2;  // per SM (registers)
+    static constexpr int NS = STAGE > 3000 ? (NB == 3 ? 4 : 3) : STAGE > 2000 ? 5 : 8;  // stages per warp
+    static constexpr bool QSMEM = NB > 1;                 // the queries' fragments stay in shared memory
+    static constexpr int PITCH = D + 4;                   // floats per row of the join buffer
     // [stages of 4 warps][join rows; at a unit's start, its queries in f16]
     // [row factors][per-warp maxima and sums][place]
     static constexpr int JOFF = 4 * NS * STAGE;
     static constexpr int FOFF = JOFF + ROWS * PITCH * 4;
     static constexpr int WOFF = FOFF + ROWS * 4;
     static constexpr int POFF = WOFF + 2 * 4 * ROWS * 4;
-    static constexpr int SMEM = POFF + 64;
+    static constexpr int GOFF = POFF + 64;                // fragments [n][step][lane]
+    static constexpr int SMEM = GOFF + (QSMEM ? NB * KSTEPS * 256 : 0);
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
 };
 
-template <int FMT, bool BF, int D, int NB>
+template <int FMT, int D, int NB>
 __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS) attn_stream_kernel(AttnArgs a) {
     using C = StreamCfg<FMT, D, NB>;
-    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr int KT = kStreamKeys, ROWS = C::ROWS, NT = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int nc = gridDim.x, R = a.T * a.G;
+    int nc = gridDim.x;
+    const int R = a.T * a.G;
     pdl_launch_dependents();
 
     const AttnPlace place = attn_place<KT, kStreamThreads>(a, a.c.Hk, reinterpret_cast<int64_t *>(smem + C::POFF),
-                                                           [&](int64_t N) { return attn_first_tile(blockIdx.x, N, nc); });
+                                                           [&](int64_t N) {
+        if (N < nc) nc = (int)N;  // no block without a tile
+        return attn_first_tile(blockIdx.x, N, nc);
+    });
     const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
-    if (x0 == x1) return;
+    if ((int)blockIdx.x >= nc) return;
     const int steps = (int)(x1 - x0);
 
     uint8_t *ring = smem + warp * C::NS * C::STAGE;
     AttnWalk in, out;  // the tile being copied, the tile being computed
     in.template start<KT>(a, place, x0, 1);
     out = in;
+
+    // Queries of a unit: TPR threads per row, EPT elements each (the first unit's are fetched
+    // before its keys).
+    constexpr int TPR = NB == 3 ? 4 : kStreamThreads / ROWS, EPT = D / TPR;
+    const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
+    uint32_t raw[EPT / 2];
+    auto fetch_queries = [&](const AttnWalk &w) {
+        const int r = min(row, R - 1), tok = r / a.G;
+        const uint16_t *q = static_cast<const uint16_t *>(a.q) + w.b * a.qb + (int64_t)tok * a.qt +
+                     (int64_t)(w.hk * a.G + r - tok * a.G) * a.qh + part * EPT;
+        if (a.q_vec) {
+            if constexpr (EPT >= 8) {
+#pragma unroll
+                for (int i = 0; i < EPT / 8; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                    raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
+                }
+            } else {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(q));
+                raw[0] = u.x, raw[1] = u.y;
+            }
+        } else {
+            const uint16_t *u = q;
+#pragma unroll
+            for (int i = 0; i < EPT / 2; ++i) raw[i] = u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
+        }
+    };
+    fetch_queries(out);
 
     // Copies run NS - 1 tiles ahead; the page of the tile after that is already on its way.
     AttnPages where;
@@ -143,18 +176,23 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             const int64_t row = (int64_t)attn_group(a, page, in.hk, where.off) << 4;
             const uint8_t *kp = a.c.kc + row * C::RB + ksrc, *vp = a.c.vc + row * C::RB + vsrc;
             const uint32_t st = dst0 + (uint32_t)put * C::STAGE;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int j = 0; j < C::NKC; ++j)
-                    cp_async<C::KC>(st + C::KOFF + (n * C::NKC + j) * 32 * C::KC, kp + n * 8 * C::RB + j * 4 * C::KC,
-                                    n * 8 + g < left);
             const uint32_t sv = st + C::VOFF - lane * (C::KC - C::VB);
+            auto copy = [&](auto whole) {  // whole: no key of the 16 lies beyond the last
+                constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = (j & 1) + (j >> 1) * 8;
-                cp_async<C::VB>(sv + j * 32 * C::VB, vp + r * C::RB, 2 * t + r < left);
-            }
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < C::NKC; ++j)
+                        cp_async<C::KC>(st + C::KOFF + (n * C::NKC + j) * 32 * C::KC, kp + n * 8 * C::RB + j * 4 * C::KC,
+                                        ALL || n * 8 + g < left);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = (j & 1) + (j >> 1) * 8;
+                    cp_async<C::VB>(sv + j * 32 * C::VB, vp + r * C::RB, ALL || 2 * t + r < left);
+                }
+            };
+            if (left >= 16) copy(std::true_type());
+            else copy(std::false_type());
             if (lane < 8)
                 cp_async<16>(st + C::SOFF + lane * (16 - C::KC), (lane < 4 ? a.c.ks : a.c.vs) + row + (lane & 3) * 4, true);
         }
@@ -172,9 +210,10 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         else cp_commit();
     }
 
-    uint32_t qf[NB][C::KSTEPS][2];
+    uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : C::KSTEPS][2];
+    uint2 *const qsm = reinterpret_cast<uint2 *>(smem + C::GOFF) + lane;
     float f[NB][2];                        // score factors of rows 8 n + 2t and + 1
-    float m[NB][2], l[NB][2], svref = 1e-30f;
+    float m[NB][2], l[NB][2], svref = 1e-30f, inv = 1e30f;  // inv = 1 / svref
     float acc[NB][NT][4];
     bool fresh = true;                     // the next tile begins a unit (for this block)
     int which = 0, get = 0;                // slot of a partial result; stage being read
@@ -184,32 +223,16 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         if (fresh) {
             // ---------------- queries of the unit: rows as f16 in shared memory, then fragments
             fresh = false;
-            constexpr int TPR = kStreamThreads / ROWS, EPT = D / TPR;  // threads per row, elements per thread
-            const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
+            if (step > 0) fetch_queries(out);
             float v[EPT];
-            if (row < R) {
-                const T *q = static_cast<const T *>(a.q) + out.b * a.qb + (int64_t)(row / a.G) * a.qt +
-                             (int64_t)(out.hk * a.G + row % a.G) * a.qh + part * EPT;
-                if (EPT % 8 == 0 && a.q_vec) {
-                    if constexpr (EPT % 8 == 0) {
 #pragma unroll
-                        for (int i = 0; i < EPT; i += 8) {
-                            float u[8];
-                            ld8(q + i, u);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) v[i + k] = u[k];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < EPT; ++i) v[i] = to_f32(q[i]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < EPT; ++i) v[i] = 0.f;
+            for (int i = 0; i < EPT; i += 2) {
+                const float2 x = attn_unpack(a, row < R ? raw[i / 2] : 0u);
+                v[i] = x.x;
+                v[i + 1] = x.y;
             }
             float down = 1.f, up = 1.f;
-            if constexpr (BF) {
+            if (a.bf) {
                 float mx = 0.f;
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) mx = fmaxf(mx, fabsf(v[i]));
@@ -226,21 +249,28 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             for (int i = 0; i < EPT; i += 2)
                 *reinterpret_cast<__half2 *>(qs + i) = __floats2half2_rn(v[i] * down, v[i + 1] * down);
             float *fac = reinterpret_cast<float *>(smem + C::FOFF);
-            if (part == 0) fac[row] = a.scale * kLog2e * up;
+            if (part == 0 && row < ROWS) fac[row] = a.scale * kLog2e * up;
             __syncthreads();
             const uint16_t *qr = reinterpret_cast<const uint16_t *>(smem + C::JOFF);
+            // the elements of this thread in step s, in the order its code words give
+            auto fragment = [&](int n, int s) {
+                const uint16_t *r = qr + (8 * n + g) * (D + 8);
+                if constexpr (FMT == kKvInt4) {
+                    const uint16_t *p = r + t * (D / 4) + (s >> 1) * 8 + (s & 1) * 2;
+                    return make_uint2(p[0] | ((uint32_t)p[4] << 16), p[1] | ((uint32_t)p[5] << 16));
+                } else {
+                    return *reinterpret_cast<const uint2 *>(r + (s >> 2) * 64 + t * 16 + (s & 3) * 4);
+                }
+            };
+            if constexpr (C::QSMEM) {
+                for (int i = warp; i < NB * C::KSTEPS; i += 4) qsm[i * 32] = fragment(i / C::KSTEPS, i % C::KSTEPS);
+            }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const uint16_t *r = qr + (8 * n + g) * (D + 8);
+                if constexpr (!C::QSMEM) {
 #pragma unroll
-                for (int s = 0; s < C::KSTEPS; ++s) {
-                    // the elements of this thread in step s, in the order its code words give
-                    if constexpr (FMT == kKvInt4) {
-                        const uint16_t *p = r + t * (D / 4) + (s >> 1) * 8 + (s & 1) * 2;
-                        qf[n][s][0] = p[0] | ((uint32_t)p[4] << 16);
-                        qf[n][s][1] = p[1] | ((uint32_t)p[5] << 16);
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(r + (s >> 2) * 64 + t * 16 + (s & 3) * 4);
+                    for (int s = 0; s < C::KSTEPS; ++s) {
+                        const uint2 u = fragment(n, s);
                         qf[n][s][0] = u.x;
                         qf[n][s][1] = u.y;
                     }
@@ -253,6 +283,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 for (int i = 0; i < NT; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
             }
             svref = 1e-30f;
+            inv = 1e30f;
             __syncthreads();  // the queries' buffer is the join buffer too
         }
 
@@ -264,11 +295,14 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         const int key = out.tile * KT + warp * 16;
         if (key < out.ctx + a.T) {
             const uint8_t *st = ring + get * C::STAGE;
-            float s[NB][4], s2[NB][4];
+            // one block of rows: two chains of sums (even and odd steps), half the latency of one
+            float s[NB][4], s2[1][4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int j = 0; j < 4; ++j) {
+                s2[0][j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[n][j] = s2[n][j] = 0.f;
+                for (int n = 0; n < NB; ++n) s[n][j] = 0.f;
+            }
             uint32_t w[2][C::KB / 4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -283,7 +317,6 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         w[n][0] = u.x, w[n][1] = u.y;
                     }
                 }
-            // two chains of sums (even and odd steps): half the latency of one
 #pragma unroll
             for (int i = 0; i < C::KSTEPS; ++i) {
                 uint32_t x[4];
@@ -303,7 +336,14 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NB; ++n) mma16816(i & 1 ? s2[n] : s[n], x, qf[n][i][0], qf[n][i][1]);
+                for (int n = 0; n < NB; ++n) {
+                    if constexpr (C::QSMEM) {
+                        const uint2 u = qsm[(n * C::KSTEPS + i) * 32];
+                        mma16816(s[n], x, u.x, u.y);
+                    } else {
+                        mma16816(i & 1 ? s2[n] : s[n], x, qf[n][i][0], qf[n][i][1]);
+                    }
+                }
             }
             const float *sc = reinterpret_cast<const float *>(st + C::SOFF);
             const float sk[2] = {sc[g], sc[g + 8]};
@@ -313,7 +353,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) z[n][j] = (s[n][j] + s2[n][j]) * sk[j >> 1] * f[n][j & 1];
+                for (int j = 0; j < 4; ++j) z[n][j] = (NB == 1 ? s[n][j] + s2[0][j] : s[n][j]) * sk[j >> 1] * f[n][j & 1];
             uint32_t unseen = 0;
             if (key + 16 > out.ctx) {  // new tokens' keys, or the end
                 const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
@@ -343,6 +383,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 if (rv > svref) {  // twice the largest: the next slightly larger one changes nothing
                     cv = svref / (2.f * rv);
                     svref = 2.f * rv;
+                    inv = __frcp_rn(svref);
                 }
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
@@ -362,7 +403,6 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         }
                     }
             }
-            const float inv = __frcp_rn(svref);
             const float wv[2] = {sv[0] * inv, sv[1] * inv};
             uint32_t pb[NB][2];
 #pragma unroll
@@ -370,7 +410,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 float p[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = ex2(z[n][j] - m[n][j & 1] + kAttnUp);
+                    const float e = ex2(z[n][j] - (m[n][j & 1] - kAttnUp));
                     l[n][j & 1] += e;
                     p[j] = e * wv[j >> 1];
                 }
@@ -470,40 +510,47 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
+                            // pair i of lane group g's run lies at place (i + g) % NT of it: no
+                            // two lanes of a half-warp meet in a bank
                             float2 *d = reinterpret_cast<float2 *>(jb + (8 * n + 2 * t + r) * C::PITCH + g * (D / 8));
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) {  // elements 2i, 2i + 1 of the run
+                            for (int i = 0; i < NT; ++i) {
+                                float2 *p = d + ((i + g) & (NT - 1));
                                 float2 u = make_float2(acc[n][i][r] * c[n][r], acc[n][i][2 + r] * c[n][r]);
-                                if (turn > 0) u.x += d[i].x, u.y += d[i].y;
-                                d[i] = u;
+                                if (turn > 0) u.x += p->x, u.y += p->y;
+                                *p = u;
                             }
                         }
                 }
                 __syncthreads();
             }
             const bool whole = last && step >= out.tile;  // the block saw the unit from its first tile on
-            constexpr int TPR = kStreamThreads / ROWS, EPT = D / TPR;
-            const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
             if (row < R) {
                 float M = wm[row], Ls = 0.f;
 #pragma unroll
                 for (int i = 1; i < 4; ++i) M = fmaxf(M, wm[i * ROWS + row]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) Ls += wl[i * ROWS + row] * ex2(wm[i * ROWS + row] - M);
-                const float *src = jb + row * C::PITCH + part * EPT;
+                float v[EPT];
+#pragma unroll
+                for (int e = 0; e < EPT; e += 2) {
+                    const int i = (part * EPT + e) / 2, h = i / NT;  // pair of the row, lane group that wrote it
+                    const float2 u = *reinterpret_cast<const float2 *>(jb + row * C::PITCH + h * (D / 8) + 2 * ((i + h) & (NT - 1)));
+                    v[e] = u.x, v[e + 1] = u.y;
+                }
                 if (whole) {
                     const float rl = Ls == 0.f ? 0.f : 1.f / Ls;
                     const int64_t out_row = ((int64_t)out.b * a.T + row / a.G) * a.Hq + out.hk * a.G + row % a.G;
-                    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + out_row * D + part * EPT);
+                    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + out_row * D + part * EPT);
 #pragma unroll
-                    for (int e = 0; e < EPT; e += 2) o[e / 2] = pack2(T(), src[e] * rl, src[e + 1] * rl);
+                    for (int e = 0; e < EPT; e += 2) o[e / 2] = attn_pack(a, v[e] * rl, v[e + 1] * rl);
                     if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnUp + log2f(Ls)) * kLn2;
                 } else {
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
                     float *o = slot + row * D + part * EPT;
 #pragma unroll
                     for (int e = 0; e < EPT; e += 4)
-                        *reinterpret_cast<float4 *>(o + e) = *reinterpret_cast<const float4 *>(src + e);
+                        *reinterpret_cast<float4 *>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     if (part == 0) {
                         slot[ROWS * D + row] = M - kAttnUp;
                         slot[ROWS * (D + 1) + row] = Ls;
@@ -519,28 +566,30 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     cp_wait<0>();
 }
 
-template <int FMT, bool BF, int D, int NB>
+template <int FMT, int D, int NB>
 cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     using C = StreamCfg<FMT, D, NB>;
     static const cudaError_t attr = cudaFuncSetAttribute(
-        attn_stream_kernel<FMT, BF, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        attn_stream_kernel<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (attr != cudaSuccess) return attr;
     const int nc = sms * C::BLOCKS;
-    attn_stream_kernel<FMT, BF, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
+    attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<BF, kStreamKeys, C::ROWS, D, true>(a, 1, nc, st);
+    return launch_join<kStreamKeys, C::ROWS, D, true>(a, 1, nc, st);
 }
 
-template <int FMT, bool BF, int D>
+template <int FMT, int D>
 cudaError_t launch_stream_n(const AttnArgs &a, int sms, cudaStream_t st) {
-    return a.T * a.G <= 8 ? launch_stream_d<FMT, BF, D, 1>(a, sms, st) : launch_stream_d<FMT, BF, D, 2>(a, sms, st);
+    const int rows = a.T * a.G;
+    return rows <= 8    ? launch_stream_d<FMT, D, 1>(a, sms, st)
+           : rows <= 16 ? launch_stream_d<FMT, D, 2>(a, sms, st)
+                        : launch_stream_d<FMT, D, 3>(a, sms, st);
 }
 
 template <int FMT>
-cudaError_t launch_stream(const AttnArgs &a, bool bf, int sms, cudaStream_t st) {
-    if (a.c.D == 128) return bf ? launch_stream_n<FMT, true, 128>(a, sms, st) : launch_stream_n<FMT, false, 128>(a, sms, st);
-    return bf ? launch_stream_n<FMT, true, 64>(a, sms, st) : launch_stream_n<FMT, false, 64>(a, sms, st);
+cudaError_t launch_stream(const AttnArgs &a, int sms, cudaStream_t st) {
+    return a.c.D == 128 ? launch_stream_n<FMT, 128>(a, sms, st) : launch_stream_n<FMT, 64>(a, sms, st);
 }
 
 }  // namespace

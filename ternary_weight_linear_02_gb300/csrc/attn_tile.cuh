@@ -84,10 +84,9 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-template <int FMT, bool BF, int D>
+template <int FMT, int D>
 __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, int rtiles) {
     using C = AttnTileCfg<FMT, D>;
-    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr int KT = kTileKeys, ROWS = kTileRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -99,7 +98,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 11);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nc = gridDim.x, R = a.T * a.G, units = a.c.Hk * rtiles;
+    int nc = gridDim.x;
+    const int R = a.T * a.G, units = a.c.Hk * rtiles;
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -115,9 +115,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         fence_barrier_init();
     }
     const AttnPlace place = attn_place<KT, kTileThreads>(a, units, reinterpret_cast<int64_t *>(smem + C::POFF),
-                                                         [&](int64_t N) { return attn_first_tile(blockIdx.x, N, nc); });
+                                                         [&](int64_t N) {
+        if (N < nc) nc = (int)N;  // no block without a tile
+        return attn_first_tile(blockIdx.x, N, nc);
+    });
     const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
-    if (x0 == x1) return;
+    if ((int)blockIdx.x >= nc) return;
     const int steps = (int)(x1 - x0);
     if (warp == 4) tc::tmem_alloc(tmem_slot, C::COLS);
     tc::fence_before_sync();
@@ -223,12 +226,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int g = min(first + (n0 + i) * QR + lane / QL, R - 1), tok = g / a.G;
-                    const T *q = static_cast<const T *>(a.q) + w.b * a.qb + (int64_t)tok * a.qt +
+                    const uint16_t *q = static_cast<const uint16_t *>(a.q) + w.b * a.qb + (int64_t)tok * a.qt +
                                  (int64_t)(w.hk * a.G + g - tok * a.G) * a.qh + c * 8;
                     if (a.q_vec) {
                         raw[i] = __ldg(reinterpret_cast<const uint4 *>(q));
                     } else {
-                        const uint16_t *u = reinterpret_cast<const uint16_t *>(q);
+                        const uint16_t *u = q;
                         raw[i] = make_uint4(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16,
                                             u[4] | (uint32_t)u[5] << 16, u[6] | (uint32_t)u[7] << 16);
                     }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     const int r = dw * 32 + (n0 + i) * QR + lane / QL;
                     uint4 h = raw[i];
                     float up = 1.f;
-                    if constexpr (BF) {
+                    if (a.bf) {
                         const uint32_t x[4] = {h.x, h.y, h.z, h.w};
                         // bf16 magnitudes compare as their bits
                         uint32_t mx = 0;
@@ -508,13 +511,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         tc::wait_ld();
                         if (grow < R) {
                             if (whole) {
-                                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + out_row * D + h * 32);
+                                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_row * D + h * 32);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     uint32_t w[4];
 #pragma unroll
                                     for (int i = 0; i < 4; ++i)
-                                        w[i] = pack2(T(), __uint_as_float(o[8 * k + 2 * i]) * rl, __uint_as_float(o[8 * k + 2 * i + 1]) * rl);
+                                        w[i] = attn_pack(a, __uint_as_float(o[8 * k + 2 * i]) * rl, __uint_as_float(o[8 * k + 2 * i + 1]) * rl);
                                     dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
                                 }
                             } else {
@@ -557,23 +560,22 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     }
 }
 
-template <int FMT, bool BF, int D>
+template <int FMT, int D>
 cudaError_t launch_tile_d(const AttnArgs &a, int sms, cudaStream_t st) {
     using C = AttnTileCfg<FMT, D>;
     static const cudaError_t attr =
-        cudaFuncSetAttribute(attn_tile_kernel<FMT, BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::REQ);
+        cudaFuncSetAttribute(attn_tile_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::REQ);
     if (attr != cudaSuccess) return attr;
     const int nc = sms * 2, rtiles = (a.T * a.G + kTileRows - 1) / kTileRows;
-    attn_tile_kernel<FMT, BF, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
+    attn_tile_kernel<FMT, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<BF, kTileKeys, kTileRows, D, false>(a, rtiles, nc, st);
+    return launch_join<kTileKeys, kTileRows, D, false>(a, rtiles, nc, st);
 }
 
 template <int FMT>
-cudaError_t launch_tile(const AttnArgs &a, bool bf, int sms, cudaStream_t st) {
-    if (a.c.D == 128) return bf ? launch_tile_d<FMT, true, 128>(a, sms, st) : launch_tile_d<FMT, false, 128>(a, sms, st);
-    return bf ? launch_tile_d<FMT, true, 64>(a, sms, st) : launch_tile_d<FMT, false, 64>(a, sms, st);
+cudaError_t launch_tile(const AttnArgs &a, int sms, cudaStream_t st) {
+    return a.c.D == 128 ? launch_tile_d<FMT, 128>(a, sms, st) : launch_tile_d<FMT, 64>(a, sms, st);
 }
 
 }  // namespace

@@ -6,10 +6,10 @@ namespace tl {
 
 namespace {
 
-// Rows of a kv head (new tokens x query heads that share it): up to 16 the cache's bytes bound
-// the call and the streaming kernel's warp MMAs keep up with them; above, it would read
-// the cache once per 16 rows, and the tcgen05 kernel takes 128 rows at a time.
-constexpr int64_t kStreamMaxRows = 16;
+// Rows of a kv head (new tokens x query heads that share it): up to 24 the streaming kernel,
+// whose warp MMAs keep up with the cache's bytes; above, it would read the cache once
+// per 24 rows, and the tcgen05 kernel takes 128 rows at a time.
+constexpr int64_t kStreamMaxRows = 24;
 bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 
 }  // namespace
@@ -17,17 +17,17 @@ bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 // Two slots per block (attn_sched.cuh): rows of D, a maximum and a sum each.
 int64_t tree_attention_workspace(int64_t, int64_t T, int Hq, int Hk, int D) {
     const int64_t rows = T * (Hq / Hk);
-    const int64_t blocks = use_tile(rows) ? 2 : rows <= 8 ? 4 : 3, slot = use_tile(rows) ? 128 : rows <= 8 ? 8 : 16;
+    const int64_t blocks = rows <= 8 ? 4 : rows <= 16 ? 3 : 2, slot = rows <= 8 ? 8 : rows <= 16 ? 16 : use_tile(rows) ? 128 : 24;
     return kMaxSms * blocks * 2 * slot * (D + 2) * 4;
 }
 
-cudaError_t launch_tree_attention(const AttnArgs &a, bool bf, int sm_count, cudaStream_t st) {
+cudaError_t launch_tree_attention(const AttnArgs &a, int sm_count, cudaStream_t st) {
     const int sms = sm_count < kMaxSms ? sm_count : kMaxSms;
     const bool tile = use_tile((int64_t)a.T * a.G);
     switch (a.c.fmt) {
-    case 0: return launch_attn_int8(a, bf, tile, sms, st);
-    case 1: return launch_attn_fp8(a, bf, tile, sms, st);
-    default: return launch_attn_int4(a, bf, tile, sms, st);
+    case 0: return launch_attn_int8(a, tile, sms, st);
+    case 1: return launch_attn_fp8(a, tile, sms, st);
+    default: return launch_attn_int4(a, tile, sms, st);
     }
 }
 

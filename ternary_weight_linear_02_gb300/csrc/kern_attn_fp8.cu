@@ -4,8 +4,8 @@
 
 namespace tl {
 
-cudaError_t launch_attn_fp8(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st) {
-    return tile ? launch_tile<kKvFp8>(a, bf, sms, st) : launch_stream<kKvFp8>(a, bf, sms, st);
+cudaError_t launch_attn_fp8(const AttnArgs &a, bool tile, int sms, cudaStream_t st) {
+    return tile ? launch_tile<kKvFp8>(a, sms, st) : launch_stream<kKvFp8>(a, sms, st);
 }
 
 }  // namespace tl

@@ -4,8 +4,8 @@
 
 namespace tl {
 
-cudaError_t launch_attn_int4(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st) {
-    return tile ? launch_tile<kKvInt4>(a, bf, sms, st) : launch_stream<kKvInt4>(a, bf, sms, st);
+cudaError_t launch_attn_int4(const AttnArgs &a, bool tile, int sms, cudaStream_t st) {
+    return tile ? launch_tile<kKvInt4>(a, sms, st) : launch_stream<kKvInt4>(a, sms, st);
 }
 
 }  // namespace tl

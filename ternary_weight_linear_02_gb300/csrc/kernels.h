@@ -268,14 +268,15 @@ struct AttnArgs {
     float *ws;
     int B, T, Hq, G;     // batch, new tokens, query heads, query heads per kv head
     int q_vec;           // every q row starts on a 16-byte boundary
+    int bf;              // q and out are bf16 (else fp16)
     int *status;
 };
 // SMs that a workspace is laid out for (the GPU has 152; more are left unused)
 constexpr int kMaxSms = 160;
-cudaError_t launch_attn_int8(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st);
-cudaError_t launch_attn_fp8(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st);
-cudaError_t launch_attn_int4(const AttnArgs &a, bool bf, bool tile, int sms, cudaStream_t st);
-cudaError_t launch_tree_attention(const AttnArgs &a, bool bf, int sm_count, cudaStream_t st);
+cudaError_t launch_attn_int8(const AttnArgs &a, bool tile, int sms, cudaStream_t st);
+cudaError_t launch_attn_fp8(const AttnArgs &a, bool tile, int sms, cudaStream_t st);
+cudaError_t launch_attn_int4(const AttnArgs &a, bool tile, int sms, cudaStream_t st);
+cudaError_t launch_tree_attention(const AttnArgs &a, int sm_count, cudaStream_t st);
 int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D);
 
 }  // namespace tl
