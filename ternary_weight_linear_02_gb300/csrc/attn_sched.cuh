@@ -9,6 +9,11 @@
 // GPU, and the division -- and with it the order of every sum -- depends on the
 // sizes alone.
 //
+// In that count each unit has OV more tiles than it has keys for, before its own: they
+// stand for the cost of beginning and ending a unit (queries, joins), without which a
+// block given a run of short units would be the last to end by far.  Nothing is done in
+// them, and a block whose run ends within them does not touch the unit.
+//
 // A block that runs through a whole unit writes its output.  Otherwise it leaves a
 // partial result (unnormalised rows, running maximum, running sum): in its slot 0
 // if the unit is the first of its run, else in slot 1 (it is then the last).
@@ -23,9 +28,14 @@
 namespace tl {
 
 constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite: no inf - inf)
-// f16 weights: 2^kAttnUp times their ratio to the running maximum, which lags the true one
-// by at most 2^kAttnSlack; times a value scale of at most half the reference: below 2^15
-constexpr float kAttnUp = 14.f, kAttnSlack = 2.f;
+// f16 weights: 2^kAttnUp times their ratio to the reference m of their row, times a value scale
+// of at most half its reference.  m moves only when a score exceeds it by kAttnSlack
+// (so weights stay below 2^15), and then kAttnMargin beyond the score: the largest weight
+// lies between 2^9 and 2^15, weights down to 2^-23 of it keep all 11 bits, and none above
+// 2^-33 vanishes.  With scores of a standard deviation of 2.6 (3.7 in powers of two) and no
+// margin, half the 64-key tiles moved some row of a warp, which cost more than the tile
+// itself (8 trees of 64 over 16384 keys: MARGIN_FIGS).
+constexpr float kAttnUp = 14.f, kAttnSlack = 2.f, kAttnMargin = 3.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -53,15 +63,23 @@ struct AttnPlace {
     int b, ctx;      // ctx: b's context
 };
 
-// Number of tiles of sequence b over all its units.
-template <int KT>
+// Keys per tile, and tiles counted beside a unit's own.
+template <int KEYS, int BESIDE>
+struct AttnTiling {
+    static constexpr int KT = KEYS, OV = BESIDE;
+    // own tiles of a unit of a sequence with ctx committed keys
+    static __device__ __forceinline__ int tiles(const AttnArgs &a, int ctx) { return (ctx + a.T + KT - 1) / KT; }
+};
+
+// Tiles counted for sequence b.
+template <typename TL>
 __device__ __forceinline__ int64_t attn_tiles(const AttnArgs &a, int b, int units) {
-    return (int64_t)((attn_context(a, b) + a.T + KT - 1) / KT) * units;
+    return (int64_t)(TL::tiles(a, attn_context(a, b)) + TL::OV) * units;
 }
 
 // Up to kPlaceFast sequences: every warp on its own, one load per 32 sequences and no barrier.
 constexpr int kPlaceFast = 128;
-template <int KT, typename Pick>
+template <typename TL, typename Pick>
 __device__ __forceinline__ AttnPlace attn_place_warp(const AttnArgs &a, int units, Pick pick) {
     constexpr int CH = kPlaceFast / 32;
     const int lane = threadIdx.x & 31;
@@ -74,7 +92,7 @@ __device__ __forceinline__ AttnPlace attn_place_warp(const AttnArgs &a, int unit
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        int v = c * 32 + lane < a.B ? (ctx[c] + a.T + KT - 1) / KT : 0;
+        int v = c * 32 + lane < a.B ? TL::tiles(a, ctx[c]) + TL::OV : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -104,14 +122,14 @@ __device__ __forceinline__ AttnPlace attn_place_warp(const AttnArgs &a, int unit
 
 // Executed by the whole block (NTHR threads); sh: NTHR / 32 + 2 64-bit words of shared
 // memory.  pick(N) gives the tile that is looked for.
-template <int KT, int NTHR, typename Pick>
+template <typename TL, int NTHR, typename Pick>
 __device__ __forceinline__ AttnPlace attn_place(const AttnArgs &a, int units, int64_t *sh, Pick pick) {
-    if (a.B <= kPlaceFast) return attn_place_warp<KT>(a, units, pick);
+    if (a.B <= kPlaceFast) return attn_place_warp<TL>(a, units, pick);
     constexpr int NW = NTHR / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // inclusive sums over one chunk of NTHR sequences; `total` of the chunk in sh[NW]
     auto scan = [&](int b0) -> int64_t {
-        const int64_t own = b0 + tid < a.B ? attn_tiles<KT>(a, b0 + tid, units) : 0;
+        const int64_t own = b0 + tid < a.B ? attn_tiles<TL>(a, b0 + tid, units) : 0;
         int64_t v = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -143,7 +161,7 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs &a, int units, in
             __syncthreads();
             base += sh[NW + 1];
         }
-        const int64_t own = b0 + tid < a.B ? attn_tiles<KT>(a, b0 + tid, units) : 0;
+        const int64_t own = b0 + tid < a.B ? attn_tiles<TL>(a, b0 + tid, units) : 0;
         if (tid == 0) sh[0] = -1;
         __syncthreads();
         if (x >= base + e && x < base + e + own) {
@@ -186,22 +204,34 @@ struct AttnSlot {
 // A walk over a block's run of tiles: sequence b, kv head hk, row block rt, tile of the unit.
 struct AttnWalk {
     int b, hk, rt, tile, tiles, ctx;
-    template <int KT>
-    __device__ __forceinline__ void start(const AttnArgs &a, const AttnPlace &p, int64_t x, int rtiles) {
+    int at, end;  // counted tiles from the run's start on; at < end: the walk is inside the run
+    template <typename TL>
+    __device__ __forceinline__ void start(const AttnArgs &a, const AttnPlace &p, int64_t x0, int64_t x1, int rtiles) {
         b = p.b;
         ctx = p.ctx;
-        tiles = (ctx + a.T + KT - 1) / KT;
-        const int64_t r = x - p.before;
+        tiles = TL::tiles(a, ctx);
+        const int64_t r = x0 - p.before;
         // a sequence's tiles fit 32 bits in any cache that fits memory; wider division otherwise
-        const int unit = r < (1ll << 31) ? (int)((unsigned)r / (unsigned)tiles) : (int)(r / tiles);
-        tile = (int)(r - (int64_t)unit * tiles);
+        const int all = tiles + TL::OV;
+        const int unit = r < (1ll << 31) ? (int)((unsigned)r / (unsigned)all) : (int)(r / all);
+        const int v = (int)(r - (int64_t)unit * all) - TL::OV;
+        tile = v < 0 ? 0 : v;
+        at = tile - v;
+        end = (int)(x1 - x0);
         hk = rtiles == 1 ? unit : unit / rtiles;
         rt = unit - hk * rtiles;
     }
-    // to the next tile (not past the last of the call); whether a unit begins there
-    template <int KT>
+    __device__ __forceinline__ bool inside() const { return at < end; }
+    __device__ __forceinline__ bool last_of_unit() const { return tile + 1 == tiles; }
+    // whether the next tile is inside the run too
+    template <typename TL>
+    __device__ __forceinline__ bool more() const { return at + 1 + (last_of_unit() ? TL::OV : 0) < end; }
+    // to the next tile; whether a unit begins there
+    template <typename TL>
     __device__ __forceinline__ bool next(const AttnArgs &a, int rtiles) {
+        ++at;
         if (++tile < tiles) return false;
+        at += TL::OV;
         tile = 0;
         if (++rt < rtiles) return true;
         rt = 0;
@@ -209,14 +239,14 @@ struct AttnWalk {
         hk = 0;
         if (++b < a.B) {
             ctx = attn_context(a, b);
-            tiles = (ctx + a.T + KT - 1) / KT;
+            tiles = TL::tiles(a, ctx);
         }
         return true;
     }
 };
 
-// Pages of the keys key0 + KT tile of a unit's tiles, without a division per tile: page index pi
-// in the sequence's row of the page table, place off in the page.
+// Pages of the keys of a unit's tiles: page index pi in the sequence's row of
+// the page table, place off in the page; moved along without a division.
 struct AttnPages {
     int pi, off, last;  // last: page index of the unit's last key
     __device__ __forceinline__ void start(const AttnArgs &a, const AttnWalk &w, int key) {
@@ -261,12 +291,12 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v
 struct AttnParts {
     int c0, c1, first;
 };
-template <int KT>
+template <typename TL>
 __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int unit, int units, int nc, int64_t *sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t pre = 0, all = 0;  // tiles before sequence b, and of the call
     for (int i = threadIdx.x; i < a.B; i += 128) {
-        const int64_t n = attn_tiles<KT>(a, i, units);
+        const int64_t n = attn_tiles<TL>(a, i, units);
         all += n;
         if (i < b) pre += n;
     }
@@ -281,10 +311,10 @@ __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int un
     pre = sh[0] + sh[1] + sh[2] + sh[3];
     const int64_t N = sh[4] + sh[5] + sh[6] + sh[7];
     if (N < nc) nc = (int)N;
-    const int64_t tiles = attn_tiles<KT>(a, b, 1), s = pre + unit * tiles;
-    r.c0 = attn_block_of(s, N, nc);
+    const int64_t tiles = attn_tiles<TL>(a, b, 1), s = pre + unit * tiles;
+    r.c0 = attn_block_of(s + TL::OV, N, nc);
     r.c1 = attn_block_of(s + tiles - 1, N, nc);
-    r.first = attn_first_tile(r.c0, N, nc) == s ? 0 : 1;
+    r.first = attn_first_tile(r.c0, N, nc) >= s ? 0 : 1;
     return r;
 }
 
@@ -335,7 +365,7 @@ struct AttnSum {
 // WIDE (few rows, many parts: single tokens over long contexts): one block per row,
 // its four warps sharing the parts.  Otherwise 16 rows per block, each warp taking
 // whole rows.
-template <int KT, int ROWS, int D, bool WIDE>
+template <typename TL, int ROWS, int D, bool WIDE>
 __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
     __shared__ int64_t sh[8];
     __shared__ float sm[4], sl[4], so[4][D];
@@ -346,7 +376,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
     const int64_t u = blockIdx.x / per_unit;
     const int slice = blockIdx.x % per_unit;
     const int b = (int)(u / units), unit = (int)(u % units), hk = unit / rtiles, rt = unit % rtiles;
-    const AttnParts p = attn_parts<KT>(a, b, unit, units, nc, sh);
+    const AttnParts p = attn_parts<TL>(a, b, unit, units, nc, sh);
     pdl_wait();
     if (p.c0 == p.c1) return;
     // the output row of row `grow` of the unit's (sequence, kv head)
@@ -393,7 +423,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, 
     }
 }
 
-template <int KT, int ROWS, int D, bool WIDE>
+template <typename TL, int ROWS, int D, bool WIDE>
 cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
     const int R = a.T * a.G, per_unit = WIDE ? R : ((R < ROWS ? R : ROWS) + 15) / 16;
     cudaLaunchConfig_t cfg = {};
@@ -405,7 +435,7 @@ cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<KT, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<TL, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
 }
 
 }  // namespace tl

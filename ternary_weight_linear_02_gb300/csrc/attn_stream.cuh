@@ -35,7 +35,8 @@ namespace tl {
 
 namespace {
 
-constexpr int kStreamKeys = 64, kStreamThreads = 128;
+constexpr int kStreamThreads = 128;
+using StreamTiling = AttnTiling<64, 2>;  // (a unit costs about two tiles beside its own)
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool valid) {
@@ -114,25 +115,25 @@ struct StreamCfg {
 template <int FMT, int D, int NB>
 __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS) attn_stream_kernel(AttnArgs a) {
     using C = StreamCfg<FMT, D, NB>;
-    constexpr int KT = kStreamKeys, ROWS = C::ROWS, NT = D / 16;
+    using TL = StreamTiling;
+    constexpr int KT = TL::KT, ROWS = C::ROWS, NT = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int nc = gridDim.x;
     const int R = a.T * a.G;
     pdl_launch_dependents();
 
-    const AttnPlace place = attn_place<KT, kStreamThreads>(a, a.c.Hk, reinterpret_cast<int64_t *>(smem + C::POFF),
+    const AttnPlace place = attn_place<TL, kStreamThreads>(a, a.c.Hk, reinterpret_cast<int64_t *>(smem + C::POFF),
                                                            [&](int64_t N) {
         if (N < nc) nc = (int)N;  // no block without a tile
         return attn_first_tile(blockIdx.x, N, nc);
     });
     const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
     if ((int)blockIdx.x >= nc) return;
-    const int steps = (int)(x1 - x0);
-
     uint8_t *ring = smem + warp * C::NS * C::STAGE;
     AttnWalk in, out;  // the tile being copied, the tile being computed
-    in.template start<KT>(a, place, x0, 1);
+    in.template start<TL>(a, place, x0, x1, 1);
+    if (!in.inside()) return;
     out = in;
 
     // Queries of a unit: TPR threads per row, EPT elements each (the first unit's are fetched
@@ -170,7 +171,11 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     const uint32_t dst0 = smem_u32(ring) + lane * C::KC;
     const int ksrc = g * C::RB + t * C::KC, vsrc = 2 * t * C::RB + g * C::VB;
     int put = 0;  // stage being filled
-    auto issue = [&](bool more) {
+    auto issue = [&]() {
+        if (!in.inside()) {
+            cp_commit();
+            return;
+        }
         const int left = in.ctx + a.T - (in.tile * KT + warp * 16);  // keys from the warp's first one on
         if (left > 0) {
             const int64_t row = (int64_t)attn_group(a, page, in.hk, where.off) << 4;
@@ -198,32 +203,33 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         }
         cp_commit();
         put = put + 1 == C::NS ? 0 : put + 1;
-        if (more) {
-            if (in.template next<KT>(a, 1)) where.start(a, in, in.tile * KT + warp * 16);
-            else where.next(a, KT);
-            page = where.fetch(a, in.b);
+        if (in.template next<TL>(a, 1)) {
+            if (!in.inside()) return;
+            where.start(a, in, warp * 16);
+        } else {
+            if (!in.inside()) return;
+            where.next(a, KT);
         }
+        page = where.fetch(a, in.b);
     };
 #pragma unroll 1
-    for (int i = 0; i < C::NS - 1; ++i) {
-        if (i < steps) issue(i + 1 < steps);
-        else cp_commit();
-    }
+    for (int i = 0; i < C::NS - 1; ++i) issue();
 
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : C::KSTEPS][2];
     uint2 *const qsm = reinterpret_cast<uint2 *>(smem + C::GOFF) + lane;
     float f[NB][2];                        // score factors of rows 8 n + 2t and + 1
     float m[NB][2], l[NB][2], svref = 1e-30f, inv = 1e30f;  // inv = 1 / svref
     float acc[NB][NT][4];
-    bool fresh = true;                     // the next tile begins a unit (for this block)
+    bool fresh = true, whole = true;       // the next tile begins a unit (for this block); the unit from its start
     int which = 0, get = 0;                // slot of a partial result; stage being read
 
 #pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
+    for (bool first = true; out.inside(); first = false) {
         if (fresh) {
             // ---------------- queries of the unit: rows as f16 in shared memory, then fragments
             fresh = false;
-            if (step > 0) fetch_queries(out);
+            whole = out.tile == 0;
+            if (!first) fetch_queries(out);
             float v[EPT];
 #pragma unroll
             for (int i = 0; i < EPT; i += 2) {
@@ -288,8 +294,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         }
 
         // ---------------- one group of 16 keys
-        if (step + C::NS - 1 < steps) issue(step + C::NS < steps);
-        else cp_commit();
+        issue();
         cp_wait<C::NS - 1>();
         __syncwarp();  // the scales were copied by other lanes
         const int key = out.tile * KT + warp * 16;
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         float x = fmaxf(z[n][r], z[n][2 + r]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        x = fmaxf(x, m[n][r]);
+                        x = x > m[n][r] + kAttnSlack ? x + kAttnMargin : m[n][r];
                         const float c = ex2(m[n][r] - x);
                         m[n][r] = x;
                         l[n][r] *= c;
@@ -478,8 +483,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
         get = get + 1 == C::NS ? 0 : get + 1;
 
         // ---------------- the end of a unit, or of the run: join the warps, write
-        const bool last = out.tile + 1 == out.tiles;
-        if (last || step + 1 == steps) {
+        const bool last = out.last_of_unit();
+        if (last || !out.template more<TL>()) {
+            whole = whole && last;
             float *wm = reinterpret_cast<float *>(smem + C::WOFF), *wl = wm + 4 * ROWS;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -524,7 +530,6 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 }
                 __syncthreads();
             }
-            const bool whole = last && step >= out.tile;  // the block saw the unit from its first tile on
             if (row < R) {
                 float M = wm[row], Ls = 0.f;
 #pragma unroll
@@ -561,7 +566,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             fresh = true;
             __syncthreads();  // the join buffers may be written again
         }
-        if (step + 1 < steps) out.template next<KT>(a, 1);
+        out.template next<TL>(a, 1);
     }
     cp_wait<0>();
 }
@@ -576,7 +581,7 @@ cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<kStreamKeys, C::ROWS, D, true>(a, 1, nc, st);
+    return launch_join<StreamTiling, C::ROWS, D, true>(a, 1, nc, st);
 }
 
 template <int FMT, int D>

@@ -33,7 +33,8 @@ namespace tl {
 namespace {
 
 constexpr int kLowExp = -80;  // of the value scale before any key
-constexpr int kTileKeys = 64, kTileRows = 128, kTileThreads = 256;
+using TileTiling = AttnTiling<64, 4>;  // (a unit costs about four tiles beside its own)
+constexpr int kTileKeys = TileTiling::KT, kTileRows = 128, kTileThreads = 256;
 
 template <int FMT, int D>
 struct AttnTileCfg {
@@ -87,7 +88,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 template <int FMT, int D>
 __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, int rtiles) {
     using C = AttnTileCfg<FMT, D>;
-    constexpr int KT = kTileKeys, ROWS = kTileRows;
+    using TL = TileTiling;
+    constexpr int KT = TL::KT, ROWS = kTileRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -114,14 +116,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         *abort_flag = 0;
         fence_barrier_init();
     }
-    const AttnPlace place = attn_place<KT, kTileThreads>(a, units, reinterpret_cast<int64_t *>(smem + C::POFF),
+    const AttnPlace place = attn_place<TL, kTileThreads>(a, units, reinterpret_cast<int64_t *>(smem + C::POFF),
                                                          [&](int64_t N) {
         if (N < nc) nc = (int)N;  // no block without a tile
         return attn_first_tile(blockIdx.x, N, nc);
     });
     const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
     if ((int)blockIdx.x >= nc) return;
-    const int steps = (int)(x1 - x0);
+    AttnWalk at;
+    at.template start<TL>(a, place, x0, x1, rtiles);
+    if (!at.inside()) return;
     if (warp == 4) tc::tmem_alloc(tmem_slot, C::COLS);
     tc::fence_before_sync();
     __syncthreads();
@@ -136,9 +140,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         if (a.status) atomicExch(a.status, kStatusTimeout);
         return false;
     };
-
-    AttnWalk at;
-    at.template start<KT>(a, place, x0, rtiles);
 
     if (warp >= 4) {
         // ---------------- decoders
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         where.start(a, ahead, at.tile * KT + (lane & 3) * 16);
         page = where.fetch(a, ahead.b);
         auto fetch = [&]() {
-            if (ahead.template next<KT>(a, rtiles)) where.start(a, ahead, ahead.tile * KT + (lane & 3) * 16);
+            if (ahead.template next<TL>(a, rtiles)) where.start(a, ahead, ahead.tile * KT + (lane & 3) * 16);
             else where.next(a, KT);
             page = where.fetch(a, ahead.b);
         };
@@ -314,12 +315,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         load(a.c.kc, kreg);
         load(a.c.vc, vreg);
         load_scales();
-        if (steps > 1) fetch();
+        if (ahead.template more<TL>()) fetch();
         int unit = 0;         // row factors' buffer
         bool fresh = true, before = true;  // the tile begins a unit (for this block); the one before it did
 #pragma unroll 1
-        for (int j = 0; j < steps; ++j) {
-            const bool more = j + 1 < steps;
+        int j = 0;
+        for (; at.inside(); ++j) {
+            const bool more = at.template more<TL>();
             if (j > 1 && !wait(sdone, j - 2)) break;  // S of tile j - 2 is computed: its keys' stage is free
             if (fresh) {
                 if (j > 0 && !wait(sdone, j - 1)) break;  // and the last unit's queries are
@@ -352,16 +354,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             publish(vfull + (j & 1));
             if (more) {
                 load(a.c.vc, vreg);
-                if (j + 2 < steps) fetch();
+                if (ahead.template more<TL>()) fetch();
             }
             // this tile's scores, then -- its softmax done meanwhile -- the last one's product
             if (dw == 0 && (!scores(j) || (j > 0 && !values(j - 1, before)))) break;
             before = fresh;
-            fresh = at.tile + 1 == at.tiles;
+            fresh = at.last_of_unit();
             if (fresh) ++unit;
-            if (more) at.template next<KT>(a, rtiles);
+            at.template next<TL>(a, rtiles);
         }
-        if (dw == 0) values(steps - 1, before);
+        if (dw == 0 && !at.inside()) values(j - 1, before);
     } else {
         // ---------------- softmax: thread = row = TMEM lane
         const int row = threadIdx.x;
@@ -369,12 +371,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         float m = kAttnLow, l = 0.f, f = 0.f;
         int ve = kLowExp;                     // svref = 2^ve
         int unit = 0, which = 0;
-        bool fresh = true;
+        bool fresh = true, whole = true;      // whole: the block sees the unit from its first tile on
 #pragma unroll 1
-        for (int j = 0; j < steps; ++j) {
+        for (int j = 0; at.inside(); ++j) {
             const int grow = at.rt * ROWS + row;
             const bool live = at.rt * ROWS + warp * 32 < R;  // the warp has rows
-            const bool last = at.tile + 1 == at.tiles;
+            const bool last = at.last_of_unit();
             const uint32_t scol = lane_base + C::SCOL + (uint32_t)(j & 1) * KT;
             if (!wait(sdone, j)) break;
             tc::fence_after_sync();
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 tc::ld_32x32b_x32(scol, s[0]);
                 tc::ld_32x32b_x32(scol + 32, s[1]);
                 if (fresh) {
+                    whole = at.tile == 0;
                     f = reinterpret_cast<const float *>(smem + C::FOFF)[(unit & 3) * 128 + row];
                     m = kAttnLow;
                     l = 0.f;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 top *= f;
                 const bool bigger = svmax > __uint_as_float((uint32_t)(ve + 127) << 23);
                 if (__any_sync(0xffffffffu, top > m + kAttnSlack || bigger)) {
-                    const float mn = fmaxf(m, top);
+                    const float mn = top > m + kAttnSlack ? top + kAttnMargin : m;
                     // a power of two in (2 svmax, 4 svmax]
                     const int vn = bigger ? min(120, (int)(__float_as_uint(svmax) >> 23) - 127 + 2) : ve;
                     const float c = ex2(m - mn + (float)(ve - vn));
@@ -494,12 +497,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull + (j & 1));
             fresh = false;
-            if (last || j + 1 == steps) {
+            if (last || !at.template more<TL>()) {
                 // ---------------- the unit's output, or this block's part of it
                 if (!wait(odone, j)) break;
                 tc::fence_after_sync();
                 if (live) {
-                    const bool whole = last && j >= at.tile;  // the block saw the unit from its first tile on
+                    whole = whole && last;
                     const float rl = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                     const int g = min(grow, R - 1);
                     const int64_t out_row = ((int64_t)at.b * a.T + g / a.G) * a.Hq + at.hk * a.G + g % a.G;
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 fresh = true;
                 ++unit;
             }
-            if (j + 1 < steps) at.template next<KT>(a, rtiles);
+            at.template next<TL>(a, rtiles);
         }
     }
     __syncwarp();
@@ -570,7 +573,7 @@ cudaError_t launch_tile_d(const AttnArgs &a, int sms, cudaStream_t st) {
     attn_tile_kernel<FMT, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<kTileKeys, kTileRows, D, false>(a, rtiles, nc, st);
+    return launch_join<TileTiling, kTileRows, D, false>(a, rtiles, nc, st);
 }
 
 template <int FMT>
