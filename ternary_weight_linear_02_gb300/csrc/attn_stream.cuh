@@ -36,7 +36,9 @@ namespace tl {
 namespace {
 
 constexpr int kStreamThreads = 128;
-using StreamTiling = AttnTiling<64, 2>;  // (a unit costs about two tiles beside its own)
+// GR: groups of 16 keys that a warp takes per tile
+template <int GR>
+using StreamTiling = AttnTiling<64 * GR, 2 / GR>;  // (a unit costs about 128 keys beside its own)
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool valid) {
@@ -60,7 +62,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -96,9 +98,11 @@ struct StreamCfg {
     static constexpr int KSTEPS = D / 16;
     // one stage of one warp: keys' copies, values' copies, 16 + 16 scales
     static constexpr int KOFF = 0, VOFF = 2 * NKC * KC * 32, SOFF = VOFF + 4 * VB * 32;
-    static constexpr int STAGE = SOFF + 128;
-    static constexpr int BLOCKS = NB == 1 ? 4 : NB == 2 ? 3 : 2;  // per SM (registers)
-    static constexpr int NS = STAGE > 3000 ? (NB == 3 ? 4 : 3) : STAGE > 2000 ? 5 : 8;  // stages per warp
+    static constexpr int GROUP = SOFF + 128;              // bytes of one group
+    static constexpr int GR = NB == 1 ? 2 : 1;            // groups per tile and warp
+    static constexpr int STAGE = GR * GROUP;
+    static constexpr int BLOCKS = 3;                      // per SM (registers)
+    static constexpr int NS = (GROUP > 3000 ? 2 + 2 / NB : GROUP > 2000 ? 6 : 8) / GR;  // stages per warp
     static constexpr bool QSMEM = NB > 1;                 // the queries' fragments stay in shared memory
     static constexpr int PITCH = D + 4;                   // floats per row of the join buffer
     // [stages of 4 warps][join rows; at a unit's start, its queries in f16]
@@ -115,7 +119,8 @@ struct StreamCfg {
 template <int FMT, int D, int NB>
 __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS) attn_stream_kernel(AttnArgs a) {
     using C = StreamCfg<FMT, D, NB>;
-    using TL = StreamTiling;
+    constexpr int GR = C::GR;
+    using TL = StreamTiling<GR>;
     constexpr int KT = TL::KT, ROWS = C::ROWS, NT = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 
     // Queries of a unit: TPR threads per row, EPT elements each (the first unit's are fetched
     // before its keys).
-    constexpr int TPR = NB == 3 ? 4 : kStreamThreads / ROWS, EPT = D / TPR;
+    constexpr int TPR = kStreamThreads / ROWS, EPT = D / TPR;
     const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
     uint32_t raw[EPT / 2];
     auto fetch_queries = [&](const AttnWalk &w) {
@@ -165,9 +170,17 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     fetch_queries(out);
 
     // Copies run NS - 1 tiles ahead; the page of the tile after that is already on its way.
-    AttnPages where;
-    where.start(a, in, in.tile * KT + warp * 16);
-    int page = where.fetch(a, in.b);
+    AttnPages where[GR];
+    int page[GR];
+    auto locate = [&](bool start) {
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+            if (start) where[i].start(a, in, in.tile * KT + i * 64 + warp * 16);
+            else where[i].next(a, KT);
+            page[i] = where[i].fetch(a, in.b);
+        }
+    };
+    locate(true);
     const uint32_t dst0 = smem_u32(ring) + lane * C::KC;
     const int ksrc = g * C::RB + t * C::KC, vsrc = 2 * t * C::RB + g * C::VB;
     int put = 0;  // stage being filled
@@ -176,41 +189,38 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             cp_commit();
             return;
         }
-        const int left = in.ctx + a.T - (in.tile * KT + warp * 16);  // keys from the warp's first one on
-        if (left > 0) {
-            const int64_t row = (int64_t)attn_group(a, page, in.hk, where.off) << 4;
-            const uint8_t *kp = a.c.kc + row * C::RB + ksrc, *vp = a.c.vc + row * C::RB + vsrc;
-            const uint32_t st = dst0 + (uint32_t)put * C::STAGE;
-            const uint32_t sv = st + C::VOFF - lane * (C::KC - C::VB);
-            auto copy = [&](auto whole) {  // whole: no key of the 16 lies beyond the last
-                constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+        for (int i = 0; i < GR; ++i) {
+            const int left = in.ctx + a.T - (in.tile * KT + i * 64 + warp * 16);  // keys from the group's first one on
+            if (left > 0) {
+                const int64_t row = (int64_t)attn_group(a, page[i], in.hk, where[i].off) << 4;
+                const uint8_t *kp = a.c.kc + row * C::RB + ksrc, *vp = a.c.vc + row * C::RB + vsrc;
+                const uint32_t st = dst0 + (uint32_t)(put * C::STAGE + i * C::GROUP);
+                const uint32_t sv = st + C::VOFF - lane * (C::KC - C::VB);
+                auto copy = [&](auto whole) {  // whole: no key of the 16 lies beyond the last
+                    constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-                    for (int j = 0; j < C::NKC; ++j)
-                        cp_async<C::KC>(st + C::KOFF + (n * C::NKC + j) * 32 * C::KC, kp + n * 8 * C::RB + j * 4 * C::KC,
-                                        ALL || n * 8 + g < left);
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = (j & 1) + (j >> 1) * 8;
-                    cp_async<C::VB>(sv + j * 32 * C::VB, vp + r * C::RB, ALL || 2 * t + r < left);
-                }
-            };
-            if (left >= 16) copy(std::true_type());
-            else copy(std::false_type());
-            if (lane < 8)
-                cp_async<16>(st + C::SOFF + lane * (16 - C::KC), (lane < 4 ? a.c.ks : a.c.vs) + row + (lane & 3) * 4, true);
+                        for (int j = 0; j < C::NKC; ++j)
+                            cp_async<C::KC>(st + C::KOFF + (n * C::NKC + j) * 32 * C::KC, kp + n * 8 * C::RB + j * 4 * C::KC,
+                                            ALL || n * 8 + g < left);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = (j & 1) + (j >> 1) * 8;
+                        cp_async<C::VB>(sv + j * 32 * C::VB, vp + r * C::RB, ALL || 2 * t + r < left);
+                    }
+                };
+                if (left >= 16) copy(std::true_type());
+                else copy(std::false_type());
+                if (lane < 8)
+                    cp_async<16>(st + C::SOFF + lane * (16 - C::KC), (lane < 4 ? a.c.ks : a.c.vs) + row + (lane & 3) * 4, true);
+            }
         }
         cp_commit();
         put = put + 1 == C::NS ? 0 : put + 1;
-        if (in.template next<TL>(a, 1)) {
-            if (!in.inside()) return;
-            where.start(a, in, warp * 16);
-        } else {
-            if (!in.inside()) return;
-            where.next(a, KT);
-        }
-        page = where.fetch(a, in.b);
+        const bool start = in.template next<TL>(a, 1);
+        if (in.inside()) locate(start);
     };
 #pragma unroll 1
     for (int i = 0; i < C::NS - 1; ++i) issue();
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             for (int i = 0; i < EPT; i += 2)
                 *reinterpret_cast<__half2 *>(qs + i) = __floats2half2_rn(v[i] * down, v[i + 1] * down);
             float *fac = reinterpret_cast<float *>(smem + C::FOFF);
-            if (part == 0 && row < ROWS) fac[row] = a.scale * kLog2e * up;
+            if (part == 0) fac[row] = a.scale * kLog2e * up;
             __syncthreads();
             const uint16_t *qr = reinterpret_cast<const uint16_t *>(smem + C::JOFF);
             // the elements of this thread in step s, in the order its code words give
@@ -293,108 +303,123 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             __syncthreads();  // the queries' buffer is the join buffer too
         }
 
-        // ---------------- one group of 16 keys
+        // ---------------- GR groups of 16 keys (independent chains up to the weights)
         issue();
         cp_wait<C::NS - 1>();
         __syncwarp();  // the scales were copied by other lanes
         const int key = out.tile * KT + warp * 16;
         if (key < out.ctx + a.T) {
-            const uint8_t *st = ring + get * C::STAGE;
-            // one block of rows: two chains of sums (even and odd steps), half the latency of one
-            float s[NB][4], s2[1][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s2[0][j] = 0.f;
-#pragma unroll
-                for (int n = 0; n < NB; ++n) s[n][j] = 0.f;
-            }
-            uint32_t w[2][C::KB / 4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int j = 0; j < C::NKC; ++j) {
-                    const uint8_t *p = st + C::KOFF + ((n * C::NKC + j) * 32 + lane) * C::KC;
-                    if constexpr (C::KC == 16) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-                        w[n][4 * j] = u.x, w[n][4 * j + 1] = u.y, w[n][4 * j + 2] = u.z, w[n][4 * j + 3] = u.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                        w[n][0] = u.x, w[n][1] = u.y;
-                    }
-                }
-#pragma unroll
-            for (int i = 0; i < C::KSTEPS; ++i) {
-                uint32_t x[4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    if constexpr (FMT == kKvInt4) {
-                        const uint32_t u = i & 1 ? w[n][i >> 1] >> 8 : w[n][i >> 1];
-                        x[n] = int4_lo(u);
-                        x[2 + n] = int4_hi(u);
-                    } else if constexpr (FMT == kKvInt8) {
-                        const uint32_t u = w[n][i] ^ 0x80808080u;
-                        x[n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4140));
-                        x[2 + n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4342));
-                    } else {
-                        x[n] = e4m3x2_raw(w[n][i]);
-                        x[2 + n] = e4m3x2_raw(w[n][i] >> 16);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    if constexpr (C::QSMEM) {
-                        const uint2 u = qsm[(n * C::KSTEPS + i) * 32];
-                        mma16816(s[n], x, u.x, u.y);
-                    } else {
-                        mma16816(i & 1 ? s2[n] : s[n], x, qf[n][i][0], qf[n][i][1]);
-                    }
-                }
-            }
-            const float *sc = reinterpret_cast<const float *>(st + C::SOFF);
-            const float sk[2] = {sc[g], sc[g + 8]};
-            float sv[2] = {sc[16 + g], sc[24 + g]};
+            const uint8_t *const stage = ring + get * C::STAGE;
             // z: scores in powers of two; [0], [1]: key g of rows 2t, 2t + 1; [2], [3]: key g + 8
-            float z[NB][4];
+            float z[GR][NB][4], sv[GR][2];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int gr = 0; gr < GR; ++gr) {
+                const uint8_t *st = stage + gr * C::GROUP;
+                float s[NB][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) z[n][j] = (NB == 1 ? s[n][j] + s2[0][j] : s[n][j]) * sk[j >> 1] * f[n][j & 1];
-            uint32_t unseen = 0;
-            if (key + 16 > out.ctx) {  // new tokens' keys, or the end
-                const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
-                bool any[2] = {false, false};
+                for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                uint32_t w[2][C::KB / 4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < C::NKC; ++j) {
+                        const uint8_t *p = st + C::KOFF + ((n * C::NKC + j) * 32 + lane) * C::KC;
+                        if constexpr (C::KC == 16) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+                            w[n][4 * j] = u.x, w[n][4 * j + 1] = u.y, w[n][4 * j + 2] = u.z, w[n][4 * j + 3] = u.w;
+                        } else {
+                            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                            w[n][0] = u.x, w[n][1] = u.y;
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < C::KSTEPS; ++i) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        if constexpr (FMT == kKvInt4) {
+                            const uint32_t u = i & 1 ? w[n][i >> 1] >> 8 : w[n][i >> 1];
+                            x[n] = int4_lo(u);
+                            x[2 + n] = int4_hi(u);
+                        } else if constexpr (FMT == kKvInt8) {
+                            const uint32_t u = w[n][i] ^ 0x80808080u;
+                            x[n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4140));
+                            x[2 + n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4342));
+                        } else {
+                            x[n] = e4m3x2_raw(w[n][i]);
+                            x[2 + n] = e4m3x2_raw(w[n][i] >> 16);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        if constexpr (C::QSMEM) {
+                            const uint2 u = qsm[(n * C::KSTEPS + i) * 32];
+                            mma16816(s[n], x, u.x, u.y);
+                        } else {
+                            mma16816(s[n], x, qf[n][i][0], qf[n][i][1]);
+                        }
+                    }
+                }
+                const float *sc = reinterpret_cast<const float *>(st + C::SOFF);
+                const float sk[2] = {sc[g], sc[g + 8]};
+                sv[gr][0] = sc[16 + g];
+                sv[gr][1] = sc[24 + g];
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int i = key + g + (j >> 1) * 8 - out.ctx;  // index of the new token
-                        const int tok = min(R - 1, 8 * n + 2 * t + (j & 1)) / a.G;
-                        bool u = i < 0;
-                        if (i >= 0 && i < a.T) u = tree ? tree[tok * a.tree_r + i] != 0 : i <= tok;
-                        if (u) any[j >> 1] = true;
-                        else z[n][j] = -INFINITY, unseen |= 1u << (4 * n + j);
-                    }
-                if (!any[0]) sv[0] = 0.f;  // unseen scales may hold anything
-                if (!any[1]) sv[1] = 0.f;
+                    for (int j = 0; j < 4; ++j) z[gr][n][j] = s[n][j] * sk[j >> 1] * f[n][j & 1];
             }
-            bool move = fmaxf(sv[0], sv[1]) > svref;
+            uint32_t unseen = 0;
+            if (key + (GR - 1) * 64 + 16 > out.ctx) {  // new tokens' keys, or the end
+                const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                    bool any[2] = {false, false};
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int i = key + gr * 64 + g + (j >> 1) * 8 - out.ctx;  // index of the new token
+                            const int tok = min(R - 1, 8 * n + 2 * t + (j & 1)) / a.G;
+                            bool u = i < 0;
+                            if (i >= 0 && i < a.T) u = tree ? tree[tok * a.tree_r + i] != 0 : i <= tok;
+                            if (u) any[j >> 1] = true;
+                            else z[gr][n][j] = -INFINITY, unseen |= 1u << (4 * (gr * NB + n) + j);
+                        }
+                    if (!any[0]) sv[gr][0] = 0.f;  // unseen scales may hold anything
+                    if (!any[1]) sv[gr][1] = 0.f;
+                }
+            }
+            float svm = fmaxf(sv[0][0], sv[0][1]), top[NB][2];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
-                move = move || fmaxf(z[n][0], z[n][2]) > m[n][0] + kAttnSlack || fmaxf(z[n][1], z[n][3]) > m[n][1] + kAttnSlack;
-            if (__any_sync(0xffffffffu, move)) {
-                float rv = fmaxf(sv[0], sv[1]), cv = 1.f;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) rv = fmaxf(rv, __shfl_xor_sync(0xffffffffu, rv, o));
-                if (rv > svref) {  // twice the largest: the next slightly larger one changes nothing
-                    cv = svref / (2.f * rv);
-                    svref = 2.f * rv;
+                for (int r = 0; r < 2; ++r) top[n][r] = fmaxf(z[0][n][r], z[0][n][2 + r]);
+#pragma unroll
+            for (int gr = 1; gr < GR; ++gr) {
+                svm = fmaxf(svm, fmaxf(sv[gr][0], sv[gr][1]));
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) top[n][r] = fmaxf(top[n][r], fmaxf(z[gr][n][r], z[gr][n][2 + r]));
+            }
+            bool move = svm > svref;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) move = move || top[n][0] > m[n][0] + kAttnSlack || top[n][1] > m[n][1] + kAttnSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                float cv = 1.f;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, o));
+                if (svm > svref) {  // twice the largest: the next slightly larger one changes nothing
+                    cv = svref / (2.f * svm);
+                    svref = 2.f * svm;
                     inv = __frcp_rn(svref);
                 }
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float x = fmaxf(z[n][r], z[n][2 + r]);
+                        float x = top[n][r];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                         x = x > m[n][r] + kAttnSlack ? x + kAttnMargin : m[n][r];
@@ -408,73 +433,77 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         }
                     }
             }
-            const float wv[2] = {sv[0] * inv, sv[1] * inv};
-            uint32_t pb[NB][2];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                float p[4];
+            for (int gr = 0; gr < GR; ++gr) {
+                const uint8_t *st = stage + gr * C::GROUP;
+                const float wv[2] = {sv[gr][0] * inv, sv[gr][1] * inv};
+                uint32_t pb[NB][2];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float e = ex2(z[gr][n][j] - (m[n][j & 1] - kAttnUp));
+                        l[n][j & 1] += e;
+                        p[j] = e * wv[j >> 1];
+                    }
+                    if (unseen) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (unseen >> (4 * (gr * NB + n) + j) & 1u) p[j] = 0.f;
+                    }
+                    pb[n][0] = transpose8x8(pack2(__half(), p[0], p[1]));
+                    pb[n][1] = transpose8x8(pack2(__half(), p[2], p[3]));
+                }
+                // values: elements 2i and 2i + 1 of lane group g's run are its rows of MMA i
+                uint32_t v[4][C::VB / 4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = ex2(z[n][j] - (m[n][j & 1] - kAttnUp));
-                    l[n][j & 1] += e;
-                    p[j] = e * wv[j >> 1];
+                    const uint8_t *p = st + C::VOFF + (j * 32 + lane) * C::VB;
+                    if constexpr (C::VB == 16) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+                        v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
+                    } else if constexpr (C::VB == 8) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                        v[j][0] = u.x, v[j][1] = u.y;
+                    } else {
+                        v[j][0] = *reinterpret_cast<const uint32_t *>(p);
+                    }
                 }
-                if (unseen) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (unseen >> (4 * n + j) & 1u) p[j] = 0.f;
-                }
-                pb[n][0] = transpose8x8(pack2(__half(), p[0], p[1]));
-                pb[n][1] = transpose8x8(pack2(__half(), p[2], p[3]));
-            }
-            // values: elements 2i and 2i + 1 of lane group g's run are its rows of MMA i
-            uint32_t v[4][C::VB / 4];
+                for (int i = 0; i < C::VB / 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint8_t *p = st + C::VOFF + (j * 32 + lane) * C::VB;
-                if constexpr (C::VB == 16) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-                    v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
-                } else if constexpr (C::VB == 8) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                    v[j][0] = u.x, v[j][1] = u.y;
-                } else {
-                    v[j][0] = *reinterpret_cast<const uint32_t *>(p);
-                }
-            }
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if constexpr (FMT == kKvInt4) {  // elements 0-3, then 4-7, of the two keys of a pair
+                            const uint32_t sel = hh ? 0x7632 : 0x5410;
+                            const uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
+                            const uint32_t a0[4] = {int4_lo(x), int4_hi(x), int4_lo(y), int4_hi(y)};
+                            const uint32_t a1[4] = {int4_lo(x >> 8), int4_hi(x >> 8), int4_lo(y >> 8), int4_hi(y >> 8)};
 #pragma unroll
-            for (int i = 0; i < C::VB / 4; ++i) {
+                            for (int n = 0; n < NB; ++n) {
+                                mma16816(acc[n][4 * i + 2 * hh], a0, pb[n][0], pb[n][1]);
+                                mma16816(acc[n][4 * i + 2 * hh + 1], a1, pb[n][0], pb[n][1]);
+                            }
+                        } else {  // bytes 0, 1, then 2, 3, interleaved over the pair's keys
+                            const uint32_t sel = hh ? 0x7362 : 0x5140;
+                            uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
+                            uint32_t a0[4];
+                            if constexpr (FMT == kKvInt8) {
+                                x ^= 0x80808080u;
+                                y ^= 0x80808080u;
+                                a0[0] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4140));
+                                a0[1] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4342));
+                                a0[2] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4140));
+                                a0[3] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4342));
+                            } else {
+                                a0[0] = e4m3x2_f16x2(x);
+                                a0[1] = e4m3x2_f16x2(x >> 16);
+                                a0[2] = e4m3x2_f16x2(y);
+                                a0[3] = e4m3x2_f16x2(y >> 16);
+                            }
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    if constexpr (FMT == kKvInt4) {  // elements 0-3, then 4-7, of the two keys of a pair
-                        const uint32_t sel = hh ? 0x7632 : 0x5410;
-                        const uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
-                        const uint32_t a0[4] = {int4_lo(x), int4_hi(x), int4_lo(y), int4_hi(y)};
-                        const uint32_t a1[4] = {int4_lo(x >> 8), int4_hi(x >> 8), int4_lo(y >> 8), int4_hi(y >> 8)};
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            mma16816(acc[n][4 * i + 2 * hh], a0, pb[n][0], pb[n][1]);
-                            mma16816(acc[n][4 * i + 2 * hh + 1], a1, pb[n][0], pb[n][1]);
+                            for (int n = 0; n < NB; ++n) mma16816(acc[n][2 * i + hh], a0, pb[n][0], pb[n][1]);
                         }
-                    } else {  // bytes 0, 1, then 2, 3, interleaved over the pair's keys
-                        const uint32_t sel = hh ? 0x7362 : 0x5140;
-                        uint32_t x = __byte_perm(v[0][i], v[1][i], sel), y = __byte_perm(v[2][i], v[3][i], sel);
-                        uint32_t a0[4];
-                        if constexpr (FMT == kKvInt8) {
-                            x ^= 0x80808080u;
-                            y ^= 0x80808080u;
-                            a0[0] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4140));
-                            a0[1] = int8_f16x2(__byte_perm(x, 0x64646464u, 0x4342));
-                            a0[2] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4140));
-                            a0[3] = int8_f16x2(__byte_perm(y, 0x64646464u, 0x4342));
-                        } else {
-                            a0[0] = e4m3x2_f16x2(x);
-                            a0[1] = e4m3x2_f16x2(x >> 16);
-                            a0[2] = e4m3x2_f16x2(y);
-                            a0[3] = e4m3x2_f16x2(y >> 16);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) mma16816(acc[n][2 * i + hh], a0, pb[n][0], pb[n][1]);
                     }
                 }
             }
@@ -581,15 +610,13 @@ cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<StreamTiling, C::ROWS, D, true>(a, 1, nc, st);
+    return launch_join<StreamTiling<C::GR>, C::ROWS, D, true>(a, 1, nc, st);
 }
 
 template <int FMT, int D>
 cudaError_t launch_stream_n(const AttnArgs &a, int sms, cudaStream_t st) {
     const int rows = a.T * a.G;
-    return rows <= 8    ? launch_stream_d<FMT, D, 1>(a, sms, st)
-           : rows <= 16 ? launch_stream_d<FMT, D, 2>(a, sms, st)
-                        : launch_stream_d<FMT, D, 3>(a, sms, st);
+    return rows <= 8 ? launch_stream_d<FMT, D, 1>(a, sms, st) : launch_stream_d<FMT, D, 2>(a, sms, st);
 }
 
 template <int FMT>

@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         if (ahead.template more<TL>()) fetch();
         int unit = 0;         // row factors' buffer
         bool fresh = true, before = true;  // the tile begins a unit (for this block); the one before it did
-#pragma unroll 1
         int j = 0;
+#pragma unroll 1
         for (; at.inside(); ++j) {
             const bool more = at.template more<TL>();
             if (j > 1 && !wait(sdone, j - 2)) break;  // S of tile j - 2 is computed: its keys' stage is free

@@ -6,10 +6,12 @@ namespace tl {
 
 namespace {
 
-// Rows of a kv head (new tokens x query heads that share it): up to 24 the streaming kernel,
-// whose warp MMAs keep up with the cache's bytes; above, it would read the cache once
-// per 24 rows, and the tcgen05 kernel takes 128 rows at a time.
-constexpr int64_t kStreamMaxRows = 24;
+// Rows of a kv head (new tokens x query heads that share it): up to 16 the streaming kernel,
+// whose warp MMAs keep up with the cache's bytes (6 sequences of up to 4099 keys, 32 heads,
+// int4: 78 us at 16 rows against 106 us); above, it would need more registers than a
+// thread has or read the cache twice, and the tcgen05 kernel takes 128 rows at a time
+// (106 us at 25 rows, against 125 us of a three-block streaming form at 24).
+constexpr int64_t kStreamMaxRows = 16;
 bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 
 }  // namespace
@@ -17,7 +19,7 @@ bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 // Two slots per block (attn_sched.cuh): rows of D, a maximum and a sum each.
 int64_t tree_attention_workspace(int64_t, int64_t T, int Hq, int Hk, int D) {
     const int64_t rows = T * (Hq / Hk);
-    const int64_t blocks = rows <= 8 ? 4 : rows <= 16 ? 3 : 2, slot = rows <= 8 ? 8 : rows <= 16 ? 16 : use_tile(rows) ? 128 : 24;
+    const int64_t blocks = use_tile(rows) ? 2 : 3, slot = use_tile(rows) ? 128 : rows <= 8 ? 8 : 16;
     return kMaxSms * blocks * 2 * slot * (D + 2) * 4;
 }
 
