@@ -5,15 +5,17 @@
 //
 // A block owns 128 rows of one (sequence, kv head) -- TMEM lanes, one softmax thread
 // each -- and walks tiles of 64 keys; two blocks per SM.
-//  * Warps 4-7 decode: codes go from global memory to registers a tile ahead, become f16
-//    (exact) and are stored to one of two stages of shared memory in 128-byte-swizzled
-//    rows, keys and values alike: keys are read as a K-major operand, values as an
-//    MN-major one, so neither is transposed.  They also place the queries at a unit's
-//    start (f16; from bf16 scaled by the power of two of the row's largest element) and
-//    the tile's scales.
-//  * Warp 4 also issues tcgen05.mma (kind::f16, fp32 in TMEM): S = Q K^T from shared memory
-//    into one of two buffers, so that the scores of the next tile are computed during
-//    the softmax of this one, and O += P V with P from TMEM.
+//  * Warp 4 copies: a tile's codes and scales land in shared memory as they lie in the cache
+//    (bulk copies of 16 keys of one page), keys three tiles ahead and values two.  It
+//    also issues tcgen05.mma (kind::f16, fp32 in TMEM): S = Q K^T from shared memory into
+//    one of two buffers, so that the scores of the next tile are computed during the
+//    softmax of this one, and O += P V with P from TMEM.
+//  * Warps 5-7 decode codes to f16 (exact) in 128-byte-swizzled rows, keys and values alike:
+//    keys are read as a K-major operand, values as an MN-major one, so neither is
+//    transposed.  They also place the queries at a unit's start (f16; from bf16 scaled by
+//    the power of two of the row's largest element).  Codes that came through registers
+//    instead, a tile ahead, were waited for with every other load of their warp
+//    (page table, scales): 5000 cycles a tile against STAGED_CYCLES.
 //  * Warps 0-3: a row's 64 scores are read once into registers; P (f16) overwrites the
 //    first half of them in TMEM.  The weights hold the value scale relative to a power of two
 //    svref at least twice the largest scale met, 2^14 up, so that weights down to 2^-28 of
@@ -43,25 +45,34 @@ struct AttnTileCfg {
     static constexpr int UB = 16 * KvCode<FMT>::bits / 8; // bytes of 16 codes
     static constexpr int RB = D / 16 * UB;                // bytes per row of codes
     static constexpr int LANES = D / 16;                  // threads per row
-    // A pass is one load and store of a warp: RPP rows.  The issuing warp takes FEW of the
-    // tile's passes, the other three MANY each.
-    static constexpr int RPP = 32 / LANES, PASSES = kTileKeys / RPP;
-    static constexpr int FEW = D == 128 ? 1 : 0, MANY = (PASSES - FEW + 2) / 3;
+    // A pass is one load and store of a warp: RPP rows; the three decoder warps take turns.
+    static constexpr int RPP = 32 / LANES, PASSES = kTileKeys / RPP, MANY = (PASSES + 2) / 3;
     static constexpr uint32_t SCOL = 0, OCOL = 128, COLS = 256;  // S: two buffers of 64 columns
-    static constexpr int KSTAGE = HALVES * KBLOCK;
-    static constexpr int QOFF = 0, KOFF = HALVES * QBLOCK, VOFF = KOFF + 2 * KSTAGE;
-    static constexpr int SKOFF = VOFF + 2 * KSTAGE;       // key scales [4][64], value scales [4][64],
-    static constexpr int SVOFF = SKOFF + 4 * kTileKeys * 4;
+    static constexpr int TILE = HALVES * KBLOCK;          // keys or values of a tile as f16
+    static constexpr int QOFF = 0, KOFF = HALVES * QBLOCK, VOFF = KOFF + TILE;
+    // codes as they lie in the cache: two stages of keys, two of values; scales of four tiles
+    static constexpr int CODES = kTileKeys * RB, CKOFF = VOFF + TILE, CVOFF = CKOFF + 2 * CODES;
+    static constexpr int SKOFF = CVOFF + 2 * CODES, SVOFF = SKOFF + 4 * kTileKeys * 4;
     static constexpr int SMOFF = SVOFF + 4 * kTileKeys * 4;  // largest value scale [4],
     static constexpr int FOFF = SMOFF + 16;               // row factors [4][128]
     static constexpr int BOFF = FOFF + 4 * 512;           // barriers, TMEM slot, abort flag
-    static constexpr int POFF = BOFF + 128;               // place of the run (14 words)
-    static constexpr int SMEM = POFF + 112 + 1024;        // 1 KB of alignment slack
+    static constexpr int POFF = BOFF + 128;               // place of the run (10 words)
+    static constexpr int SMEM = POFF + 80 + 1024;         // 1 KB of alignment slack
     // no more blocks per SM than its 512 TMEM columns serve
     static constexpr int REQ = SMEM > 80 * 1024 ? SMEM : 80 * 1024;
     static_assert(2 * (REQ + 1024) <= 228 * 1024 && 3 * (REQ + 1024) > 228 * 1024, "two blocks per SM");
 };
 
+__device__ __forceinline__ void sts_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t (&w)[4]) {
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
     asm("mul.rn.f32x2 %0, %1, %2;"
@@ -93,11 +104,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    // two of each: tile j uses number j & 1, in its phase j >> 1
+    // tile j: number j & 1 in phase j >> 1 of the pairs, phase j of the single ones
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::BOFF);
-    uint64_t *kfull = bars, *vfull = bars + 2, *sdone = bars + 4, *pfull = bars + 6, *odone = bars + 8;
-    uint64_t *fin = bars + 10;  // after a give-up: every product issued has ended
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 11);
+    uint64_t *ckfull = bars, *cvfull = bars + 2, *sdone = bars + 4, *pfull = bars + 6, *odone = bars + 8;
+    uint64_t *kfull = bars + 10, *vfull = bars + 11;
+    uint64_t *fin = bars + 12;  // after a give-up: every product issued has ended
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int nc = gridDim.x;
@@ -106,12 +118,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(kfull + i, 4);  // one arrival per decoder warp
-            mbar_init(vfull + i, 4);
+            mbar_init(ckfull + i, 1);  // the copies' bytes
+            mbar_init(cvfull + i, 1);
             mbar_init(sdone + i, 1);
-            mbar_init(pfull + i, 4);  // one per softmax warp
+            mbar_init(pfull + i, 4);  // one arrival per softmax warp
             mbar_init(odone + i, 1);
         }
+        mbar_init(kfull, 3);  // one per decoder warp
+        mbar_init(vfull, 3);
         mbar_init(fin, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -132,101 +146,160 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    auto wait = [&](uint64_t *bar, int j) -> bool {  // of tile j
-        const uint32_t parity = (uint32_t)(j >> 1) & 1u;
-        if (mbar_try_wait(bar + (j & 1), parity)) return true;
-        if (!*abort_flag && mbar_wait_bounded(bar + (j & 1), parity)) return true;
+    auto wait_phase = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (!*abort_flag && mbar_wait_bounded(bar, parity)) return true;
         *abort_flag = 1;
         if (a.status) atomicExch(a.status, kStatusTimeout);
         return false;
     };
+    auto wait = [&](uint64_t *pair, int j) -> bool { return wait_phase(pair + (j & 1), (uint32_t)(j >> 1) & 1u); };
+    auto wait1 = [&](uint64_t *bar, int j) -> bool { return wait_phase(bar, (uint32_t)j & 1u); };
 
-    if (warp >= 4) {
+    if (warp == 4) {
+        // ---------------- copies and products: the whole warp walks; lane i of the first four
+        // copies group i of 16 keys, and one lane issues the products, so that descriptors
+        // stay in uniform registers
+        constexpr uint32_t idesc_s = tc::idesc_f16(KT, false);
+        constexpr uint32_t idesc_o = tc::idesc_f16(D, false) | tc::kIdescBTransposed;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        AttnWalk ahead = at;  // the tile that is copied next; its page is fetched a tile before
+        AttnPages where;
+        where.start(a, ahead, ahead.tile * KT + (lane & 3) * 16);
+        int page = where.fetch(a, ahead.b);
+        uint32_t group = 0, group1 = 0;  // of the tile whose keys were copied last, and of the one before
+        int groups = 0, groups1 = 0;     // (none: 0)
+        constexpr uint32_t codes = 16 * C::RB;
+        auto copy_keys = [&](int j) {  // and both sides' scales
+            group1 = group;
+            groups1 = groups;
+            groups = 0;
+            if (!ahead.inside()) return;
+            groups = min(KT / 16, (ahead.ctx + a.T - ahead.tile * KT + 15) >> 4);
+            group = attn_group(a, page, ahead.hk, where.off);
+            uint64_t *bar = ckfull + (j & 1);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)groups * (codes + 128));
+            __syncwarp();
+            if (lane < groups) {
+                const int64_t row = (int64_t)group << 4;
+                bulk_g2s(smem + C::CKOFF + (j & 1) * C::CODES + lane * codes, a.c.kc + row * C::RB, codes, bar);
+                bulk_g2s(smem + C::SKOFF + (j & 3) * KT * 4 + lane * 64, a.c.ks + row, 64, bar);
+                bulk_g2s(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 64, a.c.vs + row, 64, bar);
+            }
+            __syncwarp();
+            const bool start = ahead.template next<TL>(a, rtiles);
+            if (!ahead.inside()) return;
+            if (start) where.start(a, ahead, (lane & 3) * 16);
+            else where.next(a, KT);
+            page = where.fetch(a, ahead.b);
+        };
+        auto copy_values = [&](int j, uint32_t grp, int n) {
+            if (n == 0) return;
+            uint64_t *bar = cvfull + (j & 1);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * codes);
+            __syncwarp();
+            if (lane < n)
+                bulk_g2s(smem + C::CVOFF + (j & 1) * C::CODES + lane * codes, a.c.vc + ((int64_t)grp << 4) * C::RB, codes, bar);
+            __syncwarp();
+        };
+        auto scores = [&](int j) -> bool {
+            // S buffer j & 1 holds P of tile j - 2: its product has to be done
+            if ((j > 1 && !wait(odone, j - 2)) || !wait1(kfull, j)) return false;
+            tc::fence_after_sync();
+            const uint64_t qd = tc::desc_sw128(smem + C::QOFF), kd = tc::desc_sw128(smem + C::KOFF);
+            const uint32_t d = tm + C::SCOL + (uint32_t)(j & 1) * KT;
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc::mma_ss(d, qd + (uint64_t)((k >> 2) * (C::QBLOCK >> 4) + (k & 3) * 2),
+                               kd + (uint64_t)((k >> 2) * (C::KBLOCK >> 4) + (k & 3) * 2), idesc_s, k > 0);
+                tc::commit(sdone + (j & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto values = [&](int j, bool first) -> bool {
+            if (!wait(pfull, j) || !wait1(vfull, j)) return false;
+            tc::fence_after_sync();
+            const uint64_t vd = tc::desc_sw128_mn(smem + C::VOFF, C::KBLOCK);
+            const uint32_t p = tm + C::SCOL + (uint32_t)(j & 1) * KT;
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    tc::mma_ts(tm + C::OCOL, p + k * 8, vd + (uint64_t)(k * 128), idesc_o, !first || k > 0);
+                tc::commit(odone + (j & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        copy_keys(0);
+        copy_values(0, group, groups);
+        copy_keys(1);
+        copy_values(1, group, groups);
+        bool fresh = true;  // the tile begins a unit (for this block)
+        bool ok = scores(0);
+        if (ok) copy_keys(2);
+        int j = 0;
+#pragma unroll 1
+        for (; ok && at.inside(); ++j) {
+            // The next tile's scores, computed during this one's softmax.  Its keys' stage and the
+            // scales of the tile before this are then free (kfull; odone in scores), and after
+            // this tile's product its values' stage is (vfull).
+            if (at.template more<TL>()) ok = scores(j + 1);
+            if (ok) copy_keys(j + 3);
+            ok = ok && values(j, fresh);
+            if (ok) copy_values(j + 2, group1, groups1);
+            fresh = at.last_of_unit();
+            at.template next<TL>(a, rtiles);
+        }
+        if (!ok) {  // given up: the copies in flight still land before the block ends
+            for (int i = j; i < j + 4; ++i) {
+                mbar_wait_bounded(ckfull + (i & 1), (uint32_t)(i >> 1) & 1u, 1ll << 22);
+                mbar_wait_bounded(cvfull + (i & 1), (uint32_t)(i >> 1) & 1u, 1ll << 22);
+            }
+        }
+    } else if (warp >= 5) {
         // ---------------- decoders
-        const int dw = warp - 4;
+        const int dw = warp - 5;
         // LANES threads per row of codes; the store order keeps each 8 lanes' 16-byte
         // chunks in different banks
         const int cu = C::LANES == 8 ? (lane & 3) + 4 * (lane >> 4) : lane & 3;
         const int rin = C::LANES == 8 ? (lane >> 2) & 3 : lane >> 2;  // row within a pass
-        const int pass0 = dw == 0 ? C::PASSES - 1 : (dw - 1) * C::MANY;
-        auto row_of = [&](int i) { return min(pass0 + i, C::PASSES - 1) * C::RPP + rin; };
-        using Unit = typename std::conditional<C::UB == 16, uint4, uint2>::type;
-        Unit kreg[C::MANY], vreg[C::MANY];
-        float2 sreg;  // 2 per lane: warp 1 of the four stores key scales, warp 2 value scales
-        // Lane i (of each four) holds group i of 16 keys of the tile that is loaded next: its page
-        // is fetched a tile before its use.
-        AttnWalk ahead = at;
-        AttnPages where;
-        int page;
-        uint32_t group;
-        where.start(a, ahead, at.tile * KT + (lane & 3) * 16);
-        page = where.fetch(a, ahead.b);
-        auto fetch = [&]() {
-            if (ahead.template next<TL>(a, rtiles)) where.start(a, ahead, ahead.tile * KT + (lane & 3) * 16);
-            else where.next(a, KT);
-            page = where.fetch(a, ahead.b);
-        };
-        // Addresses of this thread's codes (keys and values alike) and scales.  Loads carry no
-        // condition (their registers would be waited for at once): places beyond the last
-        // key repeat it, which is a finite code that weighs nothing.
-        int64_t at_codes[C::MANY], at_scale;
-        // f(constant number of passes) for this warp
-        auto share = [&](auto f) {
-            if (dw == 0) f(std::integral_constant<int, C::FEW>());
-            else f(std::integral_constant<int, C::MANY>());
-        };
-        auto settle = [&]() {
-            group = attn_group(a, page, ahead.hk, where.off);
-            const int last = ahead.ctx + a.T - ahead.tile * KT - 1;  // place of the last key, from the tile's start
-            share([&](auto n) {
+        // Passes turn, turn + 3 .. of a tile.  A row's 16-byte chunk c lies at c ^ (row & 7): with
+        // four rows to a pass every second pass flips bit 2 of the row (and of the chunk),
+        // with eight all passes agree.
+        const uint32_t smem0 = smem_u32(smem);
+        auto decode = [&](int turn, uint32_t from, uint32_t to) {
+            const int r0 = turn * C::RPP + rin;
+            const uint32_t src = smem0 + from + (uint32_t)(r0 * C::RB + cu * C::UB);
+            const uint32_t dst = smem0 + to + (uint32_t)((cu >> 2) * C::KBLOCK + r0 * 128);
+            const uint32_t ch0 = (uint32_t)((2 * (cu & 3)) ^ (r0 & 7)) << 4;
+            uint32_t w[C::MANY][4];
 #pragma unroll
-                for (int i = 0; i < decltype(n)::value; ++i) {
-                    const int r = min(row_of(i), last);
-                    at_codes[i] = (((int64_t)__shfl_sync(0xffffffffu, group, r >> 4) << 4) + (r & 15)) * C::RB + cu * C::UB;
-                }
-            });
-            const int r = min(lane * 2, last) & ~1;
-            at_scale = ((int64_t)__shfl_sync(0xffffffffu, group, r >> 4) << 4) + (r & 15);
-        };
-        auto load = [&](const uint8_t *codes, Unit(&reg)[C::MANY]) {
-            share([&](auto n) {
+            for (int i = 0; i < C::MANY; ++i)
+                if (turn + 3 * i < C::PASSES) lds<C::UB>(src + i * 3 * C::RPP * C::RB, w[i]);
 #pragma unroll
-                for (int i = 0; i < decltype(n)::value; ++i) {
-                    if constexpr (C::UB == 16) reg[i] = ldg_nc_v4(codes + at_codes[i]);
-                    else reg[i] = ldg_nc_v2(codes + at_codes[i]);
-                }
-            });
-        };
-        auto load_scales = [&]() { sreg = __ldg(reinterpret_cast<const float2 *>((dw == 2 ? a.c.vs : a.c.ks) + at_scale)); };
-        uint8_t *const put = smem + (cu >> 2) * C::KBLOCK;
-        auto store = [&](int stage, const Unit(&reg)[C::MANY]) {
-            share([&](auto n) {
-#pragma unroll
-                for (int i = 0; i < decltype(n)::value; ++i) {
-                    uint32_t w[4], h[8];
-                    if constexpr (C::UB == 16) w[0] = reg[i].x, w[1] = reg[i].y, w[2] = reg[i].z, w[3] = reg[i].w;
-                    else w[0] = reg[i].x, w[1] = reg[i].y;
-                    codes16_f16<FMT>(w, h);
-                    const int r = row_of(i), x = r & 7;
-                    uint8_t *row = put + stage + r * 128;
-                    *reinterpret_cast<uint4 *>(row + (((2 * (cu & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(row + (((2 * (cu & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-            });
+            for (int i = 0; i < C::MANY; ++i) {
+                if (turn + 3 * i >= C::PASSES) break;
+                uint32_t h[8];
+                codes16_f16<FMT>(w[i], h);
+                const uint32_t ch = C::RPP == 4 && (i & 1) ? ch0 ^ 64u : ch0;
+                sts_v4(dst + i * 3 * C::RPP * 128 + ch, h[0], h[1], h[2], h[3]);
+                sts_v4(dst + i * 3 * C::RPP * 128 + (ch ^ 16u), h[4], h[5], h[6], h[7]);
+            }
         };
         // The unit's rows as f16, D / 8 lanes per row; rows beyond the last repeat it or are left
         // as they are (a row only ever meets its own scores and outputs).
         auto queries = [&](const AttnWalk &w, int buf) {
-            constexpr int QL = D / 8, QR = 32 / QL, N = 32 / QR;  // lanes per row, rows per pass, passes
-            const int first = w.rt * ROWS + dw * 32;
-            const int c = lane % QL;
+            constexpr int QL = D / 8, QR = 32 / QL;  // lanes per row, rows per pass
+            const int c = lane % QL, r1 = min(ROWS, R - w.rt * ROWS);
             float *fac = reinterpret_cast<float *>(smem + C::FOFF) + buf * 128;
 #pragma unroll 1
-            for (int n0 = 0; n0 < N && first + n0 * QR < R; n0 += 8) {
+            for (int n0 = dw * 8 * QR; n0 < r1; n0 += 24 * QR) {  // eight passes at a time
                 uint4 raw[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int g = min(first + (n0 + i) * QR + lane / QL, R - 1), tok = g / a.G;
+                    const int g = min(w.rt * ROWS + n0 + i * QR + lane / QL, R - 1), tok = g / a.G;
                     const uint16_t *q = static_cast<const uint16_t *>(a.q) + w.b * a.qb + (int64_t)tok * a.qt +
                                  (int64_t)(w.hk * a.G + g - tok * a.G) * a.qh + c * 8;
                     if (a.q_vec) {
@@ -239,7 +312,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int r = dw * 32 + (n0 + i) * QR + lane / QL;
+                    const int r = n0 + i * QR + lane / QL;
                     uint4 h = raw[i];
                     float up = 1.f;
                     if (a.bf) {
@@ -275,95 +348,36 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             if (lane == 0) mbar_arrive(bar);
         };
 
-        // Products, issued by the first decoder warp: the whole warp walks and one lane
-        // issues, so that descriptors stay in uniform registers.
-        constexpr uint32_t idesc_s = tc::idesc_f16(KT, false);
-        constexpr uint32_t idesc_o = tc::idesc_f16(D, false) | tc::kIdescBTransposed;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        auto scores = [&](int j) -> bool {  // S buffer j & 1 held P of tile j - 2: odone(j - 2) was waited for
-            if (!wait(kfull, j)) return false;
-            tc::fence_after_sync();
-            const uint64_t qd = tc::desc_sw128(smem + C::QOFF);
-            const uint64_t kd = tc::desc_sw128(smem + C::KOFF + (j & 1) * C::KSTAGE);
-            const uint32_t d = tm + C::SCOL + (uint32_t)(j & 1) * KT;
-            if (tc::elect_one()) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_ss(d, qd + (uint64_t)((k >> 2) * (C::QBLOCK >> 4) + (k & 3) * 2),
-                               kd + (uint64_t)((k >> 2) * (C::KBLOCK >> 4) + (k & 3) * 2), idesc_s, k > 0);
-                tc::commit(sdone + (j & 1));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](int j, bool first) -> bool {
-            if (!wait(pfull, j) || !wait(vfull, j)) return false;
-            tc::fence_after_sync();
-            const uint64_t vd = tc::desc_sw128_mn(smem + C::VOFF + (j & 1) * C::KSTAGE, C::KBLOCK);
-            const uint32_t p = tm + C::SCOL + (uint32_t)(j & 1) * KT;
-            if (tc::elect_one()) {
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    tc::mma_ts(tm + C::OCOL, p + k * 8, vd + (uint64_t)(k * 128), idesc_o, !first || k > 0);
-                tc::commit(odone + (j & 1));
-            }
-            __syncwarp();
-            return true;
-        };
-
-        settle();
-        load(a.c.kc, kreg);
-        load(a.c.vc, vreg);
-        load_scales();
-        if (ahead.template more<TL>()) fetch();
         int unit = 0;         // row factors' buffer
-        bool fresh = true, before = true;  // the tile begins a unit (for this block); the one before it did
-        int j = 0;
+        auto keys = [&](int j, bool fresh) -> bool {  // of tile j = `at`
+            if (!wait(ckfull, j) || (j > 0 && !wait(sdone, j - 1))) return false;  // the last tile's keys have been read
+            if (fresh) queries(at, unit++ & 3);                                    // (and the last unit's queries)
+            decode(dw, C::CKOFF + (j & 1) * C::CODES, C::KOFF);
+            if (dw == 1) {  // the largest value scale among keys that every row sees
+                const int k = at.tile * KT + lane * 2;
+                const float2 v = *reinterpret_cast<const float2 *>(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 8);
+                // (negative scales do not count: the others compare as their bits)
+                uint32_t mx = k < at.ctx ? __float_as_uint(fmaxf(v.x, 0.f)) : 0u;
+                if (k + 1 < at.ctx) mx = max(mx, __float_as_uint(fmaxf(v.y, 0.f)));
+                mx = __reduce_max_sync(0xffffffffu, mx);
+                if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::SMOFF)[j & 3] = mx;
+            }
+            publish(kfull);
+            return true;
+        };
+        // the next tile's keys before this one's values: its scores are computed first
+        bool more = true, ok = keys(0, true);
 #pragma unroll 1
-        for (; at.inside(); ++j) {
-            const bool more = at.template more<TL>();
-            if (j > 1 && !wait(sdone, j - 2)) break;  // S of tile j - 2 is computed: its keys' stage is free
-            if (fresh) {
-                if (j > 0 && !wait(sdone, j - 1)) break;  // and the last unit's queries are
-                queries(at, unit & 3);
-            }
-            store(C::KOFF + (j & 1) * C::KSTAGE, kreg);
-            if (dw == 1 || dw == 2) {
-                const int keys = at.ctx + a.T - at.tile * KT;
-                if (lane * 2 >= keys) sreg.x = 0.f;
-                if (lane * 2 + 1 >= keys) sreg.y = 0.f;
-                reinterpret_cast<float2 *>(smem + (dw == 2 ? C::SVOFF : C::SKOFF) + (j & 3) * KT * 4)[lane] = sreg;
-                if (dw == 2) {  // the largest value scale among keys that every row sees
-                    const int k = at.tile * KT + lane * 2;
-                    float mx = 0.f;
-                    if (k < at.ctx) mx = sreg.x;
-                    if (k + 1 < at.ctx) mx = fmaxf(mx, sreg.y);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    if (lane == 0) reinterpret_cast<float *>(smem + C::SMOFF)[j & 3] = mx;
-                }
-            }
-            publish(kfull + (j & 1));
+        for (int j = 0; ok && more; ++j) {
+            more = at.template more<TL>();
             if (more) {
-                settle();
-                load(a.c.kc, kreg);
-                load_scales();
+                const bool fresh = at.template next<TL>(a, rtiles);
+                if (!keys(j + 1, fresh)) break;
             }
-            if (j > 1 && !wait(odone, j - 2)) break;  // the product of tile j - 2 is done: its values' stage is free
-            store(C::VOFF + (j & 1) * C::KSTAGE, vreg);
-            publish(vfull + (j & 1));
-            if (more) {
-                load(a.c.vc, vreg);
-                if (ahead.template more<TL>()) fetch();
-            }
-            // this tile's scores, then -- its softmax done meanwhile -- the last one's product
-            if (dw == 0 && (!scores(j) || (j > 0 && !values(j - 1, before)))) break;
-            before = fresh;
-            fresh = at.last_of_unit();
-            if (fresh) ++unit;
-            at.template next<TL>(a, rtiles);
+            if (!wait(cvfull, j) || (j > 0 && !wait(odone, j - 1))) break;  // the last tile's values have been read
+            decode(2 - dw, C::CVOFF + (j & 1) * C::CODES, C::VOFF);
+            publish(vfull);
         }
-        if (dw == 0 && !at.inside()) values(j - 1, before);
     } else {
         // ---------------- softmax: thread = row = TMEM lane
         const int row = threadIdx.x;
