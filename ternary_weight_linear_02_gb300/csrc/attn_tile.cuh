@@ -169,22 +169,27 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         int page = where.fetch(a, ahead.b);
         uint32_t group = 0, group1 = 0;  // of the tile whose keys were copied last, and of the one before
         int groups = 0, groups1 = 0;     // (none: 0)
+        bool one = false, one1 = false;  // whole, within one page: one copy (each takes the warp about 70 cycles)
         constexpr uint32_t codes = 16 * C::RB;
         auto copy_keys = [&](int j) {  // and both sides' scales
             group1 = group;
             groups1 = groups;
+            one1 = one;
             groups = 0;
+            one = false;
             if (!ahead.inside()) return;
             groups = min(KT / 16, (ahead.ctx + a.T - ahead.tile * KT + 15) >> 4);
             group = attn_group(a, page, ahead.hk, where.off);
+            one = groups == KT / 16 && __shfl_sync(0xffffffffu, where.off, 0) + KT <= a.c.P;
             uint64_t *bar = ckfull + (j & 1);
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)groups * (codes + 128));
             __syncwarp();
-            if (lane < groups) {
+            if (lane < (one ? 1 : groups)) {
                 const int64_t row = (int64_t)group << 4;
-                bulk_g2s(smem + C::CKOFF + (j & 1) * C::CODES + lane * codes, a.c.kc + row * C::RB, codes, bar);
-                bulk_g2s(smem + C::SKOFF + (j & 3) * KT * 4 + lane * 64, a.c.ks + row, 64, bar);
-                bulk_g2s(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 64, a.c.vs + row, 64, bar);
+                const uint32_t n = one ? KT / 16 : 1;
+                bulk_g2s(smem + C::CKOFF + (j & 1) * C::CODES + lane * codes, a.c.kc + row * C::RB, n * codes, bar);
+                bulk_g2s(smem + C::SKOFF + (j & 3) * KT * 4 + lane * 64, a.c.ks + row, n * 64, bar);
+                bulk_g2s(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 64, a.c.vs + row, n * 64, bar);
             }
             __syncwarp();
             const bool start = ahead.template next<TL>(a, rtiles);
@@ -193,13 +198,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             else where.next(a, KT);
             page = where.fetch(a, ahead.b);
         };
-        auto copy_values = [&](int j, uint32_t grp, int n) {
+        auto copy_values = [&](int j, uint32_t grp, int n, bool single) {
             if (n == 0) return;
             uint64_t *bar = cvfull + (j & 1);
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * codes);
             __syncwarp();
-            if (lane < n)
-                bulk_g2s(smem + C::CVOFF + (j & 1) * C::CODES + lane * codes, a.c.vc + ((int64_t)grp << 4) * C::RB, codes, bar);
+            if (lane < (single ? 1 : n))
+                bulk_g2s(smem + C::CVOFF + (j & 1) * C::CODES + lane * codes, a.c.vc + ((int64_t)grp << 4) * C::RB,
+                         single ? (uint32_t)C::CODES : codes, bar);
             __syncwarp();
         };
         auto scores = [&](int j) -> bool {
@@ -233,22 +239,22 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             return true;
         };
         copy_keys(0);
-        copy_values(0, group, groups);
+        copy_values(0, group, groups, one);
         copy_keys(1);
-        copy_values(1, group, groups);
+        copy_values(1, group, groups, one);
         bool fresh = true;  // the tile begins a unit (for this block)
         bool ok = scores(0);
         if (ok) copy_keys(2);
         int j = 0;
 #pragma unroll 1
         for (; ok && at.inside(); ++j) {
-            // The next tile's scores, computed during this one's softmax.  Its keys' stage and the
-            // scales of the tile before this are then free (kfull; odone in scores), and after
-            // this tile's product its values' stage is (vfull).
+            // The next tile's scores, computed during this one's softmax.  Free since then: the
+            // stage of the last tile's values (vfull, in values), of the next tile's keys
+            // (kfull, in scores), and the scales of the last tile (odone, in scores).
             if (at.template more<TL>()) ok = scores(j + 1);
+            if (ok && j > 0) copy_values(j + 1, group1, groups1, one1);
             if (ok) copy_keys(j + 3);
             ok = ok && values(j, fresh);
-            if (ok) copy_values(j + 2, group1, groups1);
             fresh = at.last_of_unit();
             at.template next<TL>(a, rtiles);
         }
@@ -410,7 +416,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 float svmax = reinterpret_cast<const float *>(smem + C::SMOFF)[j & 3];
                 tc::wait_ld();
                 // ---- scores: products with the key scales; the row's largest
-                float top = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < KT; k += 4) {
                     const float4 w = sk[k / 4];
@@ -448,10 +453,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                             if (!(see[c] >> k & 1u)) s[c][k] = 0xFF800000u;  // -infinity
                     }
                 }
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four short chains
 #pragma unroll
-                for (int k = 0; k < KT; k += 2)
-                    top = fmaxf(fmaxf(top, __uint_as_float(s[k >> 5][k & 31])), __uint_as_float(s[k >> 5][(k & 31) + 1]));
-                top *= f;
+                for (int k = 0; k < KT; k += 2) {
+                    float &x = tops[(k >> 1) & 3];
+                    x = fmaxf(fmaxf(x, __uint_as_float(s[k >> 5][k & 31])), __uint_as_float(s[k >> 5][(k & 31) + 1]));
+                }
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f;
                 const bool bigger = svmax > __uint_as_float((uint32_t)(ve + 127) << 23);
                 if (__any_sync(0xffffffffu, top > m + kAttnSlack || bigger)) {
                     const float mn = top > m + kAttnSlack ? top + kAttnMargin : m;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 // ---- weights, over S's first columns
                 const float off = kAttnUp - m - (float)ve;
                 const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-                float2 l2 = make_float2(0.f, 0.f);
+                float2 l2 = make_float2(0.f, 0.f), l3 = l2;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t p[16];
@@ -489,7 +497,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         float2 y = fma2(make_float2(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), f2, off2);
                         x = make_float2(ex2(x.x), ex2(x.y));
                         y = make_float2(ex2(y.x), ex2(y.y));
-                        l2 = add2(l2, add2(x, y));
+                        l2 = add2(l2, x);
+                        l3 = add2(l3, y);
                         x = mul2(x, make_float2(v.x, v.y));
                         y = mul2(y, make_float2(v.z, v.w));
                         p[k / 2] = pack2(__half(), x.x, x.y);
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                     tc::st_32x32b_x16(scol + c * 16, p);
                 }
-                l += l2.x + l2.y;
+                l += (l2.x + l2.y) + (l3.x + l3.y);
                 tc::wait_st();
             }
             tc::fence_before_sync();
