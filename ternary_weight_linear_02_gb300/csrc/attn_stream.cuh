@@ -79,14 +79,6 @@ __device__ __forceinline__ uint32_t e4m3x2_raw(uint32_t w) {
     return r;
 }
 
-// fields of 4 bits at bits 0-3 / 4-7 of each half, as f16x2 of field - 8
-__device__ __forceinline__ uint32_t int4_lo(uint32_t x) {
-    return h2_bits(__hsub2(h2_of((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(1032.f)));
-}
-__device__ __forceinline__ uint32_t int4_hi(uint32_t x) {  // 1024 + 16 u
-    return h2_bits(__hfma2(h2_of((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
-}
-
 template <int FMT, int D, int NB>
 struct StreamCfg {
     static constexpr int ROWS = 8 * NB;

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             for (int i = 0; i < C::MANY; ++i) {
                 if (turn + 3 * i >= C::PASSES) break;
                 uint32_t h[8];
-                codes16_f16<FMT>(w[i], h);
+                codes16_mma<FMT>(w[i], h);
                 const uint32_t ch = C::RPP == 4 && (i & 1) ? ch0 ^ 64u : ch0;
                 sts_v4(dst + i * 3 * C::RPP * 128 + ch, h[0], h[1], h[2], h[3]);
                 sts_v4(dst + i * 3 * C::RPP * 128 + (ch ^ 16u), h[4], h[5], h[6], h[7]);
@@ -327,8 +327,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         uint32_t mx = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mx = max(mx, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
-#pragma unroll
-                        for (int o = QL / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        mx = __reduce_max_sync(((1u << QL) - 1u) << (lane & ~(QL - 1)), mx);  // the row's lanes
                         const uint32_t e = mx >> 7;  // biased exponent of the largest
                         float down = 1.f;
                         if (e > 0 && e < 254) {
@@ -343,6 +342,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         }
                         h = make_uint4(y[0], y[1], y[2], y[3]);
                     }
+                    h = mma_order<FMT>(h);
                     *reinterpret_cast<uint4 *>(smem + C::QOFF + (c >> 3) * C::QBLOCK + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = h;
                     if (c == 0) fac[r] = a.scale * kLog2e * up;
                 }
@@ -532,9 +532,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
 #pragma unroll
                     for (int h = 0; h < D / 32; ++h) {
-                        uint32_t o[32];
-                        tc::ld_32x32b_x32(lane_base + C::OCOL + h * 32, o);
+                        uint32_t x[32], o[32];
+                        tc::ld_32x32b_x32(lane_base + C::OCOL + h * 32, x);
                         tc::wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[mma_element<FMT>(k)] = x[k];  // (registers renamed)
                         if (grow < R) {
                             if (whole) {
                                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_row * D + h * 32);

@@ -69,6 +69,44 @@ __device__ __forceinline__ void codes16_f16(const uint32_t *w, uint32_t (&r)[8])
     }
 }
 
+// Fields of 4 bits at bits 0-3 / 4-7 of each half, as f16x2 of field - 8.
+__device__ __forceinline__ uint32_t int4_lo(uint32_t x) {
+    return h2_bits(__hsub2(h2_of((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(1032.f)));
+}
+__device__ __forceinline__ uint32_t int4_hi(uint32_t x) {  // 1024 + 16 u
+    return h2_bits(__hfma2(h2_of((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
+}
+
+// The order in which codes16_mma gives the elements of each 8: the registers' pairs are
+// (0,1) (2,3) (4,5) (6,7), or for INT4 (0,4) (1,5) (2,6) (3,7), which takes 9 instructions per
+// word instead of 20.  element(i): the element at place i.
+template <int FMT>
+__host__ __device__ constexpr int mma_element(int i) {
+    return FMT == kKvInt4 ? (i & ~7) + ((i & 7) >> 1) + (i & 1) * 4 : i;
+}
+template <int FMT>
+__device__ __forceinline__ void codes16_mma(const uint32_t *w, uint32_t (&r)[8]) {
+    if constexpr (FMT == kKvInt4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            r[4 * i] = int4_lo(w[i]);
+            r[4 * i + 1] = int4_hi(w[i]);
+            r[4 * i + 2] = int4_lo(w[i] >> 8);
+            r[4 * i + 3] = int4_hi(w[i] >> 8);
+        }
+    } else {
+        codes16_f16<FMT>(w, r);
+    }
+}
+// 8 16-bit values (4 words) in that order
+template <int FMT>
+__device__ __forceinline__ uint4 mma_order(uint4 h) {
+    if constexpr (FMT == kKvInt4)
+        return make_uint4(__byte_perm(h.x, h.z, 0x5410), __byte_perm(h.x, h.z, 0x7632), __byte_perm(h.y, h.w, 0x5410),
+                          __byte_perm(h.y, h.w, 0x7632));
+    return h;
+}
+
 // The same 16 codes as fp32.
 template <int FMT>
 __device__ __forceinline__ void codes16_f32(const uint32_t *w, float (&v)[16]) {
