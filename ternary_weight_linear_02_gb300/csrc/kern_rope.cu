@@ -125,9 +125,14 @@ cudaError_t launch_rope_t(const RopeArgs &a, bool vec, int sm_count, cudaStream_
         b.x = static_cast<const T *>(a.x) + t0 * a.xt;
         b.out = static_cast<T *>(a.out) + t0 * a.ot;
         b.positions = a.positions + t0;
-        const uint32_t hgroups = (uint32_t)a.heads;
+        // two heads per thread once one per thread would fill the GPU many times over
+        const bool two = b.tokens * cols * a.heads >= (int64_t)sm_count * 2048 * 4;
+        const uint32_t hgroups = (uint32_t)(two ? (a.heads + 1) / 2 : a.heads);
         const uint32_t total = (uint32_t)(b.tokens * cols * hgroups);
-        rope_kernel<T, INTER, 1><<<(total + 255) / 256, 256, 0, st>>>(b, (uint32_t)cols, hgroups, total);
+        if (two)
+            rope_kernel<T, INTER, 2><<<(total + 255) / 256, 256, 0, st>>>(b, (uint32_t)cols, hgroups, total);
+        else
+            rope_kernel<T, INTER, 1><<<(total + 255) / 256, 256, 0, st>>>(b, (uint32_t)cols, hgroups, total);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
