@@ -110,63 +110,51 @@ __device__ __forceinline__ void put_row(const RopeCols<INTER> &rc, const float (
     if (first) scales[row] = s;
 }
 
-// One thread per column group of 16 elements (RopeCols) of two rows of a token, their loads in
-// flight together: two query heads, or one kv head's key and value.
+// One thread per column group of 16 elements (RopeCols) of a query head, or of a kv head's key and
+// value together (their loads in flight at once).  Rows are requested before their position
+// is looked at.
 template <typename T, int FMT, int D, bool INTER, bool VEC>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(KvAppendArgs a, uint32_t qpairs, uint32_t items,
-                                                        uint32_t total) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(KvAppendArgs a, uint32_t items, uint32_t total) {
     constexpr uint32_t C = D / 16;
     const uint32_t id0 = blockIdx.x * 256u + threadIdx.x;
-    const bool inside = id0 < total;
-    const uint32_t id = inside ? id0 : total - 1;
+    const uint32_t id = min(id0, total - 1);
     const uint32_t c = id % C, r = id / C;
     const int64_t t = r / items;
-    const int item = (int)(r % items);
-    const bool kv = item >= (int)qpairs;
-    const int h = kv ? item - (int)qpairs : item, h2 = item + (int)qpairs;
-
-    bool ok = inside;
-    int64_t pos = 0, slot = -1;
-    if (a.R > 0) {
-        pos = a.positions[t];
-        if (pos < 0 || pos >= a.table_rows) {
-            ok = false;
-            flag_value(a.status);
-        }
-    }
-    if (kv) slot = a.slots[t];
-    const bool second = kv || h2 < a.Hq;
-    const RopeCols<INTER> rc(c, a.R), rv(c, kv ? 0 : a.R);  // of the first row, of the second
+    const int item = (int)(r - (uint32_t)t * items);
+    const bool kv = item >= a.Hq;
+    const int h = kv ? item - a.Hq : item;
+    const int64_t pos = a.R > 0 ? a.positions[t] : 0;
+    const int64_t slot = kv ? a.slots[t] : -1;
+    const RopeCols<INTER> rc(c, a.R), rv(c, 0);
+    const T *x = kv ? static_cast<const T *>(a.k) + t * a.kt + h * a.kh : static_cast<const T *>(a.q) + t * a.qt + h * a.qh;
     float lo[8], hi[8], lo2[8], hi2[8];
+    ld8_any<T, VEC>(x + rc.a, lo);
+    ld8_any<T, VEC>(x + rc.b, hi);
+    if (kv) {
+        const T *y = static_cast<const T *>(a.v) + t * a.vt + h * a.vh;
+        ld8_any<T, VEC>(y + rv.a, lo2);
+        ld8_any<T, VEC>(y + rv.b, hi2);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = hi[i] = lo2[i] = hi2[i] = 0.f;
-    if (ok) {
-        const T *x = kv ? static_cast<const T *>(a.k) + t * a.kt + h * a.kh : static_cast<const T *>(a.q) + t * a.qt + h * a.qh;
-        const T *y = kv ? static_cast<const T *>(a.v) + t * a.vt + h * a.vh : static_cast<const T *>(a.q) + t * a.qt + h2 * a.qh;
-        ld8_any<T, VEC>(x + rc.a, lo);
-        ld8_any<T, VEC>(x + rc.b, hi);
-        if (second) {
-            ld8_any<T, VEC>(y + rv.a, lo2);
-            ld8_any<T, VEC>(y + rv.b, hi2);
-        }
-        if (rc.rotated) {
-            float cs[8], sn[8];
-            rope_row<INTER>(a.table + pos * a.R, rc, a.R, 0, cs, sn);
-            rope_turn<INTER>(lo, hi, cs, sn);
-            if (!kv) rope_turn<INTER>(lo2, hi2, cs, sn);
-        }
-        if (!kv) {
-            T *o = static_cast<T *>(a.qo) + t * a.qot;
-            st8_any<T, VEC>(o + h * a.qoh + rc.a, lo);
-            st8_any<T, VEC>(o + h * a.qoh + rc.b, hi);
-            if (second) {
-                st8_any<T, VEC>(o + h2 * a.qoh + rc.a, lo2);
-                st8_any<T, VEC>(o + h2 * a.qoh + rc.b, hi2);
-            }
-        }
+        for (int i = 0; i < 8; ++i) lo2[i] = hi2[i] = 0.f;
+    }
+    bool ok = id0 < total;
+    if (a.R > 0 && (pos < 0 || pos >= a.table_rows)) {
+        ok = false;
+        flag_value(a.status);
+    }
+    if (ok && rc.rotated) {
+        float cs[8], sn[8];
+        rope_row<INTER>(a.table + pos * a.R, rc, a.R, 0, cs, sn);
+        rope_turn<INTER>(lo, hi, cs, sn);
+    }
+    if (!kv && ok) {
+        T *o = static_cast<T *>(a.qo) + t * a.qot + h * a.qoh;
+        st8_any<T, VEC>(o + rc.a, lo);
+        st8_any<T, VEC>(o + rc.b, hi);
     }
     if (!__any_sync(0xffffffffu, kv)) return;
-    bool store = ok && kv && slot >= 0;
+    bool store = ok && slot >= 0;
     if (store && slot >= a.c.pages * a.c.P) {
         flag_value(a.status);
         store = false;
@@ -182,7 +170,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvAppendArgs a, uint3
 
 template <typename T, int FMT, int D>
 cudaError_t append_d(const KvAppendArgs &a, bool inter, bool vec, cudaStream_t st) {
-    const uint32_t qpairs = (uint32_t)(a.Hq + 1) / 2, items = qpairs + (uint32_t)a.c.Hk;
+    const uint32_t items = (uint32_t)(a.Hq + a.c.Hk);
     // tokens per launch such that every thread index fits 31 bits
     const int64_t chunk = ((int64_t)1 << 30) / ((int64_t)items * (D / 16));
     for (int64_t t0 = 0; t0 < a.tokens; t0 += chunk) {
@@ -199,11 +187,11 @@ cudaError_t append_d(const KvAppendArgs &a, bool inter, bool vec, cudaStream_t s
         const uint32_t total = (uint32_t)(b.tokens * items * (D / 16));
         const unsigned grid = (total + 255) / 256;
         if (inter) {
-            if (vec) kv_append_kernel<T, FMT, D, true, true><<<grid, 256, 0, st>>>(b, qpairs, items, total);
-            else kv_append_kernel<T, FMT, D, true, false><<<grid, 256, 0, st>>>(b, qpairs, items, total);
+            if (vec) kv_append_kernel<T, FMT, D, true, true><<<grid, 256, 0, st>>>(b, items, total);
+            else kv_append_kernel<T, FMT, D, true, false><<<grid, 256, 0, st>>>(b, items, total);
         } else {
-            if (vec) kv_append_kernel<T, FMT, D, false, true><<<grid, 256, 0, st>>>(b, qpairs, items, total);
-            else kv_append_kernel<T, FMT, D, false, false><<<grid, 256, 0, st>>>(b, qpairs, items, total);
+            if (vec) kv_append_kernel<T, FMT, D, false, true><<<grid, 256, 0, st>>>(b, items, total);
+            else kv_append_kernel<T, FMT, D, false, false><<<grid, 256, 0, st>>>(b, items, total);
         }
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
