@@ -285,8 +285,9 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bflo
     n = slots.shape[0] if slots.dim() == 1 else -1
     slots = _index(slots, "slots", torch.int64, n)
     dev = slots.device
-    both = torch.empty((2, n, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
-    k, v = both[0], both[1]
+    shape = (n, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=dev)
+    v = torch.empty(shape, dtype=dtype, device=dev)
     rc = (_ready or _lib()).ternary_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
                                             _stream(dev))
     if rc:

@@ -157,6 +157,15 @@ def test_large_scores_and_unequal_rows(t):
     c.check(c.q(14, torch.bfloat16, 3000.0), scale=1e-3, what="scaled")
 
 
+@pytest.mark.parametrize("t,share,batch", [(1, 1, 129), (1, 3, 300), (20, 1, 257), (3, 3, 128)])
+def test_large_ragged_batches(t, share, batch):
+    """More sequences than one chunk of the length scan holds, many of them without a context."""
+    g = torch.Generator().manual_seed(batch)
+    lens = (torch.rand(batch, generator=g) ** 4 * 300).int().tolist()
+    c = Case("int8", lens, t, 1, 64, 16, seed=batch)
+    c.check(c.q(share, torch.float16), what="batch")
+
+
 @pytest.mark.parametrize("t,share", [(1, 4), (10, 4)])
 def test_values_far_apart_in_size(t, share):
     """Value scales that grow by 2^40 along the context, and ones that fall; rows of zeros."""
