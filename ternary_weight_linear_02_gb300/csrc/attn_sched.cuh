@@ -286,16 +286,16 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v
 }
 
 // Where a unit's partial results lie: blocks c0 .. c1 (c0 == c1: none, its one block wrote
-// the output), the first of them in slot `first`.  Executed by a whole block of 128
-// threads; sh: 8 64-bit words.
+// the output), the first of them in slot `first`.  Executed by a whole block of NW warps;
+// sh: 2 NW 64-bit words.
 struct AttnParts {
     int c0, c1, first;
 };
-template <typename TL>
+template <typename TL, int NW>
 __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int unit, int units, int nc, int64_t *sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t pre = 0, all = 0;  // tiles before sequence b, and of the call
-    for (int i = threadIdx.x; i < a.B; i += 128) {
+    for (int i = threadIdx.x; i < a.B; i += NW * 32) {
         const int64_t n = attn_tiles<TL>(a, i, units);
         all += n;
         if (i < b) pre += n;
@@ -305,11 +305,16 @@ __device__ __forceinline__ AttnParts attn_parts(const AttnArgs &a, int b, int un
         pre += __shfl_xor_sync(0xffffffffu, pre, o);
         all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    if (lane == 0) sh[warp] = pre, sh[4 + warp] = all;
+    if (lane == 0) sh[warp] = pre, sh[NW + warp] = all;
     __syncthreads();
     AttnParts r;
-    pre = sh[0] + sh[1] + sh[2] + sh[3];
-    const int64_t N = sh[4] + sh[5] + sh[6] + sh[7];
+    int64_t N = 0;
+    pre = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        pre += sh[w];
+        N += sh[NW + w];
+    }
     if (N < nc) nc = (int)N;
     const int64_t tiles = attn_tiles<TL>(a, b, 1), s = pre + unit * tiles;
     r.c0 = attn_block_of(s + TL::OV, N, nc);
@@ -362,73 +367,68 @@ struct AttnSum {
 // Joins the partial results of each unit that more than one block worked on, in block
 // order; the grid covers every unit, and blocks of units with nothing to join leave.
 // Launched as a dependent of the main kernel: the place is computed meanwhile.
-// WIDE (few rows, many parts: single tokens over long contexts): one block per row,
-// its four warps sharing the parts.  Otherwise 16 rows per block, each warp taking
-// whole rows.
+// WIDE: one block per row, its eight warps sharing the parts (four each in flight at a
+// time): few rows, or few units, which then have many parts.  Otherwise 16 rows per
+// block, one warp each: many units have few parts.
 template <typename TL, int ROWS, int D, bool WIDE>
-__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
-    __shared__ int64_t sh[8];
-    __shared__ float sm[4], sl[4], so[4][D];
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(WIDE ? 256 : 512) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
+    constexpr int NW = WIDE ? 8 : 16, E = D / 32;
+    __shared__ int64_t sh[2 * NW];
+    __shared__ float sm[8], sl[8], so[WIDE ? 8 : 1][D];
     using Slot = AttnSlot<ROWS, D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = a.T * a.G, units = a.c.Hk * rtiles;
     const int64_t u = blockIdx.x / per_unit;
     const int slice = blockIdx.x % per_unit;
     const int b = (int)(u / units), unit = (int)(u % units), hk = unit / rtiles, rt = unit % rtiles;
-    const AttnParts p = attn_parts<TL>(a, b, unit, units, nc, sh);
+    const AttnParts p = attn_parts<TL, NW>(a, b, unit, units, nc, sh);
     pdl_wait();
-    if (p.c0 == p.c1) return;
-    // the output row of row `grow` of the unit's (sequence, kv head)
-    auto out_row = [&](int grow) { return ((int64_t)b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G; };
+    const int row = WIDE ? slice : slice * 16 + warp, grow = rt * ROWS + row;  // row of the unit, of its kv head
+    if (p.c0 == p.c1 || (WIDE && grow >= R)) return;
+    const int64_t o = ((int64_t)b * a.T + grow / a.G) * a.Hq + hk * a.G + grow % a.G;  // output row
     auto part = [&](int c) -> const float * { return c > p.c1 ? nullptr : Slot::at(a.ws, c, c == p.c0 ? p.first : 0); };
+    AttnSum<E> s;
     if constexpr (WIDE) {
-        const int row = slice;
-        AttnSum<E> s;
-        for (int c = p.c0 + warp; c <= p.c1; c += 16) {
-            const float *const x[4] = {part(c), part(c + 4), part(c + 8), part(c + 12)};
+        for (int c = p.c0 + warp; c <= p.c1; c += 4 * NW) {
+            const float *const x[4] = {part(c), part(c + NW), part(c + 2 * NW), part(c + 3 * NW)};
             s.template add4<ROWS, D>(x, row, lane);
         }
         if (lane == 0) sm[warp] = s.m, sl[warp] = s.l;
 #pragma unroll
         for (int e = 0; e < E; ++e) so[warp][lane * E + e] = s.o[e];
         __syncthreads();
-        const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-        float L = 0.f, x = 0.f;
+        float M = sm[0], L = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w]);
         const int d = threadIdx.x;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float g = ex2(sm[w] - M);
             L += sl[w] * g;
             if (d < D) x += so[w][d] * g;
         }
-        const int64_t o = out_row(row);
         if (d < D) attn_store(a, o * D + d, L == 0.f ? 0.f : x / L);
         if (a.lse && d == 0) a.lse[o] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     } else {
-        for (int row = slice * 16 + warp; row < slice * 16 + 16; row += 4) {
-            const int grow = rt * ROWS + row;
-            if (grow >= R) return;
-            AttnSum<E> s;
-            for (int c = p.c0; c <= p.c1; c += 4) {
-                const float *const x[4] = {part(c), part(c + 1), part(c + 2), part(c + 3)};
-                s.template add4<ROWS, D>(x, row, lane);
-            }
-            const int64_t o = out_row(grow);
-            const float r = s.l == 0.f ? 0.f : 1.f / s.l;
-#pragma unroll
-            for (int e = 0; e < E; ++e) attn_store(a, o * D + lane * E + e, s.o[e] * r);
-            if (a.lse && lane == 0) a.lse[o] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
+        if (grow >= R || row >= ROWS) return;
+        for (int c = p.c0; c <= p.c1; c += 4) {
+            const float *const x[4] = {part(c), part(c + 1), part(c + 2), part(c + 3)};
+            s.template add4<ROWS, D>(x, row, lane);
         }
+        const float r = s.l == 0.f ? 0.f : 1.f / s.l;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + o * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = attn_pack(a, s.o[e] * r, s.o[e + 1] * r);
+        if (a.lse && lane == 0) a.lse[o] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
     }
 }
 
 template <typename TL, int ROWS, int D, bool WIDE>
-cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
-    const int R = a.T * a.G, per_unit = WIDE ? R : ((R < ROWS ? R : ROWS) + 15) / 16;
+cudaError_t launch_join_w(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
+    const int R = a.T * a.G, rows = R < ROWS ? R : ROWS, per_unit = WIDE ? rows : (rows + 15) / 16;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.c.Hk * rtiles * per_unit), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.blockDim = dim3(WIDE ? 256 : 512, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -436,6 +436,13 @@ cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) 
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<TL, ROWS, D, WIDE>, a, rtiles, per_unit, nc);
+}
+
+template <typename TL, int ROWS, int D>
+cudaError_t launch_join(const AttnArgs &a, int rtiles, int nc, cudaStream_t st) {
+    // one block per row while all of them run at once (eight blocks of 256 threads per SM)
+    const int64_t rows = (int64_t)a.B * a.c.Hk * a.T * a.G;
+    return rows <= 1216 ? launch_join_w<TL, ROWS, D, true>(a, rtiles, nc, st) : launch_join_w<TL, ROWS, D, false>(a, rtiles, nc, st);
 }
 
 }  // namespace tl

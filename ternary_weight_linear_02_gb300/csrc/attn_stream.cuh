@@ -602,7 +602,7 @@ cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<StreamTiling<C::GR>, C::ROWS, D, true>(a, 1, nc, st);
+    return launch_join<StreamTiling<C::GR>, C::ROWS, D>(a, 1, nc, st);
 }
 
 template <int FMT, int D>

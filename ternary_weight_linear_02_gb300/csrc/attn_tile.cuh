@@ -598,7 +598,7 @@ cudaError_t launch_tile_d(const AttnArgs &a, int sms, cudaStream_t st) {
     attn_tile_kernel<FMT, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<TileTiling, kTileRows, D, false>(a, rtiles, nc, st);
+    return launch_join<TileTiling, kTileRows, D>(a, rtiles, nc, st);
 }
 
 template <int FMT>
