@@ -363,13 +363,15 @@ tl_status ternary_kv_read(const tl_kv_cache *cache, const int64_t *slots, int64_
  *   A length outside [0, max_pages * page_size - draft] is clamped, an unknown page is
  *     read as page 0; both set the device status word to TL_ERR_VALUE.
  *   workspace: device, 16-byte aligned, at least
- *     ternary_tree_attention_workspace(...) bytes; free for other use once the call's
+ *     ternary_tree_attention_workspace(...) bytes (0 where short contexts need none: it
+ *     may then be NULL); free for other use once the call's
  *     work has run.
  * Scores, softmax sums and the joined outputs are fp32.  Every run of the same call
  * gives the same bits.
  */
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
-                                         int32_t kv_heads, int32_t head_dim); /* -1: invalid */
+                                         int32_t kv_heads, int32_t head_dim,
+                                         int64_t max_keys); /* max_pages * page_size; -1: invalid */
 tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
                                  int64_t q_head_stride, int32_t dtype, int64_t batch,
                                  int64_t draft, int32_t q_heads, const tl_kv_cache *cache,

@@ -146,7 +146,7 @@ def _declare(lib):
     lib.ternary_kv_append.argtypes = [pc, p, i64, i64, p, i64, i64, i32, i64, p, p, i64, i64, p, i64, i64,
                                       i32, p, p, i64, i32, u32, p]
     lib.ternary_kv_read.argtypes = [pc, p, i64, p, p, i32, p]
-    lib.ternary_tree_attention_workspace.argtypes = [i64, i64, i32, i32, i32]
+    lib.ternary_tree_attention_workspace.argtypes = [i64, i64, i32, i32, i32, i64]
     lib.ternary_tree_attention.argtypes = [p, i64, i64, i64, i32, i64, i64, i32, pc, p, i64, i64, p, p, i64,
                                            i64, ctypes.c_float, p, p, p, i64, p]
     for f in (lib.ternary_rope_table, lib.ternary_rope, lib.ternary_kv_append, lib.ternary_kv_read,
@@ -348,7 +348,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
         raise ValueError("out must be contiguous with q's shape, dtype and device")
     lse = torch.empty((b, t, heads), dtype=torch.float32, device=dev) if return_lse else None
     lib = _ready or _lib()
-    key = (b, t, heads, cache.kv_heads, dim)
+    key = (b, t, heads, cache.kv_heads, dim, pshape[1] * cache.page_size)
     need = _ws_bytes.get(key)
     if need is None:
         need = _ws_bytes[key] = int(lib.ternary_tree_attention_workspace(*key))

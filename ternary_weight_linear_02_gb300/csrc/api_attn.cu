@@ -207,10 +207,10 @@ static bool attention_sizes(int64_t batch, int64_t draft, int32_t q_heads, int32
 }
 
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
-                                         int32_t kv_heads, int32_t head_dim) {
-    if (!attention_sizes(batch, draft, q_heads, kv_heads, head_dim)) return -1;
+                                         int32_t kv_heads, int32_t head_dim, int64_t max_keys) {
+    if (!attention_sizes(batch, draft, q_heads, kv_heads, head_dim) || max_keys < 0 || max_keys >= kMaxTokens) return -1;
     if (batch == 0 || draft == 0) return 0;
-    return tl::tree_attention_workspace(batch, draft, q_heads, kv_heads, head_dim);
+    return tl::tree_attention_workspace(batch, draft, q_heads, kv_heads, head_dim, max_keys);
 }
 
 tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
@@ -237,7 +237,7 @@ tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t 
     if (!aligned(q, 2) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(context_len, 4) ||
         !aligned(lse, 4))
         return TL_ERR_ALIGN;
-    const int64_t need = tl::tree_attention_workspace(batch, draft, q_heads, a.c.Hk, a.c.D);
+    const int64_t need = tl::tree_attention_workspace(batch, draft, q_heads, a.c.Hk, a.c.D, max_pages * a.c.P);
     if (need > 0 && !workspace) return TL_ERR_NULL;
     if (!aligned(workspace, 16)) return TL_ERR_ALIGN;
     if (workspace_bytes < need) return TL_ERR_SHAPE;

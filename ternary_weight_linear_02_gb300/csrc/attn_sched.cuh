@@ -14,6 +14,9 @@
 // block given a run of short units would be the last to end by far.  Nothing is done in
 // them, and a block whose run ends within them does not touch the unit.
 //
+// Where contexts can only be short (by the page table's width), or units are many, a block
+// takes one whole unit instead (AttnArgs::direct): nothing to find, nothing to join.
+//
 // A block that runs through a whole unit writes its output.  Otherwise it leaves a
 // partial result (unnormalised rows, running maximum, running sum): in its slot 0
 // if the unit is the first of its run, else in slot 1 (it is then the last).
@@ -220,6 +223,33 @@ struct AttnWalk {
         end = (int)(x1 - x0);
         hk = rtiles == 1 ? unit : unit / rtiles;
         rt = unit - hk * rtiles;
+    }
+    // one whole unit, the `index`-th of the call
+    template <typename TL>
+    __device__ __forceinline__ void start_unit(const AttnArgs &a, int index, int rtiles) {
+        const int units = a.c.Hk * rtiles, unit = index % units;
+        b = index / units;
+        hk = rtiles == 1 ? unit : unit / rtiles;
+        rt = unit - hk * rtiles;
+        ctx = attn_context(a, b);
+        tile = at = 0;
+        tiles = end = TL::tiles(a, ctx);
+    }
+    // a block's run, or its unit; false: the block has none
+    template <typename TL, int NTHR>
+    __device__ __forceinline__ bool start_block(const AttnArgs &a, int rtiles, int64_t *sh) {
+        if (a.direct) {
+            start_unit<TL>(a, blockIdx.x, rtiles);
+            return true;
+        }
+        int nc = gridDim.x;
+        const AttnPlace place = attn_place<TL, NTHR>(a, a.c.Hk * rtiles, sh, [&](int64_t N) {
+            if (N < nc) nc = (int)N;  // no block without a tile
+            return attn_first_tile(blockIdx.x, N, nc);
+        });
+        if ((int)blockIdx.x >= nc) return false;
+        start<TL>(a, place, attn_first_tile(blockIdx.x, place.N, nc), attn_first_tile(blockIdx.x + 1, place.N, nc), rtiles);
+        return inside();
     }
     __device__ __forceinline__ bool inside() const { return at < end; }
     __device__ __forceinline__ bool last_of_unit() const { return tile + 1 == tiles; }

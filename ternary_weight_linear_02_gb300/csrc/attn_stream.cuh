@@ -116,21 +116,12 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     constexpr int KT = TL::KT, ROWS = C::ROWS, NT = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    int nc = gridDim.x;
     const int R = a.T * a.G;
     pdl_launch_dependents();
 
-    const AttnPlace place = attn_place<TL, kStreamThreads>(a, a.c.Hk, reinterpret_cast<int64_t *>(smem + C::POFF),
-                                                           [&](int64_t N) {
-        if (N < nc) nc = (int)N;  // no block without a tile
-        return attn_first_tile(blockIdx.x, N, nc);
-    });
-    const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
-    if ((int)blockIdx.x >= nc) return;
     uint8_t *ring = smem + warp * C::NS * C::STAGE;
     AttnWalk in, out;  // the tile being copied, the tile being computed
-    in.template start<TL>(a, place, x0, x1, 1);
-    if (!in.inside()) return;
+    if (!in.template start_block<TL, kStreamThreads>(a, 1, reinterpret_cast<int64_t *>(smem + C::POFF))) return;
     out = in;
 
     // Queries of a unit: TPR threads per row, EPT elements each (the first unit's are fetched
@@ -598,10 +589,10 @@ cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     static const cudaError_t attr = cudaFuncSetAttribute(
         attn_stream_kernel<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (attr != cudaSuccess) return attr;
-    const int nc = sms * C::BLOCKS;
+    const int nc = a.direct ? a.B * a.c.Hk : sms * C::BLOCKS;
     attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.direct) return e;
     return launch_join<StreamTiling<C::GR>, C::ROWS, D>(a, 1, nc, st);
 }
 

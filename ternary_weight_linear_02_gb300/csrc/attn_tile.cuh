@@ -112,8 +112,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int nc = gridDim.x;
-    const int R = a.T * a.G, units = a.c.Hk * rtiles;
+    const int R = a.T * a.G;
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -130,16 +129,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         *abort_flag = 0;
         fence_barrier_init();
     }
-    const AttnPlace place = attn_place<TL, kTileThreads>(a, units, reinterpret_cast<int64_t *>(smem + C::POFF),
-                                                         [&](int64_t N) {
-        if (N < nc) nc = (int)N;  // no block without a tile
-        return attn_first_tile(blockIdx.x, N, nc);
-    });
-    const int64_t x0 = attn_first_tile(blockIdx.x, place.N, nc), x1 = attn_first_tile(blockIdx.x + 1, place.N, nc);
-    if ((int)blockIdx.x >= nc) return;
     AttnWalk at;
-    at.template start<TL>(a, place, x0, x1, rtiles);
-    if (!at.inside()) return;
+    if (!at.template start_block<TL, kTileThreads>(a, rtiles, reinterpret_cast<int64_t *>(smem + C::POFF))) return;
     if (warp == 4) tc::tmem_alloc(tmem_slot, C::COLS);
     tc::fence_before_sync();
     __syncthreads();
@@ -594,10 +585,10 @@ cudaError_t launch_tile_d(const AttnArgs &a, int sms, cudaStream_t st) {
     static const cudaError_t attr =
         cudaFuncSetAttribute(attn_tile_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::REQ);
     if (attr != cudaSuccess) return attr;
-    const int nc = sms * 2, rtiles = (a.T * a.G + kTileRows - 1) / kTileRows;
+    const int rtiles = (a.T * a.G + kTileRows - 1) / kTileRows, nc = a.direct ? a.B * a.c.Hk * rtiles : sms * 2;
     attn_tile_kernel<FMT, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.direct) return e;
     return launch_join<TileTiling, kTileRows, D>(a, rtiles, nc, st);
 }
 

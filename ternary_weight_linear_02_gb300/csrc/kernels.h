@@ -269,6 +269,7 @@ struct AttnArgs {
     int B, T, Hq, G;     // batch, new tokens, query heads, query heads per kv head
     int q_vec;           // every q row starts on a 16-byte boundary
     int bf;              // q and out are bf16 (else fp16)
+    int direct;          // a block per unit (attn_sched.cuh), no workspace
     int *status;
 };
 // SMs that a workspace is laid out for (the GPU has 152; more are left unused)
@@ -277,6 +278,6 @@ cudaError_t launch_attn_int8(const AttnArgs &a, bool tile, int sms, cudaStream_t
 cudaError_t launch_attn_fp8(const AttnArgs &a, bool tile, int sms, cudaStream_t st);
 cudaError_t launch_attn_int4(const AttnArgs &a, bool tile, int sms, cudaStream_t st);
 cudaError_t launch_tree_attention(const AttnArgs &a, int sm_count, cudaStream_t st);
-int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D);
+int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_keys);
 
 }  // namespace tl

@@ -107,10 +107,13 @@ def test_attention_refusals(lib):
     assert call(ws=A + 8) == ALIGN
     assert call(b=0, q=None, out=None) == OK and call(t=0, q=None, out=None) == OK
     w = lib.ternary_tree_attention_workspace
-    assert w(-1, 1, 4, 2, 64) == -1 and w(1, 1, 5, 2, 64) == -1 and w(1, 1, 4, 2, 96) == -1
-    assert w(0, 1, 4, 2, 64) == 0 and w(2, 3, 4, 2, 64) >= 0
-    if w(2, 3, 4, 2, 64) > 0:
-        assert call(ws=None) == NULL and call(ws_bytes=w(2, 3, 4, 2, 64) - 1) == SHAPE
+    assert w(-1, 1, 4, 2, 64, 64) == -1 and w(1, 1, 5, 2, 64, 64) == -1 and w(1, 1, 4, 2, 96, 64) == -1
+    assert w(1, 1, 4, 2, 64, -1) == -1 and w(1, 1, 4, 2, 64, 1 << 31) == -1
+    assert w(0, 1, 4, 2, 64, 64) == 0
+    assert w(2, 3, 4, 2, 64, 64) == 0                 # contexts of a page or two: no workspace
+    need = w(2, 3, 4, 2, 64, 1 << 16)
+    assert need > 0
+    assert call(wide=4096, ws=None) == NULL and call(wide=4096, ws_bytes=need - 1) == SHAPE
 
 
 def test_injected_launch_failure(lib):
