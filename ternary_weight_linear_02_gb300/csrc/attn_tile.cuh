@@ -15,12 +15,19 @@
 //    transposed.  They also place the queries at a unit's start (f16; from bf16 scaled by
 //    the power of two of the row's largest element).  Codes that came through registers
 //    instead, a tile ahead, were waited for with every other load of their warp
-//    (page table, scales): 5000 cycles a tile against STAGED_CYCLES.
+//    (page table, scales): 5000 cycles a tile against 3500.
 //  * Warps 0-3: a row's 64 scores are read once into registers; P (f16) overwrites the
 //    first half of them in TMEM.  The weights hold the value scale relative to a power of two
-//    svref at least twice the largest scale met, 2^14 up, so that weights down to 2^-28 of
-//    the largest keep all 11 bits.  The maximum moves only when exceeded by a factor of 4,
-//    and svref when exceeded: then O is rescaled in TMEM.
+//    svref at least twice the largest scale met, so far up that weights down to 2^-23 of the
+//    largest keep all 11 bits (kAttnUp, kAttnMargin in attn_sched.cuh).  Their reference
+//    moves only when exceeded by a factor of 4, and then a factor of 8 beyond, and svref
+//    when exceeded: then O is rescaled in TMEM.
+// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 250 to 264 us, 340
+// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 83 to 89 us.
+// Bound by the instruction stream of the three kinds of warps: 39 % of the issue slots are
+// used, and the stalls are waits for instructions and for loads.
+// Softmax warps without a row that decode too (23 rows: three more) were slower: 99 us
+// against 90 (fp8).
 // Every mbarrier wait is bounded; one that gives up sets the device status word, and the
 // block stops issuing work, frees its TMEM and returns.
 #pragma once

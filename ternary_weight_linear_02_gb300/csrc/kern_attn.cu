@@ -8,9 +8,10 @@ namespace {
 
 // Rows of a kv head (new tokens x query heads that share it): up to 16 the streaming kernel,
 // whose warp MMAs keep up with the cache's bytes (6 sequences of up to 4099 keys, 32 heads,
-// int4: 78 us at 16 rows against 106 us); above, it would need more registers than a
-// thread has or read the cache twice, and the tcgen05 kernel takes 128 rows at a time
-// (106 us at 25 rows, against 125 us of a three-block streaming form at 24).
+// int4: 75 us at 16 rows; the tcgen05 kernel 90 us at 17); above, it would need more
+// registers than a thread has or read the cache twice, and the tcgen05 kernel takes 128
+// rows at a time (90 us at 24 rows, against 125 us of a streaming form with three blocks of
+// 8 rows).
 constexpr int64_t kStreamMaxRows = 16;
 bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 
@@ -18,7 +19,12 @@ bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 // fitted to both forms over contexts of 50 to 20000 keys: beginning and ending a unit,
 // a tile (with the blocks per SM that run at once), and what dealing costs beside (finding
 // the run, partial results, the join and its launch).  The lengths are not known here: the
-// page table's width stands for them.
+// page table's width stands for them.  A unit per block against dealt, in us:
+//   one token, 28 heads on 4, fp8: 32 sequences of 100 keys 6.4 / 10.1, of 1000 16.7 / 17.4;
+//   one of 1000 16.1 / 10.4, of 20000 205 / 21; int8, 64 of up to 8192 116 / 93, and with 28
+//   kv heads 530 / 566;
+//   trees: 8 of 64, 500 keys, 28 on 4 35 / 50; 6 of 23, 32 heads, int4, 500 keys 29 / 38,
+//   4099 keys 137 / 89.
 bool use_direct(int64_t B, int64_t T, int Hq, int Hk, int64_t max_keys) {
     const int64_t rows = T * (Hq / Hk);
     const bool tile = use_tile(rows);

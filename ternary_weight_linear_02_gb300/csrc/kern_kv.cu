@@ -112,7 +112,9 @@ __device__ __forceinline__ void put_row(const RopeCols<INTER> &rc, const float (
 
 // One thread per column group of 16 elements (RopeCols) of a query head, or of a kv head's key and
 // value together (their loads in flight at once).  Rows are requested before their position
-// is looked at.
+// is looked at.  9973 tokens of 32 heads, f16 to INT4, half rotated: 82 us, 4.6 TB/s (rows,
+// codes and scales; a copy's rate is 6.7); with divisions in the place of the corrected
+// reciprocal it was bound by them.  Two rows of one tensor per thread were slower.
 template <typename T, int FMT, int D, bool INTER, bool VEC>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvAppendArgs a, uint32_t items, uint32_t total) {
     constexpr uint32_t C = D / 16;
@@ -212,7 +214,8 @@ cudaError_t append_t(const KvAppendArgs &a, bool inter, bool vec, cudaStream_t s
 }
 
 // Reading back: one thread per 16 elements of one kv head's key and value row, both loads in
-// flight together.
+// flight together.  131072 tokens of 4 heads, e4m3 to bf16: 65 us, 6.3 TB/s, 0.94 of a
+// copy's rate.
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(KvReadArgs a, uint32_t total) {
     constexpr uint32_t C = D / 16;

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(RopeTableArgs a) {
 // Vector form: rows whose starts are 16-byte aligned, R and D multiples of 16.  A thread owns one
 // column group of 16 elements (RopeCols) of one head: measured against two and four
 // heads per thread, which read a table row less often but keep fewer warps in flight
-// (16384 tokens x 32 heads of 128, half rotated: ROPE1 us against 72 and 128; a plain copy of
+// (16384 tokens x 32 heads of 128, half rotated: 48.5 us, 5.6 TB/s, against 72 and 128; a plain copy of
 // the same bytes takes 43).  The head's elements are requested before the position is
 // looked at, so that only the table row waits for it.
 template <typename T, bool INTER>
