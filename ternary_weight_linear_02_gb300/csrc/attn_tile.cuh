@@ -16,21 +16,26 @@
 //    the power of two of the row's largest element).  Codes that came through registers
 //    instead, a tile ahead, were waited for with every other load of their warp
 //    (page table, scales): 5000 cycles a tile against 3500.
-//  * Warps 0-3: a row's 64 scores are read once into registers; P (f16) overwrites the
-//    first half of them in TMEM.  The weights hold the value scale relative to a power of two
-//    svref at least twice the largest scale met, so far up that weights down to 2^-23 of the
-//    largest keep all 11 bits (kAttnUp, kAttnMargin in attn_sched.cuh).  Their reference
-//    moves only when exceeded by a factor of 4, and then a factor of 8 beyond, and svref
-//    when exceeded: then O is rescaled in TMEM.
-// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 250 to 264 us, 340
-// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 83 to 89 us.
-// Bound by the instruction stream of the three kinds of warps: 39 % of the issue slots are
-// used, and the stalls are waits for instructions and for loads.
+//  * Warps 0-3: a row's 64 scores are read in halves, for the maximum and then for the
+//    weights; P (f16) overwrites the first half of them in TMEM.  The weights hold the
+//    value scale relative to a power of two svref at least twice the largest scale met, so
+//    far up that weights down to 2^-23 of the largest keep all 11 bits (kAttnUp, kAttnMargin
+//    in attn_sched.cuh).  Their reference moves only when exceeded by a factor of 4, and
+//    then a factor of 8 beyond, and svref when exceeded: then O is rescaled in TMEM.
+// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
+// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 75 us.
+// Bound by the instruction streams of the three kinds of warps: 39 % of the issue slots are
+// used, and the stalls are waits for instructions and for loads.  So short code without
+// spills matters: loops over the halves of a tile and one decoder for keys and values took
+// these two cases from 255 and 85 us.  Two more warps (ten, one for the copies and
+// four decoders) decoded in half the time but slowed the softmax by more.
 // Softmax warps without a row that decode too (23 rows: three more) were slower: 99 us
 // against 90 (fp8).
 // Every mbarrier wait is bounded; one that gives up sets the device status word, and the
 // block stops issuing work, frees its TMEM and returns.
 #pragma once
+
+#include <climits>
 
 #include "attn_sched.cuh"
 #include "kv.cuh"
@@ -353,11 +358,25 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         };
 
         int unit = 0;         // row factors' buffer
-        auto keys = [&](int j, bool fresh) -> bool {  // of tile j = `at`
-            if (!wait(ckfull, j) || (j > 0 && !wait(sdone, j - 1))) return false;  // the last tile's keys have been read
-            if (fresh) queries(at, unit++ & 3);                                    // (and the last unit's queries)
-            decode(dw, C::CKOFF + (j & 1) * C::CODES, C::KOFF);
-            if (dw == 1) {  // the largest value scale among keys that every row sees
+        // Turns of a tile's keys and the values of the tile before, so that the scores are computed
+        // first; one copy of the code serves both.
+        bool fresh = true;  // `at` begins a unit
+#pragma unroll 1
+        for (int i = 0, last = INT_MAX;; ++i) {
+            const int j = (i >> 1) - (i & 1);  // keys of tiles 0 1 2 .., values of tiles -1 0 1 ..
+            const bool vals = i & 1;
+            if (vals) {
+                if (j < 0) continue;
+            } else if (j > last) {
+                continue;
+            }
+            uint64_t *const from = vals ? cvfull : ckfull, *const gone = vals ? odone : sdone;
+            // the codes have landed, and what was made of the tile before has been read
+            if (!wait(from, j) || (j > 0 && !wait(gone, j - 1))) break;
+            if (!vals && fresh) queries(at, unit++ & 3);  // (and the last unit's queries)
+            const int turn = vals ? 2 - dw : dw;
+            decode(turn, (vals ? C::CVOFF : C::CKOFF) + (j & 1) * C::CODES, vals ? C::VOFF : C::KOFF);
+            if (!vals && dw == 1) {  // the largest value scale among keys that every row sees
                 const int k = at.tile * KT + lane * 2;
                 const float2 v = *reinterpret_cast<const float2 *>(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 8);
                 // (negative scales do not count: the others compare as their bits)
@@ -366,21 +385,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 mx = __reduce_max_sync(0xffffffffu, mx);
                 if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::SMOFF)[j & 3] = mx;
             }
-            publish(kfull);
-            return true;
-        };
-        // the next tile's keys before this one's values: its scores are computed first
-        bool more = true, ok = keys(0, true);
-#pragma unroll 1
-        for (int j = 0; ok && more; ++j) {
-            more = at.template more<TL>();
-            if (more) {
-                const bool fresh = at.template next<TL>(a, rtiles);
-                if (!keys(j + 1, fresh)) break;
+            publish(vals ? vfull : kfull);
+            if (vals) {
+                if (j == last) break;
+            } else if (at.template more<TL>()) {
+                fresh = at.template next<TL>(a, rtiles);
+            } else {
+                last = j;
             }
-            if (!wait(cvfull, j) || (j > 0 && !wait(odone, j - 1))) break;  // the last tile's values have been read
-            decode(2 - dw, C::CVOFF + (j & 1) * C::CODES, C::VOFF);
-            publish(vfull);
         }
     } else {
         // ---------------- softmax: thread = row = TMEM lane
@@ -399,9 +411,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             if (!wait(sdone, j)) break;
             tc::fence_after_sync();
             if (live) {
-                uint32_t s[2][32];
-                tc::ld_32x32b_x32(scol, s[0]);
-                tc::ld_32x32b_x32(scol + 32, s[1]);
                 if (fresh) {
                     whole = at.tile == 0;
                     f = reinterpret_cast<const float *>(smem + C::FOFF)[(unit & 3) * 128 + row];
@@ -412,52 +421,65 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 const float4 *sk = reinterpret_cast<const float4 *>(smem + C::SKOFF + (j & 3) * KT * 4);
                 const float4 *sv = reinterpret_cast<const float4 *>(smem + C::SVOFF + (j & 3) * KT * 4);
                 float svmax = reinterpret_cast<const float *>(smem + C::SMOFF)[j & 3];
-                tc::wait_ld();
-                // ---- scores: products with the key scales; the row's largest
-#pragma unroll
-                for (int k = 0; k < KT; k += 4) {
-                    const float4 w = sk[k / 4];
-                    uint32_t *p = &s[k >> 5][k & 31];
-                    const float2 x = mul2(make_float2(__uint_as_float(p[0]), __uint_as_float(p[1])), make_float2(w.x, w.y));
-                    const float2 y = mul2(make_float2(__uint_as_float(p[2]), __uint_as_float(p[3])), make_float2(w.z, w.w));
-                    p[0] = __float_as_uint(x.x), p[1] = __float_as_uint(x.y);
-                    p[2] = __float_as_uint(y.x), p[3] = __float_as_uint(y.y);
-                }
-                uint32_t see[2] = {~0u, ~0u};
+                uint32_t see0 = ~0u, see1 = ~0u;
                 const bool edge = at.tile * KT + KT > at.ctx;  // new tokens' keys, or the end
                 if (edge) {
                     const int tok = min(grow, R - 1) / a.G;
                     const uint8_t *tree = a.tree ? a.tree + at.b * a.tree_b + (int64_t)tok * a.tree_r : nullptr;
                     const float *svs = reinterpret_cast<const float *>(sv);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         const int i0 = at.tile * KT + 32 * c - at.ctx;  // index of the new token at the chunk's start
-                        if (i0 + 32 > 0) {
-                            uint32_t bits = 0;
+                        if (i0 + 32 <= 0) continue;
+                        uint32_t bits = 0;
 #pragma unroll 4
-                            for (int k = 0; k < 32; ++k) {
-                                const int i = i0 + k;
-                                bool u = i < 0;
-                                if (i >= 0 && i < a.T) u = tree ? tree[i] != 0 : i <= tok;
-                                if (u) {
-                                    bits |= 1u << k;
-                                    svmax = fmaxf(svmax, svs[32 * c + k]);
-                                }
+                        for (int k = 0; k < 32; ++k) {
+                            const int i = i0 + k;
+                            bool u = i < 0;
+                            if (i >= 0 && i < a.T) u = tree ? tree[i] != 0 : i <= tok;
+                            if (u) {
+                                bits |= 1u << k;
+                                svmax = fmaxf(svmax, svs[32 * c + k]);
                             }
-                            see[c] = bits;
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(see[c] >> k & 1u)) s[c][k] = 0xFF800000u;  // -infinity
+                        if (c) see1 = bits;
+                        else see0 = bits;
                     }
                 }
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four short chains
+                // ---- scores of half a tile, times the key scales.  The second half is read twice and the
+                // halves share their code: all 64 held at once spilled, and the longer code cost more.
+                uint32_t s[32];
+                auto half = [&](int c) {
+                    tc::ld_32x32b_x32(scol + 32 * c, s);
+                    tc::wait_ld();
 #pragma unroll
-                for (int k = 0; k < KT; k += 2) {
-                    float &x = tops[(k >> 1) & 3];
-                    x = fmaxf(fmaxf(x, __uint_as_float(s[k >> 5][k & 31])), __uint_as_float(s[k >> 5][(k & 31) + 1]));
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 w = sk[c * 8 + k / 4];
+                        const float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(w.x, w.y));
+                        const float2 y = mul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), make_float2(w.z, w.w));
+                        s[k] = __float_as_uint(x.x), s[k + 1] = __float_as_uint(x.y);
+                        s[k + 2] = __float_as_uint(y.x), s[k + 3] = __float_as_uint(y.y);
+                    }
+                    if (edge) {
+                        const uint32_t see = c ? see1 : see0;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(see >> k & 1u)) s[k] = 0xFF800000u;  // -infinity
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 1; c >= 0; --c) {
+                    half(c);
+                    float tops[4] = {top, -INFINITY, -INFINITY, -INFINITY};  // four short chains
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float &x = tops[(k >> 1) & 3];
+                        x = fmaxf(fmaxf(x, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
+                    }
+                    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 }
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f;
+                top *= f;
                 const bool bigger = svmax > __uint_as_float((uint32_t)(ve + 127) << 23);
                 if (__any_sync(0xffffffffu, top > m + kAttnSlack || bigger)) {
                     const float mn = top > m + kAttnSlack ? top + kAttnMargin : m;
@@ -485,14 +507,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 const float off = kAttnUp - m - (float)ve;
                 const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
                 float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
+                    if (c) half(1);
                     uint32_t p[16];
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         const float4 v = sv[c * 8 + k / 4];
-                        float2 x = fma2(make_float2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), f2, off2);
-                        float2 y = fma2(make_float2(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), f2, off2);
+                        float2 x = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2, off2);
+                        float2 y = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), f2, off2);
                         x = make_float2(ex2(x.x), ex2(x.y));
                         y = make_float2(ex2(y.x), ex2(y.y));
                         l2 = add2(l2, x);
@@ -503,10 +526,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         p[k / 2 + 1] = pack2(__half(), y.x, y.y);
                     }
                     if (edge) {  // an unseen scale may be a NaN
+                        const uint32_t see = c ? see1 : see0;
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            if (!(see[c] >> (2 * k) & 1u)) p[k] &= 0xFFFF0000u;
-                            if (!(see[c] >> (2 * k + 1) & 1u)) p[k] &= 0x0000FFFFu;
+                            if (!(see >> (2 * k) & 1u)) p[k] &= 0xFFFF0000u;
+                            if (!(see >> (2 * k + 1) & 1u)) p[k] &= 0x0000FFFFu;
                         }
                     }
                     tc::st_32x32b_x16(scol + c * 16, p);
