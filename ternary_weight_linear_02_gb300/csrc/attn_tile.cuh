@@ -23,12 +23,13 @@
 //    in attn_sched.cuh).  Their reference moves only when exceeded by a factor of 4, and
 //    then a factor of 8 beyond, and svref when exceeded: then O is rescaled in TMEM.
 // Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
-// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 75 us.
+// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 73 us.
 // Bound by the instruction streams of the three kinds of warps: 39 % of the issue slots are
 // used, and the stalls are waits for instructions and for loads.  So short code without
 // spills matters: loops over the halves of a tile and one decoder for keys and values took
-// these two cases from 255 and 85 us.  Two more warps (ten, one for the copies and
-// four decoders) decoded in half the time but slowed the softmax by more.
+// these two cases from 255 and 85 us, a rolled loop for the rescaling the first in int4 from
+// 217 to 197.  Two more warps (ten, one for the copies and four decoders) decoded in half
+// the time but slowed the softmax by more.
 // Softmax warps without a row that decode too (23 rows: three more) were slower: 99 us
 // against 90 (fp8).
 // Every mbarrier wait is bounded; one that gives up sets the device status word, and the
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     if (!fresh) {
                         if (!wait(odone, j - 1)) break;  // O holds every product so far
                         tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < D / 16; ++h) {
                             uint32_t o[16];
                             tc::ld_32x32b_x16(lane_base + C::OCOL + h * 16, o);

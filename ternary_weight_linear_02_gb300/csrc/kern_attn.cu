@@ -7,11 +7,11 @@ namespace tl {
 namespace {
 
 // Rows of a kv head (new tokens x query heads that share it): up to 16 the streaming kernel,
-// whose warp MMAs keep up with the cache's bytes (6 sequences of up to 4099 keys, 32 heads,
-// int4: 75 us at 16 rows; the tcgen05 kernel 90 us at 17); above, it would need more
-// registers than a thread has or read the cache twice, and the tcgen05 kernel takes 128
-// rows at a time (90 us at 24 rows, against 125 us of a streaming form with three blocks of
-// 8 rows).
+// whose warp MMAs keep up with the cache's bytes.  Streaming against tcgen05, 32 heads, int4:
+// 6 sequences of up to 4099 keys, 9 rows 71 / 73 us, 16 rows 74 / 75; one, 13 rows 25 / 30;
+// 32 of up to 300 keys, 12 rows 46 / 68.  Above, it would need more registers than a thread
+// has or read the cache twice (24 rows in three blocks of 8: 125 us), and the tcgen05 kernel
+// takes 128 rows at a time (24 rows: 75 us).
 constexpr int64_t kStreamMaxRows = 16;
 bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 
@@ -24,7 +24,7 @@ bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 //   one of 1000 16.1 / 10.4, of 20000 205 / 21; int8, 64 of up to 8192 116 / 93, and with 28
 //   kv heads 530 / 566;
 //   trees: 8 of 64, 500 keys, 28 on 4 35 / 50; 6 of 23, 32 heads, int4, 500 keys 29 / 38,
-//   4099 keys 137 / 89.
+//   4099 keys 137 / 89 (before the tcgen05 kernel reached 73 there).
 bool use_direct(int64_t B, int64_t T, int Hq, int Hk, int64_t max_keys) {
     const int64_t rows = T * (Hq / Hk);
     const bool tile = use_tile(rows);
