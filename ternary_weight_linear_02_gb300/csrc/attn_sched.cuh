@@ -14,7 +14,7 @@
 // block given a run of short units would be the last to end by far.  Nothing is done in
 // them, and a block whose run ends within them does not touch the unit.  (6 trees of 23,
 // 32 heads, up to 4099 keys, int4: with the margin below, 249 us without these tiles and
-// that margin, 125 us with both; 83 to 89 us as things are.)
+// that margin, 125 us with both, as the kernel was then; 73 to 75 us now.)
 //
 // Where contexts can only be short (by the page table's width), or units are many, a block
 // takes one whole unit instead (AttnArgs::direct): nothing to find, nothing to join.
@@ -39,7 +39,8 @@ constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite:
 // lies between 2^9 and 2^15, weights down to 2^-23 of it keep all 11 bits, and none above
 // 2^-33 vanishes.  With scores of a standard deviation of 2.6 (3.7 in powers of two) and no
 // margin, half the 64-key tiles moved some row of a warp, which cost more than the tile
-// itself (8 trees of 64 over 16384 keys: 382 us against 265 with the margin).
+// itself (8 trees of 64 over 16384 keys: 382 us against 265 with the margin, as the kernel
+// was then; 203 us now).
 constexpr float kAttnUp = 14.f, kAttnSlack = 2.f, kAttnMargin = 3.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
