@@ -24,9 +24,9 @@
 //    then a factor of 8 beyond, and svref when exceeded: then O is rescaled in TMEM.
 // Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
 // TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 73 us.
-// Bound by the instruction streams of the three kinds of warps: 39 % of the issue slots are
-// used, and the stalls are waits for instructions and for loads.  So short code without
-// spills matters: loops over the halves of a tile and one decoder for keys and values took
+// Bound by the instruction streams of the three kinds of warps: 43 % of the issue slots are
+// used, the tensor pipe 22 %, and the stalls are waits for loads and for results.  Short code
+// without spills matters (39 %, and waits for instructions, before it): loops over the halves of a tile and one decoder for keys and values took
 // these two cases from 255 and 85 us, a rolled loop for the rescaling the first in int4 from
 // 217 to 197.  Two more warps (ten, one for the copies and four decoders) decoded in half
 // the time but slowed the softmax by more.
