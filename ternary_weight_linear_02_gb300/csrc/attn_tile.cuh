@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = a.T * a.G;
-    pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -149,6 +148,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    // Dependents may start once every block of this grid holds its TMEM (or has left for want
+    // of a run): a linear layer that follows the direct form allocates columns of its own before
+    // it waits for this grid, and a block that found none left would wait for it in turn.
+    pdl_launch_dependents();
 
     auto wait_phase = [&](uint64_t *bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
