@@ -42,6 +42,18 @@ constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite:
 // itself (8 trees of 64 over 16384 keys: 382 us against 265 with the margin, as the kernel
 // was then; 203 us now).
 constexpr float kAttnUp = 14.f, kAttnSlack = 2.f, kAttnMargin = 3.f;
+// The streaming kernel's weights, each with its value scale: products e sv.  In powers of two,
+// with score z_j and size x_j = max(log2 |sv_j|, kAttnSmall), a row's reference r follows the
+// largest z_j + x_j among the keys that this row sees:
+//   e_j = 2^(z_j - r + kAttnTop + kAttnBias),  product_j = e_j (sv_j 2^-kAttnBias).
+// r moves only when some z_j + x_j exceeds it by kAttnSlack (so products stay below 2^15), and
+// then kAttnMargin beyond: the largest lies between 2^10 and 2^15, products down to 2^-24 of
+// it keep all 11 bits of f16, whatever scales other keys or other rows have.  The sum of the
+// weights counts e_j, whose range in fp32 the bias centres: for scales of up to 2^128 terms
+// down to 2^-24 of the largest weight count, and with scales of 2^kAttnSmall and less (rows
+// of zeros) 2^25 equal weights fit.  Values below 2^kAttnSmall lose bits only beyond that.
+constexpr float kAttnTop = 13.f, kAttnBias = 16.f, kAttnSmall = -72.f, kAttnOff = kAttnTop + kAttnBias;
+constexpr float kAttnUnbias = 1.f / 65536.f;  // 2^-kAttnBias
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -50,6 +62,13 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// x_j of a value scale; finite for every bit pattern
+__device__ __forceinline__ float attn_size(float sv) { return fminf(fmaxf(lg2(fabsf(sv)), kAttnSmall), 128.f); }
 
 // Keys of sequence b, clamped to its page-table row.
 __device__ __forceinline__ int attn_context(const AttnArgs &a, int b) {
@@ -388,11 +407,12 @@ struct AttnSum {
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float mn = fmaxf(m, pm[k]), f = ex2(m - mn), g = ex2(pm[k] - mn);
+            // sums in two steps: references may lie further apart than fp32's exponents reach
+            const float mn = fmaxf(m, pm[k]), f = ex2(.5f * (m - mn)), g = ex2(.5f * (pm[k] - mn));
             m = mn;
-            l = l * f + pl[k] * g;
+            l = l * f * f + pl[k] * g * g;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[k][e] * g;
+            for (int e = 0; e < E; ++e) o[e] = o[e] * (f * f) + v[k][e] * (g * g);
         }
     }
 };
@@ -438,9 +458,9 @@ __global__ void __launch_bounds__(WIDE ? 256 : 512) attn_join_kernel(AttnArgs a,
         const int d = threadIdx.x;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float g = ex2(sm[w] - M);
-            L += sl[w] * g;
-            if (d < D) x += so[w][d] * g;
+            const float g = ex2(.5f * (sm[w] - M));
+            L += sl[w] * g * g;
+            if (d < D) x += so[w][d] * (g * g);
         }
         if (d < D) attn_store(a, o * D + d, L == 0.f ? 0.f : x / L);
         if (a.lse && d == 0) a.lse[o] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;

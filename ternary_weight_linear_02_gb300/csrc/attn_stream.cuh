@@ -1,7 +1,7 @@
 // attn_stream.cuh -- attention for few rows per kv head (single tokens, small trees):
 // the cache streams through registers once, fed to warp MMAs.
 //
-//   S^T = K Q^T, P = exp2(S sk f - m) sv, O^T += V^T P^T    (f = scale log2 e)
+//   S^T = K Q^T, P = exp2(S sk f - r) sv, O^T += V^T P^T    (f = scale log2 e)
 //
 // For at most 16 rows the bytes of the cache bound the call (16 rows x 4 flops per
 // 8-bit element: about 32 flops a byte), so everything is laid out for the stream:
@@ -20,12 +20,12 @@
 //  * codes become f16 (exact); the products are exact, sums fp32.  Queries in bf16
 //    enter as f16 scaled by the power of two of their row's largest element: exact
 //    within 2^-14 of it, below that rounded at 2^-25 of it, far under the fp32 sums.
-//  * P is rounded to f16 (2^-11 relative), kept so far up that weights down to 2^-23 of the
-//    largest keep all 11 bits (kAttnUp, kAttnMargin in attn_sched.cuh).
-//  * The value scales multiply P, relative to twice the largest scale met (svref).  The
-//    reference of the weights moves only when exceeded by a factor of 4, and then a factor
-//    of 8 beyond; svref only when exceeded: the accumulators are rescaled a few times per
-//    unit, not per tile.
+//  * P is rounded to f16 (2^-11 relative) with its value scale in it, kept so far up that
+//    products down to 2^-24 of a row's largest keep all 11 bits.  A row's reference is that of
+//    its own products (kAttnTop in attn_sched.cuh), so neither a key of a negligible weight
+//    nor one that another row sees takes bits from it.  It moves only when exceeded by a
+//    factor of 4, and then a factor of 8 beyond: the accumulators are rescaled a few times
+//    per unit, not per tile.
 // Measured: 64 sequences of 4096 to 8192 keys, 28 query heads on 4, int8, one token each:
 // 92 us, 4.5 TB/s (0.67 of a copy's rate; 5.4 TB/s with 28 kv heads): issue slots (52 % used, half of them by the codes'
 // conversions) and the equal division of tiles among blocks whose speeds differ by some
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : C::KSTEPS][2];
     uint2 *const qsm = reinterpret_cast<uint2 *>(smem + C::GOFF) + lane;
     float f[NB][2];                        // score factors of rows 8 n + 2t and + 1
-    float m[NB][2], l[NB][2], svref = 1e-30f, inv = 1e30f;  // inv = 1 / svref
+    float ref[NB][2], l[NB][2];            // reference of the products, sum of the weights
     float acc[NB][NT][4];
     bool fresh = true, whole = true;       // the next tile begins a unit (for this block); the unit from its start
     int which = 0, get = 0;                // slot of a partial result; stage being read
@@ -282,13 +282,11 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 }
                 f[n][0] = fac[8 * n + 2 * t];
                 f[n][1] = fac[8 * n + 2 * t + 1];
-                m[n][0] = m[n][1] = kAttnLow;
+                ref[n][0] = ref[n][1] = kAttnLow;
                 l[n][0] = l[n][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
             }
-            svref = 1e-30f;
-            inv = 1e30f;
             __syncthreads();  // the queries' buffer is the join buffer too
         }
 
@@ -363,7 +361,6 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
-                    bool any[2] = {false, false};
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -372,38 +369,26 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                             const int tok = min(R - 1, 8 * n + 2 * t + (j & 1)) / a.G;
                             bool u = i < 0;
                             if (i >= 0 && i < a.T) u = tree ? tree[tok * a.tree_r + i] != 0 : i <= tok;
-                            if (u) any[j >> 1] = true;
-                            else z[gr][n][j] = -INFINITY, unseen |= 1u << (4 * (gr * NB + n) + j);
+                            if (!u) z[gr][n][j] = -INFINITY, unseen |= 1u << (4 * (gr * NB + n) + j);
                         }
-                    if (!any[0]) sv[gr][0] = 0.f;  // unseen scales may hold anything
-                    if (!any[1]) sv[gr][1] = 0.f;
                 }
             }
-            float svm = fmaxf(sv[0][0], sv[0][1]), top[NB][2];
+            // the largest product of each row; the size of an unseen scale is finite too
+            float top[NB][2];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n) top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) top[n][r] = fmaxf(z[0][n][r], z[0][n][2 + r]);
-#pragma unroll
-            for (int gr = 1; gr < GR; ++gr) {
-                svm = fmaxf(svm, fmaxf(sv[gr][0], sv[gr][1]));
+            for (int gr = 0; gr < GR; ++gr) {
+                const float x0 = attn_size(sv[gr][0]), x1 = attn_size(sv[gr][1]);
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) top[n][r] = fmaxf(top[n][r], fmaxf(z[gr][n][r], z[gr][n][2 + r]));
+                    for (int r = 0; r < 2; ++r) top[n][r] = fmaxf(top[n][r], fmaxf(z[gr][n][r] + x0, z[gr][n][2 + r] + x1));
             }
-            bool move = svm > svref;
+            bool move = false;
 #pragma unroll
-            for (int n = 0; n < NB; ++n) move = move || top[n][0] > m[n][0] + kAttnSlack || top[n][1] > m[n][1] + kAttnSlack;
+            for (int n = 0; n < NB; ++n) move = move || top[n][0] > ref[n][0] + kAttnSlack || top[n][1] > ref[n][1] + kAttnSlack;
             if (__any_sync(0xffffffffu, move)) {
-                float cv = 1.f;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, o));
-                if (svm > svref) {  // twice the largest: the next slightly larger one changes nothing
-                    cv = svref / (2.f * svm);
-                    svref = 2.f * svm;
-                    inv = __frcp_rn(svref);
-                }
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -411,32 +396,33 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         float x = top[n][r];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        x = x > m[n][r] + kAttnSlack ? x + kAttnMargin : m[n][r];
-                        const float c = ex2(m[n][r] - x);
-                        m[n][r] = x;
-                        l[n][r] *= c;
+                        x = x > ref[n][r] + kAttnSlack ? x + kAttnMargin : ref[n][r];
+                        // in two steps: the sum may outlive a factor that fp32 cannot hold
+                        const float h = ex2(.5f * (ref[n][r] - x)), c = h * h;
+                        ref[n][r] = x;
+                        l[n][r] = l[n][r] * h * h;
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            acc[n][i][r] *= c * cv;
-                            acc[n][i][2 + r] *= c * cv;
+                            acc[n][i][r] *= c;
+                            acc[n][i][2 + r] *= c;
                         }
                     }
             }
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
                 const uint8_t *st = stage + gr * C::GROUP;
-                const float wv[2] = {sv[gr][0] * inv, sv[gr][1] * inv};
+                const float wv[2] = {sv[gr][0] * kAttnUnbias, sv[gr][1] * kAttnUnbias};
                 uint32_t pb[NB][2];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     float p[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float e = ex2(z[gr][n][j] - (m[n][j & 1] - kAttnUp));
+                        const float e = ex2(z[gr][n][j] - (ref[n][j & 1] - kAttnOff));
                         l[n][j & 1] += e;
                         p[j] = e * wv[j >> 1];
                     }
-                    if (unseen) {
+                    if (unseen) {  // an unseen scale may be a NaN or an infinity
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (unseen >> (4 * (gr * NB + n) + j) & 1u) p[j] = 0.f;
@@ -512,7 +498,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], o);
                     if (g == 0) {
-                        wm[warp * ROWS + 8 * n + 2 * t + r] = m[n][r];
+                        wm[warp * ROWS + 8 * n + 2 * t + r] = ref[n][r];
                         wl[warp * ROWS + 8 * n + 2 * t + r] = l[n][r];
                     }
                 }
@@ -525,7 +511,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 for (int r = 0; r < 2; ++r) {
                     const float *p = wm + 8 * n + 2 * t + r;
                     const float M = fmaxf(fmaxf(p[0], p[ROWS]), fmaxf(p[2 * ROWS], p[3 * ROWS]));
-                    c[n][r] = ex2(m[n][r] - M) * svref;
+                    c[n][r] = ex2(ref[n][r] - M) * (1.f / kAttnUnbias);  // in units of the weights' sum
                 }
 #pragma unroll 1
             for (int turn = 0; turn < 4; ++turn) {
@@ -553,7 +539,10 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
                 for (int i = 1; i < 4; ++i) M = fmaxf(M, wm[i * ROWS + row]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) Ls += wl[i * ROWS + row] * ex2(wm[i * ROWS + row] - M);
+                for (int i = 0; i < 4; ++i) {
+                    const float h = ex2(.5f * (wm[i * ROWS + row] - M));
+                    Ls += wl[i * ROWS + row] * h * h;
+                }
                 float v[EPT];
 #pragma unroll
                 for (int e = 0; e < EPT; e += 2) {
@@ -567,7 +556,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + out_row * D + part * EPT);
 #pragma unroll
                     for (int e = 0; e < EPT; e += 2) o[e / 2] = attn_pack(a, v[e] * rl, v[e + 1] * rl);
-                    if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnUp + log2f(Ls)) * kLn2;
+                    if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnOff + log2f(Ls)) * kLn2;
                 } else {
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
                     float *o = slot + row * D + part * EPT;
@@ -575,7 +564,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     for (int e = 0; e < EPT; e += 4)
                         *reinterpret_cast<float4 *>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     if (part == 0) {
-                        slot[ROWS * D + row] = M - kAttnUp;
+                        slot[ROWS * D + row] = M - kAttnOff;
                         slot[ROWS * (D + 1) + row] = Ls;
                     }
                 }
