@@ -33,27 +33,23 @@
 namespace tl {
 
 constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite: no inf - inf)
-// f16 weights: 2^kAttnUp times their ratio to the reference m of their row, times a value scale
-// of at most half its reference.  m moves only when a score exceeds it by kAttnSlack
-// (so weights stay below 2^15), and then kAttnMargin beyond the score: the largest weight
-// lies between 2^9 and 2^15, weights down to 2^-23 of it keep all 11 bits, and none above
-// 2^-33 vanishes.  With scores of a standard deviation of 2.6 (3.7 in powers of two) and no
-// margin, half the 64-key tiles moved some row of a warp, which cost more than the tile
-// itself (8 trees of 64 over 16384 keys: 382 us against 265 with the margin, as the kernel
-// was then; 203 us now).
-constexpr float kAttnUp = 14.f, kAttnSlack = 2.f, kAttnMargin = 3.f;
-// The streaming kernel's weights, each with its value scale: products e sv.  In powers of two,
-// with score z_j and size x_j = max(log2 |sv_j|, kAttnSmall), a row's reference r follows the
-// largest z_j + x_j among the keys that this row sees:
+// f16 weights, each with its value scale: products e sv.  In powers of two, with score z_j and
+// size x_j = max(log2 |sv_j|, kAttnSmall), a row's reference r follows the largest z_j + x_j
+// among the keys that this row sees:
 //   e_j = 2^(z_j - r + kAttnTop + kAttnBias),  product_j = e_j (sv_j 2^-kAttnBias).
 // r moves only when some z_j + x_j exceeds it by kAttnSlack (so products stay below 2^15), and
 // then kAttnMargin beyond: the largest lies between 2^10 and 2^15, products down to 2^-24 of
-// it keep all 11 bits of f16, whatever scales other keys or other rows have.  The sum of the
+// it keep all 11 bits of f16, whatever scales other keys or other rows have.  (The tcgen05
+// kernel may take a bound that is up to kAttnSpread higher: 2^6, 2^-20.)  The sum of the
 // weights counts e_j, whose range in fp32 the bias centres: for scales of up to 2^128 terms
 // down to 2^-24 of the largest weight count, and with scales of 2^kAttnSmall and less (rows
 // of zeros) 2^25 equal weights fit.  Values below 2^kAttnSmall lose bits only beyond that.
+// With scores of a standard deviation of 2.6 (3.7 in powers of two) and no margin, half the
+// 64-key tiles moved some row of a warp, which cost more than the tile itself (8 trees of 64
+// over 16384 keys: 382 us against 265 with the margin, as the kernel was then; 203 us now).
+constexpr float kAttnSlack = 2.f, kAttnMargin = 3.f, kAttnSpread = 4.f;
 constexpr float kAttnTop = 13.f, kAttnBias = 16.f, kAttnSmall = -72.f, kAttnOff = kAttnTop + kAttnBias;
-constexpr float kAttnUnbias = 1.f / 65536.f;  // 2^-kAttnBias
+constexpr float kAttnUnbias = 1.f / 65536.f, kAttnRebias = 65536.f;  // 2^-kAttnBias, 2^kAttnBias
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 for (int r = 0; r < 2; ++r) {
                     const float *p = wm + 8 * n + 2 * t + r;
                     const float M = fmaxf(fmaxf(p[0], p[ROWS]), fmaxf(p[2 * ROWS], p[3 * ROWS]));
-                    c[n][r] = ex2(ref[n][r] - M) * (1.f / kAttnUnbias);  // in units of the weights' sum
+                    c[n][r] = ex2(ref[n][r] - M) * kAttnRebias;  // in units of the weights' sum
                 }
 #pragma unroll 1
             for (int turn = 0; turn < 4; ++turn) {

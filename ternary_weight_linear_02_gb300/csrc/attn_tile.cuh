@@ -1,7 +1,7 @@
 // attn_tile.cuh -- attention for many rows per kv head (drafted trees, chunks of a prompt)
 // on the 5th-generation tensor cores.
 //
-//   S = Q K^T, P = exp2(S sk f - m) sv, O += P V    (f = scale log2 e)
+//   S = Q K^T, P = exp2(S sk f - r) sv, O += P V    (f = scale log2 e)
 //
 // A block owns 128 rows of one (sequence, kv head) -- TMEM lanes, one softmax thread
 // each -- and walks tiles of 64 keys; two blocks per SM.
@@ -18,10 +18,11 @@
 //    (page table, scales): 5000 cycles a tile against 3500.
 //  * Warps 0-3: a row's 64 scores are read in halves, for the maximum and then for the
 //    weights; P (f16) overwrites the first half of them in TMEM.  The weights hold the
-//    value scale relative to a power of two svref at least twice the largest scale met, so
-//    far up that weights down to 2^-23 of the largest keep all 11 bits (kAttnUp, kAttnMargin
-//    in attn_sched.cuh).  Their reference moves only when exceeded by a factor of 4, and
-//    then a factor of 8 beyond, and svref when exceeded: then O is rescaled in TMEM.
+//    value scale, so far up that products down to 2^-24 of the row's largest keep all 11 bits
+//    (kAttnTop in attn_sched.cuh).  A row's reference moves only when exceeded by a factor of
+//    4, and then a factor of 8 beyond: then O is rescaled in TMEM.  The largest score and the
+//    largest value scale together bound a tile's products; only where that bound exceeds the
+//    reference and the tile's scales lie far apart is the largest product looked for.
 // Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
 // TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 73 us.
 // Bound by the instruction streams of the three kinds of warps: 43 % of the issue slots are
@@ -47,7 +48,6 @@ namespace tl {
 
 namespace {
 
-constexpr int kLowExp = -80;  // of the value scale before any key
 using TileTiling = AttnTiling<64, 4>;  // (a unit costs about four tiles beside its own)
 constexpr int kTileKeys = TileTiling::KT, kTileRows = 128, kTileThreads = 256;
 
@@ -66,8 +66,9 @@ struct AttnTileCfg {
     // codes as they lie in the cache: two stages of keys, two of values; scales of four tiles
     static constexpr int CODES = kTileKeys * RB, CKOFF = VOFF + TILE, CVOFF = CKOFF + 2 * CODES;
     static constexpr int SKOFF = CVOFF + 2 * CODES, SVOFF = SKOFF + 4 * kTileKeys * 4;
-    static constexpr int SMOFF = SVOFF + 4 * kTileKeys * 4;  // largest value scale [4],
-    static constexpr int FOFF = SMOFF + 16;               // row factors [4][128]
+    static constexpr int SXOFF = SVOFF + 4 * kTileKeys * 4;  // sizes of the value scales, as them
+    static constexpr int SMOFF = SXOFF + 4 * kTileKeys * 4;  // largest of committed keys [4], far apart? [4]
+    static constexpr int FOFF = SMOFF + 32;               // row factors [4][128]
     static constexpr int BOFF = FOFF + 4 * 512;           // barriers, TMEM slot, abort flag
     static constexpr int POFF = BOFF + 128;               // place of the run (10 words)
     static constexpr int SMEM = POFF + 80 + 1024;         // 1 KB of alignment slack
@@ -107,6 +108,26 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
           "l"(reinterpret_cast<uint64_t &>(c)));
     return d;
+}
+
+// The largest product of a row (a lane's scores of one tile at scol), in powers of two.  Rarely
+// called, and not inlined: in place, and guarded by the softmax's own values, its code made
+// every tile dearer (8 trees of 64 over 16384 keys: 210 us against 203).
+__device__ __noinline__ float largest_product(uint32_t scol, const float *sk, const float *sx, float f, uint32_t see0, uint32_t see1) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kTileKeys; c += 16) {
+        uint32_t s[16];
+        tc::ld_32x32b_x16(scol + c, s);
+        tc::wait_ld();
+        const uint32_t see = (c & 32 ? see1 : see0) >> (c & 16);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float y = __uint_as_float(s[k]) * sk[c + k] * f + sx[c + k];
+            top = fmaxf(top, see >> k & 1u ? y : -INFINITY);
+        }
+    }
+    return top;
 }
 
 template <int FMT, int D>
@@ -378,17 +399,26 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             // the codes have landed, and what was made of the tile before has been read
             if (!wait(from, j) || (j > 0 && !wait(gone, j - 1))) break;
             if (!vals && fresh) queries(at, unit++ & 3);  // (and the last unit's queries)
+            if (!vals && dw == 2) {  // (the warp with the fewest passes) value scales: sizes, and unbiased
+                const int k = at.tile * KT + lane * 2;
+                float2 *const v = reinterpret_cast<float2 *>(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 8);
+                const float2 w = *v, x = make_float2(attn_size(w.x), attn_size(w.y));
+                *v = make_float2(w.x * kAttnUnbias, w.y * kAttnUnbias);
+                *reinterpret_cast<float2 *>(smem + C::SXOFF + (j & 3) * KT * 4 + lane * 8) = x;
+                // from kAttnSmall on, where they compare as their bits; those of new tokens' keys
+                // count for whether they lie far apart, and for the rows that see them
+                const uint32_t b0 = __float_as_uint(x.x - kAttnSmall), b1 = __float_as_uint(x.y - kAttnSmall);
+                const int n = at.ctx - k, all = n + a.T;
+                const uint32_t seen = __reduce_max_sync(0xffffffffu, max(n > 0 ? b0 : 0u, n > 1 ? b1 : 0u));
+                const uint32_t mx = __reduce_max_sync(0xffffffffu, max(all > 0 ? b0 : 0u, all > 1 ? b1 : 0u));
+                const uint32_t mn = __reduce_min_sync(0xffffffffu, min(all > 0 ? b0 : ~0u, all > 1 ? b1 : ~0u));
+                if (lane == 0) {
+                    reinterpret_cast<float *>(smem + C::SMOFF)[j & 3] = __uint_as_float(seen) + kAttnSmall;
+                    reinterpret_cast<int *>(smem + C::SMOFF)[4 + (j & 3)] = __uint_as_float(mx) - __uint_as_float(mn) > kAttnSpread;
+                }
+            }
             const int turn = vals ? 2 - dw : dw;
             decode(turn, (vals ? C::CVOFF : C::CKOFF) + (j & 1) * C::CODES, vals ? C::VOFF : C::KOFF);
-            if (!vals && dw == 1) {  // the largest value scale among keys that every row sees
-                const int k = at.tile * KT + lane * 2;
-                const float2 v = *reinterpret_cast<const float2 *>(smem + C::SVOFF + (j & 3) * KT * 4 + lane * 8);
-                // (negative scales do not count: the others compare as their bits)
-                uint32_t mx = k < at.ctx ? __float_as_uint(fmaxf(v.x, 0.f)) : 0u;
-                if (k + 1 < at.ctx) mx = max(mx, __float_as_uint(fmaxf(v.y, 0.f)));
-                mx = __reduce_max_sync(0xffffffffu, mx);
-                if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::SMOFF)[j & 3] = mx;
-            }
             publish(vals ? vfull : kfull);
             if (vals) {
                 if (j == last) break;
@@ -402,8 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         // ---------------- softmax: thread = row = TMEM lane
         const int row = threadIdx.x;
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        float m = kAttnLow, l = 0.f, f = 0.f;
-        int ve = kLowExp;                     // svref = 2^ve
+        float ref = kAttnLow, l = 0.f, f = 0.f;
         int unit = 0, which = 0;
         bool fresh = true, whole = true;      // whole: the block sees the unit from its first tile on
 #pragma unroll 1
@@ -417,20 +446,20 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             if (live) {
                 if (fresh) {
                     whole = at.tile == 0;
-                    f = reinterpret_cast<const float *>(smem + C::FOFF)[(unit & 3) * 128 + row];
-                    m = kAttnLow;
+                    f = grow < R ? reinterpret_cast<const float *>(smem + C::FOFF)[(unit & 3) * 128 + row] : 0.f;
+                    ref = kAttnLow;
                     l = 0.f;
-                    ve = kLowExp;
                 }
                 const float4 *sk = reinterpret_cast<const float4 *>(smem + C::SKOFF + (j & 3) * KT * 4);
                 const float4 *sv = reinterpret_cast<const float4 *>(smem + C::SVOFF + (j & 3) * KT * 4);
-                float svmax = reinterpret_cast<const float *>(smem + C::SMOFF)[j & 3];
+                const float4 *sx = reinterpret_cast<const float4 *>(smem + C::SXOFF + (j & 3) * KT * 4);
+                float size = reinterpret_cast<const float *>(smem + C::SMOFF)[j & 3];  // the largest that the row sees
                 uint32_t see0 = ~0u, see1 = ~0u;
                 const bool edge = at.tile * KT + KT > at.ctx;  // new tokens' keys, or the end
                 if (edge) {
                     const int tok = min(grow, R - 1) / a.G;
                     const uint8_t *tree = a.tree ? a.tree + at.b * a.tree_b + (int64_t)tok * a.tree_r : nullptr;
-                    const float *svs = reinterpret_cast<const float *>(sv);
+                    const float *sizes = reinterpret_cast<const float *>(sx);
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         const int i0 = at.tile * KT + 32 * c - at.ctx;  // index of the new token at the chunk's start
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                             if (i >= 0 && i < a.T) u = tree ? tree[i] != 0 : i <= tok;
                             if (u) {
                                 bits |= 1u << k;
-                                svmax = fmaxf(svmax, svs[32 * c + k]);
+                                size = fmaxf(size, sizes[32 * c + k]);
                             }
                         }
                         if (c) see1 = bits;
@@ -483,16 +512,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 }
-                top *= f;
-                const bool bigger = svmax > __uint_as_float((uint32_t)(ve + 127) << 23);
-                if (__any_sync(0xffffffffu, top > m + kAttnSlack || bigger)) {
-                    const float mn = top > m + kAttnSlack ? top + kAttnMargin : m;
-                    // a power of two in (2 svmax, 4 svmax]
-                    const int vn = bigger ? min(120, (int)(__float_as_uint(svmax) >> 23) - 127 + 2) : ve;
-                    const float c = ex2(m - mn + (float)(ve - vn));
-                    m = mn;
-                    ve = vn;
-                    l *= c;
+                top = top * f + size;  // no product is larger
+                if (__any_sync(0xffffffffu, grow < R && top > ref + kAttnSlack)) {
+                    if (reinterpret_cast<const volatile int *>(smem + C::SMOFF)[4 + (j & 3)])
+                        top = largest_product(scol, reinterpret_cast<const float *>(sk), reinterpret_cast<const float *>(sx), f, see0, see1);
+                    const float rn = top > ref + kAttnSlack ? top + kAttnMargin : ref;
+                    // in two steps: the sum may outlive a factor that fp32 cannot hold
+                    const float h = ex2(.5f * (ref - rn)), c2 = h * h;
+                    ref = rn;
+                    l = l * h * h;
                     if (!fresh) {
                         if (!wait(odone, j - 1)) break;  // O holds every product so far
                         tc::fence_after_sync();
@@ -502,13 +530,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                             tc::ld_32x32b_x16(lane_base + C::OCOL + h * 16, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * c2);
                             tc::st_32x32b_x16(lane_base + C::OCOL + h * 16, o);
                         }
                     }
                 }
                 // ---- weights, over S's first columns
-                const float off = kAttnUp - m - (float)ve;
+                const float off = kAttnOff - ref;
                 const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
                 float2 l2 = make_float2(0.f, 0.f), l3 = l2;
 #pragma unroll 1
@@ -552,7 +580,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 tc::fence_after_sync();
                 if (live) {
                     whole = whole && last;
-                    const float rl = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                    // O lacks the bias that l counts
+                    const float rl = whole ? (l == 0.f ? 0.f : kAttnRebias / l) : kAttnRebias;
                     const int g = min(grow, R - 1);
                     const int64_t out_row = ((int64_t)at.b * a.T + g / a.G) * a.Hq + at.hk * a.G + g % a.G;
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
@@ -577,16 +606,20 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                             } else {
                                 uint4 *dst = reinterpret_cast<uint4 *>(slot + row * D + h * 32);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                                for (int k = 0; k < 8; ++k) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__uint_as_float(o[4 * k + i]) * rl);
+                                    dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
                             }
                         }
                     }
                     if (grow < R) {
-                        // l counts in units of 2^(kAttnUp - ve), and so does O
                         if (whole) {
-                            if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m - kAttnUp + (float)ve + log2f(l)) * kLn2;
+                            if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref - kAttnOff + log2f(l)) * kLn2;
                         } else {
-                            slot[ROWS * D + row] = m - kAttnUp + (float)ve;
+                            slot[ROWS * D + row] = ref - kAttnOff;
                             slot[ROWS * (D + 1) + row] = l;
                         }
                     }

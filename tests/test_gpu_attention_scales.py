@@ -94,8 +94,8 @@ class Pool:
         assert ((lse[0].double().cpu() - l64).abs() <= lim).all(), f"{what}: lse"
 
 
-# rows per kv head: up to 8, up to 16
-FORMS = [(4, 2), (4, 1), (8, 2), (16, 1)]
+# 8 and 16 rows per kv head and the streaming kernel's single head; the tcgen05 kernel
+FORMS = [(4, 2), (4, 1), (8, 2), (16, 1), (10, 2), (24, 1), (40, 4)]
 
 
 @pytest.mark.parametrize("t,share", FORMS)
