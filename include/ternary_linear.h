@@ -277,7 +277,9 @@ tl_status ternary_rope(const void *x, int64_t x_token_stride, int64_t x_head_str
 
 typedef enum {
     TL_KV_INT8 = 0, /* two's complement -127..127                                       */
-    TL_KV_FP8 = 1,  /* e4m3 (largest 448)                                               */
+    TL_KV_FP8 = 1,  /* e4m3 (largest 448; 0x7F and 0xFF, which no append writes, are NaN:
+                       they read back as NaN and make NaN what a token that sees them
+                       computes from them -- a value that element, a key the token)     */
     TL_KV_INT4 = 2  /* two per byte, field value + 8 (1..15), the even element in the low
                        bits                                                             */
 } tl_kv_format;

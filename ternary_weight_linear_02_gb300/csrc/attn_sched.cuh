@@ -321,6 +321,31 @@ __device__ __forceinline__ uint32_t attn_group(const AttnArgs &a, int page, int 
     return ((uint32_t)page * (uint32_t)a.c.Hk + (uint32_t)hk) * (uint32_t)(a.c.P >> 4) + (uint32_t)(off >> 4);
 }
 
+// e4m3 caches: writes NaN over the elements d0 .. d0 + n - 1 of a new token's result (16-bit, or
+// fp32 where it is a part of one; written before by the same thread) where a new token that it
+// sees has a NaN code.  The products take such codes as finite, since other rows do not see them.
+// Called, and so not inlined, only where one was met.
+template <int D>
+__device__ __noinline__ void attn_put_nans(const uint8_t *codes, const int *pages, int npages, int P, int Hk, int hk, const uint8_t *tree,
+                                           int T, int tok, int ctx, int d0, int n, uint16_t *out, float *part) {
+    for (int i = 0; i < T; ++i) {
+        if (!(tree ? tree[i] != 0 : i <= tok)) continue;
+        const int pi = (ctx + i) / P, off = ctx + i - pi * P, page = pages[pi];
+        const int64_t in = (unsigned)page < (unsigned)npages ? page : 0;
+        const uint8_t *c = codes + ((in * Hk + hk) * P + off) * D;
+        for (int e = d0; e < d0 + n; ++e) {
+            if ((c[e] & 0x7F) != 0x7F) continue;
+            if (out) out[e] = 0x7FFF;  // (of either type)
+            else part[e] = __uint_as_float(0x7FC00000u);
+        }
+    }
+}
+template <int D>
+__device__ __forceinline__ void attn_put_nans(const AttnArgs &a, const AttnWalk &w, int tok, int d0, int n, void *out, float *part) {
+    attn_put_nans<D>(a.c.vc, a.pages + w.b * a.pages_stride, (int)a.c.pages, a.c.P, a.c.Hk, w.hk,
+                     a.tree ? a.tree + w.b * a.tree_b + tok * a.tree_r : nullptr, a.T, tok, w.ctx, d0, n, static_cast<uint16_t *>(out), part);
+}
+
 // 16-bit values of the call's dtype
 __device__ __forceinline__ uint32_t attn_pack(const AttnArgs &a, float lo, float hi) {
     return a.bf ? pack2(__nv_bfloat16(), lo, hi) : pack2(__half(), lo, hi);

@@ -74,17 +74,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// e4m3 for keys: NaN codes stay NaN (such a key's scores are its own)
-__device__ __forceinline__ uint32_t e4m3x2_raw(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
-        : "=r"(r)
-        : "r"(w));
-    return r;
-}
-
 template <int FMT, int D, int NB>
 struct StreamCfg {
     static constexpr int ROWS = 8 * NB;
@@ -219,6 +208,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
     float f[NB][2];                        // score factors of rows 8 n + 2t and + 1
     float ref[NB][2], l[NB][2];            // reference of the products, sum of the weights
     float acc[NB][NT][4];
+    uint32_t nans = 0;                     // e4m3: a new token's values hold a NaN code
     bool fresh = true, whole = true;       // the next tile begins a unit (for this block); the unit from its start
     int which = 0, get = 0;                // slot of a partial result; stage being read
 
@@ -333,8 +323,8 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                             x[n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4140));
                             x[2 + n] = int8_f16x2(__byte_perm(u, 0x64646464u, 0x4342));
                         } else {
-                            x[n] = e4m3x2_raw(w[n][i]);
-                            x[2 + n] = e4m3x2_raw(w[n][i] >> 16);
+                            x[n] = e4m3x2_f16x2(w[n][i]);
+                            x[2 + n] = e4m3x2_f16x2(w[n][i] >> 16);
                         }
                     }
 #pragma unroll
@@ -357,7 +347,8 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     for (int j = 0; j < 4; ++j) z[gr][n][j] = s[n][j] * sk[j >> 1] * f[n][j & 1];
             }
             uint32_t unseen = 0;
-            if (key + (GR - 1) * 64 + 16 > out.ctx) {  // new tokens' keys, or the end
+            const bool edge = key + (GR - 1) * 64 + 16 > out.ctx;  // new tokens' keys, or the end
+            if (edge) {
                 const uint8_t *tree = a.tree ? a.tree + out.b * a.tree_b : nullptr;
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
@@ -445,6 +436,19 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         v[j][0] = *reinterpret_cast<const uint32_t *>(p);
                     }
                 }
+                if constexpr (FMT == kKvFp8) {
+                    if (edge) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int i0 = key + gr * 64 + 2 * t + (j & 1) + (j >> 1) * 8 - out.ctx;  // index of the new token
+                            if (i0 < 0) continue;
+                            uint32_t met = 0;
+#pragma unroll
+                            for (int i = 0; i < C::VB / 4; ++i) v[j][i] = e4m3_finite(v[j][i], met);
+                            if (i0 < a.T) nans |= met;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < C::VB / 4; ++i) {
 #pragma unroll
@@ -502,7 +506,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         wl[warp * ROWS + 8 * n + 2 * t + r] = l[n][r];
                     }
                 }
-            __syncthreads();
+            bool nan_seen = false;
+            if constexpr (FMT == kKvFp8) nan_seen = __syncthreads_or(nans != 0), nans = 0;
+            else __syncthreads();
             float *jb = reinterpret_cast<float *>(smem + C::JOFF);
             float c[NB][2];
 #pragma unroll
@@ -556,6 +562,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + out_row * D + part * EPT);
 #pragma unroll
                     for (int e = 0; e < EPT; e += 2) o[e / 2] = attn_pack(a, v[e] * rl, v[e + 1] * rl);
+                    if (FMT == kKvFp8 && nan_seen) attn_put_nans<D>(a, out, row / a.G, part * EPT, EPT, o - part * (EPT / 2), nullptr);
                     if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnOff + log2f(Ls)) * kLn2;
                 } else {
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
@@ -563,6 +570,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
                     for (int e = 0; e < EPT; e += 4)
                         *reinterpret_cast<float4 *>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    if (FMT == kKvFp8 && nan_seen) attn_put_nans<D>(a, out, row / a.G, part * EPT, EPT, nullptr, slot + row * D);
                     if (part == 0) {
                         slot[ROWS * D + row] = M - kAttnOff;
                         slot[ROWS * (D + 1) + row] = Ls;

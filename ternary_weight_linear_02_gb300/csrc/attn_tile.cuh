@@ -68,7 +68,8 @@ struct AttnTileCfg {
     static constexpr int SKOFF = CVOFF + 2 * CODES, SVOFF = SKOFF + 4 * kTileKeys * 4;
     static constexpr int SXOFF = SVOFF + 4 * kTileKeys * 4;  // sizes of the value scales, as them
     static constexpr int SMOFF = SXOFF + 4 * kTileKeys * 4;  // largest of committed keys [4], far apart? [4]
-    static constexpr int FOFF = SMOFF + 32;               // row factors [4][128]
+    static constexpr int NOFF = SMOFF + 32;               // units with NaN codes among new values [4]
+    static constexpr int FOFF = NOFF + 16;                // row factors [4][128]
     static constexpr int BOFF = FOFF + 4 * 512;           // barriers, TMEM slot, abort flag
     static constexpr int POFF = BOFF + 128;               // place of the run (10 words)
     static constexpr int SMEM = POFF + 80 + 1024;         // 1 KB of alignment slack
@@ -130,6 +131,24 @@ __device__ __noinline__ float largest_product(uint32_t scol, const float *sk, co
     return top;
 }
 
+// Makes the e4m3 codes finite that a thread decodes of a tile's staged values (16 bytes at `codes`
+// of row r0 and every STEP-th after it), from row `held` on: the new tokens' and what lies beyond.
+// Whether a new token's held a NaN.  Not inlined: it is for the last tiles of a unit alone.
+template <int STEP, int RB>
+__device__ __noinline__ bool finite_rows(uint8_t *codes, int r0, int held, int T) {
+    uint32_t nans = 0;
+    for (int r = r0; r < kTileKeys; r += STEP, codes += STEP * RB) {
+        if (r < held) continue;
+        uint4 *const p = reinterpret_cast<uint4 *>(codes);
+        uint4 w = *p;
+        uint32_t met = 0;
+        w.x = e4m3_finite(w.x, met), w.y = e4m3_finite(w.y, met), w.z = e4m3_finite(w.z, met), w.w = e4m3_finite(w.w, met);
+        if (met) *p = w;
+        if (r - held < T) nans |= met;
+    }
+    return nans != 0;
+}
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, int rtiles) {
     using C = AttnTileCfg<FMT, D>;
@@ -160,6 +179,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         mbar_init(vfull, 3);
         mbar_init(fin, 1);
         *abort_flag = 0;
+        *reinterpret_cast<int4 *>(smem + C::NOFF) = make_int4(0, 0, 0, 0);
         fence_barrier_init();
     }
     AttnWalk at;
@@ -386,14 +406,18 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         // Turns of a tile's keys and the values of the tile before, so that the scores are computed
         // first; one copy of the code serves both.
         bool fresh = true;  // `at` begins a unit
+        int held = 0, held1 = 0, unit1 = 0;  // committed keys of the keys' tile, and of the values'; the latter's unit
 #pragma unroll 1
         for (int i = 0, last = INT_MAX;; ++i) {
             const int j = (i >> 1) - (i & 1);  // keys of tiles 0 1 2 .., values of tiles -1 0 1 ..
             const bool vals = i & 1;
             if (vals) {
                 if (j < 0) continue;
-            } else if (j > last) {
-                continue;
+            } else {
+                held1 = held;
+                unit1 = unit;
+                if (j > last) continue;
+                held = at.ctx - at.tile * KT;
             }
             uint64_t *const from = vals ? cvfull : ckfull, *const gone = vals ? odone : sdone;
             // the codes have landed, and what was made of the tile before has been read
@@ -418,6 +442,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 }
             }
             const int turn = vals ? 2 - dw : dw;
+            if (FMT == kKvFp8 && vals && held1 < KT) {  // new tokens' values
+                const int r0 = turn * C::RPP + rin;
+                if (finite_rows<3 * C::RPP, C::RB>(smem + C::CVOFF + (j & 1) * C::CODES + r0 * C::RB + cu * C::UB, r0, held1, a.T))
+                    reinterpret_cast<volatile int *>(smem + C::NOFF)[unit1 & 3] = unit1;  // (counted from 1 here)
+            }
             decode(turn, (vals ? C::CVOFF : C::CKOFF) + (j & 1) * C::CODES, vals ? C::VOFF : C::KOFF);
             publish(vals ? vfull : kfull);
             if (vals) {
@@ -616,6 +645,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         }
                     }
                     if (grow < R) {
+                        if (FMT == kKvFp8 && reinterpret_cast<volatile int *>(smem + C::NOFF)[(unit + 1) & 3] == unit + 1)
+                            attn_put_nans<D>(a, at, g / a.G, 0, D, whole ? static_cast<uint16_t *>(a.out) + out_row * D : nullptr, slot + row * D);
                         if (whole) {
                             if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref - kAttnOff + log2f(l)) * kLn2;
                         } else {

@@ -21,9 +21,8 @@ struct KvCode {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 h2_of(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 
-// two e4m3 bytes (the low 16 bits of w) as f16x2; finite for every bit pattern: the
-// two NaN patterns, which no append writes but an unwritten page may hold, become
-// the largest value, so that a code whose weight is 0 contributes 0
+// two e4m3 bytes (the low 16 bits of w) as f16x2; the two NaN patterns, which no append writes
+// but a caller or an unwritten page may hold, stay NaN
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
     uint32_t r;
     asm("{\n\t.reg .b16 l, h;\n\t"
@@ -31,7 +30,15 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
         : "=r"(r)
         : "r"(w));
-    return h2_bits(__hmin2(h2_of(r), __float2half2_rn(448.f)));
+    return r;
+}
+
+// Four e4m3 bytes with the NaN patterns turned into the largest value, for values that some rows
+// of a block do not see: with a weight of 0 they contribute 0.  found: not 0 after any.
+__device__ __forceinline__ uint32_t e4m3_finite(uint32_t w, uint32_t &found) {
+    const uint32_t n = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    found |= n;
+    return w ^ (n >> 7);
 }
 
 // Two int8 bytes already moved to the low byte of each half and offset by 128
