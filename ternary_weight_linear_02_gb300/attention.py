@@ -244,7 +244,8 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         t_rows, rot = _table(table)
         if positions is None:
             raise ValueError("a table needs positions")
-        tp, pp = table.data_ptr(), _index(positions, "positions", torch.int64, n).data_ptr()
+        positions = _index(positions, "positions", torch.int64, n)  # (a copy lives until the call)
+        tp, pp = table.data_ptr(), positions.data_ptr()
     else:
         if q is not None or interleaved:
             raise ValueError("q and interleaved need a table")
