@@ -24,6 +24,7 @@
 // if the unit is the first of its run, else in slot 1 (it is then the last).
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -65,6 +66,20 @@ __device__ __forceinline__ float lg2(float x) {
 }
 // x_j of a value scale; finite for every bit pattern
 __device__ __forceinline__ float attn_size(float sv) { return fminf(fmaxf(lg2(fabsf(sv)), kAttnSmall), 128.f); }
+
+// Allows a kernel `bytes` of dynamic shared memory on the current device.  `done`, one per kernel,
+// remembers the devices where that has succeeded (the call costs a microsecond of the host's time).
+template <typename K>
+cudaError_t attn_allow_smem(std::atomic<uint64_t> &done, K *kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Keys of sequence b, clamped to its page-table row.
 __device__ __forceinline__ int attn_context(const AttnArgs &a, int b) {

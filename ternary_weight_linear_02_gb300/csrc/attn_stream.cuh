@@ -589,12 +589,12 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 template <int FMT, int D, int NB>
 cudaError_t launch_stream_d(const AttnArgs &a, int sms, cudaStream_t st) {
     using C = StreamCfg<FMT, D, NB>;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        attn_stream_kernel<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (attr != cudaSuccess) return attr;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = attn_allow_smem(allowed, attn_stream_kernel<FMT, D, NB>, C::SMEM);
+    if (e != cudaSuccess) return e;
     const int nc = a.direct ? a.B * a.c.Hk : sms * C::BLOCKS;
     attn_stream_kernel<FMT, D, NB><<<nc, kStreamThreads, C::SMEM, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess || a.direct) return e;
     return launch_join<StreamTiling<C::GR>, C::ROWS, D>(a, 1, nc, st);
 }

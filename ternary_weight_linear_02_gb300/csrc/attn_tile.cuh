@@ -681,12 +681,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
 template <int FMT, int D>
 cudaError_t launch_tile_d(const AttnArgs &a, int sms, cudaStream_t st) {
     using C = AttnTileCfg<FMT, D>;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(attn_tile_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::REQ);
-    if (attr != cudaSuccess) return attr;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = attn_allow_smem(allowed, attn_tile_kernel<FMT, D>, C::REQ);
+    if (e != cudaSuccess) return e;
     const int rtiles = (a.T * a.G + kTileRows - 1) / kTileRows, nc = a.direct ? a.B * a.c.Hk * rtiles : sms * 2;
     attn_tile_kernel<FMT, D><<<nc, kTileThreads, C::REQ, st>>>(a, rtiles);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess || a.direct) return e;
     return launch_join<TileTiling, kTileRows, D>(a, rtiles, nc, st);
 }
