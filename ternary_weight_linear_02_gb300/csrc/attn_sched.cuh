@@ -81,6 +81,20 @@ cudaError_t attn_allow_smem(std::atomic<uint64_t> &done, K *kernel, int bytes) {
     return e;
 }
 
+// bf16 queries enter the product as f16, a row scaled by the power of two that takes its largest
+// element to [2^15, 2^16): exact for elements down to 2^-32 of it (a bf16 has 8 bits), below that
+// rounded at 2^-40 of it.  `e`: biased exponent of the largest, 255 for a row with an infinity or a
+// NaN, which stays as it is.  Rows below 2^-95 take the scale of those at 2^-95; f16 holds all
+// their bits.
+struct QueryScale {
+    float down, up;
+    __device__ __forceinline__ explicit QueryScale(uint32_t e) {
+        const uint32_t c = max(e, 32u);
+        down = e == 255u ? 1.f : __uint_as_float((269u - c) << 23);
+        up = e == 255u ? 1.f : __uint_as_float((c - 15u) << 23);
+    }
+};
+
 // Keys of sequence b, clamped to its page-table row.
 __device__ __forceinline__ int attn_context(const AttnArgs &a, int b) {
     const int c = a.ctx[b], most = (int)(a.max_keys - a.T);

@@ -18,8 +18,7 @@
 //    over a quad or eight lanes.
 //  * P changes from (keys x rows) to (rows x keys) fragments by one movmatrix per 8 keys.
 //  * codes become f16 (exact); the products are exact, sums fp32.  Queries in bf16
-//    enter as f16 scaled by the power of two of their row's largest element: exact
-//    within 2^-14 of it, below that rounded at 2^-25 of it, far under the fp32 sums.
+//    enter as f16 scaled by a power of two per row (QueryScale in attn_sched.cuh).
 //  * P is rounded to f16 (2^-11 relative) with its value scale in it, kept so far up that
 //    products down to 2^-24 of a row's largest keep all 11 bits.  A row's reference is that of
 //    its own products (kAttnTop in attn_sched.cuh), so neither a key of a negligible weight
@@ -233,11 +232,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                 for (int i = 0; i < EPT; ++i) mx = fmaxf(mx, fabsf(v[i]));
 #pragma unroll
                 for (int o = TPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const int e = (int)(__float_as_uint(mx) >> 23);  // biased exponent of the largest
-                if (e > 0 && e < 254) {
-                    down = __uint_as_float((uint32_t)(254 - e) << 23);
-                    up = __uint_as_float((uint32_t)e << 23);
-                }
+                const QueryScale by(__float_as_uint(mx) >> 23);
+                down = by.down;
+                up = by.up;
             }
             __half *qs = reinterpret_cast<__half *>(smem + C::JOFF) + row * (D + 8) + part * EPT;
 #pragma unroll
@@ -344,7 +341,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) z[gr][n][j] = s[n][j] * sk[j >> 1] * f[n][j & 1];
+                    for (int j = 0; j < 4; ++j) z[gr][n][j] = s[n][j] * (sk[j >> 1] * f[n][j & 1]);
             }
             uint32_t unseen = 0;
             const bool edge = key + (GR - 1) * 64 + 16 > out.ctx;  // new tokens' keys, or the end

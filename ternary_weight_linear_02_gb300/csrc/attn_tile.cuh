@@ -12,8 +12,8 @@
 //    softmax of this one, and O += P V with P from TMEM.
 //  * Warps 5-7 decode codes to f16 (exact) in 128-byte-swizzled rows, keys and values alike:
 //    keys are read as a K-major operand, values as an MN-major one, so neither is
-//    transposed.  They also place the queries at a unit's start (f16; from bf16 scaled by
-//    the power of two of the row's largest element).  Codes that came through registers
+//    transposed.  They also place the queries at a unit's start (f16; bf16 scaled by a power
+//    of two per row, QueryScale in attn_sched.cuh).  Codes that came through registers
 //    instead, a tile ahead, were waited for with every other load of their warp
 //    (page table, scales): 5000 cycles a tile against 3500.
 //  * Warps 0-3: a row's 64 scores are read in halves, for the maximum and then for the
@@ -37,6 +37,7 @@
 // block stops issuing work, frees its TMEM and returns.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "attn_sched.cuh"
@@ -376,12 +377,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mx = max(mx, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
                         mx = __reduce_max_sync(((1u << QL) - 1u) << (lane & ~(QL - 1)), mx);  // the row's lanes
-                        const uint32_t e = mx >> 7;  // biased exponent of the largest
-                        float down = 1.f;
-                        if (e > 0 && e < 254) {
-                            down = __uint_as_float((254 - e) << 23);
-                            up = __uint_as_float(e << 23);
-                        }
+                        const QueryScale by(mx >> 7);
+                        const float down = by.down;
+                        up = by.up;
                         uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -392,7 +390,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                     h = mma_order<FMT>(h);
                     *reinterpret_cast<uint4 *>(smem + C::QOFF + (c >> 3) * C::QBLOCK + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = h;
-                    if (c == 0) fac[r] = a.scale * kLog2e * up;
+                    if (c == 0) fac[r] = fmaxf(a.scale * kLog2e * up, FLT_MIN);  // (0 would meet infinities)
                 }
             }
         };
