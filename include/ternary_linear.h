@@ -431,13 +431,14 @@ int32_t ternary_version(void);
  * error handling above the ABI be exercised without a GPU fault. */
 void ternary_test_inject_launch_failures(int32_t n);
 
-/* Testing aid: the give-up time, in SM clock cycles, of the decode kernel's
- * main-loop waits for every later launch (cycles <= 0 restores the default of
- * about 2^30 cycles, ~0.5 s).  stall != 0 additionally makes each of those
- * launches first wait on a barrier that nothing arrives on, so the wait runs
- * out: the call then writes no output and sets the device status word to
+/* Testing aid: the give-up time, in SM clock cycles, of the main-loop waits of the
+ * decode kernel and of the tcgen05 attention kernel for every later launch
+ * (cycles <= 0 restores the default of about 2^30 cycles, ~0.5 s).  stall != 0
+ * additionally makes each of those launches first wait on a barrier that nothing
+ * arrives on, so the wait runs out: the call then writes no output (attention:
+ * NaN where partial results were to be joined) and sets the device status word to
  * TL_ERR_TIMEOUT, while every copy in flight still lands before the kernel
- * exits (those waits keep the default limit).  Lets the give-up path be tested
+ * exits (those waits have limits of their own).  Lets the give-up path be tested
  * without a fault or a hang. */
 void ternary_test_set_wait_limit(int64_t cycles, int32_t stall);
 

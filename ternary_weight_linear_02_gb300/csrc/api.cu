@@ -25,7 +25,8 @@ struct DevInfo {
 std::mutex g_mu;
 DevInfo g_dev[kMaxDevices];
 std::atomic<int> g_inject_launch_failures{0};
-// testing aids for the decode kernel's bounded waits (ternary_test_set_wait_limit)
+// testing aids for the bounded waits of the decode and the tcgen05 attention kernel
+// (ternary_test_set_wait_limit)
 std::atomic<long long> g_wait_limit{0};  // 0 = the default (~0.5 s)
 std::atomic<int> g_stall{0};
 // testing aid: the tile kernel's form (ternary_test_set_tile_mode): 0 = chosen
@@ -446,6 +447,8 @@ int tl::begin_call(CallDevice *out) {
     if (s != TL_OK) return s;
     out->sm_count = d->sm_count;
     out->status = d->status;
+    out->wait_limit = wait_limit();
+    out->stall = g_stall.load() != 0;
     return TL_OK;
 }
 

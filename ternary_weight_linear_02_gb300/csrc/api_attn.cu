@@ -264,6 +264,8 @@ tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t 
     a.G = q_heads / a.c.Hk;
     a.q_vec = rows16(q, q_token_stride, q_head_stride, 2) && (q_batch_stride * 2) % 16 == 0;
     a.status = d.status;
+    a.wait_limit = d.wait_limit;
+    a.stall = d.stall;
     a.bf = dtype == TL_BF16;
     return from_cuda(tl::launch_tree_attention(a, d.sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -33,8 +33,9 @@
 // the time but slowed the softmax by more.
 // Softmax warps without a row that decode too (23 rows: three more) were slower: 99 us
 // against 90 (fp8).
-// Every mbarrier wait is bounded; one that gives up sets the device status word, and the
-// block stops issuing work, frees its TMEM and returns.
+// Every mbarrier wait is bounded and answered alike in all lanes of a warp; one that gives up
+// sets the device status word, and the block stops issuing work, lets its copies and products
+// in flight end, makes the partial results it owes NaN, frees its TMEM and returns.
 #pragma once
 
 #include <cfloat>
@@ -132,6 +133,19 @@ __device__ __noinline__ float largest_product(uint32_t scol, const float *sk, co
     return top;
 }
 
+// The rest of a wait that has not succeeded at once, by a whole warp: all lanes see the phase
+// complete, or all give up (a warp may not part before its tcgen05 instructions).
+__device__ __noinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, long long limit) {
+    const long long t0 = clock64();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 200u))) return true;
+        if (__any_sync(0xffffffffu, *abort_flag || clock64() - t0 > limit)) break;
+    }
+    *abort_flag = 1;
+    if (status && (threadIdx.x & 31) == 0) atomicExch(status, kStatusTimeout);
+    return false;
+}
+
 // Makes the e4m3 codes finite that a thread decodes of a tile's staged values (16 bytes at `codes`
 // of row r0 and every STEP-th after it), from row `held` on: the new tokens' and what lies beyond.
 // Whether a new token's held a NaN.  Not inlined: it is for the last tiles of a unit alone.
@@ -164,6 +178,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     uint64_t *kfull = bars + 10, *vfull = bars + 11;
     uint64_t *fin = bars + 12;  // after a give-up: every product issued has ended
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
+    uint64_t *never = bars + 14;  // nothing arrives on it (testing aid)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = a.T * a.G;
@@ -179,6 +194,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         mbar_init(kfull, 3);  // one per decoder warp
         mbar_init(vfull, 3);
         mbar_init(fin, 1);
+        mbar_init(never, 1);
         *abort_flag = 0;
         *reinterpret_cast<int4 *>(smem + C::NOFF) = make_int4(0, 0, 0, 0);
         fence_barrier_init();
@@ -196,11 +212,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
     pdl_launch_dependents();
 
     auto wait_phase = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (!*abort_flag && mbar_wait_bounded(bar, parity)) return true;
-        *abort_flag = 1;
-        if (a.status) atomicExch(a.status, kStatusTimeout);
-        return false;
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_or_give_up(bar, parity, abort_flag, a.status, a.wait_limit);
     };
     auto wait = [&](uint64_t *pair, int j) -> bool { return wait_phase(pair + (j & 1), (uint32_t)(j >> 1) & 1u); };
     auto wait1 = [&](uint64_t *bar, int j) -> bool { return wait_phase(bar, (uint32_t)j & 1u); };
@@ -462,6 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
         float ref = kAttnLow, l = 0.f, f = 0.f;
         int unit = 0, which = 0;
         bool fresh = true, whole = true;      // whole: the block sees the unit from its first tile on
+        if (a.stall && !wait_or_give_up(never, 0, abort_flag, a.status, a.wait_limit)) at.end = at.at;
 #pragma unroll 1
         for (int j = 0; at.inside(); ++j) {
             const int grow = at.rt * ROWS + row;
@@ -670,6 +683,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
             if (tc::elect_one()) tc::commit(fin);
             __syncwarp();
             mbar_wait_bounded(fin, 0);
+            if (!a.direct)
+                for (int i = lane; i < 2 * ROWS; i += 32)
+                    AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, i / ROWS)[ROWS * (D + 1) + i % ROWS] = __uint_as_float(0x7FC00000u);
         }
         __syncwarp();
         tc::tmem_dealloc(tmem, C::COLS);

@@ -11,7 +11,9 @@ namespace tl {
 // ------------------------------------------------------------ shared by the ABI files
 struct CallDevice {
     int sm_count;
-    int *status;  // device status word
+    int *status;           // device status word
+    long long wait_limit;  // give-up time of bounded waits, SM cycles
+    bool stall;            // testing aid: wait on a barrier that nothing arrives on
 };
 int begin_call(CallDevice *out);  // a tl_status (api.cu)
 
@@ -270,6 +272,8 @@ struct AttnArgs {
     int q_vec;           // every q row starts on a 16-byte boundary
     int bf;              // q and out are bf16 (else fp16)
     int direct;          // a block per unit (attn_sched.cuh), no workspace
+    int stall;           // testing aid (CallDevice)
+    long long wait_limit;
     int *status;
 };
 // SMs that a workspace is laid out for (the GPU has 152; more are left unused)
