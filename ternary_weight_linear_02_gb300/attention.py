@@ -38,18 +38,39 @@ def _stream(dev: torch.device) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _index(t: torch.Tensor, what: str, dtype: torch.dtype, n: int) -> torch.Tensor:
-    if t.dtype is not dtype or t.shape != (n,):
-        raise ValueError(f"{what} must be a 1-D {dtype} tensor of {n} elements")
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _launch(dev: torch.device, f, *args) -> int:
+    """f(*args, stream) on dev, whichever device is the current one."""
+    if dev.index == _current_device():
+        return f(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, _stream(dev))
+
+
+def _cuda(t: torch.Tensor, what: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a CUDA device (no CPU path)")
+    return t.device
+
+
+def _same(t: torch.Tensor, what: str, dev: torch.device):
+    if t.device != dev:
+        _cuda(t, what)
+        raise ValueError(f"{what} must be on {dev} like the call's other tensors: it is on {t.device}")
+
+
+def _index(t: torch.Tensor, what: str, dtype: torch.dtype, n: int, dev: torch.device) -> torch.Tensor:
+    if t.dtype is not dtype or t.shape != (n,):
+        raise ValueError(f"{what} must be a 1-D {dtype} tensor of {n} elements")
+    _same(t, what, dev)
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _rows(t: torch.Tensor, what: str) -> tuple[torch.Tensor, tuple]:
+def _rows(t: torch.Tensor, what: str, dev: torch.device) -> tuple[torch.Tensor, tuple]:
     """The tensor with a dense last axis, and its strides."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on a CUDA device (no CPU path)")
+    _same(t, what, dev)
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] != 1:
         t = t.contiguous()
@@ -64,11 +85,10 @@ def _out(out: torch.Tensor, like: torch.Tensor, what: str) -> tuple:
     return st
 
 
-def _table(table: torch.Tensor) -> tuple[int, int]:
+def _table(table: torch.Tensor, dev: torch.device) -> tuple[int, int]:
     if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous fp32 tensor [positions, rotary_dim] (rope_table)")
-    if not table.is_cuda:
-        raise ValueError("table must be on a CUDA device (no CPU path)")
+    _same(table, "table", dev)
     return table.shape
 
 
@@ -93,7 +113,7 @@ class KVCache:
     """
 
     __slots__ = ("format", "k_codes", "v_codes", "k_scale", "v_scale", "pages", "kv_heads", "page_size",
-                 "head_dim", "_c", "_ref")
+                 "head_dim", "device", "_c", "_ref")
 
     def __init__(self, format: str, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
@@ -114,6 +134,7 @@ class KVCache:
                 raise ValueError("the cache's tensors must be on one device")
         self.format = format
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.device = k_codes.device
         self.pages, self.kv_heads, self.page_size, row = k_codes.shape
         self.head_dim = 2 * row if format == "int4" else row
         if self.head_dim not in (64, 128):
@@ -182,9 +203,9 @@ def rope_table(positions: int, rotary_dim: int, *, base: float = 10000.0, factor
     if positions < 0 or rotary_dim < 0:
         raise ValueError("positions and rotary_dim must not be negative")
     out = torch.empty((int(positions), int(rotary_dim)), dtype=torch.float32, device=dev)
-    _check(_lib().ternary_rope_table(out.data_ptr(), int(positions), int(rotary_dim), float(base),
-                                     float(factor), float(original_len), float(ramp[0]), float(ramp[1]),
-                                     float(magnitude), _stream(out.device)), "ternary_rope_table")
+    _check(_launch(out.device, _lib().ternary_rope_table, out.data_ptr(), int(positions), int(rotary_dim),
+                   float(base), float(factor), float(original_len), float(ramp[0]), float(ramp[1]),
+                   float(magnitude)), "ternary_rope_table")
     return out
 
 
@@ -198,20 +219,21 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, *, inter
     dt = _DT.get(x.dtype)
     if dt is None or x.dim() != 3:
         raise ValueError("x must be [tokens, heads, head_dim] in fp16, bf16 or fp32")
-    x, xs = _rows(x, "x")
+    dev = _cuda(x, "x")
+    x, xs = _rows(x, "x", dev)
     shape = x.shape
     n, heads, dim = shape
-    positions = _index(positions, "positions", torch.int64, n)
-    t_rows, rot = _table(table)
+    positions = _index(positions, "positions", torch.int64, n, dev)
+    t_rows, rot = _table(table, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
         ot, oh = heads * dim, dim
     else:
         ot, oh, _ = _out(out, x, "out")
-    rc = (_ready or _lib()).ternary_rope(
-        x.data_ptr(), xs[0], xs[1], out.data_ptr(), ot, oh, dt, n, heads, dim, positions.data_ptr(),
-        table.data_ptr(), t_rows, rot, (_INTERLEAVED if interleaved else 0) | (_INVERSE if inverse else 0),
-        _stream(x.device))
+    rc = _launch(
+        dev, (_ready or _lib()).ternary_rope, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ot, oh, dt, n, heads, dim,
+        positions.data_ptr(), table.data_ptr(), t_rows, rot,
+        (_INTERLEAVED if interleaved else 0) | (_INVERSE if inverse else 0))
     if rc:
         _check(rc, "ternary_rope")
     return out
@@ -236,15 +258,15 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     if shape != (n, cache.kv_heads, cache.head_dim) or v.shape != shape:
         raise ValueError(f"k and v must be [tokens, {cache.kv_heads}, {cache.head_dim}]: "
                          f"got {tuple(shape)} and {tuple(v.shape)}")
-    k, ks = _rows(k, "k")
-    v, vs = _rows(v, "v")
-    slots = _index(slots, "slots", torch.int64, n)
-    dev = k.device
+    dev = cache.device
+    k, ks = _rows(k, "k", dev)
+    v, vs = _rows(v, "v", dev)
+    slots = _index(slots, "slots", torch.int64, n, dev)
     if table is not None:
-        t_rows, rot = _table(table)
+        t_rows, rot = _table(table, dev)
         if positions is None:
             raise ValueError("a table needs positions")
-        positions = _index(positions, "positions", torch.int64, n)  # (a copy lives until the call)
+        positions = _index(positions, "positions", torch.int64, n, dev)  # (a copy lives until the call)
         tp, pp = table.data_ptr(), positions.data_ptr()
     else:
         if q is not None or interleaved:
@@ -255,22 +277,23 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         qshape = q.shape
         if q.dtype is not dtype or len(qshape) != 3 or qshape[0] != n or qshape[2] != cache.head_dim:
             raise ValueError("q must be [tokens, q_heads, head_dim] in k's dtype")
-        q, qs = _rows(q, "q")
+        q, qs = _rows(q, "q", dev)
         if q_out is None:
             q_out = torch.empty(qshape, dtype=dtype, device=dev)
             ot, oh = qshape[1] * qshape[2], qshape[2]
         else:
             ot, oh, _ = _out(q_out, q, "q_out")
-        rc = (_ready or _lib()).ternary_kv_append(
-            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, n, slots.data_ptr(),
-            q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), ot, oh, qshape[1], pp, tp, t_rows, rot,
-            _INTERLEAVED if interleaved else 0, _stream(dev))
+        rc = _launch(
+            dev, (_ready or _lib()).ternary_kv_append, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+            vs[1], dt, n, slots.data_ptr(), q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), ot, oh, qshape[1], pp, tp,
+            t_rows, rot, _INTERLEAVED if interleaved else 0)
     else:
         if q_out is not None:
             raise ValueError("q_out needs q")
-        rc = (_ready or _lib()).ternary_kv_append(
-            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, n, slots.data_ptr(),
-            None, 0, 0, None, 0, 0, 0, pp, tp, t_rows, rot, _INTERLEAVED if interleaved else 0, _stream(dev))
+        rc = _launch(
+            dev, (_ready or _lib()).ternary_kv_append, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+            vs[1], dt, n, slots.data_ptr(), None, 0, 0, None, 0, 0, 0, pp, tp, t_rows, rot,
+            _INTERLEAVED if interleaved else 0)
     if rc:
         _check(rc, "ternary_kv_append")
     return q_out
@@ -284,13 +307,12 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bflo
     if dt is None:
         raise ValueError("dtype must be fp16, bf16 or fp32")
     n = slots.shape[0] if slots.dim() == 1 else -1
-    slots = _index(slots, "slots", torch.int64, n)
-    dev = slots.device
+    dev = cache.device
+    slots = _index(slots, "slots", torch.int64, n, dev)
     shape = (n, cache.kv_heads, cache.head_dim)
     k = torch.empty(shape, dtype=dtype, device=dev)
     v = torch.empty(shape, dtype=dtype, device=dev)
-    rc = (_ready or _lib()).ternary_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
-                                            _stream(dev))
+    rc = _launch(dev, (_ready or _lib()).ternary_kv_read, cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt)
     if rc:
         _check(rc, "ternary_kv_read")
     return k, v
@@ -316,33 +338,33 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
     dt = _DT.get(dtype)
     if dt is None or dt == TL_F32 or q.dim() != 4:
         raise ValueError("q must be [batch, draft, q_heads, head_dim] in fp16 or bf16")
-    q, qs = _rows(q, "q")
+    dev = cache.device
+    q, qs = _rows(q, "q", dev)
     shape = q.shape
     b, t, heads, dim = shape
     if dim != cache.head_dim or heads % cache.kv_heads:
         raise ValueError("q must be [batch, draft, a multiple of kv_heads, head_dim]")
     pshape = page_table.shape
-    if page_table.dtype is not torch.int32 or len(pshape) != 2 or pshape[0] != b or not page_table.is_cuda:
-        raise ValueError("page_table must be int32 [batch, max_pages] on a CUDA device")
+    if page_table.dtype is not torch.int32 or len(pshape) != 2 or pshape[0] != b:
+        raise ValueError("page_table must be int32 [batch, max_pages]")
+    _same(page_table, "page_table", dev)
     pstride = page_table.stride()
     if pstride[1] != 1:
         page_table = page_table.contiguous()
         pstride = page_table.stride()
-    context_len = _index(context_len, "context_len", torch.int32, b)
+    context_len = _index(context_len, "context_len", torch.int32, b, dev)
     tp, tb, tr = None, 0, 0
     if tree is not None:
         tshape = tree.shape
         if (tree.dtype is not torch.bool and tree.dtype is not torch.uint8) or not (
                 tshape == (b, t, t) or tshape == (t, t) or tshape == (1, t, t)):
             raise ValueError("tree must be bool or uint8 [draft, draft] or [batch, draft, draft]")
-        if not tree.is_cuda:
-            raise ValueError("tree must be on a CUDA device (no CPU path)")
+        _same(tree, "tree", dev)
         if tree.stride(-1) != 1:
             tree = tree.contiguous()
         ts = tree.stride()
         tp, tr = tree.data_ptr(), ts[-2]
         tb = ts[0] if len(tshape) == 3 and tshape[0] > 1 else 0
-    dev = q.device
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
     elif out.shape != shape or out.dtype is not dtype or out.device != dev or not out.is_contiguous():
@@ -354,10 +376,11 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
     if need is None:
         need = _ws_bytes[key] = int(lib.ternary_tree_attention_workspace(*key))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    rc = lib.ternary_tree_attention(
-        q.data_ptr(), qs[0], qs[1], qs[2], dt, b, t, heads, cache._ref, page_table.data_ptr(), pstride[0], pshape[1],
-        context_len.data_ptr(), tp, tb, tr, dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), max(need, 0), _stream(dev))
+    rc = _launch(
+        dev, lib.ternary_tree_attention, q.data_ptr(), qs[0], qs[1], qs[2], dt, b, t, heads, cache._ref,
+        page_table.data_ptr(), pstride[0], pshape[1], context_len.data_ptr(), tp, tb, tr,
+        dim ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), max(need, 0))
     if rc:
         _check(rc, "ternary_tree_attention")
     return (out, lse) if return_lse else out

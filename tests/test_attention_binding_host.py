@@ -48,6 +48,20 @@ class Fake:
 
 
 GONE = set()
+HERE = [0]  # the current device
+
+
+class On:
+    """torch.cuda.device for the stand-ins."""
+
+    def __init__(self, dev):
+        self.index = torch.device(dev).index
+
+    def __enter__(self):
+        HERE.append(self.index)
+
+    def __exit__(self, *exc):
+        HERE.pop()
 
 
 class Library:
@@ -60,6 +74,7 @@ class Library:
             gone = [a for a in args if isinstance(a, int) and a in GONE]
             assert not gone, f"{name} was given the address of a copy that is no longer held"
             self.calls.append(name)
+            self.where = (HERE[-1], args[-1])  # current device, stream
             return 0
         return call
 
@@ -69,7 +84,9 @@ def lib(monkeypatch):
     GONE.clear()
     lib = Library()
     monkeypatch.setattr(attention, "_ready", lib)
-    monkeypatch.setattr(attention, "_stream", lambda dev: 0)
+    monkeypatch.setattr(attention, "_stream", lambda dev: 1000 + dev.index)
+    monkeypatch.setattr(attention, "_current_device", lambda: HERE[-1], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", On)
     monkeypatch.setattr(attention, "_ws_bytes", {})
     return lib
 
@@ -89,6 +106,7 @@ def append(lib, **kw):
 
 
 def rope(lib, **kw):
+    kw.pop("cache", None)
     a = dict(x=Fake(3, 8, 64), positions=Fake(3, dtype=torch.int64), table=Fake(9, 64, dtype=torch.float32), out=Fake(3, 8, 64))
     a.update(kw)
     return tl.rope(a["x"], a["positions"], a["table"], out=a["out"])
@@ -117,3 +135,50 @@ def test_copies_live_until_the_call(lib, call, arg, shape, dtype):
     t = strided(*shape, dtype=dtype)
     call(lib, **{arg: t})
     assert len(t.copies) == 1 and lib.calls[-1].startswith("ternary_")
+
+
+ARGS = {append: dict(k=((3, 2, 64), torch.bfloat16), v=((3, 2, 64), torch.bfloat16), slots=((3,), torch.int64),
+                     q=((3, 8, 64), torch.bfloat16), positions=((3,), torch.int64), table=((9, 64), torch.float32),
+                     q_out=((3, 8, 64), torch.bfloat16)),
+        rope: dict(x=((3, 8, 64), torch.bfloat16), positions=((3,), torch.int64), table=((9, 64), torch.float32),
+                   out=((3, 8, 64), torch.bfloat16)),
+        attend: dict(q=((2, 3, 8, 64), torch.bfloat16), page_table=((2, 4), torch.int32), context_len=((2,), torch.int32),
+                     tree=((2, 3, 3), torch.bool), out=((2, 3, 8, 64), torch.bfloat16))}
+
+
+def on(call, device):
+    kw = {n: Fake(*shape, dtype=dt, device=device) for n, (shape, dt) in ARGS[call].items()}
+    return dict(kw, cache=cache(device))
+
+
+@pytest.mark.parametrize("call,arg", [(c, n) for c in ARGS for n in (*ARGS[c], "cache") if (c, n) != (rope, "cache")])
+@pytest.mark.parametrize("device", ["cuda:1", "cpu"])
+def test_a_tensor_on_another_device_is_refused(lib, call, arg, device):
+    kw = on(call, "cuda:0")
+    if arg == "cache":
+        if device == "cpu":
+            return  # refused when the cache is made
+        kw["cache"] = cache(device)
+    else:
+        shape, dt = ARGS[call][arg]
+        kw[arg] = Fake(*shape, dtype=dt, device=device)
+    with pytest.raises(ValueError):
+        call(lib, **kw)
+    assert not any(n in ("ternary_rope", "ternary_kv_append", "ternary_tree_attention") for n in lib.calls)
+
+
+def test_read_refuses_slots_on_another_device(lib):
+    for device in ("cuda:1", "cpu"):
+        with pytest.raises(ValueError):
+            tl.kv_read(cache(), Fake(3, dtype=torch.int64, device=device))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("call", list(ARGS))
+def test_the_tensors_device_is_the_current_one_during_the_call(lib, call):
+    """A kernel launched on a device's default stream runs on the current device, whose pointers
+    the tensors of another device are not."""
+    for device in (0, 1):
+        call(lib, **on(call, f"cuda:{device}"))
+        assert lib.where == (device, 1000 + device)
+        assert HERE == [0]
