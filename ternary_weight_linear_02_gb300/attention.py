@@ -318,7 +318,8 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bflo
     return k, v
 
 
-_ws_bytes: dict = {}
+_ws_bytes: dict = {}   # of the sizes met last: a server's page tables grow all the time
+_WS_SIZES = 512
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, context_len: torch.Tensor,
@@ -374,6 +375,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
     key = (b, t, heads, cache.kv_heads, dim, pshape[1] * cache.page_size)
     need = _ws_bytes.get(key)
     if need is None:
+        if len(_ws_bytes) >= _WS_SIZES:
+            _ws_bytes.clear()
         need = _ws_bytes[key] = int(lib.ternary_tree_attention_workspace(*key))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     rc = _launch(

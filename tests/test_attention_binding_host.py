@@ -1,6 +1,5 @@
 """The binding of the cache and attention calls, without a GPU: the tensors are stand-ins with
 addresses of their own, the library one that records its calls."""
-import gc
 import weakref
 
 import pytest
@@ -70,7 +69,6 @@ class Library:
 
     def __getattr__(self, name):
         def call(*args):
-            gc.collect()
             gone = [a for a in args if isinstance(a, int) and a in GONE]
             assert not gone, f"{name} was given the address of a copy that is no longer held"
             self.calls.append(name)
@@ -182,3 +180,11 @@ def test_the_tensors_device_is_the_current_one_during_the_call(lib, call):
         call(lib, **on(call, f"cuda:{device}"))
         assert lib.where == (device, 1000 + device)
         assert HERE == [0]
+
+
+def test_workspace_sizes_kept_are_bounded(lib):
+    """A page table that grows by a page at a time makes a new size each time."""
+    for wide in range(1, 3000):
+        attend(lib, page_table=Fake(2, wide, dtype=torch.int32))
+    assert lib.calls.count("ternary_tree_attention") == 2999
+    assert len(attention._ws_bytes) <= 1024
