@@ -33,8 +33,9 @@ class Stack:
     """Layers of the 7B-shaped stack (sizes may be smaller), each with a cache of its own."""
 
     def __init__(self, layers=4, hidden=3584, q_heads=28, kv_heads=4, head_dim=128, ffn=18944, fmt="int8",
-                 page_size=64, pages=256, positions=32768, seed=0, device="cuda"):
-        self.q_heads, self.kv_heads, self.page_size = q_heads, kv_heads, page_size
+                 page_size=64, pages=256, positions=32768, seed=0, device="cuda", group=0):
+        """group: columns of weights that share a scale (0: one scale per row)."""
+        self.q_heads, self.kv_heads, self.page_size, self.group = q_heads, kv_heads, page_size, group
         rows = (q_heads + 2 * kv_heads) * head_dim
         self.head_dim, self.table = head_dim, tl.rope_table(positions, head_dim, base=1e6, device=device)
         self.layers = []
@@ -45,24 +46,25 @@ class Stack:
                 # scales that keep a unit-variance input at unit variance (60% of the weights are not 0)
                 s = (0.6 * k) ** -0.5
                 w[name] = (synth.packed_codes(n, k, synth.seed_for("verify", seed, i, name), device),
-                           synth.scales(n, 0, 0.9 * s, 1.1 * s, synth.seed_for("verify", seed, i, name, "s"), device))
+                           synth.scales(n, k // group if group else 0, 0.9 * s, 1.1 * s,
+                                        synth.seed_for("verify", seed, i, name, "s"), device))
             self.layers.append((w, tl.KVCache.empty(fmt, pages, page_size, kv_heads, head_dim, device)))
 
     def step(self, x, positions, slots, page_table, context_len, tree=None):
         """x [batch, draft, hidden] through every layer; the new tokens' keys and values go to
         slots (int64 [batch * draft])."""
         b, t, hidden = x.shape
-        hq, hk = self.q_heads, self.kv_heads
+        hq, hk, g = self.q_heads, self.kv_heads, self.group
         x = x.flatten(0, 1)
         for w, cache in self.layers:
-            qkv = tl.linear(norm(x), *w["qkv"], 0, static_weights=True).unflatten(1, (hq + 2 * hk, self.head_dim))
+            qkv = tl.linear(norm(x), *w["qkv"], g, static_weights=True).unflatten(1, (hq + 2 * hk, self.head_dim))
             q = qkv[:, :hq]
             tl.kv_append(cache, qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, q=q, positions=positions, table=self.table,
                          q_out=q)
             a = tl.tree_attention(q.unflatten(0, (b, t)), cache, page_table, context_len, tree)
-            x = x + tl.linear(a.flatten(0, 1).flatten(1), *w["o"], 0, static_weights=True)
-            h = tl.linear_silu_mul(norm(x), *w["gu"], 0, static_weights=True)
-            x = x + tl.linear(h, *w["down"], 0, static_weights=True)
+            x = x + tl.linear(a.flatten(0, 1).flatten(1), *w["o"], g, static_weights=True)
+            h = tl.linear_silu_mul(norm(x), *w["gu"], g, static_weights=True)
+            x = x + tl.linear(h, *w["down"], g, static_weights=True)
         return x.unflatten(0, (b, t))
 
     def accept(self, page_table, context_len, path, count):
@@ -122,12 +124,13 @@ def main(argv=None):
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--draft", type=int, default=16)
     ap.add_argument("--context", type=int, default=2000)
+    ap.add_argument("--group", type=int, default=0, choices=(0, 32, 64, 128, 256), help="columns per weight scale (0: one per row)")
     ap.add_argument("--format", choices=sorted(tl.KV_FORMATS), default="int8")
     a = ap.parse_args(argv)
     dev = torch.device("cuda", torch.cuda.current_device())
     gen, cpu = torch.Generator(device=dev).manual_seed(1), torch.Generator().manual_seed(1)
     per = -(-(a.context + a.draft) // 64)
-    stack = Stack(layers=a.layers, fmt=a.format, pages=a.batch * per, device=dev)
+    stack = Stack(layers=a.layers, fmt=a.format, pages=a.batch * per, device=dev, group=a.group)
     page_table = torch.randperm(a.batch * per, generator=gen, device=dev).int().view(a.batch, per)
     ctx = prefill(stack, a.context, page_table, gen, dev)
     parent, depth, sees = random_trees(a.batch, a.draft, cpu)
