@@ -317,8 +317,9 @@ typedef struct {
  *   slots[t]: where token t goes; negative: its k and v are not stored (padding).  A
  *     slot at or beyond pages * page_size stores nothing and sets the device status
  *     word to TL_ERR_VALUE, as does a position outside the table (neither q nor
- *     the cache is then written for that token).  Tokens with the same slot:
- *     either may be the one kept.
+ *     the cache is then written for that token).  Tokens of one call with the same
+ *     slot leave that entry undefined: its codes and scales may come from different
+ *     tokens, as several threads write a row and no order among tokens is kept.
  *   Quantisation of a row y (fp32, after the rotation, not rounded in between):
  *     scale = max|y| (1 / Q) with Q = 127, 448, 7; code = y / scale rounded to nearest
  *     even on the format's grid, 0 where scale is 0 (1 / Q rounded to fp32 first).  A
@@ -368,8 +369,14 @@ tl_status ternary_kv_read(const tl_kv_cache *cache, const int64_t *slots, int64_
  *     ternary_tree_attention_workspace(...) bytes (0 where short contexts need none: it
  *     may then be NULL); free for other use once the call's
  *     work has run.
- * Scores, softmax sums and the joined outputs are fp32.  Every run of the same call
- * gives the same bits.
+ * Scores, softmax sums and the joined outputs are fp32.  Three things enter the
+ * products in 16 bits: the codes (exact); the queries (fp16 as they are; bf16 as fp16
+ * scaled by a power of two per row, exact for elements down to 2^-32 of the row's
+ * largest); and the softmax weights, each times its key's value scale, rounded to the
+ * 11 bits of fp16, down to 2^-20 of a row's largest such product.  So an output is
+ * within 2^-11 sum_j p_j |v_j| of the fp32 result before its own rounding.
+ * Value scales may have either sign; below 2^-72 in magnitude, outputs lose bits.
+ * Every run of the same call gives the same bits.
  */
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
                                          int32_t kv_heads, int32_t head_dim,

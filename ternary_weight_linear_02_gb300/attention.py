@@ -214,7 +214,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, *, inter
     """x [tokens, heads, head_dim] (fp16, bf16 or fp32; any token and head stride) with
     the first table.shape[1] elements of each head rotated by its token's position
     (int64 [tokens]): pairs (x[i], x[i + R/2]), or (x[2i], x[2i+1]) interleaved.
-    inverse: the negative angle, which takes the output's gradient to the input's.
+    inverse: the negative angle, which takes the output's gradient to the input's (the
+    calls record nothing for autograd, as the linear layers do not).
     out: where to write; x itself rotates in place."""
     dt = _DT.get(x.dtype)
     if dt is None or x.dim() != 3:
@@ -244,7 +245,8 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
               table: torch.Tensor | None = None, interleaved: bool = False,
               q_out: torch.Tensor | None = None) -> torch.Tensor | None:
     """Write k, v [tokens, kv_heads, head_dim] (fp16 or bf16, strided views welcome) into
-    the cache at slots (int64 [tokens]; negative: padding, not stored).  With a table
+    the cache at slots (int64 [tokens]; negative: padding, not stored; a slot named by two
+    tokens of one call is left undefined, a mixture of both).  With a table
     (rope_table, rotary_dim a multiple of 16) k, and q [tokens, q_heads, head_dim] where
     given, are rotated by positions (int64 [tokens]) in the same pass; the rotated q is
     returned (written to q_out; q itself rotates in place).  k is not rounded
@@ -332,8 +334,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, co
     row t listing what token t sees; None: a chain, token t sees tokens 0 .. t.
 
     page_table int32 [batch, max_pages], context_len int32 [batch].  scale defaults to
-    head_dim ** -0.5.  Returns [batch, draft, q_heads, head_dim] in q's dtype (zeros for a
-    token that sees nothing) and, with return_lse, ln of the sum of exp of its scores,
+    head_dim ** -0.5.  Scores and sums are fp32; the weights, with their value scales, enter
+    the product with the values in fp16.  Returns [batch, draft, q_heads, head_dim] in q's
+    dtype (zeros for a token that sees nothing) and, with return_lse, ln of the sum of exp of its scores,
     fp32 [batch, draft, q_heads]."""
     dtype = q.dtype
     dt = _DT.get(dtype)
