@@ -14,7 +14,7 @@
 // block given a run of short units would be the last to end by far.  Nothing is done in
 // them, and a block whose run ends within them does not touch the unit.  (6 trees of 23,
 // 32 heads, up to 4099 keys, int4: with the margin below, 249 us without these tiles and
-// that margin, 125 us with both, as the kernel was then; 73 to 75 us now.)
+// that margin, 125 us with both, as the kernel was then; 74 us now.)
 //
 // Where contexts can only be short (by the page table's width), or units are many, a block
 // takes one whole unit instead (AttnArgs::direct): nothing to find, nothing to join.
@@ -47,7 +47,7 @@ constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite:
 // of zeros) 2^25 equal weights fit.  Values below 2^kAttnSmall lose bits only beyond that.
 // With scores of a standard deviation of 2.6 (3.7 in powers of two) and no margin, half the
 // 64-key tiles moved some row of a warp, which cost more than the tile itself (8 trees of 64
-// over 16384 keys: 382 us against 265 with the margin, as the kernel was then; 203 us now).
+// over 16384 keys: 382 us against 265 with the margin, as the kernel was then; 205 us now).
 constexpr float kAttnSlack = 2.f, kAttnMargin = 3.f, kAttnSpread = 4.f;
 constexpr float kAttnTop = 13.f, kAttnBias = 16.f, kAttnSmall = -72.f, kAttnOff = kAttnTop + kAttnBias;
 constexpr float kAttnUnbias = 1.f / 65536.f, kAttnRebias = 65536.f;  // 2^-kAttnBias, 2^kAttnBias
@@ -455,14 +455,18 @@ struct AttnSum {
                 }
             }
         }
+        // sums in two steps: references may lie further apart than fp32's exponents reach
+        const float mn = fmaxf(fmaxf(m, fmaxf(pm[0], pm[1])), fmaxf(pm[2], pm[3])), f = ex2(.5f * (m - mn)), f2 = f * f;
+        m = mn;
+        l = l * f * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f2;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            // sums in two steps: references may lie further apart than fp32's exponents reach
-            const float mn = fmaxf(m, pm[k]), f = ex2(.5f * (m - mn)), g = ex2(.5f * (pm[k] - mn));
-            m = mn;
-            l = l * f * f + pl[k] * g * g;
+            const float g = ex2(.5f * (pm[k] - mn)), g2 = g * g;
+            l += pl[k] * g * g;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * (f * f) + v[k][e] * (g * g);
+            for (int e = 0; e < E; ++e) o[e] += v[k][e] * g2;
         }
     }
 };
@@ -474,7 +478,8 @@ struct AttnSum {
 // time): few rows, or few units, which then have many parts.  Otherwise 16 rows per
 // block, one warp each: many units have few parts.
 // Bound by latency (the place, then the parts from L2): joins cost 2 to 4 us of a call (32
-// sequences of 100 keys, one token, 28 heads on 4: 10.1 us with them, 6.4 without).
+// sequences of 100 keys, one token, 28 heads on 4: 10.4 us with them, 6.5 without; one of 20000:
+// 19.3 us, and 22.1 with the parts added one after the other).
 template <typename TL, int ROWS, int D, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 256 : 512) attn_join_kernel(AttnArgs a, int rtiles, int per_unit, int nc) {
     constexpr int NW = WIDE ? 8 : 16, E = D / 32;
