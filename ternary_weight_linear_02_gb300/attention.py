@@ -5,8 +5,9 @@ rest of the package this only marshals tensors into the C ABI
 (``include/ternary_linear.h``); the work runs on the current stream of the
 tensors' device, and errors found on the host raise before anything is enqueued.
 Indices that live on the device (positions, slots, page tables, lengths) are
-checked there: one out of range skips its work and is reported by
-``device_status`` (TL_ERR_VALUE).
+checked there: one out of range is never followed (a position or slot skips its token, a
+page is read as page 0, a length is clamped) and is reported by ``device_status``
+(TL_ERR_VALUE).
 
     qkv = linear(x, w_qkv, s_qkv).unflatten(-1, (q_heads + 2 * kv_heads, 128))
     q = kv_append(cache, qkv[:, q_heads:-kv_heads], qkv[:, -kv_heads:], slots,

@@ -26,10 +26,10 @@
 //    factor of 4, and then a factor of 8 beyond: the accumulators are rescaled a few times
 //    per unit, not per tile.
 // Measured: 64 sequences of 4096 to 8192 keys, 28 query heads on 4, int8, one token each:
-// 92 us, 4.5 TB/s (0.67 of a copy's rate; 5.4 TB/s with 28 kv heads): issue slots (52 % used, half of them by the codes'
+// 91 to 95 us, 4.3 to 4.5 TB/s (0.64 to 0.66 of a copy's rate; 5.5 TB/s with 28 kv heads): issue slots (50 % used, half of them by the codes'
 // conversions) and the equal division of tiles among blocks whose speeds differ by some
-// 18 %.  One sequence of 131072 keys: 41 us.  16 rows, 6 sequences of up to 4099 keys, 32
-// heads, int4: 75 us.
+// 18 %.  One sequence of 131072 keys: 40 us.  16 rows, 6 sequences of up to 4099 keys, 32
+// heads, int4: 73 us.
 #pragma once
 
 #include "attn_sched.cuh"

@@ -23,9 +23,9 @@
 //    4, and then a factor of 8 beyond: then O is rescaled in TMEM.  The largest score and the
 //    largest value scale together bound a tile's products; only where that bound exceeds the
 //    reference and the tile's scales lie far apart is the largest product looked for.
-// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
-// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 73 us.
-// Bound by the instruction streams of the three kinds of warps: 43 % of the issue slots are
+// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 205 us, 426
+// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 74 us.
+// Bound by the instruction streams of the three kinds of warps: 44 % of the issue slots are
 // used, the tensor pipe 22 %, and the stalls are waits for loads and for results.  Short code
 // without spills matters (39 %, and waits for instructions, before it): loops over the halves of a tile and one decoder for keys and values took
 // these two cases from 255 and 85 us, a rolled loop for the rescaling the first in int4 from

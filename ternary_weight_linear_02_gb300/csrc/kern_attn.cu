@@ -8,8 +8,8 @@ namespace {
 
 // Rows of a kv head (new tokens x query heads that share it): up to 16 the streaming kernel,
 // whose warp MMAs keep up with the cache's bytes.  Streaming against tcgen05, 32 heads, int4:
-// 6 sequences of up to 4099 keys, 9 rows 71 / 73 us, 16 rows 74 / 75; one, 13 rows 25 / 30;
-// 32 of up to 300 keys, 12 rows 46 / 68.  Above, it would need more registers than a thread
+// 6 sequences of up to 4099 keys, 9 rows 69 / 72 us, 16 rows 73 / 74; one, 13 rows 26 / 30;
+// 32 of up to 300 keys, 12 rows 47 / 67.  Above, it would need more registers than a thread
 // has or read the cache twice (24 rows in three blocks of 8: 125 us), and the tcgen05 kernel
 // takes 128 rows at a time (24 rows: 75 us).
 constexpr int64_t kStreamMaxRows = 16;
@@ -20,11 +20,11 @@ bool use_tile(int64_t rows) { return rows > kStreamMaxRows; }
 // a tile (with the blocks per SM that run at once), and what dealing costs beside (finding
 // the run, partial results, the join and its launch).  The lengths are not known here: the
 // page table's width stands for them.  A unit per block against dealt, in us:
-//   one token, 28 heads on 4, fp8: 32 sequences of 100 keys 6.4 / 10.1, of 1000 16.7 / 17.4;
-//   one of 1000 16.1 / 10.4, of 20000 205 / 21; int8, 64 of up to 8192 116 / 93, and with 28
-//   kv heads 530 / 566;
-//   trees: 8 of 64, 500 keys, 28 on 4 35 / 50; 6 of 23, 32 heads, int4, 500 keys 29 / 38,
-//   4099 keys 137 / 89 (before the tcgen05 kernel reached 73 there).
+//   one token, 28 heads on 4, fp8: 32 sequences of 100 keys 6.5 / 10.4, of 1000 17.5 / 18.3;
+//   one of 1000 16.5 / 9.3, of 20000 205 / 19; int8, 64 of up to 8192 118 / 91, and with 28
+//   kv heads 527 / 547;
+//   trees: 8 of 64, 500 keys, 28 on 4 34 / 47; 6 of 23, 32 heads, int4, 500 keys 27 / 31,
+//   4099 keys 122 / 74.
 bool use_direct(int64_t B, int64_t T, int Hq, int Hk, int64_t max_keys) {
     const int64_t rows = T * (Hq / Hk);
     const bool tile = use_tile(rows);
