@@ -351,7 +351,7 @@ tl_status ternary_kv_read(const tl_kv_cache *cache, const int64_t *slots, int64_
  *     TL_BF16; out the same shape and dtype, dense; query head h reads kv head
  *     h / (q_heads / kv_heads).
  *   page_table int32 [batch, max_pages] (row stride in elements): page of key j of a
- *     sequence is page_table[b, j / page_size].
+ *     sequence is page_table[b, j / page_size].  max_pages * page_size <= 2^31 - 256.
  *   context_len int32 [batch]: keys 0 .. context_len[b] - 1 are committed and seen by
  *     every new token; keys context_len[b] + i, i < draft, are the new tokens' own
  *     (already written to the cache).

@@ -49,6 +49,8 @@ tl_status check_cache(const tl_kv_cache *c, tl::KvCache *out) {
 }
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+// keys of a sequence: counts of whole tiles (up to 128 keys) and places in them fit 31 bits
+constexpr int64_t kMaxKeys = kMaxTokens - 256;
 
 }  // namespace
 
@@ -208,7 +210,7 @@ static bool attention_sizes(int64_t batch, int64_t draft, int32_t q_heads, int32
 
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
                                          int32_t kv_heads, int32_t head_dim, int64_t max_keys) {
-    if (!attention_sizes(batch, draft, q_heads, kv_heads, head_dim) || max_keys < 0 || max_keys >= kMaxTokens) return -1;
+    if (!attention_sizes(batch, draft, q_heads, kv_heads, head_dim) || max_keys < 0 || max_keys > kMaxKeys) return -1;
     if (batch == 0 || draft == 0) return 0;
     return tl::tree_attention_workspace(batch, draft, q_heads, kv_heads, head_dim, max_keys);
 }
@@ -229,8 +231,8 @@ tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t 
     if (!stride_ok(q_batch_stride) || !stride_ok(q_token_stride) || !stride_ok(q_head_stride) ||
         !stride_ok(page_table_stride) || !stride_ok(tree_batch_stride) || !stride_ok(tree_row_stride))
         return TL_ERR_SHAPE;
-    // keys of a sequence fit 31 bits, and its page-table row holds the new tokens at least
-    if (max_pages < 0 || max_pages > (kMaxTokens - 1) / a.c.P) return TL_ERR_SHAPE;
+    // a sequence's page-table row holds the new tokens at least (below)
+    if (max_pages < 0 || max_pages > kMaxKeys / a.c.P) return TL_ERR_SHAPE;
     if (batch == 0 || draft == 0) return TL_OK;
     if (max_pages * a.c.P < draft) return TL_ERR_SHAPE;
     if (!q || !page_table || !context_len || !out) return TL_ERR_NULL;
