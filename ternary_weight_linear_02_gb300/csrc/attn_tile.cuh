@@ -69,7 +69,7 @@ struct AttnTileCfg {
     static constexpr int CODES = kTileKeys * RB, CKOFF = VOFF + TILE, CVOFF = CKOFF + 2 * CODES;
     static constexpr int SKOFF = CVOFF + 2 * CODES, SVOFF = SKOFF + 4 * kTileKeys * 4;
     static constexpr int SXOFF = SVOFF + 4 * kTileKeys * 4;  // sizes of the value scales, as them
-    static constexpr int SMOFF = SXOFF + 4 * kTileKeys * 4;  // largest of committed keys [4], far apart? [4]
+    static constexpr int SMOFF = SXOFF + 4 * kTileKeys * 4;  // largest, smallest of committed keys [4]
     static constexpr int NOFF = SMOFF + 32;               // units with NaN codes among new values [4]
     static constexpr int FOFF = NOFF + 16;                // row factors [4][128]
     static constexpr int BOFF = FOFF + 4 * 512;           // barriers, TMEM slot, abort flag
@@ -439,17 +439,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 const float2 w = *v, x = make_float2(attn_size(w.x), attn_size(w.y));
                 *v = make_float2(w.x * kAttnUnbias, w.y * kAttnUnbias);
                 *reinterpret_cast<float2 *>(smem + C::SXOFF + (j & 3) * KT * 4 + lane * 8) = x;
-                // from kAttnSmall on, where they compare as their bits; those of new tokens' keys
-                // count for whether they lie far apart, and for the rows that see them
-                const uint32_t b0 = __float_as_uint(x.x - kAttnSmall), b1 = __float_as_uint(x.y - kAttnSmall);
-                const int n = at.ctx - k, all = n + a.T;
-                const uint32_t seen = __reduce_max_sync(0xffffffffu, max(n > 0 ? b0 : 0u, n > 1 ? b1 : 0u));
-                const uint32_t mx = __reduce_max_sync(0xffffffffu, max(all > 0 ? b0 : 0u, all > 1 ? b1 : 0u));
-                const uint32_t mn = __reduce_min_sync(0xffffffffu, min(all > 0 ? b0 : ~0u, all > 1 ? b1 : ~0u));
-                if (lane == 0) {
-                    reinterpret_cast<float *>(smem + C::SMOFF)[j & 3] = __uint_as_float(seen) + kAttnSmall;
-                    reinterpret_cast<int *>(smem + C::SMOFF)[4 + (j & 3)] = __uint_as_float(mx) - __uint_as_float(mn) > kAttnSpread;
-                }
+                // from kAttnSmall on, where they compare as their bits
+                const uint32_t b0 = __float_as_uint(x.x - kAttnSmall), b1 = __float_as_uint(x.y - kAttnSmall), most = __float_as_uint(128.f - kAttnSmall);
+                const int n = at.ctx - k;
+                const uint32_t mx = __reduce_max_sync(0xffffffffu, max(n > 0 ? b0 : 0u, n > 1 ? b1 : 0u));
+                const uint32_t mn = __reduce_min_sync(0xffffffffu, min(n > 0 ? b0 : most, n > 1 ? b1 : most));
+                if (lane == 0)
+                    reinterpret_cast<float2 *>(smem + C::SMOFF)[j & 3] = make_float2(__uint_as_float(mx) + kAttnSmall, __uint_as_float(mn) + kAttnSmall);
             }
             const int turn = vals ? 2 - dw : dw;
             if (FMT == kKvFp8 && vals && held1 < KT) {  // new tokens' values
@@ -493,7 +489,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                 const float4 *sk = reinterpret_cast<const float4 *>(smem + C::SKOFF + (j & 3) * KT * 4);
                 const float4 *sv = reinterpret_cast<const float4 *>(smem + C::SVOFF + (j & 3) * KT * 4);
                 const float4 *sx = reinterpret_cast<const float4 *>(smem + C::SXOFF + (j & 3) * KT * 4);
-                float size = reinterpret_cast<const float *>(smem + C::SMOFF)[j & 3];  // the largest that the row sees
+                float2 size = reinterpret_cast<const float2 *>(smem + C::SMOFF)[j & 3];  // the largest and the smallest that the row sees
                 uint32_t see0 = ~0u, see1 = ~0u;
                 const bool edge = at.tile * KT + KT > at.ctx;  // new tokens' keys, or the end
                 if (edge) {
@@ -512,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                             if (i >= 0 && i < a.T) u = tree ? tree[i] != 0 : i <= tok;
                             if (u) {
                                 bits |= 1u << k;
-                                size = fmaxf(size, sizes[32 * c + k]);
+                                size = make_float2(fmaxf(size.x, sizes[32 * c + k]), fminf(size.y, sizes[32 * c + k]));
                             }
                         }
                         if (c) see1 = bits;
@@ -552,11 +548,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 }
-                top = top * f + size;  // no product is larger
+                top = top * f + size.x;  // no product is larger
                 if (__any_sync(0xffffffffu, grow < R && top > ref + kAttnSlack)) {
-                    if (reinterpret_cast<const volatile int *>(smem + C::SMOFF)[4 + (j & 3)])
-                        top = largest_product(scol, reinterpret_cast<const float *>(sk), reinterpret_cast<const float *>(sx), f, see0, see1);
-                    const float rn = top > ref + kAttnSlack ? top + kAttnMargin : ref;
+                    float rn = top > ref + kAttnSlack ? top + kAttnMargin : ref;
+                    const bool far = rn != ref && size.x - size.y > kAttnSpread;  // no product may be near the bound
+                    if (__any_sync(0xffffffffu, grow < R && far)) {
+                        const float y = largest_product(scol, reinterpret_cast<const float *>(sk), reinterpret_cast<const float *>(sx), f, see0, see1);
+                        if (far) rn = y > ref + kAttnSlack ? y + kAttnMargin : ref;
+                    }
                     // in two steps: the sum may outlive a factor that fp32 cannot hold
                     const float h = ex2(.5f * (ref - rn)), c2 = h * h;
                     ref = rn;
