@@ -373,10 +373,13 @@ tl_status ternary_kv_read(const tl_kv_cache *cache, const int64_t *slots, int64_
  * products in 16 bits: the codes (exact); the queries (fp16 as they are; bf16 as fp16
  * scaled by a power of two per row, exact for elements down to 2^-32 of the row's
  * largest); and the softmax weights, each times its key's value scale, rounded to the
- * 11 bits of fp16, down to 2^-20 of a row's largest such product.  So an output is
- * within 2^-11 sum_j p_j |v_j| of the fp32 result before its own rounding.
- * Value scales may have either sign; below 2^-72 in magnitude, outputs lose bits.
- * Every run of the same call gives the same bits.
+ * 11 bits of fp16, below 2^-20 of a row's largest such product w to a multiple of
+ * 2^-30 w.  So an output is within sum_j (2^-11 p_j |v_j| + 2^-31 w |code_j|) of the
+ * fp32 result before its own rounding.
+ * Value scales may have either sign.  Rows whose w is below 2^-94 lose bits, and those
+ * below 2^-104 give 0.
+ * Scores up to 2^28 in magnitude are served.  Every run of the same call gives the
+ * same bits, and so does a call that differs in what unseen keys hold.
  */
 int64_t ternary_tree_attention_workspace(int64_t batch, int64_t draft, int32_t q_heads,
                                          int32_t kv_heads, int32_t head_dim,

@@ -37,19 +37,24 @@ constexpr float kAttnLow = -3e38f;  // a running maximum before any key (finite:
 // f16 weights, each with its value scale: products e sv.  In powers of two, with score z_j and
 // size x_j = max(log2 |sv_j|, kAttnSmall), a row's reference r follows the largest z_j + x_j
 // among the keys that this row sees:
-//   e_j = 2^(z_j - r + kAttnTop + kAttnBias),  product_j = e_j (sv_j 2^-kAttnBias).
-// r moves only when some z_j + x_j exceeds it by kAttnSlack (so products stay below 2^15), and
-// then kAttnMargin beyond: the largest lies between 2^10 and 2^15, products down to 2^-24 of
+//   e_j = 2^(z_j - r),  product_j = e_j (sv_j 2^-kAttnBias).
+// r moves only when some z_j + x_j exceeds it by kAttnFull (so products stay below 2^15), and
+// then to kAttnRoom below: the largest lies between 2^10 and 2^15, products down to 2^-24 of
 // it keep all 11 bits of f16, whatever scales other keys or other rows have.  (The tcgen05
 // kernel may take a bound that is up to kAttnSpread higher: 2^6, 2^-20.)  The sum of the
 // weights counts e_j, whose range in fp32 the bias centres: for scales of up to 2^128 terms
 // down to 2^-24 of the largest weight count, and with scales of 2^kAttnSmall and less (rows
-// of zeros) 2^25 equal weights fit.  Values below 2^kAttnSmall lose bits only beyond that.
+// of zeros) 2^25 equal weights fit.  A row whose largest product is far below 2^kAttnSmall of its
+// largest weight leaves f16 at the lower end: it loses bits from 2^-94 on.
+// Differences z_j - r are exact where they matter, sums z_j + x_j are not: beyond kAttnCoarse a
+// reference taken from a sum is held against the differences that it leaves, and raised where one
+// exceeds kAttnFull.  So scores up to 2^29 give their answer; beyond, where fp32 has steps
+// larger than the room that f16 leaves, all weights of a row may vanish.
 // With scores of a standard deviation of 2.6 (3.7 in powers of two) and no margin, half the
 // 64-key tiles moved some row of a warp, which cost more than the tile itself (8 trees of 64
 // over 16384 keys: 382 us against 265 with the margin, as the kernel was then; 205 us now).
-constexpr float kAttnSlack = 2.f, kAttnMargin = 3.f, kAttnSpread = 4.f;
-constexpr float kAttnTop = 13.f, kAttnBias = 16.f, kAttnSmall = -72.f, kAttnOff = kAttnTop + kAttnBias;
+constexpr float kAttnBias = 16.f, kAttnRoom = 10.f + kAttnBias, kAttnFull = 15.f + kAttnBias, kAttnSpread = 4.f, kAttnSmall = -72.f;
+constexpr float kAttnCoarse = 1048576.f;
 constexpr float kAttnUnbias = 1.f / 65536.f, kAttnRebias = 65536.f;  // 2^-kAttnBias, 2^kAttnBias
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,6 +69,8 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// at least the sum of two terms that is y after its rounding and this one
+__device__ __forceinline__ float attn_above(float y) { return fmaf(fabsf(y), 0x1p-23f, y); }
 // x_j of a value scale; finite for every bit pattern
 __device__ __forceinline__ float attn_size(float sv) { return fminf(fmaxf(lg2(fabsf(sv)), kAttnSmall), 128.f); }
 

@@ -21,7 +21,7 @@
 //    enter as f16 scaled by a power of two per row (QueryScale in attn_sched.cuh).
 //  * P is rounded to f16 (2^-11 relative) with its value scale in it, kept so far up that
 //    products down to 2^-24 of a row's largest keep all 11 bits.  A row's reference is that of
-//    its own products (kAttnTop in attn_sched.cuh), so neither a key of a negligible weight
+//    its own products (kAttnRoom in attn_sched.cuh), so neither a key of a negligible weight
 //    nor one that another row sees takes bits from it.  It moves only when exceeded by a
 //    factor of 4, and then a factor of 8 beyond: the accumulators are rescaled a few times
 //    per unit, not per tile.
@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
             }
             bool move = false;
 #pragma unroll
-            for (int n = 0; n < NB; ++n) move = move || top[n][0] > ref[n][0] + kAttnSlack || top[n][1] > ref[n][1] + kAttnSlack;
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) move = move || attn_above(top[n][r]) - ref[n][r] > kAttnFull;
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
@@ -384,7 +386,17 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         float x = top[n][r];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        x = x > ref[n][r] + kAttnSlack ? x + kAttnMargin : ref[n][r];
+                        const float was = x;
+                        x = attn_above(x) - ref[n][r] > kAttnFull ? fmaxf(x - kAttnRoom, ref[n][r]) : ref[n][r];
+                        if (__any_sync(0xffffffffu, fabsf(was) > kAttnCoarse)) {
+                            float left = -INFINITY;
+#pragma unroll
+                            for (int gr = 0; gr < GR; ++gr)
+                                left = fmaxf(left, fmaxf(z[gr][n][r] - x + attn_size(sv[gr][0]), z[gr][n][2 + r] - x + attn_size(sv[gr][1])));
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) left = fmaxf(left, __shfl_xor_sync(0xffffffffu, left, o));
+                            if (left > kAttnFull) x = __fadd_ru(x, left - kAttnRoom);
+                        }
                         // in two steps: the sum may outlive a factor that fp32 cannot hold
                         const float h = ex2(.5f * (ref[n][r] - x)), c = h * h;
                         ref[n][r] = x;
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                     float p[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float e = ex2(z[gr][n][j] - (ref[n][j & 1] - kAttnOff));
+                        const float e = ex2(z[gr][n][j] - ref[n][j & 1]);
                         l[n][j & 1] += e;
                         p[j] = e * wv[j >> 1];
                     }
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
 #pragma unroll
                     for (int e = 0; e < EPT; e += 2) o[e / 2] = attn_pack(a, v[e] * rl, v[e + 1] * rl);
                     if (FMT == kKvFp8 && nan_seen) attn_put_nans<D>(a, out, row / a.G, part * EPT, EPT, o - part * (EPT / 2), nullptr);
-                    if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M - kAttnOff + log2f(Ls)) * kLn2;
+                    if (a.lse && part == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
                 } else {
                     float *slot = AttnSlot<ROWS, D>::at(a.ws, blockIdx.x, which);
                     float *o = slot + row * D + part * EPT;
@@ -569,7 +581,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<FMT, D, NB>::BLOCKS)
                         *reinterpret_cast<float4 *>(o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     if (FMT == kKvFp8 && nan_seen) attn_put_nans<D>(a, out, row / a.G, part * EPT, EPT, nullptr, slot + row * D);
                     if (part == 0) {
-                        slot[ROWS * D + row] = M - kAttnOff;
+                        slot[ROWS * D + row] = M;
                         slot[ROWS * (D + 1) + row] = Ls;
                     }
                 }

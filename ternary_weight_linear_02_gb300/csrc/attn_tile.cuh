@@ -19,7 +19,7 @@
 //  * Warps 0-3: a row's 64 scores are read in halves, for the maximum and then for the
 //    weights; P (f16) overwrites the first half of them in TMEM.  The weights hold the
 //    value scale, so far up that products down to 2^-24 of the row's largest keep all 11 bits
-//    (kAttnTop in attn_sched.cuh).  A row's reference moves only when exceeded by a factor of
+//    (kAttnRoom in attn_sched.cuh).  A row's reference moves only when exceeded by a factor of
 //    4, and then a factor of 8 beyond: then O is rescaled in TMEM.  The largest score and the
 //    largest value scale together bound a tile's products; only where that bound exceeds the
 //    reference and the tile's scales lie far apart is the largest product looked for.
@@ -113,10 +113,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-// The largest product of a row (a lane's scores of one tile at scol), in powers of two.  Rarely
-// called, and not inlined: in place, and guarded by the softmax's own values, its code made
-// every tile dearer (8 trees of 64 over 16384 keys: 210 us against 203).
-__device__ __noinline__ float largest_product(uint32_t scol, const float *sk, const float *sx, float f, uint32_t see0, uint32_t see1) {
+// The largest product of a row (a lane's scores of one tile at scol) over 2^base, in powers of two.
+__device__ __forceinline__ float largest_product(uint32_t scol, const float *sk, const float *sx, float f, uint32_t see0, uint32_t see1, float base) {
     float top = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < kTileKeys; c += 16) {
@@ -126,11 +124,22 @@ __device__ __noinline__ float largest_product(uint32_t scol, const float *sk, co
         const uint32_t see = (c & 32 ? see1 : see0) >> (c & 16);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const float y = __uint_as_float(s[k]) * sk[c + k] * f + sx[c + k];
+            const float y = fmaf(__uint_as_float(s[k]) * sk[c + k], f, -base) + sx[c + k];
             top = fmaxf(top, see >> k & 1u ? y : -INFINITY);
         }
     }
     return top;
+}
+// The reference of a row after a tile from its largest product.  By a whole warp.  Rarely called, and
+// not inlined: in place its code made every tile dearer.
+__device__ __noinline__ float exact_reference(uint32_t scol, const float *sk, const float *sx, float f, uint32_t see0, uint32_t see1, float ref) {
+    const float y = largest_product(scol, sk, sx, f, see0, see1, 0.f);
+    float rn = attn_above(y) - ref > kAttnFull ? fmaxf(y - kAttnRoom, ref) : ref;
+    if (__any_sync(0xffffffffu, fabsf(y) > kAttnCoarse)) {
+        const float left = largest_product(scol, sk, sx, f, see0, see1, rn);
+        if (left > kAttnFull) rn = __fadd_ru(rn, left - kAttnRoom);
+    }
+    return rn;
 }
 
 // The rest of a wait that has not succeeded at once, by a whole warp: all lanes see the phase
@@ -548,13 +557,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 }
-                top = top * f + size.x;  // no product is larger
-                if (__any_sync(0xffffffffu, grow < R && top > ref + kAttnSlack)) {
-                    float rn = top > ref + kAttnSlack ? top + kAttnMargin : ref;
+                // No product is larger than top and size say; z - r by the same operation as for the weights.
+                if (__any_sync(0xffffffffu, grow < R && fmaf(top, f, -ref) + size.x > kAttnFull)) {
+                    float rn = top * f + size.x - kAttnRoom;
+                    const float left = fmaf(top, f, -rn) + size.x;
+                    if (left > kAttnFull) rn = __fadd_ru(rn, left - kAttnRoom);
+                    if (!(fmaf(top, f, -ref) + size.x > kAttnFull)) rn = ref;
                     const bool far = rn != ref && size.x - size.y > kAttnSpread;  // no product may be near the bound
                     if (__any_sync(0xffffffffu, grow < R && far)) {
-                        const float y = largest_product(scol, reinterpret_cast<const float *>(sk), reinterpret_cast<const float *>(sx), f, see0, see1);
-                        if (far) rn = y > ref + kAttnSlack ? y + kAttnMargin : ref;
+                        const float y = exact_reference(scol, reinterpret_cast<const float *>(sk), reinterpret_cast<const float *>(sx), f, see0, see1, ref);
+                        if (far) rn = y;
                     }
                     // in two steps: the sum may outlive a factor that fp32 cannot hold
                     const float h = ex2(.5f * (ref - rn)), c2 = h * h;
@@ -575,7 +587,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                     }
                 }
                 // ---- weights, over S's first columns
-                const float off = kAttnOff - ref;
+                const float off = -ref;
                 const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
                 float2 l2 = make_float2(0.f, 0.f), l3 = l2;
 #pragma unroll 1
@@ -658,9 +670,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_tile_kernel(AttnArgs a, 
                         if (FMT == kKvFp8 && reinterpret_cast<volatile int *>(smem + C::NOFF)[(unit + 1) & 3] == unit + 1)
                             attn_put_nans<D>(a, at, g / a.G, 0, D, whole ? static_cast<uint16_t *>(a.out) + out_row * D : nullptr, slot + row * D);
                         if (whole) {
-                            if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref - kAttnOff + log2f(l)) * kLn2;
+                            if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
                         } else {
-                            slot[ROWS * D + row] = ref - kAttnOff;
+                            slot[ROWS * D + row] = ref;
                             slot[ROWS * (D + 1) + row] = l;
                         }
                     }
