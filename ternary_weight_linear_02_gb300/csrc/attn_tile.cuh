@@ -22,9 +22,9 @@
 //    (kAttnRoom in attn_sched.cuh).  A row's reference moves only when exceeded by a factor of
 //    4, and then a factor of 8 beyond: then O is rescaled in TMEM.  The largest score and the
 //    largest value scale together bound a tile's products; only where that bound exceeds the
-//    reference and the tile's scales lie far apart is the largest product looked for.
-// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 205 us, 426
-// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 74 us.
+//    reference and the scales that the row sees lie far apart is the largest product looked for.
+// Measured: 8 trees of 64 over 16384 keys, 28 query heads on 4, fp8: 204 us, 428
+// TFLOP/s of both products; 6 trees of 23, 32 heads, up to 4099 keys, int4: 75 us.
 // Bound by the instruction streams of the three kinds of warps: 44 % of the issue slots are
 // used, the tensor pipe 22 %, and the stalls are waits for loads and for results.  Short code
 // without spills matters (39 %, and waits for instructions, before it): loops over the halves of a tile and one decoder for keys and values took
