@@ -393,6 +393,111 @@ tl_status ternary_tree_attention(const void *q, int64_t q_batch_stride, int64_t 
                                  int64_t tree_row_stride, float scale, void *out, float *lse,
                                  void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The pages of a cache, and its entries, between steps: taking and giving back
+ * pages, forking sequences, closing up entries.  Everything is decided on the
+ * device from arrays that live there, so that a captured loop of steps needs no
+ * answer on the host.  The conventions of the calls above hold: an index out of
+ * range is never followed, sets the device status word to TL_ERR_VALUE, and only the work
+ * that it names is left out.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The rows (sequences) of a server and the pool of pages that they share (host
+ * struct, device pointers).  Row r holds lens[r] tokens in the pages
+ * table[r, 0 .. held[r]), in order; token j is place j % page_size of page
+ * table[r, j / page_size].  A row may hold pages ahead of its tokens.  refs[p]: how
+ * many rows hold page p; 0: free.  One pool's tables serve the caches of all layers (each
+ * cache has `pages` pages of page_size places, used alike).
+ * rows <= 8192, pages < 2^30, max_pages * page_size <= 2^31 - 256.
+ */
+typedef struct {
+    int32_t *refs;        /* [pages]                                             */
+    int32_t *table;       /* [rows, max_pages], rows table_stride elements apart */
+    int32_t *lens;        /* [rows]                                              */
+    int32_t *held;        /* [rows]                                              */
+    int64_t table_stride; /* >= max_pages                                        */
+    int64_t pages;
+    int64_t max_pages;
+    int32_t rows;
+    int32_t page_size;
+} tl_kv_pages;
+
+/*
+ * ternary_pages_free -- row r holds keep[r] tokens from now on (lens[r] = keep[r]), in
+ * its first ceil(keep[r] / page_size) pages; the pages behind them are given back
+ * (refs lowered by one each, their entries in the table 0).  keep[r] = 0 ends a row; a
+ * negative one leaves it as it is.  keep[r] may be above lens[r], up to
+ * held[r] * page_size (tokens accepted into pages held ahead); beyond that, and where
+ * held[r] is out of range, the row is left as it is and the status word set.
+ * keep int32 [rows].  A page whose count is not above 0 stays at its count and sets the
+ * status word.
+ */
+tl_status ternary_pages_free(const tl_kv_pages *pages, const int32_t *keep, void *stream);
+
+/*
+ * ternary_pages_reserve -- row r gets the pages that lens[r] + extra[r] tokens need
+ * beyond those it holds: free pages, the lowest-numbered first, to the rows in order.
+ * A row gets all it needs or none: it is served if it needs none, or if the
+ * needs of all rows up to and with it are covered by the free pages.
+ *   extra int32 [rows]; negative: the row is left as it is (ok, no slots).
+ *   ok uint8 [rows], may be NULL: 1 where the row has its pages.
+ *   slots int64 [rows, width], may be NULL: the slots of the row's next tokens,
+ *     table[r, j / page_size] * page_size + j % page_size for j = lens[r] + i, i < min(extra[r],
+ *     width); -1 behind them and where ok is 0 (as ternary_kv_append takes them).
+ * lens stays.  A row whose lens or held is out of range, or whose tokens would not fit its
+ * table, gets nothing (ok = 0) and sets the status word; that pages have run out does not.
+ */
+tl_status ternary_pages_reserve(const tl_kv_pages *pages, const int32_t *extra, int64_t *slots,
+                                int32_t width, uint8_t *ok, void *stream);
+
+/*
+ * ternary_pages_fork -- row r becomes a continuation of row parent[r] (negative: the
+ * row is left as it is): it shares the pages that are full (refs raised) and
+ * gets a page of its own for the tokens of the last, partly filled one, whose entries
+ * are copied in all layers.  lens[r] = lens[parent], held[r] = the pages of those tokens.
+ *   parent int32 [rows].  The row must hold no page (held[r] == 0) and the parent must
+ *     not be forked in the same call; otherwise the row is left as it is (ok = 0) and the status
+ *     word set.  Several rows may have one parent.
+ *   caches: host array of `layers` caches of one geometry (pages and page_size those of
+ *     the pool, no cache twice), 0..512 of them (NULL with 0: tables only).
+ *   ok uint8 [rows], may be NULL: 0 where no page was free (rows are served as in
+ *     ternary_pages_reserve; nothing of the row is then changed).
+ *   workspace: device, 16-byte aligned, ternary_pages_fork_workspace(rows) bytes.
+ */
+int64_t ternary_pages_fork_workspace(int64_t rows); /* -1: invalid */
+tl_status ternary_pages_fork(const tl_kv_pages *pages, const int32_t *parent,
+                             const tl_kv_cache *caches, int32_t layers, uint8_t *ok,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ternary_kv_copy -- the first tokens[i] places (NULL: all) of page src[i] are copied to
+ * page dst[i], keys and values, codes and scales, in every one of `layers` caches (as
+ * ternary_pages_fork takes them, at least one).  src, dst, tokens int32 [n].  A pair with a
+ * negative page is skipped.  A page that is written must not be read or written
+ * by another pair of the call.  HBM-bound.
+ */
+tl_status ternary_kv_copy(const tl_kv_cache *caches, int32_t layers, const int32_t *src,
+                          const int32_t *dst, const int32_t *tokens, int64_t n, void *stream);
+
+/*
+ * ternary_kv_compact -- of each sequence, the entries at places start[b] + keep[b, i], i <
+ * count[b], move to places start[b] + i, in every one of `layers` caches: the accepted path of
+ * a drafted tree closed up behind the committed tokens, or what is left of a context.
+ *   page_table int32 [batch, max_pages] (row stride); start, count int32 [batch]; keep
+ *   int32 [batch, n] (row stride), 0 <= keep[b, 0] < keep[b, 1] < ... for i < count[b]:
+ *   entries move towards the front, in place.  Where keep does not ascend or leaves
+ *   the table, that sequence's moves end before it and the status word is set; a
+ *   count outside 0..n is clamped and a negative start moves nothing, both set it too.
+ *   Sequences of one call must not share the pages that they write.  Places behind the
+ *   moved entries keep what they held.  max_pages * page_size <= 2^31 - 256.
+ * HBM-bound: each moved entry is read once and written once.
+ */
+tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const int32_t *page_table,
+                             int64_t page_table_stride, int64_t max_pages, const int32_t *start,
+                             const int32_t *keep, int64_t keep_stride, const int32_t *count,
+                             int64_t batch, int64_t n, void *stream);
+
 /* Kernels by M (TL_PATH_AUTO, K % 64 == 0): M <= 16 -> the decode kernel
  * (register-fed warp MMAs, TMA-staged weights) or, for 9 <= M and for plain
  * layers of 2049..4608 rows at M <= 8, the tcgen05 skinny kernel (groups 0 /
