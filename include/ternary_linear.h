@@ -445,8 +445,10 @@ tl_status ternary_pages_free(const tl_kv_pages *pages, const int32_t *keep, void
  *   slots int64 [rows, width], may be NULL: the slots of the row's next tokens,
  *     table[r, j / page_size] * page_size + j % page_size for j = lens[r] + i, i < min(extra[r],
  *     width); -1 behind them and where ok is 0 (as ternary_kv_append takes them).
- * lens stays.  A row whose lens or held is out of range, or whose tokens would not fit its
- * table, gets nothing (ok = 0) and sets the status word; that pages have run out does not.
+ * lens stays.  A row whose lens or held is out of range, whose tokens would not fit its
+ * table, or whose next token would lie in a page that another row holds too (it was cut
+ * there: fork it instead) gets nothing (ok = 0) and sets the status word; that pages have run
+ * out does not.
  */
 tl_status ternary_pages_reserve(const tl_kv_pages *pages, const int32_t *extra, int64_t *slots,
                                 int32_t width, uint8_t *ok, void *stream);
@@ -497,6 +499,45 @@ tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const in
                              int64_t page_table_stride, int64_t max_pages, const int32_t *start,
                              const int32_t *keep, int64_t keep_stride, const int32_t *count,
                              int64_t batch, int64_t n, void *stream);
+
+/*
+ * ternary_verify_drafts -- which drafted tokens stand, and the token after them, such that
+ * the tokens are distributed as the target's own would be, from given random numbers.
+ *   Nodes: 0, where a sequence stands, and 1 + i, drafted token i.  parent int32 [batch,
+ *     draft] (batch stride; 0 shares one tree): the drafted token that i follows,
+ *     -1 <= parent[b, i] < i (-1: node 0); NULL: a chain, parent i - 1.
+ *   target [batch, draft + 1, vocab], draft_probs [batch, draft, vocab] or NULL (batch and node
+ *     strides, the last axis dense; TL_F32, TL_F16 or TL_BF16, both the same): row n holds
+ *     the probabilities of the token after node n -- the target's, and those that the
+ *     drafter drew node n's children from (rows of nodes without children are not
+ *     read).  Rows are taken as they are, as if they summed to 1; an entry that is negative or NaN
+ *     counts as 0.
+ *   tokens int64 [batch, draft], uniform fp32 [batch, draft + 1] in [0, 1) (batch strides).
+ *   At a node, w = p (its target row), W = 1.  Its children are looked at in the order of
+ *   their indexes; with x the child's token and u its random number
+ *     with draft_probs:  accepted if u W q(x) < w(x); else w = max(w - W q, 0), W = sum w
+ *     without:           accepted if u W < w(x);      else W -= w(x), w(x) = 0
+ *   An accepted child is the next node.  When no child is left, the next token is the smallest v
+ *   with w(0) + .. + w(v) > uniform[b, draft] sum w (w = p where all of w is 0).
+ *   path int32 [batch, draft]: accepted drafted tokens in order, -1 behind them; count
+ *     int32 [batch]: how many; out_tokens int64 [batch, draft + 1]: their tokens, then the
+ *     drawn one, -1 behind it.
+ *   A drafted token outside [0, vocab) or with a parent out of range is not looked at, nor what
+ *   follows it; a row of which nothing can be drawn gives the token -1.  Both set the device
+ *   status word to TL_ERR_VALUE.
+ *   draft 0..1024 (0: a token is drawn), batch <= 65536, vocab 1..2^31 - 2^12.
+ * Comparisons are made in fp64; sums carry 47 bits or more, so that a draw lands where one in
+ * fp64 does but for random numbers within about 1e-13 of a border.  HBM-bound: one target row is read
+ * per sequence, and a row of each side per rejection with draft_probs.
+ */
+tl_status ternary_verify_drafts(const void *target, int64_t target_batch_stride,
+                                int64_t target_node_stride, const void *draft_probs,
+                                int64_t draft_batch_stride, int64_t draft_node_stride,
+                                int32_t dtype, const int64_t *tokens, int64_t tokens_stride,
+                                const int32_t *parent, int64_t parent_stride,
+                                const float *uniform, int64_t uniform_stride, int64_t batch,
+                                int64_t draft, int64_t vocab, int32_t *path, int32_t *count,
+                                int64_t *out_tokens, void *stream);
 
 /* Kernels by M (TL_PATH_AUTO, K % 64 == 0): M <= 16 -> the decode kernel
  * (register-fed warp MMAs, TMA-staged weights) or, for 9 <= M and for plain

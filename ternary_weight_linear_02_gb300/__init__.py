@@ -23,6 +23,8 @@ __all__ = [
     "linear_fused",
     "linear_silu_mul",
     "KVCache", "KV_FORMATS", "rope_table", "rope", "kv_append", "kv_read", "tree_attention",
+    "KVLayers", "KVPages", "pages_free", "pages_reserve", "pages_fork", "kv_copy", "kv_compact",
+    "verify_drafts",
     "device_status", "device_status_async", "status_string", "skinny_max_m", "PATHS",
 ]
 
@@ -353,3 +355,6 @@ def linear_silu_mul(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
 
 from .attention import (KVCache, KV_FORMATS, kv_append, kv_read, rope, rope_table,  # noqa: E402
                         tree_attention)
+from .pages import (KVLayers, KVPages, kv_compact, kv_copy, pages_fork, pages_free,  # noqa: E402
+                    pages_reserve)
+from .verify import verify_drafts  # noqa: E402

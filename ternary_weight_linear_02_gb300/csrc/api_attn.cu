@@ -2,28 +2,28 @@
 // include/ternary_linear.h): argument validation, then one launch function each.
 #include <cmath>
 
-#include "kernels.h"
-#include "ternary_linear.h"
+#include "api_util.h"
 
 namespace {
 
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-tl_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return TL_OK;
-    cudaGetLastError();
-    return TL_ERR_CUDA;
-}
+using tl::aligned;
+using tl::check_cache;
+using tl::from_cuda;
+using tl::stride_ok;
 
 // A strided [tokens, heads, D] tensor (or its leading axes): element alignment is
 // required, and `rows16` reports whether every row starts on a 16-byte boundary.
-// Offsets stay far inside 63 bits: |stride| < 2^40, axis < 2^31 in any use.
-bool stride_ok(int64_t s) { return s > -((int64_t)1 << 40) && s < ((int64_t)1 << 40); }
 bool rows16(const void *p, int64_t s0, int64_t s1, int size) {
     return aligned(p, 16) && (s0 * size) % 16 == 0 && (s1 * size) % 16 == 0;
 }
 
-tl_status check_cache(const tl_kv_cache *c, tl::KvCache *out) {
+constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+// keys of a sequence: counts of whole tiles (up to 128 keys) and places in them fit 31 bits
+constexpr int64_t kMaxKeys = kMaxTokens - 256;
+
+}  // namespace
+
+tl_status tl::check_cache(const tl_kv_cache *c, KvCache *out) {
     if (c == nullptr) return TL_ERR_NULL;
     if (c->format != TL_KV_INT8 && c->format != TL_KV_FP8 && c->format != TL_KV_INT4) return TL_ERR_DTYPE;
     if (c->head_dim != 64 && c->head_dim != 128) return TL_ERR_SHAPE;
@@ -47,12 +47,6 @@ tl_status check_cache(const tl_kv_cache *c, tl::KvCache *out) {
     out->fmt = c->format;
     return TL_OK;
 }
-
-constexpr int64_t kMaxTokens = (int64_t)1 << 31;
-// keys of a sequence: counts of whole tiles (up to 128 keys) and places in them fit 31 bits
-constexpr int64_t kMaxKeys = kMaxTokens - 256;
-
-}  // namespace
 
 extern "C" {
 

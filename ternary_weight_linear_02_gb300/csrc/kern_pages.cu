@@ -1,0 +1,274 @@
+// kern_pages.cu -- the pages of a pool: giving them back, taking them for the next tokens,
+// and for sequences that continue another one.
+//
+// A page is free where its reference count is 0, so there is no list of free pages to keep: taking
+// looks through the counts and gives the lowest-numbered free pages to the rows in order, by prefix
+// sums.  Which page a row gets depends on the counts alone, never on timing.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace tl {
+
+namespace {
+
+constexpr uint32_t kSat = (1u << 30) - 1;  // where page counts saturate
+constexpr uint32_t kNeeds = 1u << 31, kBad = 1u << 30;
+
+// One warp per row: the pages behind the kept ones.
+__global__ void __launch_bounds__(256) pages_free_kernel(KvPages g, const int *keep, int *status) {
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= g.rows) return;
+    const int n = keep[r], held = g.held[r];
+    if (n < 0) return;
+    if (held < 0 || held > g.max_pages || n > (int64_t)held * g.P) {
+        if (lane == 0) flag_value(status);
+        return;
+    }
+    const int stay = (int)(((uint32_t)n + (uint32_t)g.P - 1u) / (uint32_t)g.P);
+    int *row = g.table + r * g.stride;
+    for (int i = stay + lane; i < held; i += 32) {
+        const int page = row[i];
+        if ((uint32_t)page >= (uint32_t)g.pages) {
+            flag_value(status);
+        } else if (atomicSub(g.refs + page, 1) <= 0) {
+            atomicAdd(g.refs + page, 1);
+            flag_value(status);
+        }
+        row[i] = 0;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        g.held[r] = stay;
+        g.lens[r] = n;
+    }
+}
+
+// Pages that a row wants (at most kSat), kBad for a row that cannot be served.
+template <bool FORK>
+__device__ __forceinline__ uint32_t need_of(const PagesTakeArgs &a, int r) {
+    const KvPages &g = a.g;
+    const int w = a.want[r];
+    if (w < 0) return 0;
+    if constexpr (FORK) {
+        if (w >= g.rows || g.held[r] != 0 || a.want[w] >= 0) return kBad;
+        const int n = g.lens[w], held = g.held[w];
+        if (n < 0 || held < 0 || held > g.max_pages || n > (int64_t)held * g.P) return kBad;
+        return (uint32_t)n % (uint32_t)g.P ? 1u : 0u;
+    } else {
+        const int n = g.lens[r], held = g.held[r];
+        const int64_t most = g.max_pages * g.P;
+        if (n < 0 || held < 0 || held > g.max_pages || n + (int64_t)w > most) return kBad;
+        const uint32_t P = (uint32_t)g.P, last = (uint32_t)n / P;
+        if (w > 0 && (uint32_t)n % P && last < (uint32_t)held) {  // the next token goes into a page in use
+            const int page = g.table[r * g.stride + last];
+            if ((uint32_t)page >= (uint32_t)g.pages || g.refs[page] > 1) return kBad;
+        }
+        const uint32_t upto = ((uint32_t)n + (uint32_t)w + P - 1u) / P;
+        return upto > (uint32_t)held ? min(upto - (uint32_t)held, kSat) : 0u;
+    }
+}
+
+__device__ __forceinline__ uint32_t sat(uint32_t x) { return min(x, kSat); }
+
+// Inclusive prefix sum over the block's 1024 threads (saturating where SAT), and the total.
+template <bool SAT>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *part, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = SAT ? sat(v + u) : v + u;
+    }
+    __syncthreads();  // part may still be read by the call before
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    uint32_t s = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s = SAT ? sat(s + u) : s + u;
+    }
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+    if (warp > 0) v = SAT ? sat(v + before) : v + before;
+    return v;
+}
+
+// Which of 1024 pages from p0 on are free: lane j holds the word of pages p0 + 32 j ...
+__device__ __forceinline__ uint32_t free_words(const int *refs, int64_t p0, int64_t end) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;
+    int v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int64_t p = p0 + 32 * j + lane;
+        v[j] = p < end ? refs[p] : 1;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint32_t w = __ballot_sync(0xffffffffu, v[j] == 0);
+        if (lane == j) mine = w;
+    }
+    return mine;
+}
+
+// One cluster of up to 8 blocks (one block up to 32768 pages) serves all rows:
+//   needs of the rows and their running sums (every block for itself, in shared memory);
+//   free pages counted, each block a run of pages, the counts exchanged;
+//   the free page of rank k goes to the row whose sum passes k, as far as whole rows are covered;
+//   lengths, slots and answers.
+// Bound by latency: three dependent trips to memory and the cluster's barriers.
+template <bool FORK>
+__global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
+    __shared__ uint32_t cum[kMaxPageRows];
+    __shared__ uint32_t part[32], counts[8];
+    const KvPages &g = a.g;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = gridDim.x, rank = blockIdx.x;
+    if (C > 1) cluster_arrive_relaxed();
+    uint32_t total = 0;
+    for (int r0 = 0; r0 < g.rows; r0 += 1024) {
+        const int r = r0 + tid;
+        const uint32_t need = r < g.rows ? need_of<FORK>(a, r) : 0u;
+        if (need == kBad && rank == 0) flag_value(a.status);
+        uint32_t sum;
+        const uint32_t upto = block_scan<true>(need == kBad ? 0u : need, part, sum);
+        if (r < g.rows) cum[r] = sat(total + upto) | (need == kBad ? kBad : need ? kNeeds : 0u);
+        total = sat(total + sum);
+    }
+    __syncthreads();
+    if (C > 1) cluster_wait();  // every block has started
+    uint32_t have = 0;
+    if (total > 0) {
+        const int64_t per = (g.pages + C * 1024 - 1) / (C * 1024) * 1024;
+        const int64_t lo = rank * per, hi = min(lo + per, g.pages);
+        uint32_t words = 0, mine = 0;
+        for (int64_t p0 = lo; p0 < hi; p0 += 32768) {
+            words = free_words(g.refs, p0 + warp * 1024, hi);
+            mine += __popc(words);
+        }
+        uint32_t below = 0;
+        block_scan<false>(mine, part, have);
+        if (C > 1) {
+            if (tid < C) cl_st_u32(cl_map(smem_u32(&counts[rank]), tid), have);
+            cl_arrive_release();
+            cl_wait_acquire();
+            have = 0;
+            for (int i = 0; i < C; ++i) {
+                if (i == rank) below = have;
+                have += counts[i];
+            }
+        }
+        // pages given out: the largest sum of needs that the free pages cover
+        uint32_t given = 0;
+        {
+            int x = 0, y = g.rows;  // rows before x are covered, from y on not
+            while (x < y) {
+                const int m = (x + y) >> 1;
+                if ((cum[m] & kSat) <= have) x = m + 1;
+                else y = m;
+            }
+            if (x > 0) given = cum[x - 1] & kSat;
+        }
+        for (int64_t p0 = lo; p0 < hi && below < given; p0 += 32768) {
+            if (per > 32768) words = free_words(g.refs, p0 + warp * 1024, hi);
+            uint32_t sum;
+            const uint32_t n = __popc(words);
+            uint32_t k = below + block_scan<false>(n, part, sum) - n;  // rank of the lane's first free page
+            const uint32_t first = __shfl_sync(0xffffffffu, k, 0);
+            uint32_t at = first;
+            for (int j = 0; j < 32 && at < given; ++j) {
+                const uint32_t w = __shfl_sync(0xffffffffu, words, j);
+                const uint32_t nth = at + __popc(w & ((1u << lane) - 1u));
+                if ((w >> lane & 1u) && nth < given) {
+                    int x = 0, y = g.rows - 1;  // the first row whose sum is above nth
+                    while (x < y) {
+                        const int m = (x + y) >> 1;
+                        if ((cum[m] & kSat) > nth) y = m;
+                        else x = m + 1;
+                    }
+                    const uint32_t before = x > 0 ? cum[x - 1] & kSat : 0u;
+                    const int page = (int)(p0 + warp * 1024 + 32 * j + lane);
+                    const uint32_t place = FORK ? (uint32_t)g.lens[a.want[x]] / (uint32_t)g.P : (uint32_t)g.held[x] + (nth - before);
+                    g.table[x * g.stride + place] = page;
+                    g.refs[page] = 1;
+                }
+                at += __popc(w);
+            }
+            below += sum;
+        }
+        __syncthreads();
+        if (C > 1) {
+            cl_arrive_release();
+            cl_wait_acquire();
+        }
+    }
+    const auto served = [&](int r) {
+        const uint32_t c = cum[r];
+        return !(c & kBad) && (!(c & kNeeds) || (c & kSat) <= have);
+    };
+    if constexpr (FORK) {
+        if (rank != 0) return;
+        uint32_t listed = 0;
+        for (int r0 = 0; r0 < g.rows; r0 += 1024) {
+            const int r = r0 + tid;
+            const bool in = r < g.rows, ok = in && served(r), forked = ok && a.want[r] >= 0;
+            if (in && a.ok) a.ok[r] = ok;
+            uint32_t sum;
+            const uint32_t k = listed + block_scan<false>(forked, part, sum);
+            if (forked) {
+                const int n = g.lens[a.want[r]];
+                g.lens[r] = n;
+                g.held[r] = (int)(((uint32_t)n + (uint32_t)g.P - 1u) / (uint32_t)g.P);
+                a.list[k] = r;
+            }
+            listed += sum;
+        }
+        if (tid == 0) a.list[0] = (int)listed;
+    } else {
+        for (int r = rank * 1024 + tid; r < g.rows; r += C * 1024) {
+            const bool ok = served(r);
+            if (a.ok) a.ok[r] = ok;
+            if (ok && (cum[r] & kNeeds))
+                g.held[r] = (int)(((uint32_t)g.lens[r] + (uint32_t)a.want[r] + (uint32_t)g.P - 1u) / (uint32_t)g.P);
+        }
+        if (a.slots == nullptr) return;
+        const int64_t all = (int64_t)g.rows * a.width;
+        for (int64_t e = rank * 1024 + tid; e < all; e += C * 1024) {
+            const int r = (int)(e / a.width), i = (int)(e - (int64_t)r * a.width);
+            long long s = -1;
+            if (served(r) && i < a.want[r]) {
+                const uint32_t j = (uint32_t)g.lens[r] + (uint32_t)i, p = j / (uint32_t)g.P;
+                const int page = __ldcg(g.table + r * g.stride + p);  // (another block of the cluster may have written it)
+                s = (long long)page * g.P + (j - p * (uint32_t)g.P);
+            }
+            a.slots[e] = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_free(const KvPages &g, const int *keep, int *status, cudaStream_t st) {
+    pages_free_kernel<<<(g.rows + 7) / 8, 256, 0, st>>>(g, keep, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_take(const PagesTakeArgs &a, bool fork, cudaStream_t st) {
+    // a block's run of pages is looked through once and kept as bits: 32768 of them
+    int C = 1;
+    while (C < 8 && (int64_t)C * 32768 < a.g.pages) C *= 2;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(C);
+    c.blockDim = dim3(1024);
+    c.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return fork ? cudaLaunchKernelEx(&c, pages_take_kernel<true>, a) : cudaLaunchKernelEx(&c, pages_take_kernel<false>, a);
+}
+
+}  // namespace tl

@@ -284,4 +284,65 @@ cudaError_t launch_attn_int4(const AttnArgs &a, bool tile, int sms, cudaStream_t
 cudaError_t launch_tree_attention(const AttnArgs &a, int sm_count, cudaStream_t st);
 int64_t tree_attention_workspace(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_keys);
 
+// ------------------------------------------------------------ pages and entries of the cache
+constexpr int kMaxPageRows = 8192;             // rows of a pool: their needs lie in shared memory
+constexpr uint32_t kMaxPages = (1u << 30) - 2; // page counts saturate below bit 30
+struct KvPages {
+    int *refs, *table, *lens, *held;
+    int64_t stride, pages, max_pages;
+    int rows, P;
+};
+struct PagesTakeArgs {
+    KvPages g;
+    const int *want;   // extra tokens, or parents
+    long long *slots;  // [rows, width]
+    int width;
+    uint8_t *ok;
+    int *list;         // fork: count, then the rows forked
+    int *status;
+};
+cudaError_t launch_pages_free(const KvPages &g, const int *keep, int *status, cudaStream_t st);
+cudaError_t launch_pages_take(const PagesTakeArgs &a, bool fork, cudaStream_t st);
+
+// Codes and scales of the layers that one launch moves entries in (2 KB of kernel parameters)
+constexpr int kMoveLayers = 64;
+struct KvMove {
+    uint8_t *kc[kMoveLayers], *vc[kMoveLayers];
+    float *ks[kMoveLayers], *vs[kMoveLayers];
+    int64_t pages;
+    int L, P, Hk, rb;  // layers, page size, kv heads, bytes of a row of codes (a multiple of 16)
+    int *status;
+};
+cudaError_t launch_kv_copy(const KvMove &m, const int *src, const int *dst, const int *tokens, int64_t n,
+                           int sm_count, cudaStream_t st);
+// the rows listed by launch_pages_take: shared pages (where share) and copies of the last ones
+cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *parent, const int *list, bool share,
+                              int sm_count, cudaStream_t st);
+struct KvCompactArgs {
+    const int *table;
+    int64_t table_stride, max_places;
+    const int *start, *keep, *count;
+    int64_t keep_stride;
+    int64_t batch, n;
+};
+cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st);
+
+// ------------------------------------------------------------ verification of drafted tokens
+constexpr int kMaxDraft = 1024;  // drafted tokens of a sequence: what is looked up of them lies in shared memory
+struct VerifyArgs {
+    const void *target, *draft;  // [B, T + 1, V], [B, T, V]; draft may be null
+    int64_t target_b, target_n, draft_b, draft_n;  // strides (elements)
+    const int64_t *tokens;
+    const int *parent;  // null: a chain
+    const float *uniform;
+    int64_t tokens_b, parent_b, uniform_b;
+    int *path, *count;
+    int64_t *out;
+    int64_t B;
+    int T, V;
+    int blocks;  // of a cluster
+    int *status;
+};
+cudaError_t launch_verify(const VerifyArgs &a, int dtype, bool vec, cudaStream_t st);
+
 }  // namespace tl
