@@ -539,6 +539,53 @@ tl_status ternary_verify_drafts(const void *target, int64_t target_batch_stride,
                                 int64_t draft, int64_t vocab, int32_t *path, int32_t *count,
                                 int64_t *out_tokens, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters beside a shared layer.  Ternary codes cannot take up an update of their
+ * weights, so an adapter's product is added to the layer's output, for each token that of its
+ * own request:
+ *   out[m, c] = y[m, c] + s_a sum_r b[a, c, r] sum_k a[a, sh R + r, k] x[m, k],  a = which[m],
+ * sh the shard that column c lies in: a fused layer (QKV, gate/up) is one call, its shards'
+ * matrices stacked as the layer's rows are.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void *a;       /* [adapters, shards * rank, inputs], x's dtype, 16-byte aligned     */
+    const void *b;       /* [adapters, sum of shard_rows, rank], x's dtype, 16-byte aligned   */
+    const float *scale;  /* [adapters], NULL: 1                                               */
+    int64_t inputs;
+    int64_t shard_rows[8]; /* output columns of each shard, in order                          */
+    int32_t shards;      /* 1..8                                                              */
+    int32_t rank;        /* of each shard: a multiple of 8, 8..128 (smaller adapters are padded
+                            with rows and columns of zeros)                                   */
+    int32_t adapters;    /* 1..2048                                                           */
+    int32_t dtype;       /* TL_F16 or TL_BF16                                                 */
+} tl_adapters;
+
+/*
+ * ternary_lora_add -- the sum above for every token.
+ *   x [tokens, inputs], y and out [tokens, sum of shard_rows] (token strides in elements, the
+ *     last axis dense); out_dtype: of y and out, TL_F32 or the adapters' dtype.  out == y with
+ *     the same stride adds in place, any other overlap is not allowed.
+ *   which int32 [tokens]: each token's adapter; negative: none (out = y).  One beyond the
+ *     adapters counts as none and sets the device status word to TL_ERR_VALUE.
+ *   workspace: device, 16-byte aligned, ternary_lora_workspace(tokens, adapters) bytes (0 for
+ *     decode shapes: it may then be NULL); free for other use once the call's work has run.
+ * Sums are fp32 in an order that depends on sizes alone; s_a (x a^T) enters the second product in
+ * 16-bit numbers that together keep 2^-17 of it (fp32 outputs: 2^-22); the result is rounded once.
+ * ternary_lora_silu_mul -- the same for a fused gate/up layer (two shards of N columns: gate, up),
+ *   with the gated product behind it: g, u the two halves of the sum (fp32),
+ *   out[m, j] = silu(g[m, j]) u[m, j], out [tokens, N], which must not overlap y.
+ * HBM-bound: x, y and out once, the adapters that occur once per 16 to 64 tokens of theirs.
+ */
+int64_t ternary_lora_workspace(int64_t tokens, int64_t adapters); /* -1: invalid */
+tl_status ternary_lora_add(const void *x, int64_t x_stride, const tl_adapters *adapters,
+                           const int32_t *which, const void *y, int64_t y_stride, void *out,
+                           int64_t out_stride, int32_t out_dtype, int64_t tokens, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+tl_status ternary_lora_silu_mul(const void *x, int64_t x_stride, const tl_adapters *adapters,
+                                const int32_t *which, const void *y, int64_t y_stride, void *out,
+                                int64_t out_stride, int32_t out_dtype, int64_t tokens,
+                                void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Kernels by M (TL_PATH_AUTO, K % 64 == 0): M <= 16 -> the decode kernel
  * (register-fed warp MMAs, TMA-staged weights) or, for 9 <= M and for plain
  * layers of 2049..4608 rows at M <= 8, the tcgen05 skinny kernel (groups 0 /

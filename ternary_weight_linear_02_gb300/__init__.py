@@ -24,7 +24,7 @@ __all__ = [
     "linear_silu_mul",
     "KVCache", "KV_FORMATS", "rope_table", "rope", "kv_append", "kv_read", "tree_attention",
     "KVLayers", "KVPages", "pages_free", "pages_reserve", "pages_fork", "kv_copy", "kv_compact",
-    "verify_drafts",
+    "verify_drafts", "Adapters", "lora_add", "lora_silu_mul",
     "device_status", "device_status_async", "status_string", "skinny_max_m", "PATHS",
 ]
 
@@ -357,4 +357,5 @@ from .attention import (KVCache, KV_FORMATS, kv_append, kv_read, rope, rope_tabl
                         tree_attention)
 from .pages import (KVLayers, KVPages, kv_compact, kv_copy, pages_fork, pages_free,  # noqa: E402
                     pages_reserve)
+from .lora import Adapters, lora_add, lora_silu_mul  # noqa: E402
 from .verify import verify_drafts  # noqa: E402

@@ -1,0 +1,114 @@
+// kern_lora.cu -- low-rank adapters: which tiles, and how they are dealt (the kernel is in
+// kern_lora.cuh).
+#include "kern_lora.cuh"
+
+namespace tl {
+
+namespace {
+
+// Tokens sorted by adapter and cut into tiles of TM, for more tokens or adapters than each block
+// looks through by itself.  plan: [0] tiles, from 4 on (adapter, first, tokens) of each, then the
+// sorted tokens.  Where a token lies within its adapter's run hangs on the order of atomics,
+// what is computed for it does not: rows of a tile do not meet.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int *plan) {
+    extern __shared__ int sh[];
+    __shared__ int wsum[32], wtile[32];
+    const int keys = a.adapters + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *const cursor = sh, *const first = sh + keys + 1, *const tile = first + keys + 1;
+    pdl_launch_dependents();
+    for (int i = tid; i < keys; i += 1024) cursor[i] = 0;
+    __syncthreads();
+    for (int64_t t = tid; t < a.M; t += 1024) {
+        if (a.which[t] >= a.adapters) flag_value(a.status);
+        atomicAdd(&cursor[lora_key(a, t)], 1);
+    }
+    __syncthreads();
+    // running sums of tokens and of tiles over the adapters
+    const int each = (keys + 1023) / 1024;
+    int n = 0, m = 0;
+    for (int i = 0; i < each; ++i) {
+        const int k = tid * each + i;
+        if (k < keys) n += cursor[k], m += (cursor[k] + TM - 1) / TM;
+    }
+    int un = n, um = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, un, o), w = __shfl_up_sync(0xffffffffu, um, o);
+        if (lane >= o) un += u, um += w;
+    }
+    if (lane == 31) wsum[warp] = un, wtile[warp] = um;
+    __syncthreads();
+    int bn = un - n, bm = um - m;
+    for (int i = 0; i < warp; ++i) bn += wsum[i], bm += wtile[i];
+    for (int i = 0; i < each; ++i) {
+        const int k = tid * each + i;
+        if (k < keys) {
+            const int c = cursor[k];
+            first[k] = bn;
+            tile[k] = bm;
+            bn += c;
+            bm += (c + TM - 1) / TM;
+            if (k == keys - 1) first[keys] = bn, tile[keys] = bm;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < keys; i += 1024) cursor[i] = first[i];
+    const int tiles = tile[keys];
+    if (tid == 0) plan[0] = tiles;
+    for (int u = tid; u < tiles; u += 1024) {
+        int x = 0, y = keys - 1;  // the last adapter whose tiles begin at or before u and that has any
+        while (x < y) {
+            const int mid = (x + y + 1) >> 1;
+            if (tile[mid] <= u) x = mid;
+            else y = mid - 1;
+        }
+        const int at = first[x] + (u - tile[x]) * TM;
+        int *const p = plan + 4 + 3 * u;
+        p[0] = x;
+        p[1] = at;
+        p[2] = min(TM, first[x + 1] - at);
+    }
+    __syncthreads();
+    int *const order = plan + 4 + 3 * a.max_tiles;
+    for (int64_t t = tid; t < a.M; t += 1024) order[atomicAdd(&cursor[lora_key(a, t)], 1)] = (int)t;
+}
+
+// A tile takes 16 tokens, or 64 (gated 32, whose two halves' sums fill the registers) where the adapters
+// that can be there have more than 32 each on average.
+bool big_tiles(int64_t M, int64_t adapters, int ranks) {
+    const int64_t present = adapters + 1 < M ? adapters + 1 : M;
+    return ranks <= 192 && M > 32 * present;
+}
+
+int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {
+    const int64_t present = adapters + 1 < M ? adapters + 1 : M;
+    return (M + present * (TM - 1)) / TM;
+}
+
+}  // namespace
+
+int64_t lora_workspace(int64_t M, int64_t adapters) {
+    if (M <= kLoraFind && adapters <= kLoraFind) return 0;
+    return 4 * (4 + 3 * tiles_bound(M, adapters, 16) + M);
+}
+
+cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st) {
+    LoraArgs a = args;
+    const bool big = big_tiles(a.M, a.adapters, a.S * a.R);
+    const int TM = !big ? 16 : a.gated ? 32 : 64;
+    const int units = (int)tiles_bound(a.M, a.adapters, TM);
+    a.C = 8;
+    while (a.C > 1 && (int64_t)units * a.C > 4 * sm_count) a.C /= 2;
+    a.plan = nullptr;
+    if (lora_workspace(a.M, a.adapters) > 0) {
+        a.max_tiles = units;
+        int *const plan = static_cast<int *>(workspace);
+        lora_plan_kernel<<<1, 1024, 3 * (a.adapters + 2) * sizeof(int), st>>>(a, TM, plan);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        a.plan = plan;
+    }
+    return dtype == 1 ? launch_lora_bf16(a, f32, big, units, st) : launch_lora_f16(a, f32, big, units, st);
+}
+
+}  // namespace tl

@@ -345,4 +345,28 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs &a, int dtype, bool vec, cudaStream_t st);
 
+// ------------------------------------------------------------ low-rank adapters
+constexpr int kMaxShards = 8;
+struct LoraArgs {
+    const void *x, *a, *b, *y;
+    void *out;
+    const float *scale;  // null: 1
+    const int *which;
+    int64_t xs, ys, os;  // token strides (elements)
+    int64_t M, N, K;     // N: columns of y
+    int64_t shard[kMaxShards];
+    int S, R, adapters;
+    int gated;
+    int vec_x, vec_a, vec_y;  // rows start on 16-byte boundaries (y, out: columns of threads too)
+    int C;                    // blocks of a cluster
+    const int *plan;          // tiles found beforehand (null: by each block)
+    int max_tiles;
+    int *status;
+};
+// tokens and adapters up to which no workspace is needed: each block finds its tile by itself
+int64_t lora_workspace(int64_t M, int64_t adapters);
+cudaError_t launch_lora(const LoraArgs &a, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st);
+cudaError_t launch_lora_f16(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st);
+cudaError_t launch_lora_bf16(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st);
+
 }  // namespace tl
