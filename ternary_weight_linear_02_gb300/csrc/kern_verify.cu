@@ -37,6 +37,11 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
     const float e = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), h = __fadd_rn(s.hi, e);
     return {h, __fsub_rn(e, __fsub_rn(h, s.hi))};
 }
+__device__ __forceinline__ bool above(Pair a, Pair b) { return add(a, Pair{-b.hi, -b.lo}).hi > 0.f; }
+__device__ __forceinline__ Pair pair_of(double x) {
+    const float h = (float)x;
+    return {h, (float)(x - (double)h)};
+}
 __device__ __forceinline__ Pair shfl_up(Pair a, int o) {
     return {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
 }
@@ -85,8 +90,9 @@ struct Weights {
 };
 
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&v)[16 / sizeof(T)]) {
-    const uint4 r = ldg_nc_v4(p);
+__device__ __forceinline__ void load16(const T *p, float (&v)[16 / sizeof(T)], bool in) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (in) r = ldg_nc_v4(p);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -99,7 +105,8 @@ __device__ __forceinline__ void load16(const T *p, float (&v)[16 / sizeof(T)]) {
 }
 
 // Sum of the weights of tokens [lo, hi), taken by one warp.  VEC: lo is a multiple of 8 and rows
-// start on 16-byte boundaries.
+// start on 16-byte boundaries.  The last, partly filled step is read under a mask like the others: a loop of
+// single loads would wait for each.
 template <typename T, bool VEC>
 __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
     const int lane = threadIdx.x & 31;
@@ -110,13 +117,14 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
     };
     if constexpr (VEC) {
         constexpr int W = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;  // elements a load, loads in flight
-        int v = lo + lane * W;
-        for (; v + (U - 1) * 32 * W + W <= hi; v += U * 32 * W) {
+        const int whole = lo + (hi - lo) / W * W;
+        for (int v = lo + lane * W; v < whole; v += U * 32 * W) {
             float p[U][W], q[U][W];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                load16(w.p + v + u * 32 * W, p[u]);
-                if (w.q) load16(w.q + v + u * 32 * W, q[u]);
+                const bool in = v + u * 32 * W < whole;
+                load16(w.p + v + u * 32 * W, p[u], in);
+                if (w.q) load16(w.q + v + u * 32 * W, q[u], in);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -130,17 +138,16 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
                 for (int e = 0; e < W; ++e) take(w.q ? w.of(p[u][e], q[u][e]) : Pair{p[u][e], 0.f});
             }
         }
-        for (; v < hi; v += 32 * W)
-            for (int e = 0; e < W && v + e < hi; ++e) take(w.at(v + e));
+        if (whole + lane < hi) take(w.at(whole + lane));
     } else {
         constexpr int U = 8;
-        int v = lo + lane;
-        for (; v + (U - 1) * 32 < hi; v += U * 32) {
+        for (int v = lo + lane; v < hi; v += U * 32) {
             float p[U], q[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                p[u] = prob(w.p[v + u * 32]);
-                q[u] = w.q ? prob(w.q[v + u * 32]) : 0.f;
+                const bool in = v + u * 32 < hi;
+                p[u] = in ? prob(w.p[v + u * 32]) : 0.f;
+                q[u] = in && w.q ? prob(w.q[v + u * 32]) : 0.f;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -148,26 +155,64 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
                 take(w.q ? w.of(p[u], q[u]) : Pair{p[u], 0.f});
             }
         }
-        for (; v < hi; v += 32) take(w.at(v));
     }
     // acc.lo may be as large as acc.hi's last bits; the pairs' sum puts that right
     return warp_total(add(Pair{0.f, 0.f}, acc));
+}
+
+// Weights of tokens [v0, v1), at most N of them (0 beyond), by one thread.
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, Pair (&x)[N]) {
+    float p[N], q[N];
+    constexpr int W = 16 / sizeof(T);
+    if (VEC && v0 % W == 0 && v1 - v0 == N) {
+#pragma unroll
+        for (int i = 0; i < N; i += W) {
+            float r[W];
+            load16(w.p + v0 + i, r, true);
+#pragma unroll
+            for (int e = 0; e < W; ++e) p[i + e] = r[e];
+            if (w.q) {
+                load16(w.q + v0 + i, r, true);
+#pragma unroll
+                for (int e = 0; e < W; ++e) q[i + e] = r[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            p[i] = v0 + i < v1 ? prob(w.p[v0 + i]) : 0.f;
+            q[i] = v0 + i < v1 && w.q ? prob(w.q[v0 + i]) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (w.gone && w.removed(v0 + i)) p[i] = 0.f;
+        x[i] = w.q ? w.of(p[i], q[i]) : Pair{p[i], 0.f};
+    }
 }
 
 // One cluster of C blocks per sequence; block r holds tokens [r per, (r + 1) per), warp w of it a run
 // of them.  Every block follows the accepted path by itself (the entries that it turns on
 // are gathered first); sums are exchanged through distributed shared memory.
 // Bound by latency: the gather (two dependent loads), a pass, the cluster's barrier, the drawing.
+// fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
+// warp takes the SM's unit 16 cycles.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     __shared__ float px[kMaxDraft], qx[kMaxDraft], un[kMaxDraft + 1];
     __shared__ int tok[kMaxDraft], par[kMaxDraft], path[kMaxDraft], gone[kMaxDraft];
+    __shared__ uint8_t fresh[kMaxDraft];  // accepted as its node's first child
     __shared__ Pair warp_sum[kWarps], part[kWarps], block_sum[2][kMaxBlocks];
     __shared__ struct {
         int todo;  // 0: a pass over p, 1: over p and q, 2: done
         int node, count, gone, next;
         double A, W;
     } st;
+    __shared__ struct {
+        int empty, owner, run;  // nothing to draw from; block and warp's run that the number falls in
+        Pair rest;              // what is left of it there
+    } fin;
     __shared__ int found;
     const int C = (int)a.blocks, rank = (int)(blockIdx.x % (unsigned)C), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t b = blockIdx.x / (unsigned)C;
@@ -182,10 +227,12 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
         const int at = a.parent ? a.parent[b * a.parent_b + i] : i - 1;
         const bool ok = x >= 0 && x < V && at >= -1 && at < i;
         if (!ok && rank == 0) flag_value(a.status);
+        const float p = ok ? prob(target[(at + 1) * a.target_n + x]) : 0.f, q = ok && draft ? prob(draft[(at + 1) * a.draft_n + x]) : 1.f;
         tok[i] = (int)x;
         par[i] = ok ? at : -2;
-        px[i] = ok ? prob(target[(at + 1) * a.target_n + x]) : 0.f;
-        qx[i] = ok && draft ? prob(draft[(at + 1) * a.draft_n + x]) : 1.f;
+        px[i] = p;
+        qx[i] = q;
+        fresh[i] = (double)un[i] * (double)q < (double)p;  // (the product of two fp32 is exact)
     }
     if (tid == 0) {
         st.node = st.count = st.gone = st.next = 0;
@@ -200,30 +247,42 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     Weights<T> w;
     w.list = gone;
     int buf = 0;
-    double before = 0., all = 0.;  // sums of the blocks before this one, and of all
+    double all = 0., upto = 0.;  // warp 0: the sum, and (lane i) the sum of blocks 0 .. i
     const auto pass = [&] {
         const int l = min(hi, lo + warp * run), h = min(hi, l + run);
         const Pair s = sum_run<T, VEC>(w, l, h);
         if (lane == 0) warp_sum[warp] = s;
         __syncthreads();
-        Pair mine{0.f, 0.f};
-        for (int i = 0; i < kWarps; ++i) mine = add(mine, warp_sum[i]);
-        if (C > 1) {
-            if (tid < C) {
-                const uint32_t at = cl_map(smem_u32(&block_sum[buf][rank]), tid);
-                cl_st_f32(at, mine.hi);
-                cl_st_f32(at + 4, mine.lo);
+        if (warp == 0) {
+            Pair mine = lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f};
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1)
+                mine = add(mine, Pair{__shfl_xor_sync(0xffffffffu, mine.hi, o), __shfl_xor_sync(0xffffffffu, mine.lo, o)});
+            if (C > 1) {
+                if (lane < C) {
+                    const uint32_t at = cl_map(smem_u32(&block_sum[buf][rank]), lane);
+                    cl_st_f32(at, mine.hi);
+                    cl_st_f32(at + 4, mine.lo);
+                }
+                __syncwarp();
+            } else if (lane == 0) {
+                block_sum[buf][0] = mine;
             }
+        }
+        if (C > 1) {
             cl_arrive_release();
             cl_wait_acquire();
         } else {
-            if (tid == 0) block_sum[buf][0] = mine;
             __syncthreads();
         }
-        all = 0.;
-        for (int i = 0; i < C; ++i) {
-            if (i == rank) before = all;
-            all += block_sum[buf][i].d();
+        if (warp == 0) {
+            upto = lane < C ? block_sum[buf][lane].d() : 0.;
+#pragma unroll
+            for (int o = 1; o < kMaxBlocks; o <<= 1) {
+                const double u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o && lane < C) upto += u;
+            }
+            all = __shfl_sync(0xffffffffu, upto, C - 1);
         }
         buf ^= 1;  // (a block writes a buffer again only after all have passed the next barrier)
     };
@@ -231,6 +290,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
         if (warp == 0) {  // on along the tokens, until sums are needed
             int node = st.node, count = st.count, ngone = st.gone, i = st.next, todo = -1;
             double A = st.A, W = summed ? all : st.W;
+            bool first = !summed;  // no child of this node was rejected
             while (todo < 0) {
                 // the next child of this node
                 if (a.parent) {
@@ -243,29 +303,37 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
                         }
                     }
                     i = at;
-                } else {
-                    while (i < n && par[i] != node - 1) ++i;
+                } else if (i < n && par[i] != node - 1) {  // (a chain's node has one child)
+                    i = n;
                 }
                 if (i >= n) {
                     todo = 2;
                     break;
                 }
                 const int x = tok[i];
-                double p = (double)px[i];
-                const double q = (double)qx[i];
-                if (draft) {
-                    p = fmax(p - A * q, 0.);
+                bool yes;
+                double p = 0.;
+                if (first) {
+                    yes = fresh[i];
+                    if (!yes && !draft) p = (double)px[i];
                 } else {
-                    for (int j = 0; j < ngone; ++j)
-                        if (gone[j] == x) p = 0.;
+                    p = (double)px[i];
+                    if (draft) {
+                        p = fmax(p - A * (double)qx[i], 0.);
+                    } else {
+                        for (int j = 0; j < ngone; ++j)
+                            if (gone[j] == x) p = 0.;
+                    }
+                    yes = (double)un[i] * (W * (double)qx[i]) < p;
                 }
-                if ((double)un[i] * (W * q) < p) {
+                if (yes) {
                     if (lane == 0) path[count] = i;
                     ++count;
                     node = i + 1;
                     A = 0.;
                     W = 1.;
                     ngone = 0;
+                    first = true;
                 } else if (draft) {
                     A += W;
                     todo = 1;
@@ -273,6 +341,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
                     W -= p;
                     if (lane == 0) gone[ngone] = x;
                     ++ngone;
+                    first = false;
                     __syncwarp();
                 }
                 ++i;
@@ -293,100 +362,107 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
         if (todo == 2) break;  // (w and its sums are those of the pass before)
         w.p = target + (int64_t)st.node * a.target_n;
         w.q = todo == 1 ? draft + (int64_t)st.node * a.draft_n : nullptr;
-        w.ah = (float)st.A;
-        w.al = (float)(st.A - (double)w.ah);
+        const Pair A = pair_of(st.A);
+        w.ah = A.hi;
+        w.al = A.lo;
         w.gone = st.gone;
         pass();
         if (todo == 0) break;
         __syncthreads();  // st is read by all before it changes
     }
-    if (!(all > 0.) && (w.q || w.gone)) {  // nothing is left: the target's own row
-        w.q = nullptr;
+    for (bool again = false;; again = true) {
+        if (warp == 0) {
+            // the block whose tokens the number falls on: the first whose sum with those before passes it, else
+            // (the number is not below 1) the last that has any; and the warp's run within it
+            const Pair mine = lane < C ? block_sum[buf ^ 1][lane] : Pair{0.f, 0.f};
+            const uint32_t some = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+            const double t = (double)un[n] * all;
+            const uint32_t hit = __ballot_sync(0xffffffffu, mine.hi > 0.f && upto > t);
+            const int owner = hit ? __ffs(hit) - 1 : 31 - __clz(some | 1u);
+            double ahead = __shfl_sync(0xffffffffu, upto, max(owner - 1, 0));
+            if (owner == 0) ahead = 0.;
+            const Pair ws = lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f};
+            Pair c = ws;
+#pragma unroll
+            for (int o = 1; o < kWarps; o <<= 1) {
+                const Pair u = shfl_up(c, o);
+                if (lane >= o) c = add(c, u);
+            }
+            const Pair rest = pair_of(t - ahead);
+            const uint32_t any = __ballot_sync(0xffffffffu, ws.hi > 0.f);
+            const uint32_t pass_it = __ballot_sync(0xffffffffu, ws.hi > 0.f && above(c, rest));
+            const int r = pass_it ? __ffs(pass_it) - 1 : 31 - __clz(any | 1u);
+            Pair start{__shfl_sync(0xffffffffu, c.hi, max(r - 1, 0)), __shfl_sync(0xffffffffu, c.lo, max(r - 1, 0))};
+            if (r == 0) start = Pair{0.f, 0.f};
+            if (lane == 0) {
+                fin.empty = !(all > 0.);
+                fin.owner = owner;
+                fin.run = r;
+                fin.rest = add(rest, Pair{-start.hi, -start.lo});
+            }
+        }
+        if (tid == 0) found = -1;
+        __syncthreads();
+        if (again || !fin.empty || !(w.q || w.gone)) break;
+        w.q = nullptr;  // nothing is left: the target's own row
         w.gone = 0;
         pass();
+        __syncthreads();
     }
+    const int count = st.count;
     if (rank == 0) {
-        const int count = st.count;
         for (int i = tid; i < n; i += kThreads) a.path[b * n + i] = i < count ? path[i] : -1;
         for (int i = tid; i <= n; i += kThreads)
             if (i != count) a.out[b * (n + 1) + i] = i < count ? tok[path[i]] : -1;
         if (tid == 0) {
             a.count[b] = count;
-            if (!(all > 0.)) {
+            if (fin.empty) {
                 a.out[b * (n + 1) + count] = -1;
                 flag_value(a.status);
             }
         }
     }
-    if (!(all > 0.)) return;
-    // the block whose tokens the number falls on: the first whose sum with those before passes it, else
-    // (the number is not below 1) the last that has any
-    const double t = (double)un[n] * all;
-    int owner = -1;
-    {
-        double c = 0.;
-        int last = 0;
-        for (int i = 0; i < C; ++i) {
-            const double s = block_sum[buf ^ 1][i].d();
-            c += s;
-            if (s > 0.) last = i;
-            if (owner < 0 && s > 0. && c > t) owner = i;
-        }
-        if (owner < 0) owner = last;
-    }
-    if (owner != rank) return;
-    // and the warp's run within it
-    int which = -1, last = 0;
-    Pair c{0.f, 0.f}, start{0.f, 0.f};
-    for (int i = 0; i < kWarps; ++i) {
-        const Pair s = warp_sum[i];
-        const Pair next = add(c, s);
-        if (s.hi > 0.f && which < 0 && (before + next.d() > t)) {
-            which = i;
-            start = c;
-        }
-        if (s.hi > 0.f) last = i;
-        c = next;
-    }
-    if (which < 0) {
-        which = last;
-        start = Pair{0.f, 0.f};
-        for (int i = 0; i < last; ++i) start = add(start, warp_sum[i]);
-    }
-    const double from = before + start.d();
-    const int l = min(hi, lo + which * run), h = min(hi, l + run), each = (h - l + kThreads - 1) / kThreads;
+    if (fin.empty || fin.owner != rank) return;
+    // the run's tokens dealt to the threads, neighbours to each
+    const Pair rest = fin.rest;
+    const int l = min(hi, lo + fin.run * run), h = min(hi, l + run), each = (((h - l + kThreads - 1) / kThreads) + 7) & ~7;
     const int v0 = min(h, l + tid * each), v1 = min(h, v0 + each);
-    Pair s{0.f, 0.f};
-    for (int v = v0; v < v1; ++v) s = add(s, w.at(v));
-    Pair upto = s;
+    Pair s{0.f, 0.f}, x[8];
+    for (int v = v0; v < v1; v += 8) {
+        weights_at<T, VEC, 8>(w, v, min(v1, v + 8), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = add(s, x[i]);
+    }
+    Pair c = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Pair u = shfl_up(upto, o);
-        if (lane >= o) upto = add(upto, u);
+        const Pair u = shfl_up(c, o);
+        if (lane >= o) c = add(c, u);
     }
-    if (lane == 31) part[warp] = upto;
-    if (tid == 0) found = -1;
+    if (lane == 31) part[warp] = c;
     __syncthreads();
     Pair ahead{0.f, 0.f};
     for (int i = 0; i < warp; ++i) ahead = add(ahead, part[i]);
-    const Pair prev = shfl_up(upto, 1);
-    const Pair mine = lane > 0 ? add(ahead, prev) : ahead;  // of the threads before this one
+    const Pair prev = shfl_up(c, 1);
+    if (lane > 0) ahead = add(ahead, prev);
     // the first thread whose tokens pass the number, else the last that has any: candidates compete
     // with the former ahead of the latter
-    const bool any = s.hi > 0.f, passes = any && from + add(mine, s).d() > t;
-    if (any) atomicMax(&found, passes ? 2 * kThreads - tid : tid);
+    const bool any = s.hi > 0.f, passes = any && above(add(ahead, s), rest);
+    const int key = passes ? 2 * kThreads - tid : tid;
+    if (any) atomicMax(&found, key);
     __syncthreads();
-    if (!any || found != (passes ? 2 * kThreads - tid : tid)) return;
-    double sum = from + mine.d();
-    int v = -1;
-    for (int i = v0; i < v1; ++i) {
-        const double x = w.at(i).d();
-        if (!(x > 0.)) continue;
-        v = i;
-        sum += x;
-        if (sum > t) break;
+    if (!any || found != key) return;
+    int token = -1;
+    for (int v = v0; v < v1; v += 8) {
+        if (each > 8) weights_at<T, VEC, 8>(w, v, min(v1, v + 8), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (x[i].hi > 0.f && !(token >= 0 && above(ahead, rest))) {
+                token = v + i;
+                ahead = add(ahead, x[i]);
+            }
     }
-    a.out[b * (n + 1) + st.count] = v;
+    a.out[b * (n + 1) + count] = token;
 }
 
 template <typename T>
