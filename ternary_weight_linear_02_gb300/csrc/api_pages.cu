@@ -47,11 +47,7 @@ tl::KvMove move_of(const tl_kv_cache *c, int first, int layers, int *status) {
     tl::KvMove m{};
     m.status = status;
     m.L = layers - first < tl::kMoveLayers ? layers - first : tl::kMoveLayers;
-    if (m.L <= 0) {
-        m.L = 0;
-        m.Hk = 1;
-        return m;
-    }
+    if (m.L == 0) return m;
     m.pages = c->pages;
     m.P = c->page_size;
     m.Hk = c->kv_heads;
@@ -101,7 +97,7 @@ tl_status ternary_pages_reserve(const tl_kv_pages *pages, const int32_t *extra, 
 
 int64_t ternary_pages_fork_workspace(int64_t rows) {
     if (rows < 0 || rows > tl::kMaxPageRows) return -1;
-    return (rows + 1) * (int64_t)sizeof(int32_t);
+    return 16 + rows * (int64_t)sizeof(tl::ForkItem);
 }
 
 tl_status ternary_pages_fork(const tl_kv_pages *pages, const int32_t *parent,
@@ -119,12 +115,13 @@ tl_status ternary_pages_fork(const tl_kv_pages *pages, const int32_t *parent,
     if (const int s = tl::begin_call(&d)) return (tl_status)s;
     a.want = parent;
     a.ok = ok;
-    a.list = static_cast<int *>(workspace);
+    a.listed = static_cast<int *>(workspace);
+    a.items = reinterpret_cast<tl::ForkItem *>(static_cast<char *>(workspace) + 16);
     a.status = d.status;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = tl::launch_pages_take(a, true, st);
     for (int i = 0; e == cudaSuccess && (i == 0 || i < layers); i += tl::kMoveLayers)
-        e = tl::launch_fork_apply(move_of(caches, i, layers, d.status), a.g, parent, a.list, i == 0, d.sm_count, st);
+        e = tl::launch_fork_apply(move_of(caches, i, layers, d.status), a.g, a.listed, a.items, i == 0, d.sm_count, st);
     return from_cuda(e);
 }
 

@@ -9,74 +9,93 @@ namespace tl {
 
 namespace {
 
-// The first n places of one head of a page to another page: keys, values, and their scales.
-__device__ __forceinline__ void copy_head(const KvMove &m, int layer, int h, int src, int dst, int n) {
+constexpr int kMovers = 256;  // threads of a block that closes up a long context
+
+// Copies are dealt to warps: a warp moves the first n places of one head of a page, keys or values, codes
+// and scales, eight 16-byte pieces a lane in flight.  `task` counts (layer, head, keys or values).
+__device__ __forceinline__ void copy_head(const KvMove &m, uint32_t task, int src, int dst, int n) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t lh = task >> 1, layer = lh / (uint32_t)m.Hk, h = lh - layer * (uint32_t)m.Hk;
+    uint8_t *const codes = task & 1u ? m.vc[layer] : m.kc[layer];
+    float *const scales = task & 1u ? m.vs[layer] : m.ks[layer];
     const int64_t s = ((int64_t)src * m.Hk + h) * m.P, d = ((int64_t)dst * m.Hk + h) * m.P;
+    const uint4 *const from = reinterpret_cast<const uint4 *>(codes + s * m.rb);
+    uint4 *const to = reinterpret_cast<uint4 *>(codes + d * m.rb);
     const int pieces = n * (m.rb >> 4);
-    const uint4 *k = reinterpret_cast<const uint4 *>(m.kc[layer] + s * m.rb), *v = reinterpret_cast<const uint4 *>(m.vc[layer] + s * m.rb);
-    uint4 *ko = reinterpret_cast<uint4 *>(m.kc[layer] + d * m.rb), *vo = reinterpret_cast<uint4 *>(m.vc[layer] + d * m.rb);
-    for (int i0 = 0; i0 < pieces; i0 += 512) {
-        const int i = i0 + threadIdx.x, j = i + 256;
-        uint4 a, b, c, e;
-        if (i < pieces) a = k[i], b = v[i];
-        if (j < pieces) c = k[j], e = v[j];
-        if (i < pieces) ko[i] = a, vo[i] = b;
-        if (j < pieces) ko[j] = c, vo[j] = e;
+    float sc[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (e * 32 + lane < n) sc[e] = scales[s + e * 32 + lane];
+    int i = lane;
+    for (; i + 7 * 32 < pieces; i += 8 * 32) {
+        uint4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = from[i + e * 32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[i + e * 32] = v[e];
     }
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const float a = m.ks[layer][s + i], b = m.vs[layer][s + i];
-        m.ks[layer][d + i] = a;
-        m.vs[layer][d + i] = b;
+    {
+        uint4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i + e * 32 < pieces) v[e] = from[i + e * 32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i + e * 32 < pieces) to[i + e * 32] = v[e];
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (e * 32 + lane < n) scales[d + e * 32 + lane] = sc[e];
+    for (int e = 64 + lane; e < n; e += 32) scales[d + e] = scales[s + e];
 }
 
 __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ KvMove m, const int *src, const int *dst, const int *tokens,
-                                                      int64_t n) {
-    const uint32_t per = (uint32_t)(m.L * m.Hk);
-    const int64_t units = n * per;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t i = u / per;
-        const uint32_t lh = (uint32_t)(u - i * per), layer = lh / (uint32_t)m.Hk;
+                                                      uint32_t n) {
+    const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u, total = n * per;
+    for (uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5); u < total; u += gridDim.x * 8u) {
+        const uint32_t i = u / per;
         const int s = src[i], d = dst[i], t = tokens ? tokens[i] : m.P;
         if (s < 0 || d < 0) continue;
         if (s >= m.pages || d >= m.pages || t < 0 || t > m.P) {
-            if (threadIdx.x == 0) flag_value(m.status);
+            if ((threadIdx.x & 31) == 0) flag_value(m.status);
             continue;
         }
-        copy_head(m, (int)layer, (int)(lh - layer * (uint32_t)m.Hk), s, d, t);
+        copy_head(m, u - i * per, s, d, t);
     }
 }
 
-// The rows that pages_take listed (list[0] of them): a unit that shares the full pages, and one for
-// each head and layer of the last page's entries.
-__global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__ KvMove m, KvPages g, const int *parent, const int *list, int share) {
-    const uint32_t per = (uint32_t)(m.L * m.Hk) + (uint32_t)share;
-    const int64_t units = (int64_t)list[0] * per;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t i = u / per;
-        const uint32_t j = (uint32_t)(u - i * per);
-        const int r = list[1 + i], p = parent[r];
-        const uint32_t n = (uint32_t)g.lens[p], full = n / (uint32_t)g.P;
-        const int *from = g.table + p * g.stride;
-        int *to = g.table + r * g.stride;
-        if (share && j == 0) {
-            for (uint32_t e = threadIdx.x; e < full; e += 256) {
-                const int page = from[e];
-                to[e] = page;
-                if ((uint32_t)page < (uint32_t)g.pages) atomicAdd(g.refs + page, 1);
-                else flag_value(m.status);
+// The rows that pages_take listed: their full pages, `runs` of 256 a row (0: not in this launch), and copies of the
+// places in use of their last pages.  A warp a task.
+__global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__ KvMove m, KvPages g, const int *listed,
+                                                         const ForkItem *items, uint32_t runs) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u + runs;
+    const uint64_t total = (uint64_t)*listed * per;
+    for (uint64_t w = blockIdx.x * 8u + (threadIdx.x >> 5); w < total; w += gridDim.x * 8u) {
+        const uint32_t i = total >> 32 ? (uint32_t)(w / per) : (uint32_t)w / per, u = (uint32_t)(w - (uint64_t)i * per);
+        const ForkItem it = items[i];
+        if (u < runs) {
+            const int *const from = g.table + it.parent * g.stride;
+            int *const to = g.table + it.row * g.stride;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t at = (int64_t)u * 256 + e * 32 + lane;
+                if (at < it.full) {
+                    const int page = from[at];
+                    to[at] = page;
+                    if ((uint32_t)page < (uint32_t)g.pages) atomicAdd(g.refs + page, 1);
+                    else flag_value(m.status);
+                }
             }
             continue;
         }
-        const int part = (int)(n - full * (uint32_t)g.P);
-        if (part == 0) continue;
-        const uint32_t lh = j - (uint32_t)share, layer = lh / (uint32_t)m.Hk;
-        const int s = from[full], d = to[full];
-        if ((uint32_t)s >= (uint32_t)g.pages || (uint32_t)d >= (uint32_t)g.pages) {
-            if (threadIdx.x == 0) flag_value(m.status);
+        if (it.places == 0) continue;
+        if ((uint32_t)it.src >= (uint32_t)m.pages || (uint32_t)it.dst >= (uint32_t)m.pages) {
+            if (lane == 0) flag_value(m.status);
             continue;
         }
-        copy_head(m, (int)layer, (int)(lh - layer * (uint32_t)m.Hk), s, d, part);
+        copy_head(m, u - runs, it.src, it.dst, it.places);
     }
 }
 
@@ -110,9 +129,8 @@ struct Moves {
             n = start < 0 || n < 0 ? 0 : (int)a.n;
         }
     }
-    // rows of move i, or false where the sequence's moves end
-    __device__ __forceinline__ bool at(const KvMove &m, const KvCompactArgs &a, int i, int64_t &src, int64_t &dst) const {
-        const int k = keep[i], before = i > 0 ? keep[i - 1] : -1;
+    // rows of move i (k = keep[i], before = keep[i - 1]), or false where the sequence's moves end
+    __device__ __forceinline__ bool rows(const KvMove &m, const KvCompactArgs &a, int i, int k, int before, int64_t &src, int64_t &dst) const {
         const int64_t place = (int64_t)start + k;
         if (k <= before || k < i || place >= a.max_places) {  // (k < i: an earlier one did not ascend)
             flag_value(m.status);
@@ -143,7 +161,7 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
     for (int i0 = 0; i0 < mv.n && more; i0 += 16) {
         int64_t src = -1, dst = -1;
         bool ok = true;
-        if (lane < 16 && i0 + lane < mv.n) ok = mv.at(m, a, i0 + lane, src, dst);
+        if (lane < 16 && i0 + lane < mv.n) ok = mv.rows(m, a, i0 + lane, mv.keep[i0 + lane], i0 + lane > 0 ? mv.keep[i0 + lane - 1] : -1, src, dst);
         const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
         if (bad) {  // nothing from the first bad move on
             more = false;
@@ -177,12 +195,13 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
     }
 }
 
-// Many moves: a block per (sequence, layer, head, keys or values), eight 16-byte pieces a thread in
-// flight, the next group's rows looked up and requested before this one is written.
+// Many moves: a block per (sequence, layer, head, keys or values), eight 16-byte pieces a thread in flight.  While a
+// group's pieces travel, the next one's rows are looked up and the keep of the one after it is requested; the next
+// group is requested before this one is written.
 template <int PIECES>
-__global__ void __launch_bounds__(256) compact_block_kernel(const __grid_constant__ KvMove m, KvCompactArgs a) {
-    constexpr int ROWS = 256 * 8 / PIECES, EACH = ROWS / 256;  // moves a group; looked up by each thread
-    __shared__ int64_t rows[2][2][ROWS];                       // [buffer][from, to]; -1: nothing to move
+__global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_constant__ KvMove m, KvCompactArgs a) {
+    constexpr int ROWS = kMovers * 8 / PIECES, EACH = ROWS / kMovers;  // moves a group; looked up by each thread
+    extern __shared__ int64_t rows[];                                  // [buffer][from, to][ROWS]; -1: nothing to move
     __shared__ int end;
     const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u, tid = threadIdx.x;
     const int64_t u = blockIdx.x, b = u / per;
@@ -192,16 +211,26 @@ __global__ void __launch_bounds__(256) compact_block_kernel(const __grid_constan
     uint8_t *const codes = rest & 1u ? m.vc[layer] : m.kc[layer];
     float *const scales = rest & 1u ? m.vs[layer] : m.ks[layer];
     if (tid == 0) end = mv.n;
-    __syncthreads();
+    int k[EACH], before[EACH];
+    const auto fetch = [&](int i0) {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int i = i0 + e * kMovers + (int)tid;
+            if (i < mv.n) {
+                k[e] = mv.keep[i];
+                before[e] = i > 0 ? mv.keep[i - 1] : -1;
+            }
+        }
+    };
     const auto look = [&](int i0, int buf) {
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int k = e * 256 + tid, i = i0 + k;
+            const int r = e * kMovers + (int)tid, i = i0 + r;
             int64_t src = -1, dst = -1;
-            if (i < mv.n && !mv.at(m, a, i, src, dst)) atomicMin(&end, i);
+            if (i < mv.n && !mv.rows(m, a, i, k[e], before[e], src, dst)) atomicMin(&end, i);
             if (src < 0 || dst < 0 || src == dst) src = dst = -1;
-            rows[buf][0][k] = src;
-            rows[buf][1][k] = dst;
+            rows[(buf * 2 + 0) * ROWS + r] = src;
+            rows[(buf * 2 + 1) * ROWS + r] = dst;
         }
     };
     uint4 piece[8];
@@ -210,22 +239,27 @@ __global__ void __launch_bounds__(256) compact_block_kernel(const __grid_constan
         const int lim = end - i0;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const int k = p * (ROWS / 8) + (int)tid / PIECES;
-            const int64_t s = rows[buf][0][k];
-            if (s >= 0 && k < lim) piece[p] = *reinterpret_cast<const uint4 *>(codes + ((head + s) * PIECES + tid % PIECES) * 16);
+            const int r = p * (ROWS / 8) + (int)tid / PIECES;
+            const int64_t s = rows[buf * 2 * ROWS + r];
+            if (s >= 0 && r < lim) piece[p] = *reinterpret_cast<const uint4 *>(codes + ((head + s) * PIECES + tid % PIECES) * 16);
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int64_t s = rows[buf][0][e * 256 + tid];
-            if (s >= 0 && e * 256 + (int)tid < lim) scale[e] = scales[head + s];
+            const int r = e * kMovers + (int)tid;
+            const int64_t s = rows[buf * 2 * ROWS + r];
+            if (s >= 0 && r < lim) scale[e] = scales[head + s];
         }
     };
+    fetch(0);
+    __syncthreads();  // end is set
     look(0, 0);
+    fetch(ROWS);
     __syncthreads();
     load(0, 0);
     int buf = 0;
     for (int i0 = 0; i0 < end; i0 += ROWS, buf ^= 1) {
         look(i0 + ROWS, buf ^ 1);
+        fetch(i0 + 2 * ROWS);
         const uint4 was[8] = {piece[0], piece[1], piece[2], piece[3], piece[4], piece[5], piece[6], piece[7]};
         float had[EACH];
 #pragma unroll
@@ -235,14 +269,15 @@ __global__ void __launch_bounds__(256) compact_block_kernel(const __grid_constan
         load(i0 + ROWS, buf ^ 1);
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const int k = p * (ROWS / 8) + (int)tid / PIECES;
-            const int64_t d = rows[buf][1][k];
-            if (d >= 0 && k < lim) *reinterpret_cast<uint4 *>(codes + ((head + d) * PIECES + tid % PIECES) * 16) = was[p];
+            const int r = p * (ROWS / 8) + (int)tid / PIECES;
+            const int64_t d = rows[(buf * 2 + 1) * ROWS + r];
+            if (d >= 0 && r < lim) *reinterpret_cast<uint4 *>(codes + ((head + d) * PIECES + tid % PIECES) * 16) = was[p];
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int64_t d = rows[buf][1][e * 256 + tid];
-            if (d >= 0 && e * 256 + (int)tid < lim) scales[head + d] = had[e];
+            const int r = e * kMovers + (int)tid;
+            const int64_t d = rows[(buf * 2 + 1) * ROWS + r];
+            if (d >= 0 && r < lim) scales[head + d] = had[e];
         }
         __syncthreads();  // rows of this group are done with
     }
@@ -262,7 +297,7 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
         c.count += b0;
         const int64_t units = c.batch * per;
         if (a.n <= 64) compact_warp_kernel<PIECES><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(m, c, units);
-        else compact_block_kernel<PIECES><<<(unsigned)(units * 2), 256, 0, st>>>(m, c);
+        else compact_block_kernel<PIECES><<<(unsigned)(units * 2), kMovers, kMovers * 8 / PIECES * 4 * sizeof(int64_t), st>>>(m, c);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -272,15 +307,30 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_copy(const KvMove &m, const int *src, const int *dst, const int *tokens, int64_t n, int sm_count, cudaStream_t st) {
-    const int64_t units = n * m.L * m.Hk, most = (int64_t)sm_count * 8;
-    kv_copy_kernel<<<(unsigned)(units < most ? units : most), 256, 0, st>>>(m, src, dst, tokens, n);
-    return cudaGetLastError();
+    const int64_t per = (int64_t)m.L * m.Hk * 2, chunk = ((int64_t)1 << 31) / per;  // copies of a launch: tasks fit 32 bits
+    for (int64_t i0 = 0; i0 < n; i0 += chunk) {
+        const int64_t c = n - i0 < chunk ? n - i0 : chunk, blocks = (c * per + 7) / 8, most = (int64_t)sm_count * 8;
+        kv_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(m, src + i0, dst + i0, tokens ? tokens + i0 : nullptr, (uint32_t)c);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
-cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *parent, const int *list, bool share, int sm_count, cudaStream_t st) {
-    const int64_t units = (int64_t)g.rows * (m.L * m.Hk + (share ? 1 : 0)), most = (int64_t)sm_count * 8;
-    fork_apply_kernel<<<(unsigned)(units < most ? units : most), 256, 0, st>>>(m, g, parent, list, share);
-    return cudaGetLastError();
+cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *listed, const ForkItem *items, bool share, int sm_count,
+                              cudaStream_t st) {
+    const int64_t runs = share ? (g.max_pages + 255) / 256 : 0, blocks = (g.rows * ((int64_t)m.L * m.Hk * 2 + runs) + 7) / 8,
+                  most = (int64_t)sm_count * 8;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(blocks < most ? blocks > 0 ? blocks : 1 : most));
+    c.blockDim = dim3(256);
+    c.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, fork_apply_kernel, m, g, listed, items, (uint32_t)runs);
 }
 
 cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {

@@ -13,6 +13,7 @@ namespace {
 
 constexpr uint32_t kSat = (1u << 30) - 1;  // where page counts saturate
 constexpr uint32_t kNeeds = 1u << 31, kBad = 1u << 30;
+constexpr int kListed = 4096;  // free pages that a block lists at a time
 
 // One warp per row: the pages behind the kept ones.
 __global__ void __launch_bounds__(256) pages_free_kernel(KvPages g, const int *keep, int *status) {
@@ -122,10 +123,12 @@ template <bool FORK>
 __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
     __shared__ uint32_t cum[kMaxPageRows];
     __shared__ uint32_t part[32], counts[8];
+    __shared__ uint16_t list[kListed];
     const KvPages &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = gridDim.x, rank = blockIdx.x;
     if (C > 1) cluster_arrive_relaxed();
+    if (FORK) pdl_launch_dependents();
     uint32_t total = 0;
     for (int r0 = 0; r0 < g.rows; r0 += 1024) {
         const int r = r0 + tid;
@@ -174,13 +177,20 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
             if (per > 32768) words = free_words(g.refs, p0 + warp * 1024, hi);
             uint32_t sum;
             const uint32_t n = __popc(words);
-            uint32_t k = below + block_scan<false>(n, part, sum) - n;  // rank of the lane's first free page
-            const uint32_t first = __shfl_sync(0xffffffffu, k, 0);
-            uint32_t at = first;
-            for (int j = 0; j < 32 && at < given; ++j) {
-                const uint32_t w = __shfl_sync(0xffffffffu, words, j);
-                const uint32_t nth = at + __popc(w & ((1u << lane) - 1u));
-                if ((w >> lane & 1u) && nth < given) {
+            const uint32_t k0 = block_scan<false>(n, part, sum) - n;  // the lane's free pages before its own
+            const uint32_t take = min(sum, given - below);
+            // the batch's free pages in order, a part of them at a time, then a thread for each
+            for (uint32_t a0 = 0; a0 < take; a0 += kListed) {
+                uint32_t w = words, k = k0;
+                while (w && k < a0 + kListed) {
+                    const int bit = __ffs(w) - 1;
+                    if (k >= a0) list[k - a0] = (uint16_t)(warp * 1024 + 32 * lane + bit);
+                    w &= w - 1u;
+                    ++k;
+                }
+                __syncthreads();
+                for (uint32_t i = tid; i < min(take - a0, (uint32_t)kListed); i += 1024) {
+                    const uint32_t nth = below + a0 + i;
                     int x = 0, y = g.rows - 1;  // the first row whose sum is above nth
                     while (x < y) {
                         const int m = (x + y) >> 1;
@@ -188,12 +198,12 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
                         else x = m + 1;
                     }
                     const uint32_t before = x > 0 ? cum[x - 1] & kSat : 0u;
-                    const int page = (int)(p0 + warp * 1024 + 32 * j + lane);
+                    const int page = (int)(p0 + list[i]);
                     const uint32_t place = FORK ? (uint32_t)g.lens[a.want[x]] / (uint32_t)g.P : (uint32_t)g.held[x] + (nth - before);
                     g.table[x * g.stride + place] = page;
                     g.refs[page] = 1;
                 }
-                at += __popc(w);
+                __syncthreads();
             }
             below += sum;
         }
@@ -215,16 +225,21 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
             const bool in = r < g.rows, ok = in && served(r), forked = ok && a.want[r] >= 0;
             if (in && a.ok) a.ok[r] = ok;
             uint32_t sum;
-            const uint32_t k = listed + block_scan<false>(forked, part, sum);
+            const uint32_t k = listed + block_scan<false>(forked, part, sum) - forked;
             if (forked) {
-                const int n = g.lens[a.want[r]];
+                const int p = a.want[r], n = g.lens[p], full = (int)((uint32_t)n / (uint32_t)g.P), places = n - full * g.P;
                 g.lens[r] = n;
-                g.held[r] = (int)(((uint32_t)n + (uint32_t)g.P - 1u) / (uint32_t)g.P);
-                a.list[k] = r;
+                g.held[r] = full + (places > 0);
+                ForkItem it{r, p, full, places, -1, -1, 0, 0};
+                if (places > 0) {
+                    it.src = g.table[p * g.stride + full];
+                    it.dst = __ldcg(g.table + r * g.stride + full);  // (written above, by any block of the cluster)
+                }
+                a.items[k] = it;
             }
             listed += sum;
         }
-        if (tid == 0) a.list[0] = (int)listed;
+        if (tid == 0) *a.listed = (int)listed;
     } else {
         for (int r = rank * 1024 + tid; r < g.rows; r += C * 1024) {
             const bool ok = served(r);

@@ -175,7 +175,7 @@ def pages_fork(pages: KVPages, parent: torch.Tensor, layers=None) -> torch.Tenso
             raise ValueError(f"layers must be on {dev} like the pages: they are on {layers.device}")
         array, n = layers._array, layers.count
     lib = _ready or _lib()
-    need = 4 * (pages.rows + 1)   # ternary_pages_fork_workspace
+    need = 16 + 32 * pages.rows   # ternary_pages_fork_workspace
     ok = torch.empty(pages.rows, dtype=torch.bool, device=dev)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
     rc = _launch(dev, lib.ternary_pages_fork, pages._ref, parent.data_ptr(), array, n, ok.data_ptr(), ws.data_ptr(), need)

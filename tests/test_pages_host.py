@@ -62,7 +62,7 @@ def test_fork(lib):
         return lib.ternary_pages_fork(p or pool(), parent, caches, layers, None, ws, size, None)
 
     assert fork(parent=None) == NULL and fork(parent=E + 2) == ALIGN and fork(ws=None) == NULL and fork(ws=A + 8) == ALIGN
-    assert lib.ternary_pages_fork_workspace(3) == 16 and lib.ternary_pages_fork_workspace(-1) == -1
+    assert lib.ternary_pages_fork_workspace(3) == 16 + 3 * 32 and lib.ternary_pages_fork_workspace(-1) == -1
     assert lib.ternary_pages_fork_workspace(8193) == -1
     assert fork(size=15) == SHAPE and fork(layers=-1) == SHAPE and fork(layers=513, caches=many(cache())) == SHAPE
     assert fork(layers=1) == NULL
