@@ -60,6 +60,9 @@ tl_status run(const void *x, int64_t x_stride, const tl_adapters *ad, const int3
     a.vec_a = a.K % 8 == 0;
     a.vec_x = a.vec_a && aligned(x, 16) && x_stride % 8 == 0;
     a.vec_y = columns8 && aligned(y, 16) && aligned(out, 16) && y_stride * size % 16 == 0 && out_stride * size % 16 == 0;
+    a.ranks = a.S * a.R;
+    a.wait_limit = d.wait_limit;
+    a.stall = d.stall;
     a.status = d.status;
     return tl::from_cuda(tl::launch_lora(a, ad->dtype, out_dtype == TL_F32, workspace, d.sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }

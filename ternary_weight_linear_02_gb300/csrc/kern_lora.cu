@@ -73,11 +73,13 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
     for (int64_t t = tid; t < a.M; t += 1024) order[atomicAdd(&cursor[lora_key(a, t)], 1)] = (int)t;
 }
 
-// A tile takes 16 tokens, or 64 (gated 32, whose two halves' sums fill the registers) where the adapters
-// that can be there have more than 32 each on average.
-bool big_tiles(int64_t M, int64_t adapters, int ranks) {
-    const int64_t present = adapters + 1 < M ? adapters + 1 : M;
-    return ranks <= 192 && M > 32 * present;
+// Tiles of 128 tokens where the adapters that can be there have more than 32 each on average and rows
+// of x and a start on 16 bytes; the ranks of one launch's shards then take up to 128 columns of tensor memory, and
+// more shards are more launches (a gated layer's two belong together).
+constexpr int kBigRanks = 128;
+bool big_tiles(const LoraArgs &a) {
+    const int64_t present = a.adapters + 1 < a.M ? a.adapters + 1 : a.M;
+    return a.vec_x && a.R * (a.gated ? 2 : 1) <= kBigRanks && a.M > 32 * present;
 }
 
 int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {
@@ -94,11 +96,11 @@ int64_t lora_workspace(int64_t M, int64_t adapters) {
 
 cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st) {
     LoraArgs a = args;
-    const bool big = big_tiles(a.M, a.adapters, a.S * a.R);
-    const int TM = !big ? 16 : a.gated ? 32 : 64;
+    const bool big = big_tiles(a);
+    const int TM = big ? 128 : 16;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
     a.C = 8;
-    while (a.C > 1 && (int64_t)units * a.C > 4 * sm_count) a.C /= 2;
+    while (a.C > 1 && (int64_t)units * a.C > 2 * sm_count) a.C /= 2;
     a.plan = nullptr;
     if (lora_workspace(a.M, a.adapters) > 0) {
         a.max_tiles = units;
@@ -108,7 +110,19 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
         if (e != cudaSuccess) return e;
         a.plan = plan;
     }
-    return dtype == 1 ? launch_lora_bf16(a, f32, big, units, st) : launch_lora_f16(a, f32, big, units, st);
+    a.overlap = 1;
+    const int shards = a.S, at_once = big ? (kBigRanks / a.R < shards ? kBigRanks / a.R : shards) : shards;
+    for (int s0 = 0; s0 < shards; s0 += at_once) {
+        LoraArgs b = a;
+        b.S = shards - s0 < at_once ? shards - s0 : at_once;
+        b.rank0 = s0 * a.R;
+        for (int i = 0; i < s0; ++i) b.col0 += a.shard[i];
+        for (int i = 0; i < b.S; ++i) b.shard[i] = a.shard[s0 + i];
+        b.overlap = s0 == 0;
+        const cudaError_t e = dtype == 1 ? launch_lora_bf16(b, f32, big, units, st) : launch_lora_f16(b, f32, big, units, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace tl

@@ -4,17 +4,19 @@
 // SiLU-gated product of a fused gate/up layer behind it.
 //
 // One launch.  Work is dealt in tiles of up to TM tokens of one adapter, a cluster of C blocks a tile:
-//   * shrink: each block takes a run of K, its warps chunks of it, and keeps h's partial sums (TM x S R)
-//     in shared memory; they are added over the cluster in a fixed order through distributed
+//   * shrink: each block takes a run of K and keeps h's partial sums (TM x S R) in shared
+//     memory; they are added over the cluster in a fixed order through distributed
 //     shared memory, by every block for itself;
-//   * expand: each block takes a run of output columns, adds h B^T to y and writes.
-// So x and y are read once and out is written once, A and B once per tile.  With few tokens a tile is
-// 16 rows and the adapter's matrices are the traffic; with many it is 64 and the
-// activations are: 0.7 R operations a byte either way, far below what the tensor cores would need to bound
-// it, so warp MMAs fed straight from global memory serve (operands are loaded in the order
-// the fragments want: an MMA sums over k, any order of k will do if both sides share it).
+//   * expand: each block takes a share of the output columns, adds h B^T to y and writes.
+// So x and y are read once and out is written once, A and B once per tile.  Two forms:
+//   * few tokens an adapter: tiles of 16, the adapter's matrices are the traffic.  Warp MMAs fed
+//     straight from global memory (an MMA sums over k: any order of k will do that both operands
+//     share, so every lane loads 16 contiguous bytes);
+//   * many: tiles of 128, the activations are the traffic.  Rows of x and A go through a ring of shared-memory
+//     stages (16-byte copies, whatever the tokens' order) into tcgen05 MMAs, h lies in tensor memory.
+// Either way there are 0.7 R operations a byte: memory bounds it.
 //
-// h enters the second product in 16 bits.  One rounding there would double the error of a 16-bit
+// h enters the second product in 16 bits.  One rounding there would add as much error as that of a 16-bit
 // output, so h is split into two numbers of T (three where bf16 feeds an fp32 output), each the
 // rounded rest of those before: 2^-17 of h or less.  f16 takes a row scaled by a power of two, so that
 // large sums do not overflow.
@@ -25,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace tl {
 
@@ -90,29 +93,45 @@ __device__ __forceinline__ uint4 load8(const T *p, int n, bool vec) {
     return r;
 }
 
-// 8 (or 4) contiguous outputs as floats, of which the first n exist.  Not through the read-only path:
+// N (4 or 8) contiguous elements of y as they are, of which the first n exist.  Not through the read-only path:
 // out may be y.
 template <typename O, int N>
-__device__ __forceinline__ void load_out(const O *p, int n, bool vec, float (&v)[N]) {
-    if (vec && n >= N) {
-        if constexpr (sizeof(O) == 4) {
+struct Raw {
+    static constexpr int WORDS = N * sizeof(O) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const O *p, int n, bool vec) {
+        if (vec && n >= N) {
+            if constexpr (WORDS == 2) {
+                const uint2 r = *reinterpret_cast<const uint2 *>(p);
+                w[0] = r.x, w[1] = r.y;
+            } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(p + i);
-                v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+                for (int i = 0; i < WORDS; i += 4) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + i);
+                    w[i] = r.x, w[i + 1] = r.y, w[i + 2] = r.z, w[i + 3] = r.w;
+                }
             }
+        } else if constexpr (sizeof(O) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
         } else {
-            O h[N];
-            if constexpr (N == 8) *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(p);
-            else *reinterpret_cast<uint2 *>(h) = *reinterpret_cast<const uint2 *>(p);
+            const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = to_f(h[i]);
+            for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) w[i >> 1] |= (uint32_t)u[i] << (16 * (i & 1));
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
     }
-}
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(O) == 4) {
+            return __uint_as_float(w[i]);
+        } else {
+            const uint16_t h = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            return to_f(*reinterpret_cast<const O *>(&h));
+        }
+    }
+};
 template <typename O, int N>
 __device__ __forceinline__ void store_out(O *p, int n, bool vec, const float (&v)[N]) {
     if (vec && n >= N) {
@@ -141,214 +160,461 @@ __device__ __forceinline__ float cl_ld_f32(uint32_t addr) {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+template <bool BIG>
+struct Form {
+    static constexpr int TM = BIG ? 128 : 16;  // tokens of a tile
+    static constexpr int NT = 6, U = 2;        // small: n-tiles of 8 ranks a pass of the shrink; chunks in flight
+    static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
+};
+
 // Sizes of a block's shared memory (bytes), the same on the host.
 struct Smem {
-    int ranks;   // S R
-    int hstride; // elements of T between rows of the split h: LDS.64 of 4 rows hit other banks
-    int part, split, total;  // ends of: partial sums; split h or warps' sums; a row of each warp
-    __host__ __device__ Smem(int tm, int S, int R, int ns, int nt) {
+    int ranks, npad;  // S R, and rounded up to 16
+    int pstride;      // floats between rows of the partial sums: 16-byte stores of 8 rows hit other banks
+    int hstride;      // elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
+    int stage;        // BIG: a stage
+    int split, rows;  // where the split h (small: before that the warps' sums) and the warps' rows begin
+    int total;
+    __host__ __device__ Smem(bool big, int S, int R, int ns) {
+        const int tm = big ? 128 : 16;
         ranks = S * R;
+        npad = (ranks + 15) & ~15;
+        pstride = ranks + 4;
         const int steps = S * ((R + 15) / 16);
         hstride = steps * 16 + (steps % 2 ? 0 : 16);
-        part = tm * ranks * 4;
-        const int hs = ns * tm * hstride * 2, red = 4 * tm * nt * 8 * 4;
-        split = part + (hs > red ? hs : red);
-        total = split + kWarps * ranks * 4;
+        stage = (128 + npad) * 128;
+        split = tm * pstride * 4;
+        const int hs = ns * tm * hstride * 2, red = big ? 0 : 4 * 16 * Form<false>::NT * 8 * 4;
+        rows = split + (hs > red ? hs : red);
+        total = rows + kWarps * ranks * 4;
+        if (big) {
+            const int ring = Form<true>::STAGES * stage;  // done with before the sums are stored
+            total = (total > ring ? total : ring) + 1024; // stages lie on 1024 bytes
+        }
     }
 };
 
-// TM = 16 G tokens a tile.  O: type of y and out.
-template <typename T, typename O, int G, bool GATED>
-__global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ LoraArgs a) {
-    constexpr int TM = 16 * G, NT = G == 1 ? 8 : 4;  // n-tiles of 8 ranks a pass of the shrink
-    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int toks[TM];
-    __shared__ float up[TM];  // what a row of the split h has to be multiplied by
-    __shared__ int tile_a, tile_k, tile_n;
-    __shared__ int hist[kLoraFind + 1], wsum[kWarps], tok_cnt[4][kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
-    const int unit = (int)(blockIdx.x / (unsigned)C);
-    if (C > 1) cluster_arrive_relaxed();
-    // ---- the tile
+// What a block knows of its tile.
+template <int TM>
+struct Tile {
+    int toks[TM];   // tokens, -1 behind the last
+    int adapter, nth, count;
+};
+
+// ---- the tile: looked up in the plan, or found by each block.  False: there are fewer tiles.
+template <int TM>
+__device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int unit, bool report) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.plan != nullptr) {
         pdl_wait();
-        if (unit >= a.plan[0]) {
-            if (C > 1) cluster_wait();
-            return;
-        }
-        const int *tile = a.plan + 4 + 3 * unit;
-        const int ad = tile[0], first = tile[1], n = tile[2];
-        if (tid < TM) toks[tid] = tid < n ? a.plan[4 + 3 * a.max_tiles + first + tid] : -1;
-        if (tid == 0) tile_a = ad, tile_n = n;
-    } else {
-        const int M = (int)a.M, keys = a.adapters + 1;
-        int key[4];
-        for (int i = tid; i < keys; i += kThreads) hist[i] = 0;
-        if (tid < TM) toks[tid] = -1;
-        if (tid == 0) tile_a = -1;
+        if (unit >= a.plan[0]) return false;
+        const int *p = a.plan + 4 + 3 * unit;
+        const int n = p[2];
+        if (tid < TM) tile.toks[tid] = tid < n ? a.plan[4 + 3 * a.max_tiles + p[1] + tid] : -1;
+        if (tid == 0) tile.adapter = p[0], tile.count = n;
         __syncthreads();
+        return true;
+    }
+    __shared__ int hist[kLoraFind + 1], wsum[kWarps], tok_cnt[4][kWarps];
+    const int M = (int)a.M, keys = a.adapters + 1;
+    int key[4];
+    for (int i = tid; i < keys; i += kThreads) hist[i] = 0;
+    if (tid < TM) tile.toks[tid] = -1;
+    if (tid == 0) tile.adapter = -1;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tk = i * kThreads + tid;
-            key[i] = -1;
-            if (tk < M) {
-                key[i] = lora_key(a, tk);
-                if (unit == 0 && rank == 0 && a.which[tk] >= a.adapters) flag_value(a.status);
-                atomicAdd(&hist[key[i]], 1);
-            }
-        }
-        __syncthreads();
-        const int each = (keys + kThreads - 1) / kThreads;  // adapters of a thread, neighbours
-        int mine = 0;
-        for (int i = 0; i < each; ++i) {
-            const int k = tid * each + i;
-            if (k < keys) mine += (hist[k] + TM - 1) / TM;
-        }
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
-        }
-        if (lane == 31) wsum[warp] = upto;
-        __syncthreads();
-        int before = upto - mine;
-        for (int i = 0; i < warp; ++i) before += wsum[i];
-        if (mine > 0 && unit >= before && unit < before + mine) {
-            int u = unit - before;
-            for (int i = 0; i < each; ++i) {
-                const int k = tid * each + i;
-                if (k >= keys) break;
-                const int n = (hist[k] + TM - 1) / TM;
-                if (u < n) {
-                    tile_a = k;
-                    tile_k = u;
-                    tile_n = min(TM, hist[k] - u * TM);
-                    break;
-                }
-                u -= n;
-            }
-        }
-        __syncthreads();
-        if (tile_a < 0) {  // fewer tiles than there might have been
-            if (C > 1) cluster_wait();
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t hit = __ballot_sync(0xffffffffu, key[i] == tile_a);
-            if (lane == 0) tok_cnt[i][warp] = __popc(hit);
-        }
-        __syncthreads();
-        int at = -tile_k * TM;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t hit = __ballot_sync(0xffffffffu, key[i] == tile_a);
-            int r = at;
-            for (int w = 0; w < kWarps; ++w) {
-                const int c = tok_cnt[i][w];
-                if (w < warp) r += c;
-                at += c;
-            }
-            r += __popc(hit & ((1u << lane) - 1u));
-            if (key[i] == tile_a && r >= 0 && r < TM) toks[r] = i * kThreads + tid;
+    for (int i = 0; i < 4; ++i) {
+        const int tk = i * kThreads + tid;
+        key[i] = -1;
+        if (tk < M) {
+            key[i] = lora_key(a, tk);
+            if (report && a.which[tk] >= a.adapters) flag_value(a.status);
+            atomicAdd(&hist[key[i]], 1);
         }
     }
     __syncthreads();
-    const int ad = tile_a, count = tile_n;
-    const bool has = ad < a.adapters;
-    if (!has && !GATED && a.out == a.y) {  // nothing is added to these
-        if (C > 1) cluster_wait();
-        return;
+    const int each = (keys + kThreads - 1) / kThreads;  // adapters of a thread, neighbours
+    int mine = 0;
+    for (int i = 0; i < each; ++i) {
+        const int k = tid * each + i;
+        if (k < keys) mine += (hist[k] + TM - 1) / TM;
     }
-    const int S = a.S, R = a.R, K = (int)a.K;
-    const Smem sz(TM, S, R, NS, NT);
-    float *const part = reinterpret_cast<float *>(smem);
-    T *const hs = reinterpret_cast<T *>(smem + sz.part);
-    float *const red = reinterpret_cast<float *>(smem + sz.part);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+    }
+    if (lane == 31) wsum[warp] = upto;
+    __syncthreads();
+    int before = upto - mine;
+    for (int i = 0; i < warp; ++i) before += wsum[i];
+    if (mine > 0 && unit >= before && unit < before + mine) {
+        int u = unit - before;
+        for (int i = 0; i < each; ++i) {
+            const int k = tid * each + i;
+            if (k >= keys) break;
+            const int n = (hist[k] + TM - 1) / TM;
+            if (u < n) {
+                tile.adapter = k;
+                tile.nth = u;
+                tile.count = min(TM, hist[k] - u * TM);
+                break;
+            }
+            u -= n;
+        }
+    }
+    __syncthreads();
+    if (tile.adapter < 0) return false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, key[i] == tile.adapter);
+        if (lane == 0) tok_cnt[i][warp] = __popc(hit);
+    }
+    __syncthreads();
+    int at = -tile.nth * TM;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, key[i] == tile.adapter);
+        int r = at;
+        for (int w = 0; w < kWarps; ++w) {
+            const int c = tok_cnt[i][w];
+            if (w < warp) r += c;
+            at += c;
+        }
+        r += __popc(hit & ((1u << lane) - 1u));
+        if (key[i] == tile.adapter && r >= 0 && r < TM) tile.toks[r] = i * kThreads + tid;
+    }
+    __syncthreads();
+    return true;
+}
+
+// ---- shrink, few tokens: 16 rows, the warps take chunks of 32 k, operands from global memory to registers.
+template <typename T>
+__device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *A, int c0, int c1,
+                                             float *part, float *red) {
+    constexpr int NT = Form<false>::NT, U = Form<false>::U;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, K = (int)a.K;
+    const T *xr[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        live[i] = i * 8 + g < tile.count;
+        xr[i] = static_cast<const T *>(a.x) + (int64_t)(live[i] ? tile.toks[i * 8 + g] : tile.toks[0]) * a.xs;
+    }
+    const int tiles = sz.ranks >> 3, passes = (tiles + NT - 1) / NT, np = (tiles + passes - 1) / passes;
+    for (int j0 = 0; j0 < tiles; j0 += np) {
+        const int nt = min(np, tiles - j0);
+        float acc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+        for (int c = c0 + warp; c < c1; c += U * kWarps) {
+            uint4 xv[U][2], av[U][NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = (c + u * kWarps) * 32 + t * 8, n = c + u * kWarps < c1 ? K - k : 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) xv[u][i] = load8(xr[i] + k, live[i] ? n : 0, a.vec_x);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) av[u][j] = load8(A + (int64_t)((j0 + j) * 8 + g) * K + k, j < nt ? n : 0, a.vec_a);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t f0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
+                const uint32_t f1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (j < nt) {
+                        mma16816<T>(acc[j], f0, av[u][j].x, av[u][j].y);
+                        mma16816<T>(acc[j], f1, av[u][j].z, av[u][j].w);
+                    }
+            }
+        }
+        // the warps' sums: halves added in a fixed order
+#pragma unroll
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            __syncthreads();
+            if (warp >= half && warp < 2 * half) {
+                float *p = red + (warp - half) * (16 * NT * 8);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[(j * 4 + e) * 32 + lane] = acc[j][e];
+            }
+            __syncthreads();
+            if (warp < half) {
+                const float *p = red + warp * (16 * NT * 8);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] += p[(j * 4 + e) * 32 + lane];
+            }
+        }
+        if (warp == 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (j < nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[((e >> 1) * 8 + g) * sz.pstride + (j0 + j) * 8 + 2 * t + (e & 1)] = acc[j][e];
+        }
+    }
+}
+
+// ---- shrink, many tokens: 128 rows of x and the adapter's rows of A, 64 k a stage (rows of 128 bytes, swizzled as the
+// MMA reads them), copied by all warps; one of them issues a stage's MMAs once all have its copies.  (A ninth warp
+// for that would leave 96 registers a thread instead of 128 with two blocks on an SM.)  Every wait gives up after a
+// while: the sums are NaN then.  On return the sums are stored.
+template <typename T>
+__device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *A, int k0, int k1,
+                                           unsigned char *ring, float *part) {
+    using F = Form<true>;
+    constexpr int ST = F::STAGES, LAG = F::LAG;
+    __shared__ uint64_t full[ST], empty[ST], done, never;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t cols = 32;
+    while (cols < (uint32_t)sz.npad) cols *= 2;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], kThreads);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        mbar_init(&never, 1);
+        dead = 0;
+        fence_barrier_init();
+    }
+    constexpr int kIssuer = kWarps - 1;
+    if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, cols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = tmem_slot;
+    const int n = (k1 - k0 + 63) / 64;
+    const uint32_t idesc = tc::idesc_f16(16, std::is_same<T, __nv_bfloat16>::value) - (2u << 17) + ((uint32_t)(sz.npad >> 3) << 17);
+    const int row = tid >> 1, h = (tid & 1) * 4;  // half a row of either matrix
+    const bool live = row < tile.count, mine = row < sz.npad, real = row < sz.ranks;
+    const T *const x = static_cast<const T *>(a.x) + (int64_t)tile.toks[live ? row : 0] * a.xs;
+    const T *const w = A + (int64_t)(real ? row : 0) * a.K;
+    const uint32_t base = smem_u32(ring) + row * 128;
+    bool ok = true;
+    if (a.stall && warp == kIssuer) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&never, 0, a.wait_limit));
+    // a stage's copies of this thread have landed: say so; the issuer waits for all and multiplies
+    const auto landed = [&](int it) {
+        const int s = it % ST;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&full[s]);
+        if (warp != kIssuer) return;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (it / ST) & 1, a.wait_limit));
+        if (!ok) return;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+            const uint64_t xd = tc::desc_sw128(ring + s * sz.stage), ad = tc::desc_sw128(ring + s * sz.stage + 128 * 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc::mma_ss(tm, xd + kk * 2, ad + kk * 2, idesc, (it | kk) != 0);
+            tc::commit(&empty[s]);
+        }
+        __syncwarp();
+    };
+    for (int it = 0; it < n && ok; ++it) {
+        const int s = it % ST;
+        if (it >= ST) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], (it / ST - 1) & 1, a.wait_limit));
+        if (!ok) break;
+        const uint32_t dst = base + s * sz.stage;
+        const int k = k0 + it * 64;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int kk = k + (h + c) * 8;
+            const bool in = kk < k1;
+            const uint32_t at = dst + (((h + c) ^ (row & 7)) << 4);
+            copy16(at, x + (live && in ? kk : 0), live && in);
+            if (mine) copy16(at + 128 * 128, w + (real && in ? kk : 0), real && in);
+        }
+        copies_commit();
+        if (it >= LAG) {
+            copies_wait<LAG>();
+            landed(it - LAG);
+        }
+    }
+    copies_wait<0>();
+    for (int it = max(0, n - LAG); it < n && ok; ++it) landed(it);
+    if (!ok) dead = 1;
+    if (warp == kIssuer) {
+        if (tc::elect_one()) tc::commit(&done);
+        __syncwarp();
+    }
+    // all MMAs that were issued have ended (or the default limit is over): nothing reads the ring
+    if (!mbar_wait_bounded(&done, 0)) dead = 1;
+    __syncthreads();
+    tc::fence_after_sync();
+    const bool bad = dead != 0;
+    if (bad && tid == 0) atomicExch(a.status, kStatusTimeout);
+    if (warp < 4) {  // lane = row
+        float *const row = part + (warp * 32 + lane) * sz.pstride;
+        for (int c = 0; c < sz.npad; c += 16) {
+            uint32_t r[16];
+            tc::ld_32x32b_x16(tm + ((uint32_t)(warp * 32) << 16) + c, r);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (c + i < sz.ranks) {
+                    const float none = bad ? __uint_as_float(0x7FC00000u) : 0.f;  // (a run of K may be empty)
+                    *reinterpret_cast<float4 *>(row + c + i) =
+                        bad || n == 0 ? make_float4(none, none, none, none)
+                                      : make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+                }
+        }
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    if (warp == kIssuer) tc::tmem_dealloc(tm, cols);
+}
+
+// ---- expand: rows [r0, r0 + 16 G) of the tile, U blocks of 8 J columns (gated: of either half).
+template <typename T, typename O, int TM, int G, int U, bool GATED>
+__device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, const Smem &sz, const T *hs, const float *up, const T *B,
+                                       int sh, int64_t off, int64_t wide, int64_t blk, int64_t stride, int64_t blocks, int r0) {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
+    constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;  // n-tiles a block; contiguous columns of a thread; halves
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
+    const bool has = B != nullptr;
     const O *const y = static_cast<const O *>(a.y);
     O *const out = static_cast<O *>(a.out);
-    if (has) {
-        // ---- shrink
-        const T *const A = static_cast<const T *>(a.a) + (int64_t)ad * sz.ranks * K;
-        const T *xr[2 * G];
-        bool live[2 * G];
+    int64_t col[U];
+    int left[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t b = blk + u * stride;
+        col[u] = off + b * (J * 8);
+        left[u] = b < blocks ? (int)min((int64_t)(J * 8), wide - b * (J * 8)) : 0;
+    }
+    Raw<O, W> yv[U][H][2 * G];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) {
-            const int row = (i >> 1) * 16 + (i & 1) * 8 + g;
-            live[i] = row < count;
-            xr[i] = static_cast<const T *>(a.x) + (int64_t)(live[i] ? toks[row] : toks[0]) * a.xs;
+            const int row = r0 + i * 8 + g, n = left[u] - t * W;
+            if (row < tile.count && n > 0) {
+                const O *p = y + tile.toks[row] * a.ys + col[u] + t * W;
+#pragma unroll
+                for (int q = 0; q < H; ++q) yv[u][q][i].load(p + q * wide, n, a.vec_y);
+            }
         }
-        const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C;
-        const int c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-        for (int r0 = 0; r0 < sz.ranks; r0 += NT * 8) {
-            const int nt = min(NT, (sz.ranks - r0) >> 3);
-            float acc[G][NT][4];
+    float acc[U][H][G][J][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < H; ++q)
 #pragma unroll
             for (int i = 0; i < G; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-            for (int c = c0 + warp; c < c1; c += kWarps) {
-                const int k = c * 32 + t * 8, n = K - k;
-                uint4 xv[2 * G], av[NT];
+                    for (int e = 0; e < 4; ++e) acc[u][q][i][j][e] = 0.f;
+    if (has) {
+        for (int st = 0; st < steps; ++st) {
+            uint2 bv[U][H][J];
+            const int r = st * 16 + 4 * t;
 #pragma unroll
-                for (int i = 0; i < 2 * G; ++i) xv[i] = live[i] ? load8(xr[i] + k, n, a.vec_x) : make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    av[j] = j < nt ? load8(A + (int64_t)(r0 + j * 8 + g) * K + k, n, a.vec_a) : make_uint4(0, 0, 0, 0);
+                for (int q = 0; q < H; ++q)
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const uint32_t f0[4] = {xv[2 * i].x, xv[2 * i + 1].x, xv[2 * i].y, xv[2 * i + 1].y};
-                    const uint32_t f1[4] = {xv[2 * i].z, xv[2 * i + 1].z, xv[2 * i].w, xv[2 * i + 1].w};
+                    for (int j = 0; j < J; ++j) {
+                        // column of the fragment's n = g: such that a thread's results are neighbours
+                        const int c = (g >> 1) * W + 2 * j + (g & 1);
+                        bv[u][q][j] = c < left[u] && r < R ? ldg_nc_v2(B + (q * wide + col[u] + c) * R + r) : make_uint2(0, 0);
+                    }
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        if (j < nt) {
-                            mma16816<T>(acc[i][j], f0, av[j].x, av[j].y);
-                            mma16816<T>(acc[i][j], f1, av[j].z, av[j].w);
-                        }
-                }
-            }
-            // the warps' sums: halves added in a fixed order
+            for (int i = 0; i < G; ++i)
 #pragma unroll
-            for (int half = kWarps / 2; half > 0; half >>= 1) {
-                __syncthreads();
-                if (warp >= half && warp < 2 * half) {
-                    float *p = red + (warp - half) * (TM * NT * 8);
+                for (int q = 0; q < H; ++q)
 #pragma unroll
-                    for (int i = 0; i < G; ++i)
+                    for (int n = 0; n < NS; ++n) {
+                        const T *h = hs + (n * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + 4 * t;
+                        const uint2 x = *reinterpret_cast<const uint2 *>(h), z = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                        const uint32_t f[4] = {x.x, z.x, x.y, z.y};
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
+                        for (int u = 0; u < U; ++u)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) p[((i * NT + j) * 4 + e) * 32 + lane] = acc[i][j][e];
-                }
-                __syncthreads();
-                if (warp < half) {
-                    const float *p = red + warp * (TM * NT * 8);
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][j][e] += p[((i * NT + j) * 4 + e) * 32 + lane];
-                }
-            }
-            if (warp == 0) {
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        if (j < nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                part[(i * 16 + (e >> 1) * 8 + g) * sz.ranks + r0 + j * 8 + 2 * t + (e & 1)] = acc[i][j][e];
-            }
+                            for (int j = 0; j < J; ++j) mma16816<T>(acc[u][q][i][j], f, bv[u][q][j].x, bv[u][q][j].y);
+                    }
         }
-        __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) {
+            const int row = r0 + i * 8 + g, n = left[u] - t * W;
+            if (row >= tile.count || n <= 0) continue;
+            const float f = has ? up[row] : 0.f;
+            float v[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                v[j] = yv[u][0][i][j];
+                if (has) v[j] = __fmaf_rn(acc[u][0][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, v[j]);
+                if constexpr (GATED) {
+                    float w = yv[u][1][i][j];
+                    if (has) w = __fmaf_rn(acc[u][1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, w);
+                    v[j] = silu(v[j]) * w;
+                }
+            }
+            store_out<O, W>(out + tile.toks[row] * a.os + col[u] + t * W, n, a.vec_y, v);
+        }
+}
+
+// O: type of y and out.
+template <typename T, typename O, bool BIG, bool GATED>
+__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+    using F = Form<BIG>;
+    constexpr int TM = F::TM;
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char *const smem = BIG ? smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) : smem_raw;
+    __shared__ Tile<TM> tile;
+    __shared__ float up[TM];  // what a row of the split h has to be multiplied by
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
+    const int unit = (int)(blockIdx.x / (unsigned)C);
+    if (C > 1) cluster_arrive_relaxed();
+    const bool any = find_tile<TM>(a, tile, unit, unit == 0 && rank == 0);
+    const int ad = any ? tile.adapter : a.adapters;
+    const bool has = ad < a.adapters;
+    if (!any || (!has && !GATED && a.out == a.y)) {  // fewer tiles, or tokens to which nothing is added in place
+        if (C > 1) cluster_wait();
+        return;
+    }
+    const int S = a.S, R = a.R, K = (int)a.K, steps = (R + 15) / 16;
+    const Smem sz(BIG, S, R, NS);
+    float *const part = reinterpret_cast<float *>(smem);
+    T *const hs = reinterpret_cast<T *>(smem + sz.split);
+    const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
+    if (has) {
+        const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
+        if constexpr (BIG) {
+            const int chunks = (K + 63) / 64, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
+            shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
+        } else {
+            const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
+            shrink_small<T>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.split));
+            __syncthreads();
+        }
     }
     if (C > 1) {
         cluster_wait();  // (every block has started)
@@ -358,18 +624,21 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ 
     if (has) {
         // ---- h = s (the blocks' sums, in their order), split into NS numbers of T; a warp per row
         const float s = a.scale ? a.scale[ad] : 1.f;
-        const int steps = (R + 15) / 16;
-        float *const mine = reinterpret_cast<float *>(smem + sz.split) + warp * sz.ranks;
+        float *const mine = reinterpret_cast<float *>(smem + sz.rows) + warp * sz.ranks;
         for (int row = warp; row < TM; row += kWarps) {
             uint32_t top = 0;
             for (int e = lane; e < sz.ranks; e += 32) {
                 float v = 0.f;
-                if (row < count) {
+                if (row < tile.count) {
                     if (C > 1) {
-                        const uint32_t at = smem_u32(part + row * sz.ranks + e);
-                        for (int i = 0; i < C; ++i) v += cl_ld_f32(cl_map(at, i));
+                        const uint32_t at = smem_u32(part + row * sz.pstride + e);
+                        float p[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) p[i] = i < C ? cl_ld_f32(cl_map(at, i)) : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v += p[i];
                     } else {
-                        v = part[row * sz.ranks + e];
+                        v = part[row * sz.pstride + e];
                     }
                     v *= s;
                 }
@@ -399,86 +668,25 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ 
     }
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
-    // ---- expand: columns in blocks of 32 (gated: 16 of either half), dealt to the cluster's warps
     {
-        constexpr int J = GATED ? 2 : 4, W = 2 * J;  // n-tiles a block; contiguous columns of a thread
-        const T *const B = static_cast<const T *>(a.b) + (has ? (int64_t)ad * a.N * R : 0);
-        const int steps = (R + 15) / 16, kk = C * kWarps;
-        const int shards = GATED ? 1 : S;
-        int skip = rank * kWarps + warp;  // blocks of columns before this warp's next one
-        int64_t off = 0;
+        // columns in blocks of 32 (gated: 16 of either half), and (BIG) runs of 32 rows, dealt to the cluster's warps
+        constexpr int G = BIG ? 2 : 1, U = BIG ? 1 : 2, J = GATED ? 2 : 4;
+        const int kk = C * kWarps, shards = GATED ? 1 : S;
+        const int runs = BIG ? (tile.count + 16 * G - 1) / (16 * G) : 1;
+        int64_t skip = rank * kWarps + warp, off = a.col0;  // items before this warp's next one
         for (int sh = 0; sh < shards; ++sh) {
-            const int64_t wide = a.shard[sh];
-            const int64_t blocks = (wide + J * 8 - 1) / (J * 8);
-            int64_t blk = skip;
-            for (; blk < blocks; blk += kk) {
-                const int64_t col0 = off + blk * (J * 8);       // first column
-                const int left = (int)min((int64_t)(J * 8), wide - blk * (J * 8));
-                constexpr int H = GATED ? 2 : 1;
-                float acc[H][G][J][4];
-#pragma unroll
-                for (int p = 0; p < H; ++p)
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[p][i][j][e] = 0.f;
-                if (has) {
-                    for (int st = 0; st < steps; ++st) {
-                        uint2 bv[H][J];
-                        const int r = st * 16 + 4 * t;
-#pragma unroll
-                        for (int p = 0; p < H; ++p)
-#pragma unroll
-                            for (int j = 0; j < J; ++j) {
-                                // column of the fragment's n = g: such that a thread's results are neighbours
-                                const int c = (g >> 1) * W + 2 * j + (g & 1);
-                                bv[p][j] = c < left && r < R ? ldg_nc_v2(B + (p * wide + col0 + c) * R + r) : make_uint2(0, 0);
-                            }
-#pragma unroll
-                        for (int i = 0; i < G; ++i)
-#pragma unroll
-                            for (int p = 0; p < H; ++p)
-#pragma unroll
-                                for (int n = 0; n < NS; ++n) {
-                                    const T *h = hs + (n * TM + i * 16 + g) * sz.hstride + ((GATED ? p : sh) * steps + st) * 16 + 4 * t;
-                                    const uint2 lo = *reinterpret_cast<const uint2 *>(h), hi = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                                    const uint32_t f[4] = {lo.x, hi.x, lo.y, hi.y};
-#pragma unroll
-                                    for (int j = 0; j < J; ++j) mma16816<T>(acc[p][i][j], f, bv[p][j].x, bv[p][j].y);
-                                }
-                    }
+            const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8), items = blocks * runs;
+            int64_t it = skip;
+            if constexpr (BIG) {
+                for (; it < items; it += kk) {
+                    const int64_t blk = it / runs;
+                    expand<T, O, TM, G, 1, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, 0, blocks, (int)(it - blk * runs) * 16 * G);
                 }
-                const int n = left - t * W;
-                if (n > 0) {
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int row = i * 16 + q * 8 + g;
-                            if (row >= count) continue;
-                            const int64_t tok = toks[row], col = col0 + t * W;
-                            const float f = has ? up[row] : 0.f;
-                            float v[W];
-                            load_out<O, W>(y + tok * a.ys + col, n, a.vec_y, v);
-#pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                if (has) v[j] = __fmaf_rn(acc[0][i][j >> 1][2 * q + (j & 1)], f, v[j]);
-                            if constexpr (GATED) {
-                                float w[W];
-                                load_out<O, W>(y + tok * a.ys + wide + col, n, a.vec_y, w);
-#pragma unroll
-                                for (int j = 0; j < W; ++j) {
-                                    if (has) w[j] = __fmaf_rn(acc[1][i][j >> 1][2 * q + (j & 1)], f, w[j]);
-                                    v[j] = silu(v[j]) * w[j];
-                                }
-                            }
-                            store_out<O, W>(out + tok * a.os + col, n, a.vec_y, v);
-                        }
-                }
+            } else {
+                for (; it < items; it += (int64_t)U * kk) expand<T, O, TM, 1, U, GATED>(a, tile, sz, hs, up, B, sh, off, wide, it, kk, blocks, 0);
+                while (it - kk >= items) it -= kk;  // the first of its items that is not here
             }
-            skip = (int)(blk - blocks);
+            skip = it - items;
             off += wide;
         }
     }
@@ -499,13 +707,12 @@ cudaError_t allow_smem(std::atomic<uint64_t> &done, K *kernel) {
     return e;
 }
 
-template <typename T, typename O, int G, bool GATED>
+template <typename T, typename O, bool BIG, bool GATED>
 cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
-    constexpr int TM = 16 * G, NT = G == 1 ? 8 : 4;
     constexpr int NS = std::is_same<T, __nv_bfloat16>::value && sizeof(O) == 4 ? 3 : 2;
-    const Smem sz(TM, a.S, a.R, NS, NT);
+    const Smem sz(BIG, a.S, a.R, NS);
     static std::atomic<uint64_t> done{0};
-    if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, G, GATED>)) return e;
+    if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>)) return e;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)units * (unsigned)a.C);
     c.blockDim = dim3(kThreads);
@@ -517,24 +724,24 @@ cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     at[n].val.clusterDim.x = (unsigned)a.C;
     at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
     ++n;
-    if (a.plan) {
+    if (a.plan && a.overlap) {
         at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
     }
     c.attrs = at;
     c.numAttrs = n;
-    return cudaLaunchKernelEx(&c, lora_kernel<T, O, G, GATED>, a);
+    return cudaLaunchKernelEx(&c, lora_kernel<T, O, BIG, GATED>, a);
 }
 
 template <typename T>
 cudaError_t launch_type(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st) {
     if (a.gated) {
-        if (f32) return big ? launch_one<T, float, 2, true>(a, units, st) : launch_one<T, float, 1, true>(a, units, st);
-        return big ? launch_one<T, T, 2, true>(a, units, st) : launch_one<T, T, 1, true>(a, units, st);
+        if (f32) return big ? launch_one<T, float, true, true>(a, units, st) : launch_one<T, float, false, true>(a, units, st);
+        return big ? launch_one<T, T, true, true>(a, units, st) : launch_one<T, T, false, true>(a, units, st);
     }
-    if (f32) return big ? launch_one<T, float, 4, false>(a, units, st) : launch_one<T, float, 1, false>(a, units, st);
-    return big ? launch_one<T, T, 4, false>(a, units, st) : launch_one<T, T, 1, false>(a, units, st);
+    if (f32) return big ? launch_one<T, float, true, false>(a, units, st) : launch_one<T, float, false, false>(a, units, st);
+    return big ? launch_one<T, T, true, false>(a, units, st) : launch_one<T, T, false, false>(a, units, st);
 }
 
 }  // namespace lora

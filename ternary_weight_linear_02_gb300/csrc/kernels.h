@@ -292,13 +292,18 @@ struct KvPages {
     int64_t stride, pages, max_pages;
     int rows, P;
 };
+struct alignas(16) ForkItem {
+    int row, parent, full, places;  // full pages, places in use of the last one
+    int src, dst, pad0, pad1;       // pages of those places
+};
 struct PagesTakeArgs {
     KvPages g;
     const int *want;   // extra tokens, or parents
     long long *slots;  // [rows, width]
     int width;
     uint8_t *ok;
-    int *list;         // fork: count, then the rows forked
+    int *listed;       // fork: how many rows were forked, and what is to be done for each
+    ForkItem *items;
     int *status;
 };
 cudaError_t launch_pages_free(const KvPages &g, const int *keep, int *status, cudaStream_t st);
@@ -315,9 +320,9 @@ struct KvMove {
 };
 cudaError_t launch_kv_copy(const KvMove &m, const int *src, const int *dst, const int *tokens, int64_t n,
                            int sm_count, cudaStream_t st);
-// the rows listed by launch_pages_take: shared pages (where share) and copies of the last ones
-cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *parent, const int *list, bool share,
-                              int sm_count, cudaStream_t st);
+// the rows listed by launch_pages_take: their shared pages (where share), and copies of the last ones
+cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *listed, const ForkItem *items, bool share, int sm_count,
+                              cudaStream_t st);
 struct KvCompactArgs {
     const int *table;
     int64_t table_stride, max_places;
@@ -356,11 +361,16 @@ struct LoraArgs {
     int64_t M, N, K;     // N: columns of y
     int64_t shard[kMaxShards];
     int S, R, adapters;
+    int ranks, rank0;         // rows of a for an adapter; the first of this launch's shards
+    int64_t col0;             // first column of this launch's shards
     int gated;
     int vec_x, vec_a, vec_y;  // rows start on 16-byte boundaries (y, out: columns of threads too)
     int C;                    // blocks of a cluster
     const int *plan;          // tiles found beforehand (null: by each block)
     int max_tiles;
+    int overlap;              // the launch before is the plan's
+    int stall;                // testing aid (CallDevice)
+    long long wait_limit;
     int *status;
 };
 // tokens and adapters up to which no workspace is needed: each block finds its tile by itself

@@ -81,7 +81,7 @@ CASES = [  # tokens, inputs, shards, rank, adapters
     (1, 64, (32,), 8, 1), (1, 3584, (3584, 512, 512), 16, 3), (16, 1024, (1024,), 16, 8), (7, 200, (40, 8, 24), 24, 2),
     (33, 1000, (72, 56), 32, 5), (64, 4096, (256,), 64, 64), (100, 264, (96,), 128, 3), (257, 512, (320,), 16, 2),
     (300, 2048, (128, 64), 64, 4), (1024, 256, (64,), 8, 700), (1025, 256, (64,), 8, 3), (3001, 320, (104,), 16, 40),
-    (2000, 96, (32,) * 8, 128, 7), (90, 72, (16,), 8, 2000), (1, 8, (8,), 8, 1)]
+    (2000, 96, (32,) * 8, 128, 7), (700, 136, (24, 8) * 4, 24, 5), (500, 4096, (48, 16, 16), 64, 2), (129, 8, (40,), 16, 1), (90, 72, (16,), 8, 2000), (1, 8, (8,), 8, 1)]
 
 
 @pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torch.bfloat16, torch.float32),
