@@ -22,11 +22,11 @@
 // large sums do not overflow.
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc.cuh"
 
 namespace tl {
@@ -693,26 +693,14 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     if (C > 1) cl_wait_acquire();
 }
 
-// Raises the kernel's shared-memory limit on the current device, once per device.
 constexpr int kMaxSmem = 200 * 1024;
-template <typename K>
-cudaError_t allow_smem(std::atomic<uint64_t> &done, K *kernel) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
 
 template <typename T, typename O, bool BIG, bool GATED>
 cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     constexpr int NS = std::is_same<T, __nv_bfloat16>::value && sizeof(O) == 4 ? 3 : 2;
     const Smem sz(BIG, a.S, a.R, NS);
     static std::atomic<uint64_t> done{0};
-    if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>)) return e;
+    if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>, kMaxSmem)) return e;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)units * (unsigned)a.C);
     c.blockDim = dim3(kThreads);
