@@ -52,5 +52,5 @@ extern "C" tl_status ternary_verify_drafts(const void *target, int64_t target_ba
     };
     const bool vec = rows16(target, target_batch_stride, target_node_stride) &&
                      (!a.draft || rows16(draft_probs, draft_batch_stride, draft_node_stride));
-    return tl::from_cuda(tl::launch_verify(a, dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
+    return tl::from_cuda(tl::launch_verify(a, dtype, vec, d.sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -1,10 +1,22 @@
 // kern_lora.cu -- low-rank adapters: which tiles, and how they are dealt (the kernel is in
 // kern_lora.cuh).
+#include <climits>
+
 #include "kern_lora.cuh"
 
 namespace tl {
 
 namespace {
+
+// Lanes of one key count together, since runs of tokens would queue up at one address: the lanes of this lane's
+// key, and the count of the key before this lane's (negative keys are not counted).
+__device__ __forceinline__ uint32_t same_key(int key) { return __match_any_sync(0xffffffffu, key); }
+__device__ __forceinline__ int count_key(int *counts, int key, uint32_t same) {
+    const int lane = threadIdx.x & 31, leader = __ffs(same) - 1;
+    int base = 0;
+    if (lane == leader && key >= 0) base = atomicAdd(&counts[key], __popc(same));
+    return __shfl_sync(0xffffffffu, base, leader) + __popc(same & ((1u << lane) - 1u));
+}
 
 // Tokens sorted by adapter and cut into tiles of TM, for more tokens or adapters than each block
 // looks through by itself.  plan: [0] tiles, from 4 on (adapter, first, tokens) of each, then the
@@ -13,14 +25,33 @@ namespace {
 __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int *plan) {
     extern __shared__ int sh[];
     __shared__ int wsum[32], wtile[32];
+    constexpr int N = 8;  // tokens of a thread looked up together (kept, where these are all)
     const int keys = a.adapters + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *const cursor = sh, *const first = sh + keys + 1, *const tile = first + keys + 1;
     pdl_launch_dependents();
+    int key[N];
+    uint32_t same[N];
+    const auto look = [&](int64_t t0, bool report) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t t = t0 + i * 1024 + tid;
+            key[i] = t < a.M ? a.which[t] : INT_MIN;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (report && key[i] >= a.adapters) flag_value(a.status);
+            key[i] = key[i] == INT_MIN && t0 + i * 1024 + tid >= a.M ? -1 : key[i] >= 0 && key[i] < a.adapters ? key[i] : a.adapters;
+        }
+    };
     for (int i = tid; i < keys; i += 1024) cursor[i] = 0;
     __syncthreads();
-    for (int64_t t = tid; t < a.M; t += 1024) {
-        if (a.which[t] >= a.adapters) flag_value(a.status);
-        atomicAdd(&cursor[lora_key(a, t)], 1);
+    for (int64_t t0 = 0; t0 < a.M; t0 += N * 1024) {
+        look(t0, true);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            same[i] = same_key(key[i]);
+            count_key(cursor, key[i], same[i]);
+        }
     }
     __syncthreads();
     // running sums of tokens and of tiles over the adapters
@@ -44,7 +75,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
         const int k = tid * each + i;
         if (k < keys) {
             const int c = cursor[k];
-            first[k] = bn;
+            first[k] = cursor[k] = bn;
             tile[k] = bm;
             bn += c;
             bm += (c + TM - 1) / TM;
@@ -52,11 +83,21 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
         }
     }
     __syncthreads();
-    for (int i = tid; i < keys; i += 1024) cursor[i] = first[i];
+    int *const order = plan + 4 + 3 * a.max_tiles;
+    for (int64_t t0 = 0; t0 < a.M; t0 += N * 1024) {
+        const bool again = a.M > N * 1024;
+        if (again) look(t0, false);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (again) same[i] = same_key(key[i]);
+            const int at = count_key(cursor, key[i], same[i]);
+            if (key[i] >= 0) order[at] = (int)(t0 + i * 1024 + tid);
+        }
+    }
     const int tiles = tile[keys];
     if (tid == 0) plan[0] = tiles;
     for (int u = tid; u < tiles; u += 1024) {
-        int x = 0, y = keys - 1;  // the last adapter whose tiles begin at or before u and that has any
+        int x = 0, y = keys - 1;  // the last adapter whose tiles begin at or before u: it has some
         while (x < y) {
             const int mid = (x + y + 1) >> 1;
             if (tile[mid] <= u) x = mid;
@@ -68,9 +109,6 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
         p[1] = at;
         p[2] = min(TM, first[x + 1] - at);
     }
-    __syncthreads();
-    int *const order = plan + 4 + 3 * a.max_tiles;
-    for (int64_t t = tid; t < a.M; t += 1024) order[atomicAdd(&cursor[lora_key(a, t)], 1)] = (int)t;
 }
 
 // Tiles of 128 tokens where the adapters that can be there have more than 32 each on average and rows
@@ -100,7 +138,7 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
     const int TM = big ? 128 : 16;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
     a.C = 8;
-    while (a.C > 1 && (int64_t)units * a.C > 2 * sm_count) a.C /= 2;
+    while (a.C > 1 && (int64_t)units * a.C > (big ? 2 : 4) * sm_count) a.C /= 2;
     a.plan = nullptr;
     if (lora_workspace(a.M, a.adapters) > 0) {
         a.max_tiles = units;

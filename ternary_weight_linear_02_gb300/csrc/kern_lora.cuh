@@ -158,7 +158,14 @@ __device__ __forceinline__ float cl_ld_f32(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+__device__ __forceinline__ float4 cl_ld_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// (the quotient within 2 ulp; 0 instead of less than 2^-119 below g = -87)
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
 
 // 16 bytes from global to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
@@ -174,8 +181,9 @@ __device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("pre
 template <bool BIG>
 struct Form {
     static constexpr int TM = BIG ? 128 : 16;  // tokens of a tile
-    static constexpr int NT = 6, U = 2;        // small: n-tiles of 8 ranks a pass of the shrink; chunks in flight
+    static constexpr int NT = 6, U = 1;        // small: n-tiles of 8 ranks a pass of the shrink; chunks in flight
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
+    static constexpr int Q = BIG ? 4 : 2;      // steps of 16 ranks whose entries of B a thread holds
 };
 
 // Sizes of a block's shared memory (bytes), the same on the host.
@@ -184,7 +192,7 @@ struct Smem {
     int pstride;      // floats between rows of the partial sums: 16-byte stores of 8 rows hit other banks
     int hstride;      // elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
     int stage;        // BIG: a stage
-    int split, rows;  // where the split h (small: before that the warps' sums) and the warps' rows begin
+    int split;        // where the split h begins (small: before that the warps' sums)
     int total;
     __host__ __device__ Smem(bool big, int S, int R, int ns) {
         const int tm = big ? 128 : 16;
@@ -196,8 +204,7 @@ struct Smem {
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
         const int hs = ns * tm * hstride * 2, red = big ? 0 : 4 * 16 * Form<false>::NT * 8 * 4;
-        rows = split + (hs > red ? hs : red);
-        total = rows + kWarps * ranks * 4;
+        total = split + (hs > red ? hs : red);
         if (big) {
             const int ring = Form<true>::STAGES * stage;  // done with before the sums are stored
             total = (total > ring ? total : ring) + 1024; // stages lie on 1024 bytes
@@ -484,10 +491,10 @@ __device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &t
     if (warp == kIssuer) tc::tmem_dealloc(tm, cols);
 }
 
-// ---- expand: rows [r0, r0 + 16 G) of the tile, U blocks of 8 J columns (gated: of either half).
-template <typename T, typename O, int TM, int G, int U, bool GATED>
+// ---- expand: rows [r0, r0 + 16 G) of the tile, a block of 8 J columns (gated: of either half), any sizes.
+template <typename T, typename O, int TM, int G, bool GATED>
 __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, const Smem &sz, const T *hs, const float *up, const T *B,
-                                       int sh, int64_t off, int64_t wide, int64_t blk, int64_t stride, int64_t blocks, int r0) {
+                                       int sh, int64_t off, int64_t wide, int64_t blk, int r0) {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
     constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
     constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;  // n-tiles a block; contiguous columns of a thread; halves
@@ -495,92 +502,178 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
     const bool has = B != nullptr;
     const O *const y = static_cast<const O *>(a.y);
     O *const out = static_cast<O *>(a.out);
-    int64_t col[U];
-    int left[U];
+    const int64_t col = off + blk * (J * 8);
+    const int left = (int)min((int64_t)(J * 8), wide - blk * (J * 8)), n = left - t * W;
+    Raw<O, W> yv[H][2 * G];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t b = blk + u * stride;
-        col[u] = off + b * (J * 8);
-        left[u] = b < blocks ? (int)min((int64_t)(J * 8), wide - b * (J * 8)) : 0;
-    }
-    Raw<O, W> yv[U][H][2 * G];
+    for (int i = 0; i < 2 * G; ++i) {
+        const int row = r0 + i * 8 + g;
+        if (row < tile.count && n > 0) {
+            const O *p = y + tile.toks[row] * a.ys + col + t * W;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 2 * G; ++i) {
-            const int row = r0 + i * 8 + g, n = left[u] - t * W;
-            if (row < tile.count && n > 0) {
-                const O *p = y + tile.toks[row] * a.ys + col[u] + t * W;
-#pragma unroll
-                for (int q = 0; q < H; ++q) yv[u][q][i].load(p + q * wide, n, a.vec_y);
-            }
+            for (int q = 0; q < H; ++q) yv[q][i].load(p + q * wide, n, a.vec_y);
         }
-    float acc[U][H][G][J][4];
+    }
+    float acc[H][G][J][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int q = 0; q < H; ++q)
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[q][i][j][e] = 0.f;
+    for (int st = 0; has && st < steps; ++st) {
+        uint2 bv[H][J];
+        const int r = st * 16 + 4 * t;
 #pragma unroll
         for (int q = 0; q < H; ++q)
 #pragma unroll
-            for (int i = 0; i < G; ++i)
+            for (int j = 0; j < J; ++j) {
+                // column of the fragment's n = g: such that a thread's results are neighbours
+                const int c = (g >> 1) * W + 2 * j + (g & 1);
+                bv[q][j] = c < left && r < R ? ldg_nc_v2(B + (q * wide + col + c) * R + r) : make_uint2(0, 0);
+            }
 #pragma unroll
-                for (int j = 0; j < J; ++j)
+        for (int i = 0; i < G; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[u][q][i][j][e] = 0.f;
-    if (has) {
-        for (int st = 0; st < steps; ++st) {
-            uint2 bv[U][H][J];
-            const int r = st * 16 + 4 * t;
+            for (int q = 0; q < H; ++q)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int s = 0; s < NS; ++s) {
+                    const T *h = hs + (s * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + 4 * t;
+                    const uint2 x = *reinterpret_cast<const uint2 *>(h), z = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                    const uint32_t f[4] = {x.x, z.x, x.y, z.y};
 #pragma unroll
-                for (int q = 0; q < H; ++q)
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        // column of the fragment's n = g: such that a thread's results are neighbours
-                        const int c = (g >> 1) * W + 2 * j + (g & 1);
-                        bv[u][q][j] = c < left[u] && r < R ? ldg_nc_v2(B + (q * wide + col[u] + c) * R + r) : make_uint2(0, 0);
-                    }
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-#pragma unroll
-                for (int q = 0; q < H; ++q)
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        const T *h = hs + (n * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + 4 * t;
-                        const uint2 x = *reinterpret_cast<const uint2 *>(h), z = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                        const uint32_t f[4] = {x.x, z.x, x.y, z.y};
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int j = 0; j < J; ++j) mma16816<T>(acc[u][q][i][j], f, bv[u][q][j].x, bv[u][q][j].y);
-                    }
-        }
+                    for (int j = 0; j < J; ++j) mma16816<T>(acc[q][i][j], f, bv[q][j].x, bv[q][j].y);
+                }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < 2 * G; ++i) {
+        const int row = r0 + i * 8 + g;
+        if (row >= tile.count || n <= 0) continue;
+        const float f = !has ? 0.f : kBf ? 1.f : up[row];
+        float v[W];
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) {
-            const int row = r0 + i * 8 + g, n = left[u] - t * W;
-            if (row >= tile.count || n <= 0) continue;
-            const float f = has ? up[row] : 0.f;
-            float v[W];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                v[j] = yv[u][0][i][j];
-                if (has) v[j] = __fmaf_rn(acc[u][0][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, v[j]);
-                if constexpr (GATED) {
-                    float w = yv[u][1][i][j];
-                    if (has) w = __fmaf_rn(acc[u][1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, w);
-                    v[j] = silu(v[j]) * w;
-                }
+        for (int j = 0; j < W; ++j) {
+            v[j] = yv[0][i][j];
+            if (has) v[j] = __fmaf_rn(acc[0][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, v[j]);
+            if constexpr (GATED) {
+                float w = yv[1][i][j];
+                if (has) w = __fmaf_rn(acc[1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, w);
+                v[j] = silu(v[j]) * w;
             }
-            store_out<O, W>(out + tile.toks[row] * a.os + col[u] + t * W, n, a.vec_y, v);
         }
+        store_out<O, W>(out + tile.toks[row] * a.os + col + t * W, n, a.vec_y, v);
+    }
+}
+
+// ---- expand where whole blocks of columns start on 16 bytes and a thread holds its entries of B for all ranks: they
+// are loaded once for all rows of the tile, pointers move along without products.
+template <typename T, typename O, int TM, bool GATED>
+__device__ __forceinline__ void expand_whole(const LoraArgs &a, const Tile<TM> &tile, const Smem &sz, const T *hs, const float *up,
+                                             const T *B, int sh, int64_t off, int64_t wide, int64_t blk, int64_t kk, int64_t blocks) {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2, G = TM == 16 ? 1 : 2, Q = Form<TM == 128>::Q;
+    constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
+    const T *bp = B + (off + blk * (J * 8) + (g >> 1) * W + (g & 1)) * R + 4 * t;
+    const O *yp = static_cast<const O *>(a.y) + off + blk * (J * 8) + t * W;
+    O *op = static_cast<O *>(a.out) + off + blk * (J * 8) + t * W;
+    const T *const h0 = hs + g * sz.hstride + (GATED ? 0 : sh) * steps * 16 + 4 * t;
+    for (; blk < blocks; blk += kk) {
+        uint2 bv[Q][H][J];
+#pragma unroll
+        for (int z = 0; z < Q; ++z)
+#pragma unroll
+            for (int q = 0; q < H; ++q)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    bv[z][q][j] = make_uint2(0, 0);
+                    if (z * 16 + 4 * t < R) bv[z][q][j] = ldg_nc_v2(bp + q * wide * R + 2 * j * R + z * 16);
+                }
+        for (int r0 = 0; r0 < tile.count; r0 += 16 * G) {
+            Raw<O, W> yv[H][2 * G];
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i)
+                if (r0 + i * 8 + g < tile.count) {
+                    const O *p = yp + tile.toks[r0 + i * 8 + g] * a.ys;
+#pragma unroll
+                    for (int q = 0; q < H; ++q) yv[q][i].load(p + q * wide, W, true);
+                }
+            float acc[H][G][J][4];
+#pragma unroll
+            for (int q = 0; q < H; ++q)
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[q][i][j][e] = 0.f;
+#pragma unroll
+            for (int z = 0; z < Q; ++z) {
+                if (z >= steps) break;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int q = 0; q < H; ++q)
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) {
+                            const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + (q * steps + z) * 16;
+                            const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                            const uint32_t f[4] = {x.x, v.x, x.y, v.y};
+#pragma unroll
+                            for (int j = 0; j < J; ++j) mma16816<T>(acc[q][i][j], f, bv[z][q][j].x, bv[z][q][j].y);
+                        }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) {
+                const int row = r0 + i * 8 + g;
+                if (row >= tile.count) continue;
+                const float f = kBf ? 1.f : up[row];
+                float v[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    v[j] = __fmaf_rn(acc[0][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[0][i][j]);
+                    if constexpr (GATED) v[j] = silu(v[j]) * __fmaf_rn(acc[1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[1][i][j]);
+                }
+                store_out<O, W>(op + tile.toks[row] * a.os, W, true, v);
+            }
+        }
+        bp += kk * (J * 8) * R;
+        yp += kk * (J * 8);
+        op += kk * (J * 8);
+    }
+}
+
+// What this warp will expand, requested into the L2 while the shrink runs: few tokens leave too few warps to
+// cover the trips to memory otherwise.
+template <typename T, typename O, bool GATED>
+__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<16> &tile, const T *B, int first, int kk) {
+    constexpr int J = GATED ? 2 : 4, H = GATED ? 2 : 1;
+    const int lane = threadIdx.x & 31, shards = GATED ? 1 : a.S;
+    const int lines = (J * 8 * a.R * 2 + 127) / 128;  // of a block's rows of B
+    int64_t skip = first, off = a.col0;
+    for (int sh = 0; sh < shards; ++sh) {
+        const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
+        int64_t blk = skip;
+        for (; blk < blocks; blk += kk) {
+            const int64_t col = off + blk * (J * 8);
+            const int left = (int)min((int64_t)(J * 8), wide - blk * (J * 8));
+            for (int i = lane; i < lines * H && B != nullptr; i += 32) {
+                const int q = i / lines, at = (i - q * lines) * 64;
+                if (at < left * a.R) prefetch_line(B + (q * wide + col) * a.R + at);
+            }
+            const int row = lane & 15, q = lane >> 4;
+            if (row < tile.count && q < H) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + q * wide + col);
+        }
+        skip = blk - blocks;
+        off += wide;
+    }
 }
 
 // O: type of y and out.
 template <typename T, typename O, bool BIG, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __grid_constant__ LoraArgs a) {
     using F = Form<BIG>;
     constexpr int TM = F::TM;
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -588,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char *const smem = BIG ? smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) : smem_raw;
     __shared__ Tile<TM> tile;
-    __shared__ float up[TM];  // what a row of the split h has to be multiplied by
+    __shared__ float up[TM];       // what a row of the split h has to be multiplied by (f16)
+    __shared__ float row_top[TM];  // f16: largest magnitude of a row of the partial sums
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
     const int unit = (int)(blockIdx.x / (unsigned)C);
@@ -605,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     float *const part = reinterpret_cast<float *>(smem);
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
+    if constexpr (!BIG) want_expand<T, O, GATED>(a, tile, B, rank * kWarps + warp, C * kWarps);
     if (has) {
         const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
         if constexpr (BIG) {
@@ -616,77 +711,97 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
             __syncthreads();
         }
     }
+    if (!kBf && has) {
+        for (int row = warp; row < tile.count; row += kWarps) {
+            float top = 0.f;
+            bool odd = false;
+            for (int e = lane; e < sz.ranks; e += 32) {
+                const float v = fabsf(part[row * sz.pstride + e]);
+                odd = odd || !isfinite(v);
+                top = fmaxf(top, v);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) row_top[row] = odd ? __uint_as_float(0x7F800000u) : top;
+        }
+        __syncthreads();
+    }
     if (C > 1) {
         cluster_wait();  // (every block has started)
         cl_arrive_release();
         cl_wait_acquire();
     }
     if (has) {
-        // ---- h = s (the blocks' sums, in their order), split into NS numbers of T; a warp per row
+        // ---- h = s (the blocks' sums, in their order), split into NS numbers of T
         const float s = a.scale ? a.scale[ad] : 1.f;
-        float *const mine = reinterpret_cast<float *>(smem + sz.rows) + warp * sz.ranks;
-        for (int row = warp; row < TM; row += kWarps) {
-            uint32_t top = 0;
-            for (int e = lane; e < sz.ranks; e += 32) {
-                float v = 0.f;
-                if (row < tile.count) {
-                    if (C > 1) {
-                        const uint32_t at = smem_u32(part + row * sz.pstride + e);
-                        float p[8];
+        if constexpr (!kBf) {
+            // f16: a row scaled such that the sum of its blocks' largest lies in [2^14, 2^15); one with an infinity or a
+            // NaN as it is
+            if (tid < TM) {
+                float top = 0.f;
+                for (int i = 0; i < C; ++i) top += C > 1 ? cl_ld_f32(cl_map(smem_u32(&row_top[tid]), i)) : row_top[tid];
+                const uint32_t ex = max((__float_as_uint(top * s) & 0x7FFFFFFFu) >> 23, 15u);
+                up[tid] = ex < 255u ? __uint_as_float((ex - 14u) << 23) : 1.f;
+            }
+            __syncthreads();
+        }
+        const int quads = steps * 4, row_quads = S * quads;
+        constexpr int U = BIG ? 4 : 2;
+        for (int i0 = tid; i0 < tile.count * row_quads; i0 += U * kThreads) {
+            float4 v[U];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) p[i] = i < C ? cl_ld_f32(cl_map(at, i)) : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v += p[i];
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads, row = i / row_quads, e = i - row * row_quads, sh = e / quads, r = (e - sh * quads) * 4;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row < tile.count && r < R) {
+                    const float *p = part + row * sz.pstride + sh * R + r;
+                    if (C == 1) {
+                        v[u] = *reinterpret_cast<const float4 *>(p);
                     } else {
-                        v = part[row * sz.pstride + e];
+                        const uint32_t at = smem_u32(p);
+                        for (int c = 0; c < C; ++c) {
+                            const float4 x = cl_ld_v4(cl_map(at, c));
+                            v[u].x += x.x, v[u].y += x.y, v[u].z += x.z, v[u].w += x.w;
+                        }
                     }
-                    v *= s;
-                }
-                top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
-                mine[e] = v;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // f16: the row's largest to [2^14, 2^15); a row with an infinity or a NaN as it is
-            const uint32_t ex = max(top >> 23, 15u);
-            const bool turn = !kBf && ex < 255u;
-            const float down = turn ? __uint_as_float((268u - ex) << 23) : 1.f;
-            if (lane == 0) up[row] = turn ? __uint_as_float((ex - 14u) << 23) : 1.f;
-            __syncwarp();
-            for (int e = lane; e < S * steps * 16; e += 32) {
-                const int sh = e / (steps * 16), r = e - sh * steps * 16;
-                float v = r < R ? mine[sh * R + r] * down : 0.f;
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const T h = of_f<T>(v);
-                    hs[(i * TM + row) * sz.hstride + e] = h;
-                    v = isfinite(to_f(h)) ? v - to_f(h) : 0.f;
                 }
             }
-            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads, row = i / row_quads, e = i - row * row_quads;
+                if (row >= tile.count) continue;
+                const float f = kBf ? 1.f : 1.f / up[row];  // (a power of two)
+                float z[4] = {v[u].x * s * f, v[u].y * s * f, v[u].z * s * f, v[u].w * s * f};
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    T h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        h[j] = of_f<T>(z[j]);
+                        z[j] = isfinite(to_f(h[j])) ? z[j] - to_f(h[j]) : 0.f;
+                    }
+                    *reinterpret_cast<uint2 *>(hs + (n * TM + row) * sz.hstride + e * 4) = *reinterpret_cast<const uint2 *>(h);
+                }
+            }
         }
     }
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
     {
-        // columns in blocks of 32 (gated: 16 of either half), and (BIG) runs of 32 rows, dealt to the cluster's warps
-        constexpr int G = BIG ? 2 : 1, U = BIG ? 1 : 2, J = GATED ? 2 : 4;
+        // columns in blocks of 32 (gated: 16 of either half), dealt to the cluster's warps
+        constexpr int G = BIG ? 2 : 1, J = GATED ? 2 : 4;
         const int kk = C * kWarps, shards = GATED ? 1 : S;
-        const int runs = BIG ? (tile.count + 16 * G - 1) / (16 * G) : 1;
-        int64_t skip = rank * kWarps + warp, off = a.col0;  // items before this warp's next one
+        int64_t skip = rank * kWarps + warp, off = a.col0;  // blocks before this warp's next one
         for (int sh = 0; sh < shards; ++sh) {
-            const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8), items = blocks * runs;
-            int64_t it = skip;
-            if constexpr (BIG) {
-                for (; it < items; it += kk) {
-                    const int64_t blk = it / runs;
-                    expand<T, O, TM, G, 1, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, 0, blocks, (int)(it - blk * runs) * 16 * G);
-                }
-            } else {
-                for (; it < items; it += (int64_t)U * kk) expand<T, O, TM, 1, U, GATED>(a, tile, sz, hs, up, B, sh, off, wide, it, kk, blocks, 0);
-                while (it - kk >= items) it -= kk;  // the first of its items that is not here
-            }
-            skip = it - items;
+            const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
+            if (has && R <= 16 * F::Q && a.vec_y && wide % (J * 8) == 0)
+                expand_whole<T, O, TM, GATED>(a, tile, sz, hs, up, B, sh, off, wide, skip, kk, blocks);
+            else
+                for (int64_t blk = skip; blk < blocks; blk += kk)
+                    for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
+                        expand<T, O, TM, G, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, r0);
+            skip = skip >= blocks ? skip - blocks : kk - 1 - (blocks - 1 - skip) % kk;
             off += wide;
         }
     }

@@ -21,7 +21,7 @@ namespace tl {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxBlocks = 8;
+constexpr int kMaxBlocks = 8;
 
 struct Pair {
     float hi, lo;
@@ -74,9 +74,9 @@ struct Weights {
     const int *list;
     __device__ __forceinline__ Pair of(float p, float q) const {
         const float t = __fmul_rn(ah, q), te = __fmaf_rn(al, q, __fmaf_rn(ah, q, -t));
-        Pair d = two_sum(p, -t);
-        d.lo = __fsub_rn(d.lo, te);
-        return __fadd_rn(d.hi, d.lo) > 0.f ? d : Pair{0.f, 0.f};
+        // p - t and what its rounding lost: exact where p >= t, and where they are near each other; else w is 0
+        const float d = __fsub_rn(p, t), e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), t), te);
+        return __fadd_rn(d, e) > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
     }
     __device__ __forceinline__ bool removed(int v) const {
         for (int i = 0; i < gone; ++i)
@@ -90,9 +90,7 @@ struct Weights {
 };
 
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&v)[16 / sizeof(T)], bool in) {
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (in) r = ldg_nc_v4(p);
+__device__ __forceinline__ void values16(uint4 r, float (&v)[16 / sizeof(T)]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -116,27 +114,43 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
         acc = {s.hi, __fadd_rn(acc.lo, __fadd_rn(s.lo, x.lo))};
     };
     if constexpr (VEC) {
-        constexpr int W = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;  // elements a load, loads in flight
+        // two steps of U loads in flight: one travels while the other is added
+        constexpr int W = 16 / sizeof(T), U = sizeof(T) == 4 ? 2 : 1, STEP = U * 32 * W;
         const int whole = lo + (hi - lo) / W * W;
-        for (int v = lo + lane * W; v < whole; v += U * 32 * W) {
-            float p[U][W], q[U][W];
+        uint4 p[2][U], q[2][U];
+        const auto request = [&](int v, uint4 (&x)[U], uint4 (&y)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool in = v + u * 32 * W < whole;
-                load16(w.p + v + u * 32 * W, p[u], in);
-                if (w.q) load16(w.q + v + u * 32 * W, q[u], in);
+                x[u] = y[u] = make_uint4(0, 0, 0, 0);
+                if (in) x[u] = ldg_nc_v4(w.p + v + u * 32 * W);
+                if (in && w.q) y[u] = ldg_nc_v4(w.q + v + u * 32 * W);
             }
+        };
+        const auto add_up = [&](int v, const uint4 (&x)[U], const uint4 (&y)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                float pv[W], qv[W];
+                values16<T>(x[u], pv);
+                values16<T>(y[u], qv);
                 for (int i = 0; i < w.gone; ++i) {
                     const unsigned at = (unsigned)(w.list[i] - (v + u * 32 * W));
 #pragma unroll
                     for (int e = 0; e < W; ++e)
-                        if (at == (unsigned)e) p[u][e] = 0.f;
+                        if (at == (unsigned)e) pv[e] = 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < W; ++e) take(w.q ? w.of(p[u][e], q[u][e]) : Pair{p[u][e], 0.f});
+                for (int e = 0; e < W; ++e) take(w.q ? w.of(pv[e], qv[e]) : Pair{pv[e], 0.f});
             }
+        };
+        int v = lo + lane * W;
+        request(v, p[0], q[0]);
+        request(v + STEP, p[1], q[1]);
+        for (; v < whole; v += 2 * STEP) {
+            add_up(v, p[0], q[0]);
+            request(v + 2 * STEP, p[0], q[0]);
+            add_up(v + STEP, p[1], q[1]);
+            request(v + 3 * STEP, p[1], q[1]);
         }
         if (whole + lane < hi) take(w.at(whole + lane));
     } else {
@@ -169,11 +183,11 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 #pragma unroll
         for (int i = 0; i < N; i += W) {
             float r[W];
-            load16(w.p + v0 + i, r, true);
+            values16<T>(ldg_nc_v4(w.p + v0 + i), r);
 #pragma unroll
             for (int e = 0; e < W; ++e) p[i + e] = r[e];
             if (w.q) {
-                load16(w.q + v0 + i, r, true);
+                values16<T>(ldg_nc_v4(w.q + v0 + i), r);
 #pragma unroll
                 for (int e = 0; e < W; ++e) q[i + e] = r[e];
             }
@@ -198,8 +212,9 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 // Bound by latency: the gather (two dependent loads), a pass, the cluster's barrier, the drawing.
 // fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
 // warp takes the SM's unit 16 cycles.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
+template <typename T, bool VEC, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(VerifyArgs a) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ float px[kMaxDraft], qx[kMaxDraft], un[kMaxDraft + 1];
     __shared__ int tok[kMaxDraft], par[kMaxDraft], path[kMaxDraft], gone[kMaxDraft];
     __shared__ uint8_t fresh[kMaxDraft];  // accepted as its node's first child
@@ -465,11 +480,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     a.out[b * (n + 1) + count] = token;
 }
 
-template <typename T>
-cudaError_t launch_t(const VerifyArgs &a, bool vec, cudaStream_t st) {
+template <typename T, bool VEC, int THREADS>
+cudaError_t launch_one(const VerifyArgs &a, cudaStream_t st) {
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(a.B * a.blocks));
-    c.blockDim = dim3(kThreads);
+    c.blockDim = dim3(THREADS);
     c.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -477,16 +492,27 @@ cudaError_t launch_t(const VerifyArgs &a, bool vec, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    return vec ? cudaLaunchKernelEx(&c, verify_kernel<T, true>, a) : cudaLaunchKernelEx(&c, verify_kernel<T, false>, a);
+    return cudaLaunchKernelEx(&c, verify_kernel<T, VEC, THREADS>, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const VerifyArgs &a, bool vec, int sm_count, cudaStream_t st) {
+    // 512 threads a block where two such on each SM hold the batch: a pass is then the shorter; many
+    // sequences share the SMs better in blocks of 256
+    const bool wide = a.B * a.blocks <= 2 * sm_count;
+    if (vec) return wide ? launch_one<T, true, 512>(a, st) : launch_one<T, true, 256>(a, st);
+    return wide ? launch_one<T, false, 512>(a, st) : launch_one<T, false, 256>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs &args, int dtype, bool vec, cudaStream_t st) {
+cudaError_t launch_verify(const VerifyArgs &args, int dtype, bool vec, int sm_count, cudaStream_t st) {
     VerifyArgs a = args;
     a.blocks = 1;
     while (a.blocks < kMaxBlocks && a.V > 4096 * a.blocks) a.blocks *= 2;
-    return dtype == 0 ? launch_t<__half>(a, vec, st) : dtype == 1 ? launch_t<__nv_bfloat16>(a, vec, st) : launch_t<float>(a, vec, st);
+    return dtype == 0   ? launch_t<__half>(a, vec, sm_count, st)
+           : dtype == 1 ? launch_t<__nv_bfloat16>(a, vec, sm_count, st)
+                        : launch_t<float>(a, vec, sm_count, st);
 }
 
 }  // namespace tl

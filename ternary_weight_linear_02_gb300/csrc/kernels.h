@@ -348,7 +348,7 @@ struct VerifyArgs {
     int blocks;  // of a cluster
     int *status;
 };
-cudaError_t launch_verify(const VerifyArgs &a, int dtype, bool vec, cudaStream_t st);
+cudaError_t launch_verify(const VerifyArgs &a, int dtype, bool vec, int sm_count, cudaStream_t st);
 
 // ------------------------------------------------------------ low-rank adapters
 constexpr int kMaxShards = 8;
