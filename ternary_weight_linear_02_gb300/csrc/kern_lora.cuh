@@ -413,11 +413,16 @@ __device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &t
     const uint32_t tm = tmem_slot;
     const int n = (k1 - k0 + 63) / 64;
     const uint32_t idesc = tc::idesc_f16(16, std::is_same<T, __nv_bfloat16>::value) - (2u << 17) + ((uint32_t)(sz.npad >> 3) << 17);
-    const int row = tid >> 1, h = (tid & 1) * 4;  // half a row of either matrix
-    const bool live = row < tile.count, mine = row < sz.npad, real = row < sz.ranks;
-    const T *const x = static_cast<const T *>(a.x) + (int64_t)tile.toks[live ? row : 0] * a.xs;
-    const T *const w = A + (int64_t)(real ? row : 0) * a.K;
-    const uint32_t base = smem_u32(ring) + row * 128;
+    // eight lanes copy a row's 128 bytes: a warp's request is four whole lines
+    const int row = tid >> 3, c = tid & 7;  // rows row + 32 i
+    const T *x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = row + 32 * i;
+        x[i] = static_cast<const T *>(a.x) + (int64_t)tile.toks[r < tile.count ? r : 0] * a.xs + c * 8;
+    }
+    const T *const w = A + (int64_t)row * a.K + c * 8;
+    const uint32_t base = smem_u32(ring) + row * 128 + ((c ^ (row & 7)) << 4);  // (32 i rows on, the swizzle is the same)
     bool ok = true;
     if (a.stall && warp == kIssuer) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&never, 0, a.wait_limit));
     // a stage's copies of this thread have landed: say so; the issuer waits for all and multiplies
@@ -443,13 +448,13 @@ __device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &t
         if (!ok) break;
         const uint32_t dst = base + s * sz.stage;
         const int k = k0 + it * 64;
+        const bool in = k + c * 8 < k1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int kk = k + (h + c) * 8;
-            const bool in = kk < k1;
-            const uint32_t at = dst + (((h + c) ^ (row & 7)) << 4);
-            copy16(at, x + (live && in ? kk : 0), live && in);
-            if (mine) copy16(at + 128 * 128, w + (real && in ? kk : 0), real && in);
+        for (int i = 0; i < 4; ++i) {
+            const int r = row + 32 * i;
+            const bool xi = in && r < tile.count, wi = in && r < sz.ranks;
+            copy16(dst + i * 4096, xi ? x[i] + k : static_cast<const T *>(a.x), xi);
+            if (r < sz.npad) copy16(dst + 16384 + i * 4096, wi ? w + (int64_t)(32 * i) * a.K + k : A, wi);
         }
         copies_commit();
         if (it >= LAG) {
@@ -645,10 +650,9 @@ __device__ __forceinline__ void expand_whole(const LoraArgs &a, const Tile<TM> &
     }
 }
 
-// What this warp will expand, requested into the L2 while the shrink runs: few tokens leave too few warps to
-// cover the trips to memory otherwise.
-template <typename T, typename O, bool GATED>
-__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<16> &tile, const T *B, int first, int kk) {
+// What this warp will expand, requested into the L2 while the sums are joined.
+template <typename T, typename O, int TM, bool GATED>
+__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<TM> &tile, const T *B, int first, int kk) {
     constexpr int J = GATED ? 2 : 4, H = GATED ? 2 : 1;
     const int lane = threadIdx.x & 31, shards = GATED ? 1 : a.S;
     const int lines = (J * 8 * a.R * 2 + 127) / 128;  // of a block's rows of B
@@ -663,8 +667,10 @@ __device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<16> &t
                 const int q = i / lines, at = (i - q * lines) * 64;
                 if (at < left * a.R) prefetch_line(B + (q * wide + col) * a.R + at);
             }
-            const int row = lane & 15, q = lane >> 4;
-            if (row < tile.count && q < H) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + q * wide + col);
+            for (int i = lane; i < TM * H; i += 32) {
+                const int q = i / TM, row = i - q * TM;
+                if (row < tile.count) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + q * wide + col);
+            }
         }
         skip = blk - blocks;
         off += wide;
@@ -699,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __gri
     float *const part = reinterpret_cast<float *>(smem);
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
-    if constexpr (!BIG) want_expand<T, O, GATED>(a, tile, B, rank * kWarps + warp, C * kWarps);
     if (has) {
         const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
         if constexpr (BIG) {
@@ -711,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __gri
             __syncthreads();
         }
     }
+    want_expand<T, O, TM, GATED>(a, tile, B, rank * kWarps + warp, C * kWarps);
     if (!kBf && has) {
         for (int row = warp; row < tile.count; row += kWarps) {
             float top = 0.f;
