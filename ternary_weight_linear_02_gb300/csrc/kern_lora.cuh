@@ -176,6 +176,16 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+    return r;
+}
 __device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <bool BIG>
@@ -183,8 +193,9 @@ struct Form {
     static constexpr int TM = BIG ? 128 : 16;  // tokens of a tile
     static constexpr int NT = 6, U = 1;        // small: n-tiles of 8 ranks a pass of the shrink; chunks in flight
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
-    static constexpr int Q = BIG ? 4 : 2;      // steps of 16 ranks whose entries of B a thread holds
 };
+
+constexpr int kBigSteps = 4;  // steps of 16 ranks whose entries of B a thread of expand_big holds
 
 // Sizes of a block's shared memory (bytes), the same on the host.
 struct Smem {
@@ -192,9 +203,11 @@ struct Smem {
     int pstride;      // floats between rows of the partial sums: 16-byte stores of 8 rows hit other banks
     int hstride;      // elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
     int stage;        // BIG: a stage
-    int split;        // where the split h begins (small: before that the warps' sums)
+    int split;        // where the split h begins
+    int blocks;       // small: where the warps' sums, and after them the stages of B and y begin
     int total;
-    __host__ __device__ Smem(bool big, int S, int R, int ns) {
+    // stage: bytes of a stage of expand_small (0: not used)
+    __host__ __device__ Smem(bool big, int S, int R, int ns, int small_stage) {
         const int tm = big ? 128 : 16;
         ranks = S * R;
         npad = (ranks + 15) & ~15;
@@ -203,8 +216,9 @@ struct Smem {
         hstride = steps * 16 + (steps % 2 ? 0 : 16);
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
-        const int hs = ns * tm * hstride * 2, red = big ? 0 : 4 * 16 * Form<false>::NT * 8 * 4;
-        total = split + (hs > red ? hs : red);
+        blocks = split + ns * tm * hstride * 2;
+        const int red = 4 * 16 * Form<false>::NT * 8 * 4, stages = 2 * kWarps * small_stage;
+        total = blocks + (big ? 0 : red > stages ? red : stages);
         if (big) {
             const int ring = Form<true>::STAGES * stage;  // done with before the sums are stored
             total = (total > ring ? total : ring) + 1024; // stages lie on 1024 bytes
@@ -572,13 +586,167 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
     }
 }
 
-// ---- expand where whole blocks of columns start on 16 bytes and a thread holds its entries of B for all ranks: they
-// are loaded once for all rows of the tile, pointers move along without products.
-template <typename T, typename O, int TM, bool GATED>
-__device__ __forceinline__ void expand_whole(const LoraArgs &a, const Tile<TM> &tile, const Smem &sz, const T *hs, const float *up,
+// ---- expand, few tokens, where blocks of columns are whole and start on 16 bytes and the rank is 8, 16 or 32.  B's
+// rows (columns of the output) are the wide side of the MMA and 8 tokens the narrow one, so that no MMA row is idle
+// with 8 tokens or more, and a thread has W neighbouring columns of two tokens.  Each warp copies its blocks' B and y
+// into two stages of its own, the first ones while the sums are joined.
+template <typename O, bool GATED>
+struct Blocks {
+    static constexpr int W = GATED ? 4 : 8, H = GATED ? 2 : 1;  // columns of a thread; halves
+    static constexpr int COLS = 8 * W;                          // columns of a block (gated: of either half)
+    static constexpr int YROW = COLS * sizeof(O);               // bytes of a token's columns
+    static constexpr int YBYTES = 16 * H * YROW;
+    __host__ __device__ static int stage(int R) { return H * COLS * R * 2 + YBYTES; }
+    __host__ __device__ static bool ranks(int R) { return R == 8 || R == 16 || R == 32; }
+    // place of byte `at` of a half's rows of B that belongs to the columns of threads g: 32-byte granules of 4 threads'
+    // columns exchange places, which leaves no bank conflicts
+    __device__ static uint32_t b_place(int at, int g) { return (uint32_t)(at ^ ((g & 3) << 5)); }
+    // place of 16-byte piece c of token row r
+    __device__ static uint32_t y_piece(int r, int c) { return (uint32_t)(r * YROW + ((c ^ (((r >> 1) & 3) << (GATED ? 0 : 1))) << 4)); }
+};
+
+template <typename T, typename O, bool GATED>
+struct ExpandSmall {
+    using L = Blocks<O, GATED>;
+    static constexpr int W = L::W, H = L::H, I = W / 2;
+    const LoraArgs &a;
+    const Tile<16> &tile;
+    const T *const B;
+    const uint32_t base;  // shared memory of this warp
+    const int first, kk, lane;
+
+    // block i of this warp: its shard and first column; false: there is none
+    __device__ __forceinline__ bool block(int i, int &sh, int64_t &col) const {
+        int64_t n = first + (int64_t)i * kk;
+        col = a.col0;
+        for (sh = 0; sh < (GATED ? 1 : a.S); ++sh) {
+            const int64_t blocks = a.shard[sh] / L::COLS;
+            if (n < blocks) {
+                col += n * L::COLS;
+                return true;
+            }
+            n -= blocks;
+            col += a.shard[sh];
+        }
+        return false;
+    }
+    __device__ __forceinline__ void copy(int i) const {
+        int sh;
+        int64_t col;
+        if (block(i, sh, col)) {
+            const uint32_t to = base + (i & 1) * L::stage(a.R), yt = to + H * L::COLS * a.R * 2;
+            const int64_t wide = a.shard[0];
+            const int pieces = L::COLS * a.R / 8, shift = 28 - __clz(W * a.R);  // log2 of the pieces of a thread's columns
+#pragma unroll
+            for (int q = 0; q < H; ++q) {
+                const T *b = B + (q * wide + col) * a.R;
+                for (int p = lane; p < pieces; p += 32) copy16(to + q * pieces * 16 + L::b_place(p * 16, p >> shift), b + p * 8, true);
+                constexpr int C = L::YROW / 16;  // pieces of a token
+#pragma unroll
+                for (int p = 0; p < 16 * C; p += 32) {
+                    const int r = (p + lane) / C, c = (p + lane) % C;
+                    if (r < tile.count)
+                        copy16(yt + q * 16 * L::YROW + L::y_piece(r, c),
+                               static_cast<const O *>(a.y) + tile.toks[r] * a.ys + q * wide + col + c * (16 / (int)sizeof(O)), true);
+                }
+            }
+        }
+        copies_commit();
+    }
+    __device__ __forceinline__ void run(const Smem &sz, const T *hs, const float *up) const {
+        constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+        constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
+        const int g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
+        const bool two = tile.count > 8;  // the second group of 8 tokens has some
+        int sh;
+        int64_t col;
+        for (int i = 0; block(i, sh, col); ++i) {
+            copies_wait<1>();
+            __syncwarp();
+            const uint32_t bs = base + (i & 1) * L::stage(R), ys = bs + H * L::COLS * R * 2;
+            float acc[2][H][I][4];
+#pragma unroll
+            for (int n8 = 0; n8 < 2; ++n8)
+#pragma unroll
+                for (int q = 0; q < H; ++q)
+#pragma unroll
+                    for (int m = 0; m < I; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[n8][q][m][e] = 0.f;
+            for (int z = 0; z < steps; ++z) {
+#pragma unroll
+                for (int q = 0; q < H; ++q) {
+                    uint2 h[2][NS];
+#pragma unroll
+                    for (int n8 = 0; n8 < 2; ++n8)
+#pragma unroll
+                        for (int n = 0; n < NS; ++n)
+                            h[n8][n] = *reinterpret_cast<const uint2 *>(hs + (n * 16 + n8 * 8 + g) * sz.hstride +
+                                                                        ((GATED ? q : sh) * steps + z) * 16 + 4 * t);
+#pragma unroll
+                    for (int m = 0; m < I; ++m) {
+                        uint2 x = make_uint2(0, 0), v = make_uint2(0, 0);
+                        if (z * 16 + 4 * t < R) {
+                            const int at = ((g * W + 2 * m) * R + z * 16 + 4 * t) * 2, at2 = at + R * 2;  // bytes of two columns
+                            x = lds8(bs + q * L::COLS * R * 2 + L::b_place(at, g));
+                            v = lds8(bs + q * L::COLS * R * 2 + L::b_place(at2, g));
+                        }
+                        const uint32_t f[4] = {x.x, v.x, x.y, v.y};
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) {
+                            mma16816<T>(acc[0][q][m], f, h[0][n].x, h[0][n].y);
+                            if (two) mma16816<T>(acc[1][q][m], f, h[1][n].x, h[1][n].y);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n8 = 0; n8 < 2; ++n8) {
+                if (n8 == 1 && !two) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = n8 * 8 + 2 * t + e;
+                    if (row >= tile.count) continue;
+                    const float f = kBf ? 1.f : up[row];
+                    Raw<O, W> yv[H];
+#pragma unroll
+                    for (int q = 0; q < H; ++q) {
+                        const uint32_t yr = ys + q * 16 * L::YROW;
+                        if constexpr (Raw<O, W>::WORDS == 2) {
+                            const uint2 r = lds8(yr + L::y_piece(row, g >> 1) + (g & 1) * 8);
+                            yv[q].w[0] = r.x, yv[q].w[1] = r.y;
+                        } else {
+                            constexpr int C = Raw<O, W>::WORDS / 4;
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                const uint4 r = lds16(yr + L::y_piece(row, g * C + c));
+                                yv[q].w[4 * c] = r.x, yv[q].w[4 * c + 1] = r.y, yv[q].w[4 * c + 2] = r.z, yv[q].w[4 * c + 3] = r.w;
+                            }
+                        }
+                    }
+                    float o[W];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        o[j] = __fmaf_rn(acc[n8][0][j >> 1][2 * (j & 1) + e], f, yv[0][j]);
+                        if constexpr (GATED) o[j] = silu(o[j]) * __fmaf_rn(acc[n8][1][j >> 1][2 * (j & 1) + e], f, yv[1][j]);
+                    }
+                    store_out<O, W>(static_cast<O *>(a.out) + tile.toks[row] * a.os + col + g * W, W, true, o);
+                }
+            }
+            __syncwarp();  // the stage is read by all
+            copy(i + 2);
+        }
+        copies_wait<0>();
+    }
+};
+
+// ---- expand, many tokens, where blocks of columns are whole and start on 16 bytes and a thread holds its entries of
+// B for all ranks: they are loaded once for all rows of the tile, pointers move along without products.
+template <typename T, typename O, bool GATED>
+__device__ __forceinline__ void expand_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *hs, const float *up,
                                              const T *B, int sh, int64_t off, int64_t wide, int64_t blk, int64_t kk, int64_t blocks) {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2, G = TM == 16 ? 1 : 2, Q = Form<TM == 128>::Q;
+    constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, G = 2, Q = kBigSteps;
     constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
     const T *bp = B + (off + blk * (J * 8) + (g >> 1) * W + (g & 1)) * R + 4 * t;
@@ -650,10 +818,11 @@ __device__ __forceinline__ void expand_whole(const LoraArgs &a, const Tile<TM> &
     }
 }
 
-// What this warp will expand, requested into the L2 while the sums are joined.
-template <typename T, typename O, int TM, bool GATED>
-__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<TM> &tile, const T *B, int first, int kk) {
-    constexpr int J = GATED ? 2 : 4, H = GATED ? 2 : 1;
+// What this warp will expand, requested into the L2 while the sums are joined.  (With few tokens a tile
+// there are more columns than rows, and requests of single lines cost more than they save.)
+template <typename T, typename O, bool GATED>
+__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<128> &tile, const T *B, int first, int kk) {
+    constexpr int TM = 128, J = GATED ? 2 : 4, H = GATED ? 2 : 1;
     const int lane = threadIdx.x & 31, shards = GATED ? 1 : a.S;
     const int lines = (J * 8 * a.R * 2 + 127) / 128;  // of a block's rows of B
     int64_t skip = first, off = a.col0;
@@ -679,7 +848,7 @@ __device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<TM> &t
 
 // O: type of y and out.
 template <typename T, typename O, bool BIG, bool GATED>
-__global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
     using F = Form<BIG>;
     constexpr int TM = F::TM;
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -701,7 +870,9 @@ __global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __gri
         return;
     }
     const int S = a.S, R = a.R, K = (int)a.K, steps = (R + 15) / 16;
-    const Smem sz(BIG, S, R, NS);
+    using L = Blocks<O, GATED>;
+    const bool whole = !BIG && a.whole;  // blocks of columns for expand_small
+    const Smem sz(BIG, S, R, NS, whole ? L::stage(R) : 0);
     float *const part = reinterpret_cast<float *>(smem);
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
@@ -712,11 +883,20 @@ __global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __gri
             shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
         } else {
             const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-            shrink_small<T>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.split));
+            shrink_small<T>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.blocks));
             __syncthreads();
         }
     }
-    want_expand<T, O, TM, GATED>(a, tile, B, rank * kWarps + warp, C * kWarps);
+    const int w0 = rank * kWarps + warp, kk = C * kWarps;
+    if constexpr (BIG) {
+        if (has) want_expand<T, O, GATED>(a, tile, B, w0, kk);
+    } else {
+        if (has && whole) {
+            const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
+            ex.copy(0);
+            ex.copy(1);
+        }
+    }
     if (!kBf && has) {
         for (int row = warp; row < tile.count; row += kWarps) {
             float top = 0.f;
@@ -795,18 +975,27 @@ __global__ void __launch_bounds__(kThreads, BIG ? 2 : 3) lora_kernel(const __gri
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
     {
-        // columns in blocks of 32 (gated: 16 of either half), dealt to the cluster's warps
+        // columns in blocks, dealt to the cluster's warps
         constexpr int G = BIG ? 2 : 1, J = GATED ? 2 : 4;
-        const int kk = C * kWarps, shards = GATED ? 1 : S;
-        int64_t skip = rank * kWarps + warp, off = a.col0;  // blocks before this warp's next one
-        for (int sh = 0; sh < shards; ++sh) {
+        bool done = false;
+        if constexpr (!BIG) {
+            if (has && whole) {
+                const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
+                ex.run(sz, hs, up);
+                done = true;
+            }
+        }
+        int64_t skip = w0, off = a.col0;  // blocks before this warp's next one
+        for (int sh = 0; sh < (GATED ? 1 : S) && !done; ++sh) {
             const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
-            if (has && R <= 16 * F::Q && a.vec_y && wide % (J * 8) == 0)
-                expand_whole<T, O, TM, GATED>(a, tile, sz, hs, up, B, sh, off, wide, skip, kk, blocks);
-            else
-                for (int64_t blk = skip; blk < blocks; blk += kk)
-                    for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
-                        expand<T, O, TM, G, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, r0);
+            bool big = false;
+            if constexpr (BIG) {
+                big = has && R <= 16 * kBigSteps && a.vec_y && wide % (J * 8) == 0;
+                if (big) expand_big<T, O, GATED>(a, tile, sz, hs, up, B, sh, off, wide, skip, kk, blocks);
+            }
+            for (int64_t blk = skip; blk < blocks && !big; blk += kk)
+                for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
+                    expand<T, O, TM, G, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, r0);
             skip = skip >= blocks ? skip - blocks : kk - 1 - (blocks - 1 - skip) % kk;
             off += wide;
         }
@@ -819,7 +1008,15 @@ constexpr int kMaxSmem = 200 * 1024;
 template <typename T, typename O, bool BIG, bool GATED>
 cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     constexpr int NS = std::is_same<T, __nv_bfloat16>::value && sizeof(O) == 4 ? 3 : 2;
-    const Smem sz(BIG, a.S, a.R, NS);
+    using L = Blocks<O, GATED>;
+    LoraArgs b = a;
+    b.whole = !BIG && a.vec_y && L::ranks(a.R);
+    for (int i = 0; i < a.S; ++i) b.whole = b.whole && a.shard[i] % L::COLS == 0;
+    Smem sz(BIG, a.S, a.R, NS, b.whole ? L::stage(a.R) : 0);
+    if (sz.total > kMaxSmem && b.whole) {
+        b.whole = 0;
+        sz = Smem(BIG, a.S, a.R, NS, 0);
+    }
     static std::atomic<uint64_t> done{0};
     if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>, kMaxSmem)) return e;
     cudaLaunchConfig_t c{};
@@ -840,7 +1037,7 @@ cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     }
     c.attrs = at;
     c.numAttrs = n;
-    return cudaLaunchKernelEx(&c, lora_kernel<T, O, BIG, GATED>, a);
+    return cudaLaunchKernelEx(&c, lora_kernel<T, O, BIG, GATED>, b);
 }
 
 template <typename T>

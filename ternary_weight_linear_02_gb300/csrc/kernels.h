@@ -365,6 +365,7 @@ struct LoraArgs {
     int64_t col0;             // first column of this launch's shards
     int gated;
     int vec_x, vec_a, vec_y;  // rows start on 16-byte boundaries (y, out: columns of threads too)
+    int whole;                // columns come in whole blocks (the launcher's answer)
     int C;                    // blocks of a cluster
     const int *plan;          // tiles found beforehand (null: by each block)
     int max_tiles;
