@@ -191,7 +191,7 @@ __device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("pre
 template <bool BIG>
 struct Form {
     static constexpr int TM = BIG ? 128 : 16;  // tokens of a tile
-    static constexpr int NT = 6, U = 1;        // small: n-tiles of 8 ranks a pass of the shrink; chunks in flight
+    static constexpr int NT = 6;               // small: n-tiles of 8 ranks a pass of the shrink
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
 };
 
@@ -204,10 +204,10 @@ struct Smem {
     int hstride;      // elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
     int stage;        // BIG: a stage
     int split;        // where the split h begins
-    int blocks;       // small: where the warps' sums, and after them the stages of B and y begin
+    int blocks, red;  // small: where the stages of B and y, and the warps' sums begin
     int total;
     // stage: bytes of a stage of expand_small (0: not used)
-    __host__ __device__ Smem(bool big, int S, int R, int ns, int small_stage) {
+    __host__ __device__ Smem(bool big, bool gated, int S, int R, int ns, int small_stage) {
         const int tm = big ? 128 : 16;
         ranks = S * R;
         npad = (ranks + 15) & ~15;
@@ -217,8 +217,10 @@ struct Smem {
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
         blocks = split + ns * tm * hstride * 2;
-        const int red = 4 * 16 * Form<false>::NT * 8 * 4, stages = 2 * kWarps * small_stage;
-        total = blocks + (big ? 0 : red > stages ? red : stages);
+        const int red_bytes = 4 * 16 * Form<false>::NT * 8 * 4, stages = 2 * kWarps * small_stage;
+        // (gated: a third block on each SM is worth more than copying before the sums are added)
+        red = blocks + (gated ? 0 : stages);
+        total = big ? blocks : gated ? blocks + (red_bytes > stages ? red_bytes : stages) : red + red_bytes;
         if (big) {
             const int ring = Form<true>::STAGES * stage;  // done with before the sums are stored
             total = (total > ring ? total : ring) + 1024; // stages lie on 1024 bytes
@@ -247,8 +249,34 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int
         __syncthreads();
         return true;
     }
-    __shared__ int hist[kLoraFind + 1], wsum[kWarps], tok_cnt[4][kWarps];
     const int M = (int)a.M, keys = a.adapters + 1;
+    if (M <= 32) {  // one warp sees them all: the tokens of an adapter by their lanes
+        if (warp == 0) {
+            const int key = lane < M ? lora_key(a, lane) : -1;
+            if (report && lane < M && a.which[lane] >= a.adapters) flag_value(a.status);
+            const uint32_t same = __match_any_sync(0xffffffffu, key);
+            const int tiles = key >= 0 && lane == __ffs(same) - 1 ? (__popc(same) + TM - 1) / TM : 0;
+            int upto = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, unit >= upto - tiles && unit < upto);
+            const int who = hit ? __ffs(hit) - 1 : 0;
+            const uint32_t mine = __shfl_sync(0xffffffffu, same, who);
+            const int nth = unit - __shfl_sync(0xffffffffu, upto - tiles, who), ad = __shfl_sync(0xffffffffu, key, who);
+            const int r = __popc(mine & ((1u << lane) - 1u)) - nth * TM;
+            if (hit && (mine >> lane & 1u) && r >= 0 && r < TM) tile.toks[r] = lane;
+            if (lane == 0) {
+                tile.adapter = hit ? ad : -1;
+                tile.count = min(TM, __popc(mine) - nth * TM);
+            }
+        }
+        __syncthreads();
+        return tile.adapter >= 0;
+    }
+    __shared__ int hist[kLoraFind + 1], wsum[kWarps], tok_cnt[4][kWarps];
     int key[4];
     for (int i = tid; i < keys; i += kThreads) hist[i] = 0;
     if (tid < TM) tile.toks[tid] = -1;
@@ -321,11 +349,11 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int
     return true;
 }
 
-// ---- shrink, few tokens: 16 rows, the warps take chunks of 32 k, operands from global memory to registers.
-template <typename T>
+// ---- shrink, few tokens: 16 rows, the warps take chunks of 32 k (U in flight), operands from global memory to registers.
+template <typename T, int U>
 __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *A, int c0, int c1,
                                              float *part, float *red) {
-    constexpr int NT = Form<false>::NT, U = Form<false>::U;
+    constexpr int NT = Form<false>::NT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, K = (int)a.K;
     const T *xr[2];
     bool live[2];
@@ -589,7 +617,7 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
 // ---- expand, few tokens, where blocks of columns are whole and start on 16 bytes and the rank is 8, 16 or 32.  B's
 // rows (columns of the output) are the wide side of the MMA and 8 tokens the narrow one, so that no MMA row is idle
 // with 8 tokens or more, and a thread has W neighbouring columns of two tokens.  Each warp copies its blocks' B and y
-// into two stages of its own, the first ones while the sums are joined.
+// into two stages of its own, the first ones before the shrink (gated: while the sums are joined).
 template <typename O, bool GATED>
 struct Blocks {
     static constexpr int W = GATED ? 4 : 8, H = GATED ? 2 : 1;  // columns of a thread; halves
@@ -872,10 +900,22 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
     const int S = a.S, R = a.R, K = (int)a.K, steps = (R + 15) / 16;
     using L = Blocks<O, GATED>;
     const bool whole = !BIG && a.whole;  // blocks of columns for expand_small
-    const Smem sz(BIG, S, R, NS, whole ? L::stage(R) : 0);
+    const Smem sz(BIG, GATED, S, R, NS, whole ? L::stage(R) : 0);
     float *const part = reinterpret_cast<float *>(smem);
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
+    const int w0 = rank * kWarps + warp, kk = C * kWarps;
+    const auto copy_first = [&] {
+        if constexpr (BIG) return;
+        else {
+        const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
+        ex.copy(0);
+        ex.copy(1);
+        }
+    };
+    if constexpr (!BIG && !GATED) {
+        if (has && whole) copy_first();
+    }
     if (has) {
         const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
         if constexpr (BIG) {
@@ -883,19 +923,14 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
             shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
         } else {
             const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-            shrink_small<T>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.blocks));
+            shrink_small<T, GATED ? 1 : 2>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.red));
             __syncthreads();
         }
     }
-    const int w0 = rank * kWarps + warp, kk = C * kWarps;
     if constexpr (BIG) {
         if (has) want_expand<T, O, GATED>(a, tile, B, w0, kk);
     } else {
-        if (has && whole) {
-            const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
-            ex.copy(0);
-            ex.copy(1);
-        }
+        if (GATED && has && whole) copy_first();
     }
     if (!kBf && has) {
         for (int row = warp; row < tile.count; row += kWarps) {
@@ -1012,10 +1047,10 @@ cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     LoraArgs b = a;
     b.whole = !BIG && a.vec_y && L::ranks(a.R);
     for (int i = 0; i < a.S; ++i) b.whole = b.whole && a.shard[i] % L::COLS == 0;
-    Smem sz(BIG, a.S, a.R, NS, b.whole ? L::stage(a.R) : 0);
+    Smem sz(BIG, GATED, a.S, a.R, NS, b.whole ? L::stage(a.R) : 0);
     if (sz.total > kMaxSmem && b.whole) {
         b.whole = 0;
-        sz = Smem(BIG, a.S, a.R, NS, 0);
+        sz = Smem(BIG, GATED, a.S, a.R, NS, 0);
     }
     static std::atomic<uint64_t> done{0};
     if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>, kMaxSmem)) return e;
