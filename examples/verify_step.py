@@ -7,7 +7,7 @@ the whole tree: per layer the fused QKV call, ``kv_append`` (rotates q and k by 
 token's depth and writes k and v to the cache in 8 or 4 bits), ``tree_attention`` (each
 token sees the context and its own ancestors), the o call, the fused gate/up call with
 the SiLU-gated product, and down.  The accepted path's entries are then moved to the
-front of the drafted places (the cache's tensors take ordinary indexing), and the
+front of the drafted places (``kv_compact``, all layers in one call), and the
 next step goes on from there.
 
     python examples/verify_step.py [--layers 4] [--batch 4] [--draft 16] [--context 2000]
@@ -50,35 +50,57 @@ class Stack:
                                         synth.seed_for("verify", seed, i, name, "s"), device))
             self.layers.append((w, tl.KVCache.empty(fmt, pages, page_size, kv_heads, head_dim, device)))
 
-    def step(self, x, positions, slots, page_table, context_len, tree=None):
+        self.caches = tl.KVLayers([c for _, c in self.layers])
+
+    def adapt(self, adapters, rank, seed=0):
+        """Random low-rank adapters for every projection, `adapters` of them: a list of one dict a layer, as `step` takes
+        them."""
+        hidden = self.layers[0][0]["o"][0].shape[0]
+        gen = torch.Generator(device=self.table.device).manual_seed(seed)
+        hd, out = self.head_dim, []
+
+        def make(shards, inputs):
+            a = torch.randn(adapters, len(shards) * rank, inputs, generator=gen, device=self.table.device) * inputs ** -0.5
+            b = torch.randn(adapters, sum(shards), rank, generator=gen, device=self.table.device) * (0.3 * rank ** -0.5)
+            return tl.Adapters(a.to(torch.bfloat16), b.to(torch.bfloat16), shards=shards)
+
+        for w, _ in self.layers:
+            ffn = w["gu"][0].shape[0] // 2
+            out.append({"qkv": make((self.q_heads * hd, self.kv_heads * hd, self.kv_heads * hd), hidden), "o": make((hidden,), self.q_heads * hd),
+                        "gu": make((ffn, ffn), hidden), "down": make((hidden,), ffn)})
+        return out
+
+    def step(self, x, positions, slots, page_table, context_len, tree=None, adapters=None, which=None):
         """x [batch, draft, hidden] through every layer; the new tokens' keys and values go to
-        slots (int64 [batch * draft])."""
+        slots (int64 [batch * draft]).  adapters (adapt), which int32 [batch * draft]: each token's adapter."""
         b, t, hidden = x.shape
         hq, hk, g = self.q_heads, self.kv_heads, self.group
+
+        def project(x, w, name, ad):
+            y = tl.linear(x, *w[name], g, static_weights=True)
+            return y if ad is None else tl.lora_add(x, ad[name], which, y, out=y)
+
         x = x.flatten(0, 1)
-        for w, cache in self.layers:
-            qkv = tl.linear(norm(x), *w["qkv"], g, static_weights=True).unflatten(1, (hq + 2 * hk, self.head_dim))
+        for i, (w, cache) in enumerate(self.layers):
+            ad = None if adapters is None else adapters[i]
+            qkv = project(norm(x), w, "qkv", ad).unflatten(1, (hq + 2 * hk, self.head_dim))
             q = qkv[:, :hq]
             tl.kv_append(cache, qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, q=q, positions=positions, table=self.table,
                          q_out=q)
             a = tl.tree_attention(q.unflatten(0, (b, t)), cache, page_table, context_len, tree)
-            x = x + tl.linear(a.flatten(0, 1).flatten(1), *w["o"], g, static_weights=True)
-            h = tl.linear_silu_mul(norm(x), *w["gu"], g, static_weights=True)
-            x = x + tl.linear(h, *w["down"], g, static_weights=True)
+            x = x + project(a.flatten(0, 1).flatten(1), w, "o", ad)
+            n = norm(x)
+            if ad is None:
+                h = tl.linear_silu_mul(n, *w["gu"], g, static_weights=True)
+            else:  # the gated product waits for what the adapters add
+                h = tl.lora_silu_mul(n, ad["gu"], which, tl.linear(n, *w["gu"], g, static_weights=True))
+            x = x + project(h, w, "down", ad)
         return x.unflatten(0, (b, t))
 
     def accept(self, page_table, context_len, path, count):
         """Moves each sequence's accepted drafted entries (path int64 [batch, n], indexes of drafted
         tokens in order; the first count[b] of them are kept) to the front of the drafted places."""
-        n = path.shape[1]
-        at = torch.arange(n, device=path.device)
-        keep = at < count[:, None]
-        src = slots_of(page_table, context_len[:, None] + path, self.page_size)[keep]
-        dst = slots_of(page_table, context_len[:, None] + at, self.page_size)[keep]
-        for _, c in self.layers:
-            for ten in (c.k_codes, c.v_codes, c.k_scale, c.v_scale):
-                raw = ten.view(torch.uint8) if ten.dtype == torch.float8_e4m3fn else ten
-                raw[dst // self.page_size, :, dst % self.page_size] = raw[src // self.page_size, :, src % self.page_size]
+        tl.kv_compact(self.caches, page_table, context_len, path.int(), count.int())
         return context_len + count.int()
 
 
