@@ -1,7 +1,9 @@
 /*
  * ternary_linear.h -- C ABI of libternary_gb300.so, a ternary-weight linear
  * layer for NVIDIA GB300 (sm_103a), with the rotary positions, quantised cache and
- * attention that a decode step needs between its QKV and its o layer.
+ * attention that a decode step needs between its QKV and its o layer, and what a
+ * server does around the layers: pages of the cache, drafted tokens verified,
+ * low-rank adapters of many requests.
  *
  * Format (all calls): a weight matrix W[N,K] with entries in {-1,0,+1} is
  * stored packed as uint8 [N, ceil(K/4)], row-major, K contiguous (written

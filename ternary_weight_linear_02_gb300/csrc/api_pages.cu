@@ -50,6 +50,9 @@ tl::KvMove move_of(const tl_kv_cache *c, int first, int layers, int *status) {
     if (m.L == 0) return m;
     m.pages = c->pages;
     m.P = c->page_size;
+    m.shift = -1;
+    for (int i = 4; i <= 20; ++i)
+        if (m.P == 1 << i) m.shift = i;
     m.Hk = c->kv_heads;
     m.rb = c->format == TL_KV_INT4 ? c->head_dim / 2 : c->head_dim;
     for (int i = 0; i < m.L; ++i) {

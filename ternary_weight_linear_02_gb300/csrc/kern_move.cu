@@ -4,12 +4,13 @@
 // A head's codes of a page are contiguous (page_size rows of rb bytes), so are its scales.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace tl {
 
 namespace {
 
-constexpr int kMovers = 256;  // threads of a block that closes up a long context
+constexpr int kMovers = 512, kPieces = 4;  // threads of a block that closes up a long context; pieces in flight a group of each
 
 // Copies are dealt to warps: a warp moves the first n places of one head of a page, keys or values, codes
 // and scales, eight 16-byte pieces a lane in flight.  `task` counts (layer, head, keys or values).
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__
 
 // Row (place of one head of the pool) of a sequence's place; -1 for a page that the pool does not have.
 __device__ __forceinline__ int64_t row_of(const KvMove &m, const KvCompactArgs &a, const int *pages, uint32_t place) {
-    const uint32_t p = place / (uint32_t)m.P;
+    const uint32_t p = m.shift >= 0 ? place >> m.shift : place / (uint32_t)m.P;
     const int page = pages[p];
     if ((uint32_t)page >= (uint32_t)m.pages) {
         flag_value(m.status);
@@ -195,15 +196,31 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
     }
 }
 
-// Many moves: a block per (sequence, layer, head, keys or values), eight 16-byte pieces a thread in flight.  While a
-// group's pieces travel, the next one's rows are looked up and the keep of the one after it is requested; the next
-// group is requested before this one is written.
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {  // 4 or 16
+    const uint32_t d = smem_u32(dst);
+    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+// Many moves: a block per (sequence, layer, head, keys or values), in groups of 512 x 4 pieces of 16 bytes.  Two groups
+// travel to shared memory while a third is written: a thread writes what it copied itself, so the one barrier a
+// group says only that all of its reads are done.  Each lane looks up EACH moves of its warp; keep is
+// requested a group before that.
+template <int PIECES>
+struct CompactSmem {
+    static constexpr int WARP = 32 * kPieces / PIECES, EACH = (WARP + 31) / 32;  // moves of a warp; looked up by a lane
+    uint4 piece[3][kPieces][kMovers];  // (two blocks of these share an SM)
+    float scale[3][EACH][kMovers];
+};
 template <int PIECES>
 __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_constant__ KvMove m, KvCompactArgs a) {
-    constexpr int ROWS = kMovers * 8 / PIECES, EACH = ROWS / kMovers;  // moves a group; looked up by each thread
-    extern __shared__ int64_t rows[];                                  // [buffer][from, to][ROWS]; -1: nothing to move
+    using Smem = CompactSmem<PIECES>;
+    constexpr int EACH = Smem::EACH, WARP = Smem::WARP, ROWS = kMovers / 32 * WARP, STEP = 32 / PIECES;  // ROWS: moves of a group
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
     __shared__ int end;
     const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u, tid = threadIdx.x;
+    const int lane = tid & 31, w0 = (int)(tid >> 5) * WARP;
     const int64_t u = blockIdx.x, b = u / per;
     const uint32_t rest = (uint32_t)(u - b * per), lh = rest >> 1, layer = lh / (uint32_t)m.Hk;
     const int64_t head = (int64_t)(lh - layer * (uint32_t)m.Hk) * m.P;
@@ -211,80 +228,82 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
     uint8_t *const codes = rest & 1u ? m.vc[layer] : m.kc[layer];
     float *const scales = rest & 1u ? m.vs[layer] : m.ks[layer];
     if (tid == 0) end = mv.n;
+    __syncthreads();
     int k[EACH], before[EACH];
+    int64_t src[EACH], dst[EACH], to[2][EACH];  // rows, or -1: of the group looked up, and where those in flight go
     const auto fetch = [&](int i0) {
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int i = i0 + e * kMovers + (int)tid;
-            if (i < mv.n) {
+            const int i = i0 + w0 + e * 32 + lane;
+            if (e * 32 + lane < WARP && i < mv.n) {
                 k[e] = mv.keep[i];
                 before[e] = i > 0 ? mv.keep[i - 1] : -1;
             }
         }
     };
-    const auto look = [&](int i0, int buf) {
+    const auto look = [&](int i0) {
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int r = e * kMovers + (int)tid, i = i0 + r;
-            int64_t src = -1, dst = -1;
-            if (i < mv.n && !mv.rows(m, a, i, k[e], before[e], src, dst)) atomicMin(&end, i);
-            if (src < 0 || dst < 0 || src == dst) src = dst = -1;
-            rows[(buf * 2 + 0) * ROWS + r] = src;
-            rows[(buf * 2 + 1) * ROWS + r] = dst;
+            const int i = i0 + w0 + e * 32 + lane;
+            src[e] = dst[e] = -1;
+            if (e * 32 + lane < WARP && i < mv.n && !mv.rows(m, a, i, k[e], before[e], src[e], dst[e])) atomicMin(&end, i);
+            if (src[e] < 0 || dst[e] < 0 || src[e] == dst[e]) src[e] = dst[e] = -1;
         }
     };
-    uint4 piece[8];
-    float scale[EACH];
-    const auto load = [&](int i0, int buf) {
-        const int lim = end - i0;
+    const auto request = [&](int stage) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int r = p * (ROWS / 8) + (int)tid / PIECES;
-            const int64_t s = rows[buf * 2 * ROWS + r];
-            if (s >= 0 && r < lim) piece[p] = *reinterpret_cast<const uint4 *>(codes + ((head + s) * PIECES + tid % PIECES) * 16);
+        for (int p = 0; p < kPieces; ++p) {
+            const int64_t s = __shfl_sync(0xffffffffu, src[p * STEP / 32], (p * STEP + lane / PIECES) & 31);
+            if (s >= 0) copy_async(&sm.piece[stage][p][tid], codes + ((head + s) * PIECES + lane % PIECES) * 16, 16);
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int r = e * kMovers + (int)tid;
-            const int64_t s = rows[buf * 2 * ROWS + r];
-            if (s >= 0 && r < lim) scale[e] = scales[head + s];
+            if (src[e] >= 0) copy_async(&sm.scale[stage][e][tid], scales + head + src[e], 4);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch(0);
-    __syncthreads();  // end is set
-    look(0, 0);
+    look(0);
     fetch(ROWS);
-    __syncthreads();
-    load(0, 0);
-    int buf = 0;
-    for (int i0 = 0; i0 < end; i0 += ROWS, buf ^= 1) {
-        look(i0 + ROWS, buf ^ 1);
-        fetch(i0 + 2 * ROWS);
-        const uint4 was[8] = {piece[0], piece[1], piece[2], piece[3], piece[4], piece[5], piece[6], piece[7]};
-        float had[EACH];
+    request(0);
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) had[e] = scale[e];
-        __syncthreads();  // the group is read by all, the next one's rows are known to all
-        const int lim = end - i0;
-        load(i0 + ROWS, buf ^ 1);
+    for (int e = 0; e < EACH; ++e) to[0][e] = dst[e];
+    look(ROWS);
+    fetch(2 * ROWS);
+    request(1);
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int r = p * (ROWS / 8) + (int)tid / PIECES;
-            const int64_t d = rows[(buf * 2 + 1) * ROWS + r];
-            if (d >= 0 && r < lim) *reinterpret_cast<uint4 *>(codes + ((head + d) * PIECES + tid % PIECES) * 16) = was[p];
+    for (int e = 0; e < EACH; ++e) to[1][e] = dst[e];
+    int stage = 0;
+    for (int i0 = 0; i0 < end; i0 += ROWS) {
+        look(i0 + 2 * ROWS);
+        fetch(i0 + 3 * ROWS);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // the group is read by all, and its last good move is known
+        const int next = stage == 0 ? 2 : stage - 1;
+        request(next);
+        const int lim = end - i0 - w0;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int r = p * STEP + lane / PIECES;
+            const int64_t d = __shfl_sync(0xffffffffu, to[0][p * STEP / 32], r & 31);
+            if (d >= 0 && r < lim) *reinterpret_cast<uint4 *>(codes + ((head + d) * PIECES + lane % PIECES) * 16) = sm.piece[stage][p][tid];
         }
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            const int r = e * kMovers + (int)tid;
-            const int64_t d = rows[(buf * 2 + 1) * ROWS + r];
-            if (d >= 0 && r < lim) scales[head + d] = had[e];
-        }
-        __syncthreads();  // rows of this group are done with
+        for (int e = 0; e < EACH; ++e)
+            if (to[0][e] >= 0 && e * 32 + lane < lim) scales[head + to[0][e]] = sm.scale[stage][e][tid];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) to[0][e] = to[1][e], to[1][e] = dst[e];
+        stage = stage == 2 ? 0 : stage + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int PIECES>
 cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    constexpr int bytes = sizeof(CompactSmem<PIECES>);
+    if (a.n > 64)
+        if (const cudaError_t e = allow_smem(done, compact_block_kernel<PIECES>, bytes)) return e;
     const int64_t per = (int64_t)m.L * m.Hk;
     // sequences of a launch, such that blocks are counted in 31 bits
     const int64_t chunk = ((int64_t)1 << 29) / per;
@@ -297,7 +316,7 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
         c.count += b0;
         const int64_t units = c.batch * per;
         if (a.n <= 64) compact_warp_kernel<PIECES><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(m, c, units);
-        else compact_block_kernel<PIECES><<<(unsigned)(units * 2), kMovers, kMovers * 8 / PIECES * 4 * sizeof(int64_t), st>>>(m, c);
+        else compact_block_kernel<PIECES><<<(unsigned)(units * 2), kMovers, bytes, st>>>(m, c);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

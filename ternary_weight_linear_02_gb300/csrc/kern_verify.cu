@@ -16,6 +16,7 @@
 // at 1/64 of the rate), decisions are made in fp64.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace tl {
 
@@ -72,6 +73,11 @@ struct Weights {
     float ah, al;  // A
     int gone;
     const int *list;
+    // a thread's own entries of the rows, kept in shared memory while a node's children are rejected one by one:
+    // 0 not kept, 1 to be kept, 2 there
+    uint4 *kept;
+    int keep, threads;
+    __device__ __forceinline__ uint4 &slot(int i) const { return kept[i * threads + (int)threadIdx.x]; }
     __device__ __forceinline__ Pair of(float p, float q) const {
         const float t = __fmul_rn(ah, q), te = __fmaf_rn(al, q, __fmaf_rn(ah, q, -t));
         // p - t and what its rounding lost: exact where p >= t, and where they are near each other; else w is 0
@@ -122,14 +128,25 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool in = v + u * 32 * W < whole;
+                const int at = 2 * ((v + u * 32 * W - lo) / (32 * W));
                 x[u] = y[u] = make_uint4(0, 0, 0, 0);
-                if (in) x[u] = ldg_nc_v4(w.p + v + u * 32 * W);
-                if (in && w.q) y[u] = ldg_nc_v4(w.q + v + u * 32 * W);
+                if (in && w.keep == 2) {
+                    x[u] = w.slot(at);
+                    y[u] = w.slot(at + 1);
+                } else {
+                    if (in) x[u] = ldg_nc_v4(w.p + v + u * 32 * W);
+                    if (in && w.q) y[u] = ldg_nc_v4(w.q + v + u * 32 * W);
+                }
             }
         };
         const auto add_up = [&](int v, const uint4 (&x)[U], const uint4 (&y)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (w.keep == 1 && v + u * 32 * W < whole) {
+                    const int at = 2 * ((v + u * 32 * W - lo) / (32 * W));
+                    w.slot(at) = x[u];
+                    w.slot(at + 1) = y[u];
+                }
                 float pv[W], qv[W];
                 values16<T>(x[u], pv);
                 values16<T>(y[u], qv);
@@ -154,14 +171,29 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
         }
         if (whole + lane < hi) take(w.at(whole + lane));
     } else {
-        constexpr int U = 8;
+        constexpr int U = 8;  // (a slot holds two tokens)
         for (int v = lo + lane; v < hi; v += U * 32) {
             float p[U], q[U];
+            const int at = (v - lo) / (32 * 2);
+            if (w.keep == 2) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = v + u * 32 < hi;
-                p[u] = in ? prob(w.p[v + u * 32]) : 0.f;
-                q[u] = in && w.q ? prob(w.q[v + u * 32]) : 0.f;
+                for (int u = 0; u < U; u += 2) {
+                    const uint4 s = w.slot(at + u / 2);
+                    p[u] = __uint_as_float(s.x), q[u] = __uint_as_float(s.y), p[u + 1] = __uint_as_float(s.z), q[u + 1] = __uint_as_float(s.w);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = v + u * 32 < hi;
+                    p[u] = in ? prob(w.p[v + u * 32]) : 0.f;
+                    q[u] = in && w.q ? prob(w.q[v + u * 32]) : 0.f;
+                }
+                if (w.keep == 1) {
+#pragma unroll
+                    for (int u = 0; u < U; u += 2)
+                        w.slot(at + u / 2) =
+                            make_uint4(__float_as_uint(p[u]), __float_as_uint(q[u]), __float_as_uint(p[u + 1]), __float_as_uint(q[u + 1]));
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -259,8 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
     const int run = (((hi - lo + kWarps - 1) / kWarps) + 7) & ~7;
     __syncthreads();
     if (C > 1) cluster_wait();  // every block has started
+    extern __shared__ uint4 kept[];
     Weights<T> w;
     w.list = gone;
+    w.kept = kept;
+    w.threads = kThreads;
+    w.keep = 0;
+    int kept_node = -1;
     int buf = 0;
     double all = 0., upto = 0.;  // warp 0: the sum, and (lane i) the sum of blocks 0 .. i
     const auto pass = [&] {
@@ -381,6 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
         w.ah = A.hi;
         w.al = A.lo;
         w.gone = st.gone;
+        w.keep = todo == 0 || !a.keep ? 0 : kept_node == st.node ? 2 : 1;
+        if (w.keep) kept_node = st.node;
         pass();
         if (todo == 0) break;
         __syncthreads();  // st is read by all before it changes
@@ -420,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
         __syncthreads();
         if (again || !fin.empty || !(w.q || w.gone)) break;
         w.q = nullptr;  // nothing is left: the target's own row
-        w.gone = 0;
+        w.gone = w.keep = 0;
         pass();
         __syncthreads();
     }
@@ -482,7 +521,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
 
 template <typename T, bool VEC, int THREADS>
 cudaError_t launch_one(const VerifyArgs &a, cudaStream_t st) {
+    // rows kept by the threads: only a tree looks at a node's rows more than once.  Up to 80 KB, so that two blocks
+    // of 512 threads share an SM
+    constexpr int kMost = 80 * 1024, WARPS = THREADS / 32;
+    const int64_t per = (((a.V + (int64_t)a.blocks - 1) / a.blocks) + 255) & ~(int64_t)255, run = (((per + WARPS - 1) / WARPS) + 7) & ~(int64_t)7;
+    const int64_t slots = VEC ? 2 * ((run + 32 * (16 / (int)sizeof(T)) - 1) / (32 * (16 / (int)sizeof(T)))) : (run + 8 * 32 - 1) / (8 * 32) * 4;
+    VerifyArgs b = a;
+    b.keep = a.parent && a.draft && THREADS == 512 && slots * THREADS * 16 <= kMost;
+    const auto kernel = verify_kernel<T, VEC, THREADS>;
+    static std::atomic<uint64_t> done{0};
+    if (b.keep)
+        if (const cudaError_t e = allow_smem(done, kernel, kMost)) return e;
     cudaLaunchConfig_t c{};
+    c.dynamicSmemBytes = b.keep ? (size_t)(slots * THREADS * 16) : 0;
     c.gridDim = dim3((unsigned)(a.B * a.blocks));
     c.blockDim = dim3(THREADS);
     c.stream = st;
@@ -492,7 +543,7 @@ cudaError_t launch_one(const VerifyArgs &a, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, verify_kernel<T, VEC, THREADS>, a);
+    return cudaLaunchKernelEx(&c, kernel, b);
 }
 
 template <typename T>

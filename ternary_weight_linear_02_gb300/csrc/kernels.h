@@ -316,6 +316,7 @@ struct KvMove {
     float *ks[kMoveLayers], *vs[kMoveLayers];
     int64_t pages;
     int L, P, Hk, rb;  // layers, page size, kv heads, bytes of a row of codes (a multiple of 16)
+    int shift;         // P = 1 << shift, or -1
     int *status;
 };
 cudaError_t launch_kv_copy(const KvMove &m, const int *src, const int *dst, const int *tokens, int64_t n,
@@ -346,6 +347,7 @@ struct VerifyArgs {
     int64_t B;
     int T, V;
     int blocks;  // of a cluster
+    int keep;    // threads keep their entries of a node's rows in shared memory
     int *status;
 };
 cudaError_t launch_verify(const VerifyArgs &a, int dtype, bool vec, int sm_count, cudaStream_t st);
