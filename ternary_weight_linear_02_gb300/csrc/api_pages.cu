@@ -33,6 +33,8 @@ tl_status check_layers(const tl_kv_cache *c, int32_t layers) {
         if (c[i].pages != c->pages || c[i].page_size != c->page_size || c[i].kv_heads != c->kv_heads ||
             c[i].head_dim != c->head_dim || c[i].format != c->format)
             return TL_ERR_SHAPE;
+        // rows are counted in 32 bits (2^32 of 32 bytes and their scales, keys and values: beyond any memory)
+        if (c[i].pages * c[i].kv_heads >= (((int64_t)1 << 32) - 1) / c[i].page_size) return TL_ERR_SHAPE;
         if (c[i].k_codes == c[i].v_codes || c[i].k_scale == c[i].v_scale) return TL_ERR_VALUE;
         for (int j = 0; j < i; ++j)
             if (c[i].k_codes == c[j].k_codes || c[i].v_codes == c[j].v_codes || c[i].k_scale == c[j].k_scale ||

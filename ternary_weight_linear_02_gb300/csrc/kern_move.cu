@@ -106,16 +106,28 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__
 // order, a group's reads before its writes, therefore give what reading everything first
 // would, and the next group may be read before this one is written.
 
-// Row (place of one head of the pool) of a sequence's place; -1 for a page that the pool does not have.
-__device__ __forceinline__ int64_t row_of(const KvMove &m, const KvCompactArgs &a, const int *pages, uint32_t place) {
-    const uint32_t p = m.shift >= 0 ? place >> m.shift : place / (uint32_t)m.P;
-    const int page = pages[p];
-    if ((uint32_t)page >= (uint32_t)m.pages) {
-        flag_value(m.status);
-        return -1;
+// Rows of a cache are counted in 32 bits (the call checks it: more would not fit this GPU's memory).
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// A place of a sequence on its way to its row of the pool (of one head): first the entry of the page table is requested,
+// then, when it is there, looked at.
+struct Place {
+    int page;
+    uint32_t off;
+    __device__ __forceinline__ void request(const KvMove &m, const int *pages, uint32_t place) {
+        const uint32_t p = m.shift >= 0 ? place >> m.shift : place / (uint32_t)m.P;
+        page = pages[p];
+        off = place - p * (uint32_t)m.P;
     }
-    return (int64_t)page * m.Hk * m.P + (place - p * (uint32_t)m.P);
-}
+    // kNone for a page that the pool does not have
+    __device__ __forceinline__ uint32_t row(const KvMove &m) const {
+        if ((uint32_t)page >= (uint32_t)m.pages) {
+            flag_value(m.status);
+            return kNone;
+        }
+        return (uint32_t)page * (uint32_t)(m.Hk * m.P) + off;
+    }
+};
 
 struct Moves {
     int start, n;  // first place; moves of the sequence
@@ -130,16 +142,22 @@ struct Moves {
             n = start < 0 || n < 0 ? 0 : (int)a.n;
         }
     }
-    // rows of move i (k = keep[i], before = keep[i - 1]), or false where the sequence's moves end
-    __device__ __forceinline__ bool rows(const KvMove &m, const KvCompactArgs &a, int i, int k, int before, int64_t &src, int64_t &dst) const {
+    // move i (k = keep[i], before = keep[i - 1]): where its entry lies and goes; false where the sequence's moves end
+    __device__ __forceinline__ bool request(const KvMove &m, const KvCompactArgs &a, int i, int k, int before, Place &src, Place &dst) const {
         const int64_t place = (int64_t)start + k;
         if (k <= before || k < i || place >= a.max_places) {  // (k < i: an earlier one did not ascend)
             flag_value(m.status);
             return false;
         }
-        src = row_of(m, a, pages, (uint32_t)place);
-        dst = k == i ? src : row_of(m, a, pages, (uint32_t)(start + i));
+        src.request(m, pages, (uint32_t)place);
+        dst.request(m, pages, (uint32_t)(start + i));
         return true;
+    }
+    // their rows; both kNone where nothing moves
+    __device__ __forceinline__ void rows(const KvMove &m, const Place &from, const Place &to, uint32_t &src, uint32_t &dst) const {
+        src = from.row(m);
+        dst = to.row(m);
+        if (src == kNone || dst == kNone || src == dst) src = dst = kNone;
     }
 };
 
@@ -154,36 +172,39 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
     const uint32_t per = (uint32_t)(m.L * m.Hk);
     const int64_t b = u / per;
     const uint32_t lh = (uint32_t)(u - b * per), layer = lh / (uint32_t)m.Hk;
-    const int64_t head = (int64_t)(lh - layer * (uint32_t)m.Hk) * m.P;
+    const uint32_t head = (lh - layer * (uint32_t)m.Hk) * (uint32_t)m.P;
     const Moves mv(m, a, b);
     uint8_t *const kc = m.kc[layer], *const vc = m.vc[layer];
     float *const ks = m.ks[layer], *const vs = m.vs[layer];
     bool more = true;
     for (int i0 = 0; i0 < mv.n && more; i0 += 16) {
-        int64_t src = -1, dst = -1;
+        uint32_t src = kNone, dst = kNone;
         bool ok = true;
-        if (lane < 16 && i0 + lane < mv.n) ok = mv.rows(m, a, i0 + lane, mv.keep[i0 + lane], i0 + lane > 0 ? mv.keep[i0 + lane - 1] : -1, src, dst);
+        if (lane < 16 && i0 + lane < mv.n) {
+            Place from, to;
+            ok = mv.request(m, a, i0 + lane, mv.keep[i0 + lane], i0 + lane > 0 ? mv.keep[i0 + lane - 1] : -1, from, to);
+            if (ok) mv.rows(m, from, to, src, dst);
+        }
         const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
         if (bad) {  // nothing from the first bad move on
             more = false;
-            if (lane >= __ffs(bad) - 1) src = dst = -1;
+            if (lane >= __ffs(bad) - 1) src = dst = kNone;
         }
-        if (src < 0 || dst < 0 || src == dst) src = dst = -1;
         uint4 k[PASSES], v[PASSES];
         int64_t to[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int row = p * ROWS + lane / PIECES;
-            const int64_t s = __shfl_sync(0xffffffffu, src, row), d = __shfl_sync(0xffffffffu, dst, row);
-            to[p] = d < 0 ? -1 : ((head + d) * PIECES + lane % PIECES) * 16;
-            if (d >= 0) {
-                const int64_t from = ((head + s) * PIECES + lane % PIECES) * 16;
+            const uint32_t s = __shfl_sync(0xffffffffu, src, row), d = __shfl_sync(0xffffffffu, dst, row);
+            to[p] = d == kNone ? -1 : ((int64_t)(head + d) * PIECES + lane % PIECES) * 16;
+            if (d != kNone) {
+                const int64_t from = ((int64_t)(head + s) * PIECES + lane % PIECES) * 16;
                 k[p] = *reinterpret_cast<const uint4 *>(kc + from);
                 v[p] = *reinterpret_cast<const uint4 *>(vc + from);
             }
         }
         float x = 0.f, y = 0.f;
-        if (dst >= 0) x = ks[head + src], y = vs[head + src];
+        if (dst != kNone) x = ks[head + src], y = vs[head + src];
         __syncwarp();
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
@@ -191,7 +212,7 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
                 *reinterpret_cast<uint4 *>(kc + to[p]) = k[p];
                 *reinterpret_cast<uint4 *>(vc + to[p]) = v[p];
             }
-        if (dst >= 0) ks[head + dst] = x, vs[head + dst] = y;
+        if (dst != kNone) ks[head + dst] = x, vs[head + dst] = y;
         __syncwarp();
     }
 }
@@ -204,8 +225,8 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes
 
 // Many moves: a block per (sequence, layer, head, keys or values), in groups of 512 x 4 pieces of 16 bytes.  Two groups
 // travel to shared memory while a third is written: a thread writes what it copied itself, so the one barrier a
-// group says only that all of its reads are done.  Each lane looks up EACH moves of its warp; keep is
-// requested a group before that.
+// group says only that all of its reads are done.  Each lane looks up EACH moves of its warp: keep is
+// requested two groups before an entry is, the page a group before.
 template <int PIECES>
 struct CompactSmem {
     static constexpr int WARP = 32 * kPieces / PIECES, EACH = (WARP + 31) / 32;  // moves of a warp; looked up by a lane
@@ -223,14 +244,15 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
     const int lane = tid & 31, w0 = (int)(tid >> 5) * WARP;
     const int64_t u = blockIdx.x, b = u / per;
     const uint32_t rest = (uint32_t)(u - b * per), lh = rest >> 1, layer = lh / (uint32_t)m.Hk;
-    const int64_t head = (int64_t)(lh - layer * (uint32_t)m.Hk) * m.P;
+    const uint32_t head = (lh - layer * (uint32_t)m.Hk) * (uint32_t)m.P;
     const Moves mv(m, a, b);
     uint8_t *const codes = rest & 1u ? m.vc[layer] : m.kc[layer];
     float *const scales = rest & 1u ? m.vs[layer] : m.ks[layer];
+    uint8_t *const mine = codes + lane % PIECES * 16;
     if (tid == 0) end = mv.n;
     __syncthreads();
     int k[EACH], before[EACH];
-    int64_t src[EACH], dst[EACH], to[2][EACH];  // rows, or -1: of the group looked up, and where those in flight go
+    uint32_t src[EACH], dst[EACH], to[2][EACH];  // rows, or kNone: of the group looked up, and where those in flight go
     const auto fetch = [&](int i0) {
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
@@ -241,56 +263,71 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
             }
         }
     };
-    const auto look = [&](int i0) {
+    Place from[EACH], into[EACH];
+    bool good[EACH];
+    const auto look = [&](int i0) {  // entries of the page table are requested ..
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
             const int i = i0 + w0 + e * 32 + lane;
-            src[e] = dst[e] = -1;
-            if (e * 32 + lane < WARP && i < mv.n && !mv.rows(m, a, i, k[e], before[e], src[e], dst[e])) atomicMin(&end, i);
-            if (src[e] < 0 || dst[e] < 0 || src[e] == dst[e]) src[e] = dst[e] = -1;
+            good[e] = e * 32 + lane < WARP && i < mv.n;
+            if (good[e] && !mv.request(m, a, i, k[e], before[e], from[e], into[e])) {
+                good[e] = false;
+                atomicMin(&end, i);
+            }
+        }
+    };
+    const auto found = [&] {  // .. and looked at, a group later
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            src[e] = dst[e] = kNone;
+            if (good[e]) mv.rows(m, from[e], into[e], src[e], dst[e]);
         }
     };
     const auto request = [&](int stage) {
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            const int64_t s = __shfl_sync(0xffffffffu, src[p * STEP / 32], (p * STEP + lane / PIECES) & 31);
-            if (s >= 0) copy_async(&sm.piece[stage][p][tid], codes + ((head + s) * PIECES + lane % PIECES) * 16, 16);
+            const uint32_t s = __shfl_sync(0xffffffffu, src[p * STEP / 32], (p * STEP + lane / PIECES) & 31);
+            if (s != kNone) copy_async(&sm.piece[stage][p][tid], mine + (int64_t)(head + s) * (PIECES * 16), 16);
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            if (src[e] >= 0) copy_async(&sm.scale[stage][e][tid], scales + head + src[e], 4);
+            if (src[e] != kNone) copy_async(&sm.scale[stage][e][tid], scales + (head + src[e]), 4);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch(0);
     look(0);
     fetch(ROWS);
+    found();
     request(0);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) to[0][e] = dst[e];
     look(ROWS);
     fetch(2 * ROWS);
+    found();
     request(1);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) to[1][e] = dst[e];
+    look(2 * ROWS);
+    fetch(3 * ROWS);
     int stage = 0;
     for (int i0 = 0; i0 < end; i0 += ROWS) {
-        look(i0 + 2 * ROWS);
-        fetch(i0 + 3 * ROWS);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();  // the group is read by all, and its last good move is known
-        const int next = stage == 0 ? 2 : stage - 1;
-        request(next);
+        found();
+        request(stage == 0 ? 2 : stage - 1);
+        look(i0 + 3 * ROWS);
+        fetch(i0 + 4 * ROWS);
         const int lim = end - i0 - w0;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int r = p * STEP + lane / PIECES;
-            const int64_t d = __shfl_sync(0xffffffffu, to[0][p * STEP / 32], r & 31);
-            if (d >= 0 && r < lim) *reinterpret_cast<uint4 *>(codes + ((head + d) * PIECES + lane % PIECES) * 16) = sm.piece[stage][p][tid];
+            const uint32_t d = __shfl_sync(0xffffffffu, to[0][p * STEP / 32], r & 31);
+            if (d != kNone && r < lim) *reinterpret_cast<uint4 *>(mine + (int64_t)(head + d) * (PIECES * 16)) = sm.piece[stage][p][tid];
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e)
-            if (to[0][e] >= 0 && e * 32 + lane < lim) scales[head + to[0][e]] = sm.scale[stage][e][tid];
+            if (to[0][e] != kNone && e * 32 + lane < lim) scales[head + to[0][e]] = sm.scale[stage][e][tid];
 #pragma unroll
         for (int e = 0; e < EACH; ++e) to[0][e] = to[1][e], to[1][e] = dst[e];
         stage = stage == 2 ? 0 : stage + 1;
