@@ -525,8 +525,8 @@ tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const in
  *     int32 [batch]: how many; out_tokens int64 [batch, draft + 1]: their tokens, then the
  *     drawn one, -1 behind it.
  *   A drafted token outside [0, vocab) or with a parent out of range is not looked at, nor what
- *   follows it; a row of which nothing can be drawn gives the token -1.  Both set the device
- *   status word to TL_ERR_VALUE.
+ *   follows it; a row of which nothing can be drawn (none of it is above 0, or its sum is
+ *   infinite) gives the token -1.  Both set the device status word to TL_ERR_VALUE.
  *   draft 0..1024 (0: a token is drawn), batch <= 65536, vocab 1..2^31 - 2^12.
  * Comparisons are made in fp64; sums carry 47 bits or more, so that a draw lands where one in
  * fp64 does but for random numbers within about 1e-13 of a border.  HBM-bound: one target row is read
@@ -606,7 +606,7 @@ int32_t ternary_skinny_max_m(void);
 /*
  * ternary_device_status -- read (and optionally clear) the current device's
  * status word.  Kernels whose waits are bounded write a non-zero code there
- * when a wait gives up, and the cache and attention calls when an index is out of
+ * when a wait gives up, and the cache, attention and serving calls when an index is out of
  * range; *code receives TL_OK, TL_ERR_TIMEOUT or TL_ERR_VALUE.  Synchronous:
  * call after the work in question has completed (e.g. after a stream sync).
  */
@@ -637,11 +637,11 @@ int32_t ternary_version(void);
 void ternary_test_inject_launch_failures(int32_t n);
 
 /* Testing aid: the give-up time, in SM clock cycles, of the main-loop waits of the
- * decode kernel and of the tcgen05 attention kernel for every later launch
+ * decode kernel, of the tcgen05 attention kernel and of the adapters' tcgen05 form for every later launch
  * (cycles <= 0 restores the default of about 2^30 cycles, ~0.5 s).  stall != 0
  * additionally makes each of those launches first wait on a barrier that nothing
  * arrives on, so the wait runs out: the call then writes no output (attention:
- * NaN where partial results were to be joined) and sets the device status word to
+ * NaN where partial results were to be joined; adapters: NaN) and sets the device status word to
  * TL_ERR_TIMEOUT, while every copy in flight still lands before the kernel
  * exits (those waits have limits of their own).  Lets the give-up path be tested
  * without a fault or a hang. */

@@ -241,11 +241,15 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.plan != nullptr) {
         pdl_wait();
-        if (unit >= a.plan[0]) return false;
+        if (unit >= min(a.plan[0], a.max_tiles)) return false;
         const int *p = a.plan + 4 + 3 * unit;
-        const int n = p[2];
-        if (tid < TM) tile.toks[tid] = tid < n ? a.plan[4 + 3 * a.max_tiles + p[1] + tid] : -1;
-        if (tid == 0) tile.adapter = p[0], tile.count = n;
+        // (the bounds hold unless the workspace is written meanwhile)
+        const int n = min(max(p[2], 1), TM), first = (int)min((int64_t)max(p[1], 0), a.M - n);
+        if (tid < TM) {
+            const int tk = tid < n ? a.plan[4 + 3 * a.max_tiles + max(first, 0) + tid] : 0;
+            tile.toks[tid] = tk >= 0 && tk < a.M ? tk : 0;
+        }
+        if (tid == 0) tile.adapter = min(max(p[0], 0), a.adapters), tile.count = n;
         __syncthreads();
         return true;
     }
@@ -643,9 +647,8 @@ struct ExpandSmall {
     const uint32_t base;  // shared memory of this warp
     const int first, kk, lane;
 
-    // block i of this warp: its shard and first column; false: there is none
-    __device__ __forceinline__ bool block(int i, int &sh, int64_t &col) const {
-        int64_t n = first + (int64_t)i * kk;
+    // block n: its shard and first column; false: there is none
+    __device__ __forceinline__ bool block(int64_t n, int &sh, int64_t &col) const {
         col = a.col0;
         for (sh = 0; sh < (GATED ? 1 : a.S); ++sh) {
             const int64_t blocks = a.shard[sh] / L::COLS;
@@ -658,11 +661,11 @@ struct ExpandSmall {
         }
         return false;
     }
-    __device__ __forceinline__ void copy(int i) const {
+    __device__ __forceinline__ void copy(int stage, int64_t n) const {
         int sh;
         int64_t col;
-        if (block(i, sh, col)) {
-            const uint32_t to = base + (i & 1) * L::stage(a.R), yt = to + H * L::COLS * a.R * 2;
+        if (block(n, sh, col)) {
+            const uint32_t to = base + stage * L::stage(a.R), yt = to + H * L::COLS * a.R * 2;
             const int64_t wide = a.shard[0];
             const int pieces = L::COLS * a.R / 8, shift = 28 - __clz(W * a.R);  // log2 of the pieces of a thread's columns
 #pragma unroll
@@ -681,14 +684,18 @@ struct ExpandSmall {
         }
         copies_commit();
     }
+    __device__ __forceinline__ void copy_first() const {
+        copy(0, first);
+        copy(1, (int64_t)first + kk);
+    }
     __device__ __forceinline__ void run(const Smem &sz, const T *hs, const float *up) const {
         constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
         constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
         const int g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
         const bool two = tile.count > 8;  // the second group of 8 tokens has some
         int sh;
-        int64_t col;
-        for (int i = 0; block(i, sh, col); ++i) {
+        int64_t col, now = first;
+        for (int i = 0; block(now, sh, col); ++i, now += kk) {
             copies_wait<1>();
             __syncwarp();
             const uint32_t bs = base + (i & 1) * L::stage(R), ys = bs + H * L::COLS * R * 2;
@@ -762,7 +769,7 @@ struct ExpandSmall {
                 }
             }
             __syncwarp();  // the stage is read by all
-            copy(i + 2);
+            copy(i & 1, now + 2 * kk);
         }
         copies_wait<0>();
     }
@@ -894,7 +901,15 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
     const int ad = any ? tile.adapter : a.adapters;
     const bool has = ad < a.adapters;
     if (!any || (!has && !GATED && a.out == a.y)) {  // fewer tiles, or tokens to which nothing is added in place
-        if (C > 1) cluster_wait();
+        // (meeting the others at every barrier all the same: should `which` change meanwhile, a block that found a
+        // tile reads this one's memory)
+        if (C > 1) {
+            cluster_wait();
+            for (int i = 0; i < 2; ++i) {
+                cl_arrive_release();
+                cl_wait_acquire();
+            }
+        }
         return;
     }
     const int S = a.S, R = a.R, K = (int)a.K, steps = (R + 15) / 16;
@@ -909,8 +924,7 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
         if constexpr (BIG) return;
         else {
         const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
-        ex.copy(0);
-        ex.copy(1);
+        ex.copy_first();
         }
     };
     if constexpr (!BIG && !GATED) {

@@ -239,8 +239,8 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 }
 
 // One cluster of C blocks per sequence; block r holds tokens [r per, (r + 1) per), warp w of it a run
-// of them.  Every block follows the accepted path by itself (the entries that it turns on
-// are gathered first); sums are exchanged through distributed shared memory.
+// of them.  Every block follows the accepted path by itself: the entries that it turns on are gathered and given to
+// all first, sums are exchanged through distributed shared memory.
 // Bound by latency: the gather (two dependent loads), a pass, the cluster's barrier, the drawing.
 // fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
 // warp takes the SM's unit 16 cycles.
@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
     constexpr int kWarps = kThreads / 32;
     __shared__ float px[kMaxDraft], qx[kMaxDraft], un[kMaxDraft + 1];
     __shared__ int tok[kMaxDraft], par[kMaxDraft], path[kMaxDraft], gone[kMaxDraft];
-    __shared__ uint8_t fresh[kMaxDraft];  // accepted as its node's first child
     __shared__ Pair warp_sum[kWarps], part[kWarps], block_sum[2][kMaxBlocks];
     __shared__ struct {
         int todo;  // 0: a pass over p, 1: over p and q, 2: done
@@ -267,20 +266,44 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
     const T *target = static_cast<const T *>(a.target) + b * a.target_b;
     const T *draft = a.draft ? static_cast<const T *>(a.draft) + b * a.draft_b : nullptr;
     if (C > 1) cluster_arrive_relaxed();
-    for (int i = tid; i <= n; i += kThreads) {
-        un[i] = a.uniform[b * a.uniform_b + i];
-        if (i == n) break;
-        const int64_t x = a.tokens[b * a.tokens_b + i];
-        const int at = a.parent ? a.parent[b * a.parent_b + i] : i - 1;
-        const bool ok = x >= 0 && x < V && at >= -1 && at < i;
-        if (!ok && rank == 0) flag_value(a.status);
-        const float p = ok ? prob(target[(at + 1) * a.target_n + x]) : 0.f, q = ok && draft ? prob(draft[(at + 1) * a.draft_n + x]) : 1.f;
-        tok[i] = (int)x;
-        par[i] = ok ? at : -2;
-        px[i] = p;
-        qx[i] = q;
-        fresh[i] = (double)un[i] * (double)q < (double)p;  // (the product of two fp32 is exact)
+    // entry i is looked up by one block and given to all (a thread for each of them): whatever happens to the inputs
+    // meanwhile, all blocks take the same decisions and meet at the same barriers
+    for (int e0 = 0; e0 * C + rank <= n; e0 += kThreads / C) {
+        const int i = (e0 + tid / C) * C + rank, to = tid % C;
+        float u = 0.f, p = 0.f, q = 1.f;
+        int64_t x = 0;
+        int up = -4;  // (parent, accepted as its node's first child)
+        if (i <= n) u = a.uniform[b * a.uniform_b + i];
+        if (i < n) {
+            x = a.tokens[b * a.tokens_b + i];
+            const int at = a.parent ? a.parent[b * a.parent_b + i] : i - 1;
+            if (x >= 0 && x < V && at >= -1 && at < i) {
+                p = prob(target[(at + 1) * a.target_n + x]);
+                if (draft) q = prob(draft[(at + 1) * a.draft_n + x]);
+                up = at * 2 + ((double)u * (double)q < (double)p ? 1 : 0);  // (the product of two fp32 is exact)
+            } else if (to == 0) {
+                flag_value(a.status);
+            }
+        }
+        if (C > 1 && e0 == 0) cluster_wait();  // every block has started
+        if (i > n) continue;
+        if (C > 1) {
+            cl_st_f32(cl_map(smem_u32(&un[i]), to), u);
+            if (i == n) continue;
+            cl_st_f32(cl_map(smem_u32(&px[i]), to), p);
+            cl_st_f32(cl_map(smem_u32(&qx[i]), to), q);
+            cl_st_u32(cl_map(smem_u32(&tok[i]), to), (uint32_t)x);
+            cl_st_u32(cl_map(smem_u32(&par[i]), to), (uint32_t)up);
+        } else {
+            un[i] = u;
+            if (i == n) continue;
+            px[i] = p;
+            qx[i] = q;
+            tok[i] = (int)x;
+            par[i] = up;
+        }
     }
+    if (C > 1 && rank > n) cluster_wait();  // (no entry was this block's)
     if (tid == 0) {
         st.node = st.count = st.gone = st.next = 0;
         st.A = 0.;
@@ -289,8 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
     // tokens of this block, and of each of its warps
     const int per = (((V + C - 1) / C) + 255) & ~255, lo = min(V, rank * per), hi = min(V, lo + per);
     const int run = (((hi - lo + kWarps - 1) / kWarps) + 7) & ~7;
-    __syncthreads();
-    if (C > 1) cluster_wait();  // every block has started
+    if (C > 1) {
+        cl_arrive_release();
+        cl_wait_acquire();
+    } else {
+        __syncthreads();
+    }
     extern __shared__ uint4 kept[];
     Weights<T> w;
     w.list = gone;
@@ -348,14 +375,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
                 if (a.parent) {
                     int at = n;
                     for (int j = i; j < n; j += 32) {
-                        const uint32_t hit = __ballot_sync(0xffffffffu, j + lane < n && par[min(j + lane, n - 1)] == node - 1);
+                        const uint32_t hit = __ballot_sync(0xffffffffu, j + lane < n && par[min(j + lane, n - 1)] >> 1 == node - 1);
                         if (hit) {
                             at = j + __ffs(hit) - 1;
                             break;
                         }
                     }
                     i = at;
-                } else if (i < n && par[i] != node - 1) {  // (a chain's node has one child)
+                } else if (i < n && par[i] >> 1 != node - 1) {  // (a chain's node has one child)
                     i = n;
                 }
                 if (i >= n) {
@@ -366,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
                 bool yes;
                 double p = 0.;
                 if (first) {
-                    yes = fresh[i];
+                    yes = par[i] & 1;
                     if (!yes && !draft) p = (double)px[i];
                 } else {
                     p = (double)px[i];
