@@ -576,7 +576,7 @@ typedef struct {
  * ternary_lora_silu_mul -- the same for a fused gate/up layer (two shards of N columns: gate, up),
  *   with the gated product behind it: g, u the two halves of the sum (fp32),
  *   out[m, j] = silu(g[m, j]) u[m, j], out [tokens, N], which must not overlap y.
- * HBM-bound: x, y and out once, the adapters that occur once per 16 to 64 tokens of theirs.
+ * HBM-bound: x, y and out once, the adapters that occur once per 16 or 128 tokens of theirs.
  */
 int64_t ternary_lora_workspace(int64_t tokens, int64_t adapters); /* -1: invalid */
 tl_status ternary_lora_add(const void *x, int64_t x_stride, const tl_adapters *adapters,

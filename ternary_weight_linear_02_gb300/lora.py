@@ -83,47 +83,60 @@ def _lib():
 
 def _rows(t: torch.Tensor, what: str, cols: int, dev: torch.device) -> tuple[torch.Tensor, int]:
     """[tokens, cols] with a dense last axis, and its token stride."""
-    _same(t, what, dev)
-    if t.dim() != 2:
-        t = t.reshape(-1, cols)
+    if t.device != dev:
+        _same(t, what, dev)
     st = t.stride()
+    if len(st) != 2:
+        t = t.reshape(-1, cols)
+        st = t.stride()
     if st[1] != 1 and cols > 1:
         t = t.contiguous()
         st = t.stride()
     return t, st[0]
 
 
-def _call(f, what: str, x, adapters: Adapters, which, y, out, cols: int):
-    dev, k = adapters.device, adapters.inputs
-    if x.dtype is not adapters.dtype or x.dim() < 1 or x.shape[-1] != k:
+def _call(name: str, x, adapters: Adapters, which, y, out, cols: int):
+    dev, k, kind = adapters.device, adapters.inputs, y.dtype
+    shape = x.shape
+    if x.dtype is not adapters.dtype or len(shape) < 1 or shape[-1] != k:
         raise ValueError(f"x must be [..., {k}] in the adapters' dtype")
-    n, lead = adapters.outputs, x.shape[:-1]
-    if y.shape != (*lead, n) or (y.dtype is not torch.float32 and y.dtype is not adapters.dtype):
+    n, lead = adapters.outputs, shape[:-1]
+    if y.shape != (*lead, n) or (kind is not torch.float32 and kind is not adapters.dtype):
         raise ValueError(f"y must be [..., {n}] with x's leading dimensions, in the adapters' dtype or fp32")
     x, xs = _rows(x, "x", k, dev)
     m = x.shape[0]
-    if which.dtype is not torch.int32 or which.numel() != m or which.shape != lead and which.dim() != 1:
+    wshape = which.shape
+    if which.dtype is not torch.int32 or not (wshape == lead or wshape == (m,)):
         raise ValueError("which must be int32, one number for each token")
-    _same(which, "which", dev)
-    which = which.contiguous()
+    if which.device != dev:
+        _same(which, "which", dev)
+    if not which.is_contiguous():
+        which = which.contiguous()
     if out is None:
-        out = torch.empty((*lead, cols), dtype=y.dtype, device=dev)
-    elif out.shape != (*lead, cols) or out.dtype is not y.dtype or out.device != dev or out.dim() != 2 and not out.is_contiguous():
-        raise ValueError(f"out must be [..., {cols}] with y's leading dimensions, dtype and device (contiguous unless two-dimensional)")
-    o = out if out.dim() == 2 else out.view(-1, cols)
-    if o.stride(1) != 1 and cols > 1:
-        raise ValueError("out must be dense in its last axis")
-    if out is not y:
-        y, ys = _rows(y, "y", n, dev)
+        o = out = torch.empty((*lead, cols), dtype=kind, device=dev)
+        os = cols
+        if len(lead) != 1:
+            o = out.view(-1, cols)
     else:
-        y, ys = o, o.stride(0)
+        if out.shape != (*lead, cols) or out.dtype is not kind or out.device != dev or len(lead) != 1 and not out.is_contiguous():
+            raise ValueError(f"out must be [..., {cols}] with y's leading dimensions, dtype and device (contiguous unless two-dimensional)")
+        o = out if len(lead) == 1 else out.view(-1, cols)
+        os, dense = o.stride()
+        if dense != 1 and cols > 1:
+            raise ValueError("out must be dense in its last axis")
+    if out is y:
+        y, ys = o, os
+    else:
+        y, ys = _rows(y, "y", n, dev)
     lib = _ready or _lib()
-    need = int(lib.ternary_lora_workspace(m, adapters.count)) if m > 1024 or adapters.count > 1024 else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    rc = _launch(dev, f(lib), x.data_ptr(), xs, adapters._ref, which.data_ptr(), y.data_ptr(), ys, o.data_ptr(), o.stride(0), _DT[y.dtype], m,
-                 None if ws is None else ws.data_ptr(), max(need, 0))
+    ws, need = None, 0
+    if m > 1024 or adapters.count > 1024:
+        need = int(lib.ternary_lora_workspace(m, adapters.count))
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = _launch(dev, getattr(lib, name), x.data_ptr(), xs, adapters._ref, which.data_ptr(), y.data_ptr(), ys, o.data_ptr(), os, _DT[kind], m,
+                 None if ws is None else ws.data_ptr(), need)
     if rc:
-        _check(rc, what)
+        _check(rc, name)
     return out
 
 
@@ -131,7 +144,7 @@ def lora_add(x: torch.Tensor, adapters: Adapters, which: torch.Tensor, y: torch.
     """y + each token's adapter product: x [..., inputs] (fp16 or bf16, the adapters' dtype), y [..., outputs] (that dtype or
     fp32) what the shared layer gave for x, which int32 [...]: each token's adapter, negative: none.  Sums are fp32, the
     result is rounded once to y's dtype.  out: where to write; y itself adds in place."""
-    return _call(lambda lib: lib.ternary_lora_add, "ternary_lora_add", x, adapters, which, y, out, adapters.outputs)
+    return _call("ternary_lora_add", x, adapters, which, y, out, adapters.outputs)
 
 
 def lora_silu_mul(x: torch.Tensor, adapters: Adapters, which: torch.Tensor, y: torch.Tensor, *, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -140,4 +153,4 @@ def lora_silu_mul(x: torch.Tensor, adapters: Adapters, which: torch.Tensor, y: t
     stay fp32, the result is rounded once to y's dtype."""
     if len(adapters.shards) != 2 or adapters.shards[0] != adapters.shards[1]:
         raise ValueError("a gated layer has two shards of one size: gate and up")
-    return _call(lambda lib: lib.ternary_lora_silu_mul, "ternary_lora_silu_mul", x, adapters, which, y, out, adapters.outputs // 2)
+    return _call("ternary_lora_silu_mul", x, adapters, which, y, out, adapters.outputs // 2)

@@ -29,9 +29,15 @@ def _lib():
     return _ready
 
 
-def _dense(t: torch.Tensor, what: str, dev: torch.device) -> torch.Tensor:
-    _same(t, what, dev)
-    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
+def _dense(t: torch.Tensor, what: str, dev: torch.device) -> tuple[torch.Tensor, tuple]:
+    """The tensor with a dense last axis, and its strides."""
+    if t.device != dev:
+        _same(t, what, dev)
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        t = t.contiguous()
+        st = t.stride()
+    return t, st
 
 
 def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor, *, draft: torch.Tensor | None = None,
@@ -52,38 +58,41 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
 
     Returns (path int32 [batch, draft], count int32 [batch], tokens int64 [batch, draft + 1]): the indexes of the
     accepted tokens in order, how many, and their tokens followed by the drawn one; -1 behind."""
-    dt = _DT.get(target.dtype)
-    if dt is None or target.dim() != 3 or target.shape[1] < 1:
+    kind = target.dtype
+    dt, shape = _DT.get(kind), target.shape
+    if dt is None or len(shape) != 3 or shape[1] < 1:
         raise ValueError("target must be [batch, draft + 1, vocab] in fp32, fp16 or bf16")
-    dev = _cuda(target, "target")
-    b, n, v = target.shape
+    dev = target.device
+    if not target.is_cuda:
+        _cuda(target, "target")
+    b, n, v = shape
     n -= 1
     if tokens.dtype is not torch.int64 or tokens.shape != (b, n):
         raise ValueError(f"tokens must be int64 [batch, draft] = [{b}, {n}]")
     if uniform.dtype is not torch.float32 or uniform.shape != (b, n + 1):
         raise ValueError(f"uniform must be fp32 [batch, draft + 1] = [{b}, {n + 1}]")
-    target = _dense(target, "target", dev)
-    tokens = _dense(tokens, "tokens", dev)
-    uniform = _dense(uniform, "uniform", dev)
-    ts = target.stride()
+    target, (tb, tn, _) = _dense(target, "target", dev)
+    tokens, (xb, _) = _dense(tokens, "tokens", dev)
+    uniform, (ub, _) = _dense(uniform, "uniform", dev)
     qp, qb, qn = None, 0, 0
     if draft is not None:
-        if draft.dtype is not target.dtype or draft.dim() != 3 or draft.shape[0] != b or draft.shape[1] < n or draft.shape[2] != v:
+        shape = draft.shape
+        if draft.dtype is not kind or len(shape) != 3 or shape[0] != b or shape[1] < n or shape[2] != v:
             raise ValueError("draft must be [batch, draft, vocab] in target's dtype")
-        draft = _dense(draft, "draft", dev)
-        qp, (qb, qn, _) = draft.data_ptr(), draft.stride()
+        draft, (qb, qn, _) = _dense(draft, "draft", dev)
+        qp = draft.data_ptr()
     pp, pb = None, 0
     if parent is not None:
-        if parent.dtype is not torch.int32 or parent.shape not in ((n,), (b, n)):
+        shape = parent.shape
+        if parent.dtype is not torch.int32 or not (shape == (b, n) or shape == (n,)):
             raise ValueError("parent must be int32 [draft] or [batch, draft]")
-        parent = _dense(parent, "parent", dev)
-        pp, pb = parent.data_ptr(), parent.stride(0) if parent.dim() == 2 else 0
+        parent, st = _dense(parent, "parent", dev)
+        pp, pb = parent.data_ptr(), st[0] if len(shape) == 2 else 0
     path = torch.empty((b, n), dtype=torch.int32, device=dev)
     count = torch.empty(b, dtype=torch.int32, device=dev)
     out = torch.empty((b, n + 1), dtype=torch.int64, device=dev)
-    rc = _launch(dev, (_ready or _lib()).ternary_verify_drafts, target.data_ptr(), ts[0], ts[1], qp, qb, qn, dt,
-                 tokens.data_ptr(), tokens.stride(0), pp, pb, uniform.data_ptr(), uniform.stride(0), b, n, v,
-                 path.data_ptr(), count.data_ptr(), out.data_ptr())
+    rc = _launch(dev, (_ready or _lib()).ternary_verify_drafts, target.data_ptr(), tb, tn, qp, qb, qn, dt, tokens.data_ptr(), xb, pp,
+                 pb, uniform.data_ptr(), ub, b, n, v, path.data_ptr(), count.data_ptr(), out.data_ptr())
     if rc:
         _check(rc, "ternary_verify_drafts")
     return path, count, out
