@@ -173,7 +173,7 @@ tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const in
     a.n = n;
     cudaError_t e = cudaSuccess;
     for (int i = 0; e == cudaSuccess && i < layers; i += tl::kMoveLayers)
-        e = tl::launch_kv_compact(move_of(caches, i, layers, d.status), a, reinterpret_cast<cudaStream_t>(stream));
+        e = tl::launch_kv_compact(move_of(caches, i, layers, d.status), a, d.sm_count, reinterpret_cast<cudaStream_t>(stream));
     return from_cuda(e);
 }
 

@@ -111,13 +111,18 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
     }
 }
 
-// Tiles of 128 tokens where the adapters that can be there have more than 32 each on average and rows
-// of x and a start on 16 bytes; the ranks of one launch's shards then take up to 128 columns of tensor memory, and
-// more shards are more launches (a gated layer's two belong together).
+// Tiles of 128 tokens where tiles of 16 would read the adapters again and again: 100 MB of them or more, from 128 tokens an
+// adapter that can be there on average.  Rows of x and a start on 16 bytes; up to 64 ranks, held by the threads that
+// expand; the ranks of one launch's shards take up to 128 columns of tensor memory, and more shards are more launches.
+// Measured (us, tiles of 16 / 128; tokens x adapters, rank, 3584 to 3584 columns): 2048 x 2, 16: 26 / 31; 8192 x 64, 16: 75 /
+// 94; 8192 x 6, 16: 66 / 61; 2048 x 16, 32: 43 / 39; 8192 x 16, 32: 112 / 80; 2048 x 8, 64 (4096): 50 / 55; 8192 x 6, 64: 139 /
+// 90; from 18944 columns 296 / 131; rank 128 74 / 122.  Gated layers, whose columns are many, keep to tiles of 16:
+// 1024 x 4, 16, 2 x 18944: 75 against 143.
 constexpr int kBigRanks = 128;
 bool big_tiles(const LoraArgs &a) {
     const int64_t present = a.adapters + 1 < a.M ? a.adapters + 1 : a.M;
-    return a.vec_x && a.R * (a.gated ? 2 : 1) <= kBigRanks && a.M > 32 * present;
+    const double again = (double)a.M / 16 * a.R * 2 * ((double)a.S * a.K + a.N);
+    return a.vec_x && !a.gated && a.R <= 64 && a.M >= 128 * present && again >= 100e6;
 }
 
 int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {
@@ -137,8 +142,10 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
     const bool big = big_tiles(a);
     const int TM = big ? 128 : 16;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
+    // blocks a tile: as many as the SMs hold twice over (gated, where three fit and expanding is most of the work, four
+    // times: 333 x 40 45 us against 66; plain 1024 x 8 15.6 us against 22.5 with four times)
     a.C = 8;
-    while (a.C > 1 && (int64_t)units * a.C > (big ? 2 : 4) * sm_count) a.C /= 2;
+    while (a.C > 1 && (int64_t)units * a.C > (a.gated ? 4 : 2) * sm_count) a.C /= 2;
     a.plan = nullptr;
     if (lora_workspace(a.M, a.adapters) > 0) {
         a.max_tiles = units;

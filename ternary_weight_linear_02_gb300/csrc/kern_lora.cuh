@@ -200,7 +200,7 @@ struct Form {
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
 };
 
-constexpr int kBigSteps = 4;  // steps of 16 ranks whose entries of B a thread of expand_big holds
+constexpr int kBigSteps = 4;  // steps of 16 ranks (the launcher's rule: up to 64) whose entries of B a thread of expand_big holds
 
 // Sizes of a block's shared memory (bytes), the same on the host.
 struct Smem {
@@ -780,63 +780,53 @@ struct ExpandSmall {
     }
 };
 
-// ---- expand, many tokens, where blocks of columns are whole and start on 16 bytes and a thread holds its entries of
-// B for all ranks: they are loaded once for all rows of the tile, pointers move along without products.
-template <typename T, typename O, bool GATED>
+// ---- expand, many tokens, where blocks of 32 columns are whole and start on 16 bytes: a thread holds its entries of
+// B for all ranks, loaded once for all rows of the tile.
+template <typename T, typename O>
 __device__ __forceinline__ void expand_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *hs, const float *up,
-                                             const T *B, int sh, int64_t off, int64_t wide, int64_t blk, int64_t kk, int64_t blocks) {
+                                           const T *B, int sh, int64_t off, int64_t blk, int64_t kk, int64_t blocks) {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, G = 2, Q = kBigSteps;
-    constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;
+    constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, G = 2, Q = kBigSteps, J = 4, W = 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
-    const T *bp = B + (off + blk * (J * 8) + (g >> 1) * W + (g & 1)) * R + 4 * t;
-    const O *yp = static_cast<const O *>(a.y) + off + blk * (J * 8) + t * W;
-    O *op = static_cast<O *>(a.out) + off + blk * (J * 8) + t * W;
-    const T *const h0 = hs + g * sz.hstride + (GATED ? 0 : sh) * steps * 16 + 4 * t;
+    // column of a fragment's n = g, and a thread's own: such that a thread's results are neighbours
+    const T *bp = B + (off + blk * 32 + (g >> 1) * W + (g & 1)) * R + 4 * t;
+    const O *yp = static_cast<const O *>(a.y) + off + blk * 32 + t * W;
+    O *op = static_cast<O *>(a.out) + off + blk * 32 + t * W;
+    const T *const h0 = hs + g * sz.hstride + sh * steps * 16 + 4 * t;
     for (; blk < blocks; blk += kk) {
-        uint2 bv[Q][H][J];
+        uint2 bv[Q][J];
 #pragma unroll
         for (int z = 0; z < Q; ++z)
 #pragma unroll
-            for (int q = 0; q < H; ++q)
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    bv[z][q][j] = make_uint2(0, 0);
-                    if (z * 16 + 4 * t < R) bv[z][q][j] = ldg_nc_v2(bp + q * wide * R + 2 * j * R + z * 16);
-                }
+            for (int j = 0; j < J; ++j) {
+                bv[z][j] = make_uint2(0, 0);
+                if (z * 16 + 4 * t < R) bv[z][j] = ldg_nc_v2(bp + 2 * j * R + z * 16);
+            }
         for (int r0 = 0; r0 < tile.count; r0 += 16 * G) {
-            Raw<O, W> yv[H][2 * G];
+            Raw<O, W> yv[2 * G];
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i)
-                if (r0 + i * 8 + g < tile.count) {
-                    const O *p = yp + tile.toks[r0 + i * 8 + g] * a.ys;
+                if (r0 + i * 8 + g < tile.count) yv[i].load(yp + tile.toks[r0 + i * 8 + g] * a.ys, W, true);
+            float acc[G][J][4];
 #pragma unroll
-                    for (int q = 0; q < H; ++q) yv[q][i].load(p + q * wide, W, true);
-                }
-            float acc[H][G][J][4];
+            for (int i = 0; i < G; ++i)
 #pragma unroll
-            for (int q = 0; q < H; ++q)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < G; ++i)
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[q][i][j][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 #pragma unroll
             for (int z = 0; z < Q; ++z) {
                 if (z >= steps) break;
 #pragma unroll
                 for (int i = 0; i < G; ++i)
 #pragma unroll
-                    for (int q = 0; q < H; ++q)
+                    for (int n = 0; n < NS; ++n) {
+                        const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + z * 16;
+                        const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                        const uint32_t f[4] = {x.x, v.x, x.y, v.y};
 #pragma unroll
-                        for (int n = 0; n < NS; ++n) {
-                            const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + (q * steps + z) * 16;
-                            const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                            const uint32_t f[4] = {x.x, v.x, x.y, v.y};
-#pragma unroll
-                            for (int j = 0; j < J; ++j) mma16816<T>(acc[q][i][j], f, bv[z][q][j].x, bv[z][q][j].y);
-                        }
+                        for (int j = 0; j < J; ++j) mma16816<T>(acc[i][j], f, bv[z][j].x, bv[z][j].y);
+                    }
             }
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i) {
@@ -845,41 +835,30 @@ __device__ __forceinline__ void expand_big(const LoraArgs &a, const Tile<128> &t
                 const float f = kBf ? 1.f : up[row];
                 float v[W];
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    v[j] = __fmaf_rn(acc[0][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[0][i][j]);
-                    if constexpr (GATED) v[j] = silu(v[j]) * __fmaf_rn(acc[1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[1][i][j]);
-                }
+                for (int j = 0; j < W; ++j) v[j] = __fmaf_rn(acc[i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[i][j]);
                 store_out<O, W>(op + tile.toks[row] * a.os, W, true, v);
             }
         }
-        bp += kk * (J * 8) * R;
-        yp += kk * (J * 8);
-        op += kk * (J * 8);
+        bp += kk * 32 * R;
+        yp += kk * 32;
+        op += kk * 32;
     }
 }
 
 // What this warp will expand, requested into the L2 while the sums are joined.  (With few tokens a tile
 // there are more columns than rows, and requests of single lines cost more than they save.)
-template <typename T, typename O, bool GATED>
+template <typename T, typename O>
 __device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<128> &tile, const T *B, int first, int kk) {
-    constexpr int TM = 128, J = GATED ? 2 : 4, H = GATED ? 2 : 1;
-    const int lane = threadIdx.x & 31, shards = GATED ? 1 : a.S;
-    const int lines = (J * 8 * a.R * 2 + 127) / 128;  // of a block's rows of B
+    const int lane = threadIdx.x & 31;
     int64_t skip = first, off = a.col0;
-    for (int sh = 0; sh < shards; ++sh) {
-        const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
+    for (int sh = 0; sh < a.S; ++sh) {
+        const int64_t wide = a.shard[sh], blocks = (wide + 31) / 32;
         int64_t blk = skip;
         for (; blk < blocks; blk += kk) {
-            const int64_t col = off + blk * (J * 8);
-            const int left = (int)min((int64_t)(J * 8), wide - blk * (J * 8));
-            for (int i = lane; i < lines * H && B != nullptr; i += 32) {
-                const int q = i / lines, at = (i - q * lines) * 64;
-                if (at < left * a.R) prefetch_line(B + (q * wide + col) * a.R + at);
-            }
-            for (int i = lane; i < TM * H; i += 32) {
-                const int q = i / TM, row = i - q * TM;
-                if (row < tile.count) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + q * wide + col);
-            }
+            const int64_t col = off + blk * 32;
+            const int bytes = (int)min((int64_t)32, wide - blk * 32) * a.R * 2;
+            for (int i = lane * 128; i < bytes; i += 4096) prefetch_line(reinterpret_cast<const char *>(B + col * a.R) + i);
+            for (int row = lane; row < tile.count; row += 32) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + col);
         }
         skip = blk - blocks;
         off += wide;
@@ -888,7 +867,8 @@ __device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<128> &
 
 // O: type of y and out.
 template <typename T, typename O, bool BIG, bool GATED>
-__global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+    static_assert(!(BIG && GATED), "gated layers keep to tiles of 16");
     using F = Form<BIG>;
     constexpr int TM = F::TM;
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -947,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
         }
     }
     if constexpr (BIG) {
-        if (has) want_expand<T, O, GATED>(a, tile, B, w0, kk);
+        if (has) want_expand<T, O>(a, tile, B, w0, kk);
     } else {
         if (GATED && has && whole) copy_first();
     }
@@ -1044,8 +1024,8 @@ __global__ void __launch_bounds__(kThreads, !BIG && GATED ? 3 : 2) lora_kernel(c
             const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
             bool big = false;
             if constexpr (BIG) {
-                big = has && R <= 16 * kBigSteps && a.vec_y && wide % (J * 8) == 0;
-                if (big) expand_big<T, O, GATED>(a, tile, sz, hs, up, B, sh, off, wide, skip, kk, blocks);
+                big = has && a.vec_y && wide % 32 == 0;
+                if (big) expand_big<T, O>(a, tile, sz, hs, up, B, sh, off, skip, kk, blocks);
             }
             for (int64_t blk = skip; blk < blocks && !big; blk += kk)
                 for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
@@ -1096,10 +1076,7 @@ cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_type(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st) {
-    if (a.gated) {
-        if (f32) return big ? launch_one<T, float, true, true>(a, units, st) : launch_one<T, float, false, true>(a, units, st);
-        return big ? launch_one<T, T, true, true>(a, units, st) : launch_one<T, T, false, true>(a, units, st);
-    }
+    if (a.gated) return f32 ? launch_one<T, float, false, true>(a, units, st) : launch_one<T, T, false, true>(a, units, st);
     if (f32) return big ? launch_one<T, float, true, false>(a, units, st) : launch_one<T, float, false, false>(a, units, st);
     return big ? launch_one<T, T, true, false>(a, units, st) : launch_one<T, T, false, false>(a, units, st);
 }

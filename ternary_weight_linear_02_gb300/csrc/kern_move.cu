@@ -344,10 +344,16 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
 }
 
 template <int PIECES>
-cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
+cudaError_t compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaStream_t st) {
+    // Which form: a warp takes about 1.2 us for 16 moves, more where many warps share the SMs; a block 2.3 us and 6.5 ns a
+    // move, two of them for each unit, two on an SM.  Measured (us, warps / blocks; sequences x layers of 4 heads, moves
+    // of 128 bytes): 1 x 28, 64: 6.8 / 3.7; 4 x 28, 64: 6.8 / 8.4, 128: 11.1 / 8.7; 16 x 28, 64: 8.6 / 29, 256: 34 / 44, 512:
+    // 63 / 62; 64 x 28, 128: 46 / 132; 8 x 4, 128: 11.1 / 3.9.
+    const double units_all = (double)a.batch * m.L * m.Hk, share = units_all / sm_count;
+    const bool blocks = (share > 1 ? share : 1) * (2.3 + 0.0065 * (double)a.n) < (double)((a.n + 15) / 16) * (1.2 + 0.00075 * units_all);
     static std::atomic<uint64_t> done{0};
     constexpr int bytes = sizeof(CompactSmem<PIECES>);
-    if (a.n > 64)
+    if (blocks)
         if (const cudaError_t e = allow_smem(done, compact_block_kernel<PIECES>, bytes)) return e;
     const int64_t per = (int64_t)m.L * m.Hk;
     // sequences of a launch, such that blocks are counted in 31 bits
@@ -360,7 +366,7 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
         c.start += b0;
         c.count += b0;
         const int64_t units = c.batch * per;
-        if (a.n <= 64) compact_warp_kernel<PIECES><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(m, c, units);
+        if (!blocks) compact_warp_kernel<PIECES><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(m, c, units);
         else compact_block_kernel<PIECES><<<(unsigned)(units * 2), kMovers, bytes, st>>>(m, c);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -397,8 +403,10 @@ cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *list
     return cudaLaunchKernelEx(&c, fork_apply_kernel, m, g, listed, items, (uint32_t)runs);
 }
 
-cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st) {
-    return m.rb == 128 ? compact<8>(m, a, st) : m.rb == 64 ? compact<4>(m, a, st) : compact<2>(m, a, st);
+cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaStream_t st) {
+    return m.rb == 128  ? compact<8>(m, a, sm_count, st)
+           : m.rb == 64 ? compact<4>(m, a, sm_count, st)
+                        : compact<2>(m, a, sm_count, st);
 }
 
 }  // namespace tl

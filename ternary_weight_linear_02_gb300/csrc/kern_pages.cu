@@ -124,8 +124,7 @@ __device__ __forceinline__ uint32_t free_words(const int *refs, int64_t p0, int6
 //   the free page of rank k goes to the row whose sum passes k, as far as whole rows are covered;
 //   lengths, slots and answers.
 // Bound by latency: three dependent loads, the cluster's two barriers, the table's new entries read back for the
-// slots.  A pool that 256 threads look through at once (8192 pages) has no more: 1024 cost their barriers
-// (16 rows: 8.8 us with the freeing before, 12.9 with 1024).  1021 rows over 200 thousand pages: 13 us, of which
+// slots.  1021 rows over 200 thousand pages: 13 us, of which
 // counting 4, needs 2, the exchange 1.4, giving out 3.3, slots 1.7.  Each lane giving out the pages that it found
 // took 38 us: free pages lie together, so one warp had most of them.
 template <bool FORK>
@@ -290,7 +289,9 @@ cudaError_t launch_pages_take(const PagesTakeArgs &a, bool fork, cudaStream_t st
     // a block's run of pages is looked through once and kept as bits: up to 32768 of them
     int C = 1;
     while (C < 8 && (int64_t)C * 32768 < a.g.pages) C *= 2;
-    const int threads = a.g.pages <= 8192 && a.g.rows <= 1024 ? 256 : 1024, bytes = a.g.rows * 12;
+    // 256 threads for a small server: 16 rows of 1100 pages 9.2 us against 12.5 with 1024, 250 rows 14.1 and 14.4, 1000 rows
+    // 30 and 18.6 (freeing before included)
+    const int threads = a.g.pages <= 8192 && a.g.rows <= 256 ? 256 : 1024, bytes = a.g.rows * 12;
     static std::atomic<uint64_t> done[2];
     const auto kernel = fork ? pages_take_kernel<true> : pages_take_kernel<false>;
     if (bytes > 32 * 1024)

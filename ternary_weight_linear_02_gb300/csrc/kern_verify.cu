@@ -22,7 +22,7 @@ namespace tl {
 
 namespace {
 
-constexpr int kMaxBlocks = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxBlocks = 8;
 
 struct Pair {
     float hi, lo;
@@ -247,9 +247,8 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 // ten rejections, one pass each).
 // fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
 // warp takes the SM's unit 16 cycles.
-template <typename T, bool VEC, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(VerifyArgs a) {
-    constexpr int kWarps = kThreads / 32;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
     __shared__ float px[kMaxDraft], qx[kMaxDraft], un[kMaxDraft + 1];
     __shared__ int tok[kMaxDraft], par[kMaxDraft], path[kMaxDraft], gone[kMaxDraft];
     __shared__ Pair warp_sum[kWarps], part[kWarps], block_sum[2][kMaxBlocks];
@@ -549,23 +548,24 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
     a.out[b * (n + 1) + count] = token;
 }
 
-template <typename T, bool VEC, int THREADS>
-cudaError_t launch_one(const VerifyArgs &a, cudaStream_t st) {
-    // rows kept by the threads: only a tree looks at a node's rows more than once.  Up to 80 KB, so that two blocks
-    // of 512 threads share an SM
-    constexpr int kMost = 80 * 1024, WARPS = THREADS / 32;
-    const int64_t per = (((a.V + (int64_t)a.blocks - 1) / a.blocks) + 255) & ~(int64_t)255, run = (((per + WARPS - 1) / WARPS) + 7) & ~(int64_t)7;
-    const int64_t slots = VEC ? 2 * ((run + 32 * (16 / (int)sizeof(T)) - 1) / (32 * (16 / (int)sizeof(T)))) : (run + 8 * 32 - 1) / (8 * 32) * 4;
+template <typename T, bool VEC>
+cudaError_t launch_one(const VerifyArgs &a, int sm_count, cudaStream_t st) {
+    // Rows kept by the threads: only a tree looks at a node's rows more than once (24 trees of 31 over 50021 tokens 41.7 us,
+    // 58.6 without), and only where the batch fits the SMs beside them.
+    constexpr int kMost = 96 * 1024, kFixed = 31 * 1024, kSm = 227 * 1024;
+    const int64_t per = (((a.V + (int64_t)a.blocks - 1) / a.blocks) + 255) & ~(int64_t)255, run = (((per + kWarps - 1) / kWarps) + 7) & ~(int64_t)7;
+    constexpr int STEP = VEC ? 32 * (16 / (int)sizeof(T)) : 8 * 32;
+    const int64_t bytes = (run + STEP - 1) / STEP * (VEC ? 2 : 4) * kThreads * 16;
     VerifyArgs b = a;
-    b.keep = a.parent && a.draft && THREADS == 512 && slots * THREADS * 16 <= kMost;
-    const auto kernel = verify_kernel<T, VEC, THREADS>;
+    b.keep = a.parent && a.draft && bytes <= kMost && a.B * a.blocks <= kSm / (kFixed + bytes) * sm_count;
+    const auto kernel = verify_kernel<T, VEC>;
     static std::atomic<uint64_t> done{0};
     if (b.keep)
         if (const cudaError_t e = allow_smem(done, kernel, kMost)) return e;
     cudaLaunchConfig_t c{};
-    c.dynamicSmemBytes = b.keep ? (size_t)(slots * THREADS * 16) : 0;
     c.gridDim = dim3((unsigned)(a.B * a.blocks));
-    c.blockDim = dim3(THREADS);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = b.keep ? (size_t)bytes : 0;
     c.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -578,18 +578,14 @@ cudaError_t launch_one(const VerifyArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_t(const VerifyArgs &a, bool vec, int sm_count, cudaStream_t st) {
-    // 512 threads a block where two such on each SM hold the batch: a pass is then the shorter; many
-    // sequences share the SMs better in blocks of 256
-    const bool wide = a.B * a.blocks <= 2 * sm_count;
-    if (vec) return wide ? launch_one<T, true, 512>(a, st) : launch_one<T, true, 256>(a, st);
-    return wide ? launch_one<T, false, 512>(a, st) : launch_one<T, false, 256>(a, st);
+    return vec ? launch_one<T, true>(a, sm_count, st) : launch_one<T, false>(a, sm_count, st);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &args, int dtype, bool vec, int sm_count, cudaStream_t st) {
     VerifyArgs a = args;
-    a.blocks = 1;
+    a.blocks = 1;  // (256 threads each: 512 took 10.4 us for a chain where 256 take 9.6, and 24 for 38 long ones where 256 take 18)
     while (a.blocks < kMaxBlocks && a.V > 4096 * a.blocks) a.blocks *= 2;
     return dtype == 0   ? launch_t<__half>(a, vec, sm_count, st)
            : dtype == 1 ? launch_t<__nv_bfloat16>(a, vec, sm_count, st)

@@ -331,7 +331,7 @@ struct KvCompactArgs {
     int64_t keep_stride;
     int64_t batch, n;
 };
-cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, cudaStream_t st);
+cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaStream_t st);
 
 // ------------------------------------------------------------ verification of drafted tokens
 constexpr int kMaxDraft = 1024;  // drafted tokens of a sequence: what is looked up of them lies in shared memory

@@ -81,7 +81,8 @@ CASES = [  # tokens, inputs, shards, rank, adapters
     (1, 64, (32,), 8, 1), (1, 3584, (3584, 512, 512), 16, 3), (16, 1024, (1024,), 16, 8), (7, 200, (40, 8, 24), 24, 2),
     (33, 1000, (72, 56), 32, 5), (64, 4096, (256,), 64, 64), (100, 264, (96,), 128, 3), (257, 512, (320,), 16, 2),
     (300, 2048, (128, 64), 64, 4), (1024, 256, (64,), 8, 700), (1025, 256, (64,), 8, 3), (3001, 320, (104,), 16, 40),
-    (2000, 96, (32,) * 8, 128, 7), (700, 136, (24, 8) * 4, 24, 5), (500, 4096, (48, 16, 16), 64, 2), (129, 8, (40,), 16, 1), (90, 72, (16,), 8, 2000), (1, 8, (8,), 8, 1)]
+    (2000, 96, (32,) * 8, 128, 7), (2048, 9000, (256, 96, 100), 64, 3), (2100, 9000, (3500,), 32, 2),
+    (1500, 15000, (64,) * 5, 24, 4), (700, 136, (24, 8) * 4, 24, 5), (500, 4096, (48, 16, 16), 64, 2), (129, 8, (40,), 16, 1), (90, 72, (16,), 8, 2000), (1, 8, (8,), 8, 1)]
 
 
 @pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torch.bfloat16, torch.float32),
@@ -101,7 +102,7 @@ def test_add(tokens, inputs, shards, rank, n, dtype, out_dtype):
 
 @pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torch.bfloat16, torch.float32)])
 @pytest.mark.parametrize("tokens,inputs,half,rank,n", [(1, 512, 1024, 16, 1), (16, 3584, 2000, 8, 9), (50, 136, 24, 32, 3), (300, 256, 96, 16, 4),
-                                                       (1500, 128, 40, 64, 5), (77, 100, 33, 16, 2)])
+                                                       (1500, 128, 40, 64, 5), (77, 100, 33, 16, 2), (60, 256, 64, 32, 2)])
 def test_silu_mul(tokens, inputs, half, rank, n, dtype, out_dtype):
     x, y, a, b, s, which = make(tokens, inputs, (half, half), rank, n, dtype, out_dtype, seed=half)
     got = tl.lora_silu_mul(x, tl.Adapters(a, b, s, shards=(half, half)), which, y)
@@ -135,10 +136,10 @@ def test_strides():
     assert tl.lora_add(x[:0], ad, which[:0], y[:0]).shape == (0, 96)
 
 
-@pytest.mark.parametrize("tokens,n", [(40, 3), (900, 4), (5000, 3)])
-def test_runs_and_orders(tokens, n):
+@pytest.mark.parametrize("tokens,inputs,n", [(40, 512, 3), (900, 512, 4), (5000, 512, 3), (4100, 14000, 3)])
+def test_runs_and_orders(tokens, inputs, n):
     """A token's result does not hang on where it stands or on what else is in the batch with tiles of one size."""
-    x, y, a, b, s, _ = make(tokens, 512, (96,), 16, n, torch.bfloat16, torch.bfloat16, seed=tokens)
+    x, y, a, b, s, _ = make(tokens, inputs, (96,), 16, n, torch.bfloat16, torch.bfloat16, seed=tokens)
     gen = torch.Generator(device=DEV).manual_seed(1)
     cuts = torch.randint(0, tokens, (n,), generator=gen, device=DEV).sort().values
     which = torch.searchsorted(cuts, torch.arange(tokens, device=DEV), right=True).int() - 1
@@ -199,9 +200,9 @@ def test_adapters_out_of_range(tokens):
     assert torch.equal(got[inside < 0], y[inside < 0])
 
 
-@pytest.mark.parametrize("tokens", [16, 1500])
-def test_replayed_with_other_adapters(tokens):
-    x, y, a, b, s, which = make(tokens, 256, (96,), 16, 6, torch.bfloat16, torch.bfloat16, seed=5)
+@pytest.mark.parametrize("tokens,inputs", [(16, 256), (1500, 256), (2000, 30000)])
+def test_replayed_with_other_adapters(tokens, inputs):
+    x, y, a, b, s, which = make(tokens, inputs, (96,), 16, 6, torch.bfloat16, torch.bfloat16, seed=5)
     ad = tl.Adapters(a, b, s)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -240,7 +240,7 @@ def test_copy_refuses_pages_and_counts():
 
 
 @pytest.mark.parametrize("fmt,heads,dim", [("int8", 2, 128), ("fp8", 1, 64), ("int4", 3, 128), ("int4", 1, 64)])
-@pytest.mark.parametrize("batch,n,page,layers", [(1, 1, 16, 1), (5, 17, 16, 3), (33, 64, 64, 2), (3, 65, 48, 1), (4, 1000, 32, 2), (2, 5000, 64, 1)])
+@pytest.mark.parametrize("batch,n,page,layers", [(40, 130, 32, 24), (1, 1, 16, 1), (5, 17, 16, 3), (33, 64, 64, 2), (3, 65, 48, 1), (4, 1000, 32, 2), (2, 5000, 64, 1)])
 def test_compact(fmt, heads, dim, batch, n, page, layers):
     """Paths of drafted trees (n up to 64) and contexts of which a part is kept, in place."""
     rng = random.Random(batch * n + dim)
