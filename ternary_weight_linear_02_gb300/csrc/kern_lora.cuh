@@ -169,8 +169,12 @@ __device__ __forceinline__ float4 cl_ld_v4(uint32_t addr) {
     return v;
 }
 
-// (the quotient within 2 ulp; 0 instead of less than 2^-119 below g = -87)
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+// The quotient is within 2 ulp (0 instead of less than 2^-119 below g = -87).  The exponential for a 16-bit output is the
+// short one, within 2 + 1.2 |g| ulp: 2^-16 of the result, where its rounding takes 2^-9 or 2^-12.
+template <typename O>
+__device__ __forceinline__ float silu(float g) {
+    return __fdividef(g, 1.f + (sizeof(O) == 4 ? expf(-g) : __expf(-g)));
+}
 
 // 16 bytes from global to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
@@ -616,7 +620,7 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
             if constexpr (GATED) {
                 float w = yv[1][i][j];
                 if (has) w = __fmaf_rn(acc[1][i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, w);
-                v[j] = silu(v[j]) * w;
+                v[j] = silu<O>(v[j]) * w;
             }
         }
         store_out<O, W>(out + tile.toks[row] * a.os + col + t * W, n, a.vec_y, v);
@@ -768,7 +772,7 @@ struct ExpandSmall {
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
                         o[j] = __fmaf_rn(acc[n8][0][j >> 1][2 * (j & 1) + e], f, yv[0][j]);
-                        if constexpr (GATED) o[j] = silu(o[j]) * __fmaf_rn(acc[n8][1][j >> 1][2 * (j & 1) + e], f, yv[1][j]);
+                        if constexpr (GATED) o[j] = silu<O>(o[j]) * __fmaf_rn(acc[n8][1][j >> 1][2 * (j & 1) + e], f, yv[1][j]);
                     }
                     store_out<O, W>(static_cast<O *>(a.out) + tile.toks[row] * a.os + col + g * W, W, true, o);
                 }
