@@ -319,9 +319,10 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
     look(2 * ROWS);
     fetch(3 * ROWS);
     int stage = 0;
-    for (int i0 = 0; i0 < end; i0 += ROWS) {
+    for (int i0 = 0;; i0 += ROWS) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();  // the group is read by all, and its last good move is known
+        __syncthreads();  // the group is read by all, and its last good move is known:
+        if (i0 >= end) break;  // only later groups lower `end` from here on, so all leave the loop together
         found();
         request(stage == 0 ? 2 : stage - 1);
         look(i0 + 3 * ROWS);
