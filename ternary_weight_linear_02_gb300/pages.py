@@ -75,6 +75,8 @@ class KVPages:
     __slots__ = ("page_size", "refs", "table", "lens", "held", "pages", "rows", "max_pages", "device", "_c", "_ref")
 
     def __init__(self, page_size: int, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, held: torch.Tensor):
+        if not 16 <= page_size <= 1 << 20 or page_size % 16:
+            raise ValueError("page_size must be a multiple of 16, up to 2^20")
         for t, n in ((refs, 1), (table, 2), (lens, 1), (held, 1)):
             if t.dtype is not torch.int32 or t.dim() != n or t.stride(-1) != 1 and t.shape[-1] > 1:
                 raise ValueError("refs [pages], table [rows, max_pages], lens [rows] and held [rows] must be int32, dense")
@@ -85,8 +87,6 @@ class KVPages:
         self.rows, self.max_pages = table.shape
         if lens.shape[0] != self.rows or held.shape[0] != self.rows:
             raise ValueError("lens and held must have one element for each row of the table")
-        if page_size < 16 or page_size % 16:
-            raise ValueError("page_size must be a multiple of 16")
         stride = table.stride(0) if self.rows > 1 else max(table.stride(0), self.max_pages)
         if stride < self.max_pages:
             raise ValueError("rows of the table must not overlap")
@@ -146,8 +146,8 @@ def pages_reserve(pages: KVPages, extra: torch.Tensor, width: int) -> tuple[torc
     int64 [rows, width], ok bool [rows]): the slots of the row's next min(extra, width) tokens, as kv_append takes
     them, -1 behind them and where ok is False (no page was left).  lens stays: pages_free moves it on
     when the tokens are there."""
-    if width < 0:
-        raise ValueError("width must not be negative")
+    if not 0 <= width < 1 << 31:
+        raise ValueError("width must be 0 or more, in 32 bits")
     dev = pages.device
     extra = _index(extra, "extra", torch.int32, pages.rows, dev)
     slots = torch.empty((pages.rows, int(width)), dtype=torch.int64, device=dev)

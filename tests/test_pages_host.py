@@ -116,3 +116,18 @@ def test_binding_refuses():
         tl.KVLayers([])
     with pytest.raises(ValueError, match="KVCache"):
         tl.KVLayers([i])
+
+
+class _FakePages:
+    device, rows = torch.device("cpu"), 3
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    """Sizes are passed in 32 bits: what does not fit is refused, not cut off."""
+    i, table = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int32)
+    for size in (8, 24, (1 << 20) + 16, (1 << 32) + 16):
+        with pytest.raises(ValueError, match="page_size"):
+            tl.KVPages(size, i, table, i, i)
+    for width in (-1, 1 << 31, (1 << 32) + 1):
+        with pytest.raises(ValueError, match="width"):
+            tl.pages_reserve(_FakePages(), i, width)
