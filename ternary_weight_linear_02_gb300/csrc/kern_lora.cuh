@@ -169,11 +169,20 @@ __device__ __forceinline__ float4 cl_ld_v4(uint32_t addr) {
     return v;
 }
 
-// The quotient is within 2 ulp (0 instead of less than 2^-119 below g = -87).  The exponential for a 16-bit output is the
-// short one, within 2 + 1.2 |g| ulp: 2^-16 of the result, where its rounding takes 2^-9 or 2^-12.
+// For fp32 outputs the quotient is within 2 ulp (0 instead of less than 2^-119 below g = -87).  For 16-bit outputs the
+// special functions' own instructions, 2^x within 2 ulp and 1/x within 1, without the scaling that the functions
+// put around them for subnormal numbers (a third of the instructions): with the rounding of g log2(e), within 5 + 1.2
+// |g| ulp, 2^-16 of the result, where its rounding takes 2^-9 or 2^-12; 0 instead of less than 2^-119 here too.
 template <typename O>
 __device__ __forceinline__ float silu(float g) {
-    return __fdividef(g, 1.f + (sizeof(O) == 4 ? expf(-g) : __expf(-g)));
+    if constexpr (sizeof(O) == 4) {
+        return __fdividef(g, 1.f + expf(-g));
+    } else {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return g * r;
+    }
 }
 
 // 16 bytes from global to shared memory, or zeros.
