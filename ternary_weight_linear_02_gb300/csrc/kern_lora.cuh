@@ -651,8 +651,11 @@ struct Blocks {
     // place of byte `at` of a half's rows of B that belongs to the columns of threads g: 32-byte granules of 4 threads'
     // columns exchange places, which leaves no bank conflicts
     __device__ static uint32_t b_place(int at, int g) { return (uint32_t)(at ^ ((g & 3) << 5)); }
-    // place of 16-byte piece c of token row r
-    __device__ static uint32_t y_piece(int r, int c) { return (uint32_t)(r * YROW + ((c ^ (((r >> 1) & 3) << (GATED ? 0 : 1))) << 4)); }
+    // place of 16-byte piece c of token row r (rows of 64 bytes: two of them span the banks)
+    __device__ static uint32_t y_piece(int r, int c) { return (uint32_t)(r * YROW + ((c ^ ((r & 3) << (YROW == 64 ? 0 : 1))) << 4)); }
+    // place of token row r in the split h: a thread's two tokens are t and t + 4 of a group of 8, so that groups of up to
+    // 4 tokens take half the work
+    __device__ static int h_row(int r) { return (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1); }
 };
 
 template <typename T, typename O, bool GATED>
@@ -758,7 +761,7 @@ struct ExpandSmall {
                 if (n8 == 1 && !two) break;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = n8 * 8 + 2 * t + e;
+                    const int row = n8 * 8 + t + 4 * e;
                     if (row >= tile.count) continue;
                     const float f = kBf ? 1.f : up[row];
                     Raw<O, W> yv[H];
@@ -1005,6 +1008,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
                 const int i = i0 + u * kThreads, row = i / row_quads, e = i - row * row_quads;
                 if (row >= tile.count) continue;
                 const float f = kBf ? 1.f : 1.f / up[row];  // (a power of two)
+                const int place = whole ? L::h_row(row) : row;
                 float z[4] = {v[u].x * s * f, v[u].y * s * f, v[u].z * s * f, v[u].w * s * f};
 #pragma unroll
                 for (int n = 0; n < NS; ++n) {
@@ -1014,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
                         h[j] = of_f<T>(z[j]);
                         z[j] = isfinite(to_f(h[j])) ? z[j] - to_f(h[j]) : 0.f;
                     }
-                    *reinterpret_cast<uint2 *>(hs + (n * TM + row) * sz.hstride + e * 4) = *reinterpret_cast<const uint2 *>(h);
+                    *reinterpret_cast<uint2 *>(hs + (n * TM + place) * sz.hstride + e * 4) = *reinterpret_cast<const uint2 *>(h);
                 }
             }
         }
