@@ -142,10 +142,15 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
     const bool big = big_tiles(a);
     const int TM = big ? 128 : 16;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
-    // blocks a tile: as many as the SMs hold twice over (gated, where three fit and expanding is most of the work, four
-    // times: 333 x 40 45 us against 66; plain 1024 x 8 15.6 us against 22.5 with four times)
-    a.C = 8;
-    while (a.C > 1 && (int64_t)units * a.C > (a.gated ? 4 : 2) * sm_count) a.C /= 2;
+    // Blocks a tile: 8, 6, 4, 2 or 1, as many as make two blocks an SM (gated, where three fit: 2.7) of the tiles that tokens
+    // spread evenly over the adapters would give.  (Of all that there could be, a third more, blocks would be too
+    // few.)  Measured (us, C = 2, 4, 6, 8; tokens x adapters, rank 16, 3584 columns in): gated 2 x 18944, 333 x 40: 86 / 53 / 42 / 41;
+    // 512 x 64: 82 / 56 / 52 / 62; 1024 x 4: 97 / 61 / 57 / 69; 1000 x 200: 119 / 114 / 118 / 124; plain 18944, 333 x 40: 40 / 28 /
+    // 24 / 33; 3584, 64 x 64: 15 / 12 / 13 / 16; 1024 x 8: 19 / 16 / 26 / 23; 1024 x 100: 22 / 27 / 37 / 37; tiles of 128, rank 32, 8192 x
+    // 16: 79 / 69 / 81 / 80; rank 64, 18944 to 3584, 8192 x 6: 157 / 132 / 164 / 156.  7 is worse than 6 and 8 throughout.
+    const double present = (double)(a.adapters + 1 < a.M ? a.adapters + 1 : a.M), even = (double)a.M / TM + present / 2;
+    const double most = (a.gated ? 2.7 : 2.0) * sm_count / (even > present ? even : present);
+    a.C = most >= 8 ? 8 : most >= 6 ? 6 : most >= 4 ? 4 : most >= 2 ? 2 : 1;
     a.plan = nullptr;
     if (lora_workspace(a.M, a.adapters) > 0) {
         a.max_tiles = units;

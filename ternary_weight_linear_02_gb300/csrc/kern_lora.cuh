@@ -16,7 +16,7 @@
 //     stages (16-byte copies, whatever the tokens' order) into tcgen05 MMAs, h lies in tensor memory.
 // Either way there are 0.7 R operations a byte: memory should bound it.  Measured: 16 tokens of 8 adapters, rank 16,
 // fused QKV of 3584: 9.6 us (finding the tile 0.9, shrink 2.8, sums 1.6, expand 1.7); 333 tokens of 40 adapters,
-// rank 16, gated layer of 2 x 18944: 43 us, 98 MB, 14.4 at a copy's rate: bound by instructions (57 % of
+// rank 16, gated layer of 2 x 18944: 41 us, 98 MB, 14.4 at a copy's rate: bound by instructions (57 % of
 // the issue slots), the gated product's before all; 8192 tokens of 6 adapters, rank 64, 18944 to 3584, f16: 132 us,
 // 445 MB, 65.6 at a copy's rate: the plan 6, shrink 53 (5.9 TB/s), sums 10, expand 27 to 45, where warp
 // MMAs (12 thousand an SM, 2.9 cycles each) take 18.
