@@ -64,6 +64,22 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uin
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// the same with nothing to add to
+template <typename T>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816_first<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+template <>
+__device__ __forceinline__ void mma16816_first<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
 template <>
@@ -646,7 +662,7 @@ struct Blocks {
     static constexpr int COLS = 8 * W;                          // columns of a block (gated: of either half)
     static constexpr int YROW = COLS * sizeof(O);               // bytes of a token's columns
     static constexpr int YBYTES = 16 * H * YROW;
-    __host__ __device__ static int stage(int R) { return H * COLS * R * 2 + YBYTES; }
+    __host__ __device__ static constexpr int stage(int R) { return H * COLS * R * 2 + YBYTES; }
     __host__ __device__ static bool ranks(int R) { return R == 8 || R == 16 || R == 32; }
     // place of byte `at` of a half's rows of B that belongs to the columns of threads g: 32-byte granules of 4 threads'
     // columns exchange places, which leaves no bank conflicts
@@ -658,124 +674,138 @@ struct Blocks {
     __device__ static int h_row(int r) { return (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1); }
 };
 
-template <typename T, typename O, bool GATED>
+// What a thread reads and writes lies at places that it works out once (R is a template's for that): a block of columns took
+// three times the instructions with places worked out anew.
+template <typename T, typename O, bool GATED, int R>
 struct ExpandSmall {
     using L = Blocks<O, GATED>;
-    static constexpr int W = L::W, H = L::H, I = W / 2;
+    static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2, STEPS = (R + 15) / 16;
+    static constexpr int W = L::W, H = L::H, I = W / 2, STAGE = L::stage(R);
+    static constexpr int BHALF = L::COLS * R * 2, YHALF = 16 * L::YROW;      // bytes of a half's B and y in a stage
+    static constexpr int BI = BHALF / 512, C = L::YROW / 16, YI = 16 * C / 32, YSTEP = 32 / C;  // copies of a lane; pieces and rows
+    static constexpr int SHIFT = W * R == 32 ? 2 : W * R == 64 ? 3 : W * R == 128 ? 4 : 5;  // log2 of the pieces of a thread's columns
+    static constexpr int YX = L::YROW == 64 ? 0 : 1;
     const LoraArgs &a;
-    const Tile<16> &tile;
-    const T *const B;
-    const uint32_t base;  // shared memory of this warp
-    const int first, kk, lane;
+    const T *bp;       // the lane's first piece of block 0's B
+    const O *yp[YI];   // and of its rows of y
+    uint32_t base, bto, yto;
+    int first, kk, total, count, lane;
 
-    // block n: its shard and first column; false: there is none
-    __device__ __forceinline__ bool block(int64_t n, int &sh, int64_t &col) const {
-        col = a.col0;
-        for (sh = 0; sh < (GATED ? 1 : a.S); ++sh) {
-            const int64_t blocks = a.shard[sh] / L::COLS;
-            if (n < blocks) {
-                col += n * L::COLS;
-                return true;
-            }
-            n -= blocks;
-            col += a.shard[sh];
+    __device__ __forceinline__ ExpandSmall(const LoraArgs &args, const Tile<16> &tile, const T *B, uint32_t base_, int first_, int kk_)
+        : a(args), base(base_), first(first_), kk(kk_), count(tile.count), lane(threadIdx.x & 31) {
+        // (shards are whole blocks: block n has columns n COLS on, whatever shard they are in)
+        total = (int)((GATED ? a.shard[0] : launch_columns()) / L::COLS);
+        bp = B + a.col0 * R + lane * 8;
+        bto = (uint32_t)(lane * 16 ^ ((lane >> SHIFT & 3) << 5));
+        yto = H * BHALF + L::y_piece(lane / C, lane % C);
+#pragma unroll
+        for (int i = 0; i < YI; ++i) {
+            const int r = i * YSTEP + lane / C;
+            yp[i] = static_cast<const O *>(a.y) + (int64_t)tile.toks[r < count ? r : 0] * a.ys + a.col0 + lane % C * (16 / (int)sizeof(O));
         }
-        return false;
     }
-    __device__ __forceinline__ void copy(int stage, int64_t n) const {
-        int sh;
-        int64_t col;
-        if (block(n, sh, col)) {
-            const uint32_t to = base + stage * L::stage(a.R), yt = to + H * L::COLS * a.R * 2;
-            const int64_t wide = a.shard[0];
-            const int pieces = L::COLS * a.R / 8, shift = 28 - __clz(W * a.R);  // log2 of the pieces of a thread's columns
+    __device__ __forceinline__ int64_t launch_columns() const {
+        int64_t n = 0;
+        for (int i = 0; i < a.S; ++i) n += a.shard[i];
+        return n;
+    }
+    __device__ __forceinline__ void copy(int stage, int n) const {
+        if (n < total) {
+            const uint32_t to = base + stage * STAGE;
+            const T *b = bp + (int64_t)n * (L::COLS * R);
 #pragma unroll
             for (int q = 0; q < H; ++q) {
-                const T *b = B + (q * wide + col) * a.R;
-                for (int p = lane; p < pieces; p += 32) copy16(to + q * pieces * 16 + L::b_place(p * 16, p >> shift), b + p * 8, true);
-                constexpr int C = L::YROW / 16;  // pieces of a token
 #pragma unroll
-                for (int p = 0; p < 16 * C; p += 32) {
-                    const int r = (p + lane) / C, c = (p + lane) % C;
-                    if (r < tile.count)
-                        copy16(yt + q * 16 * L::YROW + L::y_piece(r, c),
-                               static_cast<const O *>(a.y) + tile.toks[r] * a.ys + q * wide + col + c * (16 / (int)sizeof(O)), true);
-                }
+                for (int i = 0; i < BI; ++i)
+                    copy16(to + q * BHALF + i * 512 + (bto ^ ((((i << (5 - SHIFT)) & 3) << 5))), b + i * 256, true);
+                b += a.shard[0] * R;
             }
+#pragma unroll
+            for (int i = 0; i < YI; ++i)
+                if (i * YSTEP + lane / C < count) {
+                    const O *y = yp[i] + (int64_t)n * L::COLS;
+#pragma unroll
+                    for (int q = 0; q < H; ++q) {
+                        copy16(to + q * YHALF + i * YSTEP * L::YROW + (yto ^ ((i * YSTEP & 3) << YX << 4)), y, true);
+                        y += a.shard[0];
+                    }
+                }
         }
         copies_commit();
     }
     __device__ __forceinline__ void copy_first() const {
         copy(0, first);
-        copy(1, (int64_t)first + kk);
+        copy(1, first + kk);
     }
-    __device__ __forceinline__ void run(const Smem &sz, const T *hs, const float *up) const {
-        constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-        constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
-        const int g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
-        const bool two = tile.count > 8;  // the second group of 8 tokens has some
-        int sh;
-        int64_t col, now = first;
-        for (int i = 0; block(now, sh, col); ++i, now += kk) {
+    // rows: where the tile's tokens are in out
+    __device__ __forceinline__ void run(const Smem &sz, const T *hs, const float *up, char *const *rows) const {
+        const int g = lane >> 2, t = lane & 3;
+        const bool two = count > 8;  // the second group of 8 tokens has some
+        const T *h0 = hs + g * sz.hstride + 4 * t;
+        // the rows of B of a thread's columns: the bits that are exchanged (5 and 6) in four registers, the others are added
+        uint32_t bx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bx[j] = base + (uint32_t)((g * W * R * 2 + 8 * t) ^ (((g & 3) ^ j) << 5));
+        // (a row of 16 bytes has two loads of 8: threads t < 2)
+        const uint32_t y0 = base + H * BHALF + t * L::YROW +
+                            (W * sizeof(O) == 8 ? (((g >> 1) ^ (t << YX)) << 4) + (g & 1) * 8 : ((g * (W * (int)sizeof(O) / 16)) ^ (t << YX)) << 4);
+        const uint32_t at = (uint32_t)(a.col0 + g * W);
+        int sh = 0, end = GATED ? total : (int)(a.shard[0] / L::COLS);
+        int stage = 0;
+        for (int now = first; now < total; now += kk) {
             copies_wait<1>();
             __syncwarp();
-            const uint32_t bs = base + (i & 1) * L::stage(R), ys = bs + H * L::COLS * R * 2;
-            float acc[2][H][I][4];
-#pragma unroll
-            for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-                for (int q = 0; q < H; ++q)
-#pragma unroll
-                    for (int m = 0; m < I; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[n8][q][m][e] = 0.f;
-            for (int z = 0; z < steps; ++z) {
-#pragma unroll
-                for (int q = 0; q < H; ++q) {
-                    uint2 h[2][NS];
-#pragma unroll
-                    for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-                        for (int n = 0; n < NS; ++n)
-                            h[n8][n] = *reinterpret_cast<const uint2 *>(hs + (n * 16 + n8 * 8 + g) * sz.hstride +
-                                                                        ((GATED ? q : sh) * steps + z) * 16 + 4 * t);
-#pragma unroll
-                    for (int m = 0; m < I; ++m) {
-                        uint2 x = make_uint2(0, 0), v = make_uint2(0, 0);
-                        if (z * 16 + 4 * t < R) {
-                            const int at = ((g * W + 2 * m) * R + z * 16 + 4 * t) * 2, at2 = at + R * 2;  // bytes of two columns
-                            x = lds8(bs + q * L::COLS * R * 2 + L::b_place(at, g));
-                            v = lds8(bs + q * L::COLS * R * 2 + L::b_place(at2, g));
-                        }
-                        const uint32_t f[4] = {x.x, v.x, x.y, v.y};
-#pragma unroll
-                        for (int n = 0; n < NS; ++n) {
-                            mma16816<T>(acc[0][q][m], f, h[0][n].x, h[0][n].y);
-                            if (two) mma16816<T>(acc[1][q][m], f, h[1][n].x, h[1][n].y);
-                        }
-                    }
+            if constexpr (!GATED) {
+                while (now >= end) {
+                    ++sh;
+                    end += (int)(a.shard[sh] / L::COLS);
+                    h0 += STEPS * 16;
                 }
             }
+            const uint32_t off = (uint32_t)(stage * STAGE);
 #pragma unroll
             for (int n8 = 0; n8 < 2; ++n8) {
                 if (n8 == 1 && !two) break;
+                float acc[H][I][4];
+#pragma unroll
+                for (int z = 0; z < STEPS; ++z)
+#pragma unroll
+                    for (int q = 0; q < H; ++q) {
+                        uint2 h[NS];
+#pragma unroll
+                        for (int n = 0; n < NS; ++n)
+                            h[n] = *reinterpret_cast<const uint2 *>(h0 + (n * 16 + n8 * 8) * sz.hstride + (q * STEPS + z) * 16);
+#pragma unroll
+                        for (int m = 0; m < I; ++m) {
+                            uint2 x = make_uint2(0, 0), v = make_uint2(0, 0);
+                            const int c0 = 2 * m * R * 2 + z * 32, c1 = c0 + R * 2;  // (fields of bits apart from g's and t's)
+                            if (R >= 16 || t < 2) {
+                                x = lds8(bx[c0 >> 5 & 3] + off + q * BHALF + (c0 & ~96));
+                                v = lds8(bx[c1 >> 5 & 3] + off + q * BHALF + (c1 & ~96));
+                            }
+                            const uint32_t f[4] = {x.x, v.x, x.y, v.y};
+                            if (z == 0) mma16816_first<T>(acc[q][m], f, h[0].x, h[0].y);
+#pragma unroll
+                            for (int n = z == 0 ? 1 : 0; n < NS; ++n) mma16816<T>(acc[q][m], f, h[n].x, h[n].y);
+                        }
+                    }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = n8 * 8 + t + 4 * e;
-                    if (row >= tile.count) continue;
+                    if (row >= count) continue;
                     const float f = kBf ? 1.f : up[row];
                     Raw<O, W> yv[H];
 #pragma unroll
                     for (int q = 0; q < H; ++q) {
-                        const uint32_t yr = ys + q * 16 * L::YROW;
+                        const uint32_t yr = y0 + off + q * YHALF + (n8 * 8 + 4 * e) * L::YROW;
                         if constexpr (Raw<O, W>::WORDS == 2) {
-                            const uint2 r = lds8(yr + L::y_piece(row, g >> 1) + (g & 1) * 8);
+                            const uint2 r = lds8(yr);
                             yv[q].w[0] = r.x, yv[q].w[1] = r.y;
                         } else {
-                            constexpr int C = Raw<O, W>::WORDS / 4;
 #pragma unroll
-                            for (int c = 0; c < C; ++c) {
-                                const uint4 r = lds16(yr + L::y_piece(row, g * C + c));
+                            for (int c = 0; c < Raw<O, W>::WORDS / 4; ++c) {
+                                const uint4 r = lds16(yr + c * 16);
                                 yv[q].w[4 * c] = r.x, yv[q].w[4 * c + 1] = r.y, yv[q].w[4 * c + 2] = r.z, yv[q].w[4 * c + 3] = r.w;
                             }
                         }
@@ -783,18 +813,28 @@ struct ExpandSmall {
                     float o[W];
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        o[j] = __fmaf_rn(acc[n8][0][j >> 1][2 * (j & 1) + e], f, yv[0][j]);
-                        if constexpr (GATED) o[j] = silu<O>(o[j]) * __fmaf_rn(acc[n8][1][j >> 1][2 * (j & 1) + e], f, yv[1][j]);
+                        o[j] = __fmaf_rn(acc[0][j >> 1][2 * (j & 1) + e], f, yv[0][j]);
+                        if constexpr (GATED) o[j] = silu<O>(o[j]) * __fmaf_rn(acc[1][j >> 1][2 * (j & 1) + e], f, yv[1][j]);
                     }
-                    store_out<O, W>(static_cast<O *>(a.out) + tile.toks[row] * a.os + col + g * W, W, true, o);
+                    O *const p = reinterpret_cast<O *>(rows[row]) + (at + (uint32_t)now * (uint32_t)L::COLS);
+                    store_out<O, W>(p, W, true, o);
                 }
             }
             __syncwarp();  // the stage is read by all
-            copy(i & 1, now + 2 * kk);
+            copy(stage, now + 2 * kk);
+            stage ^= 1;
         }
         copies_wait<0>();
     }
 };
+
+// f with R as a constant, where Blocks::ranks(R)
+template <typename F>
+__device__ __forceinline__ void with_rank(int R, F f) {
+    if (R == 8) f(std::integral_constant<int, 8>{});
+    else if (R == 16) f(std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 32>{});
+}
 
 // ---- expand, many tokens, where blocks of 32 columns are whole and start on 16 bytes: a thread holds its entries of
 // B for all ranks, loaded once for all rows of the tile.
@@ -894,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     __shared__ Tile<TM> tile;
     __shared__ float up[TM];       // what a row of the split h has to be multiplied by (f16)
     __shared__ float row_top[TM];  // f16: largest magnitude of a row of the partial sums
+    __shared__ char *out_row[TM];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
     const int unit = (int)(blockIdx.x / (unsigned)C);
@@ -921,12 +962,12 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
     const int w0 = rank * kWarps + warp, kk = C * kWarps;
+    if (whole && tid < tile.count) out_row[tid] = reinterpret_cast<char *>(static_cast<O *>(a.out) + tile.toks[tid] * a.os);
     const auto copy_first = [&] {
-        if constexpr (BIG) return;
-        else {
-        const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
-        ex.copy_first();
-        }
+        if constexpr (!BIG)
+            with_rank(R, [&](auto r) {
+                ExpandSmall<T, O, GATED, decltype(r)::value>(a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk).copy_first();
+            });
     };
     if constexpr (!BIG && !GATED) {
         if (has && whole) copy_first();
@@ -1031,8 +1072,10 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
         bool done = false;
         if constexpr (!BIG) {
             if (has && whole) {
-                const ExpandSmall<T, O, GATED> ex{a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk, lane};
-                ex.run(sz, hs, up);
+                with_rank(R, [&](auto r) {
+                    ExpandSmall<T, O, GATED, decltype(r)::value>(a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk)
+                        .run(sz, hs, up, out_row);
+                });
                 done = true;
             }
         }
