@@ -57,8 +57,7 @@ tl_status run(const void *x, int64_t x_stride, const tl_adapters *ad, const int3
     a.R = ad->rank;
     a.adapters = ad->adapters;
     a.gated = gated;
-    a.vec_a = a.K % 8 == 0;
-    a.vec_x = a.vec_a && aligned(x, 16) && x_stride % 8 == 0;
+    a.vec_x = a.K % 8 == 0 && aligned(x, 16) && x_stride % 8 == 0;
     a.vec_y = columns8 && aligned(y, 16) && aligned(out, 16) && y_stride * size % 16 == 0 && out_stride * size % 16 == 0;
     a.ranks = a.S * a.R;
     a.wait_limit = d.wait_limit;

@@ -388,7 +388,8 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int
 }
 
 // ---- shrink, few tokens: 16 rows, the warps take chunks of 32 k (U in flight), operands from global memory to registers.
-template <typename T, int U>
+// VEC: rows start on 16 bytes.
+template <typename T, int U, bool VEC>
 __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *A, int c0, int c1,
                                              float *part, float *red) {
     constexpr int NT = Form<false>::NT;
@@ -414,9 +415,9 @@ __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &
             for (int u = 0; u < U; ++u) {
                 const int k = (c + u * kWarps) * 32 + t * 8, n = c + u * kWarps < c1 ? K - k : 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) xv[u][i] = load8(xr[i] + k, live[i] ? n : 0, a.vec_x);
+                for (int i = 0; i < 2; ++i) xv[u][i] = load8(xr[i] + k, live[i] ? n : 0, VEC);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) av[u][j] = load8(A + (int64_t)((j0 + j) * 8 + g) * K + k, j < nt ? n : 0, a.vec_a);
+                for (int j = 0; j < NT; ++j) av[u][j] = load8(A + (int64_t)((j0 + j) * 8 + g) * K + k, j < nt ? n : 0, VEC);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -691,9 +692,10 @@ struct ExpandSmall {
     const O *yp[YI];   // and of its rows of y
     uint32_t base, bto, yto;
     int first, kk, total, count, lane;
+    bool has;          // there is an adapter: else y goes through as it is (gated: through the product)
 
     __device__ __forceinline__ ExpandSmall(const LoraArgs &args, const Tile<16> &tile, const T *B, uint32_t base_, int first_, int kk_)
-        : a(args), base(base_), first(first_), kk(kk_), count(tile.count), lane(threadIdx.x & 31) {
+        : a(args), base(base_), first(first_), kk(kk_), count(tile.count), lane(threadIdx.x & 31), has(B != nullptr) {
         // (shards are whole blocks: block n has columns n COLS on, whatever shard they are in)
         total = (int)((GATED ? a.shard[0] : launch_columns()) / L::COLS);
         bp = B + a.col0 * R + lane * 8;
@@ -716,6 +718,7 @@ struct ExpandSmall {
             const T *b = bp + (int64_t)n * (L::COLS * R);
 #pragma unroll
             for (int q = 0; q < H; ++q) {
+                if (!has) break;
 #pragma unroll
                 for (int i = 0; i < BI; ++i)
                     copy16(to + q * BHALF + i * 512 + (bto ^ ((((i << (5 - SHIFT)) & 3) << 5))), b + i * 256, true);
@@ -768,6 +771,14 @@ struct ExpandSmall {
             for (int n8 = 0; n8 < 2; ++n8) {
                 if (n8 == 1 && !two) break;
                 float acc[H][I][4];
+                if (!has) {
+#pragma unroll
+                    for (int q = 0; q < H; ++q)
+#pragma unroll
+                        for (int m = 0; m < I; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[q][m][e] = 0.f;
+                } else
 #pragma unroll
                 for (int z = 0; z < STEPS; ++z)
 #pragma unroll
@@ -794,7 +805,7 @@ struct ExpandSmall {
                 for (int e = 0; e < 2; ++e) {
                     const int row = n8 * 8 + t + 4 * e;
                     if (row >= count) continue;
-                    const float f = kBf ? 1.f : up[row];
+                    const float f = kBf || !has ? 1.f : up[row];
                     Raw<O, W> yv[H];
 #pragma unroll
                     for (int q = 0; q < H; ++q) {
@@ -970,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             });
     };
     if constexpr (!BIG && !GATED) {
-        if (has && whole) copy_first();
+        if (whole) copy_first();
     }
     if (has) {
         const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
@@ -979,14 +990,16 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
         } else {
             const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-            shrink_small<T, GATED ? 1 : 2>(a, tile, sz, A, c0, c1, part, reinterpret_cast<float *>(smem + sz.red));
+            float *const red = reinterpret_cast<float *>(smem + sz.red);
+            if (a.vec_x) shrink_small<T, GATED ? 1 : 2, true>(a, tile, sz, A, c0, c1, part, red);
+            else shrink_small<T, 1, false>(a, tile, sz, A, c0, c1, part, red);
             __syncthreads();
         }
     }
     if constexpr (BIG) {
         if (has) want_expand<T, O>(a, tile, B, w0, kk);
     } else {
-        if (GATED && has && whole) copy_first();
+        if (GATED && whole) copy_first();
     }
     if (!kBf && has) {
         for (int row = warp; row < tile.count; row += kWarps) {
@@ -1071,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
         constexpr int G = BIG ? 2 : 1, J = GATED ? 2 : 4;
         bool done = false;
         if constexpr (!BIG) {
-            if (has && whole) {
+            if (whole) {
                 with_rank(R, [&](auto r) {
                     ExpandSmall<T, O, GATED, decltype(r)::value>(a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk)
                         .run(sz, hs, up, out_row);

@@ -366,7 +366,7 @@ struct LoraArgs {
     int ranks, rank0;         // rows of a for an adapter; the first of this launch's shards
     int64_t col0;             // first column of this launch's shards
     int gated;
-    int vec_x, vec_a, vec_y;  // rows start on 16-byte boundaries (y, out: columns of threads too)
+    int vec_x, vec_y;         // rows start on 16-byte boundaries (y, out: columns of threads too)
     int whole;                // columns come in whole blocks (the launcher's answer)
     int C;                    // blocks of a cluster
     const int *plan;          // tiles found beforehand (null: by each block)
