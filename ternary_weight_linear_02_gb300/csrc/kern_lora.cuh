@@ -388,11 +388,11 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int
 }
 
 // ---- shrink, few tokens: 16 rows, the warps take chunks of 32 k (U in flight), operands from global memory to registers.
-// VEC: rows start on 16 bytes.
-template <typename T, int U, bool VEC>
+// VEC: rows start on 16 bytes.  NT: n-tiles of 8 ranks a pass.
+template <typename T, int U, int NT, bool VEC>
 __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *A, int c0, int c1,
                                              float *part, float *red) {
-    constexpr int NT = Form<false>::NT;
+    static_assert(NT <= Form<false>::NT, "the sums' buffer");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, K = (int)a.K;
     const T *xr[2];
     bool live[2];
@@ -431,32 +431,29 @@ __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &
                     }
             }
         }
-        // the warps' sums: halves added in a fixed order
-#pragma unroll
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
-            __syncthreads();
-            if (warp >= half && warp < 2 * half) {
-                float *p = red + (warp - half) * (16 * NT * 8);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[(j * 4 + e) * 32 + lane] = acc[j][e];
-            }
-            __syncthreads();
-            if (warp < half) {
-                const float *p = red + warp * (16 * NT * 8);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] += p[(j * 4 + e) * 32 + lane];
-            }
-        }
-        if (warp == 0) {
+        // the warps' sums: of w and w + 4 by one of the two, then those four by all threads, in a fixed order
+        constexpr int SUMS = 16 * NT * 8;
+        float *const mine = red + (warp & 3) * SUMS + lane;
+        __syncthreads();
+        if (warp >= 4) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                if (j < nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) part[((e >> 1) * 8 + g) * sz.pstride + (j0 + j) * 8 + 2 * t + (e & 1)] = acc[j][e];
+                for (int e = 0; e < 4; ++e) mine[(j * 4 + e) * 32] = acc[j][e];
+        }
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(j * 4 + e) * 32] += acc[j][e];
+        }
+        __syncthreads();
+        for (int i = tid; i < nt * 128; i += kThreads) {
+            const float *p = red + i;
+            const int e = i >> 5 & 3, l = i & 31;
+            part[((e >> 1) * 8 + (l >> 2)) * sz.pstride + (j0 + (i >> 7)) * 8 + 2 * (l & 3) + (e & 1)] =
+                ((p[0] + p[SUMS]) + p[2 * SUMS]) + p[3 * SUMS];
         }
     }
 }
@@ -991,8 +988,9 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
         } else {
             const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
             float *const red = reinterpret_cast<float *>(smem + sz.red);
-            if (a.vec_x) shrink_small<T, GATED ? 1 : 2, true>(a, tile, sz, A, c0, c1, part, red);
-            else shrink_small<T, 1, false>(a, tile, sz, A, c0, c1, part, red);
+            constexpr int NT = GATED ? 4 : Form<false>::NT;  // (gated: what 80 registers hold with two loads of each in flight)
+            if (a.vec_x) shrink_small<T, 2, NT, true>(a, tile, sz, A, c0, c1, part, red);
+            else shrink_small<T, 1, NT, false>(a, tile, sz, A, c0, c1, part, red);
             __syncthreads();
         }
     }
