@@ -220,7 +220,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
     return r;
 }
-__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <bool BIG>
 struct Form {
@@ -229,7 +228,7 @@ struct Form {
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
 };
 
-constexpr int kBigSteps = 4;  // steps of 16 ranks (the launcher's rule: up to 64) whose entries of B a thread of expand_big holds
+constexpr int kBigSteps = 4;  // steps of 16 ranks (the launcher's rule: up to 64) whose entries of B a thread of ExpandBig holds
 
 // Sizes of a block's shared memory (bytes), the same on the host.
 struct Smem {
@@ -250,6 +249,7 @@ struct Smem {
         hstride = steps * 16 + (steps % 2 ? 0 : 16);
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
+        if (big && split < kWarps * 4096) split = kWarps * 4096;  // two stages of y for each warp, when the sums are joined
         blocks = split + ns * tm * hstride * 2;
         const int red_bytes = 4 * 16 * Form<false>::NT * 8 * 4, stages = 2 * kWarps * small_stage;
         // (gated: a third block on each SM is worth more than copying before the sums are added)
@@ -845,89 +845,103 @@ __device__ __forceinline__ void with_rank(int R, F f) {
 }
 
 // ---- expand, many tokens, where blocks of 32 columns are whole and start on 16 bytes: a thread holds its entries of
-// B for all ranks, loaded once for all rows of the tile.
+// B for all ranks, loaded once for all rows of the tile; rows of y come through two stages of the warp's own (their
+// trips took 15 us of 133 where each was waited for).  B null: y goes through as it is.
 template <typename T, typename O>
-__device__ __forceinline__ void expand_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *hs, const float *up,
-                                           const T *B, int sh, int64_t off, int64_t blk, int64_t kk, int64_t blocks) {
-    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, G = 2, Q = kBigSteps, J = 4, W = 8;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
-    // column of a fragment's n = g, and a thread's own: such that a thread's results are neighbours
-    const T *bp = B + (off + blk * 32 + (g >> 1) * W + (g & 1)) * R + 4 * t;
-    const O *yp = static_cast<const O *>(a.y) + off + blk * 32 + t * W;
-    O *op = static_cast<O *>(a.out) + off + blk * 32 + t * W;
-    const T *const h0 = hs + g * sz.hstride + sh * steps * 16 + 4 * t;
-    for (; blk < blocks; blk += kk) {
-        uint2 bv[Q][J];
+struct ExpandBig {
+    static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, Q = kBigSteps, J = 4, W = 8;
+    static constexpr int G = sizeof(O) == 4 ? 1 : 2, ROWS = 16 * G;         // rows of a stage
+    static constexpr int YROW = 32 * sizeof(O), C = YROW / 16, YI = ROWS * C / 32;  // bytes of a row, its pieces; copies of a lane
+    static constexpr int STAGE = ROWS * YROW;
+    static __device__ __forceinline__ uint32_t place(int row, int c) { return (uint32_t)(row * YROW + ((c ^ (C == 8 ? row & 1 : 0)) << 4)); }
+
+    // stages: shared memory of this warp; yrow, orow: the tile's rows of y and out
+    static __device__ __forceinline__ void run(const LoraArgs &a, int count, const Smem &sz, const T *hs, const float *up, const T *B,
+                                               int sh, int64_t off, int64_t blk, int64_t kk, int64_t blocks, uint32_t stages,
+                                               const char *const *yrow, char *const *orow) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
+        const bool has = B != nullptr;
+        // column of a fragment's n = g, and a thread's own: such that a thread's results are neighbours
+        const T *bp = B + (off + blk * 32 + (g >> 1) * W + (g & 1)) * R + 4 * t;
+        const T *const h0 = hs + g * sz.hstride + sh * steps * 16 + 4 * t;
+        int64_t next = blk;  // what is copied next: a block of columns and rows of it
+        int rows = 0;
+        const auto copy = [&](int stage) {
+            if (next < blocks) {
+                const int64_t at = (off + next * 32) * (int)sizeof(O) + lane % C * 16;
 #pragma unroll
-        for (int z = 0; z < Q; ++z)
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                bv[z][j] = make_uint2(0, 0);
-                if (z * 16 + 4 * t < R) bv[z][j] = ldg_nc_v2(bp + 2 * j * R + z * 16);
+                for (int i = 0; i < YI; ++i) {
+                    const int row = i * (32 / C) + lane / C;
+                    if (rows + row < count) copy16(stages + stage * STAGE + place(row, lane % C), yrow[rows + row] + at, true);
+                }
+                rows += ROWS;
+                if (rows >= count) rows = 0, next += kk;
             }
-        for (int r0 = 0; r0 < tile.count; r0 += 16 * G) {
-            Raw<O, W> yv[2 * G];
+            copies_commit();
+        };
+        copy(0);
+        copy(1);
+        int stage = 0;
+        for (; blk < blocks; blk += kk) {
+            uint2 bv[Q][J];
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i)
-                if (r0 + i * 8 + g < tile.count) yv[i].load(yp + tile.toks[r0 + i * 8 + g] * a.ys, W, true);
-            float acc[G][J][4];
+            for (int z = 0; z < Q; ++z)
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-#pragma unroll
-            for (int z = 0; z < Q; ++z) {
-                if (z >= steps) break;
+                for (int j = 0; j < J; ++j) {
+                    bv[z][j] = make_uint2(0, 0);
+                    if (has && z * 16 + 4 * t < R) bv[z][j] = ldg_nc_v2(bp + 2 * j * R + z * 16);
+                }
+            bp += kk * 32 * R;
+            const int64_t at = (off + blk * 32 + t * W) * (int)sizeof(O);
+            for (int r0 = 0; r0 < count; r0 += ROWS) {
+                float acc[G][J][4];
 #pragma unroll
                 for (int i = 0; i < G; ++i)
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + z * 16;
-                        const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                        const uint32_t f[4] = {x.x, v.x, x.y, v.y};
+                    for (int j = 0; j < J; ++j)
 #pragma unroll
-                        for (int j = 0; j < J; ++j) mma16816<T>(acc[i][j], f, bv[z][j].x, bv[z][j].y);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+#pragma unroll
+                for (int z = 0; z < Q; ++z) {
+                    if (z >= steps || !has) break;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+#pragma unroll
+                        for (int i = 0; i < G; ++i) {
+                            const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + z * 16;
+                            const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                            const uint32_t f[4] = {x.x, v.x, x.y, v.y};
+#pragma unroll
+                            for (int j = 0; j < J; ++j) mma16816<T>(acc[i][j], f, bv[z][j].x, bv[z][j].y);
+                        }
+                }
+                copies_wait<1>();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2 * G; ++i) {
+                    const int row = i * 8 + g;
+                    if (r0 + row >= count) continue;
+                    const float f = kBf || !has ? 1.f : up[r0 + row];
+                    Raw<O, W> yv;
+#pragma unroll
+                    for (int c = 0; c < Raw<O, W>::WORDS / 4; ++c) {
+                        const uint4 q = lds16(stages + stage * STAGE + place(row, t * (Raw<O, W>::WORDS / 4) + c));
+                        yv.w[4 * c] = q.x, yv.w[4 * c + 1] = q.y, yv.w[4 * c + 2] = q.z, yv.w[4 * c + 3] = q.w;
                     }
-            }
+                    float v[W];
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i) {
-                const int row = r0 + i * 8 + g;
-                if (row >= tile.count) continue;
-                const float f = kBf ? 1.f : up[row];
-                float v[W];
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = __fmaf_rn(acc[i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[i][j]);
-                store_out<O, W>(op + tile.toks[row] * a.os, W, true, v);
+                    for (int j = 0; j < W; ++j) v[j] = __fmaf_rn(acc[i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[j]);
+                    store_out<O, W>(reinterpret_cast<O *>(orow[r0 + row] + at), W, true, v);
+                }
+                __syncwarp();  // the stage is read by all
+                copy(stage);
+                stage ^= 1;
             }
         }
-        bp += kk * 32 * R;
-        yp += kk * 32;
-        op += kk * 32;
+        copies_wait<0>();
     }
-}
-
-// What this warp will expand, requested into the L2 while the sums are joined.  (With few tokens a tile
-// there are more columns than rows, and requests of single lines cost more than they save.)
-template <typename T, typename O>
-__device__ __forceinline__ void want_expand(const LoraArgs &a, const Tile<128> &tile, const T *B, int first, int kk) {
-    const int lane = threadIdx.x & 31;
-    int64_t skip = first, off = a.col0;
-    for (int sh = 0; sh < a.S; ++sh) {
-        const int64_t wide = a.shard[sh], blocks = (wide + 31) / 32;
-        int64_t blk = skip;
-        for (; blk < blocks; blk += kk) {
-            const int64_t col = off + blk * 32;
-            const int bytes = (int)min((int64_t)32, wide - blk * 32) * a.R * 2;
-            for (int i = lane * 128; i < bytes; i += 4096) prefetch_line(reinterpret_cast<const char *>(B + col * a.R) + i);
-            for (int row = lane; row < tile.count; row += 32) prefetch_line(static_cast<const O *>(a.y) + tile.toks[row] * a.ys + col);
-        }
-        skip = blk - blocks;
-        off += wide;
-    }
-}
+};
 
 // O: type of y and out.
 template <typename T, typename O, bool BIG, bool GATED>
@@ -943,6 +957,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     __shared__ float up[TM];       // what a row of the split h has to be multiplied by (f16)
     __shared__ float row_top[TM];  // f16: largest magnitude of a row of the partial sums
     __shared__ char *out_row[TM];
+    __shared__ const char *y_row[BIG ? TM : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
     const int unit = (int)(blockIdx.x / (unsigned)C);
@@ -970,7 +985,8 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
     const int w0 = rank * kWarps + warp, kk = C * kWarps;
-    if (whole && tid < tile.count) out_row[tid] = reinterpret_cast<char *>(static_cast<O *>(a.out) + tile.toks[tid] * a.os);
+    if (BIG && tid < tile.count) y_row[tid] = reinterpret_cast<const char *>(static_cast<const O *>(a.y) + tile.toks[tid] * a.ys);
+    if ((BIG || whole) && tid < tile.count) out_row[tid] = reinterpret_cast<char *>(static_cast<O *>(a.out) + tile.toks[tid] * a.os);
     const auto copy_first = [&] {
         if constexpr (!BIG)
             with_rank(R, [&](auto r) {
@@ -994,11 +1010,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             __syncthreads();
         }
     }
-    if constexpr (BIG) {
-        if (has) want_expand<T, O>(a, tile, B, w0, kk);
-    } else {
-        if (GATED && whole) copy_first();
-    }
+    if (GATED && whole) copy_first();
     if (!kBf && has) {
         for (int row = warp; row < tile.count; row += kWarps) {
             float top = 0.f;
@@ -1077,6 +1089,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     }
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
+    if (BIG && C > 1) cl_wait_acquire();  // (the stages of y lie where the sums were)
     {
         // columns in blocks, dealt to the cluster's warps
         constexpr int G = BIG ? 2 : 1, J = GATED ? 2 : 4;
@@ -1095,8 +1108,9 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
             bool big = false;
             if constexpr (BIG) {
-                big = has && a.vec_y && wide % 32 == 0;
-                if (big) expand_big<T, O>(a, tile, sz, hs, up, B, sh, off, skip, kk, blocks);
+                using E = ExpandBig<T, O>;
+                big = a.vec_y && wide % 32 == 0;
+                if (big) E::run(a, tile.count, sz, hs, up, B, sh, off, skip, kk, blocks, smem_u32(smem) + warp * 2 * E::STAGE, y_row, out_row);
             }
             for (int64_t blk = skip; blk < blocks && !big; blk += kk)
                 for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
@@ -1105,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             off += wide;
         }
     }
-    if (C > 1) cl_wait_acquire();
+    if (!BIG && C > 1) cl_wait_acquire();
 }
 
 constexpr int kMaxSmem = 200 * 1024;
