@@ -215,6 +215,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
     return r;
 }
+// a 16 x 16 fragment: lanes 0-15 give rows' first halves, 16-31 their second
+__device__ __forceinline__ void ldmatrix_x4(uint32_t at, uint32_t (&f)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at));
+}
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 r;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
@@ -234,7 +238,7 @@ constexpr int kBigSteps = 4;  // steps of 16 ranks (the launcher's rule: up to 6
 struct Smem {
     int ranks, npad;  // S R, and rounded up to 16
     int pstride;      // floats between rows of the partial sums: 16-byte stores of 8 rows hit other banks
-    int hstride;      // elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
+    int hstride;      // elements of T between rows of the split h: loads (8 bytes of 4 rows; big: 16 of 8) hit other banks
     int stage;        // BIG: a stage
     int split;        // where the split h begins
     int blocks, red;  // small: where the stages of B and y, and the warps' sums begin
@@ -246,7 +250,7 @@ struct Smem {
         npad = (ranks + 15) & ~15;
         pstride = ranks + 4;
         const int steps = S * ((R + 15) / 16);
-        hstride = steps * 16 + (steps % 2 ? 0 : 16);
+        hstride = steps * 16 + (big ? 8 : steps % 2 ? 0 : 16);
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
         if (big && split < kWarps * 4096) split = kWarps * 4096;  // two stages of y for each warp, when the sums are joined
@@ -623,9 +627,11 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
             for (int q = 0; q < H; ++q)
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const T *h = hs + (s * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + 4 * t;
-                    const uint2 x = *reinterpret_cast<const uint2 *>(h), z = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                    const uint32_t f[4] = {x.x, z.x, x.y, z.y};
+                    const T *h = hs + (s * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + (TM == 128 ? 2 : 4) * t;
+                    const T *h8 = h + 8 * sz.hstride;
+                    constexpr int SECOND = TM == 128 ? 8 : 2;  // where ranks 4 t + 2, 4 t + 3 are
+                    const uint32_t f[4] = {*reinterpret_cast<const uint32_t *>(h), *reinterpret_cast<const uint32_t *>(h8),
+                                           *reinterpret_cast<const uint32_t *>(h + SECOND), *reinterpret_cast<const uint32_t *>(h8 + SECOND)};
 #pragma unroll
                     for (int j = 0; j < J; ++j) mma16816<T>(acc[q][i][j], f, bv[q][j].x, bv[q][j].y);
                 }
@@ -851,25 +857,25 @@ template <typename T, typename O>
 struct ExpandBig {
     static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, Q = kBigSteps, J = 4, W = 8;
-    static constexpr int G = sizeof(O) == 4 ? 1 : 2, ROWS = 16 * G;         // rows of a stage
+    static constexpr int G = 1, ROWS = 16 * G;  // rows of a stage (32: 131 us, registers run out)
     static constexpr int YROW = 32 * sizeof(O), C = YROW / 16, YI = ROWS * C / 32;  // bytes of a row, its pieces; copies of a lane
     static constexpr int STAGE = ROWS * YROW;
     static __device__ __forceinline__ uint32_t place(int row, int c) { return (uint32_t)(row * YROW + ((c ^ (C == 8 ? row & 1 : 0)) << 4)); }
 
     // stages: shared memory of this warp; yrow, orow: the tile's rows of y and out
     static __device__ __forceinline__ void run(const LoraArgs &a, int count, const Smem &sz, const T *hs, const float *up, const T *B,
-                                               int sh, int64_t off, int64_t blk, int64_t kk, int64_t blocks, uint32_t stages,
+                                               int sh, int64_t off, int blk, int kk, int blocks, uint32_t stages,
                                                const char *const *yrow, char *const *orow) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
         const bool has = B != nullptr;
         // column of a fragment's n = g, and a thread's own: such that a thread's results are neighbours
-        const T *bp = B + (off + blk * 32 + (g >> 1) * W + (g & 1)) * R + 4 * t;
-        const T *const h0 = hs + g * sz.hstride + sh * steps * 16 + 4 * t;
-        int64_t next = blk;  // what is copied next: a block of columns and rows of it
-        int rows = 0;
+        const T *const b0 = B + (off + (g >> 1) * W + (g & 1)) * R + 4 * t;
+        const uint32_t h0 = smem_u32(hs) + 2 * ((lane & 15) * sz.hstride + (lane >> 4) * 8 + sh * steps * 16), hrow = 2 * sz.hstride;
+        const uint32_t ycol = (uint32_t)off * (uint32_t)sizeof(O);
+        int next = blk, rows = 0;  // what is copied next: a block of columns and rows of it
         const auto copy = [&](int stage) {
             if (next < blocks) {
-                const int64_t at = (off + next * 32) * (int)sizeof(O) + lane % C * 16;
+                const uint32_t at = ycol + next * YROW + lane % C * 16;
 #pragma unroll
                 for (int i = 0; i < YI; ++i) {
                     const int row = i * (32 / C) + lane / C;
@@ -885,6 +891,7 @@ struct ExpandBig {
         int stage = 0;
         for (; blk < blocks; blk += kk) {
             uint2 bv[Q][J];
+            const T *const bp = b0 + (int64_t)blk * (32 * R);
 #pragma unroll
             for (int z = 0; z < Q; ++z)
 #pragma unroll
@@ -892,29 +899,34 @@ struct ExpandBig {
                     bv[z][j] = make_uint2(0, 0);
                     if (has && z * 16 + 4 * t < R) bv[z][j] = ldg_nc_v2(bp + 2 * j * R + z * 16);
                 }
-            bp += kk * 32 * R;
-            const int64_t at = (off + blk * 32 + t * W) * (int)sizeof(O);
+            const uint32_t at = ycol + blk * YROW + t * (W * (int)sizeof(O));
             for (int r0 = 0; r0 < count; r0 += ROWS) {
                 float acc[G][J][4];
+                if (has) {
+                    // steps of (16 ranks, number of the split h, 16 rows), the next one's fragment on its way
+                    constexpr int STEPS = Q * NS * G;
+                    const uint32_t hr = h0 + r0 * hrow;
+                    uint32_t f[2][4];
+                    const auto load = [&](int s) { ldmatrix_x4(hr + (s / G % NS * TM + s % G * 16) * hrow + s / (G * NS) * 32, f[s & 1]); };
+                    load(0);
 #pragma unroll
-                for (int i = 0; i < G; ++i)
+                    for (int s = 0; s < STEPS; ++s) {
+                        const int z = s / (G * NS);
+                        if (z >= steps) break;
+                        if (s + 1 < STEPS && (s + 1) / (G * NS) < steps) load(s + 1);
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-#pragma unroll
-                for (int z = 0; z < Q; ++z) {
-                    if (z >= steps || !has) break;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int i = 0; i < G; ++i) {
-                            const T *h = h0 + (n * TM + r0 + i * 16) * sz.hstride + z * 16;
-                            const uint2 x = *reinterpret_cast<const uint2 *>(h), v = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
-                            const uint32_t f[4] = {x.x, v.x, x.y, v.y};
-#pragma unroll
-                            for (int j = 0; j < J; ++j) mma16816<T>(acc[i][j], f, bv[z][j].x, bv[z][j].y);
+                        for (int j = 0; j < J; ++j) {
+                            if (s < G) mma16816_first<T>(acc[s % G][j], f[s & 1], bv[z][j].x, bv[z][j].y);
+                            else mma16816<T>(acc[s % G][j], f[s & 1], bv[z][j].x, bv[z][j].y);
                         }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
                 }
                 copies_wait<1>();
                 __syncwarp();
@@ -1082,7 +1094,14 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
                         h[j] = of_f<T>(z[j]);
                         z[j] = isfinite(to_f(h[j])) ? z[j] - to_f(h[j]) : 0.f;
                     }
-                    *reinterpret_cast<uint2 *>(hs + (n * TM + place) * sz.hstride + e * 4) = *reinterpret_cast<const uint2 *>(h);
+                    const uint2 w = *reinterpret_cast<const uint2 *>(h);
+                    if constexpr (BIG) {  // in the order in which ldmatrix gives a thread ranks 4 t .. 4 t + 3
+                        T *const at = hs + (n * TM + row) * sz.hstride + (e >> 2) * 16 + (e & 3) * 2;
+                        *reinterpret_cast<uint32_t *>(at) = w.x;
+                        *reinterpret_cast<uint32_t *>(at + 8) = w.y;
+                    } else {
+                        *reinterpret_cast<uint2 *>(hs + (n * TM + place) * sz.hstride + e * 4) = w;
+                    }
                 }
             }
         }
@@ -1110,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             if constexpr (BIG) {
                 using E = ExpandBig<T, O>;
                 big = a.vec_y && wide % 32 == 0;
-                if (big) E::run(a, tile.count, sz, hs, up, B, sh, off, skip, kk, blocks, smem_u32(smem) + warp * 2 * E::STAGE, y_row, out_row);
+                if (big) E::run(a, tile.count, sz, hs, up, B, sh, off, (int)skip, kk, (int)blocks, smem_u32(smem) + warp * 2 * E::STAGE, y_row, out_row);
             }
             for (int64_t blk = skip; blk < blocks && !big; blk += kk)
                 for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
