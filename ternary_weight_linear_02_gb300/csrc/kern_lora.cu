@@ -120,9 +120,10 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
 // 1024 x 4, 16, 2 x 18944: 75 against 143.
 constexpr int kBigRanks = 128;
 bool big_tiles(const LoraArgs &a) {
+    if (!a.vec_x || !a.vec_y || a.gated || a.R > 64) return false;
     const int64_t present = a.adapters + 1 < a.M ? a.adapters + 1 : a.M;
     const double again = (double)a.M / 16 * a.R * 2 * ((double)a.S * a.K + a.N);
-    return a.vec_x && !a.gated && a.R <= 64 && a.M >= 128 * present && again >= 100e6;
+    return a.M >= 128 * present && again >= 100e6;
 }
 
 int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {
@@ -161,7 +162,8 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
         a.plan = plan;
     }
     a.overlap = 1;
-    const int shards = a.S, at_once = big ? (kBigRanks / a.R < shards ? kBigRanks / a.R : shards) : shards;
+    const int shards = a.S, most_shards = kBigRanks / ((a.R + 15) / 16 * 16),
+              at_once = big && most_shards < shards ? most_shards : shards;
     for (int s0 = 0; s0 < shards; s0 += at_once) {
         LoraArgs b = a;
         b.S = shards - s0 < at_once ? shards - s0 : at_once;

@@ -215,9 +215,8 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
     return r;
 }
-// a 16 x 16 fragment: lanes 0-15 give rows' first halves, 16-31 their second
-__device__ __forceinline__ void ldmatrix_x4(uint32_t at, uint32_t (&f)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at));
+__device__ __forceinline__ void sts16(uint32_t at, uint4 r) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 r;
@@ -232,14 +231,13 @@ struct Form {
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
 };
 
-constexpr int kBigSteps = 4;  // steps of 16 ranks (the launcher's rule: up to 64) whose entries of B a thread of ExpandBig holds
-
 // Sizes of a block's shared memory (bytes), the same on the host.
 struct Smem {
     int ranks, npad;  // S R, and rounded up to 16
     int pstride;      // floats between rows of the partial sums: 16-byte stores of 8 rows hit other banks
-    int hstride;      // elements of T between rows of the split h: loads (8 bytes of 4 rows; big: 16 of 8) hit other banks
-    int stage;        // BIG: a stage
+    int hstride;      // small: elements of T between rows of the split h: 8-byte loads of 4 rows hit other banks
+    int stage;        // BIG: a stage of the shrink
+    int hper, htiles; // BIG: shards in a tile of the split h (64 ranks, each shard's rounded up to 16), such tiles
     int split;        // where the split h begins
     int blocks, red;  // small: where the stages of B and y, and the warps' sums begin
     int total;
@@ -250,11 +248,16 @@ struct Smem {
         npad = (ranks + 15) & ~15;
         pstride = ranks + 4;
         const int steps = S * ((R + 15) / 16);
-        hstride = steps * 16 + (big ? 8 : steps % 2 ? 0 : 16);
+        hstride = steps * 16 + (steps % 2 ? 0 : 16);
         stage = (128 + npad) * 128;
         split = tm * pstride * 4;
-        if (big && split < kWarps * 4096) split = kWarps * 4096;  // two stages of y for each warp, when the sums are joined
-        blocks = split + ns * tm * hstride * 2;
+        hper = big ? 4 / ((R + 15) / 16) : 1;
+        htiles = (S + hper - 1) / hper;
+        if (big) {  // two stages of B and y, when the sums are joined; h begins on 1024 bytes
+            const int expand = 2 * 8192 + kWarps * 4096;
+            split = ((split > expand ? split : expand) + 1023) & ~1023;
+        }
+        blocks = split + (big ? ns * htiles * 16384 : ns * tm * hstride * 2);
         const int red_bytes = 4 * 16 * Form<false>::NT * 8 * 4, stages = 2 * kWarps * small_stage;
         // (gated: a third block on each SM is worth more than copying before the sums are added)
         red = blocks + (gated ? 0 : stages);
@@ -466,17 +469,18 @@ __device__ __forceinline__ void shrink_small(const LoraArgs &a, const Tile<16> &
 // MMA reads them), copied by all warps; one of them issues a stage's MMAs once all have its copies.  (A ninth warp
 // for that would leave 96 registers a thread instead of 128 with two blocks on an SM.)  Every wait gives up after a
 // while: the sums are NaN then.  On return the sums are stored.
+constexpr uint32_t kTmemCols = 128;  // of a block: the shrink's sums (up to 128 ranks), then two blocks of columns
+
+// Returns the tensor memory, which the caller frees.
 template <typename T>
-__device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *A, int k0, int k1,
-                                           unsigned char *ring, float *part) {
+__device__ __forceinline__ uint32_t shrink_big(const LoraArgs &a, const Tile<128> &tile, const Smem &sz, const T *A, int k0, int k1,
+                                               unsigned char *ring, float *part) {
     using F = Form<true>;
     constexpr int ST = F::STAGES, LAG = F::LAG;
     __shared__ uint64_t full[ST], empty[ST], done, never;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t cols = 32;
-    while (cols < (uint32_t)sz.npad) cols *= 2;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], kThreads);
@@ -488,7 +492,7 @@ __device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &t
         fence_barrier_init();
     }
     constexpr int kIssuer = kWarps - 1;
-    if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, cols);
+    if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, kTmemCols);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -575,13 +579,14 @@ __device__ __forceinline__ void shrink_big(const LoraArgs &a, const Tile<128> &t
         tc::fence_before_sync();
     }
     __syncthreads();
-    if (warp == kIssuer) tc::tmem_dealloc(tm, cols);
+    return tm;
 }
 
-// ---- expand: rows [r0, r0 + 16 G) of the tile, a block of 8 J columns (gated: of either half), any sizes.
-template <typename T, typename O, int TM, int G, bool GATED>
-__device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, const Smem &sz, const T *hs, const float *up, const T *B,
-                                       int sh, int64_t off, int64_t wide, int64_t blk, int r0) {
+// ---- expand, few tokens: a block of 8 J columns (gated: of either half), any sizes.
+template <typename T, typename O, bool GATED>
+__device__ __forceinline__ void expand(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *hs, const float *up, const T *B,
+                                       int sh, int64_t off, int64_t wide, int64_t blk) {
+    constexpr int TM = 16, G = 1, r0 = 0;
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
     constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
     constexpr int J = GATED ? 2 : 4, W = 2 * J, H = GATED ? 2 : 1;  // n-tiles a block; contiguous columns of a thread; halves
@@ -627,11 +632,9 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<TM> &tile, 
             for (int q = 0; q < H; ++q)
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const T *h = hs + (s * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + (TM == 128 ? 2 : 4) * t;
-                    const T *h8 = h + 8 * sz.hstride;
-                    constexpr int SECOND = TM == 128 ? 8 : 2;  // where ranks 4 t + 2, 4 t + 3 are
-                    const uint32_t f[4] = {*reinterpret_cast<const uint32_t *>(h), *reinterpret_cast<const uint32_t *>(h8),
-                                           *reinterpret_cast<const uint32_t *>(h + SECOND), *reinterpret_cast<const uint32_t *>(h8 + SECOND)};
+                    const T *h = hs + (s * TM + r0 + i * 16 + g) * sz.hstride + ((GATED ? q : sh) * steps + st) * 16 + 4 * t;
+                    const uint2 x = *reinterpret_cast<const uint2 *>(h), z = *reinterpret_cast<const uint2 *>(h + 8 * sz.hstride);
+                    const uint32_t f[4] = {x.x, z.x, x.y, z.y};
 #pragma unroll
                     for (int j = 0; j < J; ++j) mma16816<T>(acc[q][i][j], f, bv[q][j].x, bv[q][j].y);
                 }
@@ -850,108 +853,154 @@ __device__ __forceinline__ void with_rank(int R, F f) {
     else f(std::integral_constant<int, 32>{});
 }
 
-// ---- expand, many tokens, where blocks of 32 columns are whole and start on 16 bytes: a thread holds its entries of
-// B for all ranks, loaded once for all rows of the tile; rows of y come through two stages of the warp's own (their
-// trips took 15 us of 133 where each was waited for).  B null: y goes through as it is.
+// ---- expand, many tokens: blocks of 64 columns (32 of fp32) of a shard, dealt to the cluster's blocks; a shard's last may
+// be cut short (to eights that start on 16 bytes: the launcher's rule).  The split h (K-major, swizzled as the MMA reads it) times a block's rows of B on tcgen05,
+// into one of two accumulators while the other's columns are added to y.  B and y are copied two blocks of
+// columns ahead; a warp has 32 rows of half the columns, reads a row of its accumulator a thread, and goes through its
+// stage of y, so that global memory is read and written in 64-byte pieces of rows.  (Warp MMAs with B in registers: 33 us
+// where this takes LATER; they alone took 20.)  B null: y goes through as it is.
 template <typename T, typename O>
 struct ExpandBig {
     static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    static constexpr int TM = 128, NS = kBf && sizeof(O) == 4 ? 3 : 2, Q = kBigSteps, J = 4, W = 8;
-    static constexpr int G = 1, ROWS = 16 * G;  // rows of a stage (32: 131 us, registers run out)
-    static constexpr int YROW = 32 * sizeof(O), C = YROW / 16, YI = ROWS * C / 32;  // bytes of a row, its pieces; copies of a lane
-    static constexpr int STAGE = ROWS * YROW;
-    static __device__ __forceinline__ uint32_t place(int row, int c) { return (uint32_t)(row * YROW + ((c ^ (C == 8 ? row & 1 : 0)) << 4)); }
+    static constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
+    static constexpr int COLS = 128 / sizeof(O), HALF = COLS / 2, W = 16 / sizeof(O);  // columns of a block, of a warp, of 16 bytes
+    static constexpr int B_STAGE = 8192, Y_STAGE = 2048;
 
-    // stages: shared memory of this warp; yrow, orow: the tile's rows of y and out
-    static __device__ __forceinline__ void run(const LoraArgs &a, int count, const Smem &sz, const T *hs, const float *up, const T *B,
-                                               int sh, int64_t off, int blk, int kk, int blocks, uint32_t stages,
-                                               const char *const *yrow, char *const *orow) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = a.R, steps = (R + 15) / 16;
-        const bool has = B != nullptr;
-        // column of a fragment's n = g, and a thread's own: such that a thread's results are neighbours
-        const T *const b0 = B + (off + (g >> 1) * W + (g & 1)) * R + 4 * t;
-        const uint32_t h0 = smem_u32(hs) + 2 * ((lane & 15) * sz.hstride + (lane >> 4) * 8 + sh * steps * 16), hrow = 2 * sz.hstride;
-        const uint32_t ycol = (uint32_t)off * (uint32_t)sizeof(O);
-        int next = blk, rows = 0;  // what is copied next: a block of columns and rows of it
-        const auto copy = [&](int stage) {
-            if (next < blocks) {
-                const uint32_t at = ycol + next * YROW + lane % C * 16;
+    const LoraArgs &a;
+    const Smem &sz;
+    unsigned char *const smem;
+    const T *const B;
+    const char *const *const yrow;
+    char *const *const orow;
+    const int count, rank, lane, warp, steps;
+
+    __device__ __forceinline__ static uint32_t y_place(int row, int c) { return (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4)); }
+    __device__ __forceinline__ uint32_t y_stage(int s) const { return smem_u32(smem) + 2 * B_STAGE + (warp * 2 + s) * Y_STAGE; }
+    // block n: its shard, first column and columns
+    struct Place {
+        int sh, col, left;
+    };
+    __device__ __forceinline__ Place locate(int n) const {
+        Place p{0, (int)a.col0, (int)a.shard[0]};
+        for (int blocks; n >= (blocks = (p.left + COLS - 1) / COLS) && p.sh + 1 < a.S; n -= blocks) p.col += p.left, p.left = (int)a.shard[++p.sh];
+        p.col += n * COLS;
+        p.left -= n * COLS;
+        return p;
+    }
+    // the lane's 16 bytes of rows of the warp's half: where they begin; none where the block is cut short before them
+    __device__ __forceinline__ uint32_t y_column(const Place &p) const {
+        return (uint32_t)(p.col + (warp >> 2) * HALF + (lane & 3) * W) * (uint32_t)sizeof(O);
+    }
+    __device__ __forceinline__ bool y_there(const Place &p) const { return (warp >> 2) * HALF + (lane & 3) * W < p.left; }
+    __device__ __forceinline__ void copy_b(const Place &at, int s) const {
+        if (B) {
+            const int c = threadIdx.x >> 2;
+            if (c < COLS && c < at.left) {  // (what is behind stays what it was: columns do not meet)
+                const T *const b = B + (int64_t)(at.col + c) * a.R;
+                const uint32_t to = smem_u32(smem) + s * B_STAGE + c * 128;
 #pragma unroll
-                for (int i = 0; i < YI; ++i) {
-                    const int row = i * (32 / C) + lane / C;
-                    if (rows + row < count) copy16(stages + stage * STAGE + place(row, lane % C), yrow[rows + row] + at, true);
+                for (int i = 0; i < 2; ++i) {
+                    const int p = (threadIdx.x & 3) + 4 * i;  // (zeros up to whole steps of 16 ranks)
+                    if (p < 2 * steps) copy16(to + ((p ^ (c & 7)) << 4), p * 8 < a.R ? b + p * 8 : b, p * 8 < a.R);
                 }
-                rows += ROWS;
-                if (rows >= count) rows = 0, next += kk;
             }
-            copies_commit();
+        }
+        copies_commit();
+    }
+    __device__ __forceinline__ void copy_y(const Place &p, int s) const {
+        const uint32_t at = y_column(p), to = y_stage(s);
+        const int rows = y_there(p) ? count : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2), all = (warp & 3) * 32 + row;
+            if (all < rows) copy16(to + y_place(row, lane & 3), yrow[all] + at, true);
+        }
+        copies_commit();
+    }
+    // tm: tensor memory of two accumulators; done: their barriers.  False: a wait gave up (the results are NaN).
+    __device__ __forceinline__ bool run(const float *up, uint32_t tm, uint64_t *done) const {
+        int blocks = 0;
+        for (int i = 0; i < a.S; ++i) blocks += ((int)a.shard[i] + COLS - 1) / COLS;
+        const int C = a.C, n = rank < blocks ? (blocks - 1 - rank) / C + 1 : 0;
+        const uint32_t idesc = tc::idesc_f16(COLS, kBf);
+        bool ok = true;
+        const auto copy = [&](int i) {
+            if (i < n) {
+                const Place p = locate(rank + i * C);
+                copy_b(p, i & 1);
+                copy_y(p, i & 1);
+            } else {
+                copies_commit();
+                copies_commit();
+            }
+        };
+        const auto multiply = [&](int i) {
+            const int sh = locate(rank + i * C).sh;
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+                const uint64_t bd = tc::desc_sw128(smem + (i & 1) * B_STAGE);
+                for (int q = 0; q < NS; ++q) {
+                    const uint64_t hd = tc::desc_sw128(smem + sz.split + (q * sz.htiles + sh / sz.hper) * 16384) + sh % sz.hper * steps * 2;
+                    for (int z = 0; z < steps; ++z) tc::mma_ss(tm + (i & 1) * COLS, hd + z * 2, bd + z * 2, idesc, (q | z) != 0);
+                }
+                tc::commit(&done[i & 1]);
+            }
+            __syncwarp();
         };
         copy(0);
         copy(1);
-        int stage = 0;
-        for (; blk < blocks; blk += kk) {
-            uint2 bv[Q][J];
-            const T *const bp = b0 + (int64_t)blk * (32 * R);
-#pragma unroll
-            for (int z = 0; z < Q; ++z)
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    bv[z][j] = make_uint2(0, 0);
-                    if (has && z * 16 + 4 * t < R) bv[z][j] = ldg_nc_v2(bp + 2 * j * R + z * 16);
-                }
-            const uint32_t at = ycol + blk * YROW + t * (W * (int)sizeof(O));
-            for (int r0 = 0; r0 < count; r0 += ROWS) {
-                float acc[G][J][4];
-                if (has) {
-                    // steps of (16 ranks, number of the split h, 16 rows), the next one's fragment on its way
-                    constexpr int STEPS = Q * NS * G;
-                    const uint32_t hr = h0 + r0 * hrow;
-                    uint32_t f[2][4];
-                    const auto load = [&](int s) { ldmatrix_x4(hr + (s / G % NS * TM + s % G * 16) * hrow + s / (G * NS) * 32, f[s & 1]); };
-                    load(0);
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
-                        const int z = s / (G * NS);
-                        if (z >= steps) break;
-                        if (s + 1 < STEPS && (s + 1) / (G * NS) < steps) load(s + 1);
-#pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            if (s < G) mma16816_first<T>(acc[s % G][j], f[s & 1], bv[z][j].x, bv[z][j].y);
-                            else mma16816<T>(acc[s % G][j], f[s & 1], bv[z][j].x, bv[z][j].y);
-                        }
-                    }
+        copies_wait<3>();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        if (B && n > 0 && warp == 0) multiply(0);
+        const int row0 = (warp & 3) * 32;
+        for (int i = 0; i < n; ++i) {
+            const int s = i & 1;
+            copies_wait<1>();  // the next block's B, and before it this one's y
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc::fence_before_sync();
+            __syncthreads();
+            if (B && i + 1 < n && warp == 0) multiply(i + 1);
+            if (B && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&done[s], (i >> 1) & 1));
+            if (row0 < count) {
+                uint32_t acc[HALF];
+                if (B && ok) {
+                    tc::fence_after_sync();
+                    const uint32_t from = tm + ((uint32_t)row0 << 16) + s * COLS + (warp >> 2) * HALF;
+                    if constexpr (HALF == 32) tc::ld_32x32b_x32(from, acc);
+                    else tc::ld_32x32b_x16(from, acc);
+                    tc::wait_ld();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < G; ++i)
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+                    for (int c = 0; c < HALF; ++c) acc[c] = ok ? 0u : 0x7FC00000u;
                 }
-                copies_wait<1>();
+                const float f = kBf || !B ? 1.f : up[row0 + lane];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t at = y_stage(s) + y_place(lane, c);
+                    const uint4 q = lds16(at);
+                    Raw<O, W> y;
+                    y.w[0] = q.x, y.w[1] = q.y, y.w[2] = q.z, y.w[3] = q.w;
+                    O v[W];
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[e] = of_f<O>(__fmaf_rn(__uint_as_float(acc[c * W + e]), f, y[e]));
+                    sts16(at, *reinterpret_cast<const uint4 *>(v));
+                }
                 __syncwarp();
+                const Place p = locate(rank + i * C);
+                const uint32_t at = y_column(p);
+                const int rows = y_there(p) ? count : 0;
 #pragma unroll
-                for (int i = 0; i < 2 * G; ++i) {
-                    const int row = i * 8 + g;
-                    if (r0 + row >= count) continue;
-                    const float f = kBf || !has ? 1.f : up[r0 + row];
-                    Raw<O, W> yv;
-#pragma unroll
-                    for (int c = 0; c < Raw<O, W>::WORDS / 4; ++c) {
-                        const uint4 q = lds16(stages + stage * STAGE + place(row, t * (Raw<O, W>::WORDS / 4) + c));
-                        yv.w[4 * c] = q.x, yv.w[4 * c + 1] = q.y, yv.w[4 * c + 2] = q.z, yv.w[4 * c + 3] = q.w;
-                    }
-                    float v[W];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[j] = __fmaf_rn(acc[i >> 1][j >> 1][2 * (i & 1) + (j & 1)], f, yv[j]);
-                    store_out<O, W>(reinterpret_cast<O *>(orow[r0 + row] + at), W, true, v);
+                for (int j = 0; j < 4; ++j) {
+                    const int row = j * 8 + (lane >> 2);
+                    if (row0 + row < rows) *reinterpret_cast<uint4 *>(orow[row0 + row] + at) = lds16(y_stage(s) + y_place(row, lane & 3));
                 }
                 __syncwarp();  // the stage is read by all
-                copy(stage);
-                stage ^= 1;
             }
+            copy(i + 2);
         }
         copies_wait<0>();
+        return ok;
     }
 };
 
@@ -997,6 +1046,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
     const T *const B = has ? static_cast<const T *>(a.b) + (int64_t)ad * a.N * R : nullptr;
     const int w0 = rank * kWarps + warp, kk = C * kWarps;
+    uint32_t tmem = 0;
     if (BIG && tid < tile.count) y_row[tid] = reinterpret_cast<const char *>(static_cast<const O *>(a.y) + tile.toks[tid] * a.ys);
     if ((BIG || whole) && tid < tile.count) out_row[tid] = reinterpret_cast<char *>(static_cast<O *>(a.out) + tile.toks[tid] * a.os);
     const auto copy_first = [&] {
@@ -1012,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
         const T *const A = static_cast<const T *>(a.a) + ((int64_t)ad * a.ranks + a.rank0) * K;
         if constexpr (BIG) {
             const int chunks = (K + 63) / 64, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-            shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
+            tmem = shrink_big<T>(a, tile, sz, A, c0 * 64, min(K, c1 * 64), smem, part);
         } else {
             const int chunks = (K + 31) / 32, per = (chunks + C - 1) / C, c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
             float *const red = reinterpret_cast<float *>(smem + sz.red);
@@ -1095,10 +1145,10 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
                         z[j] = isfinite(to_f(h[j])) ? z[j] - to_f(h[j]) : 0.f;
                     }
                     const uint2 w = *reinterpret_cast<const uint2 *>(h);
-                    if constexpr (BIG) {  // in the order in which ldmatrix gives a thread ranks 4 t .. 4 t + 3
-                        T *const at = hs + (n * TM + row) * sz.hstride + (e >> 2) * 16 + (e & 3) * 2;
-                        *reinterpret_cast<uint32_t *>(at) = w.x;
-                        *reinterpret_cast<uint32_t *>(at + 8) = w.y;
+                    if constexpr (BIG) {
+                        const int sh = e / quads, k = sh % sz.hper * steps * 16 + (e - sh * quads) * 4;
+                        *reinterpret_cast<uint2 *>(smem + sz.split + (n * sz.htiles + sh / sz.hper) * 16384 + row * 128 +
+                                                   (((k >> 3) ^ (row & 7)) << 4) + (k & 4) * 2) = w;
                     } else {
                         *reinterpret_cast<uint2 *>(hs + (n * TM + place) * sz.hstride + e * 4) = w;
                     }
@@ -1108,32 +1158,33 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     }
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
-    if (BIG && C > 1) cl_wait_acquire();  // (the stages of y lie where the sums were)
-    {
-        // columns in blocks, dealt to the cluster's warps
-        constexpr int G = BIG ? 2 : 1, J = GATED ? 2 : 4;
-        bool done = false;
-        if constexpr (!BIG) {
-            if (whole) {
-                with_rank(R, [&](auto r) {
-                    ExpandSmall<T, O, GATED, decltype(r)::value>(a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk)
-                        .run(sz, hs, up, out_row);
-                });
-                done = true;
-            }
+    if constexpr (BIG) {
+        __shared__ uint64_t expanded[2];
+        if (C > 1) cl_wait_acquire();  // (the stages of B and y lie where the sums were)
+        if (tid == 0) {
+            mbar_init(&expanded[0], 1);
+            mbar_init(&expanded[1], 1);
+            fence_barrier_init();
         }
+        __syncthreads();
+        const ExpandBig<T, O> ex{a, sz, smem, B, y_row, out_row, tile.count, rank, lane, warp, steps};
+        const bool ok = ex.run(up, tmem, expanded);
+        if (!ok && lane == 0) atomicExch(a.status, kStatusTimeout);
+        tc::fence_before_sync();
+        __syncthreads();
+        if (has && warp == kWarps - 1) tc::tmem_dealloc(tmem, kTmemCols);
+    } else {
+        // columns in blocks, dealt to the cluster's warps
+        constexpr int J = GATED ? 2 : 4;
+        if (whole)
+            with_rank(R, [&](auto r) {
+                ExpandSmall<T, O, GATED, decltype(r)::value>(a, tile, B, smem_u32(smem + sz.blocks) + warp * 2 * L::stage(R), w0, kk)
+                    .run(sz, hs, up, out_row);
+            });
         int64_t skip = w0, off = a.col0;  // blocks before this warp's next one
-        for (int sh = 0; sh < (GATED ? 1 : S) && !done; ++sh) {
+        for (int sh = 0; sh < (GATED ? 1 : S) && !whole; ++sh) {
             const int64_t wide = a.shard[sh], blocks = (wide + J * 8 - 1) / (J * 8);
-            bool big = false;
-            if constexpr (BIG) {
-                using E = ExpandBig<T, O>;
-                big = a.vec_y && wide % 32 == 0;
-                if (big) E::run(a, tile.count, sz, hs, up, B, sh, off, (int)skip, kk, (int)blocks, smem_u32(smem) + warp * 2 * E::STAGE, y_row, out_row);
-            }
-            for (int64_t blk = skip; blk < blocks && !big; blk += kk)
-                for (int r0 = 0; r0 < tile.count; r0 += 16 * G)
-                    expand<T, O, TM, G, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk, r0);
+            for (int64_t blk = skip; blk < blocks; blk += kk) expand<T, O, GATED>(a, tile, sz, hs, up, B, sh, off, wide, blk);
             skip = skip >= blocks ? skip - blocks : kk - 1 - (blocks - 1 - skip) % kk;
             off += wide;
         }
