@@ -111,19 +111,20 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
     }
 }
 
-// Tiles of 128 tokens where tiles of 16 would read the adapters again and again: 100 MB of them or more, from 128 tokens an
-// adapter that can be there on average.  Rows of x and a start on 16 bytes; up to 64 ranks, held by the threads that
-// expand; the ranks of one launch's shards take up to 128 columns of tensor memory, and more shards are more launches.
-// Measured (us, tiles of 16 / 128; tokens x adapters, rank, 3584 to 3584 columns): 2048 x 2, 16: 26 / 31; 8192 x 64, 16: 75 /
-// 94; 8192 x 6, 16: 66 / 61; 2048 x 16, 32: 43 / 39; 8192 x 16, 32: 112 / 80; 2048 x 8, 64 (4096): 50 / 55; 8192 x 6, 64: 139 /
-// 90; from 18944 columns 296 / 131; rank 128 74 / 122.  Gated layers, whose columns are many, keep to tiles of 16:
-// 1024 x 4, 16, 2 x 18944: 75 against 143.
+// Tiles of 128 tokens where tiles of 16 would read the adapters again and again: from 32 ranks on, 2048 tokens and 120 an
+// adapter that can be there on average; below, 256 tokens an adapter and 70 MB of the adapters read again (B a quarter: the
+// expand gains least).  Rows and columns (eights) start on 16 bytes; up to 64 ranks, which h's tiles of shared memory
+// hold; the ranks of one launch's shards, each rounded up to 16, take up to 128 columns of tensor memory, and more shards
+// are more launches.  Measured (us, tiles of 16 / 128; tokens x adapters, 3584 to 3584 columns): rank 16, 2048 x 2: 24 / 28;
+// 4096 x 6: 34 / 35; 8192 x 32: 66 / 78; 8192 x 6: 60 / 51; 4096 x 4 to 18944: 76 / 87; from 18944: 84 / 56; rank 24, 4096 x 4: 46 /
+// 37; rank 32, 2048 x 16: 38 / 38; 8192 x 48: 102 / 88; 8192 x 16: 98 / 58; rank 64, 1024 x 4: 25 / 31; 2048 x 8: 48 / 46; 8192 x 6:
+// 137 / 60; from 18944: 340 / 103; to 18944, rank 32, 2048 x 4: 66 / 79.  Gated layers, whose columns are many, keep to tiles of 16.
 constexpr int kBigRanks = 128;
 bool big_tiles(const LoraArgs &a) {
     if (!a.vec_x || !a.vec_y || a.gated || a.R > 64) return false;
     const int64_t present = a.adapters + 1 < a.M ? a.adapters + 1 : a.M;
-    const double again = (double)a.M / 16 * a.R * 2 * ((double)a.S * a.K + a.N);
-    return a.M >= 128 * present && again >= 100e6;
+    if (a.R >= 32) return a.M >= 2048 && a.M >= 120 * present;
+    return a.M >= 256 * present && (double)a.M / 16 * a.R * 2 * ((double)a.S * a.K + (double)a.N / 4) >= 70e6;
 }
 
 int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {

@@ -179,6 +179,9 @@ __device__ __forceinline__ float cl_ld_f32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void cl_st_v2(uint32_t addr, uint2 v) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
 __device__ __forceinline__ float4 cl_ld_v4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
@@ -253,8 +256,8 @@ struct Smem {
         split = tm * pstride * 4;
         hper = big ? 4 / ((R + 15) / 16) : 1;
         htiles = (S + hper - 1) / hper;
-        if (big) {  // two stages of B and y, when the sums are joined; h begins on 1024 bytes
-            const int expand = 2 * 8192 + kWarps * 4096;
+        if (big) {  // four stages of B and two of y, when the sums are joined; h begins on 1024 bytes
+            const int expand = 4 * 8192 + kWarps * 4096;
             split = ((split > expand ? split : expand) + 1023) & ~1023;
         }
         blocks = split + (big ? ns * htiles * 16384 : ns * tm * hstride * 2);
@@ -855,8 +858,8 @@ __device__ __forceinline__ void with_rank(int R, F f) {
 
 // ---- expand, many tokens: blocks of 64 columns (32 of fp32) of a shard, dealt to the cluster's blocks; a shard's last may
 // be cut short (to eights that start on 16 bytes: the launcher's rule).  The split h (K-major, swizzled as the MMA reads it) times a block's rows of B on tcgen05,
-// into one of two accumulators while the other's columns are added to y.  B and y are copied two blocks of
-// columns ahead; a warp has 32 rows of half the columns, reads a row of its accumulator a thread, and goes through its
+// into one of two accumulators while the other's columns are added to y.  B is copied three blocks of columns ahead, y
+// two; a warp has 32 rows of half the columns, reads a row of its accumulator a thread, and goes through its
 // stage of y, so that global memory is read and written in 64-byte pieces of rows.  (Warp MMAs with B in registers: 33 us
 // where this takes LATER; they alone took 20.)  B null: y goes through as it is.
 template <typename T, typename O>
@@ -864,7 +867,7 @@ struct ExpandBig {
     static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int NS = kBf && sizeof(O) == 4 ? 3 : 2;
     static constexpr int COLS = 128 / sizeof(O), HALF = COLS / 2, W = 16 / sizeof(O);  // columns of a block, of a warp, of 16 bytes
-    static constexpr int B_STAGE = 8192, Y_STAGE = 2048;
+    static constexpr int B_STAGE = COLS * 128, B_STAGES = 4, Y_STAGE = 2048;
 
     const LoraArgs &a;
     const Smem &sz;
@@ -875,7 +878,7 @@ struct ExpandBig {
     const int count, rank, lane, warp, steps;
 
     __device__ __forceinline__ static uint32_t y_place(int row, int c) { return (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4)); }
-    __device__ __forceinline__ uint32_t y_stage(int s) const { return smem_u32(smem) + 2 * B_STAGE + (warp * 2 + s) * Y_STAGE; }
+    __device__ __forceinline__ uint32_t y_stage(int s) const { return smem_u32(smem) + B_STAGES * B_STAGE + (warp * 2 + s) * Y_STAGE; }
     // block n: its shard, first column and columns
     struct Place {
         int sh, col, left;
@@ -905,7 +908,6 @@ struct ExpandBig {
                 }
             }
         }
-        copies_commit();
     }
     __device__ __forceinline__ void copy_y(const Place &p, int s) const {
         const uint32_t at = y_column(p), to = y_stage(s);
@@ -915,7 +917,6 @@ struct ExpandBig {
             const int row = i * 8 + (lane >> 2), all = (warp & 3) * 32 + row;
             if (all < rows) copy16(to + y_place(row, lane & 3), yrow[all] + at, true);
         }
-        copies_commit();
     }
     // tm: tensor memory of two accumulators; done: their barriers.  False: a wait gave up (the results are NaN).
     __device__ __forceinline__ bool run(const float *up, uint32_t tm, uint64_t *done) const {
@@ -924,21 +925,17 @@ struct ExpandBig {
         const int C = a.C, n = rank < blocks ? (blocks - 1 - rank) / C + 1 : 0;
         const uint32_t idesc = tc::idesc_f16(COLS, kBf);
         bool ok = true;
-        const auto copy = [&](int i) {
-            if (i < n) {
-                const Place p = locate(rank + i * C);
-                copy_b(p, i & 1);
-                copy_y(p, i & 1);
-            } else {
-                copies_commit();
-                copies_commit();
-            }
+        const auto copy = [&](int i, bool b, bool y) {
+            if (i >= n) return;
+            const Place p = locate(rank + i * C);
+            if (b) copy_b(p, i % B_STAGES);
+            if (y) copy_y(p, i & 1);
         };
         const auto multiply = [&](int i) {
             const int sh = locate(rank + i * C).sh;
             tc::fence_after_sync();
             if (tc::elect_one()) {
-                const uint64_t bd = tc::desc_sw128(smem + (i & 1) * B_STAGE);
+                const uint64_t bd = tc::desc_sw128(smem + i % B_STAGES * B_STAGE);
                 for (int q = 0; q < NS; ++q) {
                     const uint64_t hd = tc::desc_sw128(smem + sz.split + (q * sz.htiles + sh / sz.hper) * 16384) + sh % sz.hper * steps * 2;
                     for (int z = 0; z < steps; ++z) tc::mma_ss(tm + (i & 1) * COLS, hd + z * 2, bd + z * 2, idesc, (q | z) != 0);
@@ -947,8 +944,16 @@ struct ExpandBig {
             }
             __syncwarp();
         };
-        copy(0);
-        copy(1);
+        // groups of copies, in the order in which they are waited for
+        copy(0, true, false);
+        copies_commit();
+        copy(1, true, false);
+        copy(0, false, true);
+        copies_commit();
+        copy(2, true, false);
+        copies_commit();
+        copy(1, false, true);
+        copies_commit();
         copies_wait<3>();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
@@ -956,7 +961,9 @@ struct ExpandBig {
         const int row0 = (warp & 3) * 32;
         for (int i = 0; i < n; ++i) {
             const int s = i & 1;
-            copies_wait<1>();  // the next block's B, and before it this one's y
+            copy(i + 3, true, false);
+            copies_commit();
+            copies_wait<3>();  // the next block's B and this one's y have landed
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc::fence_before_sync();
             __syncthreads();
@@ -997,7 +1004,8 @@ struct ExpandBig {
                 }
                 __syncwarp();  // the stage is read by all
             }
-            copy(i + 2);
+            copy(i + 2, false, true);
+            copies_commit();
         }
         copies_wait<0>();
         return ok;
@@ -1110,13 +1118,16 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
         }
         const int quads = steps * 4, row_quads = S * quads;
         constexpr int U = BIG ? 4 : 2;
-        for (int i0 = tid; i0 < tile.count * row_quads; i0 += U * kThreads) {
+        // BIG: a block joins a share of the rows and gives them to all; few tokens: every block joins all
+        const int per_block = BIG ? (tile.count + C - 1) / C : tile.count, row0 = BIG ? min(rank * per_block, tile.count) : 0;
+        const int rows_end = min(row0 + per_block, tile.count);
+        for (int i0 = tid; i0 < (rows_end - row0) * row_quads; i0 += U * kThreads) {
             float4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kThreads, row = i / row_quads, e = i - row * row_quads, sh = e / quads, r = (e - sh * quads) * 4;
+                const int i = i0 + u * kThreads, in = i / row_quads, row = row0 + in, e = i - in * row_quads, sh = e / quads, r = (e - sh * quads) * 4;
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row < tile.count && r < R) {
+                if (row < rows_end && r < R) {
                     const float *p = part + row * sz.pstride + sh * R + r;
                     if (C == 1) {
                         v[u] = *reinterpret_cast<const float4 *>(p);
@@ -1131,8 +1142,8 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kThreads, row = i / row_quads, e = i - row * row_quads;
-                if (row >= tile.count) continue;
+                const int i = i0 + u * kThreads, in = i / row_quads, row = row0 + in, e = i - in * row_quads;
+                if (row >= rows_end) continue;
                 const float f = kBf ? 1.f : 1.f / up[row];  // (a power of two)
                 const int place = whole ? L::h_row(row) : row;
                 float z[4] = {v[u].x * s * f, v[u].y * s * f, v[u].z * s * f, v[u].w * s * f};
@@ -1147,8 +1158,11 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
                     const uint2 w = *reinterpret_cast<const uint2 *>(h);
                     if constexpr (BIG) {
                         const int sh = e / quads, k = sh % sz.hper * steps * 16 + (e - sh * quads) * 4;
-                        *reinterpret_cast<uint2 *>(smem + sz.split + (n * sz.htiles + sh / sz.hper) * 16384 + row * 128 +
-                                                   (((k >> 3) ^ (row & 7)) << 4) + (k & 4) * 2) = w;
+                        unsigned char *const at = smem + sz.split + (n * sz.htiles + sh / sz.hper) * 16384 + row * 128 +
+                                                  (((k >> 3) ^ (row & 7)) << 4) + (k & 4) * 2;
+                        if (C == 1) *reinterpret_cast<uint2 *>(at) = w;
+                        else
+                            for (int c = 0; c < C; ++c) cl_st_v2(cl_map(smem_u32(at), c), w);
                     } else {
                         *reinterpret_cast<uint2 *>(hs + (n * TM + place) * sz.hstride + e * 4) = w;
                     }
@@ -1156,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
             }
         }
     }
+    if (BIG) asm volatile("fence.proxy.async;" ::: "memory");  // (h, of any block of the cluster, is read by MMAs)
     __syncthreads();
     if (C > 1) cl_arrive_release();  // the others' sums are read
     if constexpr (BIG) {
