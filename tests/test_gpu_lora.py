@@ -233,3 +233,41 @@ def test_after_the_shared_layer():
     keep = y.clone()
     tl.lora_add(x, ad, which, y, out=y)
     close(y, *exact(x, keep, a, b, s, which, shards))
+
+
+MANY = [  # tokens, inputs, shards, rank, adapters: tiles of 128 tokens, from one block a tile to eight, columns cut short
+    (2048, 520, (264, 96, 104), 64, 3), (2304, 328, (72,), 40, 4), (2048, 17408, (40, 16), 8, 2), (1300, 6800, (64, 8, 72, 136), 16, 4),
+    (2100, 264, (128, 40, 0, 24), 48, 5), (5000, 72, (200,), 32, 6), (9000, 72, (72,), 56, 5), (16000, 40, (136, 8), 32, 4), (20000, 40, (72,), 32, 4),
+    (2048, 8, (8,), 32, 1), (3000, 3000, (1000,), 64, 24)]
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torch.bfloat16, torch.float32),
+                                             (torch.float16, torch.float32)])
+@pytest.mark.parametrize("tokens,inputs,shards,rank,n", MANY)
+def test_many_tokens(tokens, inputs, shards, rank, n, dtype, out_dtype):
+    x, y, a, b, s, which = make(tokens, inputs, shards, rank, n, dtype, out_dtype, seed=tokens + rank)
+    ad = tl.Adapters(a, b, s, shards=shards)
+    z, off = exact(x, y, a, b, s, which, shards)
+    got = tl.lora_add(x, ad, which, y)
+    close(got, z, off)
+    assert torch.equal(got[which < 0], y[which < 0])
+    wide = torch.full((tokens, y.shape[1] + 24), 3.0, dtype=out_dtype, device=DEV)  # rows of a larger tensor, in place
+    part = wide[:, 8:-16]
+    part.copy_(y)
+    tl.lora_add(x, ad, which, part, out=part)
+    assert torch.equal(part, got) and bool((wide[:, :8] == 3).all()) and bool((wide[:, -16:] == 3).all())
+
+
+def test_values_that_are_no_numbers_stay_in_their_rows_of_large_tiles():
+    tokens, k = 2304, 264
+    x, y, a, b, s, which = make(tokens, k, (136,), 40, 3, torch.float16, torch.float16, seed=33)
+    clean = tl.lora_add(x, tl.Adapters(a, b, s), which, y)
+    x[7, 3], x[300, 5], y[11, 4] = float("inf"), float("nan"), float("nan")
+    got = tl.lora_add(x, tl.Adapters(a, b, s), which, y)
+    odd = torch.zeros(tokens, dtype=torch.bool, device=DEV)
+    odd[7], odd[300], odd[11] = True, True, True
+    assert torch.equal(got[~odd], clean[~odd])
+    for row in (7, 300):
+        if int(which[row]) >= 0:
+            assert not torch.isfinite(got[row]).all()
+    assert torch.isnan(got[11, 4]) and torch.equal(got[11, 5:], clean[11, 5:])
