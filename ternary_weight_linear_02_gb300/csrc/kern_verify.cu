@@ -243,7 +243,7 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 // all first, sums are exchanged through distributed shared memory.
 // Bound by latency: the gather (two dependent loads), a pass, the cluster's barrier, the drawing.  One chain of 4 over
 // 32000 tokens 9.2 us (launch and gather 2, pass 3, exchange 1.6, drawing 2), 64 chains over 131072 tokens 22 us
-// (67 MB: 9.9 at a copy's rate; the pass takes 10), 24 trees of 31 over 50021 tokens 42 us (the longest has
+// (67 MB: 9.9 at a copy's rate; the pass takes 10), 24 trees of 31 over 50021 tokens 41 us (the longest has
 // ten rejections, one pass each).
 // fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
 // warp takes the SM's unit 16 cycles.
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
         int todo;  // 0: a pass over p, 1: over p and q, 2: done
         int node, count, gone, next;
         double A, W;
+        Pair a;  // A (made once: fp64 in every warp would hold the pass up)
     } st;
     __shared__ struct {
         int empty, owner, run;  // nothing to draw from; block and warp's run that the number falls in
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
                         for (int j = 0; j < ngone; ++j)
                             if (gone[j] == x) p = 0.;
                     }
-                    yes = (double)un[i] * (W * (double)qx[i]) < p;
+                    yes = W * ((double)un[i] * (double)qx[i]) < p;  // (the product of two fp32 is exact)
                 }
                 if (yes) {
                     if (lane == 0) path[count] = i;
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
                 st.next = i;
                 st.A = A;
                 st.W = W;
+                if (todo == 1) st.a = pair_of(A);
                 st.todo = todo == 2 && A == 0. ? 0 : todo;
             }
         }
@@ -443,9 +445,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
         if (todo == 2) break;  // (w and its sums are those of the pass before)
         w.p = target + (int64_t)st.node * a.target_n;
         w.q = todo == 1 ? draft + (int64_t)st.node * a.draft_n : nullptr;
-        const Pair A = pair_of(st.A);
-        w.ah = A.hi;
-        w.al = A.lo;
+        w.ah = st.a.hi;
+        w.al = st.a.lo;
         w.gone = st.gone;
         w.keep = todo == 0 || !a.keep ? 0 : kept_node == st.node ? 2 : 1;
         if (w.keep) kept_node = st.node;
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
 
 template <typename T, bool VEC>
 cudaError_t launch_one(const VerifyArgs &a, int sm_count, cudaStream_t st) {
-    // Rows kept by the threads: only a tree looks at a node's rows more than once (24 trees of 31 over 50021 tokens 41.7 us,
+    // Rows kept by the threads: only a tree looks at a node's rows more than once (24 trees of 31 over 50021 tokens 40.6 us,
     // 58.6 without), and only where the batch fits the SMs beside them.
     constexpr int kMost = 96 * 1024, kFixed = 31 * 1024, kSm = 227 * 1024;
     const int64_t per = (((a.V + (int64_t)a.blocks - 1) / a.blocks) + 255) & ~(int64_t)255, run = (((per + kWarps - 1) / kWarps) + 7) & ~(int64_t)7;
