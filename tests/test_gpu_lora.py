@@ -271,3 +271,20 @@ def test_values_that_are_no_numbers_stay_in_their_rows_of_large_tiles():
         if int(which[row]) >= 0:
             assert not torch.isfinite(got[row]).all()
     assert torch.isnan(got[11, 4]) and torch.equal(got[11, 5:], clean[11, 5:])
+
+
+@pytest.mark.parametrize("share", [0.0, 0.1, 0.45, 0.55, 0.95, 1.0])
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+def test_tokens_without_an_adapter_among_many(share, out_dtype):
+    """From none of them to all: their rows are copied, beside the others' or by themselves, or left as they are."""
+    tokens, shards = 3100, (136, 48)
+    x, y, a, b, s, which = make(tokens, 72, shards, 48, 3, torch.float16, out_dtype, seed=77)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    which = torch.randint(0, 3, (tokens,), generator=gen, device=DEV).int()
+    which[torch.rand(tokens, generator=gen, device=DEV) < share] = -1
+    ad = tl.Adapters(a, b, s, shards=shards)
+    got = tl.lora_add(x, ad, which, y, out=torch.full_like(y, float("nan")))
+    close(got, *exact(x, y, a, b, s, which, shards))
+    assert torch.equal(got[which < 0], y[which < 0])
+    tl.lora_add(x, ad, which, y, out=y)
+    assert torch.equal(y, got)
