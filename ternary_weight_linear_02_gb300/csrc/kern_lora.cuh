@@ -6,20 +6,20 @@
 // One launch.  Work is dealt in tiles of up to TM tokens of one adapter, a cluster of C blocks a tile:
 //   * shrink: each block takes a run of K and keeps h's partial sums (TM x S R) in shared
 //     memory; they are added over the cluster in a fixed order through distributed
-//     shared memory, by every block for itself;
+//     shared memory;
 //   * expand: each block takes a share of the output columns, adds h B^T to y and writes.
 // So x and y are read once and out is written once, A and B once per tile.  Two forms:
 //   * few tokens an adapter: tiles of 16, the adapter's matrices are the traffic.  Warp MMAs fed
 //     straight from global memory (an MMA sums over k: any order of k will do that both operands
 //     share, so every lane loads 16 contiguous bytes);
 //   * many: tiles of 128, the activations are the traffic.  Rows of x and A go through a ring of shared-memory
-//     stages (16-byte copies, whatever the tokens' order) into tcgen05 MMAs, h lies in tensor memory.
+//     stages (16-byte copies, whatever the tokens' order) into tcgen05 MMAs, and so do the split h and B.
 // Either way there are 0.7 R operations a byte: memory should bound it.  Measured: 16 tokens of 8 adapters, rank 16,
-// fused QKV of 3584: 9.6 us (finding the tile 0.9, shrink 2.8, sums 1.6, expand 1.7); 333 tokens of 40 adapters,
-// rank 16, gated layer of 2 x 18944: 41 us, 98 MB, 14.4 at a copy's rate: bound by instructions (57 % of
-// the issue slots), the gated product's before all; 8192 tokens of 6 adapters, rank 64, 18944 to 3584, f16: 132 us,
-// 445 MB, 65.6 at a copy's rate: the plan 6, shrink 53 (5.9 TB/s), sums 10, expand 27 to 45, where warp
-// MMAs (12 thousand an SM, 2.9 cycles each) take 18.
+// fused QKV of 3584: 7.9 us (finding the tile 0.9, shrink 2.2, sums 1.5, expand 1.3); 333 tokens of 40 adapters,
+// rank 16, gated layer of 2 x 18944: 30 us, 98 MB, 14.4 at a copy's rate: finding the tile 2.6, shrink 6 (a burst
+// of 12 MB), sums 3, expand 10 (where three blocks share an SM 15); 8192 tokens of 6 adapters, rank 64,
+// 18944 to 3584, f16: 103 us, 445 MB, 65.6 at a copy's rate: the plan 6, shrink 52 (6.5 TB/s), sums 8, expand 19 to 28
+// (where two blocks share an SM).
 //
 // h enters the second product in 16 bits.  One rounding there would add as much error as that of a 16-bit
 // output, so h is split into two numbers of T (three where bf16 feeds an fp32 output), each the
@@ -244,7 +244,7 @@ struct Smem {
     int split;        // where the split h begins
     int blocks, red;  // small: where the stages of B and y, and the warps' sums begin
     int total;
-    // stage: bytes of a stage of expand_small (0: not used)
+    // small_stage: bytes of a stage of ExpandSmall (0: not used)
     __host__ __device__ Smem(bool big, bool gated, int S, int R, int ns, int small_stage) {
         const int tm = big ? 128 : 16;
         ranks = S * R;
@@ -860,8 +860,9 @@ __device__ __forceinline__ void with_rank(int R, F f) {
 // be cut short (to eights that start on 16 bytes: the launcher's rule).  The split h (K-major, swizzled as the MMA reads it) times a block's rows of B on tcgen05,
 // into one of two accumulators while the other's columns are added to y.  B is copied three blocks of columns ahead, y
 // two; a warp has 32 rows of half the columns, reads a row of its accumulator a thread, and goes through its
-// stage of y, so that global memory is read and written in 64-byte pieces of rows.  (Warp MMAs with B in registers: 33 us
-// where this takes LATER; they alone took 20.)  B null: y goes through as it is.
+// stage of y, so that global memory is read and written in 64-byte pieces of rows.  8192 tokens of 6 adapters, 18944 to 3584:
+// 103 us; by warp MMAs with B in registers 119 (their rate alone 20).  Stores hold it up most (12 us, the products 6, y 3).
+// B null: y goes through as it is.
 template <typename T, typename O>
 struct ExpandBig {
     static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -1048,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     }
     const int S = a.S, R = a.R, K = (int)a.K, steps = (R + 15) / 16;
     using L = Blocks<O, GATED>;
-    const bool whole = !BIG && a.whole;  // blocks of columns for expand_small
+    const bool whole = !BIG && a.whole;  // blocks of columns for ExpandSmall
     const Smem sz(BIG, GATED, S, R, NS, whole ? L::stage(R) : 0);
     float *const part = reinterpret_cast<float *>(smem);
     T *const hs = reinterpret_cast<T *>(smem + sz.split);
