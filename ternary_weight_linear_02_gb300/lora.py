@@ -113,7 +113,7 @@ def _call(name: str, x, adapters: Adapters, which, y, out, cols: int):
     if not which.is_contiguous():
         which = which.contiguous()
     if out is None:
-        o = out = torch.empty((*lead, cols), dtype=kind, device=dev)
+        o = out = torch.empty_like(y, memory_format=torch.contiguous_format) if cols == n else y.new_empty((*lead, cols))
         os = cols
         if len(lead) != 1:
             o = out.view(-1, cols)

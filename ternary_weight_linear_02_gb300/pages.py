@@ -150,8 +150,8 @@ def pages_reserve(pages: KVPages, extra: torch.Tensor, width: int) -> tuple[torc
         raise ValueError("width must be 0 or more, in 32 bits")
     dev = pages.device
     extra = _index(extra, "extra", torch.int32, pages.rows, dev)
-    slots = torch.empty((pages.rows, int(width)), dtype=torch.int64, device=dev)
-    ok = torch.empty(pages.rows, dtype=torch.bool, device=dev)
+    slots = extra.new_empty((pages.rows, int(width)), dtype=torch.int64)
+    ok = torch.empty_like(extra, dtype=torch.bool)
     rc = _launch(dev, (_ready or _lib()).ternary_pages_reserve, pages._ref, extra.data_ptr(), slots.data_ptr(), int(width),
                  ok.data_ptr())
     if rc:
@@ -176,8 +176,8 @@ def pages_fork(pages: KVPages, parent: torch.Tensor, layers=None) -> torch.Tenso
         array, n = layers._array, layers.count
     lib = _ready or _lib()
     need = 16 + 32 * pages.rows   # ternary_pages_fork_workspace
-    ok = torch.empty(pages.rows, dtype=torch.bool, device=dev)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ok = torch.empty_like(parent, dtype=torch.bool)
+    ws = parent.new_empty(need, dtype=torch.uint8)
     rc = _launch(dev, lib.ternary_pages_fork, pages._ref, parent.data_ptr(), array, n, ok.data_ptr(), ws.data_ptr(), need)
     if rc:
         _check(rc, "ternary_pages_fork")
