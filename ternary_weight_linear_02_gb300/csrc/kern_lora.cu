@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
     const int keys = a.adapters + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *const cursor = sh, *const first = sh + keys + 1, *const tile = first + keys + 1;
     pdl_launch_dependents();
+    pdl_wait();
     int key[N];
     uint32_t same[N];
     const auto look = [&](int64_t t0, bool report) {
@@ -157,12 +158,10 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
     if (lora_workspace(a.M, a.adapters) > 0) {
         a.max_tiles = units;
         int *const plan = static_cast<int *>(workspace);
-        lora_plan_kernel<<<1, 1024, 3 * (a.adapters + 2) * sizeof(int), st>>>(a, TM, plan);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_chained(lora_plan_kernel, 1, 1024, 3 * (a.adapters + 2) * sizeof(int), 0, st, a, TM, plan);
         if (e != cudaSuccess) return e;
         a.plan = plan;
     }
-    a.overlap = 1;
     const int shards = a.S, most_shards = kBigRanks / ((a.R + 15) / 16 * 16),
               at_once = big && most_shards < shards ? most_shards : shards;
     for (int s0 = 0; s0 < shards; s0 += at_once) {
@@ -171,7 +170,6 @@ cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspa
         b.rank0 = s0 * a.R;
         for (int i = 0; i < s0; ++i) b.col0 += a.shard[i];
         for (int i = 0; i < b.S; ++i) b.shard[i] = a.shard[s0 + i];
-        b.overlap = s0 == 0;
         const cudaError_t e = dtype == 1 ? launch_lora_bf16(b, f32, big, units, st) : launch_lora_f16(b, f32, big, units, st);
         if (e != cudaSuccess) return e;
     }

@@ -284,7 +284,6 @@ template <int TM>
 __device__ __forceinline__ bool find_tile(const LoraArgs &a, Tile<TM> &tile, int unit, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.plan != nullptr) {
-        pdl_wait();
         if (unit >= min(a.plan[0], a.max_tiles)) return false;
         const int *p = a.plan + 4 + 3 * unit;
         // (the bounds hold unless the workspace is written meanwhile)
@@ -1032,6 +1031,9 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 2) lora_kernel(const __g
     const int C = a.C, rank = (int)(blockIdx.x % (unsigned)C);
     const int unit = (int)(blockIdx.x / (unsigned)C);
     if (C > 1) cluster_arrive_relaxed();
+    // (tiles of 128 hold tensor memory: a kernel that came early might take it first and wait for this one)
+    if (!BIG) pdl_launch_dependents();
+    pdl_wait();
     const bool any = find_tile<TM>(a, tile, unit, unit == 0 && rank == 0);
     const int ad = any ? tile.adapter : a.adapters;
     const bool has = ad < a.adapters;
@@ -1224,25 +1226,7 @@ cudaError_t launch_one(const LoraArgs &a, int units, cudaStream_t st) {
     }
     static std::atomic<uint64_t> done{0};
     if (const cudaError_t e = allow_smem(done, lora_kernel<T, O, BIG, GATED>, kMaxSmem)) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)units * (unsigned)a.C);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = sz.total;
-    c.stream = st;
-    cudaLaunchAttribute at[2];
-    int n = 0;
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = (unsigned)a.C;
-    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-    ++n;
-    if (a.plan && a.overlap) {
-        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
-    c.attrs = at;
-    c.numAttrs = n;
-    return cudaLaunchKernelEx(&c, lora_kernel<T, O, BIG, GATED>, b);
+    return launch_chained(lora_kernel<T, O, BIG, GATED>, (unsigned)units * (unsigned)a.C, kThreads, sz.total, (unsigned)a.C, st, b);
 }
 
 template <typename T>

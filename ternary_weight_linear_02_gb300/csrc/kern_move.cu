@@ -55,6 +55,8 @@ __device__ __forceinline__ void copy_head(const KvMove &m, uint32_t task, int sr
 
 __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ KvMove m, const int *src, const int *dst, const int *tokens,
                                                       uint32_t n) {
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u, total = n * per;
     for (uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5); u < total; u += gridDim.x * 8u) {
         const uint32_t i = u / per;
@@ -72,6 +74,7 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ Kv
 // places in use of their last pages.  A warp a task.
 __global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__ KvMove m, KvPages g, const int *listed,
                                                          const ForkItem *items, uint32_t runs) {
+    pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u + runs;
@@ -172,6 +175,8 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
     constexpr int ROWS = 32 / PIECES, PASSES = 16 / ROWS;  // rows a pass of the warp
     const int lane = threadIdx.x & 31;
     const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    pdl_launch_dependents();
+    pdl_wait();
     if (u >= units) return;
     const uint32_t per = (uint32_t)(m.L * m.Hk);
     const int64_t b = u / per;
@@ -251,6 +256,8 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
     const uint32_t per = (uint32_t)(m.L * m.Hk) * 2u, tid = threadIdx.x;
     const int lane = tid & 31, w0 = (int)(tid >> 5) * WARP;
     const int64_t u = blockIdx.x, b = u / per;
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t rest = (uint32_t)(u - b * per), lh = rest >> 1, layer = lh / (uint32_t)m.Hk;
     const uint32_t head = (lh - layer * (uint32_t)m.Hk) * (uint32_t)m.P;
     const Moves mv(m, a, b);
@@ -367,9 +374,8 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaS
         c.start += b0;
         c.count += b0;
         const int64_t units = c.batch * per;
-        if (!blocks) compact_warp_kernel<PIECES><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(m, c, units);
-        else compact_block_kernel<PIECES><<<(unsigned)(units * 2), kMovers, bytes, st>>>(m, c);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = blocks ? launch_chained(compact_block_kernel<PIECES>, (unsigned)(units * 2), kMovers, bytes, 0, st, m, c)
+                                     : launch_chained(compact_warp_kernel<PIECES>, (unsigned)((units + 7) / 8), 256, 0, 0, st, m, c, units);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -381,8 +387,8 @@ cudaError_t launch_kv_copy(const KvMove &m, const int *src, const int *dst, cons
     const int64_t per = (int64_t)m.L * m.Hk * 2, chunk = ((int64_t)1 << 31) / per;  // copies of a launch: tasks fit 32 bits
     for (int64_t i0 = 0; i0 < n; i0 += chunk) {
         const int64_t c = n - i0 < chunk ? n - i0 : chunk, blocks = (c * per + 7) / 8, most = (int64_t)sm_count * 8;
-        kv_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(m, src + i0, dst + i0, tokens ? tokens + i0 : nullptr, (uint32_t)c);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_chained(kv_copy_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, 0, st, m, src + i0, dst + i0,
+                                             tokens ? tokens + i0 : nullptr, (uint32_t)c);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -392,16 +398,8 @@ cudaError_t launch_fork_apply(const KvMove &m, const KvPages &g, const int *list
                               cudaStream_t st) {
     const int64_t runs = share ? (g.max_pages + 255) / 256 : 0, blocks = (g.rows * ((int64_t)m.L * m.Hk * 2 + runs) + 7) / 8,
                   most = (int64_t)sm_count * 8;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(blocks < most ? blocks > 0 ? blocks : 1 : most));
-    c.blockDim = dim3(256);
-    c.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, fork_apply_kernel, m, g, listed, items, (uint32_t)runs);
+    return launch_chained(fork_apply_kernel, (unsigned)(blocks < most ? blocks > 0 ? blocks : 1 : most), 256, 0, 0, st, m, g, listed, items,
+                          (uint32_t)runs);
 }
 
 cudaError_t launch_kv_compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaStream_t st) {

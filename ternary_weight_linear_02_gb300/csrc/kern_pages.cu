@@ -19,6 +19,8 @@ constexpr int kListed = 4096;  // free pages that a block lists at a time
 // One warp per row: the pages behind the kept ones.  Three dependent trips to memory: 3 us for 1021 rows.
 __global__ void __launch_bounds__(256) pages_free_kernel(KvPages g, const int *keep, int *status) {
     const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
     if (r >= g.rows) return;
     const int n = keep[r], held = g.held[r];
     if (n < 0) return;
@@ -137,7 +139,8 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
     const int C = gridDim.x, rank = blockIdx.x;
     int *const place = reinterpret_cast<int *>(cum) + g.rows, *const tokens = place + g.rows;
     if (C > 1) cluster_arrive_relaxed();
-    if (FORK) pdl_launch_dependents();
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t batch = threads * 32, per = (g.pages + C * 1024 - 1) / (C * 1024) * 1024;
     const int64_t lo = rank * per, hi = min(lo + per, g.pages);
     uint32_t words = 0, free_here = 0;
@@ -281,8 +284,7 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
 }  // namespace
 
 cudaError_t launch_pages_free(const KvPages &g, const int *keep, int *status, cudaStream_t st) {
-    pages_free_kernel<<<(g.rows + 7) / 8, 256, 0, st>>>(g, keep, status);
-    return cudaGetLastError();
+    return launch_chained(pages_free_kernel, (unsigned)(g.rows + 7) / 8, 256, 0, 0, st, g, keep, status);
 }
 
 cudaError_t launch_pages_take(const PagesTakeArgs &a, bool fork, cudaStream_t st) {
@@ -296,18 +298,7 @@ cudaError_t launch_pages_take(const PagesTakeArgs &a, bool fork, cudaStream_t st
     const auto kernel = fork ? pages_take_kernel<true> : pages_take_kernel<false>;
     if (bytes > 32 * 1024)
         if (const cudaError_t e = allow_smem(done[fork], kernel, kMaxPageRows * 12)) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(C);
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = bytes;
-    c.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, a);
+    return launch_chained(kernel, (unsigned)C, (unsigned)threads, (size_t)bytes, (unsigned)C, st, a);
 }
 
 }  // namespace tl

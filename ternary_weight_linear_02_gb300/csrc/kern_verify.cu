@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
     const T *target = static_cast<const T *>(a.target) + b * a.target_b;
     const T *draft = a.draft ? static_cast<const T *>(a.draft) + b * a.draft_b : nullptr;
     if (C > 1) cluster_arrive_relaxed();
+    pdl_launch_dependents();
+    pdl_wait();
     // entry i is looked up by one block and given to all (a thread for each of them): whatever happens to the inputs
     // meanwhile, all blocks take the same decisions and meet at the same barriers
     for (int e0 = 0; e0 * C + rank <= n; e0 += kThreads / C) {
@@ -563,18 +565,7 @@ cudaError_t launch_one(const VerifyArgs &a, int sm_count, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     if (b.keep)
         if (const cudaError_t e = allow_smem(done, kernel, kMost)) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(a.B * a.blocks));
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = b.keep ? (size_t)bytes : 0;
-    c.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.blocks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, b);
+    return launch_chained(kernel, (unsigned)(a.B * a.blocks), kThreads, b.keep ? (size_t)bytes : 0, (unsigned)a.blocks, st, b);
 }
 
 template <typename T>

@@ -371,7 +371,6 @@ struct LoraArgs {
     int C;                    // blocks of a cluster
     const int *plan;          // tiles found beforehand (null: by each block)
     int max_tiles;
-    int overlap;              // the launch before is the plan's
     int stall;                // testing aid (CallDevice)
     long long wait_limit;
     int *status;

@@ -22,4 +22,25 @@ cudaError_t allow_smem(std::atomic<uint64_t> &done, K *kernel, int bytes) {
     return e;
 }
 
+// A launch that may begin while the kernel before it in the stream ends: the kernel calls pdl_wait() before it touches
+// anything.  cluster: blocks of a cluster (0: none).
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
+                           const A &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 }  // namespace tl
