@@ -15,7 +15,7 @@
 //   * many: tiles of 128, the activations are the traffic.  Rows of x and A go through a ring of shared-memory
 //     stages (16-byte copies, whatever the tokens' order) into tcgen05 MMAs, and so do the split h and B.
 // Either way there are 0.7 R operations a byte: memory should bound it.  Measured: 16 tokens of 8 adapters, rank 16,
-// fused QKV of 3584: 7.9 us (finding the tile 0.9, shrink 2.2, sums 1.5, expand 1.3); 333 tokens of 40 adapters,
+// fused QKV of 3584: 7.4 us (finding the tile 0.9, shrink 2.2, sums 1.5, expand 1.3); 333 tokens of 40 adapters,
 // rank 16, gated layer of 2 x 18944: 30 us, 98 MB, 14.4 at a copy's rate: finding the tile 2.6, shrink 6 (a burst
 // of 12 MB), sums 3, expand 10 (where three blocks share an SM 15); 8192 tokens of 6 adapters, rank 64,
 // 18944 to 3584, f16: 103 us, 445 MB, 65.6 at a copy's rate: the plan 6, shrink 52 (6.5 TB/s), sums 8, expand 19 to 28

@@ -168,7 +168,7 @@ struct Moves {
 };
 
 // Few moves a sequence: a warp per (sequence, layer, head), 16 moves at a time, keys and values
-// together.  PIECES: 16-byte pieces of a row of codes.  The accepted paths of 64 trees in 28 layers: 5.8 us (2.5 at a
+// together.  PIECES: 16-byte pieces of a row of codes.  The accepted paths of 64 trees in 28 layers: 5.5 us (2.5 at a
 // copy's rate): one wave of four dependent trips to memory.
 template <int PIECES>
 __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant__ KvMove m, KvCompactArgs a, int64_t units) {

@@ -242,7 +242,7 @@ __device__ __forceinline__ void weights_at(const Weights<T> &w, int v0, int v1, 
 // of them.  Every block follows the accepted path by itself: the entries that it turns on are gathered and given to
 // all first, sums are exchanged through distributed shared memory.
 // Bound by latency: the gather (two dependent loads), a pass, the cluster's barrier, the drawing.  One chain of 4 over
-// 32000 tokens 9.2 us (launch and gather 2, pass 3, exchange 1.6, drawing 2), 64 chains over 131072 tokens 22 us
+// 32000 tokens 9.0 us (launch and gather 2, pass 3, exchange 1.6, drawing 2), 64 chains over 131072 tokens 22 us
 // (67 MB: 9.9 at a copy's rate; the pass takes 10), 24 trees of 31 over 50021 tokens 41 us (the longest has
 // ten rejections, one pass each).
 // fp64 is left to one warp, and to one step per drafted token: at its rate here each operation of a
