@@ -120,12 +120,17 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
 // 4096 x 6: 34 / 35; 8192 x 32: 66 / 78; 8192 x 6: 60 / 51; 4096 x 4 to 18944: 76 / 87; from 18944: 84 / 56; rank 24, 4096 x 4: 46 /
 // 37; rank 32, 2048 x 16: 38 / 38; 8192 x 48: 102 / 88; 8192 x 16: 98 / 58; rank 64, 1024 x 4: 25 / 31; 2048 x 8: 48 / 46; 8192 x 6:
 // 137 / 60; from 18944: 340 / 103; to 18944, rank 32, 2048 x 4: 66 / 79.  Gated layers, whose columns are many, keep to tiles of 16.
+// fp32 outputs, whose blocks of columns are half as wide: 256 tokens an adapter and 110 MB of A read again.  Rank 16, 8192 x 6:
+// 94 / 102; from 18944: 232 / 167; rank 32, 2048 x 4: 43 / 56; 8192 x 16: 118 / 109; rank 48, 4096 x 4: 65 / 81; rank 64, 2048 x 8:
+// 55 / 70; 8192 x 6: 157 / 116; from 18944: 362 / 181.
 constexpr int kBigRanks = 128;
-bool big_tiles(const LoraArgs &a) {
+bool big_tiles(const LoraArgs &a, bool f32) {
     if (!a.vec_x || !a.vec_y || a.gated || a.R > 64) return false;
     const int64_t present = a.adapters + 1 < a.M ? a.adapters + 1 : a.M;
+    const double ranks = (double)a.M / 16 * a.R * 2, again = ranks * a.S * a.K;
+    if (f32) return a.M >= 256 * present && again >= 110e6;
     if (a.R >= 32) return a.M >= 2048 && a.M >= 120 * present;
-    return a.M >= 256 * present && (double)a.M / 16 * a.R * 2 * ((double)a.S * a.K + (double)a.N / 4) >= 70e6;
+    return a.M >= 256 * present && again + ranks * a.N / 4 >= 70e6;
 }
 
 int64_t tiles_bound(int64_t M, int64_t adapters, int TM) {
@@ -142,7 +147,7 @@ int64_t lora_workspace(int64_t M, int64_t adapters) {
 
 cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st) {
     LoraArgs a = args;
-    const bool big = big_tiles(a);
+    const bool big = big_tiles(a, f32);
     const int TM = big ? 128 : 16;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
     // Blocks a tile: 8, 6, 4, 2 or 1, as many as make two blocks an SM (gated, where three fit: 2.7) of the tiles that tokens

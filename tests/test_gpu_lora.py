@@ -238,7 +238,7 @@ def test_after_the_shared_layer():
 MANY = [  # tokens, inputs, shards, rank, adapters: tiles of 128 tokens, from one block a tile to eight, columns cut short
     (2048, 520, (264, 96, 104), 64, 3), (2304, 328, (72,), 40, 4), (2048, 17408, (40, 16), 8, 2), (1300, 6800, (64, 8, 72, 136), 16, 4),
     (2100, 264, (128, 40, 0, 24), 48, 5), (5000, 72, (200,), 32, 6), (9000, 72, (72,), 56, 5), (16000, 40, (136, 8), 32, 4), (20000, 40, (72,), 32, 4),
-    (2048, 8, (8,), 32, 1), (3000, 3000, (1000,), 64, 24)]
+    (2048, 8, (8,), 32, 1), (3000, 3000, (1000,), 64, 24), (2300, 30000, (104, 72), 64, 3)]
 
 
 @pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torch.bfloat16, torch.float32),
