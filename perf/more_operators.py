@@ -228,10 +228,8 @@ def prepare(case, seed):
         s["refs"] = torch.bincount(table[used].long(), minlength=pages).int()
         s["lens"] = torch.tensor(lens, dtype=torch.int32, device=DEV)
         keep = s["lens"] - torch.randint(0, width + 1, (rows,), generator=gen, device=DEV).int()
-        least = torch.zeros_like(keep)
-        least[odd] = least[odd - 1] = both * page  # no row is cut inside a page that another one holds too
         what = torch.rand(rows, generator=gen, device=DEV)
-        keep = torch.where(what < 0.05, torch.zeros_like(keep), torch.maximum(keep, least))  # an answer that has ended
+        keep = torch.where(what < 0.05, torch.zeros_like(keep), keep.clamp(min=0))  # an answer that has ended
         s["keep"] = torch.where(what > 0.95, torch.full_like(keep, -1), keep)  # a row that this step leaves alone
         s["extra"] = torch.randint(0, width + 1, (rows,), generator=gen, device=DEV).int()
         return s
