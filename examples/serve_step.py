@@ -47,21 +47,24 @@ class Server:
         return (vs.norm(x) @ self.head.T).float().softmax(-1)
 
     def prompt(self, row, tokens):
-        """Writes a prompt into a row and draws the token after it."""
+        """Writes a prompt into a row and draws the token after it.  Returns ok, on the device: False where it found no pages
+        (the row stays as it is)."""
         n = tokens.shape[0]
         extra = torch.full((self.rows,), -1, dtype=torch.int32, device=tokens.device)
         extra[row] = n
-        slots, _ = tl.pages_reserve(self.pages, extra, n)
+        slots, ok = tl.pages_reserve(self.pages, extra, n)
         ctx = self.pages.lens[row:row + 1]
         x = self.stack.step(self.embed[tokens][None], torch.arange(n, device=tokens.device), slots[row], self.pages.table[row:row + 1], ctx,
                             adapters=self.adapters, which=self.which[row].expand(n))
-        tl.pages_free(self.pages, torch.where(extra >= 0, self.pages.lens + extra, extra))
-        self.last[row] = torch.multinomial(self.probabilities(x[0, -1:]), 1, generator=self.gen)[0, 0]
+        tl.pages_free(self.pages, torch.where(ok & (extra >= 0), self.pages.lens + extra, -1))
+        drawn = torch.multinomial(self.probabilities(x[0, -1:]), 1, generator=self.gen)[0, 0]
+        self.last[row] = torch.where(ok[row], drawn, self.last[row])
+        return ok[row]
 
     def fork(self, parent):
-        """Rows continue others (int32 [rows], -1: a row stays)."""
+        """Rows continue others (int32 [rows], -1: a row stays).  Returns ok: False where no page was left (the row stays empty)."""
         ok = tl.pages_fork(self.pages, parent, self.stack.caches)
-        child = parent >= 0
+        child = ok & (parent >= 0)
         self.last = torch.where(child, self.last[parent.clamp(min=0).long()], self.last)
         return ok
 
@@ -73,12 +76,15 @@ class Server:
         return torch.multinomial(rows.flatten(0, 1), 1, generator=self.gen).view(b, t), q
 
     def step(self, parent, depth, sees):
-        """One step: parent int32 [rows, draft], depth and sees of the trees (verify_step.random_trees) on the device."""
+        """One step: parent int32 [rows, draft], depth and sees of the trees (verify_step.random_trees) on the device.  A row that
+        is empty or for which no pages are left takes no part: it keeps its tokens, entries and pages, and ok is False for it."""
         b, t = parent.shape
         dev, pages = self.last.device, self.pages
         drafted, q = self.draft(parent, depth)
         tokens = torch.cat([self.last[:, None], drafted], 1)                      # the row's newest token heads its tree
-        slots, ok = tl.pages_reserve(pages, torch.full((b,), t + 1, dtype=torch.int32, device=dev), t + 1)
+        live = pages.lens > 0
+        slots, ok = tl.pages_reserve(pages, torch.where(live, t + 1, -1).int(), t + 1)
+        ok = ok & live
         tree = torch.zeros(b, t + 1, t + 1, dtype=torch.bool, device=dev)
         tree[:, :, 0] = True
         tree[:, 1:, 1:] = sees
@@ -88,10 +94,11 @@ class Server:
         target = self.probabilities(x)
         uniform = torch.rand(b, t + 1, generator=self.gen, device=dev)
         path, count, out = tl.verify_drafts(target, drafted, uniform, draft=q, parent=parent)
+        path, count, out = torch.where(ok[:, None], path, -1), torch.where(ok, count, 0), torch.where(ok[:, None], out, -1)
         start = pages.lens + 1
-        tl.kv_compact(self.stack.caches, pages.table, start, path, count)
-        tl.pages_free(pages, start + count)
-        self.last = out.gather(1, count[:, None].long())[:, 0]
+        tl.kv_compact(self.stack.caches, pages, start, path, count)
+        tl.pages_free(pages, torch.where(ok, start + count, -1))
+        self.last = torch.where(ok, out.gather(1, count[:, None].long())[:, 0], self.last)
         return dict(target=target, q=q, drafted=drafted, uniform=uniform, path=path, count=count, tokens=out, slots=slots, ok=ok)
 
 
@@ -108,12 +115,13 @@ def main(argv=None):
     most = a.prompt + a.steps * (a.draft + 1) + a.draft + 1
     stack = vs.Stack(layers=a.layers, fmt=a.format, pages=a.rows * (-(-most // 64)), device=dev)
     server = Server(stack, a.rows, -(-most // 64))
-    server.prompt(0, torch.randint(0, server.vocab, (a.prompt,), generator=server.gen, device=dev))
+    if not bool(server.prompt(0, torch.randint(0, server.vocab, (a.prompt,), generator=server.gen, device=dev))):
+        raise RuntimeError("no pages were left for the prompt")
     parent = torch.zeros(a.rows, dtype=torch.int32, device=dev)
     parent[0] = -1
     if not bool(server.fork(parent).all()):
         raise RuntimeError("no page was left for a fork")
-    cpu, got, counts = torch.Generator().manual_seed(1), None, []
+    cpu, counts, served = torch.Generator().manual_seed(1), [], []
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for i in range(a.steps):
         tree, depth, sees = vs.random_trees(a.rows, a.draft, cpu)
@@ -122,9 +130,10 @@ def main(argv=None):
             start.record()
         got = server.step(tree, depth, sees)
         counts.append(got["count"])
+        served.append(got["ok"])
     end.record()
     torch.cuda.synchronize()
-    if tl.device_status() != 0 or not bool(got["ok"].all()):
+    if tl.device_status() != 0 or not bool(torch.stack(served).all()):
         raise RuntimeError("a row found no pages, or a call reported an index out of range")
     mean = float(torch.stack(counts).float().mean()) + 1
     print(f"{mean:.2f} tokens a step and row, {start.elapsed_time(end) / max(a.steps - 1, 1):.3f} ms a step: {a.layers} layers, {a.rows} rows, "

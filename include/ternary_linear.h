@@ -450,7 +450,9 @@ tl_status ternary_pages_free(const tl_kv_pages *pages, const int32_t *keep, void
  * lens stays.  A row whose lens or held is out of range, whose tokens would not fit its
  * table, or whose next token would lie in a page that another row holds too (it was cut
  * there: fork it instead) gets nothing (ok = 0) and sets the status word; that pages have run
- * out does not.
+ * out does not.  Where ok is 0 the table's entries behind held[r] are none of the row's pages (0,
+ * another row's page, if it never had more): what else the step does for the row is to be left out
+ * (count 0 for ternary_pages_compact, keep -1 for ternary_pages_free).
  */
 tl_status ternary_pages_reserve(const tl_kv_pages *pages, const int32_t *extra, int64_t *slots,
                                 int32_t width, uint8_t *ok, void *stream);
@@ -501,6 +503,17 @@ tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const in
                              int64_t page_table_stride, int64_t max_pages, const int32_t *start,
                              const int32_t *keep, int64_t keep_stride, const int32_t *count,
                              int64_t batch, int64_t n, void *stream);
+
+/*
+ * ternary_pages_compact -- the same for the rows of a pool (start, count int32 [rows], keep int32
+ * [rows, n]): a row's places end with the pages that it holds, so that a row which found no
+ * pages moves nothing of the page that its table names behind them.
+ *   caches: as ternary_pages_fork takes them, at least one.  A held[r] out of range moves nothing
+ *   of that row and sets the status word.
+ */
+tl_status ternary_pages_compact(const tl_kv_pages *pages, const tl_kv_cache *caches, int32_t layers,
+                                const int32_t *start, const int32_t *keep, int64_t keep_stride,
+                                const int32_t *count, int64_t n, void *stream);
 
 /*
  * ternary_verify_drafts -- which drafted tokens stand, and the token after them, such that

@@ -66,6 +66,37 @@ tl::KvMove move_of(const tl_kv_cache *c, int first, int layers, int *status) {
     return m;
 }
 
+// held: pages of each sequence (null: all of its table's)
+tl_status compact(const tl_kv_cache *caches, int32_t layers, const int32_t *page_table, int64_t page_table_stride, int64_t max_pages,
+                  const int32_t *held, const int32_t *start, const int32_t *keep, int64_t keep_stride, const int32_t *count,
+                  int64_t batch, int64_t n, void *stream) {
+    if (layers < 1) return TL_ERR_SHAPE;
+    if (const tl_status s = check_layers(caches, layers)) return s;
+    if (batch < 0 || batch > (1 << 16) || n < 0 || n >= ((int64_t)1 << 31)) return TL_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > kMaxPlaces / caches->page_size) return TL_ERR_SHAPE;
+    if (!tl::stride_ok(page_table_stride) || !tl::stride_ok(keep_stride)) return TL_ERR_SHAPE;
+    if (batch == 0 || n == 0) return TL_OK;
+    if (!start || !keep || !count || (!page_table && max_pages > 0)) return TL_ERR_NULL;
+    if (!aligned(page_table, 4) || !aligned(start, 4) || !aligned(keep, 4) || !aligned(count, 4)) return TL_ERR_ALIGN;
+    tl::CallDevice d;
+    if (const int s = tl::begin_call(&d)) return (tl_status)s;
+    tl::KvCompactArgs a{};
+    a.table = page_table;
+    a.table_stride = page_table_stride;
+    a.max_places = max_pages * caches->page_size;
+    a.start = start;
+    a.keep = keep;
+    a.keep_stride = keep_stride;
+    a.count = count;
+    a.held = held;
+    a.batch = batch;
+    a.n = n;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; e == cudaSuccess && i < layers; i += tl::kMoveLayers)
+        e = tl::launch_kv_compact(move_of(caches, i, layers, d.status), a, d.sm_count, reinterpret_cast<cudaStream_t>(stream));
+    return from_cuda(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,30 +182,16 @@ tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const in
                              int64_t page_table_stride, int64_t max_pages, const int32_t *start,
                              const int32_t *keep, int64_t keep_stride, const int32_t *count,
                              int64_t batch, int64_t n, void *stream) {
-    if (layers < 1) return TL_ERR_SHAPE;
-    if (const tl_status s = check_layers(caches, layers)) return s;
-    if (batch < 0 || batch > (1 << 16) || n < 0 || n >= ((int64_t)1 << 31)) return TL_ERR_SHAPE;
-    if (max_pages < 0 || max_pages > kMaxPlaces / caches->page_size) return TL_ERR_SHAPE;
-    if (!tl::stride_ok(page_table_stride) || !tl::stride_ok(keep_stride)) return TL_ERR_SHAPE;
-    if (batch == 0 || n == 0) return TL_OK;
-    if (!start || !keep || !count || (!page_table && max_pages > 0)) return TL_ERR_NULL;
-    if (!aligned(page_table, 4) || !aligned(start, 4) || !aligned(keep, 4) || !aligned(count, 4)) return TL_ERR_ALIGN;
-    tl::CallDevice d;
-    if (const int s = tl::begin_call(&d)) return (tl_status)s;
-    tl::KvCompactArgs a{};
-    a.table = page_table;
-    a.table_stride = page_table_stride;
-    a.max_places = max_pages * caches->page_size;
-    a.start = start;
-    a.keep = keep;
-    a.keep_stride = keep_stride;
-    a.count = count;
-    a.batch = batch;
-    a.n = n;
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; e == cudaSuccess && i < layers; i += tl::kMoveLayers)
-        e = tl::launch_kv_compact(move_of(caches, i, layers, d.status), a, d.sm_count, reinterpret_cast<cudaStream_t>(stream));
-    return from_cuda(e);
+    return compact(caches, layers, page_table, page_table_stride, max_pages, nullptr, start, keep, keep_stride, count, batch, n, stream);
+}
+
+tl_status ternary_pages_compact(const tl_kv_pages *pages, const tl_kv_cache *caches, int32_t layers,
+                                const int32_t *start, const int32_t *keep, int64_t keep_stride,
+                                const int32_t *count, int64_t n, void *stream) {
+    tl::KvPages g;
+    if (const tl_status s = check_pages(pages, &g)) return s;
+    if (layers > 0 && caches && (caches->pages != g.pages || caches->page_size != g.P)) return TL_ERR_SHAPE;
+    return compact(caches, layers, g.table, g.stride, g.max_pages, g.held, start, keep, keep_stride, count, g.rows, n, stream);
 }
 
 }  // extern "C"

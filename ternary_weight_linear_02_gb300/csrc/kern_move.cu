@@ -137,21 +137,28 @@ struct Place {
 
 struct Moves {
     int start, n;  // first place; moves of the sequence
+    int64_t places;  // that the sequence has
     const int *keep, *pages;
     __device__ __forceinline__ Moves(const KvMove &m, const KvCompactArgs &a, int64_t b) {
         start = a.start[b];
         n = a.count[b];
         keep = a.keep + b * a.keep_stride;
         pages = a.table + b * a.table_stride;
+        places = a.max_places;
+        if (a.held) {  // entries of the table behind the held ones are nobody's, or 0
+            const int64_t has = (int64_t)a.held[b] * m.P;
+            if (has < 0 || has > places) flag_value(m.status);
+            places = has <= places ? has : 0;
+        }
         if (n < 0 || n > a.n || start < 0) {
             flag_value(m.status);
             n = start < 0 || n < 0 ? 0 : (int)a.n;
         }
     }
     // move i (k = keep[i], before = keep[i - 1]): where its entry lies and goes; false where the sequence's moves end
-    __device__ __forceinline__ bool request(const KvMove &m, const KvCompactArgs &a, int i, int k, int before, Place &src, Place &dst) const {
+    __device__ __forceinline__ bool request(const KvMove &m, int i, int k, int before, Place &src, Place &dst) const {
         const int64_t place = (int64_t)start + k;
-        if (k <= before || k < i || place >= a.max_places) {  // (k < i: an earlier one did not ascend)
+        if (k <= before || k < i || place >= places) {  // (k < i: an earlier one did not ascend)
             flag_value(m.status);
             return false;
         }
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(256) compact_warp_kernel(const __grid_constant
         bool ok = true;
         if (lane < 16 && i0 + lane < mv.n) {
             Place from, to;
-            ok = mv.request(m, a, i0 + lane, mv.keep[i0 + lane], i0 + lane > 0 ? mv.keep[i0 + lane - 1] : -1, from, to);
+            ok = mv.request(m, i0 + lane, mv.keep[i0 + lane], i0 + lane > 0 ? mv.keep[i0 + lane - 1] : -1, from, to);
             if (ok) mv.rows(m, from, to, src, dst);
         }
         const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kMovers) compact_block_kernel(const __grid_con
         for (int e = 0; e < EACH; ++e) {
             const int i = i0 + w0 + e * 32 + lane;
             good[e] = e * 32 + lane < WARP && i < mv.n;
-            if (good[e] && !mv.request(m, a, i, k[e], before[e], from[e], into[e])) {
+            if (good[e] && !mv.request(m, i, k[e], before[e], from[e], into[e])) {
                 good[e] = false;
                 atomicMin(&end, i);
             }
@@ -373,6 +380,7 @@ cudaError_t compact(const KvMove &m, const KvCompactArgs &a, int sm_count, cudaS
         c.keep += b0 * a.keep_stride;
         c.start += b0;
         c.count += b0;
+        if (c.held) c.held += b0;
         const int64_t units = c.batch * per;
         const cudaError_t e = blocks ? launch_chained(compact_block_kernel<PIECES>, (unsigned)(units * 2), kMovers, bytes, 0, st, m, c)
                                      : launch_chained(compact_warp_kernel<PIECES>, (unsigned)((units + 7) / 8), 256, 0, 0, st, m, c, units);

@@ -328,6 +328,7 @@ struct KvCompactArgs {
     const int *table;
     int64_t table_stride, max_places;
     const int *start, *keep, *count;
+    const int *held;  // pages of each sequence (null: all of its table's)
     int64_t keep_stride;
     int64_t batch, n;
 };

@@ -7,11 +7,15 @@ the host and can be captured.  Like the rest of the package this only marshals t
 (``include/ternary_linear.h``); an index out of range is never followed and is reported by
 ``device_status`` (TL_ERR_VALUE).
 
-    slots, ok = pages_reserve(pages, extra, draft)        # room for the drafted tokens
+    slots, ok = pages_reserve(pages, extra, draft + 1)    # room for the row's newest token and the drafted ones
     kv_append(cache, k, v, slots.flatten(), ...)          # in every layer, then tree_attention(..)
     path, count, tokens = verify_drafts(target, drafted, uniform, draft=q, parent=parent)
-    kv_compact(layers, pages.table, pages.lens + 1, path, count)   # behind the root, itself a new token
-    pages_free(pages, pages.lens + 1 + count)             # .. and what was not accepted given back
+    count = torch.where(ok, count, 0)                     # a row that found no pages: the step did nothing for it
+    kv_compact(layers, pages, pages.lens + 1, path, count)             # behind the newest token, the tree's root
+    pages_free(pages, torch.where(ok, pages.lens + 1 + count, -1))     # .. and what was not accepted given back
+
+Where ok is False the row's tokens have no slots, and behind the pages that it holds its table names pages of other rows: nothing
+that was computed for the row in this step is of use, and its entries must not be moved.
 """
 from __future__ import annotations
 
@@ -114,8 +118,9 @@ def _declare(lib):
     lib.ternary_pages_fork.argtypes = [pp, p, p, i32, p, p, i64, p]
     lib.ternary_kv_copy.argtypes = [p, i32, p, p, p, i64, p]
     lib.ternary_kv_compact.argtypes = [p, i32, p, i64, i64, p, p, i64, p, i64, i64, p]
+    lib.ternary_pages_compact.argtypes = [pp, p, i32, p, p, i64, p, i64, p]
     for f in (lib.ternary_pages_free, lib.ternary_pages_reserve, lib.ternary_pages_fork, lib.ternary_kv_copy,
-              lib.ternary_kv_compact):
+              lib.ternary_kv_compact, lib.ternary_pages_compact):
         f.restype = ctypes.c_int
     return lib
 
@@ -145,7 +150,8 @@ def pages_reserve(pages: KVPages, extra: torch.Tensor, width: int) -> tuple[torc
     holds: the lowest-numbered free ones, to the rows in order, to each all it needs or none.  Returns (slots
     int64 [rows, width], ok bool [rows]): the slots of the row's next min(extra, width) tokens, as kv_append takes
     them, -1 behind them and where ok is False (no page was left).  lens stays: pages_free moves it on
-    when the tokens are there."""
+    when the tokens are there.  Where ok is False the row keeps what it has, and nothing else of the step may be done for it
+    (this module's loop shows how)."""
     if not 0 <= width < 1 << 31:
         raise ValueError("width must be 0 or more, in 32 bits")
     dev = pages.device
@@ -207,24 +213,37 @@ def _dense(t: torch.Tensor, what: str, rows: int, dev: torch.device) -> torch.Te
     return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
 
 
-def kv_compact(layers, page_table: torch.Tensor, start: torch.Tensor, keep: torch.Tensor, count: torch.Tensor) -> None:
+def kv_compact(layers, page_table, start: torch.Tensor, keep: torch.Tensor, count: torch.Tensor) -> None:
     """Closes up entries in place, in every layer (KVLayers, or KVCache objects): of each sequence, the entry
     at place start[b] + keep[b, i] moves to place start[b] + i, for i < count[b].  page_table int32 [batch,
     max_pages], start and count int32 [batch], keep int32 [batch, n] with 0 <= keep[b, 0] < keep[b, 1] < ..
 
+    page_table may be a KVPages: its rows, whose places end with the pages that they hold (a plain table has no such
+    end: what it names behind them would be moved).
+
     verify_drafts' path and count after a drafted tree; or with start 0 the entries that are left of a
     context.  Sequences must not share the pages that are written."""
     layers = _layers(layers)
-    dev = _cuda(page_table, "page_table")
+    pool = page_table if isinstance(page_table, KVPages) else None
+    if pool is not None:
+        page_table, dev, b = pool.table, pool.device, pool.rows
+        if (layers.first.pages, layers.first.page_size) != (pool.pages, pool.page_size):
+            raise ValueError("the caches must have the pages' number and size")
+    else:
+        dev = _cuda(page_table, "page_table")
+        b = page_table.shape[0] if page_table.dim() else 0
+        page_table = _dense(page_table, "page_table", b, dev)
     if dev != layers.device:
         raise ValueError(f"page_table must be on {layers.device} like the layers: it is on {dev}")
-    b = page_table.shape[0] if page_table.dim() else 0
-    page_table = _dense(page_table, "page_table", b, dev)
     keep = _dense(keep, "keep", b, dev)
     start = _index(start, "start", torch.int32, b, dev)
     count = _index(count, "count", torch.int32, b, dev)
-    rc = _launch(dev, (_ready or _lib()).ternary_kv_compact, layers._array, layers.count, page_table.data_ptr(),
-                 page_table.stride(0), page_table.shape[1], start.data_ptr(), keep.data_ptr(), keep.stride(0),
-                 count.data_ptr(), b, keep.shape[1])
+    lib = _ready or _lib()
+    if pool is not None:
+        rc = _launch(dev, lib.ternary_pages_compact, pool._ref, layers._array, layers.count, start.data_ptr(), keep.data_ptr(),
+                     keep.stride(0), count.data_ptr(), keep.shape[1])
+    else:
+        rc = _launch(dev, lib.ternary_kv_compact, layers._array, layers.count, page_table.data_ptr(), page_table.stride(0),
+                     page_table.shape[1], start.data_ptr(), keep.data_ptr(), keep.stride(0), count.data_ptr(), b, keep.shape[1])
     if rc:
-        _check(rc, "ternary_kv_compact")
+        _check(rc, "ternary_kv_compact" if pool is None else "ternary_pages_compact")
