@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a) {
         if (each > 8) weights_at<T, VEC, 8>(w, v, min(v1, v + 8), x);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (x[i].hi > 0.f && !(token >= 0 && above(ahead, rest))) {
+            // (a weight's hi may be 0 or below, all of it in lo: p less A q where that rounds to p)
+            if (__fadd_rn(x[i].hi, x[i].lo) > 0.f && !(token >= 0 && above(ahead, rest))) {
                 token = v + i;
                 ahead = add(ahead, x[i]);
             }
