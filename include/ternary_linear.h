@@ -541,8 +541,9 @@ tl_status ternary_pages_compact(const tl_kv_pages *pages, const tl_kv_cache *cac
  *   follows it; a row of which nothing can be drawn (none of it is above 0, or its sum is
  *   infinite) gives the token -1.  Both set the device status word to TL_ERR_VALUE.
  *   draft 0..1024 (0: a token is drawn), batch <= 65536, vocab 1..2^31 - 2^12.
- * Comparisons are made in fp64; sums carry 47 bits or more, so that a draw lands where one in
- * fp64 does but for random numbers within about 1e-13 of a border.  HBM-bound: one target row is read
+ * Comparisons are made in fp64, sums are pairs of fp32: a draw lands where one in exact arithmetic does
+ * but for random numbers within (vocab + 2^15) 2^-55 of a border (all roundings on one side; about
+ * 2^-44 as they come).  HBM-bound: one target row is read
  * per sequence, and a row of each side per rejection with draft_probs.
  */
 tl_status ternary_verify_drafts(const void *target, int64_t target_batch_stride,

@@ -12,8 +12,9 @@
 //
 // Which token a random number falls on hangs on sums of a whole vocabulary, next to whose borders fp32
 // says nothing (an error of 1e-7 moves one draw in a hundred at 130000 tokens).  Sums are
-// therefore kept as pairs of fp32 (an error-free sum and what it lost: about 47 bits; GB300 adds fp64
-// at 1/64 of the rate), decisions are made in fp64.
+// therefore kept as pairs of fp32 (an error-free sum and what it lost: within (V + 2^15) 2^-55 of the
+// sum if all roundings fell to one side, 2^-44 as they come; GB300 adds fp64 at 1/64 of the rate),
+// decisions are made in fp64.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -111,6 +112,9 @@ __device__ __forceinline__ void values16(uint4 r, float (&v)[16 / sizeof(T)]) {
 // Sum of the weights of tokens [lo, hi), taken by one warp.  VEC: lo is a multiple of 8 and rows
 // start on 16-byte boundaries.  The last, partly filled step is read under a mask like the others: a loop of
 // single loads would wait for each.
+// A lane's V / 2048 entries (up to 16 below 32768 tokens) go into one pair, in whose lo the lost parts are added in plain
+// fp32.  Every W of them (8 without VEC) lo is brought back below half a unit of hi, so that an addition loses (W + 2) 2^-48 of
+// the sum at most; left to grow, lo lost a 2^-49 n^2 of it after n (2^-29 at 2^22 tokens, one large among many small).
 template <typename T, bool VEC>
 __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
     const int lane = threadIdx.x & 31;
@@ -118,6 +122,10 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
     const auto take = [&](Pair x) {
         const Pair s = two_sum(acc.hi, x.hi);
         acc = {s.hi, __fadd_rn(acc.lo, __fadd_rn(s.lo, x.lo))};
+    };
+    const auto settle = [&] {
+        const float h = __fadd_rn(acc.hi, acc.lo);
+        acc = {h, __fsub_rn(acc.lo, __fsub_rn(h, acc.hi))};
     };
     if constexpr (VEC) {
         // two steps of U loads in flight: one travels while the other is added
@@ -158,6 +166,7 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
                 }
 #pragma unroll
                 for (int e = 0; e < W; ++e) take(w.q ? w.of(pv[e], qv[e]) : Pair{pv[e], 0.f});
+                settle();
             }
         };
         int v = lo + lane * W;
@@ -200,6 +209,7 @@ __device__ __forceinline__ Pair sum_run(const Weights<T> &w, int lo, int hi) {
                 if (w.gone && w.removed(v + u * 32)) p[u] = 0.f;
                 take(w.q ? w.of(p[u], q[u]) : Pair{p[u], 0.f});
             }
+            settle();
         }
     }
     // acc.lo may be as large as acc.hi's last bits; the pairs' sum puts that right
