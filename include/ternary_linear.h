@@ -446,7 +446,8 @@ tl_status ternary_pages_free(const tl_kv_pages *pages, const int32_t *keep, void
  *   ok uint8 [rows], may be NULL: 1 where the row has its pages.
  *   slots int64 [rows, width], may be NULL: the slots of the row's next tokens,
  *     table[r, j / page_size] * page_size + j % page_size for j = lens[r] + i, i < min(extra[r],
- *     width); -1 behind them and where ok is 0 (as ternary_kv_append takes them).
+ *     width); -1 behind them and where ok is 0 (as ternary_kv_append takes them).  A page of the
+ *     table that the pool does not have gives -1 and sets the status word.
  * lens stays.  A row whose lens or held is out of range, whose tokens would not fit its
  * table, or whose next token would lie in a page that another row holds too (it was cut
  * there: fork it instead) gets nothing (ok = 0) and sets the status word; that pages have run

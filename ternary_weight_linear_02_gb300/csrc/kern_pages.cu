@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
                 const uint32_t j = (uint32_t)tokens[r] + (uint32_t)i, p = j / P;
                 if (p < (uint64_t)g.max_pages) {  // (holds unless extra changes during the call)
                     const int page = __ldcg(g.table + r * g.stride + p);  // (another block of the cluster may have written it)
-                    s = (long long)page * g.P + (j - p * P);
+                    if ((uint32_t)page < (uint32_t)g.pages) s = (long long)page * g.P + (j - p * P);
+                    else flag_value(a.status);
                 }
             }
             a.slots[e] = s;
