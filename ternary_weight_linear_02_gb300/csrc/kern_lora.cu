@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(LoraArgs a, int TM, int
         for (int i = 0; i < N; ++i) {
             if (again) same[i] = same_key(key[i]);
             const int at = count_key(cursor, key[i], same[i]);
-            if (key[i] >= 0) order[at] = (int)(t0 + i * 1024 + tid);
+            // (a place beyond the tokens: `which` changed since they were counted)
+            if (key[i] >= 0 && at < a.M) order[at] = (int)(t0 + i * 1024 + tid);
         }
     }
     const int tiles = tile[keys];
