@@ -223,10 +223,12 @@ __global__ void __launch_bounds__(1024) pages_take_kernel(PagesTakeArgs a) {
             }
             below += sum;
         }
-        if (C > 1) {
-            cl_arrive_release();
-            cl_wait_acquire();
-        }
+    }
+    // (whatever the block found: should `want` or the tables change meanwhile, blocks find other totals, and one that
+    // skipped the barrier would leave the others waiting)
+    if (C > 1) {
+        cl_arrive_release();
+        cl_wait_acquire();
     }
     const auto served = [&](int r) {
         const uint32_t c = cum[r];
