@@ -497,7 +497,7 @@ tl_status ternary_kv_copy(const tl_kv_cache *caches, int32_t layers, const int32
  *   the table, that sequence's moves end before it and the status word is set; a
  *   count outside 0..n is clamped and a negative start moves nothing, both set it too.
  *   Sequences of one call must not share the pages that they write.  Places behind the
- *   moved entries keep what they held.  max_pages * page_size <= 2^31 - 256.
+ *   moved entries keep what they held.  max_pages * page_size <= 2^31 - 256, n <= 2^31 - 2^13.
  * HBM-bound: each moved entry is read once and written once.
  */
 tl_status ternary_kv_compact(const tl_kv_cache *caches, int32_t layers, const int32_t *page_table,

@@ -9,6 +9,8 @@ using tl::from_cuda;
 
 constexpr int64_t kMaxPlaces = ((int64_t)1 << 31) - 256;
 constexpr int32_t kMaxLayers = 512;
+// moves of a sequence: a block looks up to five groups of 1024 ahead of one in 31 bits
+constexpr int64_t kMaxMoves = ((int64_t)1 << 31) - (1 << 13);
 
 tl_status check_pages(const tl_kv_pages *p, tl::KvPages *out) {
     if (p == nullptr) return TL_ERR_NULL;
@@ -72,7 +74,7 @@ tl_status compact(const tl_kv_cache *caches, int32_t layers, const int32_t *page
                   int64_t batch, int64_t n, void *stream) {
     if (layers < 1) return TL_ERR_SHAPE;
     if (const tl_status s = check_layers(caches, layers)) return s;
-    if (batch < 0 || batch > (1 << 16) || n < 0 || n >= ((int64_t)1 << 31)) return TL_ERR_SHAPE;
+    if (batch < 0 || batch > (1 << 16) || n < 0 || n > kMaxMoves) return TL_ERR_SHAPE;
     if (max_pages < 0 || max_pages > kMaxPlaces / caches->page_size) return TL_ERR_SHAPE;
     if (!tl::stride_ok(page_table_stride) || !tl::stride_ok(keep_stride)) return TL_ERR_SHAPE;
     if (batch == 0 || n == 0) return TL_OK;
