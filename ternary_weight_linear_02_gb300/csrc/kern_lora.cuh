@@ -232,6 +232,7 @@ struct Form {
     static constexpr int TM = BIG ? 128 : 16;  // tokens of a tile
     static constexpr int NT = 6;               // small: n-tiles of 8 ranks a pass of the shrink
     static constexpr int STAGES = 4, LAG = 2;  // BIG: stages of 64 k; copies in flight behind the newest
+    static_assert(STAGES * (128 + 16) * 128 + 1024 >= tc::kSmemHolder, "holds tensor memory at the cluster's barriers");
 };
 
 // Sizes of a block's shared memory (bytes), the same on the host.

@@ -79,6 +79,7 @@ namespace {
 
 constexpr uint32_t kTmemCols = 256;    // two CTAs per SM share the 512 columns
 constexpr int kSmemFloor = 96 * 1024;  // keeps residency at <= two CTAs per SM
+static_assert(kSmemFloor >= 80 * 1024, "256 columns (tc::kSmemHolder)");
 
 // warp roles
 // warps 0-7: two decoder sets (set = warp / 4, lane quarter = warp % 4)

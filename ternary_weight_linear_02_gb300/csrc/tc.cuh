@@ -11,6 +11,14 @@ namespace tl {
 namespace tc {
 
 // ------------------------------------------------------------- TMEM management
+// Shared memory, in bytes, that a block takes at least where it holds tensor memory while it waits for its cluster.  Two
+// such kernels on two streams share SMs; if an SM took blocks of them for more than its 512 columns, each could hold what a
+// peer of the other waits for.  With this least, a block of 512 columns that takes kSmemAlone has its SM to itself, and what fits
+// beside blocks of 256 (80 KB or more) and 128 columns has room for all of them.
+constexpr int kSmemHolder = 72 * 1024, kSmemAlone = 156 * 1024, kSmemOfSm = 228 * 1024;
+static_assert(kSmemHolder + 1024 + kSmemAlone + 1024 > kSmemOfSm, "a block of 512 columns is alone");
+static_assert(2 * (80 * 1024 + 1024) + kSmemHolder + 1024 > kSmemOfSm, "two blocks of 256 columns are alone");
+
 // Allocates `ncols` (power of two >= 32) columns; the TMEM address is written
 // to *slot (shared memory).  Executed by one whole warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {

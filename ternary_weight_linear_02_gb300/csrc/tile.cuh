@@ -104,9 +104,10 @@ struct TileCfg {
     // Shared memory requested per CTA: at least enough that an SM holds no more CTAs
     // than its 512 tensor-memory columns serve.  A CTA resident beyond that would wait
     // in tcgen05.alloc; with split-K clusters its peers would wait on it at the
-    // cluster barrier while holding the columns it needs.
+    // cluster barrier while holding the columns it needs.  512 columns: no block of
+    // another kernel that holds some of them while it waits for its cluster either.
     static constexpr int TMEM_CPS = (int)(512 / TMEM_COLS);
-    static constexpr int SMEM_FLOOR = TMEM_CPS >= 2 ? 80 * 1024 : 116 * 1024;
+    static constexpr int SMEM_FLOOR = TMEM_CPS >= 2 ? 80 * 1024 : tc::kSmemAlone;
     static constexpr int SMEM_REQ = SMEM > SMEM_FLOOR ? SMEM : SMEM_FLOOR;
     static_assert(TMEM_CPS >= 1 && TMEM_CPS <= 2, "tensor memory budget");
     static_assert((TMEM_CPS + 1) * (SMEM_REQ + 1024) > 228 * 1024, "residency <= tensor memory");
