@@ -188,14 +188,14 @@ __device__ __forceinline__ float4 cl_ld_v4(uint32_t addr) {
     return v;
 }
 
-// For fp32 outputs the quotient is within 2 ulp (0 instead of less than 2^-119 below g = -87).  For 16-bit outputs the
+// For fp32 outputs as the layers' own gated products take it.  For 16-bit outputs the
 // special functions' own instructions, 2^x within 2 ulp and 1/x within 1, without the scaling that the functions
 // put around them for subnormal numbers (a third of the instructions): with the rounding of g log2(e), within 5 + 1.2
-// |g| ulp, 2^-16 of the result, where its rounding takes 2^-9 or 2^-12; 0 instead of less than 2^-119 here too.
+// |g| ulp, 2^-16 of the result, where its rounding takes 2^-9 or 2^-12; 0 instead of less than 2^-119 (g below -87).
 template <typename O>
 __device__ __forceinline__ float silu(float g) {
     if constexpr (sizeof(O) == 4) {
-        return __fdividef(g, 1.f + expf(-g));
+        return g / (1.f + expf(-g));
     } else {
         float e, r;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
