@@ -584,8 +584,8 @@ typedef struct {
  *     the same stride adds in place, any other overlap is not allowed.
  *   which int32 [tokens]: each token's adapter; negative: none (out = y).  One beyond the
  *     adapters counts as none and sets the device status word to TL_ERR_VALUE.
- *   workspace: device, 16-byte aligned, ternary_lora_workspace(tokens, adapters) bytes (0 for
- *     decode shapes: it may then be NULL); free for other use once the call's work has run.
+ *   workspace: device, 16-byte aligned, ternary_lora_workspace(tokens, adapters) bytes (0 up to 1024
+ *     tokens of up to 1024 adapters: it may then be NULL); free for other use once the call's work has run.
  * Sums are fp32 in an order that depends on sizes alone; s_a (x a^T) enters the second product in
  * 16-bit numbers that together keep 2^-17 of it (fp32 outputs: 2^-22); the result is rounded once.
  * ternary_lora_silu_mul -- the same for a fused gate/up layer (two shards of N columns: gate, up),
