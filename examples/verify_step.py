@@ -92,8 +92,9 @@ class Stack:
             n = norm(x)
             if ad is None:
                 h = tl.linear_silu_mul(n, *w["gu"], g, static_weights=True)
-            else:  # the gated product waits for what the adapters add
-                h = tl.lora_silu_mul(n, ad["gu"], which, tl.linear(n, *w["gu"], g, static_weights=True))
+            else:  # the gated product waits for what the adapters add, gate and up in fp32 up to there as in linear_silu_mul
+                y = tl.linear(n, *w["gu"], g, out_dtype=torch.float32, static_weights=True)
+                h = tl.lora_silu_mul(n, ad["gu"], which, y).to(n.dtype)
             x = x + project(h, w, "down", ad)
         return x.unflatten(0, (b, t))
 

@@ -591,6 +591,9 @@ typedef struct {
  * ternary_lora_silu_mul -- the same for a fused gate/up layer (two shards of N columns: gate, up),
  *   with the gated product behind it: g, u the two halves of the sum (fp32),
  *   out[m, j] = silu(g[m, j]) u[m, j], out [tokens, N], which must not overlap y.
+ *   y in 16 bits brings g and u already rounded: where the accuracy of ternary_linear_silu_mul is wanted, whose sums stay
+ *   fp32 up to the product, give y (and take out) in TL_F32.  silu: as there for TL_F32; 16-bit outputs within 2^-16, and 0
+ *   instead of less than 2^-119 where g is below -87.
  * HBM-bound: x, y and out once, the adapters that occur once per 16 or 128 tokens of theirs.
  */
 int64_t ternary_lora_workspace(int64_t tokens, int64_t adapters); /* -1: invalid */

@@ -23,7 +23,9 @@
 //
 // h enters the second product in 16 bits.  One rounding there would add as much error as that of a 16-bit
 // output, so h is split into two numbers of T (three where bf16 feeds an fp32 output), each the
-// rounded rest of those before: 2^-17 of h or less.  f16 takes a row scaled by a power of two, so that
+// rounded rest of those before: 2^-17 of h or less.  f16 into fp32 keeps to two, 2^-22, less than an fp32 sum of K
+// products loses: with three, 8192 tokens of 6 adapters, rank 64, 18944 to 3584, took 190 us instead of 130 (shared memory for one
+// block on an SM).  f16 takes a row scaled by a power of two, so that
 // large sums do not overflow.
 #pragma once
 

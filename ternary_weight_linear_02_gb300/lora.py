@@ -150,7 +150,8 @@ def lora_add(x: torch.Tensor, adapters: Adapters, which: torch.Tensor, y: torch.
 def lora_silu_mul(x: torch.Tensor, adapters: Adapters, which: torch.Tensor, y: torch.Tensor, *, out: torch.Tensor | None = None) -> torch.Tensor:
     """silu(g) * u of a fused gate/up layer with adapters: y [..., 2 N] what the shared layer gave (gate columns, then up
     columns), g and u its halves with each token's adapter product added (two shards of N); returns [..., N].  g and u
-    stay fp32, the result is rounded once to y's dtype."""
+    stay fp32, the result is rounded once to y's dtype.  16-bit y has g and u rounded already, which linear_silu_mul never does:
+    where that matters, take y from the layer with out_dtype=torch.float32 and round what is returned."""
     if len(adapters.shards) != 2 or adapters.shards[0] != adapters.shards[1]:
         raise ValueError("a gated layer has two shards of one size: gate and up")
     return _call("ternary_lora_silu_mul", x, adapters, which, y, out, adapters.outputs // 2)
