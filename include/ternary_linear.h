@@ -674,6 +674,13 @@ void ternary_test_set_wait_limit(int64_t cycles, int32_t stall);
  * restores 0.  Lets tests cover every form on any shape. */
 void ternary_test_set_tile_mode(int32_t mode);
 
+/* Testing aid (host only): tokens of a tile, 16 or 128, in the form that ternary_lora_add (gated: ternary_lora_silu_mul)
+ * takes for these arguments; 0 where nothing is to do, -1 where the call refuses them.  Nothing is
+ * launched.  Lets tests make sure which form they run. */
+int32_t ternary_test_lora_tile(const void *x, int64_t x_stride, const tl_adapters *adapters, const int32_t *which,
+                               const void *y, int64_t y_stride, void *out, int64_t out_stride, int32_t out_dtype,
+                               int64_t tokens, int32_t gated);
+
 #ifdef __cplusplus
 }
 #endif

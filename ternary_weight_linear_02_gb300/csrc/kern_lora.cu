@@ -146,10 +146,12 @@ int64_t lora_workspace(int64_t M, int64_t adapters) {
     return 4 * (4 + 3 * tiles_bound(M, adapters, 16) + M);
 }
 
+int lora_tile(const LoraArgs &a, bool f32) { return big_tiles(a, f32) ? 128 : 16; }
+
 cudaError_t launch_lora(const LoraArgs &args, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st) {
     LoraArgs a = args;
-    const bool big = big_tiles(a, f32);
-    const int TM = big ? 128 : 16;
+    const int TM = lora_tile(a, f32);
+    const bool big = TM == 128;
     const int units = (int)tiles_bound(a.M, a.adapters, TM);
     // Blocks a tile: 8, 6, 4, 2 or 1, as many as make two blocks an SM (gated, where three fit: 2.7) of the tiles that tokens
     // spread evenly over the adapters would give.  (Of all that there could be, a third more, blocks would be too

@@ -378,6 +378,7 @@ struct LoraArgs {
 };
 // tokens and adapters up to which no workspace is needed: each block finds its tile by itself
 int64_t lora_workspace(int64_t M, int64_t adapters);
+int lora_tile(const LoraArgs &a, bool f32);  // tokens of a tile
 cudaError_t launch_lora(const LoraArgs &a, int dtype, bool f32, void *workspace, int sm_count, cudaStream_t st);
 cudaError_t launch_lora_f16(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st);
 cudaError_t launch_lora_bf16(const LoraArgs &a, bool f32, bool big, int units, cudaStream_t st);
