@@ -584,6 +584,8 @@ typedef struct {
  *     the same stride adds in place, any other overlap is not allowed.
  *   which int32 [tokens]: each token's adapter; negative: none (out = y).  One beyond the
  *     adapters counts as none and sets the device status word to TL_ERR_VALUE.
+ *   Infinities and NaN stay with their tokens (x, y) or their adapter's tokens (a, b).  An infinite entry of b gives an
+ *     infinity or a NaN in its column: it meets each of the numbers that h is split into.
  *   workspace: device, 16-byte aligned, ternary_lora_workspace(tokens, adapters) bytes (0 up to 1024
  *     tokens of up to 1024 adapters: it may then be NULL); free for other use once the call's work has run.
  * Sums are fp32 in an order that depends on sizes alone; s_a (x a^T) enters the second product in
