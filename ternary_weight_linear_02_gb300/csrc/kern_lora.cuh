@@ -587,7 +587,9 @@ __device__ __forceinline__ uint32_t shrink_big(const LoraArgs &a, const Tile<128
     return tm;
 }
 
-// ---- expand, few tokens: a block of 8 J columns (gated: of either half), any sizes.
+// ---- expand, few tokens: a block of 8 J columns (gated: of either half), any sizes.  B's loads of a step of 16 ranks are waited for
+// one after the other: 16 tokens of 8 adapters over the fused QKV of 3584 take 10.5 us at rank 24, 12.7 at 40, 16.5 at 64 and 33 at
+// 128, where ExpandSmall takes 7.1 at 16 and 9.1 at 32; over a gated layer of 2 x 18944 39 us at 24 and 62 at 64, 11 at 16.
 template <typename T, typename O, bool GATED>
 __device__ __forceinline__ void expand(const LoraArgs &a, const Tile<16> &tile, const Smem &sz, const T *hs, const float *up, const T *B,
                                        int sh, int64_t off, int64_t wide, int64_t blk) {
