@@ -18,20 +18,22 @@ def _built():
     tl.load()
 
 
+@pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("side", [-1, 1])
-def test_a_border_between_two_halves(side, dtype):
+def test_a_border_between_two_halves(side, dtype, aligned):
     """2^22 tokens.  In the first half every lane's first entry is 2^-10 and the others are s = 2^-35 + 2^-49 - 2^-58 (bf16: 2^-35), whose sums in plain
-    fp32 drop the 2^-49: 2^-29 of the half's sum S1 in all.  The second half holds S1 (1 + side 2^-31) on its last three tokens.
+    fp32 drop the 2^-49: 2^-29 of the half's sum S1 in all.  The second half holds S1 (1 + side 2^-31) on its last five tokens.
     u = 1/2 then falls just before the end of the first half (side -1) or just behind it (+1), 2^-32 of the total away.  The
-    sums' errors, V (W + 2) 2^-59 with the W = 4 (8) entries between two renormalisations, are 2^-34.4 (2^-33.6) at most."""
+    sums' errors, V (W + 2) 2^-59 with the W = 4 (8, and where rows start anywhere) entries between two renormalisations, are 2^-34.4
+    (2^-33.6) at most."""
     vocab, run = 1 << 22, 1 << 16                       # 8 blocks of 8 warps
-    width = 4 if dtype is torch.float32 else 8
+    width = 4 if dtype is torch.float32 and aligned else 8
     small = 2.0 ** -35 + (2.0 ** -49 - 2.0 ** -58 if dtype is torch.float32 else 0.0)
     p = torch.zeros(vocab, dtype=torch.float64)
     at = torch.arange(vocab // 2)
     p[:vocab // 2] = small
-    first = (at % run < 32 * width) & (at % width == 0)
+    first = (at % run < 32 * width) & (at % width == 0) if aligned else at % run < 32
     p[:vocab // 2][first] = 2.0 ** -10
     assert torch.equal(p.to(dtype).double(), p)
     n = int(first.sum())
@@ -45,7 +47,9 @@ def test_a_border_between_two_halves(side, dtype):
         rest -= Fraction(v)
     assert 0 <= rest < Fraction(1, 1 << 38)
     p[-len(tail):] = torch.tensor(tail, dtype=torch.float64)
-    target = p.to(dtype).to(DEV)[None, None]
+    wide = torch.zeros(vocab + 1, dtype=dtype, device=DEV)
+    target = wide[(0 if aligned else 1):][None, None, :vocab]
+    target.copy_(p)
     assert torch.equal(target.cpu().double()[0, 0], p)
     out = tl.verify_drafts(target, torch.zeros(1, 0, dtype=torch.int64, device=DEV), torch.full((1, 1), 0.5, device=DEV))[2]
     token = int(out[0, 0])
